@@ -8,13 +8,18 @@ Raw C-ABI names (same signatures as ``include/fa.h``, pointers as ints):
     fa_fwd, fa_bwd, fa_fwd_gqa, fa_bwd_gqa, fa_bwd_ex (with the BwdExtras struct), fa_bwd_workspace_bytes,
     fa_status_string, fa_bwd_noalloc,
     fa_fwd_varlen, fa_bwd_varlen, fa_bwd_varlen_accumulate, fa_bwd_varlen_workspace_bytes (with the Strides /
-    VarlenProblem structs)
+    VarlenProblem structs), fa_fwd_paged_splits, fa_fwd_paged_workspace_bytes, fa_fwd_paged, fa_paged_append,
+    fa_paged_key_weights, fa_paged_evict (with the PagedProblem struct)
 Tensor helpers (grouped-query attention when k, v have fewer heads than q):
     fwd(q, k, v, ...) -> (o, lse);  bwd(q, k, v, o, lse, do, ...) -> (dq, dk, dv)
     fwd_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, ...) -> (o, lse): e4m3 inputs (fa_fwd_fp8)
     fwd_varlen(q, k, v, ...), bwd_varlen(...): [B, N, H, d] views with any strides, or packed
     [rows, H, d] sequences located by cu_seqlens; query and key lengths may differ.
     fwd_splitkv(q, k, v, ..., num_splits=None): the forward split over keys (decode shapes).
+    fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, ...): the forward of new tokens (one, a few, or a
+    chunk per sequence) over a K/V cache held in pages; paged_append(...) writes their keys and values,
+    paged_key_weights(...) adds the attention weight each cached key received and paged_evict(...) cuts long
+    sequences down to the keys of the largest weight.
     fwd_partial / merge_partials / finalize_partials: per-key-block partials and their
     log-sum-exp merge (ring.py builds sequence-sharded ring attention on them).
 """
@@ -49,6 +54,15 @@ class VarlenProblem(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class PagedProblem(ctypes.Structure):
+    """fa_paged_problem (include/fa.h)."""
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_table", ctypes.c_void_p), ("seqlens_k", ctypes.c_void_p),
+                ("seqlen_q", ctypes.c_int), ("seqlen_k", ctypes.c_int), ("cu_seqlens_q", ctypes.c_void_p),
+                ("rows_q", ctypes.c_int), ("causal", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
 class BwdExtras(ctypes.Structure):
     """fa_bwd_extras (include/fa.h): optional step-visit counts and events around the main pass."""
     _fields_ = [("step_visits", ctypes.c_void_p), ("main_begin_event", ctypes.c_void_p),
@@ -56,6 +70,7 @@ class BwdExtras(ctypes.Structure):
 
 
 _VP = ctypes.POINTER(VarlenProblem)
+_PP = ctypes.POINTER(PagedProblem)
 _SIGS = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P, _P]),
     "fa_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
@@ -81,6 +96,13 @@ _SIGS = {
     "fa_fwd_partial": (_I, [_VP, _P, Strides, _P, Strides, _P, Strides, _P, _P, _P, _P]),
     "fa_merge_partials": (_I, [_VP, _P, _P, _P, _P, _P]),
     "fa_finalize_partials": (_I, [_VP, _P, _P, _P, Strides, _P, _P]),
+    "fa_fwd_paged_splits": (_I, [_PP, _I]),
+    "fa_fwd_paged_workspace_bytes": (ctypes.c_size_t, [_PP, _I]),
+    "fa_fwd_paged": (_I, [_PP, _I, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, ctypes.c_size_t, _P,
+                          _P]),
+    "fa_paged_append": (_I, [_PP, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, _P]),
+    "fa_paged_key_weights": (_I, [_PP, _P, Strides, _P, Strides, _P, _P, _P, _P]),
+    "fa_paged_evict": (_I, [_PP, _I, _I, _P, Strides, _P, Strides, _P, _P, _P, _P, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P]),
 }
@@ -184,6 +206,35 @@ def fa_fwd_splitkv(p, num_splits, q, sq, k, sk, v, sv, o, so, lse, workspace, wo
                    stream) -> int:
     return int(lib().fa_fwd_splitkv(ctypes.byref(p), num_splits, q, sq, k, sk, v, sv, o, so, lse, workspace,
                                     workspace_bytes, dev_status, stream))
+
+
+def fa_fwd_paged_splits(p, num_sms) -> int:
+    return int(lib().fa_fwd_paged_splits(ctypes.byref(p), num_sms))
+
+
+def fa_fwd_paged_workspace_bytes(p, num_splits) -> int:
+    return int(lib().fa_fwd_paged_workspace_bytes(ctypes.byref(p), num_splits))
+
+
+def fa_fwd_paged(p, num_splits, q, sq, k_cache, sk, v_cache, sv, o, so, lse, workspace, workspace_bytes, dev_status,
+                 stream) -> int:
+    return int(lib().fa_fwd_paged(ctypes.byref(p), num_splits, q, sq, k_cache, sk, v_cache, sv, o, so, lse, workspace,
+                                  workspace_bytes, dev_status, stream))
+
+
+def fa_paged_append(p, k_new, sk_new, v_new, sv_new, k_cache, sk, v_cache, sv, key_weights, dev_status, stream) -> int:
+    return int(lib().fa_paged_append(ctypes.byref(p), k_new, sk_new, v_new, sv_new, k_cache, sk, v_cache, sv,
+                                     key_weights, dev_status, stream))
+
+
+def fa_paged_key_weights(p, q, sq, k_cache, sk, lse, key_weights, dev_status, stream) -> int:
+    return int(lib().fa_paged_key_weights(ctypes.byref(p), q, sq, k_cache, sk, lse, key_weights, dev_status, stream))
+
+
+def fa_paged_evict(p, keep, recent, k_cache, sk, v_cache, sv, key_weights, kept, seqlens_out, dev_status,
+                   stream) -> int:
+    return int(lib().fa_paged_evict(ctypes.byref(p), keep, recent, k_cache, sk, v_cache, sv, key_weights, kept,
+                                    seqlens_out, dev_status, stream))
 
 
 def fa_bwd_noalloc(q, k, v, o, dout, lse, dq, dk, dv, B, H, N, d, causal, block_mask, seqlens_k, scale, dev_status,
@@ -514,6 +565,171 @@ def fwd_splitkv(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=None
     if rc != 0:
         raise FaError(rc)
     return o, lse
+
+
+# ----------------------------------------------------------------------------- paged cache
+
+
+def _paged_view(name, t, dims):
+    """fa_strides of a [batch or page, row, head, d] view, or of packed [rows, heads, d] rows. The stride of an
+    axis of one element is never used; it is replaced by a legal one."""
+    if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == dims and t.stride(-1) == 1):
+        shape = "[rows, heads, d]" if dims == 3 else "4-D, [batch or page, row, head, d]"
+        raise ValueError(f"{name} must be a bf16 CUDA tensor, {shape}, with a contiguous last dimension")
+    n, st = t.shape, t.stride()
+    batch, row, head = (0, 0, 1) if dims == 3 else (0, 1, 2)
+    span = n[-1]
+    pick = lambda i: st[i] if n[i] > 1 else span
+    return Strides(pick(row), pick(head), 0 if dims == 3 else pick(batch))
+
+
+def _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal, scale):
+    """The fa_paged_problem of new rows q ([B, N, heads, d], or packed [rows, heads, d] with cu_seqlens_q) over a
+    cache; q is None where a call has no new rows. Also q's number of dimensions."""
+    dev = k_cache.device
+    if k_cache.dim() != 4 or (v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.device != dev)):
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, d] tensors of one shape, on one device")
+    pages, page_size, Hkv, d = k_cache.shape
+    for name, t, dims in (("page_table", page_table, 2), ("seqlens_k", seqlens_k, 1)):
+        if not (t.dtype == torch.int32 and t.is_contiguous() and t.dim() == dims and t.device == dev):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {dev}")
+    B, width = page_table.shape
+    if seqlens_k.shape[0] != B:
+        raise ValueError("page_table and seqlens_k must have one row and one length per sequence")
+    packed = cu_seqlens_q is not None
+    rows_q, Nq, H = 0, 1, Hkv
+    if q is not None:
+        H = q.shape[-2] if q.dim() >= 2 else 0
+        if q.dim() != (3 if packed else 4) or q.shape[-1] != d or q.device != dev or H < 1 or H % Hkv != 0:
+            raise ValueError("new tokens must be [B, N, heads, d] (packed: [rows, heads, d] with cu_seqlens_q) on the "
+                             "cache's device, with the cache's d and a multiple of its heads")
+        if packed:
+            if not (cu_seqlens_q.dtype == torch.int32 and cu_seqlens_q.is_contiguous() and cu_seqlens_q.device == dev
+                    and cu_seqlens_q.shape == (B + 1,)):
+                raise ValueError(f"cu_seqlens_q must be a contiguous int32 [{B + 1}] tensor on {dev}")
+            if max_seqlen_q is None:
+                raise ValueError("packed batches need max_seqlen_q")
+            rows_q, Nq = q.shape[0], int(max_seqlen_q)
+        else:
+            if q.shape[0] != B:
+                raise ValueError("page_table must have one row per sequence")
+            Nq = q.shape[1]
+    elif packed:
+        raise ValueError("cu_seqlens_q without new tokens")
+    bound = width * page_size if max_seqlen_k is None else int(max_seqlen_k)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    return PagedProblem(B, H, Hkv, d, page_size, pages, width, page_table.data_ptr(), seqlens_k.data_ptr(), Nq,
+                        min(bound, 2**31 - 1), _ptr(cu_seqlens_q), rows_q, int(causal), scale), 3 if packed else 4
+
+
+def _launch(dev, stream, call):
+    """call(stream handle) with the tensors' device current; raises FaError for an error code."""
+    with torch.cuda.device(dev):
+        rc = call(_stream(stream))
+    if rc != 0:
+        raise FaError(rc)
+
+
+def _check_weights(key_weights, p, dev):
+    shape = (p.num_pages, p.Hkv, p.page_size)
+    if not (key_weights.dtype == torch.float32 and key_weights.is_contiguous() and key_weights.device == dev
+            and key_weights.shape == shape):
+        raise ValueError(f"key_weights must be a contiguous float32 {list(shape)} tensor on {dev}")
+
+
+def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, max_seqlen_k=None, *,
+              num_splits=None, causal=False, scale=None, out=None, lse=None, workspace=None, status=None, stream=None):
+    """O, LSE of new tokens over a paged cache (fa_fwd_paged). q: [B, N, H, d] views, or packed [rows, H, d] with
+    cu_seqlens_q and max_seqlen_q; k_cache, v_cache: [num_pages, page_size, Hkv, d] (any strides); page_table: int32
+    [B, max_pages]; seqlens_k: int32 [B], the keys in the cache, the new tokens' own included (paged_append writes
+    them). Causal: token i of N sees the keys up to its own. max_seqlen_k bounds the lengths (the table's capacity
+    by default) and num_splits=None picks the split of the keys for it. LSE is [B, H, N] or [H, rows]."""
+    p, dims = _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal,
+                     scale)
+    dev = q.device
+    if q.numel() == 0:  # no new token anywhere: an empty batch
+        p = None
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+    if o.shape != q.shape or o.device != dev:
+        raise ValueError("out must have q's shape and device")
+    shape = (q.shape[1], q.shape[0]) if dims == 3 else (q.shape[0], q.shape[2], q.shape[1])
+    lse = torch.empty(shape, dtype=torch.float32, device=dev) if lse is None else lse
+    _check_aux("lse", lse, torch.float32, math.prod(shape), dev)
+    _check_aux("status", status, torch.int32, 1, dev)
+    sq, so = _paged_view("q", q, dims), _paged_view("out", o, dims)
+    sk, sv = _paged_view("k_cache", k_cache, 4), _paged_view("v_cache", v_cache, 4)
+    if p is None:
+        return o, lse
+    if num_splits is None:
+        num_splits = fa_fwd_paged_splits(p, torch.cuda.get_device_properties(dev).multi_processor_count)
+    nbytes = fa_fwd_paged_workspace_bytes(p, num_splits)
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check_aux("workspace", workspace, None, nbytes, dev)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch(dev, stream, lambda st: fa_fwd_paged(
+        p, num_splits, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, o.data_ptr(), so,
+        lse.data_ptr(), _ptr(workspace), size, _ptr(status), st))
+    return o, lse
+
+
+def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, *,
+                 key_weights=None, status=None, stream=None):
+    """Write new keys and values k, v ([B, N, Hkv, d], or packed [rows, Hkv, d] with cu_seqlens_q and max_seqlen_q)
+    into the cache (fa_paged_append): as the last keys of each sequence, whose lengths seqlens_k already count them.
+    key_weights (float32 [num_pages, Hkv, page_size]), where given, is set to 0 at the written slots."""
+    p, dims = _paged(k, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, None, False, 1.0)
+    if v.shape != k.shape or v.device != k.device or p.H != p.Hkv:
+        raise ValueError("k and v must have one shape, with the cache's heads, on the cache's device")
+    _check_aux("status", status, torch.int32, 1, k.device)
+    if key_weights is not None:
+        _check_weights(key_weights, p, k.device)
+    views = [_paged_view(n, t, dims) for n, t in (("k", k), ("v", v))]
+    views += [_paged_view(n, t, 4) for n, t in (("k_cache", k_cache), ("v_cache", v_cache))]
+    if k.numel() == 0:
+        return
+    _launch(k.device, stream, lambda st: fa_paged_append(
+        p, k.data_ptr(), views[0], v.data_ptr(), views[1], k_cache.data_ptr(), views[2], v_cache.data_ptr(), views[3],
+        _ptr(key_weights), _ptr(status), st))
+
+
+def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_seqlens_q=None, max_seqlen_q=None,
+                      max_seqlen_k=None, *, causal=False, scale=None, status=None, stream=None):
+    """Add to key_weights (float32 [num_pages, Hkv, page_size]), in place, the attention weight that the rows of q pay
+    every cached key, summed over the rows and the query heads of each K/V head (fa_paged_key_weights). q, lse and the
+    other arguments are those of fwd_paged, which returned lse."""
+    p, dims = _paged(q, k_cache, None, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal, scale)
+    _check_aux("lse", lse, torch.float32, q.numel() // p.d, q.device)
+    _check_aux("status", status, torch.int32, 1, q.device)
+    _check_weights(key_weights, p, q.device)
+    sq, sk = _paged_view("q", q, dims), _paged_view("k_cache", k_cache, 4)
+    if q.numel() > 0:
+        _launch(q.device, stream, lambda st: fa_paged_key_weights(
+            p, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(), key_weights.data_ptr(), _ptr(status), st))
+    return key_weights
+
+
+def paged_evict(k_cache, v_cache, key_weights, page_table, seqlens_k, keep, *, recent=0, max_seqlen_k=None, kept=None,
+                seqlens_out=None, status=None, stream=None):
+    """Cut every sequence longer than `keep` down to its last `recent` keys and the older ones of the largest weight,
+    per K/V head, in place in the cache and the weights (fa_paged_evict). Returns (kept, seqlens): the former index of
+    each kept key, int32 [B, Hkv, keep] (-1 past the end of a shorter sequence), and the new lengths, int32 [B]."""
+    p, _ = _paged(None, k_cache, v_cache, page_table, seqlens_k, None, None, max_seqlen_k, False, 1.0)
+    dev = k_cache.device
+    keep, recent = int(keep), int(recent)
+    if not (0 <= recent <= keep and 1 <= keep < 2**31):
+        raise ValueError("keep must be at least 1 and recent between 0 and keep")
+    _check_weights(key_weights, p, dev)
+    kept = torch.empty((p.B, p.Hkv, keep), dtype=torch.int32, device=dev) if kept is None else kept
+    seqlens_out = torch.empty((p.B,), dtype=torch.int32, device=dev) if seqlens_out is None else seqlens_out
+    _check_aux("kept", kept, torch.int32, p.B * p.Hkv * keep, dev)
+    _check_aux("seqlens_out", seqlens_out, torch.int32, p.B, dev)
+    _check_aux("status", status, torch.int32, 1, dev)
+    sk, sv = _paged_view("k_cache", k_cache, 4), _paged_view("v_cache", v_cache, 4)
+    _launch(dev, stream, lambda st: fa_paged_evict(
+        p, keep, recent, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, key_weights.data_ptr(), kept.data_ptr(),
+        seqlens_out.data_ptr(), _ptr(status), st))
+    return kept, seqlens_out
 
 
 # ----------------------------------------------------------------------------- partials

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "fa_common.cuh"
+#include "fa_paged.cuh"
 
 namespace {
 
@@ -287,6 +288,64 @@ int launch_partial(const fa::AttnShape& s, const fa_varlen_problem* p, int split
   cudaError_t e = fa_launch_fwd(a, st);
   if (e == cudaSuccess && merge) e = fa_launch_splitkv_merge(a, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Paged problem -> shape; FA_OK or an error code. `attend`: the call reads q (heads, scale and causal count).
+int paged_shape(const fa_paged_problem* p, bool attend, fa::PagedShape* out) {
+  if (p == nullptr || p->page_table == nullptr || p->seqlens_k == nullptr) return FA_ERR_INVALID_ARG;
+  const int rc = attend ? check_common(p->B, p->H, p->Hkv, p->d, p->causal, p->scale)
+                        : check_common(p->B, p->Hkv, p->Hkv, p->d, 0, 1.f);
+  if (rc != FA_OK) return rc;
+  if (p->page_size < 1 || p->num_pages < 1 || p->max_pages < 1 || p->seqlen_q < 1 || p->seqlen_k < 1)
+    return FA_ERR_INVALID_ARG;
+  if (p->cu_seqlens_q != nullptr && p->rows_q < 1) return FA_ERR_INVALID_ARG;
+  if (p->page_size < 8 || p->page_size > 65536 || (p->page_size & (p->page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  if (!aligned(p->page_table, 4) || !aligned(p->seqlens_k, 4) || !aligned(p->cu_seqlens_q, 4))
+    return FA_ERR_MISALIGNED;
+  fa::PagedShape s{};
+  s.B = p->B;
+  s.H = attend ? p->H : p->Hkv;
+  s.Hkv = p->Hkv;
+  s.d = p->d;
+  s.Nq = p->seqlen_q;
+  const long long capacity = (long long)p->max_pages * p->page_size;
+  s.max_k = capacity < p->seqlen_k ? (int)capacity : p->seqlen_k;
+  s.cu_q = p->cu_seqlens_q;
+  s.rows_q = p->cu_seqlens_q != nullptr ? p->rows_q : 0;
+  s.causal = attend ? p->causal : 0;
+  while ((1 << s.page_shift) < p->page_size) ++s.page_shift;
+  s.num_pages = p->num_pages;
+  s.max_pages = p->max_pages;
+  s.table = p->page_table;
+  s.seqlens = p->seqlens_k;
+  const double rows = s.cu_q != nullptr ? (double)s.rows_q : (double)s.B * s.Nq;
+  // Grids run over (sequence, head, token) and (sequence, K/V head, key).
+  if (rows * s.H * s.d >= kMaxElems || (double)s.B * s.H * s.Nq >= kMaxElems ||
+      (double)s.B * s.Hkv * s.max_k >= kMaxElems)
+    return FA_ERR_UNSUPPORTED;
+  *out = s;
+  return FA_OK;
+}
+
+int take_cache_strides(const fa_strides& in, const fa_paged_problem* p, FaStrides* out) {
+  const int rc = take_strides(in, false, p->num_pages, p->page_size, p->Hkv, out);
+  if (rc != FA_OK) return rc;
+  const long long most = 1ll << 38;  // tensor-map strides stay below 2^40 bytes
+  return out->row >= most || out->head >= most || out->batch >= most ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+bool paged_on_device(const fa::PagedShape& s) {
+  return device_accessible(s.table) && device_accessible(s.seqlens) && device_accessible(s.cu_q);
+}
+
+size_t paged_rows(const fa::PagedShape& s) {
+  return s.cu_q != nullptr ? (size_t)s.H * s.rows_q : (size_t)s.B * s.H * s.Nq;
+}
+
+size_t paged_workspace(const fa::PagedShape& s, int splits) {
+  if (splits == 1) return 0;
+  const size_t rows = paged_rows(s) * (size_t)splits;
+  return round_up(rows * sizeof(float)) + round_up(rows * s.d * sizeof(float));
 }
 
 }  // namespace
@@ -585,6 +644,129 @@ static int bwd_varlen_impl(const fa_varlen_problem* p, const void* q, fa_strides
       (rc = take_strides(sdv, packed, s.B, rk, s.Hkv, &t.sdv)) != FA_OK)
     return rc;
   return launch_bwd(s, t, p->scale, workspace, workspace_bytes, dev_status, stream);
+}
+
+int fa_fwd_paged_splits(const fa_paged_problem* p, int num_sms) {
+  (void)num_sms;
+  (void)p;
+  return 1;
+}
+
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_splits) {
+  fa::PagedShape s;
+  if (paged_shape(p, true, &s) != FA_OK || num_splits < 1 || num_splits > kMaxSplits) return 0;
+  return paged_workspace(s, num_splits);
+}
+
+int fa_fwd_paged(const fa_paged_problem* p, int num_splits, const void* q, fa_strides sq, const void* k_cache,
+                 fa_strides sk, const void* v_cache, fa_strides sv, void* o, fa_strides so, float* lse, void* workspace,
+                 size_t workspace_bytes, int* dev_status, void* stream) {
+  FaPagedArgs a{};
+  int rc = paged_shape(p, true, &a.s);
+  if (rc != FA_OK) return rc;
+  if (num_splits < 1 || num_splits > kMaxSplits) return FA_ERR_INVALID_ARG;
+  const size_t need = paged_workspace(a.s, num_splits);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  const bool packed = a.s.cu_q != nullptr;
+  const int rows = packed ? a.s.rows_q : a.s.Nq;
+  if ((rc = take_strides(sq, packed, a.s.B, rows, a.s.H, &a.sq)) != FA_OK ||
+      (rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK ||
+      (rc = take_strides(so, packed, a.s.B, rows, a.s.H, &a.so)) != FA_OK)
+    return rc;
+  if (!q || !k_cache || !v_cache || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(dev_status, 4) || (need > 0 && !aligned(workspace, kAlign)))
+    return FA_ERR_MISALIGNED;
+  if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = const_cast<void*>(k_cache);
+  a.v = const_cast<void*>(v_cache);
+  a.o = o;
+  a.lse = lse;
+  a.scale = p->scale;
+  a.status = dev_status;
+  a.splits = num_splits;
+  a.part_rows = paged_rows(a.s);
+  if (need > 0) {
+    a.part_lse = static_cast<float*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        round_up(a.part_rows * num_splits * sizeof(float)));
+  }
+  return fa_launch_fwd_paged(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_new, const void* v_new,
+                    fa_strides sv_new, void* k_cache, fa_strides sk, void* v_cache, fa_strides sv, float* key_weights,
+                    int* dev_status, void* stream) {
+  FaPagedArgs a{};
+  int rc = paged_shape(p, false, &a.s);
+  if (rc != FA_OK) return rc;
+  const bool packed = a.s.cu_q != nullptr;
+  const int rows = packed ? a.s.rows_q : a.s.Nq;
+  if ((rc = take_strides(sk_new, packed, a.s.B, rows, a.s.Hkv, &a.sk_new)) != FA_OK ||
+      (rc = take_strides(sv_new, packed, a.s.B, rows, a.s.Hkv, &a.sv_new)) != FA_OK ||
+      (rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK)
+    return rc;
+  if (!k_new || !v_new || !k_cache || !v_cache) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(key_weights, 4) || !aligned(dev_status, 4))
+    return FA_ERR_MISALIGNED;
+  if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.weights = key_weights;
+  a.status = dev_status;
+  return fa_launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_key_weights(const fa_paged_problem* p, const void* q, fa_strides sq, const void* k_cache, fa_strides sk,
+                         const float* lse, float* key_weights, int* dev_status, void* stream) {
+  FaPagedArgs a{};
+  int rc = paged_shape(p, true, &a.s);
+  if (rc != FA_OK) return rc;
+  const bool packed = a.s.cu_q != nullptr;
+  if ((rc = take_strides(sq, packed, a.s.B, packed ? a.s.rows_q : a.s.Nq, a.s.H, &a.sq)) != FA_OK ||
+      (rc = take_cache_strides(sk, p, &a.sk)) != FA_OK)
+    return rc;
+  if (!q || !k_cache || !lse || !key_weights) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(key_weights, 4) ||
+      !aligned(dev_status, 4))
+    return FA_ERR_MISALIGNED;
+  if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = const_cast<void*>(k_cache);
+  a.lse = const_cast<float*>(lse);
+  a.weights = key_weights;
+  a.scale = p->scale;
+  a.status = dev_status;
+  return fa_launch_paged_key_weights(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cache, fa_strides sk, void* v_cache,
+                   fa_strides sv, float* key_weights, int32_t* kept, int32_t* seqlens_out, int* dev_status,
+                   void* stream) {
+  FaPagedArgs a{};
+  int rc = paged_shape(p, false, &a.s);
+  if (rc != FA_OK) return rc;
+  if (keep < 1 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
+  if ((rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK) return rc;
+  if (!k_cache || !v_cache || !key_weights || !kept || !seqlens_out || seqlens_out == p->seqlens_k)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key_weights, 4) || !aligned(kept, 4) ||
+      !aligned(seqlens_out, 4) || !aligned(dev_status, 4))
+    return FA_ERR_MISALIGNED;
+  if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.weights = key_weights;
+  a.keep = keep;
+  a.recent = recent;
+  a.kept = kept;
+  a.seqlens_out = seqlens_out;
+  a.status = dev_status;
+  return fa_launch_paged_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,90 @@
+// Shared definitions of the paged-cache operators (attention over a cache in pages, append, key
+// weights, eviction); the readings are stated in include/fa.h.
+#pragma once
+
+#include "fa_common.cuh"
+
+namespace fa {
+
+struct PagedShape {
+  int B, H, Hkv, d;
+  int Nq;                 // fixed length: new tokens per sequence; packed: their maximum
+  int max_k;              // bound on the key count: min(the caller's, capacity)
+  const int32_t* cu_q;    // [B + 1] or null, as in AttnShape
+  int rows_q;
+  int causal;
+  int page_shift;         // log2(slots per page)
+  int num_pages, max_pages;
+  const int32_t* table;    // [B][max_pages]
+  const int32_t* seqlens;  // [B]
+};
+
+// One sequence of the batch: its new rows, its keys and the causal offset (key j visible to row i iff
+// j <= i + off). Everything is clamped to the tensors' extents, so no array in device memory can make
+// a kernel index outside them.
+__device__ __forceinline__ SeqInfo paged_seq(const PagedShape& s, int b) {
+  SeqInfo r;
+  if (s.cu_q != nullptr) {
+    r.q0 = clampi(__ldg(s.cu_q + b), 0, s.rows_q);
+    r.Lq = clampi(__ldg(s.cu_q + b + 1) - r.q0, 0, min(s.Nq, s.rows_q - r.q0));
+    r.bb = 0;
+  } else {
+    r.q0 = 0;
+    r.Lq = s.Nq;
+    r.bb = b;
+  }
+  r.Lk = clampi(__ldg(s.seqlens + b), 0, s.max_k);
+  r.k0 = 0;
+  r.off = r.Lk - r.Lq;
+  r.krows = r.Lk;
+  return r;
+}
+
+// Index of row (token i of the sequence, head h) in the LSE's order: [B][H][Nq], packed [H][rows_q].
+__device__ __forceinline__ size_t paged_row(const PagedShape& s, const SeqInfo& q, int b, int h, int i) {
+  return s.cu_q != nullptr ? (size_t)h * s.rows_q + q.q0 + i : ((size_t)b * s.H + h) * s.Nq + i;
+}
+
+// The page of the table entry `e` of sequence b, or -1 (reported) when it is none of the cache's.
+__device__ __forceinline__ int paged_page(const PagedShape& s, int b, int e, int* status) {
+  const int page = __ldg(s.table + (size_t)b * s.max_pages + e);
+  if ((unsigned)page < (unsigned)s.num_pages) return page;
+  report_status(status, FA_ERR_BOUNDS);
+  return -1;
+}
+
+// Element offset of (page, slot, head) in a cache.
+__device__ __forceinline__ size_t paged_offset(const FaStrides& t, int page, int slot, int h) {
+  return (size_t)page * t.batch + (size_t)slot * t.row + (size_t)h * t.head;
+}
+
+// Offset of (page, head, slot) in the weights, [num_pages][Hkv][page_size].
+__device__ __forceinline__ size_t weight_offset(const PagedShape& s, int page, int hk, int slot) {
+  return (((size_t)page * s.Hkv + hk) << s.page_shift) + slot;
+}
+
+}  // namespace fa
+
+struct FaPagedArgs {
+  fa::PagedShape s;
+  const void* q;
+  void *k, *v;  // the caches
+  void* o;
+  float* lse;
+  FaStrides sq, sk, sv, so;
+  const void *k_new, *v_new;  // append
+  FaStrides sk_new, sv_new;
+  float* weights;
+  float scale;
+  int* status;
+  int splits;
+  float *part_o, *part_lse;
+  size_t part_rows;
+  int keep, recent;  // evict
+  int32_t *kept, *seqlens_out;
+};
+
+cudaError_t fa_launch_fwd_paged(const FaPagedArgs& a, cudaStream_t st);
+cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
+cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);
+cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);

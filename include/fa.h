@@ -293,6 +293,96 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
                          fa_strides so, float* lse, void* stream);
 
 /*
+ * Attention over a paged K/V cache, and the cache's own operators (serving).
+ * The pages name no cache; the readings adopted:
+ *   cache      k_cache and v_cache are bf16, addressed as [page][slot][head][d] with d contiguous and the
+ *              element strides of fa_strides (row = slot, head, batch = page: multiples of 8, > 0); num_pages
+ *              pages of page_size slots (a power of two, 8 .. 65536). Element offsets are 64-bit: a cache may
+ *              hold more than 2^31 elements.
+ *   page table device int32 [B][max_pages]: key j of sequence b lies in page page_table[b][j / page_size], slot
+ *              j % page_size. Only entries that a sequence's length reaches are read. One outside
+ *              [0, num_pages) writes FA_ERR_BOUNDS into *dev_status; nothing outside the cache is read or
+ *              written, and the outputs of that sequence are undefined.
+ *   lengths    device int32 seqlens_k [B]: the keys of each sequence, its new tokens among them. For reading, a
+ *              length is clamped into [0, min(seqlen_k, max_pages * page_size)]; seqlen_k is the host's bound on
+ *              the lengths, by which grids and workspaces are sized.
+ *   new tokens [batch][row][head][d] as in fa_fwd_varlen: fixed length (seqlen_q rows per sequence) or packed
+ *              (cu_seqlens_q, rows_q; seqlen_q bounds the lengths). The new tokens of a sequence are its last
+ *              keys: token i of L_q is key i + L_k - L_q.
+ *   weights    key_weights fp32 [num_pages][Hkv][page_size], contiguous: one number per cached key and K/V head.
+ *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result.
+ *   sharing    pages may be shared by sequences for reading; a page that a call writes (fa_paged_append,
+ *              fa_paged_key_weights, fa_paged_evict) belongs to one sequence of that call, else the writes race.
+ * d, H and Hkv as for fa_fwd_gqa. Errors, ownership, dev_status and streams as for fa_fwd.
+ */
+typedef struct {
+  int B, H, Hkv, d;
+  int page_size, num_pages, max_pages;
+  const int32_t* page_table;   /* device int32 [B][max_pages] */
+  const int32_t* seqlens_k;    /* device int32 [B] */
+  int seqlen_q, seqlen_k;      /* new tokens per sequence (packed: their bound); bound on seqlens_k */
+  const int32_t* cu_seqlens_q; /* NULL (fixed length) or device int32 [B + 1] */
+  int rows_q;                  /* packed only: row extent of the new tokens' tensors */
+  int causal;
+  float scale;
+} fa_paged_problem;
+
+/*
+ * Forward attention of the new tokens over the cache: O and LSE. Key j is visible to query i iff j < L_k and
+ * (!causal || j <= i + L_k - L_q); a row with no visible key gets O = 0 and LSE = -inf. One token per sequence
+ * (decode), a few drafted ones and whole prompt chunks are the same call; rows of q outside every sequence are
+ * neither read nor written.
+ *   q, o         bf16, strides sq, so; lse fp32 as in fa_fwd_varlen ([B, H, seqlen_q], packed [H, rows_q])
+ *   num_splits   1 .. 256: the keys are split into this many ranges of whole 128-key tiles whose partial results
+ *                are merged by their log-sum-exp; fa_fwd_paged_splits(p, number of SMs) picks it
+ *   workspace    device, >= fa_fwd_paged_workspace_bytes(p, num_splits) bytes, 256-byte aligned; may be NULL
+ *                where that is 0 (one split)
+ */
+int fa_fwd_paged_splits(const fa_paged_problem* p, int num_sms);
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_splits);
+int fa_fwd_paged(const fa_paged_problem* p, int num_splits, const void* q, fa_strides sq, const void* k_cache,
+                 fa_strides sk, const void* v_cache, fa_strides sv, void* o, fa_strides so, float* lse, void* workspace,
+                 size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * Write the new tokens' keys and values into the cache: token i of sequence b goes to key i + seqlens_k[b] - L_q
+ * (the unclamped length, which counts the new tokens). A token whose place is negative or past
+ * max_pages * page_size is not written and writes FA_ERR_BOUNDS into *dev_status.
+ *   k_new, v_new  bf16 [batch][row][head][d], Hkv heads, strides sk_new, sv_new
+ *   key_weights   nullable: the weights of the written slots are set to 0
+ * p->H, seqlen_k, causal and scale are not used.
+ */
+int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_new, const void* v_new,
+                    fa_strides sv_new, void* k_cache, fa_strides sk, void* v_cache, fa_strides sv, float* key_weights,
+                    int* dev_status, void* stream);
+
+/*
+ * Add to every cached key the attention weight that the given rows paid it:
+ *   key_weights[b, hk, j] += sum over rows i that see key j and heads h of group hk of exp(scale q_ih . k_j - LSE_ih)
+ * with the LSE that fa_fwd_paged gave for the same rows, cache and lengths (or for more keys: any LSE of the
+ * caller's). A row with LSE = -inf adds nothing. Sums are fp32, in a fixed order: the result is run-to-run identical.
+ */
+int fa_paged_key_weights(const fa_paged_problem* p, const void* q, fa_strides sq, const void* k_cache, fa_strides sk,
+                         const float* lse, float* key_weights, int* dev_status, void* stream);
+
+/*
+ * Eviction: cut every sequence that is longer than `keep` down to `keep` keys, per K/V head. Its last `recent` keys
+ * stay, and the keep - recent older ones of the largest weight (equal weights: the lower index; NaN counts below
+ * every number). The kept keys, values and weights move, in their order, to places 0 .. keep - 1. Shorter sequences
+ * are left as they are.
+ *   keep, recent  keep >= 1, 0 <= recent <= keep
+ *   kept          out: int32 [B][Hkv][keep]: the former index of each kept key, ascending; a sequence of
+ *                 L <= keep keys gets 0 .. L - 1 and then -1
+ *   seqlens_out   out: int32 [B]: min(L, keep); not the array seqlens_k itself
+ * Slots past the new length keep what they held; their pages are the caller's to release. Each K/V head keeps keys
+ * of its own, so after an eviction a key index means another token in each head (kept tells which).
+ * p->H, seqlen_q, cu_seqlens_q, rows_q, causal and scale are not used.
+ */
+int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cache, fa_strides sk, void* v_cache,
+                   fa_strides sv, float* key_weights, int32_t* kept, int32_t* seqlens_out, int* dev_status,
+                   void* stream);
+
+/*
  * Backward pass that allocates nothing, for callers that cannot allocate device memory (a plugin
  * or custom operator inside another framework receives only its input and output buffers; the
  * host framework owns the memory pool, and a cudaMalloc of its own would bypass that pool's

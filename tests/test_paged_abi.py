@@ -1,0 +1,129 @@
+"""Host-side checks of the paged-cache entry points (no GPU): every refusal comes before any launch."""
+
+import pytest
+import torch
+
+import exact_io_aware_38_gb300 as fa
+from exact_io_aware_38_gb300 import build
+
+A = 0x10000  # fake device address, never dereferenced
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    build.build()
+    return fa.lib()
+
+
+def problem(**kw):
+    f = dict(B=2, H=8, Hkv=2, d=128, page_size=16, num_pages=50, max_pages=10, page_table=A, seqlens_k=A, seqlen_q=3,
+             seqlen_k=160, cu_seqlens_q=None, rows_q=0, causal=1, scale=0.1)
+    f.update(kw)
+    return fa.PagedProblem(**f)
+
+
+SQ = fa.Strides(8 * 128, 128, 3 * 8 * 128)
+SN = fa.Strides(2 * 128, 128, 3 * 2 * 128)
+SC = fa.Strides(2 * 128, 128, 16 * 2 * 128)
+
+
+def attend(p=None, splits=1, q=A, sq=SQ, k=A, sk=SC, v=A, sv=SC, o=A, so=SQ, lse=A, ws=None, nbytes=0, status=None):
+    return fa.fa_fwd_paged(p or problem(), splits, q, sq, k, sk, v, sv, o, so, lse, ws, nbytes, status, None)
+
+
+def append(p=None, kn=A, skn=SN, vn=A, svn=SN, k=A, sk=SC, v=A, sv=SC, w=None, status=None):
+    return fa.fa_paged_append(p or problem(), kn, skn, vn, svn, k, sk, v, sv, w, status, None)
+
+
+def weights(p=None, q=A, sq=SQ, k=A, sk=SC, lse=A, w=A, status=None):
+    return fa.fa_paged_key_weights(p or problem(), q, sq, k, sk, lse, w, status, None)
+
+
+def evict(p=None, keep=64, recent=8, k=A, sk=SC, v=A, sv=SC, w=A, kept=A, out=2 * A, status=None):
+    return fa.fa_paged_evict(p or problem(), keep, recent, k, sk, v, sv, w, kept, out, status, None)
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(B=0), -1), (dict(Hkv=0), -1), (dict(page_size=0), -1), (dict(num_pages=0), -1), (dict(max_pages=0), -1),
+    (dict(seqlen_k=0), -1), (dict(seqlen_q=0), -1), (dict(page_table=None), -1), (dict(seqlens_k=None), -1),
+    (dict(cu_seqlens_q=A, rows_q=0), -1), (dict(d=96), -2), (dict(page_size=24), -2), (dict(page_size=4), -2),
+    (dict(page_size=1 << 17), -2), (dict(page_table=A + 2), -3), (dict(seqlens_k=A + 1), -3),
+    (dict(cu_seqlens_q=A + 2, rows_q=9), -3),
+    (dict(B=1 << 12, max_pages=1 << 20, seqlen_k=1 << 20), -2),  # B Hkv keys past 2^31
+])
+def test_problem_refusals(kw, rc):
+    p = problem(**kw)
+    assert attend(p) == rc and weights(p) == rc and append(p) == rc and evict(p) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [(dict(H=0), -1), (dict(H=7), -1), (dict(causal=2), -1), (dict(scale=0.0), -1),
+                                   (dict(scale=float("nan")), -1)])
+def test_problem_refusals_of_calls_with_queries(kw, rc):
+    p = problem(**kw)
+    assert attend(p) == rc and weights(p) == rc
+
+
+def test_buffer_refusals():
+    for call, names in ((attend, "q k v o lse"), (append, "kn vn k v"), (weights, "q k lse w"), (evict, "k v w kept out")):
+        for n in names.split():
+            assert call(**{n: None}) == -1, (call, n)
+            assert call(**{n: A + 2}) == -3, (call, n)
+        assert call(status=A + 2) == -3
+    assert append(w=A + 2) == -3
+    bad = [fa.Strides(0, 128, 8192), fa.Strides(256, 12, 8192), fa.Strides(256, 128, 0), fa.Strides(-256, 128, 8192)]
+    for s in bad:
+        assert attend(sq=s) == attend(sk=s) == attend(sv=s) == attend(so=s) == -1
+        assert append(skn=s) == append(svn=s) == append(sk=s) == append(sv=s) == -1
+        assert weights(sq=s) == weights(sk=s) == evict(sk=s) == evict(sv=s) == -1
+    assert attend(sk=fa.Strides(256, 128, 1 << 39)) == -2
+
+
+def test_split_and_workspace_rules():
+    r256 = lambda x: (x + 255) // 256 * 256
+    p = problem()
+    rows = 2 * 8 * 3
+    assert fa.fa_fwd_paged_workspace_bytes(p, 1) == 0
+    assert fa.fa_fwd_paged_workspace_bytes(p, 5) == r256(5 * rows * 4) + r256(5 * rows * 128 * 4)
+    assert fa.fa_fwd_paged_workspace_bytes(p, 0) == fa.fa_fwd_paged_workspace_bytes(p, 257) == 0
+    for splits, ws, nbytes, rc in ((0, A, 1 << 30, -1), (257, A, 1 << 30, -1), (4, None, 1 << 30, -1), (4, A, 16, -1),
+                                   (4, A + 16, 1 << 30, -3)):
+        assert attend(splits=splits, ws=ws, nbytes=nbytes) == rc
+    for B in (1, 4, 64, 4096):
+        for n in (1, 7, 500):
+            for bound in (1, 128, 1000, 100_000):
+                q = problem(B=B, seqlen_q=n, seqlen_k=bound, max_pages=10_000)
+                s = fa.fa_fwd_paged_splits(q, 152)
+                assert 1 <= s <= 256 and s <= max(1, -(-bound // 128)), (B, n, bound, s)
+    assert fa.fa_fwd_paged_splits(problem(d=96), 152) == 1
+
+
+def test_evict_budget_and_alias():
+    for keep, recent in ((0, 0), (-1, 0), (5, 6), (5, -1)):
+        assert evict(keep=keep, recent=recent) == -1
+    assert evict(out=A) == -1  # the lengths it reads
+
+
+def test_host_arrays_are_refused():
+    """Arrays the kernels read must be device-accessible; this address is not (and there may be no GPU at all)."""
+    import ctypes
+    host = (ctypes.c_int32 * 64)()
+    p = problem(page_table=ctypes.addressof(host), seqlens_k=ctypes.addressof(host))
+    assert attend(p) == append(p) == weights(p) == evict(p) == -1
+
+
+def test_binding_refuses():
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)
+    k = z(4, 16, 2, 64)
+    table, lens = z(2, 3, dtype=torch.int32), z(2, dtype=torch.int32)
+    good = dict(q=z(2, 1, 4, 64), k_cache=k, v_cache=k, page_table=table, seqlens_k=lens)
+    for bad in (dict(), dict(page_table=table.long()), dict(seqlens_k=z(3, dtype=torch.int32)), dict(v_cache=z(4, 8, 2, 64)),
+                dict(q=z(2, 1, 3, 64)), dict(q=z(2, 1, 4, 128)), dict(q=z(3, 1, 4, 64)), dict(q=z(2, 4, 64)),
+                dict(out=z(2, 1, 4, 32)), dict(cu_seqlens_q=z(3, dtype=torch.int32))):
+        with pytest.raises(ValueError):  # the first: these are CPU tensors
+            fa.fwd_paged(**{**good, **bad})
+    for keep, recent in ((0, 0), (3, 4), (3, -1)):
+        with pytest.raises(ValueError):
+            fa.paged_evict(k, k, z(4, 2, 16, dtype=torch.float32), table, lens, keep, recent=recent)
+    for w in (z(4, 16, 2, dtype=torch.float32), z(4, 2, 16)):
+        with pytest.raises(ValueError):
+            fa.paged_evict(k, k, w, table, lens, 3)
