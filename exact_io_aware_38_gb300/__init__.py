@@ -8,7 +8,7 @@ Raw C-ABI names (same signatures as ``include/fa.h``, pointers as ints):
     fa_fwd, fa_bwd, fa_fwd_gqa, fa_bwd_gqa, fa_bwd_ex (with the BwdExtras struct), fa_bwd_workspace_bytes,
     fa_status_string, fa_bwd_noalloc,
     fa_fwd_varlen, fa_bwd_varlen, fa_bwd_varlen_accumulate, fa_bwd_varlen_workspace_bytes (with the Strides /
-    VarlenProblem structs), fa_fwd_paged_splits, fa_fwd_paged_workspace_bytes, fa_fwd_paged, fa_paged_append,
+    VarlenProblem structs), fa_fwd_paged_workspace_bytes, fa_fwd_paged, fa_paged_append,
     fa_paged_key_weights, fa_paged_evict (with the PagedProblem struct)
 Tensor helpers (grouped-query attention when k, v have fewer heads than q):
     fwd(q, k, v, ...) -> (o, lse);  bwd(q, k, v, o, lse, do, ...) -> (dq, dk, dv)
@@ -96,7 +96,6 @@ _SIGS = {
     "fa_fwd_partial": (_I, [_VP, _P, Strides, _P, Strides, _P, Strides, _P, _P, _P, _P]),
     "fa_merge_partials": (_I, [_VP, _P, _P, _P, _P, _P]),
     "fa_finalize_partials": (_I, [_VP, _P, _P, _P, Strides, _P, _P]),
-    "fa_fwd_paged_splits": (_I, [_PP, _I]),
     "fa_fwd_paged_workspace_bytes": (ctypes.c_size_t, [_PP, _I]),
     "fa_fwd_paged": (_I, [_PP, _I, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, ctypes.c_size_t, _P,
                           _P]),
@@ -208,17 +207,13 @@ def fa_fwd_splitkv(p, num_splits, q, sq, k, sk, v, sv, o, so, lse, workspace, wo
                                     workspace_bytes, dev_status, stream))
 
 
-def fa_fwd_paged_splits(p, num_sms) -> int:
-    return int(lib().fa_fwd_paged_splits(ctypes.byref(p), num_sms))
+def fa_fwd_paged_workspace_bytes(p, num_sms) -> int:
+    return int(lib().fa_fwd_paged_workspace_bytes(ctypes.byref(p), num_sms))
 
 
-def fa_fwd_paged_workspace_bytes(p, num_splits) -> int:
-    return int(lib().fa_fwd_paged_workspace_bytes(ctypes.byref(p), num_splits))
-
-
-def fa_fwd_paged(p, num_splits, q, sq, k_cache, sk, v_cache, sv, o, so, lse, workspace, workspace_bytes, dev_status,
+def fa_fwd_paged(p, num_sms, q, sq, k_cache, sk, v_cache, sv, o, so, lse, workspace, workspace_bytes, dev_status,
                  stream) -> int:
-    return int(lib().fa_fwd_paged(ctypes.byref(p), num_splits, q, sq, k_cache, sk, v_cache, sv, o, so, lse, workspace,
+    return int(lib().fa_fwd_paged(ctypes.byref(p), num_sms, q, sq, k_cache, sk, v_cache, sv, o, so, lse, workspace,
                                   workspace_bytes, dev_status, stream))
 
 
@@ -638,12 +633,12 @@ def _check_weights(key_weights, p, dev):
 
 
 def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, max_seqlen_k=None, *,
-              num_splits=None, causal=False, scale=None, out=None, lse=None, workspace=None, status=None, stream=None):
+              num_sms=None, causal=False, scale=None, out=None, lse=None, workspace=None, status=None, stream=None):
     """O, LSE of new tokens over a paged cache (fa_fwd_paged). q: [B, N, H, d] views, or packed [rows, H, d] with
     cu_seqlens_q and max_seqlen_q; k_cache, v_cache: [num_pages, page_size, Hkv, d] (any strides); page_table: int32
     [B, max_pages]; seqlens_k: int32 [B], the keys in the cache, the new tokens' own included (paged_append writes
     them). Causal: token i of N sees the keys up to its own. max_seqlen_k bounds the lengths (the table's capacity
-    by default) and num_splits=None picks the split of the keys for it. LSE is [B, H, N] or [H, rows]."""
+    by default); num_sms is the number of SMs to use (all by default). LSE is [B, H, N] or [H, rows]."""
     p, dims = _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal,
                      scale)
     dev = q.device
@@ -660,16 +655,15 @@ def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max
     sk, sv = _paged_view("k_cache", k_cache, 4), _paged_view("v_cache", v_cache, 4)
     if p is None:
         return o, lse
-    if num_splits is None:
-        num_splits = fa_fwd_paged_splits(p, torch.cuda.get_device_properties(dev).multi_processor_count)
-    nbytes = fa_fwd_paged_workspace_bytes(p, num_splits)
-    if workspace is None and nbytes > 0:
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    nbytes = fa_fwd_paged_workspace_bytes(p, num_sms)
+    if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check_aux("workspace", workspace, None, nbytes, dev)
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch(dev, stream, lambda st: fa_fwd_paged(
-        p, num_splits, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, o.data_ptr(), so,
-        lse.data_ptr(), _ptr(workspace), size, _ptr(status), st))
+        p, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, o.data_ptr(), so,
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status), st))
     return o, lse
 
 

@@ -338,14 +338,11 @@ bool paged_on_device(const fa::PagedShape& s) {
   return device_accessible(s.table) && device_accessible(s.seqlens) && device_accessible(s.cu_q);
 }
 
-size_t paged_rows(const fa::PagedShape& s) {
-  return s.cu_q != nullptr ? (size_t)s.H * s.rows_q : (size_t)s.B * s.H * s.Nq;
-}
+constexpr int kMaxSms = 1024;  // CTAs that fa_fwd_paged may be divided among
 
-size_t paged_workspace(const fa::PagedShape& s, int splits) {
-  if (splits == 1) return 0;
-  const size_t rows = paged_rows(s) * (size_t)splits;
-  return round_up(rows * sizeof(float)) + round_up(rows * s.d * sizeof(float));
+size_t paged_workspace(const fa::PagedShape& s, int num_sms) {
+  if ((long long)s.Nq * (s.H / s.Hkv) <= kPagedDecodeRows) return round_up(fa_paged_decode_workspace(s, num_sms));
+  return kAlign;
 }
 
 }  // namespace
@@ -646,27 +643,20 @@ static int bwd_varlen_impl(const fa_varlen_problem* p, const void* q, fa_strides
   return launch_bwd(s, t, p->scale, workspace, workspace_bytes, dev_status, stream);
 }
 
-int fa_fwd_paged_splits(const fa_paged_problem* p, int num_sms) {
-  (void)num_sms;
-  (void)p;
-  return 1;
-}
-
-size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_splits) {
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_sms) {
   fa::PagedShape s;
-  if (paged_shape(p, true, &s) != FA_OK || num_splits < 1 || num_splits > kMaxSplits) return 0;
-  return paged_workspace(s, num_splits);
+  if (paged_shape(p, true, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
+  return paged_workspace(s, num_sms);
 }
 
-int fa_fwd_paged(const fa_paged_problem* p, int num_splits, const void* q, fa_strides sq, const void* k_cache,
+int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
                  fa_strides sk, const void* v_cache, fa_strides sv, void* o, fa_strides so, float* lse, void* workspace,
                  size_t workspace_bytes, int* dev_status, void* stream) {
   FaPagedArgs a{};
   int rc = paged_shape(p, true, &a.s);
   if (rc != FA_OK) return rc;
-  if (num_splits < 1 || num_splits > kMaxSplits) return FA_ERR_INVALID_ARG;
-  const size_t need = paged_workspace(a.s, num_splits);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  if (num_sms < 1 || num_sms > kMaxSms || workspace == nullptr || workspace_bytes < paged_workspace(a.s, num_sms))
+    return FA_ERR_INVALID_ARG;
   const bool packed = a.s.cu_q != nullptr;
   const int rows = packed ? a.s.rows_q : a.s.Nq;
   if ((rc = take_strides(sq, packed, a.s.B, rows, a.s.H, &a.sq)) != FA_OK ||
@@ -675,7 +665,7 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_splits, const void* q, fa_st
     return rc;
   if (!q || !k_cache || !v_cache || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
-      !aligned(dev_status, 4) || (need > 0 && !aligned(workspace, kAlign)))
+      !aligned(dev_status, 4) || !aligned(workspace, kAlign))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
   a.q = q;
@@ -685,13 +675,8 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_splits, const void* q, fa_st
   a.lse = lse;
   a.scale = p->scale;
   a.status = dev_status;
-  a.splits = num_splits;
-  a.part_rows = paged_rows(a.s);
-  if (need > 0) {
-    a.part_lse = static_cast<float*>(workspace);
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        round_up(a.part_rows * num_splits * sizeof(float)));
-  }
+  a.num_sms = num_sms;
+  a.workspace = workspace;
   return fa_launch_fwd_paged(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

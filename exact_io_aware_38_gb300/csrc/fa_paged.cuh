@@ -77,13 +77,16 @@ struct FaPagedArgs {
   float* weights;
   float scale;
   int* status;
-  int splits;
-  float *part_o, *part_lse;
-  size_t part_rows;
+  int num_sms;      // CTAs the attention's work is divided among
+  void* workspace;
   int keep, recent;  // evict
   int32_t *kept, *seqlens_out;
 };
 
+// Attention of at most kPagedDecodeRows rows (tokens x grouped heads) per sequence and K/V head.
+constexpr int kPagedDecodeRows = 64;
+size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms);
+cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_fwd_paged(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);

@@ -111,6 +111,7 @@ int grid_for(size_t warps) {
 }  // namespace fa
 
 cudaError_t fa_launch_fwd_paged(const FaPagedArgs& a, cudaStream_t st) {
+  if (a.s.Nq * (a.s.H / a.s.Hkv) <= kPagedDecodeRows) return fa_launch_paged_decode(a, st);
   auto k = a.s.d == 64 ? fa::paged_rows_kernel<64> : fa::paged_rows_kernel<128>;
   return launch_dependent(k, dim3(fa::grid_for((size_t)a.s.B * a.s.H * a.s.Nq)), dim3(256), 0, st, a);
 }

@@ -1,0 +1,635 @@
+// Attention of a few new tokens per sequence over a paged cache (decode, drafted tokens): at most 64
+// rows (tokens x query heads of one K/V head), so the pass is bound by reading K and V once.
+//
+// What it computes: for the R = L_q G rows of a (sequence, K/V head), key tiles of 128 stream through
+// shared memory; S^T = K Q^T puts a key on each tensor-memory lane and a row on each column, so the
+// products cost N = 16, 32 or 64 columns instead of a 128-row tile that would be nearly empty, and a
+// softmax thread handles R numbers per tile instead of 128. P^T goes back through shared memory
+// (bf16, keys x rows) and O^T += V^T P^T accumulates in tensor memory, a head dimension per lane.
+// The exponentials are taken against a reference max per row, set by the row's first tile and raised
+// (O and the row sums rescaled) only when a score exceeds it by 2^32: exact, since fp32 and bf16 keep
+// their relative precision over that range, and one vote per tile replaces a max over 128 keys.
+//
+// Division of the work: all sequences' key tiles form one line, ordered (sequence, head, tile), which
+// the CTAs (one per SM, persistent) divide evenly, whatever the lengths are. A CTA's share
+// begins and ends inside a (sequence, head) at most twice; those pieces leave normalised fp32
+// partials (two slots per CTA) that the merge kernel joins by their log-sum-exp; whole ones are
+// written directly.
+//
+// Roles: warp 0 reads the page table and copies (TMA, a lane per page), warp 1 issues the MMAs, warps
+// 2-5 are the softmax and the epilogue. Copies run ahead across pieces, so memory never waits for an
+// epilogue.
+#include "fa_paged.cuh"
+#include "fa_tmap.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace tc;
+
+constexpr int kDecThreads = 192;
+constexpr float kNoMax = -3.0e38f;   // reference max of a row that has seen no key
+constexpr float kRaise = 32.f;       // log2 units a score may exceed the reference by
+
+template <int D, int NP>
+struct DecCfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  // K and V in flight: 192 KB, or 128 KB beside 64-row tiles.
+  static constexpr int kStages = (NP == 64 ? 2 : 3) * (D == 64 ? 2 : 1);
+  static constexpr int kQBytes = NP * D * 2;
+  static constexpr int kQBufs = 2;
+  static constexpr int kPBytes = 128 * 128;          // 128 keys x up to 64 rows, one 128-byte row per key
+  static constexpr int kSmem = kQBufs * kQBytes + 2 * kStages * kTileBytes + kPBytes + 1024;
+  static_assert(kSmem + 480 + 36 * NP <= 227 * 1024, "with the control block");
+  static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : 256;  // S x 2, O x 2
+  static constexpr uint32_t kIdS = idesc_bf16(128, NP, false, false);
+  // O^T = V^T P^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared
+  // memory and are never read (a lane's result depends on its own row alone).
+  static constexpr uint32_t kIdPV = idesc_bf16(128, NP, true, true);
+};
+
+template <int NP>
+struct DecCtl {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2];
+  uint64_t p_ready, pv_done;
+  uint64_t o_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int scan[kDecThreads / 32];
+  int b0, hk0, kt0, todo, first_cta, first_slot;  // where this CTA begins; how many tiles it has
+  int issued_q, issued_t;                         // copies issued (abort-path drain)
+  float m[NP], alpha[NP], wmax[4][NP];
+  int lim[NP];
+};
+
+__device__ __forceinline__ int tiles_of(const SeqInfo& q) { return q.Lq == 0 ? 0 : max(1, (q.Lk + 127) >> 7); }
+
+// The pieces of a CTA's share: (b, hk, key tiles [kt, end)), walked in order by every role.
+struct Pieces {
+  const PagedShape& s;
+  int b, hk, kt, todo, n, end;
+  SeqInfo seq;
+  __device__ Pieces(const PagedShape& s_, int b_, int hk_, int kt_, int todo_)
+      : s(s_), b(b_), hk(hk_), kt(kt_), todo(todo_), n(0), end(0) {
+    if (todo > 0) open();
+  }
+  __device__ void open() {
+    seq = paged_seq(s, b);
+    n = tiles_of(seq);
+    end = min(n, kt + todo);
+  }
+  __device__ bool done() const { return todo == 0; }
+  __device__ bool whole() const { return kt == 0 && end == n; }
+  __device__ void next() {
+    todo -= end - kt;
+    kt = 0;
+    if (todo == 0) return;
+    if (++hk == s.Hkv) {
+      hk = 0;
+      do seq = paged_seq(s, ++b);
+      while ((n = tiles_of(seq)) == 0);  // todo > 0: a later sequence has tiles
+    }
+    end = min(n, todo);
+  }
+};
+
+// Reduce v[0 .. N) over the 32 lanes; afterwards lane l holds, in v[0 .. max(1, N / 32)), the columns
+// column_of(l) + i. A halving exchange: N + a few shuffles instead of 5 N.
+template <int N, typename F>
+__device__ __forceinline__ void columns_reduce(float (&v)[N], int lane, F f) {
+  int cnt = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (cnt > 1) {
+      const int half = cnt / 2;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < half) {
+          const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
+          v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+      cnt = half;
+    } else {
+      v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ int column_of(int lane) {
+  return N == 16 ? lane >> 1 : N == 32 ? lane : 2 * lane;
+}
+
+__device__ __forceinline__ bool vote_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+struct DecWork {
+  float* part_o;    // [2 CTAs][NP][D]
+  float* part_lse;  // [2 CTAs][NP], log2 units
+  int4* desc;       // [CTAs]: {b, hk, first CTA, its slot}; b = -1: no (sequence, head) ends here in pieces
+};
+
+template <int D, int NP>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const DecWork wk) {
+  using C = DecCfg<D, NP>;
+  grid_dependency_wait();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) DecCtl<NP> ctl;
+  const uint32_t sKV = (smem_u32(smem_raw) + 1023u) & ~1023u;  // stage i: K then V
+  const uint32_t sP = sKV + 2 * C::kStages * C::kTileBytes;
+  const uint32_t sQ = sP + C::kPBytes;
+  volatile int* abort_flag = &ctl.abort_flag;
+  const PagedShape& s = a.s;
+  const int G = s.H / s.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto sK = [&](int i) { return sKV + 2 * i * C::kTileBytes; };
+  auto sV = [&](int i) { return sKV + (2 * i + 1) * C::kTileBytes; };
+  auto bar = [&](uint64_t& x) { return smem_u32(&x); };
+
+  if (threadIdx.x == 0) {
+    ctl.abort_flag = 0;
+    ctl.issued_q = ctl.issued_t = 0;
+    ctl.todo = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(ctl.q_full[i]), 1);
+      mbar_init(bar(ctl.q_empty[i]), 1);
+      mbar_init(bar(ctl.s_full[i]), 1);
+      mbar_init(bar(ctl.o_free[i]), 128);
+    }
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bar(ctl.k_full[i]), 1);
+      mbar_init(bar(ctl.k_empty[i]), 1);
+      mbar_init(bar(ctl.v_full[i]), 1);
+      mbar_init(bar(ctl.v_empty[i]), 1);
+    }
+    mbar_init(bar(ctl.p_ready), 128);
+    mbar_init(bar(ctl.pv_done), 1);
+    mbar_init(bar(ctl.drain), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  // Rows of Q that no copy fills (the box has Nq G rows) are zero.
+  const int box = s.Nq * G;
+  for (int i = threadIdx.x; i < C::kQBufs * (D / 64) * (NP - box) * 8; i += kDecThreads) {
+    const int r = box + i / 8 % (NP - box), part = i / 8 / (NP - box);  // part: buffer and column half
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sQ + (part * NP + r) * 128 + (i & 7) * 16), "r"(0)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  // This CTA's share [lo, hi) of the line of key tiles, and the sequence in which it begins: the
+  // threads take consecutive sequences each and a scan gives where each thread's begin.
+  int lo, hi;
+  {
+    const int per = (s.B + kDecThreads - 1) / kDecThreads, first = threadIdx.x * per;
+    const int last = min(s.B, first + per);
+    int mine = 0;
+    for (int b = first; b < last; ++b) mine += tiles_of(paged_seq(s, b)) * s.Hkv;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) ctl.scan[warp] = inc;
+    __syncthreads();
+    int base = inc - mine, total = 0;
+    for (int i = 0; i < kDecThreads / 32; ++i) {
+      if (i < warp) base += ctl.scan[i];
+      total += ctl.scan[i];
+    }
+    const int n = min((int)gridDim.x, total), c = blockIdx.x;  // no CTA before the last busy one is idle
+    lo = c < n ? (int)((long long)total * c / n) : 0;
+    hi = c < n ? (int)((long long)total * (c + 1) / n) : 0;
+    if (lo < hi && lo >= base && lo < base + mine) {
+      int b = first, at = base;
+      for (;; ++b) {
+        const int t = tiles_of(paged_seq(s, b)) * s.Hkv;
+        if (lo < at + t) break;
+        at += t;
+      }
+      const int nt = tiles_of(paged_seq(s, b));
+      const int start = at + (lo - at) / nt * nt;  // where the (sequence, head) begins
+      ctl.b0 = b;
+      ctl.hk0 = (lo - at) / nt;
+      ctl.kt0 = lo - start;
+      ctl.todo = hi - lo;
+      // The first CTA that works on it, and the slot of its piece: its first slot if it begins there.
+      const int c0 = (int)(((long long)(start + 1) * n - 1) / total);
+      ctl.first_cta = c0;
+      ctl.first_slot = 2 * c0 + ((long long)total * c0 / n == start ? 0 : 1);
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  // Only the merge waits for this grid; its blocks may be scheduled as SMs drain.
+  asm volatile("griddepcontrol.launch_dependents;");
+  Pieces w(s, ctl.b0, ctl.hk0, ctl.kt0, ctl.todo);
+  if (threadIdx.x == 0) {
+    const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
+    wk.desc[blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.first_cta, ctl.first_slot);
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ copies
+    const int P = 1 << s.page_shift, rows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
+    bool run = true;
+    int t = 0;
+    // Page of tile kt that this lane copies (-1, reported: none of the cache's, reads as zero).
+    auto page_of = [&](const Pieces& x, int kt) -> int {
+      const int key = (kt << 7) + (lane << shift);
+      return lane < per && key < x.seq.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
+    };
+    for (int piece = 0; !w.done(); ++piece) {
+      const int qb = piece % C::kQBufs, qu = piece / C::kQBufs;
+      int page = page_of(w, w.kt);
+      if (run && qu > 0) run = mbar_wait(bar(ctl.q_empty[qb]), (qu - 1) & 1, abort_flag, a.status);
+      run = __all_sync(0xffffffffu, run) && !*abort_flag;
+      if (run && lane == 0) {
+        mbar_expect_tx(bar(ctl.q_full[qb]), box * D * 2);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sQ + (qb * (D / 64) + c) * NP * 128, &tmQ, c * 64, w.hk * G, w.seq.q0, w.seq.bb,
+                      bar(ctl.q_full[qb]));
+        ctl.issued_q = piece + 1;
+      }
+      for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+        const int st = t % C::kStages, u = t / C::kStages;
+        const int left = w.seq.Lk - (kt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
+        const int slot = (kt << 7) & (P - 1);
+        const int next = kt + 1 < w.end ? page_of(w, kt + 1) : 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t full = x ? bar(ctl.v_full[st]) : bar(ctl.k_full[st]);
+          if (run && u > 0)
+            run = mbar_wait(x ? bar(ctl.v_empty[st]) : bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
+          run = __all_sync(0xffffffffu, run) && !*abort_flag;
+          if (!run) continue;
+          if (lane == 0) {
+            mbar_expect_tx(full, pages * rows * D * 2);
+            ctl.issued_t = 2 * t + x + 1;
+          }
+          __syncwarp();
+          if (lane < pages)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d((x ? sV(st) : sK(st)) + c * 16384 + lane * rows * 128, x ? &tmV : &tmK, c * 64, slot, w.hk,
+                          page, full);
+        }
+        page = next;
+      }
+      w.next();
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      bool run = true;
+      int t = 0;  // tiles whose S has been issued: t + 1 ahead of the P V
+      Pieces v = w;  // the piece of the next S
+      int vkt = v.kt, vpiece = 0;
+      auto issue_s = [&]() {
+        const int st = t % C::kStages, qb = vpiece % C::kQBufs;
+        if (run && vkt == v.kt)
+          run = mbar_wait_spin(bar(ctl.q_full[qb]), (vpiece / C::kQBufs) & 1, abort_flag, a.status);
+        if (run) run = mbar_wait_spin(bar(ctl.k_full[st]), (t / C::kStages) & 1, abort_flag, a.status);
+        fence_after_sync();
+        if (run) {
+          const uint64_t dk = desc_kmajor_sw128(sK(st)), dq = desc_kmajor_sw128(sQ + qb * C::kQBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + (t & 1) * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32),
+                   desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32), C::kIdS, kk > 0);
+          mma_commit(bar(ctl.s_full[t & 1]));
+          mma_commit(bar(ctl.k_empty[st]));
+          if (vkt + 1 == v.end) mma_commit(bar(ctl.q_empty[qb]));
+        }
+        ++t;
+        if (++vkt == v.end) {
+          v.next();
+          vkt = 0;
+          ++vpiece;
+        }
+      };
+      if (!w.done()) issue_s();
+      int j = 0;
+      for (int piece = 0; !w.done(); ++piece) {
+        for (int kt = w.kt; kt < w.end; ++kt, ++j) {
+          if (!v.done()) issue_s();
+          const int st = j % C::kStages;
+          if (run) run = mbar_wait_spin(bar(ctl.p_ready), j & 1, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.v_full[st]), (j / C::kStages) & 1, abort_flag, a.status);
+          if (run && kt == w.kt && piece >= 2)
+            run = mbar_wait_spin(bar(ctl.o_free[piece & 1]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+          fence_after_sync();
+          if (run) {
+            const uint64_t dv = desc_mnmajor_sw128(sV(st), 16384), dp = desc_mnmajor_sw128(sP, 16384);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ss(tmem + (2 + (piece & 1)) * NP, desc_add(dv, kk * 2048), desc_add(dp, kk * 2048), C::kIdPV,
+                     kk > 0 || kt > w.kt);
+            mma_commit(bar(ctl.v_empty[st]));
+            mma_commit(bar(ctl.pv_done));
+          }
+        }
+        w.next();
+      }
+      mma_commit(bar(ctl.drain));
+      mbar_wait_drain(bar(ctl.drain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, epilogue
+    const int quad = warp & 3, r = quad * 32 + lane;  // key within the tile; head dimension of O^T
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const float sl2 = a.scale * kLog2e;
+    bool run = true;
+    int t = 0;
+    for (int piece = 0; !w.done(); ++piece) {
+      const SeqInfo& seq = w.seq;
+      const int live = seq.Lq * G;  // rows that exist
+      const uint32_t tO = tmem + lane_off + (2 + (piece & 1)) * NP;
+      if (r < NP) ctl.lim[r] = s.causal ? min(seq.Lk, r / G + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
+      const int least = s.causal ? min(seq.Lk, seq.off + 1) : seq.Lk;
+      float l[NP];
+#pragma unroll
+      for (int n = 0; n < NP; ++n) l[n] = 0.f;
+      for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+        const int st = t % C::kStages;
+        if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
+        fence_after_sync();
+        float x[NP];
+        {
+          uint32_t(&u)[NP] = reinterpret_cast<uint32_t(&)[NP]>(x);
+          if constexpr (NP == 16) {
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+                  "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+                : "r"(tmem + lane_off + (t & 1) * NP));
+          } else {
+#pragma unroll
+            for (int c = 0; c < NP / 32; ++c)
+              tmem_ld32(tmem + lane_off + (t & 1) * NP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(u + c * 32));
+          }
+          tmem_ld_wait();
+        }
+        const int key = (kt << 7) + r;
+        const bool opens = kt == w.kt;
+        if (opens) named_bar_sync(1, 128);  // ctl.lim is written; the last piece's ctl.m is no longer read
+        if ((kt << 7) + 128 > least) {
+#pragma unroll
+          for (int n = 0; n < NP; ++n) x[n] = key < ctl.lim[n] ? x[n] : -INFINITY;
+        }
+        bool raise = opens;
+        if (!opens) {
+          bool big = false;
+#pragma unroll
+          for (int n = 0; n < NP; ++n) big |= fmaf(x[n], sl2, -ctl.m[n]) > kRaise;
+          raise = vote_any(big);
+        }
+        bool waited = false;
+        if (raise) {
+          float y[NP];
+#pragma unroll
+          for (int n = 0; n < NP; ++n) y[n] = x[n] * sl2;
+          columns_reduce(y, lane, [](float p, float q) { return fmaxf(p, q); });
+#pragma unroll
+          for (int i = 0; i < (NP == 64 ? 2 : 1); ++i) ctl.wmax[quad][column_of<NP>(lane) + i] = y[i];
+          named_bar_sync(1, 128);
+          if (r < NP) {
+            const float old = opens ? kNoMax : ctl.m[r];
+            const float now = fmaxf(fmaxf(fmaxf(ctl.wmax[0][r], ctl.wmax[1][r]), fmaxf(ctl.wmax[2][r], ctl.wmax[3][r])),
+                                    old);
+            ctl.alpha[r] = ex2_approx(old - now);
+            ctl.m[r] = now;
+          }
+          named_bar_sync(1, 128);
+          if (!opens) {
+            if (run) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
+            fence_after_sync();
+            waited = true;
+#pragma unroll
+            for (int c = 0; c < NP / 16; ++c) {
+              uint32_t o[16];
+              asm volatile(
+                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                    "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                  : "r"(tO + c * 16));
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * ctl.alpha[c * 16 + i]);
+                l[c * 16 + i] *= ctl.alpha[c * 16 + i];
+              }
+              tmem_st16(tO + c * 16, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        uint32_t pk[NP / 2];
+#pragma unroll
+        for (int n = 0; n < NP; n += 2) {
+          const float p0 = ex2_approx(fmaf(x[n], sl2, -ctl.m[n])), p1 = ex2_approx(fmaf(x[n + 1], sl2, -ctl.m[n + 1]));
+          l[n] += p0;
+          l[n + 1] += p1;
+          pk[n / 2] = pack_bf16x2(p0, p1);
+        }
+        // P's buffer is free once the previous P V has read it.
+        if (run && t > 0 && !waited) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
+#pragma unroll
+        for (int c = 0; c < NP / 8; ++c)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sP + r * 128 + ((c ^ (r & 7)) << 4)),
+                       "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
+                       : "memory");
+        // Value rows past the last key may hold anything, and 0 times NaN is NaN: they become 0.
+        const int valid = seq.Lk - (kt << 7);
+        if (valid < 128) {
+          if (run) run = mbar_wait(bar(ctl.v_full[st]), (t / C::kStages) & 1, abort_flag, a.status);
+          if (run && r >= valid)
+#pragma unroll
+            for (int c = 0; c < D / 64 * 8; ++c)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + (c >> 3) * 16384 + r * 128 +
+                                                                          (c & 7) * 16),
+                           "r"(0)
+                           : "memory");
+        }
+        fence_proxy_async_smem();
+        fence_before_sync();
+        if (run) mbar_arrive(bar(ctl.p_ready));
+      }
+      // ---------------------------------------------------------------- end of the piece
+      columns_reduce(l, lane, [](float p, float q) { return p + q; });
+#pragma unroll
+      for (int i = 0; i < (NP == 64 ? 2 : 1); ++i) ctl.wmax[quad][column_of<NP>(lane) + i] = l[i];
+      named_bar_sync(1, 128);
+      const bool whole = w.whole();
+      const int slot = 2 * blockIdx.x + (piece == 0 ? 0 : 1);
+      if (r < NP) {
+        const float sum = (ctl.wmax[0][r] + ctl.wmax[1][r]) + (ctl.wmax[2][r] + ctl.wmax[3][r]);
+        ctl.alpha[r] = sum > 0.f ? 1.f / sum : 0.f;
+        const float lse2 = sum > 0.f ? ctl.m[r] + log2f(sum) : -INFINITY;
+        if (whole) {
+          if (r < live) a.lse[paged_row(s, seq, w.b, w.hk * G + r % G, r / G)] = lse2 * kLn2;
+        } else {
+          wk.part_lse[(size_t)slot * NP + r] = lse2;
+        }
+      }
+      named_bar_sync(1, 128);
+      if (run) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
+      fence_after_sync();
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0, w.hk * G) + r;
+      float* part = wk.part_o + (size_t)slot * NP * D + r;
+      int i = 0, g = 0;  // token and head of the group of column n
+#pragma unroll
+      for (int c = 0; c < NP / 16; ++c) {
+        uint32_t o[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+              "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+            : "r"(tO + c * 16));
+        tmem_ld_wait();
+        if (r < D) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int n = c * 16 + k;
+            if (n < live) {
+              const float val = __uint_as_float(o[k]) * ctl.alpha[n];
+              if (whole)
+                out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
+              else
+                part[n * D] = val;
+            }
+            if (++g == G) {
+              g = 0;
+              ++i;
+            }
+          }
+        }
+      }
+      fence_before_sync();
+      if (run) mbar_arrive(bar(ctl.o_free[piece & 1]));
+      w.next();
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) {
+    // Copies still in flight land before the CTA exits: the last one issued into each buffer.
+    for (int i = max(0, ctl.issued_q - C::kQBufs); i < ctl.issued_q; ++i)
+      mbar_wait_drain(bar(ctl.q_full[i % C::kQBufs]), (i / C::kQBufs) & 1);
+    for (int i = max(0, ctl.issued_t - 2 * C::kStages); i < ctl.issued_t; ++i) {
+      const int t = i >> 1, st = t % C::kStages;
+      mbar_wait_drain((i & 1) ? bar(ctl.v_full[st]) : bar(ctl.k_full[st]), (t / C::kStages) & 1);
+    }
+  }
+}
+
+// Joins the pieces of each divided (sequence, head): M = max LSE, w = 2^(LSE - M), O = sum w O / sum w,
+// LSE = M + log2 sum w. Block c joins the one that ends in CTA c's first piece, if it began before.
+template <int D, int NP>
+__global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, const DecWork wk) {
+  grid_dependency_wait();
+  const int4 d = wk.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const PagedShape& s = a.s;
+  const SeqInfo seq = paged_seq(s, d.x);
+  const int G = s.H / s.Hkv, c1 = blockIdx.x;
+  for (int x = threadIdx.x; x < seq.Lq * G * (D / 4); x += 256) {
+    const int n = x / (D / 4), e = x % (D / 4) * 4;
+    auto slot = [&](int c) { return (size_t)(c == d.z ? d.w : 2 * c) * NP + n; };
+    float M = -INFINITY;
+    for (int c = d.z; c <= c1; ++c) M = fmaxf(M, wk.part_lse[slot(c)]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    if (M != -INFINITY)
+      for (int c = d.z; c <= c1; ++c) {
+        const float wt = exp2f(wk.part_lse[slot(c)] - M);
+        const float4 o = *reinterpret_cast<const float4*>(wk.part_o + slot(c) * D + e);
+        sum += wt;
+        acc.x += wt * o.x;
+        acc.y += wt * o.y;
+        acc.z += wt * o.z;
+        acc.w += wt * o.w;
+      }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int i = n / G, h = d.y * G + n % G;
+    uint2 v = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) = v;
+    if (e == 0) a.lse[paged_row(s, seq, d.x, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int D, int NP>
+cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
+  using C = DecCfg<D, NP>;
+  const PagedShape& s = a.s;
+  const bool packed = s.cu_q != nullptr;
+  const int P = 1 << s.page_shift, G = s.H / s.Hkv;
+  CUtensorMap tq, tk, tv;
+  // Q by tokens and heads: a box holds the G heads of a K/V head for Nq tokens, in row order token G + head.
+  if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
+                         G, s.Nq) ||
+      !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128) ||
+      !fa_make_tmap_bf16(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, P < 128 ? P : 128))
+    return cudaErrorInvalidValue;
+  DecWork wk;
+  char* ws = static_cast<char*>(a.workspace);
+  wk.desc = reinterpret_cast<int4*>(ws);
+  ws += up256((size_t)a.num_sms * sizeof(int4));
+  wk.part_lse = reinterpret_cast<float*>(ws);
+  ws += up256((size_t)a.num_sms * 2 * NP * sizeof(float));
+  wk.part_o = reinterpret_cast<float*>(ws);
+  auto kern = paged_decode_kernel<D, NP>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(a.num_sms), dim3(kDecThreads), C::kSmem, st, tq, tk, tv, a, wk);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_join_kernel<D, NP>, dim3(a.num_sms), dim3(256), 0, st, a, wk);
+}
+
+int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+}  // namespace
+}  // namespace fa
+
+size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms) {
+  const size_t rows = (size_t)num_sms * 2 * fa::padded_rows(s.Nq * (s.H / s.Hkv));
+  return fa::up256((size_t)num_sms * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
+}
+
+cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st) {
+  const int np = fa::padded_rows(a.s.Nq * (a.s.H / a.s.Hkv));
+  if (a.s.d == 64)
+    return np == 16   ? fa::launch_decode<64, 16>(a, st)
+           : np == 32 ? fa::launch_decode<64, 32>(a, st)
+                      : fa::launch_decode<64, 64>(a, st);
+  return np == 16   ? fa::launch_decode<128, 16>(a, st)
+         : np == 32 ? fa::launch_decode<128, 32>(a, st)
+                    : fa::launch_decode<128, 64>(a, st);
+}

@@ -333,14 +333,15 @@ typedef struct {
  * (decode), a few drafted ones and whole prompt chunks are the same call; rows of q outside every sequence are
  * neither read nor written.
  *   q, o         bf16, strides sq, so; lse fp32 as in fa_fwd_varlen ([B, H, seqlen_q], packed [H, rows_q])
- *   num_splits   1 .. 256: the keys are split into this many ranges of whole 128-key tiles whose partial results
- *                are merged by their log-sum-exp; fa_fwd_paged_splits(p, number of SMs) picks it
- *   workspace    device, >= fa_fwd_paged_workspace_bytes(p, num_splits) bytes, 256-byte aligned; may be NULL
- *                where that is 0 (one split)
+ *   num_sms      1 .. 1024: the CTAs that the work is divided among, one per SM (normally the device's SM count;
+ *                fewer leave SMs to other work). The division follows the lengths on the device: each CTA takes an
+ *                equal share of all key tiles, so one long sequence fills the GPU as many short ones do, and partial
+ *                results of divided sequences are merged by their log-sum-exp.
+ *   workspace    device, >= fa_fwd_paged_workspace_bytes(p, num_sms) bytes (it does not grow with the lengths),
+ *                256-byte aligned; scratch only
  */
-int fa_fwd_paged_splits(const fa_paged_problem* p, int num_sms);
-size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_splits);
-int fa_fwd_paged(const fa_paged_problem* p, int num_splits, const void* q, fa_strides sq, const void* k_cache,
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_sms);
+int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
                  fa_strides sk, const void* v_cache, fa_strides sv, void* o, fa_strides so, float* lse, void* workspace,
                  size_t workspace_bytes, int* dev_status, void* stream);
 

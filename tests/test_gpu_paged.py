@@ -151,11 +151,22 @@ def test_attend_packed(case, heads, causal):
     p.check_attend(o, l, causal)
 
 
-@pytest.mark.parametrize("splits", [1, 2, 3, 7, 64, 256])
+@pytest.mark.parametrize("sms", [1, 2, 3, 7, 64, 400])
 @pytest.mark.parametrize("n,heads", [(1, (4, 2, 128)), (3, (16, 2, 64)), (40, (8, 2, 128)), (90, (6, 2, 64))])
-def test_attend_any_split_count(n, heads, splits):
+def test_attend_any_division(n, heads, sms):
+    """The same work divided among 1 to 400 CTAs: pieces of any length, more CTAs than key tiles included."""
     p = Problem([1111, 250, 0, 1], [n] * 4, *heads, page=32, seed=n)
-    p.check_attend(*p.attend(True, num_splits=splits), True)
+    p.check_attend(*p.attend(True, num_sms=sms), True)
+
+
+def test_attend_many_sequences():
+    """More sequences than threads look for a CTA's share, many of them empty, in a packed batch with gaps."""
+    r = np.random.default_rng(12)
+    lk = r.integers(0, 300, 500) * (r.random(500) < 0.6)
+    lq = r.integers(0, 4, 500) * (r.random(500) < 0.7)
+    p = Problem(lk.tolist(), lq.tolist(), 4, 2, 64, page=32, packed=True, seed=13)
+    for sms in (1, 152):
+        p.check_attend(*p.attend(True, num_sms=sms), True)
 
 
 @pytest.mark.parametrize("n", [1, 4, 70])
@@ -423,19 +434,18 @@ def test_a_run_of_all_operators(heads):
 
 def test_captured_and_replayed_step_follows_the_lengths():
     """One decode step captured once, replayed with other lengths, rows and page tables in the same buffers, equals the
-    eager calls; two graphs share the split's workspace."""
+    eager calls; two graphs share the workspace."""
     p = Problem([700, 1200], [1, 1], 8, 2, 128, page=16, seed=92)
     q, k, v = p.cq.clone(), p.k_new.cuda(), p.v_new.cuda()
     bound = p.width * p.P
     prob = fa._paged(q, p.ck, p.cv, p.ctable, p.clen, None, None, bound, True, p.scale)[0]
-    splits = fa.fa_fwd_paged_splits(prob, torch.cuda.get_device_properties(0).multi_processor_count)
-    ws = torch.empty(max(1, fa.fa_fwd_paged_workspace_bytes(prob, splits)), dtype=torch.uint8, device="cuda")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty(fa.fa_fwd_paged_workspace_bytes(prob, sms), dtype=torch.uint8, device="cuda")
     state0 = [t.clone() for t in (p.ck, p.cv, p.cw)]
 
     def step():
         fa.paged_append(k, v, p.ck, p.cv, p.ctable, p.clen, key_weights=p.cw)
-        o, lse = fa.fwd_paged(q, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale, num_splits=splits,
-                              workspace=ws)
+        o, lse = fa.fwd_paged(q, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale, workspace=ws)
         fa.paged_key_weights(q, p.ck, p.ctable, p.clen, lse, p.cw, causal=True, scale=p.scale)
         kept, n = fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, p.clen, 500, recent=50)
         return o, lse, kept, n

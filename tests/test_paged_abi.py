@@ -27,8 +27,8 @@ SN = fa.Strides(2 * 128, 128, 3 * 2 * 128)
 SC = fa.Strides(2 * 128, 128, 16 * 2 * 128)
 
 
-def attend(p=None, splits=1, q=A, sq=SQ, k=A, sk=SC, v=A, sv=SC, o=A, so=SQ, lse=A, ws=None, nbytes=0, status=None):
-    return fa.fa_fwd_paged(p or problem(), splits, q, sq, k, sk, v, sv, o, so, lse, ws, nbytes, status, None)
+def attend(p=None, sms=152, q=A, sq=SQ, k=A, sk=SC, v=A, sv=SC, o=A, so=SQ, lse=A, ws=A, nbytes=1 << 30, status=None):
+    return fa.fa_fwd_paged(p or problem(), sms, q, sq, k, sk, v, sv, o, so, lse, ws, nbytes, status, None)
 
 
 def append(p=None, kn=A, skn=SN, vn=A, svn=SN, k=A, sk=SC, v=A, sv=SC, w=None, status=None):
@@ -64,7 +64,7 @@ def test_problem_refusals_of_calls_with_queries(kw, rc):
 
 
 def test_buffer_refusals():
-    for call, names in ((attend, "q k v o lse"), (append, "kn vn k v"), (weights, "q k lse w"), (evict, "k v w kept out")):
+    for call, names in ((attend, "q k v o lse ws"), (append, "kn vn k v"), (weights, "q k lse w"), (evict, "k v w kept out")):
         for n in names.split():
             assert call(**{n: None}) == -1, (call, n)
             assert call(**{n: A + 2}) == -3, (call, n)
@@ -78,23 +78,16 @@ def test_buffer_refusals():
     assert attend(sk=fa.Strides(256, 128, 1 << 39)) == -2
 
 
-def test_split_and_workspace_rules():
-    r256 = lambda x: (x + 255) // 256 * 256
+def test_workspace_rules():
     p = problem()
-    rows = 2 * 8 * 3
-    assert fa.fa_fwd_paged_workspace_bytes(p, 1) == 0
-    assert fa.fa_fwd_paged_workspace_bytes(p, 5) == r256(5 * rows * 4) + r256(5 * rows * 128 * 4)
-    assert fa.fa_fwd_paged_workspace_bytes(p, 0) == fa.fa_fwd_paged_workspace_bytes(p, 257) == 0
-    for splits, ws, nbytes, rc in ((0, A, 1 << 30, -1), (257, A, 1 << 30, -1), (4, None, 1 << 30, -1), (4, A, 16, -1),
-                                   (4, A + 16, 1 << 30, -3)):
-        assert attend(splits=splits, ws=ws, nbytes=nbytes) == rc
-    for B in (1, 4, 64, 4096):
-        for n in (1, 7, 500):
-            for bound in (1, 128, 1000, 100_000):
-                q = problem(B=B, seqlen_q=n, seqlen_k=bound, max_pages=10_000)
-                s = fa.fa_fwd_paged_splits(q, 152)
-                assert 1 <= s <= 256 and s <= max(1, -(-bound // 128)), (B, n, bound, s)
-    assert fa.fa_fwd_paged_splits(problem(d=96), 152) == 1
+    need = fa.fa_fwd_paged_workspace_bytes(p, 152)
+    assert need > 0 and need % 256 == 0
+    assert fa.fa_fwd_paged_workspace_bytes(problem(seqlen_k=16), 152) == need  # it does not grow with the lengths
+    assert fa.fa_fwd_paged_workspace_bytes(p, 0) == fa.fa_fwd_paged_workspace_bytes(p, 1025) == 0
+    assert fa.fa_fwd_paged_workspace_bytes(problem(d=96), 152) == 0
+    for sms, ws, nbytes, rc in ((0, A, 1 << 30, -1), (1025, A, 1 << 30, -1), (152, None, 1 << 30, -1),
+                                (152, A, need - 1, -1), (152, A + 16, 1 << 30, -3)):
+        assert attend(sms=sms, ws=ws, nbytes=nbytes) == rc
 
 
 def test_evict_budget_and_alias():
