@@ -340,9 +340,11 @@ bool paged_on_device(const fa::PagedShape& s) {
 
 constexpr int kMaxSms = 1024;  // CTAs that fa_fwd_paged may be divided among
 
+// Up to kPagedDecodeRows rows per K/V head the few-row kernel takes the call.
+bool few_rows(const fa::PagedShape& s) { return (long long)s.Nq * (s.H / s.Hkv) <= kPagedDecodeRows; }
+
 size_t paged_workspace(const fa::PagedShape& s, int num_sms) {
-  if ((long long)s.Nq * (s.H / s.Hkv) <= kPagedDecodeRows) return round_up(fa_paged_decode_workspace(s, num_sms));
-  return kAlign;
+  return round_up(few_rows(s) ? fa_paged_decode_workspace(s, num_sms) : fa_paged_chunk_workspace(s, num_sms));
 }
 
 }  // namespace
@@ -677,7 +679,9 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strid
   a.status = dev_status;
   a.num_sms = num_sms;
   a.workspace = workspace;
-  return fa_launch_fwd_paged(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = few_rows(a.s) ? fa_launch_paged_decode(a, st) : fa_launch_paged_chunk(a, st);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_new, const void* v_new,

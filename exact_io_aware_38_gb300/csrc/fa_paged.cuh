@@ -87,7 +87,9 @@ struct FaPagedArgs {
 constexpr int kPagedDecodeRows = 64;
 size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st);
-cudaError_t fa_launch_fwd_paged(const FaPagedArgs& a, cudaStream_t st);
+// Attention of more rows.
+size_t fa_paged_chunk_workspace(const fa::PagedShape& s, int num_sms);
+cudaError_t fa_launch_paged_chunk(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);

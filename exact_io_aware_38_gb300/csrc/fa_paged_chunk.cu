@@ -1,0 +1,653 @@
+// Attention of chunks of new tokens over a paged cache: more rows per K/V head than the few-row
+// kernel takes, so the pass is bound by the tensor cores (and by the exponentials beside them).
+//
+// What it computes: two 128-row query tiles share every 128-key tile; S = Q K^T, the online softmax
+// and O += P V as in the forward kernel over contiguous tensors, with P in tensor memory. A row of a
+// tile is a (token, head) pair: the gs query heads of a group lie side by side for each of tpt = 128 /
+// gs tokens, so a K/V tile serves all of them and a chunk of 32 tokens with 4 heads fills a tile.
+//
+// Division of the work: units (sequence, head group, pair of query tiles) of as many key tiles as
+// their last row sees stand in one line that the CTAs (one per SM, persistent) divide evenly; a unit
+// cut by a border leaves fp32 partials (two slots per CTA) that the merge kernel joins. A grid of one
+// CTA per unit instead runs in whole waves: 2048 tokens x 32 heads are 256 units on 152 SMs, 1.7
+// waves that take the time of 2.
+//
+// Roles (320 threads): warp 0 reads the page table and copies, warp 1 issues the MMAs, warps 2-5 and
+// 6-9 are the softmax of tile 0 and tile 1. Copies run ahead across units. Stage t of the ring holds
+// V of key tile t and K of key tile t + 1.
+// Tensor memory: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P over S.
+#include "fa_paged.cuh"
+#include "fa_softmax.cuh"
+#include "fa_tmap.h"
+
+namespace fa {
+namespace {
+
+using namespace tc;
+
+constexpr int kChThreads = 320;
+
+template <int D>
+struct ChCfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kSmem = 2 * kTileBytes + 2 * kStages * kTileBytes + 1024;
+  static constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+  static constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
+};
+
+struct ChCtl {
+  uint64_t q_full, q_empty, k0_full, k0_empty;
+  uint64_t full[4], empty[4];
+  uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t tail, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  long long scan[kChThreads / 32];
+  int b0, hv0, u0, kt0;
+  long long todo;
+  int first_cta, first_slot;
+  int issued_q, issued_k0, issued_t, issued_tail;  // copies issued (abort-path drain)
+};
+
+// How the rows are laid out: gs heads per group, Hv groups, tpt tokens per tile.
+struct ChRows {
+  int gs, Hv, per_kv, tpt;  // per_kv: groups per K/V head
+};
+
+struct JoinDesc {
+  int b, hv, u, first_cta, first_slot, pad[3];
+};
+
+struct ChWork {
+  float* part_o;    // [2 CTAs][256][D]
+  float* part_lse;  // [2 CTAs][256], log2 units
+  JoinDesc* desc;   // [CTAs]; b = -1: no unit ends here in pieces
+};
+
+// sum of floor((a i + b) / m) for 0 <= i < n (a, b >= 0), by Euclid's steps on (a, m).
+__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    n = top / m;
+    b = top % m;
+    const long long t = a;
+    a = m;
+    m = t;
+    if (m == 0) break;
+  }
+  return sum;
+}
+
+// The units of one sequence, for one head group: unit u has tokens [u U, u U + U).
+struct Units {
+  int U, nu, causal;
+  SeqInfo q;
+  __device__ Units(const PagedShape& s, const ChRows& c, int b) : U(2 * c.tpt), causal(s.causal), q(paged_seq(s, b)) {
+    nu = (q.Lq + U - 1) / U;
+  }
+  // Key tiles that token `last` of the sequence, and so any row before it, may see.
+  __device__ int tiles_to(int last) const {
+    const int keys = causal ? min(q.Lk, last + q.off + 1) : q.Lk;
+    return keys <= 0 ? 0 : (keys + 127) >> 7;
+  }
+  __device__ int tiles(int u) const { return max(1, tiles_to(min(q.Lq, (u + 1) * U) - 1)); }
+  // Key tiles of the units before u.
+  __device__ long long before(int u) const {
+    if (!causal) return (long long)u * max(1, tiles_to(q.Lq - 1));
+    long long sum = 0;
+    int n = u;
+    if (u == nu && u > 0) {
+      --n;
+      sum = tiles(n);
+    }
+    // The first units may see no key (more tokens than keys): one empty tile each.
+    const int none = q.off < 0 ? min(n, -q.off / U) : 0;
+    sum += none;
+    return sum + floor_sum(n - none, 128, U, (long long)q.off + (long long)(none + 1) * U + 127);
+  }
+};
+
+struct ChPieces {
+  const PagedShape& s;
+  const ChRows& c;
+  int b, hv, u, kt, n, end;
+  long long todo;
+  int nu;
+  SeqInfo seq;
+  __device__ ChPieces(const PagedShape& s_, const ChRows& c_, int b_, int hv_, int u_, int kt_, long long todo_)
+      : s(s_), c(c_), b(b_), hv(hv_), u(u_), kt(kt_), n(0), end(0), todo(todo_), nu(0) {
+    if (todo > 0) open();
+  }
+  __device__ void open() {
+    const Units x(s, c, b);
+    seq = x.q;
+    nu = x.nu;
+    if (nu == 0) return;
+    n = x.tiles(u);
+    end = kt + todo < n ? kt + (int)todo : n;
+  }
+  __device__ bool done() const { return todo == 0; }
+  __device__ bool whole() const { return kt == 0 && end == n; }
+  __device__ void next() {
+    todo -= end - kt;
+    kt = 0;
+    if (todo == 0) return;
+    if (++u == nu) {
+      u = 0;
+      if (++hv == c.Hv) {
+        hv = 0;
+        ++b;
+      }
+    }
+    open();
+    while (nu == 0) {  // todo > 0: a later sequence has units
+      ++b;
+      open();
+    }
+  }
+  // Key tiles query tile x sees, and whether it exists.
+  __device__ int tiles(int x) const {
+    const int first = (2 * u + x) * c.tpt, last = min(seq.Lq, first + c.tpt) - 1;
+    if (first >= seq.Lq) return 0;
+    const int keys = s.causal ? min(seq.Lk, last + seq.off + 1) : seq.Lk;
+    return keys <= 0 ? 0 : (keys + 127) >> 7;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kChThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const ChRows rows,
+                       const ChWork wk) {
+  using C = ChCfg<D>;
+  grid_dependency_wait();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ChCtl ctl;
+  const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;  // two tiles
+  const uint32_t sKV = sQ + 2 * C::kTileBytes;                // stage i: V then K
+  volatile int* abort_flag = &ctl.abort_flag;
+  const PagedShape& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto sV = [&](int i) { return sKV + 2 * i * C::kTileBytes; };
+  auto sK = [&](int i) { return sKV + (2 * i + 1) * C::kTileBytes; };
+  auto bar = [&](uint64_t& x) { return smem_u32(&x); };
+
+  if (threadIdx.x == 0) {
+    ctl.abort_flag = 0;
+    ctl.issued_q = ctl.issued_k0 = ctl.issued_t = ctl.issued_tail = 0;
+    ctl.todo = 0;
+    mbar_init(bar(ctl.q_full), 1);
+    mbar_init(bar(ctl.q_empty), 1);
+    mbar_init(bar(ctl.k0_full), 1);
+    mbar_init(bar(ctl.k0_empty), 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bar(ctl.full[i]), 1);
+      mbar_init(bar(ctl.empty[i]), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(ctl.s_full[x]), 1);
+      mbar_init(bar(ctl.p_ready[x]), 128);
+      mbar_init(bar(ctl.o_done[x]), 1);
+      mbar_init(bar(ctl.o_free[x]), 128);
+    }
+    mbar_init(bar(ctl.tail), 1);
+    mbar_init(bar(ctl.drain), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), 512);
+    tmem_relinquish();
+  }
+  // Rows of the query tiles that no copy fills are zero.
+  const int used = rows.gs * rows.tpt;
+  for (int i = threadIdx.x; i < 2 * (D / 64) * (128 - used) * 8; i += kChThreads) {
+    const int r = used + i / 8 % (128 - used), part = i / 8 / (128 - used);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sQ + (part * 128 + r) * 128 + (i & 7) * 16), "r"(0)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  {  // This CTA's share of the line of key tiles, and where it begins (as in the few-row kernel).
+    const int per = (s.B + kChThreads - 1) / kChThreads, first = threadIdx.x * per;
+    const int last = min(s.B, first + per);
+    auto tiles_of = [&](int b) {
+      const Units x(s, rows, b);
+      return x.before(x.nu) * rows.Hv;
+    };
+    long long mine = 0;
+    for (int b = first; b < last; ++b) mine += tiles_of(b);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) ctl.scan[warp] = inc;
+    __syncthreads();
+    long long base = inc - mine, total = 0;
+    for (int i = 0; i < kChThreads / 32; ++i) {
+      if (i < warp) base += ctl.scan[i];
+      total += ctl.scan[i];
+    }
+    const long long n = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
+    const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
+    if (lo < hi && lo >= base && lo < base + mine) {
+      int b = first;
+      long long at = base;
+      for (;; ++b) {
+        const long long t = tiles_of(b);
+        if (lo < at + t) break;
+        at += t;
+      }
+      const Units x(s, rows, b);
+      const long long each = x.before(x.nu);
+      const int hv = (int)((lo - at) / each);
+      at += hv * each;
+      int u = 0, top = x.nu;  // the last unit that begins at or before lo
+      while (top - u > 1) {
+        const int mid = (u + top) / 2;
+        if (x.before(mid) <= lo - at)
+          u = mid;
+        else
+          top = mid;
+      }
+      const long long start = at + x.before(u);
+      ctl.b0 = b;
+      ctl.hv0 = hv;
+      ctl.u0 = u;
+      ctl.kt0 = (int)(lo - start);
+      ctl.todo = hi - lo;
+      const long long c0 = ((start + 1) * n - 1) / total;
+      ctl.first_cta = (int)c0;
+      ctl.first_slot = 2 * (int)c0 + (total * c0 / n == start ? 0 : 1);
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;");
+  ChPieces w(s, rows, ctl.b0, ctl.hv0, ctl.u0, ctl.kt0, ctl.todo);
+  if (threadIdx.x == 0) {
+    JoinDesc d{};
+    d.b = !w.done() && w.kt > 0 && w.end == w.n ? w.b : -1;
+    d.hv = w.hv;
+    d.u = w.u;
+    d.first_cta = ctl.first_cta;
+    d.first_slot = ctl.first_slot;
+    wk.desc[blockIdx.x] = d;
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ copies
+    const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
+    bool run = true;
+    auto page_of = [&](const ChPieces& x, int kt) -> int {
+      const int key = (kt << 7) + (lane << shift);
+      return lane < per && key < x.seq.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
+    };
+    auto pages_in = [&](const ChPieces& x, int kt) -> int {
+      const int left = x.seq.Lk - (kt << 7);
+      return left <= 0 ? 0 : min(per, (left + prows - 1) >> shift);
+    };
+    auto copy = [&](uint32_t dst, const CUtensorMap* tm, const ChPieces& x, int kt, int page, uint32_t on) {
+      if (lane < pages_in(x, kt))
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(dst + c * 16384 + lane * prows * 128, tm, c * 64, (kt << 7) & (P - 1), x.hv / rows.per_kv, page,
+                      on);
+    };
+    auto copy_q = [&](const ChPieces& x, int piece) {
+      if (run && piece > 0) run = mbar_wait(bar(ctl.q_empty), (piece - 1) & 1, abort_flag, a.status);
+      run = __all_sync(0xffffffffu, run) && !*abort_flag;
+      if (!run || lane > 0) return;
+      const int tiles = (2 * x.u + 1) * rows.tpt < x.seq.Lq ? 2 : 1;
+      mbar_expect_tx(bar(ctl.q_full), tiles * used * D * 2);
+      for (int y = 0; y < tiles; ++y)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sQ + y * C::kTileBytes + c * 16384, &tmQ, c * 64, x.hv * rows.gs,
+                      x.seq.q0 + (2 * x.u + y) * rows.tpt, x.seq.bb, bar(ctl.q_full));
+      ctl.issued_q = piece + 1;
+    };
+    if (!w.done()) {
+      ChPieces v = w;  // the piece of the next K
+      int vkt = v.kt, vpiece = 0;
+      int page = page_of(w, w.kt);
+      copy_q(w, 0);
+      if (lane == 0) {
+        mbar_expect_tx(bar(ctl.k0_full), pages_in(w, w.kt) * prows * D * 2);
+        ctl.issued_k0 = 1;
+      }
+      __syncwarp();
+      copy(sK(C::kStages - 1), &tmK, w, w.kt, page, bar(ctl.k0_full));
+      int t = 0, tails = 0;
+      for (; !w.done(); w.next()) {
+        for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+          const int st = t % C::kStages;
+          if (++vkt == v.end) {
+            v.next();
+            vkt = 0;
+            ++vpiece;
+          }
+          const bool more = !v.done();
+          const int next = more ? page_of(v, vkt) : 0;
+          if (run && t == C::kStages - 1) run = mbar_wait(bar(ctl.k0_empty), 0, abort_flag, a.status);
+          if (run && t >= C::kStages)
+            run = mbar_wait(bar(ctl.empty[st]), (t / C::kStages - 1) & 1, abort_flag, a.status);
+          run = __all_sync(0xffffffffu, run) && !*abort_flag;
+          if (!run) continue;
+          const int valid = w.seq.Lk - (kt << 7);
+          const int vbytes = pages_in(w, kt) * prows * D * 2, kbytes = more ? pages_in(v, vkt) * prows * D * 2 : 0;
+          if (valid >= 128) {
+            if (lane == 0) {
+              mbar_expect_tx(bar(ctl.full[st]), vbytes + kbytes);
+              ctl.issued_t = t + 1;
+            }
+            __syncwarp();
+            copy(sV(st), &tmV, w, kt, page, bar(ctl.full[st]));
+            if (more) copy(sK(st), &tmK, v, vkt, next, bar(ctl.full[st]));
+          } else {
+            // The last tile: value rows past the last key may hold anything, and 0 times NaN is NaN.
+            // They become 0 here, between the copy of V (on a barrier of its own) and the stage.
+            if (lane == 0) {
+              mbar_add_tx(bar(ctl.full[st]), kbytes);
+              mbar_expect_tx(bar(ctl.tail), vbytes);
+              ctl.issued_t = t + 1;
+              ctl.issued_tail = tails + 1;
+            }
+            __syncwarp();
+            copy(sV(st), &tmV, w, kt, page, bar(ctl.tail));
+            if (more) copy(sK(st), &tmK, v, vkt, next, bar(ctl.full[st]));
+            run = mbar_wait(bar(ctl.tail), tails & 1, abort_flag, a.status);
+            run = __all_sync(0xffffffffu, run);
+            ++tails;
+            if (run)
+              for (int i = max(valid, 0) * (D / 8) + lane; i < 128 * (D / 8); i += 32) {
+                const int r = i / (D / 8), c = i % (D / 8);
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + (c >> 3) * 16384 + r * 128 +
+                                                                            (c & 7) * 16),
+                             "r"(0)
+                             : "memory");
+              }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ctl.full[st]));  // after a failed wait too: K may be in flight
+          }
+          if (more && vkt == 0) copy_q(v, vpiece);
+          page = next;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0 && !w.done()) {
+      bool run = true;
+      uint32_t np[2] = {0, 0}, pieces[2] = {0, 0};  // tiles whose P was awaited; pieces with tiles, per query tile
+      ChPieces v = w;
+      int vkt = v.kt, vpiece = 0;
+      int vn[2] = {v.tiles(0), v.tiles(1)};  // key tiles each query tile sees, in the piece of the next S
+      int wn[2] = {vn[0], vn[1]};
+      auto issue_s = [&](int x, uint32_t ka) {
+        const uint64_t dq = desc_kmajor_sw128(sQ + x * C::kTileBytes), dk = desc_kmajor_sw128(ka);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_ss(tmem + x * 128, desc_add(dq, off), desc_add(dk, off), C::kIdS, kk > 0);
+        }
+        mma_commit(bar(ctl.s_full[x]));
+      };
+      auto issue_pv = [&](int x, uint32_t va, bool first) {
+        const uint64_t dv = desc_mnmajor_sw128(va, 16384);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, desc_add(dv, kk * 2048), C::kIdPV,
+                 (first && kk == 0) ? 0u : 1u);
+      };
+      run = mbar_wait_spin(bar(ctl.q_full), 0, abort_flag, a.status);
+      if (run) run = mbar_wait_spin(bar(ctl.k0_full), 0, abort_flag, a.status);
+      fence_after_sync();
+      if (run) {
+        for (int x = 0; x < 2; ++x)
+          if (vkt < vn[x]) issue_s(x, sK(C::kStages - 1));
+        mma_commit(bar(ctl.k0_empty));
+        if (vkt + 1 == v.end) mma_commit(bar(ctl.q_empty));
+      }
+      int t = 0;
+      for (; !w.done() && run; w.next()) {
+        wn[0] = w.tiles(0);
+        wn[1] = w.tiles(1);
+        for (int kt = w.kt; kt < w.end && run; ++kt, ++t) {
+          const int st = t % C::kStages;
+          const bool crosses = ++vkt == v.end;  // the next S belongs to the next piece
+          if (crosses) {
+            v.next();
+            vkt = 0;
+            ++vpiece;
+            if (!v.done()) {
+              vn[0] = v.tiles(0);
+              vn[1] = v.tiles(1);
+            }
+          }
+          const bool more = !v.done();
+          run = mbar_wait_spin(bar(ctl.full[st]), (t / C::kStages) & 1, abort_flag, a.status);
+          for (int x = 0; x < 2 && run; ++x) {
+            if (kt < wn[x]) {
+              if (kt == w.kt) {  // O still holds the last piece's until its epilogue has read it
+                if (pieces[x] > 0)
+                  run = mbar_wait_spin(bar(ctl.o_free[x]), (pieces[x] - 1) & 1, abort_flag, a.status);
+                ++pieces[x];
+              }
+              if (run) run = mbar_wait_spin(bar(ctl.p_ready[x]), np[x] & 1, abort_flag, a.status);
+              ++np[x];
+              fence_after_sync();
+              if (!run) break;
+              issue_pv(x, sV(st), kt == w.kt);
+              if (kt + 1 == min(w.end, wn[x])) mma_commit(bar(ctl.o_done[x]));
+            }
+            if (more && !crosses && vkt < vn[x]) issue_s(x, sK(st));
+          }
+          if (!run) break;
+          if (crosses && more) {
+            run = mbar_wait_spin(bar(ctl.q_full), vpiece & 1, abort_flag, a.status);
+            fence_after_sync();
+            if (!run) break;
+            for (int x = 0; x < 2; ++x)
+              if (vkt < vn[x]) issue_s(x, sK(st));
+          }
+          if (more && vkt + 1 == v.end) mma_commit(bar(ctl.q_empty));
+          mma_commit(bar(ctl.empty[st]));
+        }
+      }
+      mma_commit(bar(ctl.drain));
+      mbar_wait_drain(bar(ctl.drain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, epilogue
+    const int x = (warp - 2) >> 2;
+    const int quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + x * 128, tO = tmem + lane_off + 256 + x * D;
+    const float sl2 = a.scale * kLog2e;
+    const int ti = r / rows.gs, g = r - ti * rows.gs;  // token within the tile, head within the group
+    bool run = true;
+    uint32_t cnt = 0, pieces = 0;
+    for (int piece = 0; !w.done(); ++piece, w.next()) {
+      const SeqInfo& seq = w.seq;
+      const int first = (2 * w.u + x) * rows.tpt;  // the tile's first token
+      if (first >= seq.Lq) continue;
+      const int i = first + ti;
+      const bool live = r < used && i < seq.Lq;
+      const int end = min(w.end, w.tiles(x));
+      float m = -INFINITY, l = 0.f;
+      for (int kt = w.kt; kt < end; ++kt, ++cnt) {
+        if (run) run = mbar_wait(bar(ctl.s_full[x]), cnt & 1, abort_flag, a.status);
+        fence_after_sync();
+        const int k0 = kt << 7;
+        const bool masked = (s.causal && k0 + 127 > first + seq.off) || k0 + 128 > seq.Lk;
+        const int lim = min(seq.Lk - k0, s.causal ? i + seq.off - k0 + 1 : 128);  // keys [k0, k0 + lim) visible
+        softmax_tile<D, false, 1>(tS, tO, tS, masked, lim, sl2, kt == w.kt, m, l, [] {});
+        fence_before_sync();
+        if (run) mbar_arrive(bar(ctl.p_ready[x]));
+      }
+      const bool any = w.kt < end;
+      if (any) {
+        if (run) run = mbar_wait(bar(ctl.o_done[x]), pieces & 1, abort_flag, a.status);
+        ++pieces;
+        fence_after_sync();
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f, lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+      const bool whole = w.whole();
+      const size_t slot = (size_t)(2 * blockIdx.x + (piece == 0 ? 0 : 1)) * 256 + x * 128 + r;
+      const int h = w.hv * rows.gs + g;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h);
+      float* part = wk.part_o + slot * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tmem_ld32(tO + c * 32, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (live && whole) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(out + c * 32 + k) =
+                make_uint4(pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
+                           pack_bf16x2(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
+                           pack_bf16x2(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
+                           pack_bf16x2(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+        } else if (live) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(part + c * 32 + k) =
+                make_float4(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv,
+                            __uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
+        }
+        __syncwarp();  // the next load is the whole warp's
+      }
+      if (any) {
+        fence_before_sync();
+        if (run) mbar_arrive(bar(ctl.o_free[x]));
+      }
+      if (live) {
+        if (whole)
+          a.lse[paged_row(s, seq, w.b, h, i)] = lse2 * kLn2;
+        else
+          wk.part_lse[slot] = lse2;
+      }
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) {
+    // Copies still in flight land before the CTA exits: the last ones issued on each barrier.
+    if (ctl.issued_q > 0) mbar_wait_drain(bar(ctl.q_full), (ctl.issued_q - 1) & 1);
+    if (ctl.issued_k0 > 0) mbar_wait_drain(bar(ctl.k0_full), 0);
+    if (ctl.issued_tail > 0) mbar_wait_drain(bar(ctl.tail), (ctl.issued_tail - 1) & 1);
+    for (int t = max(0, ctl.issued_t - C::kStages); t < ctl.issued_t; ++t)
+      mbar_wait_drain(bar(ctl.full[t % C::kStages]), (t / C::kStages) & 1);
+  }
+}
+
+// Joins the pieces of each divided unit by their log-sum-exp. Block (c, y) takes 32 rows of the unit
+// that ends in CTA c's first piece, if it began before.
+template <int D>
+__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs a, const ChRows rows,
+                                                               const ChWork wk) {
+  grid_dependency_wait();
+  const JoinDesc d = wk.desc[blockIdx.x];
+  if (d.b < 0) return;
+  const PagedShape& s = a.s;
+  const SeqInfo seq = paged_seq(s, d.b);
+  for (int y = threadIdx.x; y < 32 * (D / 4); y += 256) {
+    const int r = blockIdx.y * 32 + y / (D / 4), e = y % (D / 4) * 4;
+    const int rr = r & 127, i = (2 * d.u + (r >> 7)) * rows.tpt + rr / rows.gs, h = d.hv * rows.gs + rr % rows.gs;
+    if (rr >= rows.gs * rows.tpt || i >= seq.Lq) continue;
+    auto slot = [&](int c) { return (size_t)(c == d.first_cta ? d.first_slot : 2 * c) * 256 + r; };
+    float M = -INFINITY;
+    for (int c = d.first_cta; c <= (int)blockIdx.x; ++c) M = fmaxf(M, wk.part_lse[slot(c)]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    if (M != -INFINITY)
+      for (int c = d.first_cta; c <= (int)blockIdx.x; ++c) {
+        const float wt = exp2f(wk.part_lse[slot(c)] - M);
+        const float4 o = *reinterpret_cast<const float4*>(wk.part_o + slot(c) * D + e);
+        sum += wt;
+        acc.x += wt * o.x;
+        acc.y += wt * o.y;
+        acc.z += wt * o.z;
+        acc.w += wt * o.w;
+      }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (e == 0) a.lse[paged_row(s, seq, d.b, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The heads of a group: the divisor of G that fills the 128 rows of a tile best, the largest of equals
+// (a K/V tile then serves more heads).
+ChRows rows_for(const PagedShape& s) {
+  const int G = s.H / s.Hkv;
+  int best = 1;
+  for (int g = 1; g <= G && g <= 128; ++g)
+    if (G % g == 0 && 128 / g * g >= 128 / best * best) best = g;
+  return {best, s.H / best, G / best, 128 / best};
+}
+
+template <int D>
+cudaError_t launch_chunk(const FaPagedArgs& a, cudaStream_t st) {
+  using C = ChCfg<D>;
+  const PagedShape& s = a.s;
+  const bool packed = s.cu_q != nullptr;
+  const int P = 1 << s.page_shift;
+  const ChRows rows = rows_for(s);
+  CUtensorMap tq, tk, tv;
+  if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
+                         rows.gs, rows.tpt) ||
+      !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128) ||
+      !fa_make_tmap_bf16(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, P < 128 ? P : 128))
+    return cudaErrorInvalidValue;
+  ChWork wk;
+  char* ws = static_cast<char*>(a.workspace);
+  wk.desc = reinterpret_cast<JoinDesc*>(ws);
+  ws += up256((size_t)a.num_sms * sizeof(JoinDesc));
+  wk.part_lse = reinterpret_cast<float*>(ws);
+  ws += up256((size_t)a.num_sms * 512 * sizeof(float));
+  wk.part_o = reinterpret_cast<float*>(ws);
+  auto kern = paged_chunk_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(a.num_sms), dim3(kChThreads), C::kSmem, st, tq, tk, tv, a, rows, wk);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_chunk_join_kernel<D>, dim3(a.num_sms, 8), dim3(256), 0, st, a, rows, wk);
+}
+
+}  // namespace
+}  // namespace fa
+
+size_t fa_paged_chunk_workspace(const fa::PagedShape& s, int num_sms) {
+  const size_t rows = (size_t)num_sms * 512;
+  return fa::up256((size_t)num_sms * sizeof(fa::JoinDesc)) + fa::up256(rows * sizeof(float)) +
+         rows * s.d * sizeof(float);
+}
+
+cudaError_t fa_launch_paged_chunk(const FaPagedArgs& a, cudaStream_t st) {
+  return a.s.d == 64 ? fa::launch_chunk<64>(a, st) : fa::launch_chunk<128>(a, st);
+}

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             ctl.alpha[r] = ex2_approx(old - now);
             ctl.m[r] = now;
           }
+          __syncwarp();
           named_bar_sync(1, 128);
           if (!opens) {
             if (run) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
@@ -470,6 +471,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                                                                           (c & 7) * 16),
                            "r"(0)
                            : "memory");
+          __syncwarp();
         }
         fence_proxy_async_smem();
         fence_before_sync();
@@ -492,6 +494,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           wk.part_lse[(size_t)slot * NP + r] = lse2;
         }
       }
+      __syncwarp();
       named_bar_sync(1, 128);
       if (run) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
       fence_after_sync();

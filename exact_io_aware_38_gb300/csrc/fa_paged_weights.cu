@@ -20,52 +20,6 @@ __device__ __forceinline__ void load_row(const void* base, size_t off, int lane,
   for (int e = 0; e < D / 32; ++e) x[e] = __bfloat162float(p[e]);
 }
 
-// One warp per (sequence, head, new token); lane l holds elements [l D/32, (l + 1) D/32) of q, k, v, o.
-template <int D>
-__global__ void __launch_bounds__(256) paged_rows_kernel(const FaPagedArgs a) {
-  grid_dependency_wait();
-  constexpr int PER = D / 32;
-  const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31;
-  const size_t rows = (size_t)s.B * s.H * s.Nq;
-  const size_t step = ((size_t)gridDim.x * blockDim.x) >> 5;
-  for (size_t w = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < rows; w += step) {
-    const int i = (int)(w % s.Nq), h = (int)(w / s.Nq % s.H), b = (int)(w / s.Nq / s.H);
-    const SeqInfo seq = paged_seq(s, b);
-    if (i >= seq.Lq) continue;
-    const int hk = h / (s.H / s.Hkv);
-    float q[PER], k[PER], acc[PER];
-    load_row<D>(a.q, elem_offset(a.sq, seq.bb, seq.q0 + i, h), lane, q);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    const int n = s.causal ? min(seq.Lk, i + seq.off + 1) : seq.Lk;
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j) {
-      const int page = paged_page(s, b, j >> s.page_shift, a.status);
-      if (page < 0) continue;
-      const int slot = j & ((1 << s.page_shift) - 1);
-      load_row<D>(a.k, paged_offset(a.sk, page, slot, hk), lane, k);
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) x += q[e] * k[e];
-      x = warp_sum(x) * a.scale;
-      const float mn = fmaxf(m, x);
-      if (mn == -INFINITY) continue;
-      const float alpha = expf(m - mn), p = expf(x - mn);
-      load_row<D>(a.v, paged_offset(a.sv, page, slot, hk), lane, k);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = acc[e] * alpha + p * k[e];
-      l = l * alpha + p;
-      m = mn;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) out[e] = __float2bfloat16(acc[e] * inv);
-    if (lane == 0) a.lse[paged_row(s, seq, b, h, i)] = l > 0.f ? m + logf(l) : -INFINITY;
-  }
-}
-
 // One warp per (sequence, K/V head, key): the rows that see the key, in order.
 template <int D>
 __global__ void __launch_bounds__(256) paged_keys_kernel(const FaPagedArgs a) {
@@ -109,12 +63,6 @@ int grid_for(size_t warps) {
 
 }  // namespace
 }  // namespace fa
-
-cudaError_t fa_launch_fwd_paged(const FaPagedArgs& a, cudaStream_t st) {
-  if (a.s.Nq * (a.s.H / a.s.Hkv) <= kPagedDecodeRows) return fa_launch_paged_decode(a, st);
-  auto k = a.s.d == 64 ? fa::paged_rows_kernel<64> : fa::paged_rows_kernel<128>;
-  return launch_dependent(k, dim3(fa::grid_for((size_t)a.s.B * a.s.H * a.s.Nq)), dim3(256), 0, st, a);
-}
 
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st) {
   auto k = a.s.d == 64 ? fa::paged_keys_kernel<64> : fa::paged_keys_kernel<128>;

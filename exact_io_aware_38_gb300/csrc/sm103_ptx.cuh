@@ -50,6 +50,10 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar), "r"(bytes)
                : "memory");
 }
+// More bytes to come in the current phase, without an arrival (one follows).
+__device__ __forceinline__ void mbar_add_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 // Test whether the phase with the given parity has completed. If it has not, the thread is
 // suspended until it completes or kSuspendNs pass, so waiting warps leave the issue slots of
 // their SM sub-partition to the warps that compute.
