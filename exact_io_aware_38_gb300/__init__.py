@@ -9,7 +9,7 @@ Raw C-ABI names (same signatures as ``include/fa.h``, pointers as ints):
     fa_status_string, fa_bwd_noalloc,
     fa_fwd_varlen, fa_bwd_varlen, fa_bwd_varlen_accumulate, fa_bwd_varlen_workspace_bytes (with the Strides /
     VarlenProblem structs), fa_fwd_paged_workspace_bytes, fa_fwd_paged, fa_paged_append,
-    fa_paged_key_weights, fa_paged_evict (with the PagedProblem struct)
+    fa_paged_key_weights, fa_paged_key_weights_workspace_bytes, fa_paged_evict (with the PagedProblem struct)
 Tensor helpers (grouped-query attention when k, v have fewer heads than q):
     fwd(q, k, v, ...) -> (o, lse);  bwd(q, k, v, o, lse, do, ...) -> (dq, dk, dv)
     fwd_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, ...) -> (o, lse): e4m3 inputs (fa_fwd_fp8)
@@ -100,7 +100,8 @@ _SIGS = {
     "fa_fwd_paged": (_I, [_PP, _I, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, ctypes.c_size_t, _P,
                           _P]),
     "fa_paged_append": (_I, [_PP, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, _P]),
-    "fa_paged_key_weights": (_I, [_PP, _P, Strides, _P, Strides, _P, _P, _P, _P]),
+    "fa_paged_key_weights_workspace_bytes": (ctypes.c_size_t, [_PP, _I]),
+    "fa_paged_key_weights": (_I, [_PP, _I, _P, Strides, _P, Strides, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "fa_paged_evict": (_I, [_PP, _I, _I, _P, Strides, _P, Strides, _P, _P, _P, _P, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P]),
@@ -222,8 +223,14 @@ def fa_paged_append(p, k_new, sk_new, v_new, sv_new, k_cache, sk, v_cache, sv, k
                                      key_weights, dev_status, stream))
 
 
-def fa_paged_key_weights(p, q, sq, k_cache, sk, lse, key_weights, dev_status, stream) -> int:
-    return int(lib().fa_paged_key_weights(ctypes.byref(p), q, sq, k_cache, sk, lse, key_weights, dev_status, stream))
+def fa_paged_key_weights_workspace_bytes(p, num_sms) -> int:
+    return int(lib().fa_paged_key_weights_workspace_bytes(ctypes.byref(p), num_sms))
+
+
+def fa_paged_key_weights(p, num_sms, q, sq, k_cache, sk, lse, key_weights, workspace, workspace_bytes, dev_status,
+                         stream) -> int:
+    return int(lib().fa_paged_key_weights(ctypes.byref(p), num_sms, q, sq, k_cache, sk, lse, key_weights, workspace,
+                                          workspace_bytes, dev_status, stream))
 
 
 def fa_paged_evict(p, keep, recent, k_cache, sk, v_cache, sv, key_weights, kept, seqlens_out, dev_status,
@@ -688,7 +695,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=Non
 
 
 def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_seqlens_q=None, max_seqlen_q=None,
-                      max_seqlen_k=None, *, causal=False, scale=None, status=None, stream=None):
+                      max_seqlen_k=None, *, num_sms=None, causal=False, scale=None, workspace=None, status=None,
+                      stream=None):
     """Add to key_weights (float32 [num_pages, Hkv, page_size]), in place, the attention weight that the rows of q pay
     every cached key, summed over the rows and the query heads of each K/V head (fa_paged_key_weights). q, lse and the
     other arguments are those of fwd_paged, which returned lse."""
@@ -697,9 +705,17 @@ def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_se
     _check_aux("status", status, torch.int32, 1, q.device)
     _check_weights(key_weights, p, q.device)
     sq, sk = _paged_view("q", q, dims), _paged_view("k_cache", k_cache, 4)
-    if q.numel() > 0:
-        _launch(q.device, stream, lambda st: fa_paged_key_weights(
-            p, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(), key_weights.data_ptr(), _ptr(status), st))
+    if q.numel() == 0:
+        return key_weights
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(q.device).multi_processor_count
+    nbytes = fa_paged_key_weights_workspace_bytes(p, num_sms)
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _check_aux("workspace", workspace, None, nbytes, q.device)
+    _launch(q.device, stream, lambda st: fa_paged_key_weights(
+        p, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(), key_weights.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status), st))
     return key_weights
 
 

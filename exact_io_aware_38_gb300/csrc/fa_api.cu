@@ -340,11 +340,8 @@ bool paged_on_device(const fa::PagedShape& s) {
 
 constexpr int kMaxSms = 1024;  // CTAs that fa_fwd_paged may be divided among
 
-// Up to kPagedDecodeRows rows per K/V head the few-row kernel takes the call.
-bool few_rows(const fa::PagedShape& s) { return (long long)s.Nq * (s.H / s.Hkv) <= kPagedDecodeRows; }
-
 size_t paged_workspace(const fa::PagedShape& s, int num_sms) {
-  return round_up(few_rows(s) ? fa_paged_decode_workspace(s, num_sms) : fa_paged_chunk_workspace(s, num_sms));
+  return round_up(fa::paged_few_rows(s) ? fa_paged_decode_workspace(s, num_sms) : fa_paged_chunk_workspace(s, num_sms));
 }
 
 }  // namespace
@@ -680,7 +677,7 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strid
   a.num_sms = num_sms;
   a.workspace = workspace;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = few_rows(a.s) ? fa_launch_paged_decode(a, st) : fa_launch_paged_chunk(a, st);
+  const cudaError_t e = fa::paged_few_rows(a.s) ? fa_launch_paged_decode(a, st) : fa_launch_paged_chunk(a, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -710,20 +707,32 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
   return fa_launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-int fa_paged_key_weights(const fa_paged_problem* p, const void* q, fa_strides sq, const void* k_cache, fa_strides sk,
-                         const float* lse, float* key_weights, int* dev_status, void* stream) {
+size_t fa_paged_key_weights_workspace_bytes(const fa_paged_problem* p, int num_sms) {
+  fa::PagedShape s;
+  if (paged_shape(p, true, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
+  return round_up(fa_paged_weights_workspace(num_sms));
+}
+
+int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
+                         fa_strides sk, const float* lse, float* key_weights, void* workspace, size_t workspace_bytes,
+                         int* dev_status, void* stream) {
   FaPagedArgs a{};
   int rc = paged_shape(p, true, &a.s);
   if (rc != FA_OK) return rc;
+  if (num_sms < 1 || num_sms > kMaxSms || workspace == nullptr ||
+      workspace_bytes < round_up(fa_paged_weights_workspace(num_sms)))
+    return FA_ERR_INVALID_ARG;
   const bool packed = a.s.cu_q != nullptr;
   if ((rc = take_strides(sq, packed, a.s.B, packed ? a.s.rows_q : a.s.Nq, a.s.H, &a.sq)) != FA_OK ||
       (rc = take_cache_strides(sk, p, &a.sk)) != FA_OK)
     return rc;
   if (!q || !k_cache || !lse || !key_weights) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(key_weights, 4) ||
-      !aligned(dev_status, 4))
+      !aligned(dev_status, 4) || !aligned(workspace, kAlign))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
+  a.num_sms = num_sms;
+  a.workspace = workspace;
   a.q = q;
   a.k = const_cast<void*>(k_cache);
   a.lse = const_cast<float*>(lse);

@@ -63,6 +63,46 @@ __device__ __forceinline__ size_t weight_offset(const PagedShape& s, int page, i
   return (((size_t)page * s.Hkv + hk) << s.page_shift) + slot;
 }
 
+// How query rows lie in tiles: gs heads side by side for each of tpt tokens; Hv such groups of heads,
+// per_kv of them per K/V head.
+struct PagedRows {
+  int gs, Hv, per_kv, tpt;
+};
+
+// 128-row tiles: the divisor of the heads per K/V head that fills the rows best, the largest of equals
+// (a K/V tile then serves more heads).
+inline PagedRows paged_rows_for(const PagedShape& s) {
+  const int G = s.H / s.Hkv;
+  int best = 1;
+  for (int g = 1; g <= G && g <= 128; ++g)
+    if (G % g == 0 && 128 / g * g >= 128 / best * best) best = g;
+  return {best, s.H / best, G / best, 128 / best};
+}
+
+// Up to 64 rows (tokens x heads of one K/V head) fit the few-row kernels: one tile of 16, 32 or 64
+// columns per K/V head.
+inline bool paged_few_rows(const PagedShape& s) { return (long long)s.Nq * (s.H / s.Hkv) <= 64; }
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// sum of floor((a i + b) / m) for 0 <= i < n (a, b >= 0), by Euclid's steps on (a, m).
+__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    n = top / m;
+    b = top % m;
+    const long long t = a;
+    a = m;
+    m = t;
+    if (m == 0) break;
+  }
+  return sum;
+}
+
 }  // namespace fa
 
 struct FaPagedArgs {
@@ -83,13 +123,12 @@ struct FaPagedArgs {
   int32_t *kept, *seqlens_out;
 };
 
-// Attention of at most kPagedDecodeRows rows (tokens x grouped heads) per sequence and K/V head.
-constexpr int kPagedDecodeRows = 64;
+// Attention of few rows (paged_few_rows) and of more, with the workspace each needs.
 size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st);
-// Attention of more rows.
 size_t fa_paged_chunk_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_chunk(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
+size_t fa_paged_weights_workspace(int num_sms);
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);

@@ -50,11 +50,6 @@ struct ChCtl {
   int issued_q, issued_k0, issued_t, issued_tail;  // copies issued (abort-path drain)
 };
 
-// How the rows are laid out: gs heads per group, Hv groups, tpt tokens per tile.
-struct ChRows {
-  int gs, Hv, per_kv, tpt;  // per_kv: groups per K/V head
-};
-
 struct JoinDesc {
   int b, hv, u, first_cta, first_slot, pad[3];
 };
@@ -65,29 +60,11 @@ struct ChWork {
   JoinDesc* desc;   // [CTAs]; b = -1: no unit ends here in pieces
 };
 
-// sum of floor((a i + b) / m) for 0 <= i < n (a, b >= 0), by Euclid's steps on (a, m).
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long sum = 0;
-  while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long top = a * n + b;
-    n = top / m;
-    b = top % m;
-    const long long t = a;
-    a = m;
-    m = t;
-    if (m == 0) break;
-  }
-  return sum;
-}
-
 // The units of one sequence, for one head group: unit u has tokens [u U, u U + U).
 struct Units {
   int U, nu, causal;
   SeqInfo q;
-  __device__ Units(const PagedShape& s, const ChRows& c, int b) : U(2 * c.tpt), causal(s.causal), q(paged_seq(s, b)) {
+  __device__ Units(const PagedShape& s, const PagedRows& c, int b) : U(2 * c.tpt), causal(s.causal), q(paged_seq(s, b)) {
     nu = (q.Lq + U - 1) / U;
   }
   // Key tiles that token `last` of the sequence, and so any row before it, may see.
@@ -114,12 +91,12 @@ struct Units {
 
 struct ChPieces {
   const PagedShape& s;
-  const ChRows& c;
+  const PagedRows& c;
   int b, hv, u, kt, n, end;
   long long todo;
   int nu;
   SeqInfo seq;
-  __device__ ChPieces(const PagedShape& s_, const ChRows& c_, int b_, int hv_, int u_, int kt_, long long todo_)
+  __device__ ChPieces(const PagedShape& s_, const PagedRows& c_, int b_, int hv_, int u_, int kt_, long long todo_)
       : s(s_), c(c_), b(b_), hv(hv_), u(u_), kt(kt_), n(0), end(0), todo(todo_), nu(0) {
     if (todo > 0) open();
   }
@@ -162,7 +139,7 @@ struct ChPieces {
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const ChRows rows,
+                       const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const PagedRows rows,
                        const ChWork wk) {
   using C = ChCfg<D>;
   grid_dependency_wait();
@@ -566,7 +543,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
 // Joins the pieces of each divided unit by their log-sum-exp. Block (c, y) takes 32 rows of the unit
 // that ends in CTA c's first piece, if it began before.
 template <int D>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs a, const ChRows rows,
+__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs a, const PagedRows rows,
                                                                const ChWork wk) {
   grid_dependency_wait();
   const JoinDesc d = wk.desc[blockIdx.x];
@@ -599,25 +576,13 @@ __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs
   }
 }
 
-constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
-// The heads of a group: the divisor of G that fills the 128 rows of a tile best, the largest of equals
-// (a K/V tile then serves more heads).
-ChRows rows_for(const PagedShape& s) {
-  const int G = s.H / s.Hkv;
-  int best = 1;
-  for (int g = 1; g <= G && g <= 128; ++g)
-    if (G % g == 0 && 128 / g * g >= 128 / best * best) best = g;
-  return {best, s.H / best, G / best, 128 / best};
-}
-
 template <int D>
 cudaError_t launch_chunk(const FaPagedArgs& a, cudaStream_t st) {
   using C = ChCfg<D>;
   const PagedShape& s = a.s;
   const bool packed = s.cu_q != nullptr;
   const int P = 1 << s.page_shift;
-  const ChRows rows = rows_for(s);
+  const PagedRows rows = paged_rows_for(s);
   CUtensorMap tq, tk, tv;
   if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
                          rows.gs, rows.tpt) ||

@@ -378,11 +378,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         {
           uint32_t(&u)[NP] = reinterpret_cast<uint32_t(&)[NP]>(x);
           if constexpr (NP == 16) {
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-                  "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-                : "r"(tmem + lane_off + (t & 1) * NP));
+            tmem_ld16(tmem + lane_off + (t & 1) * NP, u);
           } else {
 #pragma unroll
             for (int c = 0; c < NP / 32; ++c)
@@ -429,11 +425,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
             for (int c = 0; c < NP / 16; ++c) {
               uint32_t o[16];
-              asm volatile(
-                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                    "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                  : "r"(tO + c * 16));
+              tmem_ld16(tO + c * 16, o);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -504,11 +496,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
       for (int c = 0; c < NP / 16; ++c) {
         uint32_t o[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-              "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-            : "r"(tO + c * 16));
+        tmem_ld16(tO + c * 16, o);
         tmem_ld_wait();
         if (r < D) {
 #pragma unroll
@@ -585,8 +573,6 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, co
     if (e == 0) a.lse[paged_row(s, seq, d.x, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
   }
 }
-
-constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <int D, int NP>
 cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {

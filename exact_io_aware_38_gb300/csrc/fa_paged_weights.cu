@@ -1,70 +1,518 @@
-// Attention of new tokens over a paged K/V cache, and the attention weight each cached key receives.
+// The attention weight that new tokens pay every cached key: W[j] += sum over the rows i that see key
+// j of exp(c q_i k_j - LSE_i), with the LSE known from the attention itself.
 //
-// First form, one warp per query row (or per key): the row max and row sum run along (online softmax),
-// so nothing of the size keys x rows is stored. Bound by instructions, not by memory.
+// S^T = K Q^T puts a key on each tensor-memory lane and a row on each column, so a key's sum over the
+// rows stays within one thread: no value crosses threads, no atomics, and K is read once. With few
+// rows (one query tile) the pass streams K and is bound by memory; with many it is bound by the
+// exponentials, one per (row, key) pair.
+//
+// Division of the work: units (sequence, K/V head, key tile) of as many query tiles as see the key
+// tile stand in one line that the CTAs (one per SM, persistent) divide evenly. A unit cut by a border
+// leaves 128 partial sums per piece (two slots per CTA), which the join kernel adds in the pieces'
+// order; with one query tile per unit nothing is cut.
+//
+// Roles (320 threads): warp 0 reads the page table and copies, warp 1 issues the MMAs, warps 2-5 and
+// 6-9 are two groups that take the query tiles in turn (one reads its scores while the other waits).
+// Tensor memory: four score buffers of NP columns.
 #include "fa_paged.cuh"
+#include "fa_tmap.h"
+#include "sm103_ptx.cuh"
 
 namespace fa {
 namespace {
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+using namespace tc;
 
-template <int D>
-__device__ __forceinline__ void load_row(const void* base, size_t off, int lane, float (&x)[D / 32]) {
-  const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(base) + off + lane * (D / 32);
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) x[e] = __bfloat162float(p[e]);
-}
+constexpr int kWThreads = 320;
 
-// One warp per (sequence, K/V head, key): the rows that see the key, in order.
-template <int D>
-__global__ void __launch_bounds__(256) paged_keys_kernel(const FaPagedArgs a) {
-  grid_dependency_wait();
-  constexpr int PER = D / 32;
-  const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31, G = s.H / s.Hkv;
-  const size_t keys = (size_t)s.B * s.Hkv * s.max_k;
-  const size_t step = ((size_t)gridDim.x * blockDim.x) >> 5;
-  for (size_t w = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < keys; w += step) {
-    const int j = (int)(w % s.max_k), hk = (int)(w / s.max_k % s.Hkv), b = (int)(w / s.max_k / s.Hkv);
-    const SeqInfo seq = paged_seq(s, b);
-    if (j >= seq.Lk) continue;
-    const int page = paged_page(s, b, j >> s.page_shift, a.status);
-    if (page < 0) continue;
-    const int slot = j & ((1 << s.page_shift) - 1);
-    float k[PER], q[PER];
-    load_row<D>(a.k, paged_offset(a.sk, page, slot, hk), lane, k);
-    float sum = 0.f;
-    for (int i = s.causal ? max(0, j - seq.off) : 0; i < seq.Lq; ++i)
-      for (int h = hk * G; h < hk * G + G; ++h) {
-        load_row<D>(a.q, elem_offset(a.sq, seq.bb, seq.q0 + i, h), lane, q);
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) x += q[e] * k[e];
-        x = warp_sum(x) * a.scale;
-        const float lse = a.lse[paged_row(s, seq, b, h, i)];
-        if (lse != -INFINITY) sum += expf(x - lse);
+// NP: rows of a query tile (columns of S^T); FEW: one query tile holds all rows of a K/V head (NP <=
+// 64), stays in shared memory for all key tiles of the head and the ring holds K; else the ring
+// that matters holds query tiles.
+template <int D, int NP>
+struct WCfg {
+  static constexpr bool kFew = NP <= 64;
+  static constexpr int kKBytes = 128 * D * 2, kQBytes = NP * D * 2;
+  static constexpr int kKBufs = kFew ? (NP == 64 ? 5 : 6) * (128 / D) : 2;
+  static constexpr int kQBufs = kFew ? 2 : 4;
+  static constexpr int kSmem = kKBufs * kKBytes + kQBufs * kQBytes + 1024;
+  static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : NP == 64 ? 256 : 512;
+  static constexpr uint32_t kId = idesc_bf16(128, NP, false, false);
+};
+
+template <int NP>
+struct WCtl {
+  uint64_t k_full[12], k_empty[12], q_full[4], q_empty[4], s_full[4], s_free[4], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  long long scan[kWThreads / 32];
+  int b0, hk0, kt0, it0;
+  long long todo;
+  int first_cta, first_slot;
+  int issued_k, issued_q;               // copies issued (abort-path drain)
+  alignas(16) float nlse[2][2][NP];     // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
+  alignas(16) int seen[2][2][NP];       // last key the row sees
+  float other[128];                     // the second group's sums
+};
+
+struct WJoin {
+  int b, hk, kt, first_cta, first_slot, pad[3];
+};
+
+struct WWork {
+  float* part;   // [2 CTAs][128]
+  WJoin* desc;   // [CTAs]; b = -1: no unit ends here in pieces
+};
+
+// One sequence's units, per K/V head: key tile kt is seen by the token tiles from first(kt) on, each
+// of per_kv groups.
+struct WUnits {
+  SeqInfo q;
+  int nk, ntt, tpt, per_kv, causal;
+  __device__ WUnits(const PagedShape& s, const PagedRows& c, int b)
+      : q(paged_seq(s, b)), nk(0), ntt((q.Lq + c.tpt - 1) / c.tpt), tpt(c.tpt), per_kv(c.per_kv), causal(s.causal) {
+    if (q.Lq > 0) nk = (q.Lk + 127) >> 7;
+  }
+  __device__ int first(int kt) const { return causal ? max(0, (kt << 7) - q.off) / tpt : 0; }
+  __device__ int tiles(int kt) const { return per_kv * (ntt - first(kt)); }
+  __device__ long long before(int kt) const {  // query tiles of the key tiles before kt
+    long long sum = (long long)kt * ntt;
+    if (causal) {
+      const int none = min(kt, max(0, (q.off + 127) >> 7));  // key tiles that every token sees whole
+      sum -= floor_sum(kt - none, tpt, 128, ((long long)none << 7) - q.off);
+    }
+    return sum * per_kv;
+  }
+};
+
+struct WPieces {
+  const PagedShape& s;
+  const PagedRows& c;
+  int b, hk, kt, it, end, nk;
+  long long todo;
+  bool head;  // first piece of its (sequence, K/V head) in this CTA
+  int n, tt0;
+  SeqInfo seq;
+  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, int b_, int hk_, int kt_, int it_, long long todo_)
+      : s(s_), c(c_), b(b_), hk(hk_), kt(kt_), it(it_), end(0), nk(0), todo(todo_), head(true), n(0), tt0(0) {
+    if (todo > 0) open();
+  }
+  __device__ void open() {
+    const WUnits x(s, c, b);
+    seq = x.q;
+    nk = x.nk;
+    if (nk == 0) return;
+    n = x.tiles(kt);
+    tt0 = x.first(kt);
+    end = it + todo < n ? it + (int)todo : n;
+  }
+  __device__ bool done() const { return todo == 0; }
+  __device__ bool whole() const { return it == 0 && end == n; }
+  __device__ void next() {
+    todo -= end - it;
+    it = 0;
+    if (todo == 0) return;
+    head = ++kt == nk;
+    if (head) {
+      kt = 0;
+      if (++hk == s.Hkv) {
+        hk = 0;
+        ++b;
       }
-    if (lane == 0) a.weights[weight_offset(s, page, hk, slot)] += sum;
+    }
+    open();
+    while (nk == 0) {  // todo > 0: a later sequence has units
+      ++b;
+      open();
+    }
+  }
+  // Query tile i of the unit: its first token, and its group of heads.
+  __device__ int token(int i) const { return (tt0 + i / c.per_kv) * c.tpt; }
+  __device__ int group(int i) const { return hk * c.per_kv + i % c.per_kv; }
+};
+
+template <int D, int NP>
+__global__ void __launch_bounds__(kWThreads, 1)
+    paged_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const FaPagedArgs a, const PagedRows rows, const WWork wk) {
+  using C = WCfg<D, NP>;
+  grid_dependency_wait();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WCtl<NP> ctl;
+  const uint32_t sK = (smem_u32(smem_raw) + 1023u) & ~1023u, sQ = sK + C::kKBufs * C::kKBytes;
+  volatile int* abort_flag = &ctl.abort_flag;
+  const PagedShape& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](uint64_t& x) { return smem_u32(&x); };
+
+  if (threadIdx.x == 0) {
+    ctl.abort_flag = 0;
+    ctl.issued_k = ctl.issued_q = 0;
+    ctl.todo = 0;
+    for (int i = 0; i < C::kKBufs; ++i) {
+      mbar_init(bar(ctl.k_full[i]), 1);
+      mbar_init(bar(ctl.k_empty[i]), 1);
+    }
+    for (int i = 0; i < C::kQBufs; ++i) {
+      mbar_init(bar(ctl.q_full[i]), 1);
+      mbar_init(bar(ctl.q_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(ctl.s_full[i]), 1);
+      mbar_init(bar(ctl.s_free[i]), 128);
+    }
+    mbar_init(bar(ctl.drain), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  // Rows of the query tiles that no copy fills are zero.
+  const int used = rows.gs * rows.tpt;
+  for (int i = threadIdx.x; i < C::kQBufs * (D / 64) * (NP - used) * 8; i += kWThreads) {
+    const int r = used + i / 8 % (NP - used), part = i / 8 / (NP - used);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sQ + (part * NP + r) * 128 + (i & 7) * 16), "r"(0)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  {  // This CTA's share of the line of query tiles, and where it begins (as in the attention kernels).
+    const int per = (s.B + kWThreads - 1) / kWThreads, first = threadIdx.x * per;
+    const int last = min(s.B, first + per);
+    auto tiles_of = [&](int b) {
+      const WUnits x(s, rows, b);
+      return x.before(x.nk) * s.Hkv;
+    };
+    long long mine = 0;
+    for (int b = first; b < last; ++b) mine += tiles_of(b);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) ctl.scan[warp] = inc;
+    __syncthreads();
+    long long base = inc - mine, total = 0;
+    for (int i = 0; i < kWThreads / 32; ++i) {
+      if (i < warp) base += ctl.scan[i];
+      total += ctl.scan[i];
+    }
+    const long long n = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
+    const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
+    if (lo < hi && lo >= base && lo < base + mine) {
+      int b = first;
+      long long at = base;
+      for (;; ++b) {
+        const long long t = tiles_of(b);
+        if (lo < at + t) break;
+        at += t;
+      }
+      const WUnits x(s, rows, b);
+      const long long each = x.before(x.nk);
+      const int hk = (int)((lo - at) / each);
+      at += hk * each;
+      int kt = 0, top = x.nk;
+      while (top - kt > 1) {
+        const int mid = (kt + top) / 2;
+        if (x.before(mid) <= lo - at)
+          kt = mid;
+        else
+          top = mid;
+      }
+      const long long start = at + x.before(kt);
+      ctl.b0 = b;
+      ctl.hk0 = hk;
+      ctl.kt0 = kt;
+      ctl.it0 = (int)(lo - start);
+      ctl.todo = hi - lo;
+      const long long c0 = ((start + 1) * n - 1) / total;
+      ctl.first_cta = (int)c0;
+      ctl.first_slot = 2 * (int)c0 + (total * c0 / n == start ? 0 : 1);
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;");
+  WPieces w(s, rows, ctl.b0, ctl.hk0, ctl.kt0, ctl.it0, ctl.todo);
+  if (!C::kFew && threadIdx.x == 0) {
+    WJoin d{};
+    d.b = !w.done() && w.it > 0 && w.end == w.n ? w.b : -1;
+    d.hk = w.hk;
+    d.kt = w.kt;
+    d.first_cta = ctl.first_cta;
+    d.first_slot = ctl.first_slot;
+    wk.desc[blockIdx.x] = d;
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ copies
+    const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
+    bool run = true;
+    int kn = 0, qn = 0;  // key tiles and query tiles copied
+    auto page_of = [&](const WPieces& x) -> int {
+      const int key = (x.kt << 7) + (lane << shift);
+      return lane < per && key < x.seq.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
+    };
+    auto go = [&]() {
+      run = __all_sync(0xffffffffu, run) && !*abort_flag;
+      return run;
+    };
+    auto copy_q = [&](int token, int group) {
+      const int st = qn % C::kQBufs, u = qn / C::kQBufs;
+      if (run && u > 0) run = mbar_wait(bar(ctl.q_empty[st]), (u - 1) & 1, abort_flag, a.status);
+      if (go() && lane == 0) {
+        mbar_expect_tx(bar(ctl.q_full[st]), used * D * 2);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sQ + st * C::kQBytes + c * NP * 128, &tmQ, c * 64, group * rows.gs, w.seq.q0 + token, w.seq.bb,
+                      bar(ctl.q_full[st]));
+        ctl.issued_q = qn + 1;
+      }
+      ++qn;
+    };
+    int page = w.done() ? 0 : page_of(w);
+    while (!w.done()) {
+      if (C::kFew && w.head) copy_q(0, w.hk);
+      const int st = kn % C::kKBufs, u = kn / C::kKBufs;
+      if (run && u > 0) run = mbar_wait(bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
+      if (go()) {
+        const int pages = min(per, (w.seq.Lk - (w.kt << 7) + prows - 1) >> shift);
+        if (lane == 0) {
+          mbar_expect_tx(bar(ctl.k_full[st]), pages * prows * D * 2);
+          ctl.issued_k = kn + 1;
+        }
+        __syncwarp();
+        if (lane < pages)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sK + st * C::kKBytes + c * 16384 + lane * prows * 128, &tmK, c * 64, (w.kt << 7) & (P - 1), w.hk,
+                        page, bar(ctl.k_full[st]));
+      }
+      ++kn;
+      if (!C::kFew)
+        for (int i = w.it; i < w.end; ++i) copy_q(w.token(i), w.group(i));
+      w.next();
+      page = w.done() ? 0 : page_of(w);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      bool run = true;
+      int t = 0, kn = 0, qn = 0;
+      while (!w.done() && run) {
+        const int ks = kn % C::kKBufs;
+        if (C::kFew && w.head) {
+          run = mbar_wait_spin(bar(ctl.q_full[qn % C::kQBufs]), (qn / C::kQBufs) & 1, abort_flag, a.status);
+          ++qn;
+        }
+        if (run) run = mbar_wait_spin(bar(ctl.k_full[ks]), (kn / C::kKBufs) & 1, abort_flag, a.status);
+        const uint64_t dk = desc_kmajor_sw128(sK + ks * C::kKBytes);
+        for (int i = w.it; i < w.end && run; ++i, ++t) {
+          const int qs = (C::kFew ? qn - 1 : qn) % C::kQBufs;
+          if (!C::kFew) run = mbar_wait_spin(bar(ctl.q_full[qs]), (qn / C::kQBufs) & 1, abort_flag, a.status);
+          if (run && t >= 4) run = mbar_wait_spin(bar(ctl.s_free[t & 3]), ((t >> 2) - 1) & 1, abort_flag, a.status);
+          fence_after_sync();
+          if (!run) break;
+          const uint64_t dq = desc_kmajor_sw128(sQ + qs * C::kQBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + (t & 3) * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32),
+                   desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32), C::kId, kk > 0);
+          mma_commit(bar(ctl.s_full[t & 3]));
+          if (!C::kFew) {
+            mma_commit(bar(ctl.q_empty[qs]));
+            ++qn;
+          }
+        }
+        if (!run) break;
+        mma_commit(bar(ctl.k_empty[ks]));
+        ++kn;
+        w.next();
+        if (C::kFew && !w.done() && w.head) mma_commit(bar(ctl.q_empty[(qn - 1) % C::kQBufs]));
+      }
+      mma_commit(bar(ctl.drain));
+      mbar_wait_drain(bar(ctl.drain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------------ exponentials and sums
+    const int gr = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;  // group; key (and row, for the LSE)
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const float sl2 = a.scale * kLog2e;
+    const int ti = r / rows.gs, g = r - ti * rows.gs;
+    bool run = true, hidden = false;
+    int t = 0, flip = 0;
+    bool fresh = true;  // FEW: the head changed since this group's last tile
+    // The LSE of row r of a query tile: the number to add to its scores, whether any live column
+    // must not be read as it is (out of range rows of a copied box, LSE = -inf).
+    auto load_lse = [&](int token, int head0, float& nl, int& see) -> bool {
+      const int i = token + ti;
+      const bool live = r < used && i < w.seq.Lq;
+      float l = -INFINITY;
+      if (live) l = a.lse[paged_row(s, w.seq, w.b, head0 + g, i)];
+      const bool dead = l == -INFINITY;
+      nl = dead ? -INFINITY : -l * kLog2e;
+      see = dead ? -1 : (s.causal ? i + w.seq.off : 0x7fffffff);
+      return dead && r < used;
+    };
+    while (!w.done()) {
+      fresh |= w.head;
+      float sum = 0.f;
+      const int first_t = t;
+      float nl = 0.f;
+      int see = 0;
+      bool dead = false;
+      if (!C::kFew) {  // the LSE of this group's first tile, fetched ahead
+        const int i = w.it + ((t ^ gr) & 1);
+        if (i < w.end) dead = load_lse(w.token(i), w.group(i) * rows.gs, nl, see);
+      }
+      const int key = (w.kt << 7) + r;
+      for (int i = w.it; i < w.end; ++i, ++t) {
+        if ((t & 1) != gr) continue;
+        if (!C::kFew || fresh) {
+          if (C::kFew) dead = load_lse(0, w.hk * rows.gs, nl, see);
+          flip ^= 1;
+          if (r < NP) {
+            ctl.nlse[gr][flip][r] = nl;
+            ctl.seen[gr][flip][r] = see;
+          }
+          __syncwarp();
+          uint32_t any;
+          asm volatile(
+              "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+              : "=r"(any)
+              : "r"((uint32_t)dead), "r"(1 + gr)
+              : "memory");
+          hidden = any != 0;
+          fresh = false;
+          if (!C::kFew && i + 2 < w.end) dead = load_lse(w.token(i + 2), w.group(i + 2) * rows.gs, nl, see);
+        }
+        const int first = C::kFew ? 0 : w.token(i);
+        const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > first + w.seq.off);
+        if (run) run = mbar_wait(bar(ctl.s_full[t & 3]), (t >> 2) & 1, abort_flag, a.status);
+        fence_after_sync();
+        const float* nls = ctl.nlse[gr][flip];
+        const int* sees = ctl.seen[gr][flip];
+        constexpr int W = NP < 32 ? NP : 32;
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < NP / W; ++c) {
+          uint32_t x[W];
+          if constexpr (W == 16)
+            tmem_ld16(tmem + lane_off + (t & 3) * NP + c * W, x);
+          else
+            tmem_ld32(tmem + lane_off + (t & 3) * NP + c * W, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < W; k += 2) {
+            const float2 n2 = *reinterpret_cast<const float2*>(nls + c * W + k);
+            const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(sl2, sl2),
+                                  n2);
+            float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+            if (masked) {
+              p0 = key <= sees[c * W + k] ? p0 : 0.f;
+              p1 = key <= sees[c * W + k + 1] ? p1 : 0.f;
+            }
+            part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], make_float2(p0, p1));
+          }
+        }
+        fence_before_sync();
+        if (run) mbar_arrive(bar(ctl.s_free[t & 3]));
+        sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+      }
+      // A piece of one tile belongs to one group; else the first group adds the other's sums.
+      const int tiles = t - first_t;
+      const bool owner = tiles == 1 ? (first_t & 1) == gr : gr == 0;
+      if (tiles > 1) {
+        if (gr == 1) ctl.other[r] = sum;
+        named_bar_sync(3, 256);
+        if (gr == 0) sum += ctl.other[r];
+        named_bar_sync(3, 256);
+      }
+      if (owner) {
+        if (!w.whole()) {
+          wk.part[(size_t)(2 * blockIdx.x + (first_t == 0 ? 0 : 1)) * 128 + r] = sum;
+        } else if (key < w.seq.Lk) {
+          const int page = paged_page(s, w.b, key >> s.page_shift, a.status);
+          if (page >= 0) a.weights[weight_offset(s, page, w.hk, key & ((1 << s.page_shift) - 1))] += sum;
+        }
+      }
+      __syncwarp();
+      w.next();
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) {
+    // Copies still in flight land before the CTA exits: the last one issued into each buffer.
+    for (int i = max(0, ctl.issued_q - C::kQBufs); i < ctl.issued_q; ++i)
+      mbar_wait_drain(bar(ctl.q_full[i % C::kQBufs]), (i / C::kQBufs) & 1);
+    for (int i = max(0, ctl.issued_k - C::kKBufs); i < ctl.issued_k; ++i)
+      mbar_wait_drain(bar(ctl.k_full[i % C::kKBufs]), (i / C::kKBufs) & 1);
   }
 }
 
-int grid_for(size_t warps) {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const size_t ctas = (warps + 7) / 8;
-  return (int)(ctas < (size_t)sms * 8 ? ctas : (size_t)sms * 8);
+// Adds the pieces of each divided unit, in their order: block c the one that ends in CTA c's first piece.
+__global__ void __launch_bounds__(128) paged_weights_join_kernel(const FaPagedArgs a, const WWork wk) {
+  grid_dependency_wait();
+  const WJoin d = wk.desc[blockIdx.x];
+  if (d.b < 0) return;
+  const PagedShape& s = a.s;
+  const int key = (d.kt << 7) + threadIdx.x;
+  if (key >= paged_seq(s, d.b).Lk) return;
+  float sum = wk.part[(size_t)d.first_slot * 128 + threadIdx.x];
+  for (int c = d.first_cta + 1; c <= (int)blockIdx.x; ++c) sum += wk.part[(size_t)c * 256 + threadIdx.x];
+  const int page = paged_page(s, d.b, key >> s.page_shift, a.status);
+  if (page >= 0) a.weights[weight_offset(s, page, d.hk, key & ((1 << s.page_shift) - 1))] += sum;
+}
+
+template <int D, int NP>
+cudaError_t launch_weights(const FaPagedArgs& a, const PagedRows& rows, cudaStream_t st) {
+  using C = WCfg<D, NP>;
+  static_assert(C::kSmem + sizeof(WCtl<NP>) <= 227 * 1024, "with the control block");
+  const PagedShape& s = a.s;
+  const bool packed = s.cu_q != nullptr;
+  const int P = 1 << s.page_shift;
+  CUtensorMap tq, tk;
+  if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
+                         rows.gs, rows.tpt) ||
+      !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128))
+    return cudaErrorInvalidValue;
+  WWork wk;
+  wk.desc = static_cast<WJoin*>(a.workspace);
+  wk.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + (size_t)a.num_sms * sizeof(WJoin));
+  auto kern = paged_weights_kernel<D, NP>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(a.num_sms), dim3(kWThreads), C::kSmem, st, tq, tk, a, rows, wk);
+  if (e != cudaSuccess || C::kFew) return e;
+  return launch_dependent(paged_weights_join_kernel, dim3(a.num_sms), dim3(128), 0, st, a, wk);
+}
+
+template <int D>
+cudaError_t launch_weights_d(const FaPagedArgs& a, cudaStream_t st) {
+  const int G = a.s.H / a.s.Hkv;
+  if (!paged_few_rows(a.s)) return launch_weights<D, 128>(a, paged_rows_for(a.s), st);
+  const PagedRows few{G, a.s.Hkv, 1, a.s.Nq};  // all rows of a K/V head in one tile
+  const int n = a.s.Nq * G;
+  return n <= 16 ? launch_weights<D, 16>(a, few, st)
+         : n <= 32 ? launch_weights<D, 32>(a, few, st)
+                   : launch_weights<D, 64>(a, few, st);
 }
 
 }  // namespace
 }  // namespace fa
 
+size_t fa_paged_weights_workspace(int num_sms) {
+  return (size_t)num_sms * (sizeof(fa::WJoin) + 2 * 128 * sizeof(float));
+}
+
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st) {
-  auto k = a.s.d == 64 ? fa::paged_keys_kernel<64> : fa::paged_keys_kernel<128>;
-  return launch_dependent(k, dim3(fa::grid_for((size_t)a.s.B * a.s.Hkv * a.s.max_k)), dim3(256), 0, st, a);
+  return a.s.d == 64 ? fa::launch_weights_d<64>(a, st) : fa::launch_weights_d<128>(a, st);
 }

@@ -362,9 +362,12 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
  *   key_weights[b, hk, j] += sum over rows i that see key j and heads h of group hk of exp(scale q_ih . k_j - LSE_ih)
  * with the LSE that fa_fwd_paged gave for the same rows, cache and lengths (or for more keys: any LSE of the
  * caller's). A row with LSE = -inf adds nothing. Sums are fp32, in a fixed order: the result is run-to-run identical.
+ * num_sms and workspace as for fa_fwd_paged, sized by fa_paged_key_weights_workspace_bytes.
  */
-int fa_paged_key_weights(const fa_paged_problem* p, const void* q, fa_strides sq, const void* k_cache, fa_strides sk,
-                         const float* lse, float* key_weights, int* dev_status, void* stream);
+size_t fa_paged_key_weights_workspace_bytes(const fa_paged_problem* p, int num_sms);
+int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
+                         fa_strides sk, const float* lse, float* key_weights, void* workspace, size_t workspace_bytes,
+                         int* dev_status, void* stream);
 
 /*
  * Eviction: cut every sequence that is longer than `keep` down to `keep` keys, per K/V head. Its last `recent` keys

@@ -35,8 +35,8 @@ def append(p=None, kn=A, skn=SN, vn=A, svn=SN, k=A, sk=SC, v=A, sv=SC, w=None, s
     return fa.fa_paged_append(p or problem(), kn, skn, vn, svn, k, sk, v, sv, w, status, None)
 
 
-def weights(p=None, q=A, sq=SQ, k=A, sk=SC, lse=A, w=A, status=None):
-    return fa.fa_paged_key_weights(p or problem(), q, sq, k, sk, lse, w, status, None)
+def weights(p=None, sms=152, q=A, sq=SQ, k=A, sk=SC, lse=A, w=A, ws=A, nbytes=1 << 30, status=None):
+    return fa.fa_paged_key_weights(p or problem(), sms, q, sq, k, sk, lse, w, ws, nbytes, status, None)
 
 
 def evict(p=None, keep=64, recent=8, k=A, sk=SC, v=A, sv=SC, w=A, kept=A, out=2 * A, status=None):
@@ -64,7 +64,7 @@ def test_problem_refusals_of_calls_with_queries(kw, rc):
 
 
 def test_buffer_refusals():
-    for call, names in ((attend, "q k v o lse ws"), (append, "kn vn k v"), (weights, "q k lse w"), (evict, "k v w kept out")):
+    for call, names in ((attend, "q k v o lse ws"), (append, "kn vn k v"), (weights, "q k lse w ws"), (evict, "k v w kept out")):
         for n in names.split():
             assert call(**{n: None}) == -1, (call, n)
             assert call(**{n: A + 2}) == -3, (call, n)
@@ -78,16 +78,19 @@ def test_buffer_refusals():
     assert attend(sk=fa.Strides(256, 128, 1 << 39)) == -2
 
 
-def test_workspace_rules():
-    p = problem()
-    need = fa.fa_fwd_paged_workspace_bytes(p, 152)
-    assert need > 0 and need % 256 == 0
-    assert fa.fa_fwd_paged_workspace_bytes(problem(seqlen_k=16), 152) == need  # it does not grow with the lengths
-    assert fa.fa_fwd_paged_workspace_bytes(p, 0) == fa.fa_fwd_paged_workspace_bytes(p, 1025) == 0
-    assert fa.fa_fwd_paged_workspace_bytes(problem(d=96), 152) == 0
-    for sms, ws, nbytes, rc in ((0, A, 1 << 30, -1), (1025, A, 1 << 30, -1), (152, None, 1 << 30, -1),
-                                (152, A, need - 1, -1), (152, A + 16, 1 << 30, -3)):
-        assert attend(sms=sms, ws=ws, nbytes=nbytes) == rc
+@pytest.mark.parametrize("call,size", [(attend, "fa_fwd_paged_workspace_bytes"),
+                                       (weights, "fa_paged_key_weights_workspace_bytes")])
+def test_workspace_rules(call, size):
+    size = getattr(fa, size)
+    for n in (3, 500):  # few rows, and more
+        p = problem(seqlen_q=n)
+        need = size(p, 152)
+        assert need > 0 and need % 256 == 0
+        assert size(problem(seqlen_q=n, seqlen_k=16), 152) == need  # it does not grow with the lengths
+        assert size(p, 0) == size(p, 1025) == size(problem(d=96), 152) == 0
+        for sms, ws, nbytes, rc in ((0, A, 1 << 30, -1), (1025, A, 1 << 30, -1), (152, None, 1 << 30, -1),
+                                    (152, A, need - 1, -1), (152, A + 16, 1 << 30, -3)):
+            assert call(p, sms=sms, ws=ws, nbytes=nbytes) == rc
 
 
 def test_evict_budget_and_alias():
