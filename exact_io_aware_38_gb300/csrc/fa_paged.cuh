@@ -85,22 +85,95 @@ inline bool paged_few_rows(const PagedShape& s) { return (long long)s.Nq * (s.H 
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// sum of floor((a i + b) / m) for 0 <= i < n (a, b >= 0), by Euclid's steps on (a, m).
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum of floor((a i + b) / m) for 0 <= i < n, by Euclid's steps on (a, m). The arguments and a n + b
+// are positions of keys, tokens or tiles and fit 31 bits, so the divisions are 32-bit ones.
+__device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
     a %= m;
     b %= m;
-    const long long top = a * n + b;
+    const uint32_t top = a * n + b;
     n = top / m;
     b = top % m;
-    const long long t = a;
+    const uint32_t x = a;
     a = m;
-    m = t;
+    m = x;
     if (m == 0) break;
   }
   return sum;
+}
+
+// A CTA's share of the work. Units (of key tiles, or of query tiles) stand in one line, ordered by
+// sequence, head and unit; each is kOpen positions, which stand for the time a unit takes besides its
+// tiles, and then a position per tile. CTA c of n takes [total c / n, total (c + 1) / n). A share that
+// begins inside a unit's first kOpen positions begins with its first tile; one that ends there
+// has none of them.
+struct Share {
+  int b, head, unit, tile;   // where the CTA begins
+  long long todo;            // its positions, from there
+  int first_cta, first_slot; // of the unit in which it begins: the CTA with its first tile, the slot of that piece
+};
+
+// Finds the share of CTA blockIdx.x; all threads of the CTA take part, and `sh` and `scan` (one entry per
+// warp) are in shared memory. Units(b): heads, count, before(u) (positions before unit u, one head's),
+// and open, the positions of a unit before its first tile.
+template <int kThreads, typename Make>
+__device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (B + kThreads - 1) / kThreads, first = threadIdx.x * per, last = min(B, first + per);
+  auto size_of = [&](int b) {
+    const auto x = make(b);
+    return x.before(x.count) * x.heads;
+  };
+  long long mine = 0;
+  for (int b = first; b < last; ++b) mine += size_of(b);
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (threadIdx.x == 0) sh.todo = 0;
+  if (lane == 31) scan[warp] = inc;
+  __syncthreads();
+  long long base = inc - mine, total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) base += scan[i];
+    total += scan[i];
+  }
+  const long long n = min(total, (long long)gridDim.x), c = blockIdx.x;  // no CTA before the last busy one is idle
+  const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
+  if (lo < hi && lo >= base && lo < base + mine) {  // the sequence, and the line's position where it begins
+    int b = first;
+    for (;; ++b) {
+      const long long t = per == 1 ? mine : size_of(b);
+      if (lo < base + t) break;
+      base += t;
+    }
+    sh.b = b;
+    sh.todo = base;
+  }
+  __syncthreads();
+  if (lo >= hi) return;
+  const auto x = make(sh.b);
+  const long long each = x.before(x.count), from = sh.todo;
+  const int head = (int)((lo - from) / each);
+  const long long at = from + head * each;
+  __syncthreads();
+  for (int u = threadIdx.x; u < x.count; u += kThreads) {
+    const long long start = at + x.before(u);
+    if (start > lo || lo >= at + x.before(u + 1)) continue;
+    sh.head = head;
+    sh.unit = u;
+    sh.tile = (int)(lo - start);
+    sh.todo = hi - lo;
+    const long long tile0 = start + x.open;
+    const long long c0 = ((tile0 + 1) * n - 1) / total;
+    sh.first_cta = (int)c0;
+    sh.first_slot = 2 * (int)c0 + (total * c0 / n >= start ? 0 : 1);
+  }
+  __syncthreads();
 }
 
 }  // namespace fa

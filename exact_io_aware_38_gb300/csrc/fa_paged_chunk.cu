@@ -44,9 +44,7 @@ struct ChCtl {
   uint32_t tmem_base;
   int abort_flag;
   long long scan[kChThreads / 32];
-  int b0, hv0, u0, kt0;
-  long long todo;
-  int first_cta, first_slot;
+  Share share;
   int issued_q, issued_k0, issued_t, issued_tail;  // copies issued (abort-path drain)
 };
 
@@ -60,12 +58,16 @@ struct ChWork {
   JoinDesc* desc;   // [CTAs]; b = -1: no unit ends here in pieces
 };
 
+// A unit's copies of Q and its epilogue take the time of about two key tiles.
+constexpr int kChOpen = 2;
+
 // The units of one sequence, for one head group: unit u has tokens [u U, u U + U).
 struct Units {
-  int U, nu, causal;
+  int heads, count, open, U, causal;
   SeqInfo q;
-  __device__ Units(const PagedShape& s, const PagedRows& c, int b) : U(2 * c.tpt), causal(s.causal), q(paged_seq(s, b)) {
-    nu = (q.Lq + U - 1) / U;
+  __device__ Units(const PagedShape& s, const PagedRows& c, int b)
+      : heads(c.Hv), count(0), open(kChOpen), U(2 * c.tpt), causal(s.causal), q(paged_seq(s, b)) {
+    count = (q.Lq + U - 1) / U;
   }
   // Key tiles that token `last` of the sequence, and so any row before it, may see.
   __device__ int tiles_to(int last) const {
@@ -73,47 +75,51 @@ struct Units {
     return keys <= 0 ? 0 : (keys + 127) >> 7;
   }
   __device__ int tiles(int u) const { return max(1, tiles_to(min(q.Lq, (u + 1) * U) - 1)); }
-  // Key tiles of the units before u.
   __device__ long long before(int u) const {
-    if (!causal) return (long long)u * max(1, tiles_to(q.Lq - 1));
-    long long sum = 0;
+    long long sum = (long long)u * open;
+    if (!causal) return sum + (long long)u * max(1, tiles_to(q.Lq - 1));
     int n = u;
-    if (u == nu && u > 0) {
+    if (u == count && u > 0) {
       --n;
-      sum = tiles(n);
+      sum += tiles(n);
     }
     // The first units may see no key (more tokens than keys): one empty tile each.
     const int none = q.off < 0 ? min(n, -q.off / U) : 0;
-    sum += none;
-    return sum + floor_sum(n - none, 128, U, (long long)q.off + (long long)(none + 1) * U + 127);
+    return sum + none + floor_sum(n - none, 128, U, q.off + (none + 1) * U + 127);
   }
 };
 
+// The pieces of a CTA's share: key tiles [kt, end) of the n that unit u sees.
 struct ChPieces {
   const PagedShape& s;
   const PagedRows& c;
-  int b, hv, u, kt, n, end;
-  long long todo;
-  int nu;
+  int b, hv, u, kt, n, end, nu;
+  long long todo;  // positions from the piece on
+  bool finished;
   SeqInfo seq;
-  __device__ ChPieces(const PagedShape& s_, const PagedRows& c_, int b_, int hv_, int u_, int kt_, long long todo_)
-      : s(s_), c(c_), b(b_), hv(hv_), u(u_), kt(kt_), n(0), end(0), todo(todo_), nu(0) {
-    if (todo > 0) open();
+  __device__ ChPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh)
+      : s(s_), c(c_), b(sh.b), hv(sh.head), u(sh.unit), kt(0), n(0), end(0), nu(0), todo(sh.todo), finished(false) {
+    if (todo > 0) open(sh.tile);
   }
-  __device__ void open() {
+  __device__ void open(int at) {  // at: position within the unit
     const Units x(s, c, b);
     seq = x.q;
-    nu = x.nu;
+    nu = x.count;
     if (nu == 0) return;
     n = x.tiles(u);
-    end = kt + todo < n ? kt + (int)todo : n;
+    kt = max(0, at - kChOpen);
+    const long long stop = at + todo - kChOpen;
+    end = stop < n ? (int)stop : n;
+    todo -= min((long long)(n + kChOpen - at), todo);
+    if (end <= kt) finished = true;  // the share ends before the unit's first tile
   }
-  __device__ bool done() const { return todo == 0; }
+  __device__ bool done() const { return finished || nu == 0; }
   __device__ bool whole() const { return kt == 0 && end == n; }
   __device__ void next() {
-    todo -= end - kt;
-    kt = 0;
-    if (todo == 0) return;
+    if (todo == 0) {
+      finished = true;
+      return;
+    }
     if (++u == nu) {
       u = 0;
       if (++hv == c.Hv) {
@@ -121,10 +127,10 @@ struct ChPieces {
         ++b;
       }
     }
-    open();
+    open(0);
     while (nu == 0) {  // todo > 0: a later sequence has units
       ++b;
-      open();
+      open(0);
     }
   }
   // Key tiles query tile x sees, and whether it exists.
@@ -157,7 +163,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
     ctl.issued_q = ctl.issued_k0 = ctl.issued_t = ctl.issued_tail = 0;
-    ctl.todo = 0;
     mbar_init(bar(ctl.q_full), 1);
     mbar_init(bar(ctl.q_empty), 1);
     mbar_init(bar(ctl.k0_full), 1);
@@ -191,74 +196,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
                  : "memory");
   }
   fence_proxy_async_smem();
-  {  // This CTA's share of the line of key tiles, and where it begins (as in the few-row kernel).
-    const int per = (s.B + kChThreads - 1) / kChThreads, first = threadIdx.x * per;
-    const int last = min(s.B, first + per);
-    auto tiles_of = [&](int b) {
-      const Units x(s, rows, b);
-      return x.before(x.nu) * rows.Hv;
-    };
-    long long mine = 0;
-    for (int b = first; b < last; ++b) mine += tiles_of(b);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) ctl.scan[warp] = inc;
-    __syncthreads();
-    long long base = inc - mine, total = 0;
-    for (int i = 0; i < kChThreads / 32; ++i) {
-      if (i < warp) base += ctl.scan[i];
-      total += ctl.scan[i];
-    }
-    const long long n = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
-    const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
-    if (lo < hi && lo >= base && lo < base + mine) {
-      int b = first;
-      long long at = base;
-      for (;; ++b) {
-        const long long t = tiles_of(b);
-        if (lo < at + t) break;
-        at += t;
-      }
-      const Units x(s, rows, b);
-      const long long each = x.before(x.nu);
-      const int hv = (int)((lo - at) / each);
-      at += hv * each;
-      int u = 0, top = x.nu;  // the last unit that begins at or before lo
-      while (top - u > 1) {
-        const int mid = (u + top) / 2;
-        if (x.before(mid) <= lo - at)
-          u = mid;
-        else
-          top = mid;
-      }
-      const long long start = at + x.before(u);
-      ctl.b0 = b;
-      ctl.hv0 = hv;
-      ctl.u0 = u;
-      ctl.kt0 = (int)(lo - start);
-      ctl.todo = hi - lo;
-      const long long c0 = ((start + 1) * n - 1) / total;
-      ctl.first_cta = (int)c0;
-      ctl.first_slot = 2 * (int)c0 + (total * c0 / n == start ? 0 : 1);
-    }
-  }
+  find_share<kChThreads>(s.B, [&](int b) { return Units(s, rows, b); }, ctl.share, ctl.scan);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
   asm volatile("griddepcontrol.launch_dependents;");
-  ChPieces w(s, rows, ctl.b0, ctl.hv0, ctl.u0, ctl.kt0, ctl.todo);
+  ChPieces w(s, rows, ctl.share);
   if (threadIdx.x == 0) {
     JoinDesc d{};
     d.b = !w.done() && w.kt > 0 && w.end == w.n ? w.b : -1;
     d.hv = w.hv;
     d.u = w.u;
-    d.first_cta = ctl.first_cta;
-    d.first_slot = ctl.first_slot;
+    d.first_cta = ctl.share.first_cta;
+    d.first_slot = ctl.share.first_slot;
     wk.desc[blockIdx.x] = d;
   }
 

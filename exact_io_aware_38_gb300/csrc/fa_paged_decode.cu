@@ -59,41 +59,66 @@ struct DecCtl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  int scan[kDecThreads / 32];
-  int b0, hk0, kt0, todo, first_cta, first_slot;  // where this CTA begins; how many tiles it has
+  long long scan[kDecThreads / 32];
+  Share share;
   int issued_q, issued_t;                         // copies issued (abort-path drain)
   float m[NP], alpha[NP], wmax[4][NP];
   int lim[NP];
 };
 
-__device__ __forceinline__ int tiles_of(const SeqInfo& q) { return q.Lq == 0 ? 0 : max(1, (q.Lk + 127) >> 7); }
+// A unit (sequence, K/V head) without keys still has a tile, which writes its zeros. Its epilogue takes
+// the time of about one tile.
+constexpr int kDecOpen = 1;
 
-// The pieces of a CTA's share: (b, hk, key tiles [kt, end)), walked in order by every role.
+struct DecUnits {
+  int heads, count, open;
+  SeqInfo q;
+  __device__ DecUnits(const PagedShape& s, int b) : heads(s.Hkv), count(0), open(kDecOpen), q(paged_seq(s, b)) {
+    count = q.Lq > 0;
+  }
+  __device__ int tiles() const { return max(1, (q.Lk + 127) >> 7); }
+  __device__ long long before(int u) const { return u * (tiles() + open); }
+};
+
+// The pieces of a CTA's share: key tiles [kt, end) of the n of (b, hk), walked in order by every role.
 struct Pieces {
   const PagedShape& s;
-  int b, hk, kt, todo, n, end;
+  int b, hk, kt, n, end;
+  long long todo;  // positions from the piece on
+  bool finished;
   SeqInfo seq;
-  __device__ Pieces(const PagedShape& s_, int b_, int hk_, int kt_, int todo_)
-      : s(s_), b(b_), hk(hk_), kt(kt_), todo(todo_), n(0), end(0) {
-    if (todo > 0) open();
+  __device__ Pieces(const PagedShape& s_, const Share& sh)
+      : s(s_), b(sh.b), hk(sh.head), kt(0), n(0), end(0), todo(sh.todo), finished(false) {
+    if (todo > 0) open(sh.tile);
   }
-  __device__ void open() {
-    seq = paged_seq(s, b);
-    n = tiles_of(seq);
-    end = min(n, kt + todo);
+  __device__ void open(int at) {  // at: position within the unit
+    const DecUnits x(s, b);
+    seq = x.q;
+    n = 0;
+    if (x.count == 0) return;
+    n = x.tiles();
+    kt = max(0, at - kDecOpen);
+    const long long stop = at + todo - kDecOpen;
+    end = stop < n ? (int)stop : n;
+    todo -= min((long long)(n + kDecOpen - at), todo);
+    if (end <= kt) finished = true;  // the share ends before the unit's first tile
   }
-  __device__ bool done() const { return todo == 0; }
+  __device__ bool done() const { return finished || n == 0; }
   __device__ bool whole() const { return kt == 0 && end == n; }
   __device__ void next() {
-    todo -= end - kt;
-    kt = 0;
-    if (todo == 0) return;
+    if (todo == 0) {
+      finished = true;
+      return;
+    }
     if (++hk == s.Hkv) {
       hk = 0;
-      do seq = paged_seq(s, ++b);
-      while ((n = tiles_of(seq)) == 0);  // todo > 0: a later sequence has tiles
+      ++b;
     }
-    end = min(n, todo);
+    open(0);
+    while (n == 0) {  // todo > 0: a later sequence has new tokens
+      ++b;
+      open(0);
+    }
   }
 };
 
@@ -162,7 +187,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
     ctl.issued_q = ctl.issued_t = 0;
-    ctl.todo = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(ctl.q_full[i]), 1);
       mbar_init(bar(ctl.q_empty[i]), 1);
@@ -195,59 +219,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                  : "memory");
   }
   fence_proxy_async_smem();
-  // This CTA's share [lo, hi) of the line of key tiles, and the sequence in which it begins: the
-  // threads take consecutive sequences each and a scan gives where each thread's begin.
-  int lo, hi;
-  {
-    const int per = (s.B + kDecThreads - 1) / kDecThreads, first = threadIdx.x * per;
-    const int last = min(s.B, first + per);
-    int mine = 0;
-    for (int b = first; b < last; ++b) mine += tiles_of(paged_seq(s, b)) * s.Hkv;
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) ctl.scan[warp] = inc;
-    __syncthreads();
-    int base = inc - mine, total = 0;
-    for (int i = 0; i < kDecThreads / 32; ++i) {
-      if (i < warp) base += ctl.scan[i];
-      total += ctl.scan[i];
-    }
-    const int n = min((int)gridDim.x, total), c = blockIdx.x;  // no CTA before the last busy one is idle
-    lo = c < n ? (int)((long long)total * c / n) : 0;
-    hi = c < n ? (int)((long long)total * (c + 1) / n) : 0;
-    if (lo < hi && lo >= base && lo < base + mine) {
-      int b = first, at = base;
-      for (;; ++b) {
-        const int t = tiles_of(paged_seq(s, b)) * s.Hkv;
-        if (lo < at + t) break;
-        at += t;
-      }
-      const int nt = tiles_of(paged_seq(s, b));
-      const int start = at + (lo - at) / nt * nt;  // where the (sequence, head) begins
-      ctl.b0 = b;
-      ctl.hk0 = (lo - at) / nt;
-      ctl.kt0 = lo - start;
-      ctl.todo = hi - lo;
-      // The first CTA that works on it, and the slot of its piece: its first slot if it begins there.
-      const int c0 = (int)(((long long)(start + 1) * n - 1) / total);
-      ctl.first_cta = c0;
-      ctl.first_slot = 2 * c0 + ((long long)total * c0 / n == start ? 0 : 1);
-    }
-  }
+  find_share<kDecThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
   // Only the merge waits for this grid; its blocks may be scheduled as SMs drain.
   asm volatile("griddepcontrol.launch_dependents;");
-  Pieces w(s, ctl.b0, ctl.hk0, ctl.kt0, ctl.todo);
+  Pieces w(s, ctl.share);
   if (threadIdx.x == 0) {
     const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
-    wk.desc[blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.first_cta, ctl.first_slot);
+    wk.desc[blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);
   }
 
   if (warp == 0) {

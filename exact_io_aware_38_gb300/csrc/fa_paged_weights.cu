@@ -11,8 +11,9 @@
 // leaves 128 partial sums per piece (two slots per CTA), which the join kernel adds in the pieces'
 // order; with one query tile per unit nothing is cut.
 //
-// Roles (320 threads): warp 0 reads the page table and copies, warp 1 issues the MMAs, warps 2-5 and
-// 6-9 are two groups that take the query tiles in turn (one reads its scores while the other waits).
+// Roles: warp 0 reads the page table and copies, warp 1 issues the MMAs, three groups of four warps
+// take the query tiles in turn, and with many rows a last group adds the groups' sums of a finished
+// unit to the weights, so that no exponential waits for that read and write.
 // Tensor memory: four score buffers of NP columns.
 #include "fa_paged.cuh"
 #include "fa_tmap.h"
@@ -23,7 +24,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWThreads = 320;
+constexpr int kGroups = 3;
 
 // NP: rows of a query tile (columns of S^T); FEW: one query tile holds all rows of a K/V head (NP <=
 // 64), stays in shared memory for all key tiles of the head and the ring holds K; else the ring
@@ -32,8 +33,10 @@ template <int D, int NP>
 struct WCfg {
   static constexpr bool kFew = NP <= 64;
   static constexpr int kKBytes = 128 * D * 2, kQBytes = NP * D * 2;
-  static constexpr int kKBufs = kFew ? (NP == 64 ? 5 : 6) * (128 / D) : 2;
-  static constexpr int kQBufs = kFew ? 2 : 4;
+  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128);
+  static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 2) * (128 / D);
+  static constexpr int kQBufs = kFew ? 2 : 4 * (128 / D);
+  static constexpr int kOpen = kFew ? 0 : 1;
   static constexpr int kSmem = kKBufs * kKBytes + kQBufs * kQBytes + 1024;
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : NP == 64 ? 256 : 512;
   static constexpr uint32_t kId = idesc_bf16(128, NP, false, false);
@@ -41,17 +44,15 @@ struct WCfg {
 
 template <int NP>
 struct WCtl {
-  uint64_t k_full[12], k_empty[12], q_full[4], q_empty[4], s_full[4], s_free[4], drain;
+  uint64_t k_full[12], k_empty[12], q_full[8], q_empty[8], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[kWThreads / 32];
-  int b0, hk0, kt0, it0;
-  long long todo;
-  int first_cta, first_slot;
+  long long scan[18];
+  Share share;
   int issued_k, issued_q;               // copies issued (abort-path drain)
-  alignas(16) float nlse[2][2][NP];     // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
-  alignas(16) int seen[2][2][NP];       // last key the row sees
-  float other[128];                     // the second group's sums
+  alignas(16) float nlse[kGroups][2][NP];  // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
+  alignas(16) int seen[kGroups][2][NP];    // last key the row sees
+  float sums[2][kGroups][NP == 128 ? 128 : 1];  // many rows: the groups' sums of a piece, per parity
 };
 
 struct WJoin {
@@ -67,50 +68,65 @@ struct WWork {
 // of per_kv groups.
 struct WUnits {
   SeqInfo q;
-  int nk, ntt, tpt, per_kv, causal;
-  __device__ WUnits(const PagedShape& s, const PagedRows& c, int b)
-      : q(paged_seq(s, b)), nk(0), ntt((q.Lq + c.tpt - 1) / c.tpt), tpt(c.tpt), per_kv(c.per_kv), causal(s.causal) {
-    if (q.Lq > 0) nk = (q.Lk + 127) >> 7;
+  int heads, count, open, ntt, tpt, per_kv, causal;
+  __device__ WUnits(const PagedShape& s, const PagedRows& c, int b, int open_)
+      : q(paged_seq(s, b)),
+        heads(s.Hkv),
+        count(0),
+        open(open_),
+        ntt((q.Lq + c.tpt - 1) / c.tpt),
+        tpt(c.tpt),
+        per_kv(c.per_kv),
+        causal(s.causal) {
+    if (q.Lq > 0) count = (q.Lk + 127) >> 7;
   }
   __device__ int first(int kt) const { return causal ? max(0, (kt << 7) - q.off) / tpt : 0; }
   __device__ int tiles(int kt) const { return per_kv * (ntt - first(kt)); }
-  __device__ long long before(int kt) const {  // query tiles of the key tiles before kt
+  __device__ long long before(int kt) const {
     long long sum = (long long)kt * ntt;
     if (causal) {
       const int none = min(kt, max(0, (q.off + 127) >> 7));  // key tiles that every token sees whole
-      sum -= floor_sum(kt - none, tpt, 128, ((long long)none << 7) - q.off);
+      sum -= floor_sum(kt - none, tpt, 128, (none << 7) - q.off);
     }
-    return sum * per_kv;
+    return sum * per_kv + (long long)kt * open;
   }
 };
 
+// The pieces of a CTA's share: query tiles [it, end) of the n that see key tile kt.
 struct WPieces {
   const PagedShape& s;
   const PagedRows& c;
-  int b, hk, kt, it, end, nk;
-  long long todo;
-  bool head;  // first piece of its (sequence, K/V head) in this CTA
+  int b, hk, kt, it, end, nk, open_cost;
+  long long todo;  // positions from the piece on
+  bool head;       // first piece of its (sequence, K/V head) in this CTA
   int n, tt0;
   SeqInfo seq;
-  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, int b_, int hk_, int kt_, int it_, long long todo_)
-      : s(s_), c(c_), b(b_), hk(hk_), kt(kt_), it(it_), end(0), nk(0), todo(todo_), head(true), n(0), tt0(0) {
-    if (todo > 0) open();
+  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh, int open_)
+      : s(s_), c(c_), b(sh.b), hk(sh.head), kt(sh.unit), it(0), end(0), nk(0), open_cost(open_), todo(sh.todo),
+        head(true), n(0), tt0(0) {
+    if (todo > 0) open(sh.tile);
   }
-  __device__ void open() {
-    const WUnits x(s, c, b);
+  __device__ void open(int at) {  // at: position within the unit
+    const WUnits x(s, c, b, open_cost);
     seq = x.q;
-    nk = x.nk;
+    nk = x.count;
     if (nk == 0) return;
     n = x.tiles(kt);
     tt0 = x.first(kt);
-    end = it + todo < n ? it + (int)todo : n;
+    it = max(0, at - open_cost);
+    const long long stop = at + todo - open_cost;
+    end = stop < n ? (int)stop : n;
+    todo -= min((long long)(n + open_cost - at), todo);
+    if (end <= it) finished = true;  // the share ends before the unit's first tile
   }
-  __device__ bool done() const { return todo == 0; }
+  bool finished = false;
+  __device__ bool done() const { return finished || nk == 0; }
   __device__ bool whole() const { return it == 0 && end == n; }
   __device__ void next() {
-    todo -= end - it;
-    it = 0;
-    if (todo == 0) return;
+    if (todo == 0) {
+      finished = true;
+      return;
+    }
     head = ++kt == nk;
     if (head) {
       kt = 0;
@@ -119,10 +135,10 @@ struct WPieces {
         ++b;
       }
     }
-    open();
+    open(0);
     while (nk == 0) {  // todo > 0: a later sequence has units
       ++b;
-      open();
+      open(0);
     }
   }
   // Query tile i of the unit: its first token, and its group of heads.
@@ -130,8 +146,46 @@ struct WPieces {
   __device__ int group(int i) const { return hk * c.per_kv + i % c.per_kv; }
 };
 
+// One query tile's part of a key's sum: 2^(c log2(e) s - LSE) over the columns (rows) of this thread's
+// lane, the first `cols` of them rounded up to a chunk (the others carry no weight).
+template <int NP, bool MASK>
+__device__ __forceinline__ float tile_sum(uint32_t tS, const float* nls, const int* sees, int key, int cols,
+                                          float sl2) {
+  constexpr int W = NP < 32 ? NP : 32;  // columns per wait
+  float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < NP; c += W) {
+    if (c >= cols) break;
+    uint32_t x[W];
+    if constexpr (W == 16)
+      tmem_ld16(tS + c, x);
+    else
+      tmem_ld32(tS + c, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < W; k += 4) {
+      const float4 n4 = *reinterpret_cast<const float4*>(nls + c + k);
+      const float2 sc = make_float2(sl2, sl2);
+      const float2 y0 = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc, make_float2(n4.x, n4.y));
+      const float2 y1 =
+          fma2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), sc, make_float2(n4.z, n4.w));
+      float p0 = ex2_approx(y0.x), p1 = ex2_approx(y0.y), p2 = ex2_approx(y1.x), p3 = ex2_approx(y1.y);
+      if constexpr (MASK) {
+        const int4 see = *reinterpret_cast<const int4*>(sees + c + k);
+        p0 = key <= see.x ? p0 : 0.f;
+        p1 = key <= see.y ? p1 : 0.f;
+        p2 = key <= see.z ? p2 : 0.f;
+        p3 = key <= see.w ? p3 : 0.f;
+      }
+      part[0] = add2(part[0], make_float2(p0, p1));
+      part[1] = add2(part[1], make_float2(p2, p3));
+    }
+  }
+  return (part[0].x + part[0].y) + (part[1].x + part[1].y);
+}
+
 template <int D, int NP>
-__global__ void __launch_bounds__(kWThreads, 1)
+__global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     paged_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const FaPagedArgs a, const PagedRows rows, const WWork wk) {
   using C = WCfg<D, NP>;
@@ -147,7 +201,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
     ctl.issued_k = ctl.issued_q = 0;
-    ctl.todo = 0;
     for (int i = 0; i < C::kKBufs; ++i) {
       mbar_init(bar(ctl.k_full[i]), 1);
       mbar_init(bar(ctl.k_empty[i]), 1);
@@ -160,6 +213,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(bar(ctl.s_full[i]), 1);
       mbar_init(bar(ctl.s_free[i]), 128);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(ctl.sum_ready[i]), 128 * kGroups);
+      mbar_init(bar(ctl.sum_free[i]), 128);
+    }
     mbar_init(bar(ctl.drain), 1);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
@@ -171,80 +228,26 @@ __global__ void __launch_bounds__(kWThreads, 1)
   }
   // Rows of the query tiles that no copy fills are zero.
   const int used = rows.gs * rows.tpt;
-  for (int i = threadIdx.x; i < C::kQBufs * (D / 64) * (NP - used) * 8; i += kWThreads) {
+  for (int i = threadIdx.x; i < C::kQBufs * (D / 64) * (NP - used) * 8; i += C::kThreads) {
     const int r = used + i / 8 % (NP - used), part = i / 8 / (NP - used);
     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sQ + (part * NP + r) * 128 + (i & 7) * 16), "r"(0)
                  : "memory");
   }
   fence_proxy_async_smem();
-  {  // This CTA's share of the line of query tiles, and where it begins (as in the attention kernels).
-    const int per = (s.B + kWThreads - 1) / kWThreads, first = threadIdx.x * per;
-    const int last = min(s.B, first + per);
-    auto tiles_of = [&](int b) {
-      const WUnits x(s, rows, b);
-      return x.before(x.nk) * s.Hkv;
-    };
-    long long mine = 0;
-    for (int b = first; b < last; ++b) mine += tiles_of(b);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) ctl.scan[warp] = inc;
-    __syncthreads();
-    long long base = inc - mine, total = 0;
-    for (int i = 0; i < kWThreads / 32; ++i) {
-      if (i < warp) base += ctl.scan[i];
-      total += ctl.scan[i];
-    }
-    const long long n = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
-    const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
-    if (lo < hi && lo >= base && lo < base + mine) {
-      int b = first;
-      long long at = base;
-      for (;; ++b) {
-        const long long t = tiles_of(b);
-        if (lo < at + t) break;
-        at += t;
-      }
-      const WUnits x(s, rows, b);
-      const long long each = x.before(x.nk);
-      const int hk = (int)((lo - at) / each);
-      at += hk * each;
-      int kt = 0, top = x.nk;
-      while (top - kt > 1) {
-        const int mid = (kt + top) / 2;
-        if (x.before(mid) <= lo - at)
-          kt = mid;
-        else
-          top = mid;
-      }
-      const long long start = at + x.before(kt);
-      ctl.b0 = b;
-      ctl.hk0 = hk;
-      ctl.kt0 = kt;
-      ctl.it0 = (int)(lo - start);
-      ctl.todo = hi - lo;
-      const long long c0 = ((start + 1) * n - 1) / total;
-      ctl.first_cta = (int)c0;
-      ctl.first_slot = 2 * (int)c0 + (total * c0 / n == start ? 0 : 1);
-    }
-  }
+  find_share<C::kThreads>(s.B, [&](int b) { return WUnits(s, rows, b, C::kOpen); }, ctl.share, ctl.scan);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
   asm volatile("griddepcontrol.launch_dependents;");
-  WPieces w(s, rows, ctl.b0, ctl.hk0, ctl.kt0, ctl.it0, ctl.todo);
+  WPieces w(s, rows, ctl.share, C::kOpen);
   if (!C::kFew && threadIdx.x == 0) {
     WJoin d{};
     d.b = !w.done() && w.it > 0 && w.end == w.n ? w.b : -1;
     d.hk = w.hk;
     d.kt = w.kt;
-    d.first_cta = ctl.first_cta;
-    d.first_slot = ctl.first_slot;
+    d.first_cta = ctl.share.first_cta;
+    d.first_slot = ctl.share.first_slot;
     wk.desc[blockIdx.x] = d;
   }
 
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mma_commit(bar(ctl.drain));
       mbar_wait_drain(bar(ctl.drain), 0);
     }
-  } else {
+  } else if (warp < 2 + 4 * kGroups) {
     // ------------------------------------------------------------------ exponentials and sums
     const int gr = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;  // group; key (and row, for the LSE)
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -343,103 +346,112 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int ti = r / rows.gs, g = r - ti * rows.gs;
     bool run = true, hidden = false;
     int t = 0, flip = 0;
-    bool fresh = true;  // FEW: the head changed since this group's last tile
-    // The LSE of row r of a query tile: the number to add to its scores, whether any live column
-    // must not be read as it is (out of range rows of a copied box, LSE = -inf).
-    auto load_lse = [&](int token, int head0, float& nl, int& see) -> bool {
+    bool fresh = true;  // few rows: the head changed since this group's last tile
+    // The LSE of row r of a query tile (-inf: no such row); used one tile later, so that no thread
+    // waits for the load.
+    auto load_lse = [&](int token, int head0) -> float {
       const int i = token + ti;
-      const bool live = r < used && i < w.seq.Lq;
-      float l = -INFINITY;
-      if (live) l = a.lse[paged_row(s, w.seq, w.b, head0 + g, i)];
-      const bool dead = l == -INFINITY;
-      nl = dead ? -INFINITY : -l * kLog2e;
-      see = dead ? -1 : (s.causal ? i + w.seq.off : 0x7fffffff);
-      return dead && r < used;
+      return r < used && i < w.seq.Lq ? a.lse[paged_row(s, w.seq, w.b, head0 + g, i)] : -INFINITY;
     };
-    while (!w.done()) {
-      fresh |= w.head;
-      float sum = 0.f;
-      const int first_t = t;
-      float nl = 0.f;
-      int see = 0;
-      bool dead = false;
-      if (!C::kFew) {  // the LSE of this group's first tile, fetched ahead
-        const int i = w.it + ((t ^ gr) & 1);
-        if (i < w.end) dead = load_lse(w.token(i), w.group(i) * rows.gs, nl, see);
-      }
-      const int key = (w.kt << 7) + r;
-      for (int i = w.it; i < w.end; ++i, ++t) {
-        if ((t & 1) != gr) continue;
-        if (!C::kFew || fresh) {
-          if (C::kFew) dead = load_lse(0, w.hk * rows.gs, nl, see);
-          flip ^= 1;
-          if (r < NP) {
-            ctl.nlse[gr][flip][r] = nl;
-            ctl.seen[gr][flip][r] = see;
-          }
-          __syncwarp();
-          uint32_t any;
-          asm volatile(
-              "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
-              : "=r"(any)
-              : "r"((uint32_t)dead), "r"(1 + gr)
-              : "memory");
-          hidden = any != 0;
-          fresh = false;
-          if (!C::kFew && i + 2 < w.end) dead = load_lse(w.token(i + 2), w.group(i + 2) * rows.gs, nl, see);
-        }
-        const int first = C::kFew ? 0 : w.token(i);
-        const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > first + w.seq.off);
-        if (run) run = mbar_wait(bar(ctl.s_full[t & 3]), (t >> 2) & 1, abort_flag, a.status);
-        fence_after_sync();
-        const float* nls = ctl.nlse[gr][flip];
-        const int* sees = ctl.seen[gr][flip];
-        constexpr int W = NP < 32 ? NP : 32;
-        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < NP / W; ++c) {
-          uint32_t x[W];
-          if constexpr (W == 16)
-            tmem_ld16(tmem + lane_off + (t & 3) * NP + c * W, x);
-          else
-            tmem_ld32(tmem + lane_off + (t & 3) * NP + c * W, x);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < W; k += 2) {
-            const float2 n2 = *reinterpret_cast<const float2*>(nls + c * W + k);
-            const float2 y = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(sl2, sl2),
-                                  n2);
-            float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-            if (masked) {
-              p0 = key <= sees[c * W + k] ? p0 : 0.f;
-              p1 = key <= sees[c * W + k + 1] ? p1 : 0.f;
-            }
-            part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], make_float2(p0, p1));
-          }
-        }
-        fence_before_sync();
-        if (run) mbar_arrive(bar(ctl.s_free[t & 3]));
-        sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
-      }
-      // A piece of one tile belongs to one group; else the first group adds the other's sums.
-      const int tiles = t - first_t;
-      const bool owner = tiles == 1 ? (first_t & 1) == gr : gr == 0;
-      if (tiles > 1) {
-        if (gr == 1) ctl.other[r] = sum;
-        named_bar_sync(3, 256);
-        if (gr == 0) sum += ctl.other[r];
-        named_bar_sync(3, 256);
-      }
-      if (owner) {
-        if (!w.whole()) {
-          wk.part[(size_t)(2 * blockIdx.x + (first_t == 0 ? 0 : 1)) * 128 + r] = sum;
-        } else if (key < w.seq.Lk) {
-          const int page = paged_page(s, w.b, key >> s.page_shift, a.status);
-          if (page >= 0) a.weights[weight_offset(s, page, w.hk, key & ((1 << s.page_shift) - 1))] += sum;
-        }
+    // Puts it where the group reads it; `hidden`: some column's scores must not enter the sum as they
+    // are (a copied row of another sequence, or one without weight).
+    auto stage_lse = [&](int token, float lse) {
+      const bool dead = lse == -INFINITY;
+      flip ^= 1;
+      if (r < NP) {
+        ctl.nlse[gr][flip][r] = dead ? -INFINITY : -lse * kLog2e;
+        ctl.seen[gr][flip][r] = dead ? -1 : (s.causal ? token + ti + w.seq.off : 0x7fffffff);
       }
       __syncwarp();
-      w.next();
+      uint32_t any;
+      asm volatile(
+          "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+          : "=r"(any)
+          : "r"((uint32_t)(dead && r < used)), "r"(1 + gr)
+          : "memory");
+      hidden = any != 0;
+    };
+    auto tile = [&](int token) -> float {
+      const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > token + w.seq.off);
+      const int cols = min(used, (w.seq.Lq - token) * rows.gs), key = (w.kt << 7) + r;
+      if (run) run = mbar_wait(bar(ctl.s_full[t & 3]), (t >> 2) & 1, abort_flag, a.status);
+      __syncwarp();
+      fence_after_sync();
+      const float* nls = ctl.nlse[gr][flip];
+      const int* sees = ctl.seen[gr][flip];
+      const uint32_t tS = tmem + lane_off + (t & 3) * NP;
+      const float sum = masked ? tile_sum<NP, true>(tS, nls, sees, key, cols, sl2)
+                               : tile_sum<NP, false>(tS, nls, sees, key, cols, sl2);
+      fence_before_sync();
+      if (run) mbar_arrive(bar(ctl.s_free[t & 3]));
+      return sum;
+    };
+    if constexpr (C::kFew) {
+      // One tile per key tile: its group also adds to the weights (read before the scores are there).
+      for (; !w.done(); w.next(), ++t) {
+        fresh |= w.head;
+        if (t % kGroups != gr) continue;
+        const int key = (w.kt << 7) + r;
+        float* at = nullptr;
+        float old = 0.f;
+        if (key < w.seq.Lk) {
+          const int page = paged_page(s, w.b, key >> s.page_shift, a.status);
+          if (page >= 0) {
+            at = a.weights + weight_offset(s, page, w.hk, key & ((1 << s.page_shift) - 1));
+            old = *at;
+          }
+        }
+        __syncwarp();
+        if (fresh) stage_lse(0, load_lse(0, w.hk * rows.gs));
+        fresh = false;
+        const float sum = tile(0);
+        if (at != nullptr) *at = old + sum;
+        __syncwarp();
+      }
+    } else {
+      for (int piece = 0; !w.done(); ++piece, w.next()) {
+        int i = w.it + (gr + kGroups - t % kGroups) % kGroups;  // this group's first tile of the piece
+        const int t0 = t;
+        float sum = 0.f;
+        float lse = i < w.end ? load_lse(w.token(i), w.group(i) * rows.gs) : 0.f;
+        for (; i < w.end; i += kGroups) {
+          t = t0 + (i - w.it);
+          stage_lse(w.token(i), lse);
+          if (i + kGroups < w.end) lse = load_lse(w.token(i + kGroups), w.group(i + kGroups) * rows.gs);
+          sum += tile(w.token(i));
+        }
+        t = t0 + (w.end - w.it);
+        const int pp = piece & 1;
+        if (run && piece >= 2) run = mbar_wait(bar(ctl.sum_free[pp]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+        ctl.sums[pp][gr][r] = sum;
+        if (run) mbar_arrive(bar(ctl.sum_ready[pp]));
+        __syncwarp();
+      }
+    }
+  } else if constexpr (!C::kFew) {
+    // ------------------------------------------------------------------ sums to weights
+    const int r = threadIdx.x - (64 + 128 * kGroups);
+    bool run = true;
+    for (int piece = 0; !w.done(); ++piece, w.next()) {
+      const int key = (w.kt << 7) + r, pp = piece & 1;
+      float* at = nullptr;
+      float old = 0.f;
+      if (w.whole() && key < w.seq.Lk) {
+        const int page = paged_page(s, w.b, key >> s.page_shift, a.status);
+        if (page >= 0) {
+          at = a.weights + weight_offset(s, page, w.hk, key & ((1 << s.page_shift) - 1));
+          old = *at;
+        }
+      } else if (!w.whole()) {
+        at = wk.part + (size_t)(2 * blockIdx.x + (piece == 0 ? 0 : 1)) * 128 + r;
+      }
+      if (run) run = mbar_wait(bar(ctl.sum_ready[pp]), (piece >> 1) & 1, abort_flag, a.status);
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) sum += ctl.sums[pp][g][r];
+      if (run) mbar_arrive(bar(ctl.sum_free[pp]));
+      if (at != nullptr) *at = old + sum;
+      __syncwarp();
     }
   }
 
@@ -490,7 +502,7 @@ cudaError_t launch_weights(const FaPagedArgs& a, const PagedRows& rows, cudaStre
   auto kern = paged_weights_kernel<D, NP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(a.num_sms), dim3(kWThreads), C::kSmem, st, tq, tk, a, rows, wk);
+  e = launch_dependent(kern, dim3(a.num_sms), dim3(C::kThreads), C::kSmem, st, tq, tk, a, rows, wk);
   if (e != cudaSuccess || C::kFew) return e;
   return launch_dependent(paged_weights_join_kernel, dim3(a.num_sms), dim3(128), 0, st, a, wk);
 }
