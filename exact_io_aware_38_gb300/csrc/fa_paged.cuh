@@ -201,6 +201,53 @@ size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st);
 size_t fa_paged_chunk_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_chunk(const FaPagedArgs& a, cudaStream_t st);
+namespace fa {
+
+// Joins the partials (normalised O and LSE in log2 units, in slots of ROWS rows) that CTAs c0 .. c1 left of
+// one row, for its elements [e, e + 4): M = max LSE, w = 2^(LSE - M), O = sum w O / sum w, LSE = M + log2
+// sum w. CTA c0's lie in slot0, those of a later CTA c in slot 2 c. Eight pieces are in flight at a time.
+template <int D, int ROWS>
+__device__ __forceinline__ void join_pieces(const FaPagedArgs& a, const float* part_o, const float* part_lse, int c0,
+                                            int c1, int slot0, int row, int e, const SeqInfo& seq, int b, int i,
+                                            int h) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, sum = 0.f;
+  for (int c = c0; c <= c1; c += 8) {
+    float l[8];
+    float4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const size_t at = (size_t)(c + k == c0 ? slot0 : 2 * (c + k)) * ROWS + row;
+      const bool there = c + k <= c1;
+      l[k] = there ? part_lse[at] : -INFINITY;
+      o[k] = there ? *reinterpret_cast<const float4*>(part_o + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, l[k]);
+    if (top == -INFINITY) continue;
+    const float alpha = exp2f(M - top);
+    acc = make_float4(acc.x * alpha, acc.y * alpha, acc.z * alpha, acc.w * alpha);
+    sum *= alpha;
+    M = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float w = exp2f(l[k] - M);
+      sum += w;
+      acc.x += w * o[k].x;
+      acc.y += w * o[k].y;
+      acc.z += w * o[k].z;
+      acc.w += w * o[k].w;
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (e == 0) a.lse[paged_row(a.s, seq, b, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+}  // namespace fa
+
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
 size_t fa_paged_weights_workspace(int num_sms);
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);

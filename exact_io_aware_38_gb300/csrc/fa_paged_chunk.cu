@@ -505,25 +505,7 @@ __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs
     const int r = blockIdx.y * 32 + y / (D / 4), e = y % (D / 4) * 4;
     const int rr = r & 127, i = (2 * d.u + (r >> 7)) * rows.tpt + rr / rows.gs, h = d.hv * rows.gs + rr % rows.gs;
     if (rr >= rows.gs * rows.tpt || i >= seq.Lq) continue;
-    auto slot = [&](int c) { return (size_t)(c == d.first_cta ? d.first_slot : 2 * c) * 256 + r; };
-    float M = -INFINITY;
-    for (int c = d.first_cta; c <= (int)blockIdx.x; ++c) M = fmaxf(M, wk.part_lse[slot(c)]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    if (M != -INFINITY)
-      for (int c = d.first_cta; c <= (int)blockIdx.x; ++c) {
-        const float wt = exp2f(wk.part_lse[slot(c)] - M);
-        const float4 o = *reinterpret_cast<const float4*>(wk.part_o + slot(c) * D + e);
-        sum += wt;
-        acc.x += wt * o.x;
-        acc.y += wt * o.y;
-        acc.z += wt * o.z;
-        acc.w += wt * o.w;
-      }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (e == 0) a.lse[paged_row(s, seq, d.b, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+    join_pieces<D, 256>(a, wk.part_o, wk.part_lse, d.first_cta, blockIdx.x, d.first_slot, r, e, seq, d.b, i, h);
   }
 }
 

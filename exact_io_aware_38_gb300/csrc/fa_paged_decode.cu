@@ -11,7 +11,7 @@
 // their relative precision over that range, and one vote per tile replaces a max over 128 keys.
 //
 // Division of the work: all sequences' key tiles form one line, ordered (sequence, head, tile), which
-// the CTAs (one per SM, persistent) divide evenly, whatever the lengths are. A CTA's share
+// the CTAs (one or two per SM, persistent) divide evenly, whatever the lengths are. A CTA's share
 // begins and ends inside a (sequence, head) at most twice; those pieces leave normalised fp32
 // partials (two slots per CTA) that the merge kernel joins by their log-sum-exp; whole ones are
 // written directly.
@@ -32,16 +32,25 @@ constexpr int kDecThreads = 192;
 constexpr float kNoMax = -3.0e38f;   // reference max of a row that has seen no key
 constexpr float kRaise = 32.f;       // log2 units a score may exceed the reference by
 
+// CTAs per SM.
+constexpr int dec_ctas(int d, int np) { return d == 64 && np < 64 ? 2 : 1; }
+
 template <int D, int NP>
 struct DecCfg {
   static constexpr int kTileBytes = 128 * D * 2;
-  // K and V in flight: 192 KB, or 128 KB beside 64-row tiles.
-  static constexpr int kStages = (NP == 64 ? 2 : 3) * (D == 64 ? 2 : 1);
+  // d = 128: one CTA per SM, 192 KB of K and V in flight. d = 64: tiles are half as large and the
+  // latencies of a tile (scores, exponentials, P, product) would show, so two CTAs share an SM, with
+  // 80 KB each in flight. 64-row tiles take the registers of a whole SM: one CTA, 128 KB.
+  static constexpr int kCtas = dec_ctas(D, NP);
+  static constexpr int kKStages = NP == 64 ? 256 / D : 3, kVStages = NP == 64 ? 256 / D : D == 64 ? 2 : 3;
   static constexpr int kQBytes = NP * D * 2;
   static constexpr int kQBufs = 2;
-  static constexpr int kPBytes = 128 * 128;          // 128 keys x up to 64 rows, one 128-byte row per key
-  static constexpr int kSmem = kQBufs * kQBytes + 2 * kStages * kTileBytes + kPBytes + 1024;
-  static_assert(kSmem + 480 + 36 * NP <= 227 * 1024, "with the control block");
+  // P has two buffers: 128 keys, a 128-byte row each, of which a tile's P takes 2 NP bytes. With up to 32
+  // rows they lie side by side, else one behind the other.
+  static constexpr int kPBytes = (NP == 64 ? 2 : 1) * 128 * 128;
+  static constexpr int kPStep = NP == 64 ? 128 * 128 : NP * 2;
+  static constexpr int kSmem = kQBufs * kQBytes + (kKStages + kVStages) * kTileBytes + kPBytes + 1024;
+  static_assert(kCtas * (kSmem + 480 + 36 * NP + 1024) <= 228 * 1024, "with the control block");
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : 256;  // S x 2, O x 2
   static constexpr uint32_t kIdS = idesc_bf16(128, NP, false, false);
   // O^T = V^T P^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared
@@ -52,9 +61,9 @@ struct DecCfg {
 template <int NP>
 struct DecCtl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2];
-  uint64_t p_ready, pv_done;
+  uint64_t p_ready[2], pv_done[2];  // per buffer of P
   uint64_t o_free[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -62,7 +71,9 @@ struct DecCtl {
   long long scan[kDecThreads / 32];
   Share share;
   int issued_q, issued_t;                         // copies issued (abort-path drain)
-  float m[NP], alpha[NP], wmax[4][NP];
+  alignas(16) float m[NP];
+  alignas(16) float alpha[NP];
+  float wmax[4][NP];
   int lim[NP];
 };
 
@@ -166,22 +177,22 @@ struct DecWork {
 };
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const DecWork wk) {
   using C = DecCfg<D, NP>;
   grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) DecCtl<NP> ctl;
-  const uint32_t sKV = (smem_u32(smem_raw) + 1023u) & ~1023u;  // stage i: K then V
-  const uint32_t sP = sKV + 2 * C::kStages * C::kTileBytes;
+  const uint32_t sK0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sV0 = sK0 + C::kKStages * C::kTileBytes, sP = sV0 + C::kVStages * C::kTileBytes;
   const uint32_t sQ = sP + C::kPBytes;
   volatile int* abort_flag = &ctl.abort_flag;
   const PagedShape& s = a.s;
   const int G = s.H / s.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto sK = [&](int i) { return sKV + 2 * i * C::kTileBytes; };
-  auto sV = [&](int i) { return sKV + (2 * i + 1) * C::kTileBytes; };
+  auto sK = [&](int i) { return sK0 + i * C::kTileBytes; };
+  auto sV = [&](int i) { return sV0 + i * C::kTileBytes; };
   auto bar = [&](uint64_t& x) { return smem_u32(&x); };
 
   if (threadIdx.x == 0) {
@@ -192,15 +203,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       mbar_init(bar(ctl.q_empty[i]), 1);
       mbar_init(bar(ctl.s_full[i]), 1);
       mbar_init(bar(ctl.o_free[i]), 128);
+      mbar_init(bar(ctl.p_ready[i]), 128);
+      mbar_init(bar(ctl.pv_done[i]), 1);
     }
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar(ctl.k_full[i]), 1);
       mbar_init(bar(ctl.k_empty[i]), 1);
       mbar_init(bar(ctl.v_full[i]), 1);
       mbar_init(bar(ctl.v_empty[i]), 1);
     }
-    mbar_init(bar(ctl.p_ready), 128);
-    mbar_init(bar(ctl.pv_done), 1);
     mbar_init(bar(ctl.drain), 1);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
@@ -255,12 +266,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         ctl.issued_q = piece + 1;
       }
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
-        const int st = t % C::kStages, u = t / C::kStages;
         const int left = w.seq.Lk - (kt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
         const int slot = (kt << 7) & (P - 1);
         const int next = kt + 1 < w.end ? page_of(w, kt + 1) : 0;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          const int stages = x ? C::kVStages : C::kKStages, st = t % stages, u = t / stages;
           const uint32_t full = x ? bar(ctl.v_full[st]) : bar(ctl.k_full[st]);
           if (run && u > 0)
             run = mbar_wait(x ? bar(ctl.v_empty[st]) : bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
@@ -288,10 +299,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       Pieces v = w;  // the piece of the next S
       int vkt = v.kt, vpiece = 0;
       auto issue_s = [&]() {
-        const int st = t % C::kStages, qb = vpiece % C::kQBufs;
+        const int st = t % C::kKStages, qb = vpiece % C::kQBufs;
         if (run && vkt == v.kt)
           run = mbar_wait_spin(bar(ctl.q_full[qb]), (vpiece / C::kQBufs) & 1, abort_flag, a.status);
-        if (run) run = mbar_wait_spin(bar(ctl.k_full[st]), (t / C::kStages) & 1, abort_flag, a.status);
+        if (run) run = mbar_wait_spin(bar(ctl.k_full[st]), (t / C::kKStages) & 1, abort_flag, a.status);
         fence_after_sync();
         if (run) {
           const uint64_t dk = desc_kmajor_sw128(sK(st)), dq = desc_kmajor_sw128(sQ + qb * C::kQBytes);
@@ -315,20 +326,21 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       for (int piece = 0; !w.done(); ++piece) {
         for (int kt = w.kt; kt < w.end; ++kt, ++j) {
           if (!v.done()) issue_s();
-          const int st = j % C::kStages;
-          if (run) run = mbar_wait_spin(bar(ctl.p_ready), j & 1, abort_flag, a.status);
-          if (run) run = mbar_wait_spin(bar(ctl.v_full[st]), (j / C::kStages) & 1, abort_flag, a.status);
+          const int st = j % C::kVStages;
+          if (run) run = mbar_wait_spin(bar(ctl.p_ready[j & 1]), (j >> 1) & 1, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.v_full[st]), (j / C::kVStages) & 1, abort_flag, a.status);
           if (run && kt == w.kt && piece >= 2)
             run = mbar_wait_spin(bar(ctl.o_free[piece & 1]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
           fence_after_sync();
           if (run) {
-            const uint64_t dv = desc_mnmajor_sw128(sV(st), 16384), dp = desc_mnmajor_sw128(sP, 16384);
+            const uint64_t dv = desc_mnmajor_sw128(sV(st), 16384);
+            const uint64_t dp = desc_mnmajor_sw128(sP + (j & 1) * C::kPStep, 16384);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ss(tmem + (2 + (piece & 1)) * NP, desc_add(dv, kk * 2048), desc_add(dp, kk * 2048), C::kIdPV,
                      kk > 0 || kt > w.kt);
             mma_commit(bar(ctl.v_empty[st]));
-            mma_commit(bar(ctl.pv_done));
+            mma_commit(bar(ctl.pv_done[j & 1]));
           }
         }
         w.next();
@@ -343,6 +355,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const float sl2 = a.scale * kLog2e;
     bool run = true;
     int t = 0;
+    auto wait_pv = [&](int j) -> bool {  // P V of tile j has completed
+      return mbar_wait(bar(ctl.pv_done[j & 1]), (j >> 1) & 1, abort_flag, a.status);
+    };
     for (int piece = 0; !w.done(); ++piece) {
       const SeqInfo& seq = w.seq;
       const int live = seq.Lq * G;  // rows that exist
@@ -353,7 +368,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
       for (int n = 0; n < NP; ++n) l[n] = 0.f;
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
-        const int st = t % C::kStages;
         if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
         fence_after_sync();
         float x[NP];
@@ -379,10 +393,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (!opens) {
           bool big = false;
 #pragma unroll
-          for (int n = 0; n < NP; ++n) big |= fmaf(x[n], sl2, -ctl.m[n]) > kRaise;
+          for (int n = 0; n < NP; n += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ctl.m + n);
+            big |= fmaxf(fmax3(fmaf(x[n], sl2, -m.x), fmaf(x[n + 1], sl2, -m.y), fmaf(x[n + 2], sl2, -m.z)),
+                         fmaf(x[n + 3], sl2, -m.w)) > kRaise;
+          }
           raise = vote_any(big);
         }
-        bool waited = false;
         if (raise) {
           float y[NP];
 #pragma unroll
@@ -401,9 +418,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           __syncwarp();
           named_bar_sync(1, 128);
           if (!opens) {
-            if (run) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
+            if (run) run = wait_pv(t - 1);
             fence_after_sync();
-            waited = true;
 #pragma unroll
             for (int c = 0; c < NP / 16; ++c) {
               uint32_t o[16];
@@ -421,23 +437,31 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         uint32_t pk[NP / 2];
 #pragma unroll
-        for (int n = 0; n < NP; n += 2) {
-          const float p0 = ex2_approx(fmaf(x[n], sl2, -ctl.m[n])), p1 = ex2_approx(fmaf(x[n + 1], sl2, -ctl.m[n + 1]));
+        for (int n = 0; n < NP; n += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(ctl.m + n);
+          const float p0 = ex2_approx(fmaf(x[n], sl2, -m.x)), p1 = ex2_approx(fmaf(x[n + 1], sl2, -m.y));
+          const float p2 = ex2_approx(fmaf(x[n + 2], sl2, -m.z)), p3 = ex2_approx(fmaf(x[n + 3], sl2, -m.w));
           l[n] += p0;
           l[n + 1] += p1;
+          l[n + 2] += p2;
+          l[n + 3] += p3;
           pk[n / 2] = pack_bf16x2(p0, p1);
+          pk[n / 2 + 1] = pack_bf16x2(p2, p3);
         }
-        // P's buffer is free once the previous P V has read it.
-        if (run && t > 0 && !waited) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
+        // P's buffer is free: the P V that read it, of tile t - 2, was issued before S of tile t, which has
+        // completed.
+        const uint32_t sPt = sP + (NP == 64 ? (t & 1) * C::kPStep : 0);
+        const int c0 = NP == 64 ? 0 : (t & 1) * (C::kPStep / 16);  // first 16-byte chunk of the row
 #pragma unroll
         for (int c = 0; c < NP / 8; ++c)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sP + r * 128 + ((c ^ (r & 7)) << 4)),
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sPt + r * 128 + (((c + c0) ^ (r & 7)) << 4)),
                        "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
                        : "memory");
         // Value rows past the last key may hold anything, and 0 times NaN is NaN: they become 0.
         const int valid = seq.Lk - (kt << 7);
         if (valid < 128) {
-          if (run) run = mbar_wait(bar(ctl.v_full[st]), (t / C::kStages) & 1, abort_flag, a.status);
+          const int st = t % C::kVStages;
+          if (run) run = mbar_wait(bar(ctl.v_full[st]), (t / C::kVStages) & 1, abort_flag, a.status);
           if (run && r >= valid)
 #pragma unroll
             for (int c = 0; c < D / 64 * 8; ++c)
@@ -449,7 +473,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         fence_proxy_async_smem();
         fence_before_sync();
-        if (run) mbar_arrive(bar(ctl.p_ready));
+        if (run) mbar_arrive(bar(ctl.p_ready[t & 1]));
       }
       // ---------------------------------------------------------------- end of the piece
       columns_reduce(l, lane, [](float p, float q) { return p + q; });
@@ -470,7 +494,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       }
       __syncwarp();
       named_bar_sync(1, 128);
-      if (run) run = mbar_wait(bar(ctl.pv_done), (t - 1) & 1, abort_flag, a.status);
+      if (run) run = wait_pv(t - 1);
       fence_after_sync();
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0, w.hk * G) + r;
       float* part = wk.part_o + (size_t)slot * NP * D + r;
@@ -514,15 +538,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // Copies still in flight land before the CTA exits: the last one issued into each buffer.
     for (int i = max(0, ctl.issued_q - C::kQBufs); i < ctl.issued_q; ++i)
       mbar_wait_drain(bar(ctl.q_full[i % C::kQBufs]), (i / C::kQBufs) & 1);
-    for (int i = max(0, ctl.issued_t - 2 * C::kStages); i < ctl.issued_t; ++i) {
-      const int t = i >> 1, st = t % C::kStages;
-      mbar_wait_drain((i & 1) ? bar(ctl.v_full[st]) : bar(ctl.k_full[st]), (t / C::kStages) & 1);
+    for (int i = max(0, ctl.issued_t - 8); i < ctl.issued_t; ++i) {
+      const int t = i >> 1, stages = (i & 1) ? C::kVStages : C::kKStages;
+      if (t + stages <= (ctl.issued_t - 1 - (i & 1)) >> 1) continue;  // a later copy used the buffer
+      mbar_wait_drain((i & 1) ? bar(ctl.v_full[t % stages]) : bar(ctl.k_full[t % stages]), (t / stages) & 1);
     }
   }
 }
 
-// Joins the pieces of each divided (sequence, head): M = max LSE, w = 2^(LSE - M), O = sum w O / sum w,
-// LSE = M + log2 sum w. Block c joins the one that ends in CTA c's first piece, if it began before.
+// Joins the pieces of each divided (sequence, head). Block c takes the one that ends in CTA c's first
+// piece, if it began before.
 template <int D, int NP>
 __global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, const DecWork wk) {
   grid_dependency_wait();
@@ -533,26 +558,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, co
   const int G = s.H / s.Hkv, c1 = blockIdx.x;
   for (int x = threadIdx.x; x < seq.Lq * G * (D / 4); x += 256) {
     const int n = x / (D / 4), e = x % (D / 4) * 4;
-    auto slot = [&](int c) { return (size_t)(c == d.z ? d.w : 2 * c) * NP + n; };
-    float M = -INFINITY;
-    for (int c = d.z; c <= c1; ++c) M = fmaxf(M, wk.part_lse[slot(c)]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    if (M != -INFINITY)
-      for (int c = d.z; c <= c1; ++c) {
-        const float wt = exp2f(wk.part_lse[slot(c)] - M);
-        const float4 o = *reinterpret_cast<const float4*>(wk.part_o + slot(c) * D + e);
-        sum += wt;
-        acc.x += wt * o.x;
-        acc.y += wt * o.y;
-        acc.z += wt * o.z;
-        acc.w += wt * o.w;
-      }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int i = n / G, h = d.y * G + n % G;
-    uint2 v = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) = v;
-    if (e == 0) a.lse[paged_row(s, seq, d.x, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+    join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, c1, d.w, n, e, seq, d.x, n / G, d.y * G + n % G);
   }
 }
 
@@ -572,16 +578,19 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
   DecWork wk;
   char* ws = static_cast<char*>(a.workspace);
   wk.desc = reinterpret_cast<int4*>(ws);
-  ws += up256((size_t)a.num_sms * sizeof(int4));
+  const int ctas = a.num_sms * C::kCtas;
+  ws += up256((size_t)ctas * sizeof(int4));
   wk.part_lse = reinterpret_cast<float*>(ws);
-  ws += up256((size_t)a.num_sms * 2 * NP * sizeof(float));
+  ws += up256((size_t)ctas * 2 * NP * sizeof(float));
   wk.part_o = reinterpret_cast<float*>(ws);
   auto kern = paged_decode_kernel<D, NP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(a.num_sms), dim3(kDecThreads), C::kSmem, st, tq, tk, tv, a, wk);
+  if (C::kCtas > 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_join_kernel<D, NP>, dim3(a.num_sms), dim3(256), 0, st, a, wk);
+  e = launch_dependent(kern, dim3(ctas), dim3(kDecThreads), C::kSmem, st, tq, tk, tv, a, wk);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_join_kernel<D, NP>, dim3(ctas), dim3(256), 0, st, a, wk);
 }
 
 int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -590,8 +599,9 @@ int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 }  // namespace fa
 
 size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms) {
-  const size_t rows = (size_t)num_sms * 2 * fa::padded_rows(s.Nq * (s.H / s.Hkv));
-  return fa::up256((size_t)num_sms * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
+  const int np = fa::padded_rows(s.Nq * (s.H / s.Hkv));
+  const size_t ctas = (size_t)num_sms * fa::dec_ctas(s.d, np), rows = ctas * 2 * np;
+  return fa::up256(ctas * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
 }
 
 cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st) {

@@ -1,0 +1,505 @@
+"""Models of the barrier protocols of the paged-cache kernels, checked over random interleavings
+(tests/mbarrier_model.py gives the machine; tests/test_fwd_protocol_model.py says what such a model is).
+
+A CTA walks pieces of units; here a piece is the number of its tiles. Each model has the kernel's waits, arrivals and
+commits, with copies, MMAs and commits completing at random times, and checks: no deadlock, no buffer reloaded before
+its readers have completed, no MMA before its operands are there, no operand or accumulator overwritten while it is
+read, and with waits that run out at random: every role ends and no copy is left in flight. A planted mistake must be
+found in each.
+
+decode   fa_paged_decode.cu: K and V rings of their own lengths, two Q buffers, S and P double buffered, O per piece
+         double buffered; the softmax waits for V itself in a unit's last tile, whose rows past the last key it zeroes.
+chunk    fa_paged_chunk.cu: two query tiles, one Q buffer; stage t of the ring holds V of tile t and K of tile t + 1; the
+         last tile's V comes on a barrier of its own and the copying warp completes the stage after zeroing rows.
+weights  fa_paged_weights.cu: K and Q rings, four S buffers, three groups in turn; with many rows a last group adds the
+         groups' sums, double buffered, to the weights.
+"""
+
+import random
+
+from mbarrier_model import Machine
+
+
+def tiles_of(pieces):
+    """[(piece, tile within it, last of the piece)] in order."""
+    return [(p, k, k + 1 == n) for p, n in enumerate(pieces) for k in range(n)]
+
+
+def finish(M, roles, issued):
+    """Runs the roles, then, after an abort, the exit's wait for the copies in flight: issued() names the barriers of
+    copies that were issued, with the parity of their last phases."""
+    def drain():
+        if M.aborted:
+            for name, parity in issued():
+                while not M.B[name].passes(parity):
+                    yield (name, parity)
+            M.need(not M.loads, "the CTA exits with copies in flight")
+        yield None
+    return M.run(roles, final=drain), M.errors
+
+
+def last_phases(name, n, bufs):
+    """Barrier and parity of the last copy into each of `bufs` buffers after n copies."""
+    return [(f"{name}{i % bufs}", (i // bufs) & 1) for i in range(max(0, n - bufs), n)]
+
+
+# ----------------------------------------------------------------------------- decode
+
+
+def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False):
+    M = Machine(seed, abort_p)
+    done, need = M.done, M.need
+    T = tiles_of(pieces)
+    for i in range(2):
+        for n in ("qf", "qe", "sf", "of", "pv", "p"):
+            M.bar(f"{n}{i}", 1)
+    for i in range(ks):
+        M.bar(f"kf{i}", 1), M.bar(f"ke{i}", 1)
+    for i in range(vs):
+        M.bar(f"vf{i}", 1), M.bar(f"ve{i}", 1)
+    count = {"q": 0, "k": 0, "v": 0}
+
+    def producer():
+        run = True
+        for t, (p, k, _) in enumerate(T):
+            if k == 0:
+                if run and p >= 2:
+                    run = yield from M.wait(f"qe{p % 2}", (p // 2 - 1) & 1)
+                run = run and not M.aborted
+                if run:
+                    for u in range(len(T)):
+                        need(T[u][0] != p - 2 or ("S", u) in done, f"Q of piece {p - 2} overwritten before S({u})")
+                    M.load(f"qf{p % 2}", 1, ("Q", p))
+                    count["q"] = p + 1
+            for x, n, reader in (("k", ks, "S"), ("v", vs, "PV")):
+                if run and t >= n:
+                    run = yield from M.wait(f"{x}e{t % n}", (t // n - 1) & 1)
+                run = run and not M.aborted
+                if run:
+                    need(t < n or (reader, t - n) in done, f"{x} of tile {t - n} overwritten before {reader}")
+                    M.load(f"{x}f{t % n}", 1, (x, t))
+                    count[x] = t + 1
+            yield None
+
+    def issuer():
+        run = True
+
+        def issue_s(t, run):
+            p, k, last = T[t]
+            if run and k == 0:
+                run = yield from M.wait(f"qf{p % 2}", (p // 2) & 1)
+            if run:
+                run = yield from M.wait(f"kf{t % ks}", (t // ks) & 1)
+            if run:
+                need(("Q", p) in done and ("k", t) in done, f"S({t}) before its operands")
+                need(t < 2 or ("P", t - 2) in done, f"S({t}) over S({t - 2}) before it was read")
+                M.mma("i", ("S", t))
+                M.commit("i", f"sf{t & 1}"), M.commit("i", f"ke{t % ks}")
+                if last:
+                    M.commit("i", f"qe{p % 2}")
+            return run
+        if T:
+            run = yield from issue_s(0, run)
+        for t, (p, k, _) in enumerate(T):
+            if t + 1 < len(T):
+                run = yield from issue_s(t + 1, run)
+            if run:
+                run = yield from M.wait("p0" if one_p else f"p{t & 1}", t & 1 if one_p else (t >> 1) & 1)
+            if run:
+                run = yield from M.wait(f"vf{t % vs}", (t // vs) & 1)
+            if run and k == 0 and p >= 2:
+                run = yield from M.wait(f"of{p & 1}", ((p >> 1) - 1) & 1)
+            if run:
+                need(("v", t) in done and ("P", t) in done, f"PV({t}) before its operands")
+                need(k > 0 or p < 2 or ("O", p - 2) in done, f"PV({t}) over O of piece {p - 2} before it was read")
+                M.mma("i", ("PV", t))
+                M.commit("i", f"ve{t % vs}"), M.commit("i", f"pv{t & 1}")
+            yield None
+
+    def softmax():
+        run = True
+        r = random.Random(seed + 1)
+        for t, (p, k, last) in enumerate(T):
+            if run:
+                run = yield from M.wait(f"sf{t & 1}", (t >> 1) & 1)
+            if run:
+                need(("S", t) in done, f"S({t}) read before it completed")
+            if k > 0 and r.random() < 0.2:  # the reference max is raised: O is rescaled
+                if run:
+                    run = yield from M.wait(f"pv{(t - 1) & 1}", ((t - 1) >> 1) & 1)
+                need(not run or ("PV", t - 1) in done, f"O rescaled at {t} before PV({t - 1})")
+            if run:  # no wait: PV(t - 2) was issued before S(t)
+                need(t < 2 or ("PV", t - 2) in done, f"P({t}) over P({t - 2}) before PV read it")
+            if last and r.random() < 0.7:  # the unit's last tile: V's rows past the last key become 0
+                if run:
+                    run = yield from M.wait(f"vf{t % vs}", (t // vs) & 1)
+                need(not run or (("v", t) in done and ("PV", t) not in done), f"V({t}) zeroed at the wrong time")
+            yield None
+            if run:
+                done.add(("P", t))
+                M.B["p0" if one_p else f"p{t & 1}"].arrive()
+            if last:
+                if run and not skip_pv_wait:
+                    run = yield from M.wait(f"pv{t & 1}", (t >> 1) & 1)
+                need(not run or ("PV", t) in done, f"O read before PV({t})")
+                if run:
+                    done.add(("O", p))
+                    M.B[f"of{p & 1}"].arrive()
+
+    def issued():
+        return last_phases("qf", count["q"], 2) + last_phases("kf", count["k"], ks) + last_phases("vf", count["v"], vs)
+    return finish(M, {"prod": producer(), "mma": issuer(), "soft": softmax()}, issued)
+
+
+def pieces_for(seed):
+    r = random.Random(seed * 7919)
+    return [r.choice([1, 1, 2, r.randint(1, 9)]) for _ in range(r.randint(0, 6))]
+
+
+RINGS = [(3, 3), (3, 2), (2, 2), (4, 4)]
+
+
+def test_decode_has_no_deadlock_or_hazard():
+    for seed in range(2500):
+        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed)
+        assert res == "ok" and not errs, (pieces_for(seed), RINGS[seed % 4], seed, res, errs[:3])
+
+
+def test_decode_ends_after_waits_that_run_out():
+    for seed in range(1500):
+        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, abort_p=0.02)
+        assert res == "ok" and not errs, (pieces_for(seed), RINGS[seed % 4], seed, res, errs[:3])
+
+
+def test_decode_model_finds_a_missing_wait():
+    assert any(decode(pieces_for(s), 3, 3, s, skip_pv_wait=True)[1] for s in range(500))
+    # One barrier for both buffers of P: its phase passes twice before the issuer looks.
+    assert any(decode(pieces_for(s), 3, 3, s, one_p=True)[0] == "deadlock" for s in range(500))
+
+
+# ----------------------------------------------------------------------------- chunk
+
+
+def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
+    """pieces: (tiles, tiles query tile 0 sees, tiles query tile 1 sees, the last tile is the sequence's last)."""
+    M = Machine(seed, abort_p)
+    done, need = M.done, M.need
+    T = tiles_of([n for n, *_ in pieces])
+    sees = lambda x, t: t < len(T) and T[t][1] < pieces[T[t][0]][1 + x]
+    for n in ("qf", "qe", "k0f", "k0e", "tail"):
+        M.bar(n, 1)
+    for i in range(stages):
+        M.bar(f"f{i}", 1), M.bar(f"e{i}", 1)
+    for x in (0, 1):
+        for n in ("sf", "p", "od", "of"):
+            M.bar(f"{n}{x}", 1)
+    count = {"q": 0, "k0": 0, "t": 0, "tail": 0}
+
+    def producer():
+        run = True
+        if not T:
+            return
+
+        def copy_q(p, run):
+            if run and p > 0 and not early_q:
+                run = yield from M.wait("qe", (p - 1) & 1)
+            run = run and not M.aborted
+            if run:
+                for u in range(len(T)):
+                    for x in (0, 1):
+                        need(T[u][0] != p - 1 or not sees(x, u) or (f"S{x}", u) in done, f"Q {p - 1} overwritten")
+                M.load("qf", 1, ("Q", p))
+                count["q"] = p + 1
+            return run
+        run = yield from copy_q(0, run)
+        M.load("k0f", 1, ("K", 0))
+        count["k0"] = 1
+        tails = 0
+        for t, (p, k, last) in enumerate(T):
+            b = t % stages
+            more = t + 1 < len(T)
+            if run and t == stages - 1:
+                run = yield from M.wait("k0e", 0)
+            if run and t >= stages:
+                run = yield from M.wait(f"e{b}", (t // stages - 1) & 1)
+            run = run and not M.aborted
+            if run:
+                for x in (0, 1):
+                    need(t < stages or not sees(x, t - stages) or (f"PV{x}", t - stages) in done, f"V {t} too early")
+                    need(t + 1 < stages or not sees(x, t - stages + 1) or (f"S{x}", t - stages + 1) in done,
+                         f"K {t + 1} too early")
+                count["t"] = t + 1
+                if not (last and pieces[p][3]):
+                    M.expect(f"f{b}", 2 if more else 1)
+                    M.copy(f"f{b}", 1, ("V", t))
+                    if more:
+                        M.copy(f"f{b}", 1, ("K", t + 1))
+                    done.add(("clean", t))
+                else:
+                    M.B[f"f{b}"].tx += 1 if more else 0
+                    M.load("tail", 1, ("V", t))
+                    count["tail"] = tails + 1
+                    if more:
+                        M.copy(f"f{b}", 1, ("K", t + 1))
+                    run = yield from M.wait("tail", tails & 1)
+                    tails += 1
+                    if run:
+                        done.add(("clean", t))
+                    M.B[f"f{b}"].arrive()
+            if more and T[t + 1][1] == 0:
+                run = yield from copy_q(T[t + 1][0], run)
+            yield None
+
+    def issuer():
+        if not T:
+            return
+        np, seen = [0, 0], [0, 0]
+
+        def issue_s(x, t):
+            need(("Q", T[t][0]) in done and ("K", t) in done, f"S{x}({t}) before its operands")
+            M.mma("i", (f"S{x}", t))
+            M.commit("i", f"sf{x}")
+        run = yield from M.wait("qf", 0)
+        if run:
+            run = yield from M.wait("k0f", 0)
+        if run:
+            for x in (0, 1):
+                if sees(x, 0):
+                    issue_s(x, 0)
+            M.commit("i", "k0e")
+            if T[0][2]:
+                M.commit("i", "qe")
+        for t, (p, k, last) in enumerate(T):
+            if not run:
+                break
+            more, crosses = t + 1 < len(T), last
+            run = yield from M.wait(f"f{t % stages}", (t // stages) & 1)
+            for x in (0, 1):
+                if not run:
+                    break
+                if sees(x, t):
+                    if k == 0:
+                        if seen[x] > 0:
+                            run = yield from M.wait(f"of{x}", (seen[x] - 1) & 1)
+                        seen[x] += 1
+                    if run:
+                        run = yield from M.wait(f"p{x}", np[x] & 1)
+                    np[x] += 1
+                    if not run:
+                        break
+                    # (after an abort the stage is completed as it is; the product then runs on stale data)
+                    need(M.aborted or (("V", t) in done and ("clean", t) in done), f"PV{x}({t}) before V")
+                    need((f"P{x}", t) in done, f"PV{x}({t}) before P")
+                    M.mma("i", (f"PV{x}", t))
+                    if k + 1 == min(pieces[p][0], pieces[p][1 + x]):
+                        M.commit("i", f"od{x}")
+                if more and not crosses and sees(x, t + 1):
+                    issue_s(x, t + 1)
+            if not run:
+                break
+            if crosses and more:
+                run = yield from M.wait("qf", T[t + 1][0] & 1)
+                if not run:
+                    break
+                for x in (0, 1):
+                    if sees(x, t + 1):
+                        issue_s(x, t + 1)
+            if more and T[t + 1][2]:
+                M.commit("i", "qe")
+            M.commit("i", f"e{t % stages}")
+            yield None
+
+    def softmax(x):
+        run, cnt, n = True, 0, 0
+        for p, (tiles, *vis, _) in enumerate(pieces):
+            mine = [t for t in range(len(T)) if T[t][0] == p and sees(x, t)]
+            for t in mine:
+                if run:
+                    run = yield from M.wait(f"sf{x}", cnt & 1)
+                cnt += 1
+                if run:
+                    need((f"S{x}", t) in done, f"S{x}({t}) read too early")
+                    need(T[t][1] == 0 or (f"PV{x}", t - 1) in done, f"O{x} rescaled at {t} too early")
+                yield None
+                if run:
+                    done.add((f"P{x}", t))
+                    M.B[f"p{x}"].arrive()
+            if mine:
+                if run:
+                    run = yield from M.wait(f"od{x}", n & 1)
+                n += 1
+                need(not run or (f"PV{x}", mine[-1]) in done, f"O{x} read too early")
+                if run:
+                    M.B[f"of{x}"].arrive()
+
+    def issued():
+        out = [("qf", (count["q"] - 1) & 1)] if count["q"] else []
+        out += [("k0f", 0)] if count["k0"] else []
+        out += [("tail", (count["tail"] - 1) & 1)] if count["tail"] else []
+        return out + last_phases("f", count["t"], stages)
+    return finish(M, {"prod": producer(), "mma": issuer(), "s0": softmax(0), "s1": softmax(1)}, issued)
+
+
+def chunk_pieces(seed):
+    r = random.Random(seed * 7919)
+    out = []
+    for n in pieces_for(seed):
+        kind = r.random()
+        v1 = n if kind < 0.7 else 0  # 0: no second query tile, or no key that it sees
+        v0 = r.randint(0, n) if v1 else r.choice([n, n, 0 if n == 1 else n])
+        out.append((n, v0, v1, r.random() < 0.5))
+    return out
+
+
+def test_chunk_has_no_deadlock_or_hazard():
+    for seed in range(2500):
+        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed)
+        assert res == "ok" and not errs, (chunk_pieces(seed), seed, res, errs[:3])
+
+
+def test_chunk_ends_after_waits_that_run_out():
+    for seed in range(1500):
+        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, abort_p=0.02)
+        assert res == "ok" and not errs, (chunk_pieces(seed), seed, res, errs[:3])
+
+
+def test_chunk_model_finds_a_missing_wait():
+    assert any(chunk(chunk_pieces(s), 2, s, early_q=True)[1] for s in range(500))
+
+
+# ----------------------------------------------------------------------------- weights
+
+
+def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
+    """pieces: the query tiles of each key tile (few rows: one each, and every third begins another head)."""
+    M = Machine(seed, abort_p)
+    done, need = M.done, M.need
+    T = tiles_of(pieces)
+    G, kb, qb = 3, (5 if few else 2), (2 if few else 4)
+    head = lambda p: p % 3 == 0  # few rows: Q is copied where a head begins
+    q_of = (lambda t: T[t][0] // 3) if few else (lambda t: t)
+    for n, c in (("kf", kb), ("ke", kb), ("qf", qb), ("qe", qb), ("sf", 4), ("fr", 4)):
+        for i in range(c):
+            M.bar(f"{n}{i}", 1)
+    for i in range(2):
+        M.bar(f"sr{i}", G), M.bar(f"sx{i}", 1)
+    count = {"k": 0, "q": 0}
+
+    def producer():
+        run = True
+
+        def copy_q(q, run):
+            if run and q >= qb:
+                run = yield from M.wait(f"qe{q % qb}", (q // qb - 1) & 1)
+            run = run and not M.aborted
+            if run:
+                need(all(("S", t) in done for t in range(len(T)) if q_of(t) == q - qb), f"Q {q - qb} overwritten")
+                M.load(f"qf{q % qb}", 1, ("Q", q))
+                count["q"] = q + 1
+            return run
+        for p, n in enumerate(pieces):
+            if few and head(p):
+                run = yield from copy_q(p // 3, run)
+            if run and p >= kb:
+                run = yield from M.wait(f"ke{p % kb}", (p // kb - 1) & 1)
+            run = run and not M.aborted
+            if run:
+                need(all(("S", t) in done for t in range(len(T)) if T[t][0] == p - kb), f"K {p - kb} overwritten")
+                M.load(f"kf{p % kb}", 1, ("K", p))
+                count["k"] = p + 1
+            if not few:
+                for t in range(len(T)):
+                    if T[t][0] == p:
+                        run = yield from copy_q(t, run)
+            yield None
+
+    def issuer():
+        run = True
+        for t, (p, k, last) in enumerate(T):
+            if run and few and head(p):
+                run = yield from M.wait(f"qf{p // 3 % qb}", (p // 3 // qb) & 1)
+            if run and k == 0:
+                run = yield from M.wait(f"kf{p % kb}", (p // kb) & 1)
+            if run and not few:
+                run = yield from M.wait(f"qf{t % qb}", (t // qb) & 1)
+            if run and t >= 4:
+                run = yield from M.wait(f"fr{t & 3}", ((t >> 2) - 1) & 1)
+            if not run:
+                break
+            need(("K", p) in done and ("Q", q_of(t)) in done, f"S({t}) before its operands")
+            need(t < 4 or ("read", t - 4) in done, f"S({t}) over S({t - 4})")
+            M.mma("i", ("S", t))
+            M.commit("i", f"sf{t & 3}")
+            if not few:
+                M.commit("i", f"qe{t % qb}")
+            if last:
+                M.commit("i", f"ke{p % kb}")
+                if few and t + 1 < len(T) and head(T[t + 1][0]):
+                    M.commit("i", f"qe{p // 3 % qb}")
+            yield None
+
+    def group(g):
+        run = True
+        for p in range(len(pieces)):
+            for t in range(len(T)):
+                if T[t][0] != p or t % G != g:
+                    continue
+                if run:
+                    run = yield from M.wait(f"sf{t & 3}", (t >> 2) & 1)
+                need(not run or ("S", t) in done, f"S({t}) read too early")
+                yield None
+                if run:
+                    done.add(("read", t))
+                    M.B[f"fr{t & 3}"].arrive()
+            if not few:
+                if run and p >= 2 and not no_sum_free:
+                    run = yield from M.wait(f"sx{p & 1}", ((p >> 1) - 1) & 1)
+                if run:
+                    need(p < 2 or ("sum", p - 2) in done, f"the sums of piece {p - 2} overwritten")
+                    M.B[f"sr{p & 1}"].arrive()
+                yield None
+
+    def adder():
+        run = True
+        for p in range(len(pieces)):
+            if run:
+                run = yield from M.wait(f"sr{p & 1}", (p >> 1) & 1)
+            if run:
+                done.add(("sum", p))
+                M.B[f"sx{p & 1}"].arrive()
+            yield None
+
+    roles = {"prod": producer(), "mma": issuer(), **{f"g{g}": group(g) for g in range(G)}}
+    if not few:
+        roles["add"] = adder()
+
+    def issued():
+        return last_phases("qf", count["q"], qb) + last_phases("kf", count["k"], kb)
+    return finish(M, roles, issued)
+
+
+def weight_pieces(seed, few):
+    return [1] * random.Random(seed).randint(0, 14) if few else pieces_for(seed)
+
+
+def test_weights_has_no_deadlock_or_hazard():
+    for seed in range(2500):
+        few = bool(seed & 1)
+        res, errs = weights(weight_pieces(seed, few), few, seed)
+        assert res == "ok" and not errs, (weight_pieces(seed, few), few, seed, res, errs[:3])
+
+
+def test_weights_ends_after_waits_that_run_out():
+    for seed in range(1500):
+        few = bool(seed & 1)
+        res, errs = weights(weight_pieces(seed, few), few, seed, abort_p=0.02)
+        assert res == "ok" and not errs, (weight_pieces(seed, few), few, seed, res, errs[:3])
+
+
+def test_weights_model_finds_a_missing_wait():
+    def faulty(s):
+        try:
+            return bool(weights(weight_pieces(s, False), False, s, no_sum_free=True)[1])
+        except AssertionError:  # an arrival beyond a barrier's count
+            return True
+    assert any(faulty(s) for s in range(500))
