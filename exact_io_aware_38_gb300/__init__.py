@@ -572,70 +572,107 @@ def fwd_splitkv(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=None
 # ----------------------------------------------------------------------------- paged cache
 
 
+# These calls serve single tokens, where a pass takes ten microseconds on the GPU: the checks look at each
+# tensor once, and equal strides share one structure.
+
+
 def _paged_view(name, t, dims):
     """fa_strides of a [batch or page, row, head, d] view, or of packed [rows, heads, d] rows. The stride of an
     axis of one element is never used; it is replaced by a legal one."""
-    if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == dims and t.stride(-1) == 1):
+    n, st = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(n) != dims or st[-1] != 1 or not t.is_cuda:
         shape = "[rows, heads, d]" if dims == 3 else "4-D, [batch or page, row, head, d]"
         raise ValueError(f"{name} must be a bf16 CUDA tensor, {shape}, with a contiguous last dimension")
-    n, st = t.shape, t.stride()
-    batch, row, head = (0, 0, 1) if dims == 3 else (0, 1, 2)
-    span = n[-1]
-    pick = lambda i: st[i] if n[i] > 1 else span
-    return Strides(pick(row), pick(head), 0 if dims == 3 else pick(batch))
+    if 1 in n:
+        st = [n[-1] if size == 1 else x for size, x in zip(n, st)]
+    return Strides(st[0], st[1], 0) if dims == 3 else Strides(st[1], st[2], st[0])
+
+
+def _paged_views(name_a, a, name_b, b, dims):
+    """_paged_view of two tensors of one shape."""
+    va = _paged_view(name_a, a, dims)
+    same = b.stride() == a.stride() and b.dtype is a.dtype and b.device == a.device
+    return va, va if same else _paged_view(name_b, b, dims)
 
 
 def _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal, scale):
     """The fa_paged_problem of new rows q ([B, N, heads, d], or packed [rows, heads, d] with cu_seqlens_q) over a
     cache; q is None where a call has no new rows. Also q's number of dimensions."""
     dev = k_cache.device
-    if k_cache.dim() != 4 or (v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.device != dev)):
+    shape = k_cache.shape
+    if len(shape) != 4 or (v_cache is not None and (v_cache.shape != shape or v_cache.device != dev)):
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, d] tensors of one shape, on one device")
-    pages, page_size, Hkv, d = k_cache.shape
-    for name, t, dims in (("page_table", page_table, 2), ("seqlens_k", seqlens_k, 1)):
-        if not (t.dtype == torch.int32 and t.is_contiguous() and t.dim() == dims and t.device == dev):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {dev}")
+    pages, page_size, Hkv, d = shape
+    if not (page_table.dtype is torch.int32 and page_table.dim() == 2 and page_table.is_contiguous()
+            and page_table.device == dev):
+        raise ValueError(f"page_table must be a contiguous int32 [B, max_pages] tensor on {dev}")
     B, width = page_table.shape
-    if seqlens_k.shape[0] != B:
-        raise ValueError("page_table and seqlens_k must have one row and one length per sequence")
+    if not (seqlens_k.dtype is torch.int32 and seqlens_k.shape == (B,) and seqlens_k.is_contiguous()
+            and seqlens_k.device == dev):
+        raise ValueError(f"seqlens_k must be a contiguous int32 [{B}] tensor on {dev}, as page_table has {B} rows")
     packed = cu_seqlens_q is not None
     rows_q, Nq, H = 0, 1, Hkv
     if q is not None:
-        H = q.shape[-2] if q.dim() >= 2 else 0
-        if q.dim() != (3 if packed else 4) or q.shape[-1] != d or q.device != dev or H < 1 or H % Hkv != 0:
+        n = q.shape
+        H = n[-2] if len(n) >= 2 else 0
+        if len(n) != (3 if packed else 4) or n[-1] != d or q.device != dev or H < 1 or H % Hkv != 0:
             raise ValueError("new tokens must be [B, N, heads, d] (packed: [rows, heads, d] with cu_seqlens_q) on the "
                              "cache's device, with the cache's d and a multiple of its heads")
         if packed:
-            if not (cu_seqlens_q.dtype == torch.int32 and cu_seqlens_q.is_contiguous() and cu_seqlens_q.device == dev
-                    and cu_seqlens_q.shape == (B + 1,)):
+            if not (cu_seqlens_q.dtype is torch.int32 and cu_seqlens_q.shape == (B + 1,)
+                    and cu_seqlens_q.is_contiguous() and cu_seqlens_q.device == dev):
                 raise ValueError(f"cu_seqlens_q must be a contiguous int32 [{B + 1}] tensor on {dev}")
             if max_seqlen_q is None:
                 raise ValueError("packed batches need max_seqlen_q")
-            rows_q, Nq = q.shape[0], int(max_seqlen_q)
+            rows_q, Nq = n[0], int(max_seqlen_q)
         else:
-            if q.shape[0] != B:
+            if n[0] != B:
                 raise ValueError("page_table must have one row per sequence")
-            Nq = q.shape[1]
+            Nq = n[1]
     elif packed:
         raise ValueError("cu_seqlens_q without new tokens")
     bound = width * page_size if max_seqlen_k is None else int(max_seqlen_k)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     return PagedProblem(B, H, Hkv, d, page_size, pages, width, page_table.data_ptr(), seqlens_k.data_ptr(), Nq,
-                        min(bound, 2**31 - 1), _ptr(cu_seqlens_q), rows_q, int(causal), scale), 3 if packed else 4
+                        min(bound, 2**31 - 1), cu_seqlens_q.data_ptr() if packed else None, rows_q, int(causal),
+                        1.0 / math.sqrt(d) if scale is None else float(scale)), 3 if packed else 4
 
 
-def _launch(dev, stream, call):
-    """call(stream handle) with the tensors' device current; raises FaError for an error code."""
-    with torch.cuda.device(dev):
-        rc = call(_stream(stream))
+_SMS = {}
+
+
+def _num_sms(dev):
+    """SM count of a device."""
+    n = _SMS.get(dev.index)
+    if n is None:
+        n = _SMS[dev.index] = torch.cuda.get_device_properties(dev).multi_processor_count
+    return n
+
+
+def _launch(dev, stream, call, *args):
+    """call(*args, stream handle) with the tensors' device current, on the given stream or that device's current
+    one; raises FaError for an error code."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            rc = call(*args, _stream(stream))
+    else:
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
     if rc != 0:
         raise FaError(rc)
 
 
+def _scratch(workspace, nbytes, dev):
+    """(pointer, bytes) of the caller's workspace, or of a new one, and its tensor."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), nbytes, workspace
+    _check_aux("workspace", workspace, None, nbytes, dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def _check_weights(key_weights, p, dev):
     shape = (p.num_pages, p.Hkv, p.page_size)
-    if not (key_weights.dtype == torch.float32 and key_weights.is_contiguous() and key_weights.device == dev
-            and key_weights.shape == shape):
+    if not (key_weights.dtype is torch.float32 and key_weights.shape == shape and key_weights.is_contiguous()
+            and key_weights.device == dev):
         raise ValueError(f"key_weights must be a contiguous float32 {list(shape)} tensor on {dev}")
 
 
@@ -649,29 +686,27 @@ def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max
     p, dims = _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal,
                      scale)
     dev = q.device
-    if q.numel() == 0:  # no new token anywhere: an empty batch
-        p = None
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
-    if o.shape != q.shape or o.device != dev:
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.device != dev:
         raise ValueError("out must have q's shape and device")
-    shape = (q.shape[1], q.shape[0]) if dims == 3 else (q.shape[0], q.shape[2], q.shape[1])
-    lse = torch.empty(shape, dtype=torch.float32, device=dev) if lse is None else lse
-    _check_aux("lse", lse, torch.float32, math.prod(shape), dev)
+    if lse is None:
+        n = q.shape
+        lse = torch.empty((n[1], n[0]) if dims == 3 else (n[0], n[2], n[1]), dtype=torch.float32, device=dev)
+    else:
+        _check_aux("lse", lse, torch.float32, q.numel() // p.d, dev)
     _check_aux("status", status, torch.int32, 1, dev)
-    sq, so = _paged_view("q", q, dims), _paged_view("out", o, dims)
-    sk, sv = _paged_view("k_cache", k_cache, 4), _paged_view("v_cache", v_cache, 4)
-    if p is None:
-        return o, lse
+    sq, so = _paged_views("q", q, "out", out, dims)
+    sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4)
+    if p.B == 0 or q.numel() == 0:  # no new token anywhere
+        return out, lse
     if num_sms is None:
-        num_sms = torch.cuda.get_device_properties(dev).multi_processor_count
-    nbytes = fa_fwd_paged_workspace_bytes(p, num_sms)
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check_aux("workspace", workspace, None, nbytes, dev)
-    _launch(dev, stream, lambda st: fa_fwd_paged(
-        p, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, o.data_ptr(), so,
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status), st))
-    return o, lse
+        num_sms = _num_sms(dev)
+    L, at = lib(), ctypes.byref(p)
+    ws, nbytes, _keep = _scratch(workspace, L.fa_fwd_paged_workspace_bytes(at, num_sms), dev)
+    _launch(dev, stream, L.fa_fwd_paged, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv,
+            out.data_ptr(), so, lse.data_ptr(), ws, nbytes, _ptr(status))
+    return out, lse
 
 
 def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, *,
@@ -685,13 +720,11 @@ def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=Non
     _check_aux("status", status, torch.int32, 1, k.device)
     if key_weights is not None:
         _check_weights(key_weights, p, k.device)
-    views = [_paged_view(n, t, dims) for n, t in (("k", k), ("v", v))]
-    views += [_paged_view(n, t, 4) for n, t in (("k_cache", k_cache), ("v_cache", v_cache))]
-    if k.numel() == 0:
-        return
-    _launch(k.device, stream, lambda st: fa_paged_append(
-        p, k.data_ptr(), views[0], v.data_ptr(), views[1], k_cache.data_ptr(), views[2], v_cache.data_ptr(), views[3],
-        _ptr(key_weights), _ptr(status), st))
+    skn, svn = _paged_views("k", k, "v", v, dims)
+    sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4)
+    if p.B > 0 and k.numel() > 0:
+        _launch(k.device, stream, lib().fa_paged_append, ctypes.byref(p), k.data_ptr(), skn, v.data_ptr(), svn,
+                k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, _ptr(key_weights), _ptr(status))
 
 
 def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_seqlens_q=None, max_seqlen_q=None,
@@ -701,21 +734,19 @@ def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_se
     every cached key, summed over the rows and the query heads of each K/V head (fa_paged_key_weights). q, lse and the
     other arguments are those of fwd_paged, which returned lse."""
     p, dims = _paged(q, k_cache, None, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal, scale)
-    _check_aux("lse", lse, torch.float32, q.numel() // p.d, q.device)
-    _check_aux("status", status, torch.int32, 1, q.device)
-    _check_weights(key_weights, p, q.device)
+    dev = q.device
+    _check_aux("lse", lse, torch.float32, q.numel() // p.d, dev)
+    _check_aux("status", status, torch.int32, 1, dev)
+    _check_weights(key_weights, p, dev)
     sq, sk = _paged_view("q", q, dims), _paged_view("k_cache", k_cache, 4)
-    if q.numel() == 0:
+    if p.B == 0 or q.numel() == 0:
         return key_weights
     if num_sms is None:
-        num_sms = torch.cuda.get_device_properties(q.device).multi_processor_count
-    nbytes = fa_paged_key_weights_workspace_bytes(p, num_sms)
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _check_aux("workspace", workspace, None, nbytes, q.device)
-    _launch(q.device, stream, lambda st: fa_paged_key_weights(
-        p, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(), key_weights.data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status), st))
+        num_sms = _num_sms(dev)
+    L, at = lib(), ctypes.byref(p)
+    ws, nbytes, _keep = _scratch(workspace, L.fa_paged_key_weights_workspace_bytes(at, num_sms), dev)
+    _launch(dev, stream, L.fa_paged_key_weights, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(),
+            key_weights.data_ptr(), ws, nbytes, _ptr(status))
     return key_weights
 
 
@@ -730,15 +761,19 @@ def paged_evict(k_cache, v_cache, key_weights, page_table, seqlens_k, keep, *, r
     if not (0 <= recent <= keep and 1 <= keep < 2**31):
         raise ValueError("keep must be at least 1 and recent between 0 and keep")
     _check_weights(key_weights, p, dev)
-    kept = torch.empty((p.B, p.Hkv, keep), dtype=torch.int32, device=dev) if kept is None else kept
-    seqlens_out = torch.empty((p.B,), dtype=torch.int32, device=dev) if seqlens_out is None else seqlens_out
-    _check_aux("kept", kept, torch.int32, p.B * p.Hkv * keep, dev)
-    _check_aux("seqlens_out", seqlens_out, torch.int32, p.B, dev)
+    if kept is None:
+        kept = torch.empty((p.B, p.Hkv, keep), dtype=torch.int32, device=dev)
+    else:
+        _check_aux("kept", kept, torch.int32, p.B * p.Hkv * keep, dev)
+    if seqlens_out is None:
+        seqlens_out = torch.empty((p.B,), dtype=torch.int32, device=dev)
+    else:
+        _check_aux("seqlens_out", seqlens_out, torch.int32, p.B, dev)
     _check_aux("status", status, torch.int32, 1, dev)
-    sk, sv = _paged_view("k_cache", k_cache, 4), _paged_view("v_cache", v_cache, 4)
-    _launch(dev, stream, lambda st: fa_paged_evict(
-        p, keep, recent, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, key_weights.data_ptr(), kept.data_ptr(),
-        seqlens_out.data_ptr(), _ptr(status), st))
+    sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4)
+    if p.B > 0:
+        _launch(dev, stream, lib().fa_paged_evict, ctypes.byref(p), keep, recent, k_cache.data_ptr(), sk,
+                v_cache.data_ptr(), sv, key_weights.data_ptr(), kept.data_ptr(), seqlens_out.data_ptr(), _ptr(status))
     return kept, seqlens_out
 
 
