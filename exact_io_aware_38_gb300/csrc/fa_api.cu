@@ -695,7 +695,7 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
     return rc;
   if (!k_new || !v_new || !k_cache || !v_cache) return FA_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(key_weights, 4) || !aligned(dev_status, 4))
+      !aligned(key_weights, 16) || !aligned(dev_status, 4))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
   a.k_new = k_new;
@@ -727,7 +727,7 @@ int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, 
       (rc = take_cache_strides(sk, p, &a.sk)) != FA_OK)
     return rc;
   if (!q || !k_cache || !lse || !key_weights) return FA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(key_weights, 4) ||
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(key_weights, 16) ||
       !aligned(dev_status, 4) || !aligned(workspace, kAlign))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
@@ -752,7 +752,7 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
   if ((rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK) return rc;
   if (!k_cache || !v_cache || !key_weights || !kept || !seqlens_out || seqlens_out == p->seqlens_k)
     return FA_ERR_INVALID_ARG;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key_weights, 4) || !aligned(kept, 4) ||
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key_weights, 16) || !aligned(kept, 4) ||
       !aligned(seqlens_out, 4) || !aligned(dev_status, 4))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;

@@ -41,9 +41,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const FaPagedArgs a) 
 
 // ----------------------------------------------------------------------------- eviction
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelRegs = 16;                           // weights a thread keeps in registers
-constexpr int kSelSpan = kSelThreads * kSelRegs;       // weights a CTA keeps in registers
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32, kSelRow = 4 * kSelThreads;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -58,11 +56,13 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// A store into the shared memory of CTA `cta` of the cluster, at the address that `p` has there.
-__device__ __forceinline__ void store_peer(int* p, uint32_t cta, int x) {
+// A load from the shared memory of CTA `cta` of the cluster, at the address that `p` has there.
+__device__ __forceinline__ int load_peer(const int* p, uint32_t cta) {
   uint32_t at;
+  int x;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(cta));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
 }
 
 // The order of weights as unsigned integers: larger weight, larger number; -0 equals 0, NaN is 0.
@@ -72,124 +72,195 @@ __device__ __forceinline__ uint32_t weight_rank(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int warp_add(int x) { return __reduce_add_sync(0xffffffffu, x); }
+// Sums over the threads of the CTA before this one, and over all (exclusive scan).
+__device__ __forceinline__ int cta_scan(int x, int* warp_tot, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();  // the last scan's totals are read
+  if (lane == 31) warp_tot[warp] = inc;
+  __syncthreads();
+  int before = inc - x;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kSelWarps; ++i) {
+    if (i < warp) before += warp_tot[i];
+    total += warp_tot[i];
+  }
+  return before;
+}
 
-// One cluster per (sequence, K/V head), of the size that keeps all candidates' weights in registers
-// (16 384 a CTA; beyond eight CTAs the rest is read again in each step). The rank of the last kept
-// weight is found bit by bit from the top, by counting: 32 counts over registers need no histogram
-// and so no atomics, whose conflicts the few exponents of attention weights would provoke. Then a
-// key's place is the number of larger weights before it plus that of equal ones, as far as those
-// stay; both come from ballots and one scan, in key order.
+// One cluster per (sequence, K/V head). A row is 1024 consecutive keys, four to a thread (a page holds
+// them together, so one table entry and one 16-byte load fetch them); a thread keeps R rows' weights as
+// ranks in registers and reads those of further rows again in each pass. The rank of the last kept
+// weight is found 8 bits at a time from the top, in four passes of a histogram in shared memory (summed
+// over the cluster) of which each thread scans a bin. Then a key's place is the number of larger weights
+// before it plus that of equal ones, as far as those stay, by a scan over threads and rows in key order.
+// Bound by latency: counting against bounds instead, 16 steps of 2 bits, took 13 us for 1030 keys.
+template <int R>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPagedArgs a) {
   grid_dependency_wait();
-  __shared__ int warp_cnt[2][32];
-  __shared__ int cta_cnt[2][8];                  // the cluster's counts, per parity of the step
-  __shared__ int before_gt[32], before_eq[32];   // per warp of a row of 1024 keys
-  __shared__ int cta_gt[8], cta_eq[8];
+  __shared__ int hist[2][256];
+  __shared__ int warp_tot[kSelWarps];
+  __shared__ int s_digit, s_need;
+  __shared__ int cta_tot;  // this CTA's larger and equal weights, packed below
+  __shared__ int cta_eq;
   const PagedShape& s = a.s;
   const uint32_t cta = cluster_rank(), ctas = cluster_size();
-  const int head = blockIdx.x / ctas, hk = head % s.Hkv, b = head / s.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x / ctas, hk = head % s.Hkv, b = head / s.Hkv, tid = threadIdx.x;
   const int L = paged_seq(s, b).Lk;
   int32_t* kept = a.kept + (size_t)head * a.keep;
-  if (hk == 0 && cta == 0 && threadIdx.x == 0) a.seqlens_out[b] = min(L, a.keep);
+  if (hk == 0 && cta == 0 && tid == 0) a.seqlens_out[b] = min(L, a.keep);
   if (L <= a.keep) {  // (the whole cluster)
-    for (int t = cta * kSelThreads + threadIdx.x; t < a.keep; t += ctas * kSelThreads) kept[t] = t < L ? t : -1;
+    for (int t = cta * kSelThreads + tid; t < a.keep; t += ctas * kSelThreads) kept[t] = t < L ? t : -1;
     return;
   }
   const int old = L - a.recent, take = a.keep - a.recent;  // candidates, and how many of them stay
-  for (int t = cta * kSelThreads + threadIdx.x; t < a.recent; t += ctas * kSelThreads) kept[take + t] = old + t;
+  for (int t = cta * kSelThreads + tid; t < a.recent; t += ctas * kSelThreads) kept[take + t] = old + t;
   if (take == 0) return;
-  const int rows = ((old + (int)ctas - 1) / (int)ctas + kSelThreads - 1) / kSelThreads;  // of 1024 keys, per CTA
-  const int j0 = (int)cta * rows * kSelThreads + threadIdx.x;
-  auto rank_of = [&](int j) -> uint32_t {
-    if (j >= old) return 0u;
-    const int page = paged_page(s, b, j >> s.page_shift, a.status);
-    return page < 0 ? 0u : weight_rank(a.weights[weight_offset(s, page, hk, j & ((1 << s.page_shift) - 1))]);
+  const int rows = ((old + (int)ctas - 1) / (int)ctas + kSelRow - 1) / kSelRow;  // per CTA
+  const int j0 = (int)cta * rows * kSelRow + 4 * tid;                           // first key of row 0
+  hist[0][tid] = 0;
+  // Ranks of the thread's four keys of a row; 0 past the end and on a page that is none of the cache's.
+  // No branch: such a place reads page 0, and the loads of all rows are in flight together.
+  bool bad = false;
+  auto page_at = [&](int k) {
+    return __ldg(s.table + (size_t)b * s.max_pages + (min(j0 + k * kSelRow, old - 1) >> s.page_shift));
   };
-  uint32_t r[kSelRegs];
+  auto ranks_at = [&](int k, int page) -> uint4 {
+    const int j = j0 + k * kSelRow, left = k < rows ? old - j : 0;  // keys of the four that are candidates
+    const bool ok = (unsigned)page < (unsigned)s.num_pages;
+    bad |= !ok && left > 0;
+    const float4 w = *reinterpret_cast<const float4*>(
+        a.weights + weight_offset(s, ok ? page : 0, hk, j & ((1 << s.page_shift) - 1)));
+    const int n = ok ? left : 0;
+    return make_uint4(n > 0 ? weight_rank(w.x) : 0u, n > 1 ? weight_rank(w.y) : 0u, n > 2 ? weight_rank(w.z) : 0u,
+                      n > 3 ? weight_rank(w.w) : 0u);
+  };
+  uint4 r[R];
+  {
+    int page[R];
 #pragma unroll
-  for (int k = 0; k < kSelRegs; ++k) r[k] = k < rows ? rank_of(j0 + k * kSelThreads) : 0u;
-  uint32_t last = 0u;  // the largest rank that `take` candidates reach
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t c = last | (1u << bit);
-    int cnt = 0;
+    for (int k = 0; k < R; ++k) page[k] = page_at(k);
 #pragma unroll
-    for (int k = 0; k < kSelRegs; ++k)
-      if (k < rows) cnt += r[k] >= c;
-    for (int k = kSelRegs; k < rows; ++k) cnt += rank_of(j0 + k * kSelThreads) >= c;
-    cnt = warp_add(cnt);
-    if (lane == 0) warp_cnt[bit & 1][warp] = cnt;
-    __syncthreads();
-    cnt = warp_add(warp_cnt[bit & 1][lane]);
+    for (int k = 0; k < R; ++k) r[k] = ranks_at(k, page[k]);
+    if (bad) report_status(a.status, FA_ERR_BOUNDS);
+  }
+  // Places past the end count as weights of rank 0, which changes no choice above it.
+  uint32_t last = 0u;  // the digits found so far of the rank of the last kept weight
+  int need = take;     // of the weights with those digits, how many stay
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass, buf = pass & 1;
+    const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+    auto count = [&](uint32_t x) {
+      if ((x & above) == last) atomicAdd(&hist[buf][(x >> shift) & 255], 1);
+    };
+    __syncthreads();  // the bins are 0
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (k < rows) {
+        count(r[k].x);
+        count(r[k].y);
+        count(r[k].z);
+        count(r[k].w);
+      }
+    for (int k = R; k < rows; ++k) {
+      const uint4 x = ranks_at(k, page_at(k));
+      count(x.x);
+      count(x.y);
+      count(x.z);
+      count(x.w);
+    }
+    hist[buf ^ 1][tid] = 0;
+    int bin = 255 - tid, mine;  // thread 0 has the largest digit
     if (ctas > 1) {
-      if (threadIdx.x < ctas) store_peer(&cta_cnt[bit & 1][cta], threadIdx.x, cnt);
       cluster_sync();
-      cnt = warp_add(lane < (int)ctas ? cta_cnt[bit & 1][lane] : 0);
+      mine = 0;
+      for (uint32_t c = 0; c < ctas; ++c) mine += load_peer(&hist[buf][bin], c);
+      cluster_sync();  // every CTA has read these bins before they are cleared
+    } else {
+      __syncthreads();
+      mine = hist[buf][bin];
     }
-    if (cnt >= take) last = c;
+    int total;
+    const int larger = cta_scan(mine, warp_tot, total);
+    if (larger < need && larger + mine >= need) {
+      s_digit = bin;
+      s_need = need - larger;
+    }
+    __syncthreads();
+    last |= (uint32_t)s_digit << shift;
+    need = s_need;
   }
-  // Per CTA the larger and equal weights, then the places.
-  auto larger = [&](int j, uint32_t x) { return j < old && x > last; };
-  auto equal = [&](int j, uint32_t x) { return j < old && x == last; };
-  int gt = 0, eq = 0;
+  // Places: larger and equal weights of the thread per row (packed: gt | eq << 16).
+  auto count4 = [&](uint4 x, int k) -> uint32_t {
+    const int left = k < rows ? old - (j0 + k * kSelRow) : 0;
+    uint32_t n = 0;
+    n += (left > 0 && x.x > last) + (left > 1 && x.y > last) + (left > 2 && x.z > last) + (left > 3 && x.w > last);
+    n += ((uint32_t)((left > 0 && x.x == last) + (left > 1 && x.y == last) + (left > 2 && x.z == last) +
+                     (left > 3 && x.w == last)))
+         << 16;
+    return n;
+  };
+  int gt_before = 0, eq_before = 0;  // in the CTAs before this one, then also in the rows before
+  if (ctas > 1) {
+    int gt = 0, eq = 0;
 #pragma unroll
-  for (int k = 0; k < kSelRegs; ++k)
-    if (k < rows) {
-      gt += larger(j0 + k * kSelThreads, r[k]);
-      eq += equal(j0 + k * kSelThreads, r[k]);
+    for (int k = 0; k < R; ++k) {
+      const uint32_t n = count4(r[k], k);
+      gt += n & 0xffff;
+      eq += n >> 16;
     }
-  for (int k = kSelRegs; k < rows; ++k) {
-    const uint32_t x = rank_of(j0 + k * kSelThreads);
-    gt += larger(j0 + k * kSelThreads, x);
-    eq += equal(j0 + k * kSelThreads, x);
-  }
-  gt = warp_add(gt);
-  eq = warp_add(eq);
-  __syncthreads();  // the last step's counts are read
-  if (lane == 0) {
-    warp_cnt[0][warp] = gt;
-    warp_cnt[1][warp] = eq;
-  }
-  __syncthreads();
-  gt = warp_add(warp_cnt[0][lane]);
-  eq = warp_add(warp_cnt[1][lane]);
-  if (threadIdx.x < ctas) {
-    store_peer(&cta_gt[cta], threadIdx.x, gt);
-    store_peer(&cta_eq[cta], threadIdx.x, eq);
-  }
-  cluster_sync();
-  int all_gt = 0, gt_before = 0, eq_before = 0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    all_gt += cta_gt[c];
-    if (c < cta) {
-      gt_before += cta_gt[c];
-      eq_before += cta_eq[c];
+    for (int k = R; k < rows; ++k) {
+      const uint32_t n = count4(ranks_at(k, page_at(k)), k);
+      gt += n & 0xffff;
+      eq += n >> 16;
     }
-  }
-  const int equal_stay = take - all_gt;
-  const uint32_t below = (1u << lane) - 1u;
-  auto place = [&](int k, uint32_t x) {
-    const int j = j0 + k * kSelThreads;
-    const bool g = larger(j, x), e = equal(j, x);
-    const uint32_t mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
-    if (lane == 0) {
-      before_gt[warp] = __popc(mg);
-      before_eq[warp] = __popc(me);
+    int all_gt, all_eq;
+    cta_scan(gt, warp_tot, all_gt);
+    cta_scan(eq, warp_tot, all_eq);
+    if (tid == 0) {
+      cta_tot = all_gt;
+      cta_eq = all_eq;
     }
-    __syncthreads();
-    const int wg = before_gt[lane], we = before_eq[lane];
-    const int pg = gt_before + warp_add(lane < warp ? wg : 0) + __popc(mg & below);
-    const int pe = eq_before + warp_add(lane < warp ? we : 0) + __popc(me & below);
-    if (g || (e && pe < equal_stay)) kept[pg + min(pe, equal_stay)] = j;
-    gt_before += warp_add(wg);
-    eq_before += warp_add(we);
-    __syncthreads();
+    cluster_sync();
+    for (uint32_t c = 0; c < cta; ++c) {
+      gt_before += load_peer(&cta_tot, c);
+      eq_before += load_peer(&cta_eq, c);
+    }
+    cluster_sync();  // no CTA leaves while its totals are read
+  }
+  auto place = [&](uint4 x, int k) {
+    const uint32_t n = count4(x, k);
+    int total;
+    const uint32_t before = (uint32_t)cta_scan((int)n, warp_tot, total);
+    int g = gt_before + (int)(before & 0xffff), e = eq_before + (int)(before >> 16);
+    const int j = j0 + k * kSelRow, left = k < rows ? old - j : 0;
+    auto put = [&](uint32_t y, int i) {
+      if (i >= left || y < last) return;
+      if (y > last) {
+        kept[g + min(e, need)] = j + i;
+        ++g;
+      } else {
+        if (e < need) kept[g + e] = j + i;
+        ++e;
+      }
+    };
+    put(x.x, 0);
+    put(x.y, 1);
+    put(x.z, 2);
+    put(x.w, 3);
+    gt_before += total & 0xffff;
+    eq_before += (uint32_t)total >> 16;
   };
 #pragma unroll
-  for (int k = 0; k < kSelRegs; ++k)
-    if (k < rows) place(k, r[k]);
-  for (int k = kSelRegs; k < rows; ++k) place(k, rank_of(j0 + k * kSelThreads));
+  for (int k = 0; k < R; ++k)
+    if (k < rows) place(r[k], k);
+  for (int k = R; k < rows; ++k) place(ranks_at(k, page_at(k)), k);
 }
 
 // One cluster per (sequence, K/V head, K or V). The kept rows move down in blocks of the cluster's
@@ -201,7 +272,8 @@ constexpr int kMoveThreads = 256, kMoveCtas = 8;
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {  // per: rows a CTA takes of a block
   grid_dependency_wait();
   extern __shared__ __align__(16) uint8_t rows_smem[];
-  __shared__ int from[256];
+  __shared__ const __nv_bfloat16* from[256];  // of a row of the block; null: it keeps its place
+  __shared__ __nv_bfloat16* to[256];
   const PagedShape& s = a.s;
   const int cta = (int)cluster_rank(), unit = blockIdx.x / kMoveCtas;
   const bool is_v = unit & 1;
@@ -210,46 +282,48 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedA
   const int32_t* kept = a.kept + (size_t)head * a.keep;
   const FaStrides& ts = is_v ? a.sv : a.sk;
   __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v : a.k);
-  const int chunks = s.d / 8, mask = (1 << s.page_shift) - 1;  // 16-byte chunks of a row
-  auto row_of = [&](int j) -> __nv_bfloat16* {
-    const int page = paged_page(s, b, j >> s.page_shift, a.status);
-    return page < 0 ? nullptr : base + paged_offset(ts, page, j & mask, hk);
-  };
-  auto weight_of = [&](int j) -> float* {
-    const int page = paged_page(s, b, j >> s.page_shift, a.status);
-    return page < 0 ? nullptr : a.weights + weight_offset(s, page, hk, j & mask);
-  };
+  const int shift = s.d == 128 ? 4 : 3, mask = (1 << s.page_shift) - 1;  // 16-byte chunks of a row
   for (int t0 = cta * per; t0 - cta * per < a.keep; t0 += kMoveCtas * per) {
-    const int n = min(per, a.keep - t0);  // this CTA's rows of the block (none or fewer at the end)
-    float w = 0.f;
+    const int n = max(0, min(per, a.keep - t0));  // this CTA's rows of the block (none or fewer at the end)
+    float w = 0.f, *wt = nullptr;
     __syncthreads();  // the last block's rows are written
     if ((int)threadIdx.x < n) {
-      const int j = kept[t0 + threadIdx.x];
-      from[threadIdx.x] = j == t0 + (int)threadIdx.x ? -1 : j;
-      if (!is_v && j != t0 + (int)threadIdx.x)
-        if (const float* p = weight_of(j)) w = *p;
+      const int t = t0 + threadIdx.x, j = kept[t];
+      const int pt = paged_page(s, b, t >> s.page_shift, a.status);
+      const int pj = paged_page(s, b, j >> s.page_shift, a.status);
+      const bool moves = j != t && pt >= 0 && pj >= 0;
+      from[threadIdx.x] = moves ? base + paged_offset(ts, pj, j & mask, hk) : nullptr;
+      to[threadIdx.x] = base + paged_offset(ts, max(pt, 0), t & mask, hk);
+      if (!is_v && moves) {
+        w = a.weights[weight_offset(s, pj, hk, j & mask)];
+        wt = a.weights + weight_offset(s, pt, hk, t & mask);
+      }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < n * chunks; c += kMoveThreads) {
-      const int j = from[c / chunks];
-      if (j < 0) continue;
-      if (const __nv_bfloat16* p = row_of(j))
+#pragma unroll 4
+    for (int c = threadIdx.x; c < n << shift; c += kMoveThreads) {
+      const __nv_bfloat16* p = from[c >> shift];
+      if (p != nullptr)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(rows_smem + c * 16)),
-                     "l"(p + c % chunks * 8)
+                     "l"(p + (c & ((1 << shift) - 1)) * 8)
                      : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     cluster_sync();
-    for (int c = threadIdx.x; c < n * chunks; c += kMoveThreads) {
-      const int t = t0 + c / chunks;
-      if (from[c / chunks] < 0) continue;
-      if (__nv_bfloat16* p = row_of(t))
-        *reinterpret_cast<uint4*>(p + c % chunks * 8) = *reinterpret_cast<const uint4*>(rows_smem + c * 16);
-    }
-    if (!is_v && (int)threadIdx.x < n && from[threadIdx.x] >= 0)
-      if (float* p = weight_of(t0 + threadIdx.x)) *p = w;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < n << shift; c += kMoveThreads)
+      if (from[c >> shift] != nullptr)
+        *reinterpret_cast<uint4*>(to[c >> shift] + (c & ((1 << shift) - 1)) * 8) =
+            *reinterpret_cast<const uint4*>(rows_smem + c * 16);
+    if (wt != nullptr) *wt = w;
   }
+}
+
+template <int R>
+cudaError_t launch_select(const FaPagedArgs& a, unsigned ctas, cudaStream_t st) {
+  return launch_dependent_cluster(paged_select_kernel<R>, dim3((unsigned)(a.s.B * a.s.Hkv) * ctas), dim3(kSelThreads), 0,
+                                  ctas, st, a);
 }
 
 }  // namespace
@@ -266,11 +340,12 @@ cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st) {
 
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st) {
   const long long heads = (long long)a.s.B * a.s.Hkv;
-  // The smallest cluster whose registers hold the candidates of the longest sequence.
-  unsigned ctas = 1;
-  while (ctas < 8 && (long long)ctas * fa::kSelSpan < a.s.max_k) ctas *= 2;
-  cudaError_t e = launch_dependent_cluster(fa::paged_select_kernel, dim3((unsigned)(heads * ctas)),
-                                           dim3(fa::kSelThreads), 0, ctas, st, a);
+  // Registers for the candidates of the longest sequence: up to 8 rows a thread, then CTAs, then 16 rows.
+  const long long rows = ((long long)a.s.max_k + fa::kSelRow - 1) / fa::kSelRow;
+  const unsigned ctas = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+  cudaError_t e = rows <= 2    ? fa::launch_select<2>(a, ctas, st)
+                  : rows <= 64 ? fa::launch_select<8>(a, ctas, st)
+                               : fa::launch_select<16>(a, ctas, st);
   if (e != cudaSuccess) return e;
   // A block of 8 CTAs' rows: all of `keep` where it fits (the latency is then paid once), at most 256 a CTA.
   const int share = (a.keep + fa::kMoveCtas - 1) / fa::kMoveCtas;

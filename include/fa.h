@@ -309,7 +309,8 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
  *   new tokens [batch][row][head][d] as in fa_fwd_varlen: fixed length (seqlen_q rows per sequence) or packed
  *              (cu_seqlens_q, rows_q; seqlen_q bounds the lengths). The new tokens of a sequence are its last
  *              keys: token i of L_q is key i + L_k - L_q.
- *   weights    key_weights fp32 [num_pages][Hkv][page_size], contiguous: one number per cached key and K/V head.
+ *   weights    key_weights fp32 [num_pages][Hkv][page_size], contiguous, 16-byte aligned: one number per cached key
+ *              and K/V head.
  *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result.
  *   sharing    pages may be shared by sequences for reading; a page that a call writes (fa_paged_append,
  *              fa_paged_key_weights, fa_paged_evict) belongs to one sequence of that call, else the writes race.

@@ -382,6 +382,20 @@ def test_evict(case, heads, weights):
     assert np.array_equal(p.np(p.cw), w, equal_nan=True)
 
 
+@pytest.mark.parametrize("L", [20_000, 60_000, 140_000])
+def test_evict_long(L):
+    """Lengths that take clusters of 4 and 8 CTAs, and one past what a cluster's registers hold; many equal weights."""
+    p = Problem([L, 70], [1, 1], 1, 1, 64, page=64, seed=95)
+    p.w = torch.round(p.w * 4) / 4
+    p.cw = p.w.cuda()
+    k, v, w = p.np(p.k), p.np(p.v), p.w.double().numpy().copy()
+    kept, n = paged.evict(k, v, w, p.table.numpy(), p.lk, L // 2, 100)
+    got, lens = fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, p.clen, L // 2, recent=100)
+    assert np.array_equal(got.cpu().numpy(), kept) and lens.tolist() == n.tolist()
+    assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cv), v, equal_nan=True)
+    assert np.array_equal(p.np(p.cw), w, equal_nan=True)
+
+
 # ----------------------------------------------------------------------------- together
 
 
