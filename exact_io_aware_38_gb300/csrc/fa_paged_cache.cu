@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPaged
 // shared memory: every row of a block is read before any is written, and since kept[t] >= t a block's
 // destinations hold no row that a later block still has to read. A row that keeps its place is not
 // moved. Bound by memory, with the latency of index, page and row once per block.
-constexpr int kMoveThreads = 256, kMoveCtas = 8;
+constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveRows = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {  // per: rows a CTA takes of a block
   grid_dependency_wait();
@@ -347,9 +347,10 @@ cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st) {
                   : rows <= 64 ? fa::launch_select<8>(a, ctas, st)
                                : fa::launch_select<16>(a, ctas, st);
   if (e != cudaSuccess) return e;
-  // A block of 8 CTAs' rows: all of `keep` where it fits (the latency is then paid once), at most 256 a CTA.
+  // Blocks of equal size, of at most kMoveRows rows a CTA.
   const int share = (a.keep + fa::kMoveCtas - 1) / fa::kMoveCtas;
-  const int per = share < 16 ? 16 : share > 256 ? 256 : share;
+  const int blocks = (share + fa::kMoveRows - 1) / fa::kMoveRows, even = (share + blocks - 1) / blocks;
+  const int per = even < 16 ? 16 : even;
   const size_t smem = (size_t)per * a.s.d * 2;
   e = cudaFuncSetAttribute(fa::paged_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 256 * 128 * 2);
   if (e != cudaSuccess) return e;
