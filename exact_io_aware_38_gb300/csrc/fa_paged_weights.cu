@@ -96,50 +96,56 @@ struct WUnits {
 struct WPieces {
   const PagedShape& s;
   const PagedRows& c;
-  int b, hk, kt, it, end, nk, open_cost;
+  int b, hk, kt, it, end;
   long long todo;  // positions from the piece on
   bool head;       // first piece of its (sequence, K/V head) in this CTA
+  bool finished;
   int n, tt0;
-  SeqInfo seq;
-  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh, int open_)
-      : s(s_), c(c_), b(sh.b), hk(sh.head), kt(sh.unit), it(0), end(0), nk(0), open_cost(open_), todo(sh.todo),
-        head(true), n(0), tt0(0) {
-    if (todo > 0) open(sh.tile);
+  WUnits x;
+  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh, int open)
+      : s(s_), c(c_), b(sh.b), hk(sh.head), kt(sh.unit), it(0), end(0), todo(sh.todo), head(true),
+        finished(sh.todo == 0), n(0), tt0(0), x(s_, c_, sh.todo > 0 ? sh.b : 0, open) {
+    if (todo > 0) unit(sh.tile);
   }
-  __device__ void open(int at) {  // at: position within the unit
-    const WUnits x(s, c, b, open_cost);
-    seq = x.q;
-    nk = x.count;
-    if (nk == 0) return;
+  __device__ void unit(int at) {  // opens unit kt at position `at` of it
     n = x.tiles(kt);
     tt0 = x.first(kt);
-    it = max(0, at - open_cost);
-    const long long stop = at + todo - open_cost;
+    it = max(0, at - x.open);
+    const long long stop = at + todo - x.open;
     end = stop < n ? (int)stop : n;
-    todo -= min((long long)(n + open_cost - at), todo);
-    if (end <= it) finished = true;  // the share ends before the unit's first tile
+    todo -= min((long long)(n + x.open - at), todo);
+    finished = end <= it;  // the share ends before the unit's first tile
   }
-  bool finished = false;
-  __device__ bool done() const { return finished || nk == 0; }
+  __device__ bool done() const { return finished; }
   __device__ bool whole() const { return it == 0 && end == n; }
   __device__ void next() {
     if (todo == 0) {
       finished = true;
       return;
     }
-    head = ++kt == nk;
+    head = ++kt == x.count;
     if (head) {
       kt = 0;
       if (++hk == s.Hkv) {
         hk = 0;
-        ++b;
+        do x = WUnits(s, c, ++b, x.open);
+        while (x.count == 0);  // todo > 0: a later sequence has units
       }
     }
-    open(0);
-    while (nk == 0) {  // todo > 0: a later sequence has units
-      ++b;
-      open(0);
-    }
+    unit(0);
+  }
+  __device__ void skip_to(const WPieces& o) {
+    b = o.b;
+    hk = o.hk;
+    kt = o.kt;
+    it = o.it;
+    end = o.end;
+    todo = o.todo;
+    head = o.head;
+    finished = o.finished;
+    n = o.n;
+    tt0 = o.tt0;
+    x = o.x;
   }
   // Query tile i of the unit: its first token, and its group of heads.
   __device__ int token(int i) const { return (tt0 + i / c.per_kv) * c.tpt; }
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     int kn = 0, qn = 0;  // key tiles and query tiles copied
     auto page_of = [&](const WPieces& x) -> int {
       const int key = (x.kt << 7) + (lane << shift);
-      return lane < per && key < x.seq.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
+      return lane < per && key < x.x.q.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
     };
     auto go = [&]() {
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       if (go() && lane == 0) {
         mbar_expect_tx(bar(ctl.q_full[st]), used * D * 2);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sQ + st * C::kQBytes + c * NP * 128, &tmQ, c * 64, group * rows.gs, w.seq.q0 + token, w.seq.bb,
+          tma_load_4d(sQ + st * C::kQBytes + c * NP * 128, &tmQ, c * 64, group * rows.gs, w.x.q.q0 + token, w.x.q.bb,
                       bar(ctl.q_full[st]));
         ctl.issued_q = qn + 1;
       }
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       const int st = kn % C::kKBufs, u = kn / C::kKBufs;
       if (run && u > 0) run = mbar_wait(bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
       if (go()) {
-        const int pages = min(per, (w.seq.Lk - (w.kt << 7) + prows - 1) >> shift);
+        const int pages = min(per, (w.x.q.Lk - (w.kt << 7) + prows - 1) >> shift);
         if (lane == 0) {
           mbar_expect_tx(bar(ctl.k_full[st]), pages * prows * D * 2);
           ctl.issued_k = kn + 1;
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     // waits for the load.
     auto load_lse = [&](int token, int head0) -> float {
       const int i = token + ti;
-      return r < used && i < w.seq.Lq ? a.lse[paged_row(s, w.seq, w.b, head0 + g, i)] : -INFINITY;
+      return r < used && i < w.x.q.Lq ? a.lse[paged_row(s, w.x.q, w.b, head0 + g, i)] : -INFINITY;
     };
     // Puts it where the group reads it; `hidden`: some column's scores must not enter the sum as they
     // are (a copied row of another sequence, or one without weight).
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       flip ^= 1;
       if (r < NP) {
         ctl.nlse[gr][flip][r] = dead ? -INFINITY : -lse * kLog2e;
-        ctl.seen[gr][flip][r] = dead ? -1 : (s.causal ? token + ti + w.seq.off : 0x7fffffff);
+        ctl.seen[gr][flip][r] = dead ? -1 : (s.causal ? token + ti + w.x.q.off : 0x7fffffff);
       }
       __syncwarp();
       uint32_t any;
@@ -372,8 +378,8 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       hidden = any != 0;
     };
     auto tile = [&](int token) -> float {
-      const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > token + w.seq.off);
-      const int cols = min(used, (w.seq.Lq - token) * rows.gs), key = (w.kt << 7) + r;
+      const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > token + w.x.q.off);
+      const int cols = min(used, (w.x.q.Lq - token) * rows.gs), key = (w.kt << 7) + r;
       if (run) run = mbar_wait(bar(ctl.s_full[t & 3]), (t >> 2) & 1, abort_flag, a.status);
       __syncwarp();
       fence_after_sync();
@@ -387,25 +393,42 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       return sum;
     };
     if constexpr (C::kFew) {
-      // One tile per key tile: its group also adds to the weights (read before the scores are there).
-      for (; !w.done(); w.next(), ++t) {
-        fresh |= w.head;
-        if (t % kGroups != gr) continue;
-        const int key = (w.kt << 7) + r;
-        float* at = nullptr;
-        float old = 0.f;
-        if (key < w.seq.Lk) {
-          const int page = paged_page(s, w.b, key >> s.page_shift, a.status);
-          if (page >= 0) {
-            at = a.weights + weight_offset(s, page, w.hk, key & ((1 << s.page_shift) - 1));
-            old = *at;
-          }
+      // One tile per key tile: its group also adds to the weights, which it reads a turn ahead (the page a
+      // tile earlier than the weight it leads to).
+      auto page_of = [&](const WPieces& y) -> int {
+        const int key = (y.kt << 7) + r;
+        return key < y.x.q.Lk ? __ldg(s.table + (size_t)y.b * s.max_pages + (key >> s.page_shift)) : 0;
+      };
+      auto weight_at = [&](const WPieces& y, int page) -> float* {
+        const int key = (y.kt << 7) + r;
+        if (key >= y.x.q.Lk) return nullptr;
+        if ((unsigned)page >= (unsigned)s.num_pages) {
+          report_status(a.status, FA_ERR_BOUNDS);
+          return nullptr;
         }
-        __syncwarp();
+        return a.weights + weight_offset(s, page, y.hk, key & ((1 << s.page_shift) - 1));
+      };
+      for (; t < gr && !w.done(); ++t) w.next();
+      float* at = w.done() ? nullptr : weight_at(w, page_of(w));
+      float old = at != nullptr ? *at : 0.f;
+      while (!w.done()) {
+        WPieces ahead = w;
+        bool turns = false;  // the head changes before this group's next tile
+        for (int i = 0; i < kGroups && !ahead.done(); ++i) {
+          ahead.next();
+          turns |= ahead.head;
+        }
+        const int page = ahead.done() ? 0 : page_of(ahead);
         if (fresh) stage_lse(0, load_lse(0, w.hk * rows.gs));
-        fresh = false;
+        fresh = turns;
         const float sum = tile(0);
+        float* then = ahead.done() ? nullptr : weight_at(ahead, page);
+        const float before = then != nullptr ? *then : 0.f;
         if (at != nullptr) *at = old + sum;
+        at = then;
+        old = before;
+        w.skip_to(ahead);
+        t += kGroups;
         __syncwarp();
       }
     } else {
@@ -436,7 +459,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       const int key = (w.kt << 7) + r, pp = piece & 1;
       float* at = nullptr;
       float old = 0.f;
-      if (w.whole() && key < w.seq.Lk) {
+      if (w.whole() && key < w.x.q.Lk) {
         const int page = paged_page(s, w.b, key >> s.page_shift, a.status);
         if (page >= 0) {
           at = a.weights + weight_offset(s, page, w.hk, key & ((1 << s.page_shift) - 1));
