@@ -12,9 +12,11 @@
 // order; with one query tile per unit nothing is cut.
 //
 // Roles: warp 0 reads the page table and copies, warp 1 issues the MMAs, three groups of four warps
-// take the query tiles in turn, and with many rows a last group adds the groups' sums of a finished
-// unit to the weights, so that no exponential waits for that read and write.
-// Tensor memory: four score buffers of NP columns.
+// take the query tiles in turn. With many rows a last group serves the units: it moves the next unit's key
+// tile into tensor memory, since a product of two operands in shared memory reads 256 bytes a cycle where
+// 128 come (a 128 x 128 tile took 580 cycles of the issuing thread), and adds the groups' sums of a
+// finished unit to the weights, so that no exponential waits for that read and write.
+// Tensor memory: four score buffers of NP columns; with many rows three, then two key tiles (bf16).
 #include "fa_paged.cuh"
 #include "fa_tmap.h"
 #include "sm103_ptx.cuh"
@@ -34,8 +36,9 @@ struct WCfg {
   static constexpr bool kFew = NP <= 64;
   static constexpr int kKBytes = 128 * D * 2, kQBytes = NP * D * 2;
   static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128);
-  static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 2) * (128 / D);
-  static constexpr int kQBufs = kFew ? 2 : 4 * (128 / D);
+  static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 1) * (128 / D);
+  static constexpr int kQBufs = kFew ? 2 : 5 * (128 / D);
+  static constexpr int kSBufs = kFew ? 4 : 3;
   static constexpr int kOpen = kFew ? 0 : 1;
   static constexpr int kSmem = kKBufs * kKBytes + kQBufs * kQBytes + 1024;
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : NP == 64 ? 256 : 512;
@@ -44,7 +47,8 @@ struct WCfg {
 
 template <int NP>
 struct WCtl {
-  uint64_t k_full[12], k_empty[12], q_full[8], q_empty[8], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
+  uint64_t k_full[12], k_empty[12], q_full[10], q_empty[10], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
+  uint64_t kt_full[2], kt_empty[2];  // many rows: the key tiles in tensor memory
   uint32_t tmem_base;
   int abort_flag;
   long long scan[18];
@@ -93,6 +97,7 @@ struct WUnits {
 };
 
 // The pieces of a CTA's share: query tiles [it, end) of the n that see key tile kt.
+template <bool FEW>
 struct WPieces {
   const PagedShape& s;
   const PagedRows& c;
@@ -108,6 +113,11 @@ struct WPieces {
     if (todo > 0) unit(sh.tile);
   }
   __device__ void unit(int at) {  // opens unit kt at position `at` of it
+    if (FEW) {  // one tile and no opening
+      n = end = 1;
+      --todo;
+      return;
+    }
     n = x.tiles(kt);
     tt0 = x.first(kt);
     it = max(0, at - x.open);
@@ -147,9 +157,16 @@ struct WPieces {
     tt0 = o.tt0;
     x = o.x;
   }
-  // Query tile i of the unit: its first token, and its group of heads.
-  __device__ int token(int i) const { return (tt0 + i / c.per_kv) * c.tpt; }
-  __device__ int group(int i) const { return hk * c.per_kv + i % c.per_kv; }
+  // A query tile of the unit: its first token, and the first head of its group.
+  struct Cursor {
+    int tt, g;  // token tile, group
+    __device__ Cursor(const WPieces& w, int i) : tt(w.tt0 + i / w.c.per_kv), g(i % w.c.per_kv) {}
+    __device__ void advance(const WPieces& w, int by) {
+      for (g += by; g >= w.c.per_kv; g -= w.c.per_kv) ++tt;
+    }
+    __device__ int token(const WPieces& w) const { return tt * w.c.tpt; }
+    __device__ int head0(const WPieces& w) const { return (w.hk * w.c.per_kv + g) * w.c.gs; }
+  };
 };
 
 // One query tile's part of a key's sum: 2^(c log2(e) s - LSE) over the columns (rows) of this thread's
@@ -209,7 +226,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     ctl.issued_k = ctl.issued_q = 0;
     for (int i = 0; i < C::kKBufs; ++i) {
       mbar_init(bar(ctl.k_full[i]), 1);
-      mbar_init(bar(ctl.k_empty[i]), 1);
+      mbar_init(bar(ctl.k_empty[i]), C::kFew ? 1 : 128);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(bar(ctl.q_full[i]), 1);
@@ -222,6 +239,8 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(ctl.sum_ready[i]), 128 * kGroups);
       mbar_init(bar(ctl.sum_free[i]), 128);
+      mbar_init(bar(ctl.kt_full[i]), 128);
+      mbar_init(bar(ctl.kt_empty[i]), 1);
     }
     mbar_init(bar(ctl.drain), 1);
     fence_mbar_init();
@@ -246,7 +265,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
   asm volatile("griddepcontrol.launch_dependents;");
-  WPieces w(s, rows, ctl.share, C::kOpen);
+  WPieces<C::kFew> w(s, rows, ctl.share, C::kOpen);
   if (!C::kFew && threadIdx.x == 0) {
     WJoin d{};
     d.b = !w.done() && w.it > 0 && w.end == w.n ? w.b : -1;
@@ -262,7 +281,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     bool run = true;
     int kn = 0, qn = 0;  // key tiles and query tiles copied
-    auto page_of = [&](const WPieces& x) -> int {
+    auto page_of = [&](const WPieces<C::kFew>& x) -> int {
       const int key = (x.kt << 7) + (lane << shift);
       return lane < per && key < x.x.q.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
     };
@@ -270,13 +289,13 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
       return run;
     };
-    auto copy_q = [&](int token, int group) {
+    auto copy_q = [&](int token, int head0) {
       const int st = qn % C::kQBufs, u = qn / C::kQBufs;
       if (run && u > 0) run = mbar_wait(bar(ctl.q_empty[st]), (u - 1) & 1, abort_flag, a.status);
       if (go() && lane == 0) {
         mbar_expect_tx(bar(ctl.q_full[st]), used * D * 2);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sQ + st * C::kQBytes + c * NP * 128, &tmQ, c * 64, group * rows.gs, w.x.q.q0 + token, w.x.q.bb,
+          tma_load_4d(sQ + st * C::kQBytes + c * NP * 128, &tmQ, c * 64, head0, w.x.q.q0 + token, w.x.q.bb,
                       bar(ctl.q_full[st]));
         ctl.issued_q = qn + 1;
       }
@@ -284,7 +303,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     };
     int page = w.done() ? 0 : page_of(w);
     while (!w.done()) {
-      if (C::kFew && w.head) copy_q(0, w.hk);
+      if (C::kFew && w.head) copy_q(0, w.hk * rows.gs);
       const int st = kn % C::kKBufs, u = kn / C::kKBufs;
       if (run && u > 0) run = mbar_wait(bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
       if (go()) {
@@ -300,46 +319,64 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
                         page, bar(ctl.k_full[st]));
       }
       ++kn;
-      if (!C::kFew)
-        for (int i = w.it; i < w.end; ++i) copy_q(w.token(i), w.group(i));
+      if (!C::kFew) {
+        typename WPieces<C::kFew>::Cursor at(w, w.it);
+        for (int i = w.it; i < w.end; ++i, at.advance(w, 1)) copy_q(at.token(w), at.head0(w));
+      }
       w.next();
       page = w.done() ? 0 : page_of(w);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0) {
+      // Every instruction between products is time the tensor pipe may idle: positions in the rings are
+      // counters, and with many rows the group that sees the scores releases the query tile.
       bool run = true;
-      int t = 0, kn = 0, qn = 0;
-      while (!w.done() && run) {
-        const int ks = kn % C::kKBufs;
+      int t = 0, ks = 0, qs = 0, sb = 0, qn = 0;
+      uint32_t kphase = 0, qphase = 0, sphase = 1;  // parity awaited on the ring's current buffer
+      for (int kn = 0; !w.done() && run; ++kn) {
         if (C::kFew && w.head) {
-          run = mbar_wait_spin(bar(ctl.q_full[qn % C::kQBufs]), (qn / C::kQBufs) & 1, abort_flag, a.status);
+          qs = qn % C::kQBufs;
+          run = mbar_wait_spin(bar(ctl.q_full[qs]), (qn / C::kQBufs) & 1, abort_flag, a.status);
           ++qn;
         }
-        if (run) run = mbar_wait_spin(bar(ctl.k_full[ks]), (kn / C::kKBufs) & 1, abort_flag, a.status);
+        if (run)
+          run = C::kFew ? mbar_wait_spin(bar(ctl.k_full[ks]), kphase, abort_flag, a.status)
+                        : mbar_wait_spin(bar(ctl.kt_full[kn & 1]), (kn >> 1) & 1, abort_flag, a.status);
         const uint64_t dk = desc_kmajor_sw128(sK + ks * C::kKBytes);
+        const uint32_t tK = tmem + C::kSBufs * NP + (kn & 1) * (D / 2);
         for (int i = w.it; i < w.end && run; ++i, ++t) {
-          const int qs = (C::kFew ? qn - 1 : qn) % C::kQBufs;
-          if (!C::kFew) run = mbar_wait_spin(bar(ctl.q_full[qs]), (qn / C::kQBufs) & 1, abort_flag, a.status);
-          if (run && t >= 4) run = mbar_wait_spin(bar(ctl.s_free[t & 3]), ((t >> 2) - 1) & 1, abort_flag, a.status);
+          if (!C::kFew) run = mbar_wait_spin(bar(ctl.q_full[qs]), qphase, abort_flag, a.status);
+          if (run && t >= C::kSBufs) run = mbar_wait_spin(bar(ctl.s_free[sb]), sphase, abort_flag, a.status);
           fence_after_sync();
           if (!run) break;
           const uint64_t dq = desc_kmajor_sw128(sQ + qs * C::kQBytes);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + (t & 3) * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32),
-                   desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32), C::kId, kk > 0);
-          mma_commit(bar(ctl.s_full[t & 3]));
-          if (!C::kFew) {
-            mma_commit(bar(ctl.q_empty[qs]));
-            ++qn;
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t dqk = desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32);
+            if constexpr (C::kFew)
+              mma_ss(tmem + sb * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32), dqk, C::kId, kk > 0);
+            else
+              mma_ts(tmem + sb * NP, tK + kk * 8, dqk, C::kId, kk > 0);
+          }
+          mma_commit(bar(ctl.s_full[sb]));
+          if (++sb == C::kSBufs) {
+            sb = 0;
+            sphase ^= 1;
+          }
+          if (!C::kFew && ++qs == C::kQBufs) {
+            qs = 0;
+            qphase ^= 1;
           }
         }
         if (!run) break;
-        mma_commit(bar(ctl.k_empty[ks]));
-        ++kn;
+        mma_commit(C::kFew ? bar(ctl.k_empty[ks]) : bar(ctl.kt_empty[kn & 1]));
+        if (++ks == C::kKBufs) {
+          ks = 0;
+          kphase ^= 1;
+        }
         w.next();
-        if (C::kFew && !w.done() && w.head) mma_commit(bar(ctl.q_empty[(qn - 1) % C::kQBufs]));
+        if (C::kFew && !w.done() && w.head) mma_commit(bar(ctl.q_empty[qs]));
       }
       mma_commit(bar(ctl.drain));
       mbar_wait_drain(bar(ctl.drain), 0);
@@ -380,26 +417,28 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     auto tile = [&](int token) -> float {
       const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > token + w.x.q.off);
       const int cols = min(used, (w.x.q.Lq - token) * rows.gs), key = (w.kt << 7) + r;
-      if (run) run = mbar_wait(bar(ctl.s_full[t & 3]), (t >> 2) & 1, abort_flag, a.status);
+      const int sb = t % C::kSBufs;
+      if (run) run = mbar_wait(bar(ctl.s_full[sb]), (t / C::kSBufs) & 1, abort_flag, a.status);
+      if (!C::kFew && run && r == 0) mbar_arrive(bar(ctl.q_empty[t % C::kQBufs]));  // the product has read it
       __syncwarp();
       fence_after_sync();
       const float* nls = ctl.nlse[gr][flip];
       const int* sees = ctl.seen[gr][flip];
-      const uint32_t tS = tmem + lane_off + (t & 3) * NP;
+      const uint32_t tS = tmem + lane_off + sb * NP;
       const float sum = masked ? tile_sum<NP, true>(tS, nls, sees, key, cols, sl2)
                                : tile_sum<NP, false>(tS, nls, sees, key, cols, sl2);
       fence_before_sync();
-      if (run) mbar_arrive(bar(ctl.s_free[t & 3]));
+      if (run) mbar_arrive(bar(ctl.s_free[sb]));
       return sum;
     };
     if constexpr (C::kFew) {
       // One tile per key tile: its group also adds to the weights, which it reads a turn ahead (the page a
       // tile earlier than the weight it leads to).
-      auto page_of = [&](const WPieces& y) -> int {
+      auto page_of = [&](const WPieces<C::kFew>& y) -> int {
         const int key = (y.kt << 7) + r;
         return key < y.x.q.Lk ? __ldg(s.table + (size_t)y.b * s.max_pages + (key >> s.page_shift)) : 0;
       };
-      auto weight_at = [&](const WPieces& y, int page) -> float* {
+      auto weight_at = [&](const WPieces<C::kFew>& y, int page) -> float* {
         const int key = (y.kt << 7) + r;
         if (key >= y.x.q.Lk) return nullptr;
         if ((unsigned)page >= (unsigned)s.num_pages) {
@@ -412,7 +451,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       float* at = w.done() ? nullptr : weight_at(w, page_of(w));
       float old = at != nullptr ? *at : 0.f;
       while (!w.done()) {
-        WPieces ahead = w;
+        WPieces<C::kFew> ahead = w;
         bool turns = false;  // the head changes before this group's next tile
         for (int i = 0; i < kGroups && !ahead.done(); ++i) {
           ahead.next();
@@ -436,12 +475,15 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
         int i = w.it + (gr + kGroups - t % kGroups) % kGroups;  // this group's first tile of the piece
         const int t0 = t;
         float sum = 0.f;
-        float lse = i < w.end ? load_lse(w.token(i), w.group(i) * rows.gs) : 0.f;
+        typename WPieces<C::kFew>::Cursor at(w, i);
+        float lse = i < w.end ? load_lse(at.token(w), at.head0(w)) : 0.f;
         for (; i < w.end; i += kGroups) {
           t = t0 + (i - w.it);
-          stage_lse(w.token(i), lse);
-          if (i + kGroups < w.end) lse = load_lse(w.token(i + kGroups), w.group(i + kGroups) * rows.gs);
-          sum += tile(w.token(i));
+          const int token = at.token(w);
+          stage_lse(token, lse);
+          at.advance(w, kGroups);
+          if (i + kGroups < w.end) lse = load_lse(at.token(w), at.head0(w));
+          sum += tile(token);
         }
         t = t0 + (w.end - w.it);
         const int pp = piece & 1;
@@ -452,10 +494,39 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       }
     }
   } else if constexpr (!C::kFew) {
-    // ------------------------------------------------------------------ sums to weights
-    const int r = threadIdx.x - (64 + 128 * kGroups);
+    // ------------------------------------------------------------------ the units' key tiles and sums
+    const int r = (warp & 3) * 32 + lane;  // key within the tile (the tensor-memory lane of this thread)
     bool run = true;
-    for (int piece = 0; !w.done(); ++piece, w.next()) {
+    int kn = 0;
+    // Key tile kn from shared memory into tensor memory, a row per lane.
+    auto move_k = [&]() {
+      const int ks = kn % C::kKBufs;
+      if (run && kn >= 2) run = mbar_wait(bar(ctl.kt_empty[kn & 1]), ((kn >> 1) - 1) & 1, abort_flag, a.status);
+      if (run) run = mbar_wait(bar(ctl.k_full[ks]), (kn / C::kKBufs) & 1, abort_flag, a.status);
+      __syncwarp();
+      fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(x[4 * i]), "=r"(x[4 * i + 1]), "=r"(x[4 * i + 2]), "=r"(x[4 * i + 3])
+                       : "r"(sK + ks * C::kKBytes + c * 16384 + r * 128 + ((i ^ (r & 7)) << 4))
+                       : "memory");
+        tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kSBufs * NP + (kn & 1) * (D / 2) + c * 32, x);
+      }
+      tmem_st_wait();
+      fence_before_sync();
+      if (run) {
+        mbar_arrive(bar(ctl.k_empty[ks]));
+        mbar_arrive(bar(ctl.kt_full[kn & 1]));
+      }
+      __syncwarp();
+      ++kn;
+    };
+    if (!w.done()) move_k();
+    for (int piece = 0; !w.done(); ++piece) {
       const int key = (w.kt << 7) + r, pp = piece & 1;
       float* at = nullptr;
       float old = 0.f;
@@ -468,6 +539,9 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       } else if (!w.whole()) {
         at = wk.part + (size_t)(2 * blockIdx.x + (piece == 0 ? 0 : 1)) * 128 + r;
       }
+      __syncwarp();
+      w.next();
+      if (!w.done()) move_k();
       if (run) run = mbar_wait(bar(ctl.sum_ready[pp]), (piece >> 1) & 1, abort_flag, a.status);
       float sum = 0.f;
 #pragma unroll

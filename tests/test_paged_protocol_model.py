@@ -11,8 +11,8 @@ decode   fa_paged_decode.cu: K and V rings of their own lengths, two Q buffers, 
          double buffered; the softmax waits for V itself in a unit's last tile, whose rows past the last key it zeroes.
 chunk    fa_paged_chunk.cu: two query tiles, one Q buffer; stage t of the ring holds V of tile t and K of tile t + 1; the
          last tile's V comes on a barrier of its own and the copying warp completes the stage after zeroing rows.
-weights  fa_paged_weights.cu: K and Q rings, four S buffers, three groups in turn; with many rows a last group adds the
-         groups' sums, double buffered, to the weights.
+weights  fa_paged_weights.cu: K and Q rings, score buffers, three groups in turn; with many rows a last group moves key
+         tiles into tensor memory, double buffered, and adds the groups' sums, double buffered, to the weights.
 """
 
 import random
@@ -375,10 +375,10 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
     T = tiles_of(pieces)
-    G, kb, qb = 3, (5 if few else 2), (2 if few else 4)
+    G, kb, qb, sb = 3, (5 if few else 1), (2 if few else 5), (4 if few else 3)
     head = lambda p: p % 3 == 0  # few rows: Q is copied where a head begins
     q_of = (lambda t: T[t][0] // 3) if few else (lambda t: t)
-    for n, c in (("kf", kb), ("ke", kb), ("qf", qb), ("qe", qb), ("sf", 4), ("fr", 4)):
+    for n, c in (("kf", kb), ("ke", kb), ("qf", qb), ("qe", qb), ("sf", sb), ("fr", sb), ("tf", 2), ("te", 2)):
         for i in range(c):
             M.bar(f"{n}{i}", 1)
     for i in range(2):
@@ -404,7 +404,8 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
                 run = yield from M.wait(f"ke{p % kb}", (p // kb - 1) & 1)
             run = run and not M.aborted
             if run:
-                need(all(("S", t) in done for t in range(len(T)) if T[t][0] == p - kb), f"K {p - kb} overwritten")
+                need(p < kb or ("moved", p - kb) in done or
+                     (few and all(("S", t) in done for t in range(len(T)) if T[t][0] == p - kb)), f"K {p - kb} overwritten")
                 M.load(f"kf{p % kb}", 1, ("K", p))
                 count["k"] = p + 1
             if not few:
@@ -419,21 +420,19 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
             if run and few and head(p):
                 run = yield from M.wait(f"qf{p // 3 % qb}", (p // 3 // qb) & 1)
             if run and k == 0:
-                run = yield from M.wait(f"kf{p % kb}", (p // kb) & 1)
+                run = yield from (M.wait(f"kf{p % kb}", (p // kb) & 1) if few else M.wait(f"tf{p & 1}", (p >> 1) & 1))
             if run and not few:
                 run = yield from M.wait(f"qf{t % qb}", (t // qb) & 1)
-            if run and t >= 4:
-                run = yield from M.wait(f"fr{t & 3}", ((t >> 2) - 1) & 1)
+            if run and t >= sb:
+                run = yield from M.wait(f"fr{t % sb}", (t // sb - 1) & 1)
             if not run:
                 break
-            need(("K", p) in done and ("Q", q_of(t)) in done, f"S({t}) before its operands")
-            need(t < 4 or ("read", t - 4) in done, f"S({t}) over S({t - 4})")
+            need(("K" if few else "moved", p) in done and ("Q", q_of(t)) in done, f"S({t}) before its operands")
+            need(t < sb or ("read", t - sb) in done, f"S({t}) over S({t - sb})")
             M.mma("i", ("S", t))
-            M.commit("i", f"sf{t & 3}")
-            if not few:
-                M.commit("i", f"qe{t % qb}")
+            M.commit("i", f"sf{t % sb}")
             if last:
-                M.commit("i", f"ke{p % kb}")
+                M.commit("i", f"ke{p % kb}" if few else f"te{p & 1}")
                 if few and t + 1 < len(T) and head(T[t + 1][0]):
                     M.commit("i", f"qe{p // 3 % qb}")
             yield None
@@ -445,12 +444,14 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
                 if T[t][0] != p or t % G != g:
                     continue
                 if run:
-                    run = yield from M.wait(f"sf{t & 3}", (t >> 2) & 1)
+                    run = yield from M.wait(f"sf{t % sb}", (t // sb) & 1)
                 need(not run or ("S", t) in done, f"S({t}) read too early")
+                if run and not few:
+                    M.B[f"qe{t % qb}"].arrive()
                 yield None
                 if run:
                     done.add(("read", t))
-                    M.B[f"fr{t & 3}"].arrive()
+                    M.B[f"fr{t % sb}"].arrive()
             if not few:
                 if run and p >= 2 and not no_sum_free:
                     run = yield from M.wait(f"sx{p & 1}", ((p >> 1) - 1) & 1)
@@ -459,9 +460,26 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
                     M.B[f"sr{p & 1}"].arrive()
                 yield None
 
-    def adder():
+    def unit_group():
         run = True
+
+        def move(p, run):
+            if run and p >= 2:
+                run = yield from M.wait(f"te{p & 1}", ((p >> 1) - 1) & 1)
+            if run:
+                run = yield from M.wait(f"kf{p % kb}", (p // kb) & 1)
+            if run:
+                need(("K", p) in done, f"K {p} moved before it landed")
+                need(p < 2 or all(("S", t) in done for t in range(len(T)) if T[t][0] == p - 2), f"K {p - 2} replaced")
+                done.add(("moved", p))
+                M.B[f"ke{p % kb}"].arrive()
+                M.B[f"tf{p & 1}"].arrive()
+            return run
+        if pieces:
+            run = yield from move(0, run)
         for p in range(len(pieces)):
+            if p + 1 < len(pieces):
+                run = yield from move(p + 1, run)
             if run:
                 run = yield from M.wait(f"sr{p & 1}", (p >> 1) & 1)
             if run:
@@ -471,7 +489,7 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False):
 
     roles = {"prod": producer(), "mma": issuer(), **{f"g{g}": group(g) for g in range(G)}}
     if not few:
-        roles["add"] = adder()
+        roles["unit"] = unit_group()
 
     def issued():
         return last_phases("qf", count["q"], qb) + last_phases("kf", count["k"], kb)
