@@ -116,8 +116,8 @@ struct Share {
 };
 
 // Finds the share of CTA blockIdx.x; all threads of the CTA take part, and `sh` and `scan` (one entry per
-// warp) are in shared memory. Units(b): heads, count, before(u) (positions before unit u, one head's),
-// and open, the positions of a unit before its first tile.
+// warp, at least two) are in shared memory. Units(b): heads, count, before(u) (positions before unit u, one
+// head's), tiles(u), and open, the positions of a unit before its first tile.
 template <int kThreads, typename Make>
 __device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -142,28 +142,32 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
     if (i < warp) base += scan[i];
     total += scan[i];
   }
+  __syncthreads();  // scan is read
   const long long n = min(total, (long long)gridDim.x), c = blockIdx.x;  // no CTA before the last busy one is idle
   const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
-  if (lo < hi && lo >= base && lo < base + mine) {  // the sequence, and the line's position where it begins
+  if (lo < hi && lo >= base && lo < base + mine) {  // the sequence, the line's position where it begins, its size
     int b = first;
-    for (;; ++b) {
-      const long long t = per == 1 ? mine : size_of(b);
-      if (lo < base + t) break;
-      base += t;
-    }
+    long long size = mine;
+    if (per > 1)
+      for (;; ++b) {
+        size = size_of(b);
+        if (lo < base + size) break;
+        base += size;
+      }
     sh.b = b;
-    sh.todo = base;
+    scan[0] = base;
+    scan[1] = size;
   }
   __syncthreads();
   if (lo >= hi) return;
   const auto x = make(sh.b);
-  const long long each = x.before(x.count), from = sh.todo;
-  const int head = (int)((lo - from) / each);
+  const long long from = scan[0], each = scan[1] / x.heads;
+  const long long in = lo - from;
+  const int head = in >> 31 == 0 && each >> 31 == 0 ? (int)((uint32_t)in / (uint32_t)each) : (int)(in / each);
   const long long at = from + head * each;
-  __syncthreads();
   for (int u = threadIdx.x; u < x.count; u += kThreads) {
     const long long start = at + x.before(u);
-    if (start > lo || lo >= at + x.before(u + 1)) continue;
+    if (start > lo || lo >= start + x.tiles(u) + x.open) continue;
     sh.head = head;
     sh.unit = u;
     sh.tile = (int)(lo - start);

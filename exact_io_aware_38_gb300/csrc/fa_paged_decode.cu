@@ -87,7 +87,7 @@ struct DecUnits {
   __device__ DecUnits(const PagedShape& s, int b) : heads(s.Hkv), count(0), open(kDecOpen), q(paged_seq(s, b)) {
     count = q.Lq > 0;
   }
-  __device__ int tiles() const { return max(1, (q.Lk + 127) >> 7); }
+  __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
   __device__ long long before(int u) const { return u * (tiles() + open); }
 };
 

@@ -11,12 +11,12 @@
 // leaves 128 partial sums per piece (two slots per CTA), which the join kernel adds in the pieces'
 // order; with one query tile per unit nothing is cut.
 //
-// Roles: warp 0 reads the page table and copies, warp 1 issues the MMAs, three groups of four warps
-// take the query tiles in turn. With many rows a last group serves the units: it moves the next unit's key
-// tile into tensor memory, since a product of two operands in shared memory reads 256 bytes a cycle where
-// 128 come (a 128 x 128 tile took 580 cycles of the issuing thread), and adds the groups' sums of a
-// finished unit to the weights, so that no exponential waits for that read and write.
-// Tensor memory: four score buffers of NP columns; with many rows three, then two key tiles (bf16).
+// Roles: warp 0 reads the page table and copies; one warp issues the MMAs, or with many rows two, a
+// query tile each in turn: an MMA takes its thread about 70 cycles whatever its width, so a tile's eight and
+// the waits around them fill 1200 cycles of one thread, twice what the tensor pipe needs. Groups of four
+// warps (three, with many rows four) take the query tiles in turn; with many rows a last group adds their
+// sums of a finished unit to the weights, so that no exponential waits for that read and write.
+// Tensor memory: four score buffers of NP columns.
 #include "fa_paged.cuh"
 #include "fa_tmap.h"
 #include "sm103_ptx.cuh"
@@ -26,7 +26,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kGroups = 3;
 
 // NP: rows of a query tile (columns of S^T); FEW: one query tile holds all rows of a K/V head (NP <=
 // 64), stays in shared memory for all key tiles of the head and the ring holds K; else the ring
@@ -35,11 +34,14 @@ template <int D, int NP>
 struct WCfg {
   static constexpr bool kFew = NP <= 64;
   static constexpr int kKBytes = 128 * D * 2, kQBytes = NP * D * 2;
-  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128);
-  static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 1) * (128 / D);
-  static constexpr int kQBufs = kFew ? 2 : 5 * (128 / D);
-  static constexpr int kSBufs = kFew ? 4 : 3;
-  static constexpr int kOpen = kFew ? 0 : 1;
+  // With two issuers a tile may be done before the one in front of it, so each score buffer needs a group of
+  // its own, which sees the buffer's every phase.
+  static constexpr int kGroups = kFew ? 3 : 4;
+  static constexpr int kIssuers = kFew ? 1 : 2;
+  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128 + 32);
+  static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 2) * (128 / D);
+  static constexpr int kQBufs = kFew ? 2 : 4 * (128 / D);  // (even: a buffer has one issuer, which sees its every phase)
+  static constexpr int kOpen = kFew ? 0 : 3;
   static constexpr int kSmem = kKBufs * kKBytes + kQBufs * kQBytes + 1024;
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : NP == 64 ? 256 : 512;
   static constexpr uint32_t kId = idesc_bf16(128, NP, false, false);
@@ -47,16 +49,15 @@ struct WCfg {
 
 template <int NP>
 struct WCtl {
-  uint64_t k_full[12], k_empty[12], q_full[10], q_empty[10], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
-  uint64_t kt_full[2], kt_empty[2];  // many rows: the key tiles in tensor memory
+  uint64_t k_full[12], k_empty[12], q_full[8], q_empty[8], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[18];
+  long long scan[23];
   Share share;
   int issued_k, issued_q;               // copies issued (abort-path drain)
-  alignas(16) float nlse[kGroups][2][NP];  // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
-  alignas(16) int seen[kGroups][2][NP];    // last key the row sees
-  float sums[2][kGroups][NP == 128 ? 128 : 1];  // many rows: the groups' sums of a piece, per parity
+  alignas(16) float nlse[4][2][NP];  // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
+  alignas(16) int seen[4][2][NP];    // last key the row sees
+  float sums[2][4][NP == 128 ? 128 : 1];  // many rows: the groups' sums of a piece, per parity
 };
 
 struct WJoin {
@@ -174,24 +175,23 @@ struct WPieces {
 template <int NP, bool MASK>
 __device__ __forceinline__ float tile_sum(uint32_t tS, const float* nls, const int* sees, int key, int cols,
                                           float sl2) {
-  constexpr int W = NP < 32 ? NP : 32;  // columns per wait
+  constexpr int W = 16;  // columns per load; the next ones are on their way while these are worked on
   float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t x[2][W];
+  tmem_ld16(tS, x[0]);
 #pragma unroll
   for (int c = 0; c < NP; c += W) {
     if (c >= cols) break;
-    uint32_t x[W];
-    if constexpr (W == 16)
-      tmem_ld16(tS + c, x);
-    else
-      tmem_ld32(tS + c, x);
+    const uint32_t(&y)[W] = x[(c / W) & 1];
     tmem_ld_wait();
+    if (c + W < NP) tmem_ld16(tS + c + W, x[(c / W + 1) & 1]);
 #pragma unroll
     for (int k = 0; k < W; k += 4) {
       const float4 n4 = *reinterpret_cast<const float4*>(nls + c + k);
       const float2 sc = make_float2(sl2, sl2);
-      const float2 y0 = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc, make_float2(n4.x, n4.y));
+      const float2 y0 = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), sc, make_float2(n4.x, n4.y));
       const float2 y1 =
-          fma2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), sc, make_float2(n4.z, n4.w));
+          fma2(make_float2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), sc, make_float2(n4.z, n4.w));
       float p0 = ex2_approx(y0.x), p1 = ex2_approx(y0.y), p2 = ex2_approx(y1.x), p3 = ex2_approx(y1.y);
       if constexpr (MASK) {
         const int4 see = *reinterpret_cast<const int4*>(sees + c + k);
@@ -204,6 +204,7 @@ __device__ __forceinline__ float tile_sum(uint32_t tS, const float* nls, const i
       part[1] = add2(part[1], make_float2(p2, p3));
     }
   }
+  tmem_ld_wait();  // (a load past the last columns may be under way)
   return (part[0].x + part[0].y) + (part[1].x + part[1].y);
 }
 
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     ctl.issued_k = ctl.issued_q = 0;
     for (int i = 0; i < C::kKBufs; ++i) {
       mbar_init(bar(ctl.k_full[i]), 1);
-      mbar_init(bar(ctl.k_empty[i]), C::kFew ? 1 : 128);
+      mbar_init(bar(ctl.k_empty[i]), C::kIssuers);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(bar(ctl.q_full[i]), 1);
@@ -237,12 +238,10 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       mbar_init(bar(ctl.s_free[i]), 128);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(ctl.sum_ready[i]), 128 * kGroups);
+      mbar_init(bar(ctl.sum_ready[i]), 128 * C::kGroups);
       mbar_init(bar(ctl.sum_free[i]), 128);
-      mbar_init(bar(ctl.kt_full[i]), 128);
-      mbar_init(bar(ctl.kt_empty[i]), 1);
     }
-    mbar_init(bar(ctl.drain), 1);
+    mbar_init(bar(ctl.drain), C::kIssuers);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
@@ -326,41 +325,37 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       w.next();
       page = w.done() ? 0 : page_of(w);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == C::kThreads / 32 - C::kIssuers + 1) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0) {
-      // Every instruction between products is time the tensor pipe may idle: positions in the rings are
-      // counters, and with many rows the group that sees the scores releases the query tile.
+      // Positions in the rings are counters and the group that sees the scores releases the query tile:
+      // every instruction between a thread's products is time the pipe may idle.
+      const int me = warp == 1 ? 0 : 1;
       bool run = true;
       int t = 0, ks = 0, qs = 0, sb = 0, qn = 0;
       uint32_t kphase = 0, qphase = 0, sphase = 1;  // parity awaited on the ring's current buffer
-      for (int kn = 0; !w.done() && run; ++kn) {
+      while (!w.done() && run) {
         if (C::kFew && w.head) {
           qs = qn % C::kQBufs;
           run = mbar_wait_spin(bar(ctl.q_full[qs]), (qn / C::kQBufs) & 1, abort_flag, a.status);
           ++qn;
         }
-        if (run)
-          run = C::kFew ? mbar_wait_spin(bar(ctl.k_full[ks]), kphase, abort_flag, a.status)
-                        : mbar_wait_spin(bar(ctl.kt_full[kn & 1]), (kn >> 1) & 1, abort_flag, a.status);
+        if (run) run = mbar_wait_spin(bar(ctl.k_full[ks]), kphase, abort_flag, a.status);
         const uint64_t dk = desc_kmajor_sw128(sK + ks * C::kKBytes);
-        const uint32_t tK = tmem + C::kSBufs * NP + (kn & 1) * (D / 2);
         for (int i = w.it; i < w.end && run; ++i, ++t) {
-          if (!C::kFew) run = mbar_wait_spin(bar(ctl.q_full[qs]), qphase, abort_flag, a.status);
-          if (run && t >= C::kSBufs) run = mbar_wait_spin(bar(ctl.s_free[sb]), sphase, abort_flag, a.status);
-          fence_after_sync();
-          if (!run) break;
-          const uint64_t dq = desc_kmajor_sw128(sQ + qs * C::kQBytes);
+          if (C::kIssuers == 1 || (t & 1) == me) {
+            if (!C::kFew) run = mbar_wait_spin(bar(ctl.q_full[qs]), qphase, abort_flag, a.status);
+            if (run && t >= 4) run = mbar_wait_spin(bar(ctl.s_free[sb]), sphase, abort_flag, a.status);
+            fence_after_sync();
+            if (!run) break;
+            const uint64_t dq = desc_kmajor_sw128(sQ + qs * C::kQBytes);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t dqk = desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32);
-            if constexpr (C::kFew)
-              mma_ss(tmem + sb * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32), dqk, C::kId, kk > 0);
-            else
-              mma_ts(tmem + sb * NP, tK + kk * 8, dqk, C::kId, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + sb * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32),
+                     desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32), C::kId, kk > 0);
+            mma_commit(bar(ctl.s_full[sb]));
           }
-          mma_commit(bar(ctl.s_full[sb]));
-          if (++sb == C::kSBufs) {
+          if (++sb == 4) {
             sb = 0;
             sphase ^= 1;
           }
@@ -370,7 +365,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
           }
         }
         if (!run) break;
-        mma_commit(C::kFew ? bar(ctl.k_empty[ks]) : bar(ctl.kt_empty[kn & 1]));
+        mma_commit(bar(ctl.k_empty[ks]));
         if (++ks == C::kKBufs) {
           ks = 0;
           kphase ^= 1;
@@ -381,7 +376,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       mma_commit(bar(ctl.drain));
       mbar_wait_drain(bar(ctl.drain), 0);
     }
-  } else if (warp < 2 + 4 * kGroups) {
+  } else if (warp < 2 + 4 * C::kGroups) {
     // ------------------------------------------------------------------ exponentials and sums
     const int gr = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;  // group; key (and row, for the LSE)
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -417,8 +412,8 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     auto tile = [&](int token) -> float {
       const bool masked = hidden || (s.causal && (w.kt << 7) + 127 > token + w.x.q.off);
       const int cols = min(used, (w.x.q.Lq - token) * rows.gs), key = (w.kt << 7) + r;
-      const int sb = t % C::kSBufs;
-      if (run) run = mbar_wait(bar(ctl.s_full[sb]), (t / C::kSBufs) & 1, abort_flag, a.status);
+      const int sb = t & 3;
+      if (run) run = mbar_wait(bar(ctl.s_full[sb]), (t >> 2) & 1, abort_flag, a.status);
       if (!C::kFew && run && r == 0) mbar_arrive(bar(ctl.q_empty[t % C::kQBufs]));  // the product has read it
       __syncwarp();
       fence_after_sync();
@@ -453,7 +448,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       while (!w.done()) {
         WPieces<C::kFew> ahead = w;
         bool turns = false;  // the head changes before this group's next tile
-        for (int i = 0; i < kGroups && !ahead.done(); ++i) {
+        for (int i = 0; i < C::kGroups && !ahead.done(); ++i) {
           ahead.next();
           turns |= ahead.head;
         }
@@ -467,22 +462,22 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
         at = then;
         old = before;
         w.skip_to(ahead);
-        t += kGroups;
+        t += C::kGroups;
         __syncwarp();
       }
     } else {
       for (int piece = 0; !w.done(); ++piece, w.next()) {
-        int i = w.it + (gr + kGroups - t % kGroups) % kGroups;  // this group's first tile of the piece
+        int i = w.it + (gr + C::kGroups - t % C::kGroups) % C::kGroups;  // this group's first tile of the piece
         const int t0 = t;
         float sum = 0.f;
         typename WPieces<C::kFew>::Cursor at(w, i);
         float lse = i < w.end ? load_lse(at.token(w), at.head0(w)) : 0.f;
-        for (; i < w.end; i += kGroups) {
+        for (; i < w.end; i += C::kGroups) {
           t = t0 + (i - w.it);
           const int token = at.token(w);
           stage_lse(token, lse);
-          at.advance(w, kGroups);
-          if (i + kGroups < w.end) lse = load_lse(at.token(w), at.head0(w));
+          at.advance(w, C::kGroups);
+          if (i + C::kGroups < w.end) lse = load_lse(at.token(w), at.head0(w));
           sum += tile(token);
         }
         t = t0 + (w.end - w.it);
@@ -494,39 +489,10 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       }
     }
   } else if constexpr (!C::kFew) {
-    // ------------------------------------------------------------------ the units' key tiles and sums
-    const int r = (warp & 3) * 32 + lane;  // key within the tile (the tensor-memory lane of this thread)
+    // ------------------------------------------------------------------ sums to weights
+    const int r = threadIdx.x - (64 + 128 * C::kGroups);
     bool run = true;
-    int kn = 0;
-    // Key tile kn from shared memory into tensor memory, a row per lane.
-    auto move_k = [&]() {
-      const int ks = kn % C::kKBufs;
-      if (run && kn >= 2) run = mbar_wait(bar(ctl.kt_empty[kn & 1]), ((kn >> 1) - 1) & 1, abort_flag, a.status);
-      if (run) run = mbar_wait(bar(ctl.k_full[ks]), (kn / C::kKBufs) & 1, abort_flag, a.status);
-      __syncwarp();
-      fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(x[4 * i]), "=r"(x[4 * i + 1]), "=r"(x[4 * i + 2]), "=r"(x[4 * i + 3])
-                       : "r"(sK + ks * C::kKBytes + c * 16384 + r * 128 + ((i ^ (r & 7)) << 4))
-                       : "memory");
-        tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kSBufs * NP + (kn & 1) * (D / 2) + c * 32, x);
-      }
-      tmem_st_wait();
-      fence_before_sync();
-      if (run) {
-        mbar_arrive(bar(ctl.k_empty[ks]));
-        mbar_arrive(bar(ctl.kt_full[kn & 1]));
-      }
-      __syncwarp();
-      ++kn;
-    };
-    if (!w.done()) move_k();
-    for (int piece = 0; !w.done(); ++piece) {
+    for (int piece = 0; !w.done(); ++piece, w.next()) {
       const int key = (w.kt << 7) + r, pp = piece & 1;
       float* at = nullptr;
       float old = 0.f;
@@ -539,13 +505,10 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       } else if (!w.whole()) {
         at = wk.part + (size_t)(2 * blockIdx.x + (piece == 0 ? 0 : 1)) * 128 + r;
       }
-      __syncwarp();
-      w.next();
-      if (!w.done()) move_k();
       if (run) run = mbar_wait(bar(ctl.sum_ready[pp]), (piece >> 1) & 1, abort_flag, a.status);
       float sum = 0.f;
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) sum += ctl.sums[pp][g][r];
+      for (int g = 0; g < C::kGroups; ++g) sum += ctl.sums[pp][g][r];
       if (run) mbar_arrive(bar(ctl.sum_free[pp]));
       if (at != nullptr) *at = old + sum;
       __syncwarp();
