@@ -5,38 +5,53 @@
 namespace fa {
 namespace {
 
-// Append: one warp per new token and tensor (K, V), 16 bytes a lane.
+// Append: one warp per new token and tensor (K, V), 16 bytes a lane and up to four of them in flight.
+// Bound by memory: the rows are read and written once.
 __global__ void __launch_bounds__(256) paged_append_kernel(const FaPagedArgs a) {
   grid_dependency_wait();
   const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31, chunks = s.d / 8;  // 16-byte chunks of a head's row
-  const size_t items = (size_t)s.B * s.Nq * 2;
-  const size_t step = ((size_t)gridDim.x * blockDim.x) >> 5;
-  for (size_t w = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < items; w += step) {
-    const bool is_v = w & 1;
-    const int i = (int)((w >> 1) % s.Nq), b = (int)((w >> 1) / s.Nq);
-    const SeqInfo seq = paged_seq(s, b);
-    if (i >= seq.Lq) continue;
-    const long long j = (long long)__ldg(s.seqlens + b) - seq.Lq + i;  // the unclamped length places the token
-    if (j < 0 || (j >> s.page_shift) >= s.max_pages) {
-      if (lane == 0) report_status(a.status, FA_ERR_BOUNDS);
-      continue;
-    }
-    const int page = paged_page(s, b, (int)(j >> s.page_shift), a.status);
-    if (page < 0) continue;
-    const int slot = (int)(j & ((1 << s.page_shift) - 1));
-    const FaStrides& ts = is_v ? a.sv_new : a.sk_new;
-    const FaStrides& td = is_v ? a.sv : a.sk;
-    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_v ? a.v_new : a.k_new);
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v : a.k);
-    for (int c = lane; c < s.Hkv * chunks; c += 32) {
-      const int h = c / chunks, e = c % chunks * 8;
-      *reinterpret_cast<uint4*>(dst + paged_offset(td, page, slot, h) + e) =
-          *reinterpret_cast<const uint4*>(src + elem_offset(ts, seq.bb, seq.q0 + i, h) + e);
-    }
-    if (!is_v && a.weights != nullptr)
-      for (int h = lane; h < s.Hkv; h += 32) a.weights[weight_offset(s, page, h, slot)] = 0.f;
+  const int lane = threadIdx.x & 31, shift = s.d == 128 ? 4 : 3;  // 16-byte chunks of a head's row
+  const size_t w = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (w >= (size_t)s.B * s.Nq * 2) return;
+  const bool is_v = w & 1;
+  const int i = (int)((w >> 1) % s.Nq), b = (int)((w >> 1) / s.Nq);
+  const SeqInfo seq = paged_seq(s, b);
+  if (i >= seq.Lq) return;
+  const long long j = (long long)__ldg(s.seqlens + b) - seq.Lq + i;  // the unclamped length places the token
+  if (j < 0 || (j >> s.page_shift) >= s.max_pages) {
+    if (lane == 0) report_status(a.status, FA_ERR_BOUNDS);
+    return;
   }
+  const FaStrides& ts = is_v ? a.sv_new : a.sk_new;
+  const FaStrides& td = is_v ? a.sv : a.sk;
+  const __nv_bfloat16* src =
+      reinterpret_cast<const __nv_bfloat16*>(is_v ? a.v_new : a.k_new) + elem_offset(ts, seq.bb, seq.q0 + i, 0);
+  const int chunks = s.Hkv << shift;
+  uint4 x[4];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + k * 32 + lane;
+      if (c < chunks)
+        x[k] = *reinterpret_cast<const uint4*>(src + (size_t)(c >> shift) * ts.head + (c & ((1 << shift) - 1)) * 8);
+    }
+  };
+  load(0);  // on its way while the page is looked up
+  const int page = paged_page(s, b, (int)(j >> s.page_shift), a.status);
+  if (page < 0) return;
+  const int slot = (int)(j & ((1 << s.page_shift) - 1));
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v : a.k) + paged_offset(td, page, slot, 0);
+  for (int c0 = 0; c0 < chunks; c0 += 128) {
+    if (c0 > 0) load(c0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + k * 32 + lane;
+      if (c < chunks)
+        *reinterpret_cast<uint4*>(dst + (size_t)(c >> shift) * td.head + (c & ((1 << shift) - 1)) * 8) = x[k];
+    }
+  }
+  if (!is_v && a.weights != nullptr)
+    for (int h = lane; h < s.Hkv; h += 32) a.weights[weight_offset(s, page, h, slot)] = 0.f;
 }
 
 // ----------------------------------------------------------------------------- eviction
@@ -330,12 +345,8 @@ cudaError_t launch_select(const FaPagedArgs& a, unsigned ctas, cudaStream_t st) 
 }  // namespace fa
 
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st) {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const size_t ctas = ((size_t)a.s.B * a.s.Nq * 2 + 7) / 8;
-  const unsigned grid = (unsigned)(ctas < (size_t)sms * 8 ? ctas : (size_t)sms * 8);
-  return launch_dependent(fa::paged_append_kernel, dim3(grid), dim3(256), 0, st, a);
+  const long long ctas = ((long long)a.s.B * a.s.Nq * 2 + 7) / 8;  // (below 2^30: checked with the shape)
+  return launch_dependent(fa::paged_append_kernel, dim3((unsigned)ctas), dim3(256), 0, st, a);
 }
 
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st) {

@@ -294,53 +294,67 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0) {
+      // An MMA takes this thread about 70 cycles and everything between MMAs adds to a tile's time, so the
+      // positions in the rings are counters and descriptors are built once.
       bool run = true;
-      int t = 0;  // tiles whose S has been issued: t + 1 ahead of the P V
       Pieces v = w;  // the piece of the next S
-      int vkt = v.kt, vpiece = 0;
+      int left = v.end - v.kt, ks = 0, vpiece = 0;  // its key tiles without S; ring position
+      uint32_t kphase = 0, sb = 0;
+      bool opens = true;
+      const uint64_t dk0 = desc_kmajor_sw128(sK(0)), dq0 = desc_kmajor_sw128(sQ), dv0 = desc_mnmajor_sw128(sV(0), 16384);
+      const uint64_t dp0 = desc_mnmajor_sw128(sP, 16384);
       auto issue_s = [&]() {
-        const int st = t % C::kKStages, qb = vpiece % C::kQBufs;
-        if (run && vkt == v.kt)
-          run = mbar_wait_spin(bar(ctl.q_full[qb]), (vpiece / C::kQBufs) & 1, abort_flag, a.status);
-        if (run) run = mbar_wait_spin(bar(ctl.k_full[st]), (t / C::kKStages) & 1, abort_flag, a.status);
+        const int qb = vpiece & 1;
+        if (run && opens) run = mbar_wait_spin(bar(ctl.q_full[qb]), (vpiece >> 1) & 1, abort_flag, a.status);
+        if (run) run = mbar_wait_spin(bar(ctl.k_full[ks]), kphase, abort_flag, a.status);
         fence_after_sync();
         if (run) {
-          const uint64_t dk = desc_kmajor_sw128(sK(st)), dq = desc_kmajor_sw128(sQ + qb * C::kQBytes);
+          const uint64_t dk = desc_add(dk0, ks * C::kTileBytes), dq = desc_add(dq0, qb * C::kQBytes);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + (t & 1) * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32),
+            mma_ss(tmem + sb * NP, desc_add(dk, (kk >> 2) * 16384 + (kk & 3) * 32),
                    desc_add(dq, (kk >> 2) * NP * 128 + (kk & 3) * 32), C::kIdS, kk > 0);
-          mma_commit(bar(ctl.s_full[t & 1]));
-          mma_commit(bar(ctl.k_empty[st]));
-          if (vkt + 1 == v.end) mma_commit(bar(ctl.q_empty[qb]));
+          mma_commit(bar(ctl.s_full[sb]));
+          mma_commit(bar(ctl.k_empty[ks]));
+          if (left == 1) mma_commit(bar(ctl.q_empty[qb]));
         }
-        ++t;
-        if (++vkt == v.end) {
+        sb ^= 1;
+        if (++ks == C::kKStages) {
+          ks = 0;
+          kphase ^= 1;
+        }
+        opens = --left == 0;
+        if (opens) {
           v.next();
-          vkt = 0;
+          left = v.end - v.kt;
           ++vpiece;
         }
       };
       if (!w.done()) issue_s();
-      int j = 0;
+      int vs = 0;
+      uint32_t vphase = 0, pb = 0, pphase = 0;
       for (int piece = 0; !w.done(); ++piece) {
-        for (int kt = w.kt; kt < w.end; ++kt, ++j) {
+        const uint32_t tO = tmem + (2 + (piece & 1)) * NP;
+        for (int kt = w.kt; kt < w.end; ++kt) {
           if (!v.done()) issue_s();
-          const int st = j % C::kVStages;
-          if (run) run = mbar_wait_spin(bar(ctl.p_ready[j & 1]), (j >> 1) & 1, abort_flag, a.status);
-          if (run) run = mbar_wait_spin(bar(ctl.v_full[st]), (j / C::kVStages) & 1, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.p_ready[pb]), pphase, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.v_full[vs]), vphase, abort_flag, a.status);
           if (run && kt == w.kt && piece >= 2)
             run = mbar_wait_spin(bar(ctl.o_free[piece & 1]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
           fence_after_sync();
           if (run) {
-            const uint64_t dv = desc_mnmajor_sw128(sV(st), 16384);
-            const uint64_t dp = desc_mnmajor_sw128(sP + (j & 1) * C::kPStep, 16384);
+            const uint64_t dv = desc_add(dv0, vs * C::kTileBytes), dp = desc_add(dp0, pb * C::kPStep);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ss(tmem + (2 + (piece & 1)) * NP, desc_add(dv, kk * 2048), desc_add(dp, kk * 2048), C::kIdPV,
-                     kk > 0 || kt > w.kt);
-            mma_commit(bar(ctl.v_empty[st]));
-            mma_commit(bar(ctl.pv_done[j & 1]));
+              mma_ss(tO, desc_add(dv, kk * 2048), desc_add(dp, kk * 2048), C::kIdPV, kk > 0 || kt > w.kt);
+            mma_commit(bar(ctl.v_empty[vs]));
+            mma_commit(bar(ctl.pv_done[pb]));
+          }
+          pphase ^= pb;
+          pb ^= 1;
+          if (++vs == C::kVStages) {
+            vs = 0;
+            vphase ^= 1;
           }
         }
         w.next();
