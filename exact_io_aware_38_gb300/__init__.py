@@ -661,7 +661,9 @@ def _launch(dev, stream, call, *args):
 
 
 def _scratch(workspace, nbytes, dev):
-    """(pointer, bytes) of the caller's workspace, or of a new one, and its tensor."""
+    """(pointer, bytes) of the caller's workspace, or of a new one, and its tensor; nothing where none is needed."""
+    if nbytes == 0:
+        return None, 0, None
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         return workspace.data_ptr(), nbytes, workspace
@@ -695,7 +697,8 @@ def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max
         lse = torch.empty((n[1], n[0]) if dims == 3 else (n[0], n[2], n[1]), dtype=torch.float32, device=dev)
     else:
         _check_aux("lse", lse, torch.float32, q.numel() // p.d, dev)
-    _check_aux("status", status, torch.int32, 1, dev)
+    if status is not None:
+        _check_aux("status", status, torch.int32, 1, dev)
     sq, so = _paged_views("q", q, "out", out, dims)
     sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4)
     if p.B == 0 or q.numel() == 0:  # no new token anywhere

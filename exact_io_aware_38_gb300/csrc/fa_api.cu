@@ -654,8 +654,9 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strid
   FaPagedArgs a{};
   int rc = paged_shape(p, true, &a.s);
   if (rc != FA_OK) return rc;
-  if (num_sms < 1 || num_sms > kMaxSms || workspace == nullptr || workspace_bytes < paged_workspace(a.s, num_sms))
-    return FA_ERR_INVALID_ARG;
+  if (num_sms < 1 || num_sms > kMaxSms) return FA_ERR_INVALID_ARG;
+  const size_t need = paged_workspace(a.s, num_sms);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   const bool packed = a.s.cu_q != nullptr;
   const int rows = packed ? a.s.rows_q : a.s.Nq;
   if ((rc = take_strides(sq, packed, a.s.B, rows, a.s.H, &a.sq)) != FA_OK ||
@@ -664,7 +665,7 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strid
     return rc;
   if (!q || !k_cache || !v_cache || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
-      !aligned(dev_status, 4) || !aligned(workspace, kAlign))
+      !aligned(dev_status, 4) || (need > 0 && !aligned(workspace, kAlign)))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
   a.q = q;
@@ -710,7 +711,7 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
 size_t fa_paged_key_weights_workspace_bytes(const fa_paged_problem* p, int num_sms) {
   fa::PagedShape s;
   if (paged_shape(p, true, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
-  return round_up(fa_paged_weights_workspace(num_sms));
+  return round_up(fa_paged_weights_workspace(s, num_sms));
 }
 
 int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
@@ -719,16 +720,16 @@ int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, 
   FaPagedArgs a{};
   int rc = paged_shape(p, true, &a.s);
   if (rc != FA_OK) return rc;
-  if (num_sms < 1 || num_sms > kMaxSms || workspace == nullptr ||
-      workspace_bytes < round_up(fa_paged_weights_workspace(num_sms)))
-    return FA_ERR_INVALID_ARG;
+  if (num_sms < 1 || num_sms > kMaxSms) return FA_ERR_INVALID_ARG;
+  const size_t need = round_up(fa_paged_weights_workspace(a.s, num_sms));
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   const bool packed = a.s.cu_q != nullptr;
   if ((rc = take_strides(sq, packed, a.s.B, packed ? a.s.rows_q : a.s.Nq, a.s.H, &a.sq)) != FA_OK ||
       (rc = take_cache_strides(sk, p, &a.sk)) != FA_OK)
     return rc;
   if (!q || !k_cache || !lse || !key_weights) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(key_weights, 16) ||
-      !aligned(dev_status, 4) || !aligned(workspace, kAlign))
+      !aligned(dev_status, 4) || (need > 0 && !aligned(workspace, kAlign)))
     return FA_ERR_MISALIGNED;
   if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
   a.num_sms = num_sms;

@@ -253,6 +253,6 @@ __device__ __forceinline__ void join_pieces(const FaPagedArgs& a, const float* p
 }  // namespace fa
 
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
-size_t fa_paged_weights_workspace(int num_sms);
+size_t fa_paged_weights_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);

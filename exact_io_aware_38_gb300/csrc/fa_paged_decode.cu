@@ -173,7 +173,8 @@ __device__ __forceinline__ bool vote_any(bool x) {
 struct DecWork {
   float* part_o;    // [2 CTAs][NP][D]
   float* part_lse;  // [2 CTAs][NP], log2 units
-  int4* desc;       // [CTAs]: {b, hk, first CTA, its slot}; b = -1: no (sequence, head) ends here in pieces
+  int4* desc;       // [CTAs]: {b, hk, first CTA, its slot}; b = -1: no (sequence, head) ends here in pieces. Null:
+                    // every (sequence, head) has a CTA of its own
 };
 
 template <int D, int NP>
@@ -230,7 +231,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
                  : "memory");
   }
   fence_proxy_async_smem();
-  find_share<kDecThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
+  if (wk.desc != nullptr) {
+    find_share<kDecThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
+  } else if (threadIdx.x == 0) {  // a unit per CTA
+    const DecUnits x(s, blockIdx.x / s.Hkv);
+    ctl.share = Share{(int)blockIdx.x / s.Hkv, (int)blockIdx.x % s.Hkv, 0, 0, x.count ? x.before(1) : 0, 0, 0};
+  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
   // Only the merge waits for this grid; its blocks may be scheduled as SMs drain.
   asm volatile("griddepcontrol.launch_dependents;");
   Pieces w(s, ctl.share);
-  if (threadIdx.x == 0) {
+  if (wk.desc != nullptr && threadIdx.x == 0) {
     const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
     wk.desc[blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);
   }
@@ -576,6 +582,16 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, co
   }
 }
 
+int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// Short keys and few (sequence, head) units: a CTA takes a whole one. A tile more costs about 1.2 us there,
+// the search for shares and the merge launch 4 us and a workspace (one sequence of 777 keys, 7 tiles: 16.0 us
+// undivided, 10.2 us divided).
+bool undivided(const PagedShape& s, int num_sms) {
+  const int np = padded_rows(s.Nq * (s.H / s.Hkv));
+  return s.max_k <= 3 * 128 && (long long)s.B * s.Hkv <= (long long)num_sms * dec_ctas(s.d, np);
+}
+
 template <int D, int NP>
 cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
   using C = DecCfg<D, NP>;
@@ -589,30 +605,32 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
       !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128) ||
       !fa_make_tmap_bf16(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, P < 128 ? P : 128))
     return cudaErrorInvalidValue;
-  DecWork wk;
-  char* ws = static_cast<char*>(a.workspace);
-  wk.desc = reinterpret_cast<int4*>(ws);
-  const int ctas = a.num_sms * C::kCtas;
-  ws += up256((size_t)ctas * sizeof(int4));
-  wk.part_lse = reinterpret_cast<float*>(ws);
-  ws += up256((size_t)ctas * 2 * NP * sizeof(float));
-  wk.part_o = reinterpret_cast<float*>(ws);
+  const bool whole = undivided(s, a.num_sms);
+  const int ctas = whole ? s.B * s.Hkv : a.num_sms * C::kCtas;
+  DecWork wk{};
+  if (!whole) {
+    char* ws = static_cast<char*>(a.workspace);
+    wk.desc = reinterpret_cast<int4*>(ws);
+    ws += up256((size_t)ctas * sizeof(int4));
+    wk.part_lse = reinterpret_cast<float*>(ws);
+    ws += up256((size_t)ctas * 2 * NP * sizeof(float));
+    wk.part_o = reinterpret_cast<float*>(ws);
+  }
   auto kern = paged_decode_kernel<D, NP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   if (C::kCtas > 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(ctas), dim3(kDecThreads), C::kSmem, st, tq, tk, tv, a, wk);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   return launch_dependent(paged_join_kernel<D, NP>, dim3(ctas), dim3(256), 0, st, a, wk);
 }
-
-int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 }  // namespace
 }  // namespace fa
 
 size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms) {
+  if (fa::undivided(s, num_sms)) return 0;
   const int np = fa::padded_rows(s.Nq * (s.H / s.Hkv));
   const size_t ctas = (size_t)num_sms * fa::dec_ctas(s.d, np), rows = ctas * 2 * np;
   return fa::up256(ctas * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);

@@ -556,9 +556,11 @@ cudaError_t launch_weights(const FaPagedArgs& a, const PagedRows& rows, cudaStre
                          rows.gs, rows.tpt) ||
       !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128))
     return cudaErrorInvalidValue;
-  WWork wk;
-  wk.desc = static_cast<WJoin*>(a.workspace);
-  wk.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + (size_t)a.num_sms * sizeof(WJoin));
+  WWork wk{};
+  if (!C::kFew) {
+    wk.desc = static_cast<WJoin*>(a.workspace);
+    wk.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + (size_t)a.num_sms * sizeof(WJoin));
+  }
   auto kern = paged_weights_kernel<D, NP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -581,7 +583,8 @@ cudaError_t launch_weights_d(const FaPagedArgs& a, cudaStream_t st) {
 }  // namespace
 }  // namespace fa
 
-size_t fa_paged_weights_workspace(int num_sms) {
+size_t fa_paged_weights_workspace(const fa::PagedShape& s, int num_sms) {
+  if (fa::paged_few_rows(s)) return 0;  // a key tile is one query tile's work
   return (size_t)num_sms * (sizeof(fa::WJoin) + 2 * 128 * sizeof(float));
 }
 

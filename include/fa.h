@@ -338,8 +338,9 @@ typedef struct {
  *                fewer leave SMs to other work). The division follows the lengths on the device: each CTA takes an
  *                equal share of all key tiles, so one long sequence fills the GPU as many short ones do, and partial
  *                results of divided sequences are merged by their log-sum-exp.
- *   workspace    device, >= fa_fwd_paged_workspace_bytes(p, num_sms) bytes (it does not grow with the lengths),
- *                256-byte aligned; scratch only
+ *   workspace    device, >= fa_fwd_paged_workspace_bytes(p, num_sms) bytes (it does not grow with the lengths; 0 for
+ *                short keys and few sequences, of which none is divided: it may be NULL then), 256-byte aligned;
+ *                scratch only
  */
 size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_sms);
 int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
@@ -363,7 +364,8 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
  *   key_weights[b, hk, j] += sum over rows i that see key j and heads h of group hk of exp(scale q_ih . k_j - LSE_ih)
  * with the LSE that fa_fwd_paged gave for the same rows, cache and lengths (or for more keys: any LSE of the
  * caller's). A row with LSE = -inf adds nothing. Sums are fp32, in a fixed order: the result is run-to-run identical.
- * num_sms and workspace as for fa_fwd_paged, sized by fa_paged_key_weights_workspace_bytes.
+ * num_sms and workspace as for fa_fwd_paged; the size, fa_paged_key_weights_workspace_bytes, is 0 where the rows of a
+ * K/V head (tokens x heads) are at most 64.
  */
 size_t fa_paged_key_weights_workspace_bytes(const fa_paged_problem* p, int num_sms);
 int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,

@@ -64,7 +64,7 @@ def test_problem_refusals_of_calls_with_queries(kw, rc):
 
 
 def test_buffer_refusals():
-    for call, names in ((attend, "q k v o lse ws"), (append, "kn vn k v"), (weights, "q k lse w ws"), (evict, "k v w kept out")):
+    for call, names in ((attend, "q k v o lse"), (append, "kn vn k v"), (weights, "q k lse w"), (evict, "k v w kept out")):
         for n in names.split():
             assert call(**{n: None}) == -1, (call, n)
             assert call(**{n: A + 2}) == -3, (call, n)
@@ -78,19 +78,30 @@ def test_buffer_refusals():
     assert attend(sk=fa.Strides(256, 128, 1 << 39)) == -2
 
 
-@pytest.mark.parametrize("call,size", [(attend, "fa_fwd_paged_workspace_bytes"),
-                                       (weights, "fa_paged_key_weights_workspace_bytes")])
-def test_workspace_rules(call, size):
+@pytest.mark.parametrize("call,size,kw", [
+    (attend, "fa_fwd_paged_workspace_bytes", dict(max_pages=1000, seqlen_k=4000)),
+    (attend, "fa_fwd_paged_workspace_bytes", dict(B=200)),
+    (attend, "fa_fwd_paged_workspace_bytes", dict(seqlen_q=500)),
+    (weights, "fa_paged_key_weights_workspace_bytes", dict(seqlen_q=500))])
+def test_workspace_rules(call, size, kw):
     size = getattr(fa, size)
-    for n in (3, 500):  # few rows, and more
-        p = problem(seqlen_q=n)
-        need = size(p, 152)
-        assert need > 0 and need % 256 == 0
-        assert size(problem(seqlen_q=n, seqlen_k=16), 152) == need  # it does not grow with the lengths
-        assert size(p, 0) == size(p, 1025) == size(problem(d=96), 152) == 0
-        for sms, ws, nbytes, rc in ((0, A, 1 << 30, -1), (1025, A, 1 << 30, -1), (152, None, 1 << 30, -1),
-                                    (152, A, need - 1, -1), (152, A + 16, 1 << 30, -3)):
-            assert call(p, sms=sms, ws=ws, nbytes=nbytes) == rc
+    p = problem(**kw)
+    need = size(p, 152)
+    assert need > 0 and need % 256 == 0
+    assert size(problem(**{**kw, "seqlen_k": 160_000, "max_pages": 10_000}), 152) == need  # not by the lengths
+    assert size(p, 0) == size(p, 1025) == size(problem(d=96), 152) == 0
+    for sms, ws, nbytes, rc in ((0, A, 1 << 30, -1), (1025, A, 1 << 30, -1), (152, None, 1 << 30, -1),
+                                (152, A, need - 1, -1), (152, A + 16, 1 << 30, -3)):
+        assert call(p, sms=sms, ws=ws, nbytes=nbytes) == rc
+
+
+def test_no_workspace():
+    """Few rows over short keys are not divided, and key weights of few rows never are: the workspace may be null (the
+    refusal is then the next one, an odd output pointer)."""
+    assert fa.fa_fwd_paged_workspace_bytes(problem(), 152) == 0
+    assert fa.fa_fwd_paged_workspace_bytes(problem(), 3) > 0  # more (sequence, head) units than CTAs
+    assert fa.fa_paged_key_weights_workspace_bytes(problem(max_pages=9000, seqlen_k=100_000), 152) == 0
+    assert attend(ws=None, nbytes=0, o=A + 2) == weights(ws=None, nbytes=0, w=A + 2) == -3
 
 
 def test_evict_budget_and_alias():
