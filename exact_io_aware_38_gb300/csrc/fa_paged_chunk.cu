@@ -39,13 +39,15 @@ struct ChCfg {
 struct ChCtl {
   uint64_t q_full, q_empty, k0_full, k0_empty;
   uint64_t full[4], empty[4];
-  uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
-  uint64_t tail, drain;
+  uint64_t s_full[2], o_done[2], o_free[2];
+  uint64_t p_ready, tail, drain;  // p_ready: of tile 1
   uint32_t tmem_base;
   int abort_flag;
   long long scan[kChThreads / 32];
   Share share;
   int issued_q, issued_k0, issued_t, issued_tail;  // copies issued (abort-path drain)
+  int needs_p0[4];   // by stage buffer: tile 0's softmax arrives on its last stage
+  int p0_last[128];  // by row of tile 0: the last stage its thread arrived on
 };
 
 struct JoinDesc {
@@ -168,15 +170,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
     mbar_init(bar(ctl.k0_full), 1);
     mbar_init(bar(ctl.k0_empty), 1);
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(ctl.full[i]), 1);
+      mbar_init(bar(ctl.full[i]), 1 + 128);  // the copies, and P of tile 0 (or its stand-in)
       mbar_init(bar(ctl.empty[i]), 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(ctl.s_full[x]), 1);
-      mbar_init(bar(ctl.p_ready[x]), 128);
       mbar_init(bar(ctl.o_done[x]), 1);
       mbar_init(bar(ctl.o_free[x]), 128);
     }
+    mbar_init(bar(ctl.p_ready), 128);
     mbar_init(bar(ctl.tail), 1);
     mbar_init(bar(ctl.drain), 1);
     fence_mbar_init();
@@ -272,6 +274,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (!run) continue;
           const int valid = w.seq.Lk - (kt << 7);
           const int vbytes = pages_in(w, kt) * prows * D * 2, kbytes = more ? pages_in(v, vkt) * prows * D * 2 : 0;
+          if (lane == 0) {
+            const bool p0 = kt < w.tiles(0);
+            if (!p0) mbar_arrive_cnt(bar(ctl.full[st]), 128);  // tile 0 has no P for this key tile
+            ctl.needs_p0[st] = p0;
+          }
           if (valid >= 128) {
             if (lane == 0) {
               mbar_expect_tx(bar(ctl.full[st]), vbytes + kbytes);
@@ -315,14 +322,16 @@ __global__ void __launch_bounds__(kChThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0 && !w.done()) {
+      // The pipe idles while this thread does anything but issue, so the tiles inside a unit that both query
+      // tiles see (all but its ends) run in a loop of two waits, four products and three commits.
       bool run = true;
-      uint32_t np[2] = {0, 0}, pieces[2] = {0, 0};  // tiles whose P was awaited; pieces with tiles, per query tile
+      uint32_t p1phase = 0, seen0 = 0, seen1 = 0;  // parity of tile 1's P; pieces with tiles, per query tile
       ChPieces v = w;
       int vkt = v.kt, vpiece = 0;
-      int vn[2] = {v.tiles(0), v.tiles(1)};  // key tiles each query tile sees, in the piece of the next S
-      int wn[2] = {vn[0], vn[1]};
-      auto issue_s = [&](int x, uint32_t ka) {
-        const uint64_t dq = desc_kmajor_sw128(sQ + x * C::kTileBytes), dk = desc_kmajor_sw128(ka);
+      int vn0 = v.tiles(0), vn1 = v.tiles(1);  // key tiles each query tile sees, in the piece of the next S
+      const uint64_t dq0 = desc_kmajor_sw128(sQ), dk0 = desc_kmajor_sw128(sK(0)), dv0 = desc_mnmajor_sw128(sV(0), 16384);
+      auto issue_s = [&](int x, int st) {
+        const uint64_t dq = desc_add(dq0, x * C::kTileBytes), dk = desc_add(dk0, st * 2 * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
@@ -330,66 +339,96 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         mma_commit(bar(ctl.s_full[x]));
       };
-      auto issue_pv = [&](int x, uint32_t va, bool first) {
-        const uint64_t dv = desc_mnmajor_sw128(va, 16384);
+      auto issue_pv = [&](int x, int st, bool first) {
+        const uint64_t dv = desc_add(dv0, st * 2 * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, desc_add(dv, kk * 2048), C::kIdPV,
                  (first && kk == 0) ? 0u : 1u);
       };
+      auto wait_p1 = [&]() {
+        run = mbar_wait_spin(bar(ctl.p_ready), p1phase, abort_flag, a.status);
+        p1phase ^= 1;
+        fence_after_sync();
+      };
       run = mbar_wait_spin(bar(ctl.q_full), 0, abort_flag, a.status);
       if (run) run = mbar_wait_spin(bar(ctl.k0_full), 0, abort_flag, a.status);
       fence_after_sync();
       if (run) {
-        for (int x = 0; x < 2; ++x)
-          if (vkt < vn[x]) issue_s(x, sK(C::kStages - 1));
+        if (vkt < vn0) issue_s(0, C::kStages - 1);
+        if (vkt < vn1) issue_s(1, C::kStages - 1);
         mma_commit(bar(ctl.k0_empty));
         if (vkt + 1 == v.end) mma_commit(bar(ctl.q_empty));
       }
-      int t = 0;
+      int st = 0;
+      uint32_t phase = 0;
+      auto wait_stage = [&]() {  // V of this tile, K of the next, and P of tile 0
+        run = mbar_wait_spin(bar(ctl.full[st]), phase, abort_flag, a.status);
+        fence_after_sync();
+      };
+      auto next_stage = [&]() {
+        mma_commit(bar(ctl.empty[st]));
+        if (++st == C::kStages) {
+          st = 0;
+          phase ^= 1;
+        }
+      };
       for (; !w.done() && run; w.next()) {
-        wn[0] = w.tiles(0);
-        wn[1] = w.tiles(1);
-        for (int kt = w.kt; kt < w.end && run; ++kt, ++t) {
-          const int st = t % C::kStages;
-          const bool crosses = ++vkt == v.end;  // the next S belongs to the next piece
+        const int wn0 = vn0, wn1 = vn1, last0 = min(w.end, wn0) - 1, last1 = min(w.end, wn1) - 1;
+        const int steady = min(last0, last1);  // key tiles (w.kt, steady) are inside the unit for both
+        for (int kt = w.kt; kt < w.end && run; ++kt) {
+          for (; kt > w.kt && kt < steady; ++kt) {
+            wait_stage();
+            if (!run) break;
+            issue_pv(0, st, false);
+            issue_s(0, st);
+            wait_p1();
+            if (!run) break;
+            issue_pv(1, st, false);
+            issue_s(1, st);
+            if (kt + 2 == w.end) mma_commit(bar(ctl.q_empty));
+            next_stage();
+          }
+          if (!run) break;
+          const bool crosses = kt + 1 == w.end;  // the next S belongs to the next piece
           if (crosses) {
             v.next();
-            vkt = 0;
             ++vpiece;
             if (!v.done()) {
-              vn[0] = v.tiles(0);
-              vn[1] = v.tiles(1);
+              vn0 = v.tiles(0);
+              vn1 = v.tiles(1);
             }
           }
+          vkt = crosses ? 0 : kt + 1;
           const bool more = !v.done();
-          run = mbar_wait_spin(bar(ctl.full[st]), (t / C::kStages) & 1, abort_flag, a.status);
-          for (int x = 0; x < 2 && run; ++x) {
-            if (kt < wn[x]) {
-              if (kt == w.kt) {  // O still holds the last piece's until its epilogue has read it
-                if (pieces[x] > 0)
-                  run = mbar_wait_spin(bar(ctl.o_free[x]), (pieces[x] - 1) & 1, abort_flag, a.status);
-                ++pieces[x];
-              }
-              if (run) run = mbar_wait_spin(bar(ctl.p_ready[x]), np[x] & 1, abort_flag, a.status);
-              ++np[x];
-              fence_after_sync();
-              if (!run) break;
-              issue_pv(x, sV(st), kt == w.kt);
-              if (kt + 1 == min(w.end, wn[x])) mma_commit(bar(ctl.o_done[x]));
-            }
-            if (more && !crosses && vkt < vn[x]) issue_s(x, sK(st));
+          wait_stage();
+          if (run && kt <= last0) {
+            if (kt == w.kt && seen0++ > 0)  // O still holds the last piece's until its epilogue has read it
+              run = mbar_wait_spin(bar(ctl.o_free[0]), seen0 & 1, abort_flag, a.status);
+            fence_after_sync();
+            if (!run) break;
+            issue_pv(0, st, kt == w.kt);
+            if (kt == last0) mma_commit(bar(ctl.o_done[0]));
           }
+          if (run && !crosses && vkt < vn0) issue_s(0, st);
+          if (run && kt <= last1) {
+            if (kt == w.kt && seen1++ > 0) run = mbar_wait_spin(bar(ctl.o_free[1]), seen1 & 1, abort_flag, a.status);
+            if (run) wait_p1();
+            if (!run) break;
+            issue_pv(1, st, kt == w.kt);
+            if (kt == last1) mma_commit(bar(ctl.o_done[1]));
+          }
+          if (run && !crosses && vkt < vn1) issue_s(1, st);
           if (!run) break;
           if (crosses && more) {
             run = mbar_wait_spin(bar(ctl.q_full), vpiece & 1, abort_flag, a.status);
             fence_after_sync();
             if (!run) break;
-            for (int x = 0; x < 2; ++x)
-              if (vkt < vn[x]) issue_s(x, sK(st));
+            if (vkt < vn0) issue_s(0, st);
+            if (vkt < vn1) issue_s(1, st);
           }
           if (more && vkt + 1 == v.end) mma_commit(bar(ctl.q_empty));
-          mma_commit(bar(ctl.empty[st]));
+          next_stage();
         }
       }
       mma_commit(bar(ctl.drain));
@@ -405,7 +444,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const int ti = r / rows.gs, g = r - ti * rows.gs;  // token within the tile, head within the group
     bool run = true;
     uint32_t cnt = 0, pieces = 0;
-    for (int piece = 0; !w.done(); ++piece, w.next()) {
+    int t0 = 0;  // position of the piece's first tile in the ring
+    if (x == 0) ctl.p0_last[r] = -1;
+    for (int piece = 0; !w.done(); ++piece, t0 += w.end - w.kt, w.next()) {
       const SeqInfo& seq = w.seq;
       const int first = (2 * w.u + x) * rows.tpt;  // the tile's first token
       if (first >= seq.Lq) continue;
@@ -421,7 +462,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int lim = min(seq.Lk - k0, s.causal ? i + seq.off - k0 + 1 : 128);  // keys [k0, k0 + lim) visible
         softmax_tile<D, false, 1>(tS, tO, tS, masked, lim, sl2, kt == w.kt, m, l, [] {});
         fence_before_sync();
-        if (run) mbar_arrive(bar(ctl.p_ready[x]));
+        if (run) {
+          const int t = t0 + kt - w.kt;
+          mbar_arrive(x == 0 ? bar(ctl.full[t % C::kStages]) : bar(ctl.p_ready));
+          if (x == 0) ctl.p0_last[r] = t;
+        }
       }
       const bool any = w.kt < end;
       if (any) {
@@ -486,8 +531,18 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (ctl.issued_q > 0) mbar_wait_drain(bar(ctl.q_full), (ctl.issued_q - 1) & 1);
     if (ctl.issued_k0 > 0) mbar_wait_drain(bar(ctl.k0_full), 0);
     if (ctl.issued_tail > 0) mbar_wait_drain(bar(ctl.tail), (ctl.issued_tail - 1) & 1);
-    for (int t = max(0, ctl.issued_t - C::kStages); t < ctl.issued_t; ++t)
-      mbar_wait_drain(bar(ctl.full[t % C::kStages]), (t / C::kStages) & 1);
+    for (int t = max(0, ctl.issued_t - C::kStages); t < ctl.issued_t; ++t) {
+      // The arrivals of tile 0's softmax that never came are made here: a thread that stopped earlier
+      // arrived on no later stage.
+      const int st = t % C::kStages;
+      if (mbar_test(bar(ctl.full[st]), (t / C::kStages) & 1)) continue;
+      if (ctl.needs_p0[st]) {
+        int arrived = 0;
+        for (int i = 0; i < 128; ++i) arrived += ctl.p0_last[i] >= t;
+        if (arrived < 128) mbar_arrive_cnt(bar(ctl.full[st]), 128 - arrived);
+      }
+      mbar_wait_drain(bar(ctl.full[st]), (t / C::kStages) & 1);
+    }
   }
 }
 

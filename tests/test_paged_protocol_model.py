@@ -189,11 +189,13 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
     for n in ("qf", "qe", "k0f", "k0e", "tail"):
         M.bar(n, 1)
     for i in range(stages):
-        M.bar(f"f{i}", 1), M.bar(f"e{i}", 1)
+        M.bar(f"f{i}", 2), M.bar(f"e{i}", 1)  # f: the copies, and P of tile 0 (128 threads, modelled as one arrival)
+    M.bar("p1", 1)
     for x in (0, 1):
-        for n in ("sf", "p", "od", "of"):
+        for n in ("sf", "od", "of"):
             M.bar(f"{n}{x}", 1)
     count = {"q": 0, "k0": 0, "t": 0, "tail": 0}
+    needs_p0, p0_last = {}, [-1]
 
     def producer():
         run = True
@@ -229,6 +231,9 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                     need(t + 1 < stages or not sees(x, t - stages + 1) or (f"S{x}", t - stages + 1) in done,
                          f"K {t + 1} too early")
                 count["t"] = t + 1
+                needs_p0[b] = sees(0, t)
+                if not sees(0, t):
+                    M.B[f"f{b}"].arrive()  # stands in for tile 0's softmax
                 if not (last and pieces[p][3]):
                     M.expect(f"f{b}", 2 if more else 1)
                     M.copy(f"f{b}", 1, ("V", t))
@@ -253,7 +258,7 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
     def issuer():
         if not T:
             return
-        np, seen = [0, 0], [0, 0]
+        np1, seen = 0, [0, 0]
 
         def issue_s(x, t):
             need(("Q", T[t][0]) in done and ("K", t) in done, f"S{x}({t}) before its operands")
@@ -282,9 +287,9 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                         if seen[x] > 0:
                             run = yield from M.wait(f"of{x}", (seen[x] - 1) & 1)
                         seen[x] += 1
-                    if run:
-                        run = yield from M.wait(f"p{x}", np[x] & 1)
-                    np[x] += 1
+                    if run and x == 1:
+                        run = yield from M.wait("p1", np1 & 1)
+                        np1 += 1
                     if not run:
                         break
                     # (after an abort the stage is completed as it is; the product then runs on stale data)
@@ -323,7 +328,9 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                 yield None
                 if run:
                     done.add((f"P{x}", t))
-                    M.B[f"p{x}"].arrive()
+                    M.B[f"f{t % stages}" if x == 0 else "p1"].arrive()
+                    if x == 0:
+                        p0_last[0] = t
             if mine:
                 if run:
                     run = yield from M.wait(f"od{x}", n & 1)
@@ -336,6 +343,9 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
         out = [("qf", (count["q"] - 1) & 1)] if count["q"] else []
         out += [("k0f", 0)] if count["k0"] else []
         out += [("tail", (count["tail"] - 1) & 1)] if count["tail"] else []
+        for t in range(max(0, count["t"] - stages), count["t"]):
+            if not M.B[f"f{t % stages}"].passes((t // stages) & 1) and needs_p0[t % stages] and p0_last[0] < t:
+                M.B[f"f{t % stages}"].arrive()  # the softmax arrival that never came
         return out + last_phases("f", count["t"], stages)
     return finish(M, {"prod": producer(), "mma": issuer(), "s0": softmax(0), "s1": softmax(1)}, issued)
 
