@@ -51,7 +51,8 @@ struct ChCtl {
 };
 
 struct JoinDesc {
-  int b, hv, u, first_cta, first_slot, pad[3];
+  int b, hv, u, first_cta, first_slot;
+  int Lq, q0, bb;  // of the sequence
 };
 
 struct ChWork {
@@ -60,8 +61,8 @@ struct ChWork {
   JoinDesc* desc;   // [CTAs]; b = -1: no unit ends here in pieces
 };
 
-// A unit's copies of Q and its epilogue take the time of about two key tiles.
-constexpr int kChOpen = 2;
+// A unit's copies of Q and its epilogue take the time of about four key tiles.
+constexpr int kChOpen = 4;
 
 // The units of one sequence, for one head group: unit u has tokens [u U, u U + U).
 struct Units {
@@ -212,6 +213,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
     d.u = w.u;
     d.first_cta = ctl.share.first_cta;
     d.first_slot = ctl.share.first_slot;
+    d.Lq = w.seq.Lq;
+    d.q0 = w.seq.q0;
+    d.bb = w.seq.bb;
     wk.desc[blockIdx.x] = d;
   }
 
@@ -546,21 +550,60 @@ __global__ void __launch_bounds__(kChThreads, 1)
   }
 }
 
-// Joins the pieces of each divided unit by their log-sum-exp. Block (c, y) takes 32 rows of the unit
-// that ends in CTA c's first piece, if it began before.
+// Joins the pieces of each divided unit by their log-sum-exp: M = max LSE, w = 2^(LSE - M),
+// O = sum w O / sum w, LSE = M + log2 sum w. Block (c, y) takes 32 rows of the unit that ends in CTA c's first
+// piece, if it began before; a thread takes four elements of several rows, whose loads are in flight
+// together.
 template <int D>
 __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs a, const PagedRows rows,
                                                                const ChWork wk) {
   grid_dependency_wait();
   const JoinDesc d = wk.desc[blockIdx.x];
   if (d.b < 0) return;
+  constexpr int kPer = 32 * (D / 4) / 256, kStep = 256 / (D / 4);  // rows of a thread, and between them
   const PagedShape& s = a.s;
-  const SeqInfo seq = paged_seq(s, d.b);
-  for (int y = threadIdx.x; y < 32 * (D / 4); y += 256) {
-    const int r = blockIdx.y * 32 + y / (D / 4), e = y % (D / 4) * 4;
-    const int rr = r & 127, i = (2 * d.u + (r >> 7)) * rows.tpt + rr / rows.gs, h = d.hv * rows.gs + rr % rows.gs;
+  SeqInfo seq{};
+  seq.Lq = d.Lq;
+  seq.q0 = d.q0;
+  seq.bb = d.bb;
+  const int r0 = blockIdx.y * 32 + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4, c1 = blockIdx.x;
+  float4 acc[kPer];
+  float M[kPer], sum[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    M[k] = -INFINITY;
+    sum[k] = 0.f;
+  }
+  for (int c = d.first_cta; c <= c1; ++c) {
+    const size_t slot = (size_t)(c == d.first_cta ? d.first_slot : 2 * c) * 256 + r0;
+    float l[kPer];
+    float4 o[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {  // (rows that do not exist hold anything; they are not written)
+      l[k] = wk.part_lse[slot + k * kStep];
+      o[k] = *reinterpret_cast<const float4*>(wk.part_o + (slot + k * kStep) * D + e);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (l[k] == -INFINITY) continue;
+      const float top = fmaxf(M[k], l[k]), old = exp2f(M[k] - top), w = exp2f(l[k] - top);
+      M[k] = top;
+      sum[k] = sum[k] * old + w;
+      acc[k] = make_float4(acc[k].x * old + w * o[k].x, acc[k].y * old + w * o[k].y, acc[k].z * old + w * o[k].z,
+                           acc[k].w * old + w * o[k].w);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int r = r0 + k * kStep, rr = r & 127;
+    const int i = (2 * d.u + (r >> 7)) * rows.tpt + rr / rows.gs, h = d.hv * rows.gs + rr % rows.gs;
     if (rr >= rows.gs * rows.tpt || i >= seq.Lq) continue;
-    join_pieces<D, 256>(a, wk.part_o, wk.part_lse, d.first_cta, blockIdx.x, d.first_slot, r, e, seq, d.b, i, h);
+    const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
+        make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (e == 0)
+      a.lse[paged_row(s, seq, d.b, h, i)] = sum[k] > 0.f ? (M[k] + log2f(sum[k])) * kLn2 : -INFINITY;
   }
 }
 
