@@ -90,13 +90,17 @@ def build_withhold_kv_test_lib() -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
     extra = ["-DFA_TEST_WITHHOLD_KV"]
-    objs = []
-    for src in _sources():
+
+    def compile_one(src):
         obj = os.path.join(OUT_DIR, "withhold_" + os.path.basename(src)[:-3] + ".o")
         r = subprocess.run([cc] + _flags(extra) + ["-c", src, "-o", obj], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        objs.append(obj)
+        return obj
+
+    srcs = _sources()
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+        objs = list(ex.map(compile_one, srcs))
     r = subprocess.run([cc] + ARCH + ["-shared", "-o", TEST_WITHHOLD_LIB] + objs, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

@@ -275,6 +275,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (run && t >= C::kStages)
             run = mbar_wait(bar(ctl.empty[st]), (t / C::kStages - 1) & 1, abort_flag, a.status);
           run = __all_sync(0xffffffffu, run) && !*abort_flag;
+#ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for a stage must run out cleanly
+          run = false;
+#endif
           if (!run) continue;
           const int valid = w.seq.Lk - (kt << 7);
           const int vbytes = pages_in(w, kt) * prows * D * 2, kbytes = more ? pages_in(v, vkt) * prows * D * 2 : 0;

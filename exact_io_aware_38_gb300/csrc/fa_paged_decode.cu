@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
           if (run && u > 0)
             run = mbar_wait(x ? bar(ctl.v_empty[st]) : bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
           run = __all_sync(0xffffffffu, run) && !*abort_flag;
+#ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for keys and values must run out cleanly
+          run = false;
+#endif
           if (!run) continue;
           if (lane == 0) {
             mbar_expect_tx(full, pages * rows * D * 2);

@@ -305,6 +305,9 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       if (C::kFew && w.head) copy_q(0, w.hk * rows.gs);
       const int st = kn % C::kKBufs, u = kn / C::kKBufs;
       if (run && u > 0) run = mbar_wait(bar(ctl.k_empty[st]), (u - 1) & 1, abort_flag, a.status);
+#ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for a key tile must run out cleanly
+      run = false;
+#endif
       if (go()) {
         const int pages = min(per, (w.x.q.Lk - (w.kt << 7) + prows - 1) >> shift);
         if (lane == 0) {

@@ -184,6 +184,44 @@ def test_attend_strided_cache_and_rows(d, layout, n):
     p.check_attend(o, lse, True)
 
 
+@pytest.mark.parametrize("n", [1, 3, 50])
+@pytest.mark.parametrize("heads", [(96, 1, 64), (131, 1, 64), (128, 1, 128), (65, 1, 128), (96, 2, 64)])
+def test_many_heads_per_kv_head(heads, n):
+    """Groups of heads past what one tile's rows take whole: divided groups, a prime count, one token a tile."""
+    p = Problem([300, 77], [n, n], *heads, page=32, seed=14)
+    o, lse = p.attend(True)
+    p.check_attend(o, lse, True)
+    check_weights(p, True)
+
+
+def test_page_sizes_at_both_ends():
+    for page, lk in ((8, [1000, 9]), (65536, [700, 0]), (1024, [1025, 1024])):
+        for n in (1, 33):
+            p = Problem(lk, [n, n], 4, 2, 64, page=page, seed=15, extra_pages=0 if page > 10_000 else 2)
+            o, lse = p.attend(True)
+            p.check_attend(o, lse, True)
+            check_weights(p, True)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_interleaved_cache_and_fused_projection(n):
+    """K and V as halves of one pool, q, k and v as slices of one projection: no tensor is contiguous."""
+    H, Hkv, d, P = 6, 2, 128, 16
+    p = Problem([90, 200], [n, n], H, Hkv, d, page=P, seed=16)
+    pool = torch.empty((p.pages, 2, P, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    pool[:, 0], pool[:, 1] = p.ck, p.cv
+    p.ck, p.cv = pool[:, 0], pool[:, 1]
+    fused = torch.full((2, n, H + 2 * Hkv, d), NAN, dtype=torch.bfloat16, device="cuda")
+    fused[:, :, :H], fused[:, :, H:H + Hkv], fused[:, :, H + Hkv:] = p.cq, p.k_new.cuda(), p.v_new.cuda()
+    p.cq = fused[:, :, :H]
+    fa.paged_append(fused[:, :, H:H + Hkv], fused[:, :, H + Hkv:], p.ck, p.cv, p.ctable, p.clen)
+    k, v = p.np(p.k), p.np(p.v)
+    paged.append(p.np(p.k_new), p.np(p.v_new), k, v, p.table.numpy(), p.lk)
+    assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cv), v, equal_nan=True)
+    p.k, p.v = torch.tensor(k), torch.tensor(v)
+    p.check_attend(*p.attend(True), True)
+
+
 def test_attend_extreme_scores():
     """Scores far apart in every direction: a row max that grows late and by a lot, one that never does, and keys that
     outweigh all others; a softmax is one-hot there, so O is one value row."""
@@ -315,6 +353,26 @@ def test_key_weights_of_many_rows_and_of_the_last_rows_only():
     fa.paged_key_weights(p.cq, p.ck, p.ctable, p.clen, lse[:, :, -16:].contiguous(), w, causal=True, scale=p.scale)
     live = torch.isfinite(w)
     assert torch.allclose(w[live], p.cw[live], rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("n", [3, 90])
+def test_key_weights_of_rows_without_weight(n):
+    """Rows of LSE = -inf add nothing, whatever their q holds (a padded batch)."""
+    p = Problem([300, 120], [n, n], 4, 2, 128, page=16, seed=61)
+    _, lse = p.attend(True)
+    dead = torch.zeros(2, n, dtype=torch.bool)
+    dead[0, n // 2:], dead[1, 0] = True, True
+    q = p.cq.clone()
+    q[dead.cuda()] = NAN
+    lse = lse.masked_fill(dead.cuda()[:, None], -math.inf)
+    got = fa.paged_key_weights(q, p.ck, p.ctable, p.clen, lse, p.cw, causal=True, scale=p.scale)
+    add = paged.key_weights(p.np(p.q), p.np(p.k), p.table.numpy(), p.lk, list(p.np(lse)), p.scale, True)
+    rel = p.score_error() + 2.0**-20 + 2.0**-16
+    for b, L in enumerate(p.lk):
+        j = torch.arange(L)
+        at = (p.table[b][j // 16].long(), slice(None), j % 16)
+        w, w0 = p.np(got)[at], p.np(p.w)[at]
+        assert (np.abs(w - w0 - add[b].T) <= rel * add[b].T + 2.0**-23 * w).all()
 
 
 # ----------------------------------------------------------------------------- append and evict
@@ -493,6 +551,36 @@ def test_captured_and_replayed_step_follows_the_lengths():
             eager = eager or now
             for x, y in zip(now, eager):
                 assert torch.equal(torch.nan_to_num(x.float(), 9.0), torch.nan_to_num(y.float(), 9.0))
+
+
+def test_two_streams_at_once():
+    """Calls of every kind on two streams without order between them, each with its own cache and workspace."""
+    problems = [Problem([900, 300], [n, n], 8, 2, 128, page=16, seed=96 + n) for n in (1, 60)]
+    refs, outs = [], []
+    for p in problems:
+        p.cw0, p.ck0, p.cv0 = p.cw.clone(), p.ck.clone(), p.cv.clone()
+
+    def work(p):
+        o, lse = fa.fwd_paged(p.cq, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale)
+        fa.paged_key_weights(p.cq, p.ck, p.ctable, p.clen, lse, p.cw, causal=True, scale=p.scale)
+        kept, _ = fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, p.clen, 200, recent=20)
+        return o, lse, kept, p.ck.clone(), p.cv.clone(), p.cw.clone()
+
+    for p in problems:
+        refs.append(work(p))
+        p.cw.copy_(p.cw0), p.ck.copy_(p.ck0), p.cv.copy_(p.cv0)
+    torch.cuda.synchronize()
+    for p in problems:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                p.cw.copy_(p.cw0), p.ck.copy_(p.ck0), p.cv.copy_(p.cv0)
+                last = work(p)
+            outs.append(last)
+    torch.cuda.synchronize()
+    for ref, out in zip(refs, outs):
+        for x, y in zip(ref, out):
+            assert torch.equal(torch.nan_to_num(x.float(), 9.0), torch.nan_to_num(y.float(), 9.0))
 
 
 def test_other_streams_and_back_to_back_calls():
