@@ -19,6 +19,13 @@ struct PagedShape {
   const int32_t* seqlens;  // [B]
 };
 
+// The kernels of this family are programmatic dependents of one another. Each lets its own dependent be
+// scheduled as soon as all its CTAs run, sets up what is not in global memory, and then waits for the kernel
+// before it; the dependent does the same, so one kernel's set-up lies under the other's end. The order of
+// memory stays that of the stream: nothing is read or written before the wait, and a kernel that the
+// predecessor waited for is complete when the predecessor is.
+__device__ __forceinline__ void let_dependent_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // One sequence of the batch: its new rows, its keys and the causal offset (key j visible to row i iff
 // j <= i + off). Everything is clamped to the tensors' extents, so no array in device memory can make
 // a kernel index outside them.

@@ -8,6 +8,7 @@ namespace {
 // Append: one warp per new token and tensor (K, V), 16 bytes a lane and up to four of them in flight.
 // Bound by memory: the rows are read and written once.
 __global__ void __launch_bounds__(256) paged_append_kernel(const FaPagedArgs a) {
+  let_dependent_start();
   grid_dependency_wait();
   const PagedShape& s = a.s;
   const int lane = threadIdx.x & 31, shift = s.d == 128 ? 4 : 3;  // 16-byte chunks of a head's row
@@ -118,6 +119,7 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_tot, int& total) {
 // Bound by latency: counting against bounds instead, 16 steps of 2 bits, took 13 us for 1030 keys.
 template <int R>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPagedArgs a) {
+  let_dependent_start();
   grid_dependency_wait();
   __shared__ int hist[2][256];
   __shared__ int warp_tot[kSelWarps];
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPaged
 constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveRows = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {  // per: rows a CTA takes of a block
+  let_dependent_start();
   grid_dependency_wait();
   extern __shared__ __align__(16) uint8_t rows_smem[];
   __shared__ const __nv_bfloat16* from[256];  // of a row of the block; null: it keeps its place

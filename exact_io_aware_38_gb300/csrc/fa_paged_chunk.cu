@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
                        const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const PagedRows rows,
                        const ChWork wk) {
   using C = ChCfg<D>;
-  grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   __shared__ ChCtl ctl;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;  // two tiles
@@ -199,12 +198,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
                  : "memory");
   }
   fence_proxy_async_smem();
+  __syncthreads();
+  let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
+  grid_dependency_wait();
   find_share<kChThreads>(s.B, [&](int b) { return Units(s, rows, b); }, ctl.share, ctl.scan);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  asm volatile("griddepcontrol.launch_dependents;");
   ChPieces w(s, rows, ctl.share);
   if (threadIdx.x == 0) {
     JoinDesc d{};
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
 // Joins the pieces of each divided unit by their log-sum-exp: M = max LSE, w = 2^(LSE - M),
 // O = sum w O / sum w, LSE = M + log2 sum w. Block (c, y) takes 32 rows of the unit that ends in CTA c's first
 // piece, if it began before; a thread takes four elements of several rows, whose loads are in flight
-// together.
+// together. (Letting its own dependent start early cost 4% of a mixed batch: this grid is several waves.)
 template <int D>
 __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs a, const PagedRows rows,
                                                                const ChWork wk) {

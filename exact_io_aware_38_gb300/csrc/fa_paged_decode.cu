@@ -173,8 +173,8 @@ __device__ __forceinline__ bool vote_any(bool x) {
 struct DecWork {
   float* part_o;    // [2 CTAs][NP][D]
   float* part_lse;  // [2 CTAs][NP], log2 units
-  int4* desc;       // [CTAs]: {b, hk, first CTA, its slot}; b = -1: no (sequence, head) ends here in pieces. Null:
-                    // every (sequence, head) has a CTA of its own
+  int4* desc;       // [CTAs][2]: {b, hk, first CTA, its slot}, {L_q, q0, bb, 0} of the sequence; b = -1: no (sequence,
+                    // head) ends here in pieces. Null: every (sequence, head) has a CTA of its own
 };
 
 template <int D, int NP>
@@ -182,7 +182,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const DecWork wk) {
   using C = DecCfg<D, NP>;
-  grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) DecCtl<NP> ctl;
   const uint32_t sK0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -231,6 +230,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
                  : "memory");
   }
   fence_proxy_async_smem();
+  __syncthreads();
+  let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
+  grid_dependency_wait();
   if (wk.desc != nullptr) {
     find_share<kDecThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
   } else if (threadIdx.x == 0) {  // a unit per CTA
@@ -241,12 +243,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  // Only the merge waits for this grid; its blocks may be scheduled as SMs drain.
-  asm volatile("griddepcontrol.launch_dependents;");
   Pieces w(s, ctl.share);
   if (wk.desc != nullptr && threadIdx.x == 0) {
     const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
-    wk.desc[blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);
+    wk.desc[2 * blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);
+    wk.desc[2 * blockIdx.x + 1] = make_int4(w.seq.Lq, w.seq.q0, w.seq.bb, 0);
   }
 
   if (warp == 0) {
@@ -573,11 +574,15 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
 // piece, if it began before.
 template <int D, int NP>
 __global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, const DecWork wk) {
+  let_dependent_start();
   grid_dependency_wait();
-  const int4 d = wk.desc[blockIdx.x];
+  const int4 d = wk.desc[2 * blockIdx.x], of = wk.desc[2 * blockIdx.x + 1];
   if (d.x < 0) return;
   const PagedShape& s = a.s;
-  const SeqInfo seq = paged_seq(s, d.x);
+  SeqInfo seq{};
+  seq.Lq = of.x;
+  seq.q0 = of.y;
+  seq.bb = of.z;
   const int G = s.H / s.Hkv, c1 = blockIdx.x;
   for (int x = threadIdx.x; x < seq.Lq * G * (D / 4); x += 256) {
     const int n = x / (D / 4), e = x % (D / 4) * 4;
@@ -614,7 +619,7 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
   if (!whole) {
     char* ws = static_cast<char*>(a.workspace);
     wk.desc = reinterpret_cast<int4*>(ws);
-    ws += up256((size_t)ctas * sizeof(int4));
+    ws += up256((size_t)ctas * 2 * sizeof(int4));
     wk.part_lse = reinterpret_cast<float*>(ws);
     ws += up256((size_t)ctas * 2 * NP * sizeof(float));
     wk.part_o = reinterpret_cast<float*>(ws);
@@ -636,7 +641,7 @@ size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms) {
   if (fa::undivided(s, num_sms)) return 0;
   const int np = fa::padded_rows(s.Nq * (s.H / s.Hkv));
   const size_t ctas = (size_t)num_sms * fa::dec_ctas(s.d, np), rows = ctas * 2 * np;
-  return fa::up256(ctas * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
+  return fa::up256(ctas * 2 * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
 }
 
 cudaError_t fa_launch_paged_decode(const FaPagedArgs& a, cudaStream_t st) {

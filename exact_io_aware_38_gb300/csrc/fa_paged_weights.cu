@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     paged_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const FaPagedArgs a, const PagedRows rows, const WWork wk) {
   using C = WCfg<D, NP>;
-  grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   __shared__ WCtl<NP> ctl;
   const uint32_t sK = (smem_u32(smem_raw) + 1023u) & ~1023u, sQ = sK + C::kKBufs * C::kKBytes;
@@ -258,12 +257,14 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
                  : "memory");
   }
   fence_proxy_async_smem();
+  __syncthreads();
+  let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
+  grid_dependency_wait();
   find_share<C::kThreads>(s.B, [&](int b) { return WUnits(s, rows, b, C::kOpen); }, ctl.share, ctl.scan);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  asm volatile("griddepcontrol.launch_dependents;");
   WPieces<C::kFew> w(s, rows, ctl.share, C::kOpen);
   if (!C::kFew && threadIdx.x == 0) {
     WJoin d{};
@@ -535,6 +536,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
 
 // Adds the pieces of each divided unit, in their order: block c the one that ends in CTA c's first piece.
 __global__ void __launch_bounds__(128) paged_weights_join_kernel(const FaPagedArgs a, const WWork wk) {
+  let_dependent_start();
   grid_dependency_wait();
   const WJoin d = wk.desc[blockIdx.x];
   if (d.b < 0) return;
