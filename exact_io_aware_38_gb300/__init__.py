@@ -27,6 +27,7 @@ Tensor helpers (grouped-query attention when k, v have fewer heads than q):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -633,7 +634,7 @@ def _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_
         raise ValueError("cu_seqlens_q without new tokens")
     bound = width * page_size if max_seqlen_k is None else int(max_seqlen_k)
     return PagedProblem(B, H, Hkv, d, page_size, pages, width, page_table.data_ptr(), seqlens_k.data_ptr(), Nq,
-                        min(bound, 2**31 - 1), cu_seqlens_q.data_ptr() if packed else None, rows_q, int(causal),
+                        min(bound, 2**31 - 1 if max_seqlen_k is not None else 2**31 - 2**18), cu_seqlens_q.data_ptr() if packed else None, rows_q, int(causal),
                         1.0 / math.sqrt(d) if scale is None else float(scale)), 3 if packed else 4
 
 
@@ -648,14 +649,33 @@ def _num_sms(dev):
     return n
 
 
-def _launch(dev, stream, call, *args):
-    """call(*args, stream handle) with the tensors' device current, on the given stream or that device's current
-    one; raises FaError for an error code."""
+def _on_stream(f):
+    """Runs a helper on its `stream` argument (a torch stream or a handle) as the current stream, so that what it
+    allocates belongs to that stream too: a workspace goes back to the pool when the helper returns."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        dev = (args[0] if args else next(iter(kw.values()))).device
+        if dev.type != "cuda":
+            raise ValueError(f"the tensors must be on a CUDA device, not {dev}")
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+def _launch(dev, call, *args):
+    """call(*args, stream handle) on the current stream of the tensors' device, with that device current; raises
+    FaError for an error code."""
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            rc = call(*args, _stream(stream))
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != 0:
         raise FaError(rc)
 
@@ -678,6 +698,7 @@ def _check_weights(key_weights, p, dev):
         raise ValueError(f"key_weights must be a contiguous float32 {list(shape)} tensor on {dev}")
 
 
+@_on_stream
 def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, max_seqlen_k=None, *,
               num_sms=None, causal=False, scale=None, out=None, lse=None, workspace=None, status=None, stream=None):
     """O, LSE of new tokens over a paged cache (fa_fwd_paged). q: [B, N, H, d] views, or packed [rows, H, d] with
@@ -707,11 +728,12 @@ def fwd_paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max
         num_sms = _num_sms(dev)
     L, at = lib(), ctypes.byref(p)
     ws, nbytes, _keep = _scratch(workspace, L.fa_fwd_paged_workspace_bytes(at, num_sms), dev)
-    _launch(dev, stream, L.fa_fwd_paged, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv,
+    _launch(dev, L.fa_fwd_paged, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv,
             out.data_ptr(), so, lse.data_ptr(), ws, nbytes, _ptr(status))
     return out, lse
 
 
+@_on_stream
 def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, *,
                  key_weights=None, status=None, stream=None):
     """Write new keys and values k, v ([B, N, Hkv, d], or packed [rows, Hkv, d] with cu_seqlens_q and max_seqlen_q)
@@ -726,10 +748,11 @@ def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=Non
     skn, svn = _paged_views("k", k, "v", v, dims)
     sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4)
     if p.B > 0 and k.numel() > 0:
-        _launch(k.device, stream, lib().fa_paged_append, ctypes.byref(p), k.data_ptr(), skn, v.data_ptr(), svn,
+        _launch(k.device, lib().fa_paged_append, ctypes.byref(p), k.data_ptr(), skn, v.data_ptr(), svn,
                 k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, _ptr(key_weights), _ptr(status))
 
 
+@_on_stream
 def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_seqlens_q=None, max_seqlen_q=None,
                       max_seqlen_k=None, *, num_sms=None, causal=False, scale=None, workspace=None, status=None,
                       stream=None):
@@ -748,11 +771,12 @@ def paged_key_weights(q, k_cache, page_table, seqlens_k, lse, key_weights, cu_se
         num_sms = _num_sms(dev)
     L, at = lib(), ctypes.byref(p)
     ws, nbytes, _keep = _scratch(workspace, L.fa_paged_key_weights_workspace_bytes(at, num_sms), dev)
-    _launch(dev, stream, L.fa_paged_key_weights, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(),
+    _launch(dev, L.fa_paged_key_weights, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, lse.data_ptr(),
             key_weights.data_ptr(), ws, nbytes, _ptr(status))
     return key_weights
 
 
+@_on_stream
 def paged_evict(k_cache, v_cache, key_weights, page_table, seqlens_k, keep, *, recent=0, max_seqlen_k=None, kept=None,
                 seqlens_out=None, status=None, stream=None):
     """Cut every sequence longer than `keep` down to its last `recent` keys and the older ones of the largest weight,
@@ -775,7 +799,7 @@ def paged_evict(k_cache, v_cache, key_weights, page_table, seqlens_k, keep, *, r
     _check_aux("status", status, torch.int32, 1, dev)
     sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4)
     if p.B > 0:
-        _launch(dev, stream, lib().fa_paged_evict, ctypes.byref(p), keep, recent, k_cache.data_ptr(), sk,
+        _launch(dev, lib().fa_paged_evict, ctypes.byref(p), keep, recent, k_cache.data_ptr(), sk,
                 v_cache.data_ptr(), sv, key_weights.data_ptr(), kept.data_ptr(), seqlens_out.data_ptr(), _ptr(status))
     return kept, seqlens_out
 

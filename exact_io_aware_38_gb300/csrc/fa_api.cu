@@ -290,6 +290,9 @@ int launch_partial(const fa::AttnShape& s, const fa_varlen_problem* p, int split
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Keys of all (sequence, K/V head) pairs: an index of a key, rounded up to whatever a CTA takes at a time, fits an int.
+constexpr double kMaxKeys = kMaxElems - (1 << 17);
+
 // Paged problem -> shape; FA_OK or an error code. `attend`: the call reads q (heads, scale and causal count).
 int paged_shape(const fa_paged_problem* p, bool attend, fa::PagedShape* out) {
   if (p == nullptr || p->page_table == nullptr || p->seqlens_k == nullptr) return FA_ERR_INVALID_ARG;
@@ -319,9 +322,8 @@ int paged_shape(const fa_paged_problem* p, bool attend, fa::PagedShape* out) {
   s.table = p->page_table;
   s.seqlens = p->seqlens_k;
   const double rows = s.cu_q != nullptr ? (double)s.rows_q : (double)s.B * s.Nq;
-  // Grids run over (sequence, head, token) and (sequence, K/V head, key).
   if (rows * s.H * s.d >= kMaxElems || (double)s.B * s.H * s.Nq >= kMaxElems ||
-      (double)s.B * s.Hkv * s.max_k >= kMaxElems)
+      (double)s.B * s.Hkv * s.max_k >= kMaxKeys)
     return FA_ERR_UNSUPPORTED;
   *out = s;
   return FA_OK;
@@ -750,6 +752,7 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
   int rc = paged_shape(p, false, &a.s);
   if (rc != FA_OK) return rc;
   if (keep < 1 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
+  if ((double)a.s.B * a.s.Hkv * keep >= kMaxKeys) return FA_ERR_UNSUPPORTED;
   if ((rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK) return rc;
   if (!k_cache || !v_cache || !key_weights || !kept || !seqlens_out || seqlens_out == p->seqlens_k)
     return FA_ERR_INVALID_ARG;

@@ -5,19 +5,44 @@
 namespace fa {
 namespace {
 
+// The sequence of packed row `row`: the number of sequences that end at or before it. A whole warp looks, 32
+// ends at a time, so 32 sequences take one load and 1000 take two.
+__device__ __forceinline__ int sequence_of(const PagedShape& s, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = s.B;  // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) >> 5, at = (lane + 1) * step;  // the lane's probe: sequence lo + at - 1
+    const int cnt = __popc(__ballot_sync(0xffffffffu, at <= n && __ldg(s.cu_q + lo + min(at, n)) <= row));
+    lo += cnt * step;
+    n = min(n - cnt * step, step - 1);
+  }
+  return lo;
+}
+
 // Append: one warp per new token and tensor (K, V), 16 bytes a lane and up to four of them in flight.
-// Bound by memory: the rows are read and written once.
+// Bound by memory: the rows are read and written once (134 MB of 16384 tokens in 23 us, 5.8 TB/s; a thread
+// per 16 bytes took 32 us). 64 tokens take 2.3 us, the latency of a launch and three loads in a row. Packed
+// batches take a warp per row, not per sequence and longest length, which a batch of one prompt and many
+// single tokens would leave idle.
 __global__ void __launch_bounds__(256) paged_append_kernel(const FaPagedArgs a) {
   let_dependent_start();
   grid_dependency_wait();
   const PagedShape& s = a.s;
   const int lane = threadIdx.x & 31, shift = s.d == 128 ? 4 : 3;  // 16-byte chunks of a head's row
-  const size_t w = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (w >= (size_t)s.B * s.Nq * 2) return;
+  const uint32_t w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, row = w >> 1;
   const bool is_v = w & 1;
-  const int i = (int)((w >> 1) % s.Nq), b = (int)((w >> 1) / s.Nq);
+  int b, i = 0;
+  if (s.cu_q != nullptr) {
+    if (row >= (uint32_t)s.rows_q) return;
+    b = sequence_of(s, (int)row);
+  } else {
+    b = (int)(row / (uint32_t)s.Nq);
+    i = (int)(row % (uint32_t)s.Nq);
+  }
+  if (b >= s.B) return;
   const SeqInfo seq = paged_seq(s, b);
-  if (i >= seq.Lq) return;
+  if (s.cu_q != nullptr) i = (int)row - seq.q0;
+  if (i < 0 || i >= seq.Lq) return;
   const long long j = (long long)__ldg(s.seqlens + b) - seq.Lq + i;  // the unclamped length places the token
   if (j < 0 || (j >> s.page_shift) >= s.max_pages) {
     if (lane == 0) report_status(a.status, FA_ERR_BOUNDS);
@@ -348,7 +373,8 @@ cudaError_t launch_select(const FaPagedArgs& a, unsigned ctas, cudaStream_t st) 
 }  // namespace fa
 
 cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st) {
-  const long long ctas = ((long long)a.s.B * a.s.Nq * 2 + 7) / 8;  // (below 2^30: checked with the shape)
+  const long long rows = a.s.cu_q != nullptr ? a.s.rows_q : (long long)a.s.B * a.s.Nq;
+  const long long ctas = (rows * 2 + 7) / 8;  // (threads below 2^32: rows times d are below 2^31)
   return launch_dependent(fa::paged_append_kernel, dim3((unsigned)ctas), dim3(256), 0, st, a);
 }
 

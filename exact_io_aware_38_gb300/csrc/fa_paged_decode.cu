@@ -7,8 +7,9 @@
 // softmax thread handles R numbers per tile instead of 128. P^T goes back through shared memory
 // (bf16, keys x rows) and O^T += V^T P^T accumulates in tensor memory, a head dimension per lane.
 // The exponentials are taken against a reference max per row, set by the row's first tile and raised
-// (O and the row sums rescaled) only when a score exceeds it by 2^32: exact, since fp32 and bf16 keep
-// their relative precision over that range, and one vote per tile replaces a max over 128 keys.
+// (O and the row sums rescaled) only when a score exceeds it by more than 2^8: exact, since fp32 and bf16
+// keep their relative precision over that range (a wider one would leave values near the top of bf16
+// less room in O), and one vote per tile replaces a max over 128 keys.
 //
 // Division of the work: all sequences' key tiles form one line, ordered (sequence, head, tile), which
 // the CTAs (one or two per SM, persistent) divide evenly, whatever the lengths are. A CTA's share
@@ -30,7 +31,7 @@ using namespace tc;
 
 constexpr int kDecThreads = 192;
 constexpr float kNoMax = -3.0e38f;   // reference max of a row that has seen no key
-constexpr float kRaise = 32.f;       // log2 units a score may exceed the reference by
+constexpr float kRaise = 8.f;       // log2 units a score may exceed the reference by
 
 // CTAs per SM.
 constexpr int dec_ctas(int d, int np) { return d == 64 && np < 64 ? 2 : 1; }

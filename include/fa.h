@@ -311,9 +311,14 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
  *              keys: token i of L_q is key i + L_k - L_q.
  *   weights    key_weights fp32 [num_pages][Hkv][page_size], contiguous, 16-byte aligned: one number per cached key
  *              and K/V head.
- *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result.
+ *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result. A value (not a
+ *              key) that is infinite or NaN reaches every row of its 128-key tile, also those that causally do not
+ *              see it, since a probability of 0 times it is NaN.
  *   sharing    pages may be shared by sequences for reading; a page that a call writes (fa_paged_append,
- *              fa_paged_key_weights, fa_paged_evict) belongs to one sequence of that call, else the writes race.
+ *              fa_paged_key_weights, fa_paged_evict) stands at one place of that call's table, else the writes race.
+ *   sizes      all at least 1; (sequences) x (K/V heads) x min(seqlen_k, capacity), and x keep for an eviction, stay
+ *              below 2^31 - 2^17 (a table much wider than the lengths in use needs seqlen_k).
+ *   at once    calls that may overlap (two streams, two captured graphs) each need a workspace of their own.
  * d, H and Hkv as for fa_fwd_gqa. Errors, ownership, dev_status and streams as for fa_fwd.
  */
 typedef struct {

@@ -120,7 +120,7 @@ class Problem:
 
 
 # (key lengths, new tokens): one token, lengths of 0 and 1, tile borders, more tokens than keys, odd sizes.
-FIXED = [([1], 1), ([0, 5], 1), ([127, 128, 129, 300], 1), ([777], 1), ([40, 3, 0], 5), ([300, 131], 37), ([513, 640], 130),
+FIXED = [([100, 7, 0], 200), ([1], 1), ([0, 5], 1), ([127, 128, 129, 300], 1), ([777], 1), ([40, 3, 0], 5), ([300, 131], 37), ([513, 640], 130),
          ([700], 300)]
 PACKED = [([9, 4, 131, 257, 128], [5, 0, 131, 200, 1]), ([640, 1000], [1, 333]), ([300, 2, 0, 70], [1, 5, 3, 64])]
 HEADS = [(4, 2, 128), (8, 1, 128), (2, 2, 128), (7, 1, 128), (12, 4, 64), (3, 3, 64), (10, 2, 64)]
@@ -235,6 +235,20 @@ def test_attend_extreme_scores():
             p.q = (p.q.float() * 8).to(torch.bfloat16)
             p.cq, p.ck = p.q.cuda(), p.k.cuda()
             p.check_attend(*p.attend(True), True)
+
+
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_attend_large_values_behind_growing_scores(n):
+    """Values of 2^100 and a key 2^30 times as heavy as those of the first tile behind it: O is finite and near 2^100,
+    though the sum without a common maximum is not."""
+    p = Problem([300], [n], 4, 2, 64, page=16, seed=17)
+    p.k[p.live] = 0.0
+    p.v[p.live] = 2.0**100
+    j = 200
+    p.q[:] = 1.0
+    p.k[p.table[0, j // 16], j % 16] = 30 * math.log(2) / (64 * p.scale)
+    p.cq, p.ck, p.cv = p.q.cuda(), p.k.cuda(), p.v.cuda()
+    p.check_attend(*p.attend(False), False)
 
 
 def test_attend_shared_pages_and_bound():
@@ -395,6 +409,21 @@ def test_append(heads, packed, layout):
         assert int(status.item()) == 0
         assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cv), v, equal_nan=True)
         assert np.array_equal(p.np(p.cw), w if with_weights else p.np(p.w), equal_nan=True)
+
+
+@pytest.mark.parametrize("B", [31, 33, 500, 2100])
+def test_append_of_many_packed_sequences(B):
+    """One prompt among single tokens and sequences without any, more of them than one look at their ends covers."""
+    r = np.random.default_rng(B)
+    lq = (r.random(B) < 0.6).astype(int)
+    lq[B // 3] = 300
+    lk = lq + r.integers(0, 20, B)
+    p = Problem(lk.tolist(), lq.tolist(), 2, 1, 64, page=8, packed=True, seed=72)
+    k, v, w = p.np(p.k), p.np(p.v), p.np(p.w)
+    paged.append(p.np(p.k_new), p.np(p.v_new), k, v, p.table.numpy(), lk, p.cu, w)
+    fa.paged_append(p.k_new.cuda(), p.v_new.cuda(), p.ck, p.cv, p.ctable, p.clen, key_weights=p.cw, **p.tokens)
+    assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cv), v, equal_nan=True)
+    assert np.array_equal(p.np(p.cw), w, equal_nan=True)
 
 
 def test_append_places_outside_the_table_are_reported():
@@ -589,7 +618,8 @@ def test_other_streams_and_back_to_back_calls():
     ref = p.attend(True)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    outs = [fa.fwd_paged(p.cq, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale, stream=s) for _ in range(20)]
+    outs = [fa.fwd_paged(p.cq, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale,
+                         stream=s if i % 2 else s.cuda_stream) for i in range(20)]
     with torch.cuda.stream(s):
         outs.append(fa.fwd_paged(p.cq, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale))
     torch.cuda.synchronize()

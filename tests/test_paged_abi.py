@@ -110,6 +110,15 @@ def test_evict_budget_and_alias():
     assert evict(out=A) == -1  # the lengths it reads
 
 
+def test_sizes_whose_indices_would_not_fit():
+    """Key indices and places of kept keys, rounded up to what a CTA takes at a time, stay below 2^31."""
+    wide = dict(B=1, H=1, Hkv=1, page_size=65536, max_pages=1 << 15)
+    for seqlen_k, rc in (((1 << 31) - 1, -2), ((1 << 31) - (1 << 17), -2), ((1 << 31) - (1 << 17) - 1, -1)):
+        p = problem(**wide, seqlen_k=seqlen_k)
+        assert attend(p, q=None) == weights(p, q=None) == append(p, kn=None) == evict(p, k=None) == rc
+    assert evict(problem(B=1, Hkv=1, H=1), keep=(1 << 31) - 1) == evict(problem(), keep=1 << 29) == -2
+
+
 def test_host_arrays_are_refused():
     """Arrays the kernels read must be device-accessible; this address is not (and there may be no GPU at all)."""
     import ctypes
@@ -134,3 +143,7 @@ def test_binding_refuses():
     for w in (z(4, 16, 2, dtype=torch.float32), z(4, 2, 16)):
         with pytest.raises(ValueError):
             fa.paged_evict(k, k, w, table, lens, 3)
+    for call in (lambda s: fa.fwd_paged(**good, stream=s), lambda s: fa.paged_append(k[0], k[0], k, k, table, lens, stream=s),
+                 lambda s: fa.paged_evict(k, k, z(4, 2, 16, dtype=torch.float32), table, lens, 3, stream=s)):
+        with pytest.raises(ValueError, match="CUDA"):  # a stream beside CPU tensors
+            call(0)
