@@ -87,7 +87,9 @@ inline PagedRows paged_rows_for(const PagedShape& s) {
 }
 
 // Up to 64 rows (tokens x heads of one K/V head) fit the few-row kernels: one tile of 16, 32 or 64
-// columns per K/V head.
+// columns per K/V head. Both sides at 64 rows, 8 K/V heads, d = 128: 16 sequences of 8192 keys 111 us in
+// few-row tiles and 122 in 128-row tiles, 64 of 1000 keys 76 and 100 (d = 64: 78 and 106, 59 and 80); the key
+// weights 50 and 87, 31 and 48. Four rows: 87 and 119, 51 and 99.
 inline bool paged_few_rows(const PagedShape& s) { return (long long)s.Nq * (s.H / s.Hkv) <= 64; }
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }

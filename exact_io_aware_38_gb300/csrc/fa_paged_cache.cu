@@ -380,7 +380,10 @@ cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st) {
 
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st) {
   const long long heads = (long long)a.s.B * a.s.Hkv;
-  // Registers for the candidates of the longest sequence: up to 8 rows a thread, then CTAs, then 16 rows.
+  // Registers for the candidates of the longest sequence: up to 8 rows a thread, then CTAs, then 16 rows. CTAs
+  // that need not be there cost cluster barriers (1030 keys: 4.5 us with one, 7.7 with two; 12 x 8 heads of 8192
+  // keys: 11, 15, 17 and 29 with 1, 2, 4 and 8), rows past the registers are read five times (8 heads of 16384
+  // keys: 24, 14, 12 and 12; of 65536: 123, 90, 41 and 16).
   const long long rows = ((long long)a.s.max_k + fa::kSelRow - 1) / fa::kSelRow;
   const unsigned ctas = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
   cudaError_t e = rows <= 2    ? fa::launch_select<2>(a, ctas, st)

@@ -4,7 +4,7 @@
 // What it computes: for the R = L_q G rows of a (sequence, K/V head), key tiles of 128 stream through
 // shared memory; S^T = K Q^T puts a key on each tensor-memory lane and a row on each column, so the
 // products cost N = 16, 32 or 64 columns instead of a 128-row tile that would be nearly empty, and a
-// softmax thread handles R numbers per tile instead of 128. P^T goes back through shared memory
+// softmax thread handles 16 numbers per tile instead of 128. P^T goes back through shared memory
 // (bf16, keys x rows) and O^T += V^T P^T accumulates in tensor memory, a head dimension per lane.
 // The exponentials are taken against a reference max per row, set by the row's first tile and raised
 // (O and the row sums rescaled) only when a score exceeds it by more than 2^8: exact, since fp32 and bf16
@@ -17,8 +17,8 @@
 // partials (two slots per CTA) that the merge kernel joins by their log-sum-exp; whole ones are
 // written directly.
 //
-// Roles: warp 0 reads the page table and copies (TMA, a lane per page), warp 1 issues the MMAs, warps
-// 2-5 are the softmax and the epilogue. Copies run ahead across pieces, so memory never waits for an
+// Roles: warp 0 reads the page table and copies (TMA, a lane per page), warp 1 issues the MMAs, groups of
+// four warps are the softmax and the epilogue, of 16 rows each. Copies run ahead across pieces, so memory never waits for an
 // epilogue.
 #include "fa_paged.cuh"
 #include "fa_tmap.h"
@@ -29,7 +29,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kDecThreads = 192;
 constexpr float kNoMax = -3.0e38f;   // reference max of a row that has seen no key
 constexpr float kRaise = 8.f;       // log2 units a score may exceed the reference by
 
@@ -43,6 +42,10 @@ struct DecCfg {
   // latencies of a tile (scores, exponentials, P, product) would show, so two CTAs share an SM, with
   // 80 KB each in flight. 64-row tiles take the registers of a whole SM: one CTA, 128 KB.
   static constexpr int kCtas = dec_ctas(D, NP);
+  // Groups of four softmax warps, 16 rows (columns of S^T, which are independent) each: one group for all
+  // leaves a scheduler one warp and its chain of dependent steps (64 sequences of 1000 keys, 8 K/V heads, d = 128:
+  // 64 rows 112 us with one group, 87 with two, 76 with four; 32 rows 64 and 61; d = 64: 99, 69 and 59; 54 and 41).
+  static constexpr int kGroups = NP / 16, kThreads = 64 + 128 * kGroups;
   static constexpr int kKStages = NP == 64 ? 256 / D : 3, kVStages = NP == 64 ? 256 / D : D == 64 ? 2 : 3;
   static constexpr int kQBytes = NP * D * 2;
   static constexpr int kQBufs = 2;
@@ -51,7 +54,7 @@ struct DecCfg {
   static constexpr int kPBytes = (NP == 64 ? 2 : 1) * 128 * 128;
   static constexpr int kPStep = NP == 64 ? 128 * 128 : NP * 2;
   static constexpr int kSmem = kQBufs * kQBytes + (kKStages + kVStages) * kTileBytes + kPBytes + 1024;
-  static_assert(kCtas * (kSmem + 480 + 36 * NP + 1024) <= 228 * 1024, "with the control block");
+  static_assert(kCtas * (kSmem + 576 + 36 * NP + 1024) <= 228 * 1024, "with the control block");
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : 256;  // S x 2, O x 2
   static constexpr uint32_t kIdS = idesc_bf16(128, NP, false, false);
   // O^T = V^T P^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared
@@ -69,7 +72,7 @@ struct DecCtl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[kDecThreads / 32];
+  long long scan[18];
   Share share;
   int issued_q, issued_t;                         // copies issued (abort-path drain)
   alignas(16) float m[NP];
@@ -79,7 +82,8 @@ struct DecCtl {
 };
 
 // A unit (sequence, K/V head) without keys still has a tile, which writes its zeros. Its epilogue takes
-// the time of about one tile.
+// the time of about one tile (weighed as 1, 2 or 3: 48 sequences of 1024 keys, 12 heads of d = 64, in 34.4, 34.9
+// and 35.1 us).
 constexpr int kDecOpen = 1;
 
 struct DecUnits {
@@ -134,39 +138,28 @@ struct Pieces {
   }
 };
 
-// Reduce v[0 .. N) over the 32 lanes; afterwards lane l holds, in v[0 .. max(1, N / 32)), the columns
-// column_of(l) + i. A halving exchange: N + a few shuffles instead of 5 N.
-template <int N, typename F>
-__device__ __forceinline__ void columns_reduce(float (&v)[N], int lane, F f) {
-  int cnt = N;
+// Reduce v[0 .. 16) over the 32 lanes; afterwards lane l holds column l / 2 in v[0]. A halving exchange: 16
+// shuffles instead of 80.
+template <typename F>
+__device__ __forceinline__ void columns_reduce(float (&v)[16], int lane, F f) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (cnt > 1) {
-      const int half = cnt / 2;
-      const bool up = lane & o;
+  for (int half = 8; half > 0; half >>= 1) {
+    const bool up = lane & (2 * half);
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i)
-        if (i < half) {
-          const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
-          v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
-        }
-      cnt = half;
-    } else {
-      v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    for (int i = 0; i < half; ++i) {
+      const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, 2 * half));
     }
   }
-}
-template <int N>
-__device__ __forceinline__ int column_of(int lane) {
-  return N == 16 ? lane >> 1 : N == 32 ? lane : 2 * lane;
+  v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-__device__ __forceinline__ bool vote_any(bool x) {
+__device__ __forceinline__ bool vote_any(bool x, int id) {
   uint32_t r;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(id)
       : "memory");
   return r != 0;
 }
@@ -179,7 +172,7 @@ struct DecWork {
 };
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
+__global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const DecWork wk) {
   using C = DecCfg<D, NP>;
@@ -203,8 +196,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
       mbar_init(bar(ctl.q_full[i]), 1);
       mbar_init(bar(ctl.q_empty[i]), 1);
       mbar_init(bar(ctl.s_full[i]), 1);
-      mbar_init(bar(ctl.o_free[i]), 128);
-      mbar_init(bar(ctl.p_ready[i]), 128);
+      mbar_init(bar(ctl.o_free[i]), 128 * C::kGroups);
+      mbar_init(bar(ctl.p_ready[i]), 128 * C::kGroups);
       mbar_init(bar(ctl.pv_done[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -225,7 +218,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
   }
   // Rows of Q that no copy fills (the box has Nq G rows) are zero.
   const int box = s.Nq * G;
-  for (int i = threadIdx.x; i < C::kQBufs * (D / 64) * (NP - box) * 8; i += kDecThreads) {
+  for (int i = threadIdx.x; i < C::kQBufs * (D / 64) * (NP - box) * 8; i += C::kThreads) {
     const int r = box + i / 8 % (NP - box), part = i / 8 / (NP - box);  // part: buffer and column half
     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sQ + (part * NP + r) * 128 + (i & 7) * 16), "r"(0)
                  : "memory");
@@ -235,7 +228,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
   if (wk.desc != nullptr) {
-    find_share<kDecThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
+    find_share<C::kThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
   } else if (threadIdx.x == 0) {  // a unit per CTA
     const DecUnits x(s, blockIdx.x / s.Hkv);
     ctl.share = Share{(int)blockIdx.x / s.Hkv, (int)blockIdx.x % s.Hkv, 0, 0, x.count ? x.before(1) : 0, 0, 0};
@@ -376,6 +369,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
   } else {
     // ------------------------------------------------------------------ softmax, epilogue
     const int quad = warp & 3, r = quad * 32 + lane;  // key within the tile; head dimension of O^T
+    constexpr int NC = 16;
+    const int gr = C::kGroups == 1 ? 0 : (warp - 2) >> 2, n0 = gr * NC, on = 1 + gr;  // group, first column, barrier
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const float sl2 = a.scale * kLog2e;
     bool run = true;
@@ -386,84 +381,75 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
     for (int piece = 0; !w.done(); ++piece) {
       const SeqInfo& seq = w.seq;
       const int live = seq.Lq * G;  // rows that exist
-      const uint32_t tO = tmem + lane_off + (2 + (piece & 1)) * NP;
-      if (r < NP) ctl.lim[r] = s.causal ? min(seq.Lk, r / G + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
+      const uint32_t tO = tmem + lane_off + (2 + (piece & 1)) * NP + n0;
+      if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, (n0 + r) / G + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
       const int least = s.causal ? min(seq.Lk, seq.off + 1) : seq.Lk;
-      float l[NP];
+      float l[NC];
 #pragma unroll
-      for (int n = 0; n < NP; ++n) l[n] = 0.f;
+      for (int n = 0; n < NC; ++n) l[n] = 0.f;
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
         if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
         fence_after_sync();
-        float x[NP];
+        float x[NC];
         {
-          uint32_t(&u)[NP] = reinterpret_cast<uint32_t(&)[NP]>(x);
-          if constexpr (NP == 16) {
-            tmem_ld16(tmem + lane_off + (t & 1) * NP, u);
-          } else {
-#pragma unroll
-            for (int c = 0; c < NP / 32; ++c)
-              tmem_ld32(tmem + lane_off + (t & 1) * NP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(u + c * 32));
-          }
+          tmem_ld16(tmem + lane_off + (t & 1) * NP + n0, reinterpret_cast<uint32_t(&)[NC]>(x));
           tmem_ld_wait();
         }
         const int key = (kt << 7) + r;
         const bool opens = kt == w.kt;
-        if (opens) named_bar_sync(1, 128);  // ctl.lim is written; the last piece's ctl.m is no longer read
+        if (opens) named_bar_sync(on, 128);  // ctl.lim is written; the last piece's ctl.m is no longer read
         if ((kt << 7) + 128 > least) {
 #pragma unroll
-          for (int n = 0; n < NP; ++n) x[n] = key < ctl.lim[n] ? x[n] : -INFINITY;
+          for (int n = 0; n < NC; ++n) x[n] = key < ctl.lim[n0 + n] ? x[n] : -INFINITY;
         }
         bool raise = opens;
         if (!opens) {
           bool big = false;
 #pragma unroll
-          for (int n = 0; n < NP; n += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(ctl.m + n);
+          for (int n = 0; n < NC; n += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ctl.m + n0 + n);
             big |= fmaxf(fmax3(fmaf(x[n], sl2, -m.x), fmaf(x[n + 1], sl2, -m.y), fmaf(x[n + 2], sl2, -m.z)),
                          fmaf(x[n + 3], sl2, -m.w)) > kRaise;
           }
-          raise = vote_any(big);
+          raise = vote_any(big, on);
         }
         if (raise) {
-          float y[NP];
+          float y[NC];
 #pragma unroll
-          for (int n = 0; n < NP; ++n) y[n] = x[n] * sl2;
+          for (int n = 0; n < NC; ++n) y[n] = x[n] * sl2;
           columns_reduce(y, lane, [](float p, float q) { return fmaxf(p, q); });
-#pragma unroll
-          for (int i = 0; i < (NP == 64 ? 2 : 1); ++i) ctl.wmax[quad][column_of<NP>(lane) + i] = y[i];
-          named_bar_sync(1, 128);
-          if (r < NP) {
-            const float old = opens ? kNoMax : ctl.m[r];
-            const float now = fmaxf(fmaxf(fmaxf(ctl.wmax[0][r], ctl.wmax[1][r]), fmaxf(ctl.wmax[2][r], ctl.wmax[3][r])),
+          ctl.wmax[quad][n0 + (lane >> 1)] = y[0];
+          named_bar_sync(on, 128);
+          if (r < NC) {
+            const int n = n0 + r;
+            const float old = opens ? kNoMax : ctl.m[n];
+            const float now = fmaxf(fmaxf(fmaxf(ctl.wmax[0][n], ctl.wmax[1][n]), fmaxf(ctl.wmax[2][n], ctl.wmax[3][n])),
                                     old);
-            ctl.alpha[r] = ex2_approx(old - now);
-            ctl.m[r] = now;
+            ctl.alpha[n] = ex2_approx(old - now);
+            ctl.m[n] = now;
           }
           __syncwarp();
-          named_bar_sync(1, 128);
+          named_bar_sync(on, 128);
           if (!opens) {
             if (run) run = wait_pv(t - 1);
             fence_after_sync();
+            uint32_t o[NC];
+            tmem_ld16(tO, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < NP / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tO + c * 16, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * ctl.alpha[c * 16 + i]);
-                l[c * 16 + i] *= ctl.alpha[c * 16 + i];
-              }
-              tmem_st16(tO + c * 16, o);
+            for (int i = 0; i < NC; ++i) {
+              const float alpha = ctl.alpha[n0 + i];
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              l[i] *= alpha;
             }
+            tmem_st16(tO, o);
             tmem_st_wait();
           }
         }
-        uint32_t pk[NP / 2];
+        uint32_t pk[NC / 2];
 #pragma unroll
-        for (int n = 0; n < NP; n += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(ctl.m + n);
+        for (int n = 0; n < NC; n += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(ctl.m + n0 + n);
           const float p0 = ex2_approx(fmaf(x[n], sl2, -m.x)), p1 = ex2_approx(fmaf(x[n + 1], sl2, -m.y));
           const float p2 = ex2_approx(fmaf(x[n + 2], sl2, -m.z)), p3 = ex2_approx(fmaf(x[n + 3], sl2, -m.w));
           l[n] += p0;
@@ -476,9 +462,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
         // P's buffer is free: the P V that read it, of tile t - 2, was issued before S of tile t, which has
         // completed.
         const uint32_t sPt = sP + (NP == 64 ? (t & 1) * C::kPStep : 0);
-        const int c0 = NP == 64 ? 0 : (t & 1) * (C::kPStep / 16);  // first 16-byte chunk of the row
+        const int c0 = n0 / 8 + (NP == 64 ? 0 : (t & 1) * (C::kPStep / 16));  // first 16-byte chunk of the row
 #pragma unroll
-        for (int c = 0; c < NP / 8; ++c)
+        for (int c = 0; c < NC / 8; ++c)
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sPt + r * 128 + (((c + c0) ^ (r & 7)) << 4)),
                        "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
                        : "memory");
@@ -489,7 +475,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
           if (run) run = mbar_wait(bar(ctl.v_full[st]), (t / C::kVStages) & 1, abort_flag, a.status);
           if (run && r >= valid)
 #pragma unroll
-            for (int c = 0; c < D / 64 * 8; ++c)
+            for (int c = gr * (D / 8 / C::kGroups); c < (gr + 1) * (D / 8 / C::kGroups); ++c)
               asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + (c >> 3) * 16384 + r * 128 +
                                                                           (c & 7) * 16),
                            "r"(0)
@@ -502,48 +488,45 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, NP>::kCtas)
       }
       // ---------------------------------------------------------------- end of the piece
       columns_reduce(l, lane, [](float p, float q) { return p + q; });
-#pragma unroll
-      for (int i = 0; i < (NP == 64 ? 2 : 1); ++i) ctl.wmax[quad][column_of<NP>(lane) + i] = l[i];
-      named_bar_sync(1, 128);
+      ctl.wmax[quad][n0 + (lane >> 1)] = l[0];
+      named_bar_sync(on, 128);
       const bool whole = w.whole();
       const int slot = 2 * blockIdx.x + (piece == 0 ? 0 : 1);
-      if (r < NP) {
-        const float sum = (ctl.wmax[0][r] + ctl.wmax[1][r]) + (ctl.wmax[2][r] + ctl.wmax[3][r]);
-        ctl.alpha[r] = sum > 0.f ? 1.f / sum : 0.f;
-        const float lse2 = sum > 0.f ? ctl.m[r] + log2f(sum) : -INFINITY;
+      if (r < NC) {
+        const int n = n0 + r;
+        const float sum = (ctl.wmax[0][n] + ctl.wmax[1][n]) + (ctl.wmax[2][n] + ctl.wmax[3][n]);
+        ctl.alpha[n] = sum > 0.f ? 1.f / sum : 0.f;
+        const float lse2 = sum > 0.f ? ctl.m[n] + log2f(sum) : -INFINITY;
         if (whole) {
-          if (r < live) a.lse[paged_row(s, seq, w.b, w.hk * G + r % G, r / G)] = lse2 * kLn2;
+          if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n % G, n / G)] = lse2 * kLn2;
         } else {
-          wk.part_lse[(size_t)slot * NP + r] = lse2;
+          wk.part_lse[(size_t)slot * NP + n] = lse2;
         }
       }
       __syncwarp();
-      named_bar_sync(1, 128);
+      named_bar_sync(on, 128);
       if (run) run = wait_pv(t - 1);
       fence_after_sync();
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0, w.hk * G) + r;
       float* part = wk.part_o + (size_t)slot * NP * D + r;
-      int i = 0, g = 0;  // token and head of the group of column n
+      int i = n0 / G, g = n0 % G;  // token and head of the group of column n
+      uint32_t o[NC];
+      tmem_ld16(tO, o);
+      tmem_ld_wait();
+      if (r < D) {
 #pragma unroll
-      for (int c = 0; c < NP / 16; ++c) {
-        uint32_t o[16];
-        tmem_ld16(tO + c * 16, o);
-        tmem_ld_wait();
-        if (r < D) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int n = c * 16 + k;
-            if (n < live) {
-              const float val = __uint_as_float(o[k]) * ctl.alpha[n];
-              if (whole)
-                out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
-              else
-                part[n * D] = val;
-            }
-            if (++g == G) {
-              g = 0;
-              ++i;
-            }
+        for (int k = 0; k < NC; ++k) {
+          const int n = n0 + k;
+          if (n < live) {
+            const float val = __uint_as_float(o[k]) * ctl.alpha[n];
+            if (whole)
+              out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
+            else
+              part[n * D] = val;
+          }
+          if (++g == G) {
+            g = 0;
+            ++i;
           }
         }
       }
@@ -630,7 +613,7 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (C::kCtas > 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(ctas), dim3(kDecThreads), C::kSmem, st, tq, tk, tv, a, wk);
+  e = launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tq, tk, tv, a, wk);
   if (e != cudaSuccess || whole) return e;
   return launch_dependent(paged_join_kernel<D, NP>, dim3(ctas), dim3(256), 0, st, a, wk);
 }

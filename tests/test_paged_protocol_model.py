@@ -46,13 +46,16 @@ def last_phases(name, n, bufs):
 # ----------------------------------------------------------------------------- decode
 
 
-def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False):
+def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, groups=1):
+    """groups: softmax groups, each with an equal part of every tile's rows."""
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
     T = tiles_of(pieces)
     for i in range(2):
-        for n in ("qf", "qe", "sf", "of", "pv", "p"):
+        for n in ("qf", "qe", "sf", "pv"):
             M.bar(f"{n}{i}", 1)
+        for n in ("of", "p"):
+            M.bar(f"{n}{i}", groups)
     for i in range(ks):
         M.bar(f"kf{i}", 1), M.bar(f"ke{i}", 1)
     for i in range(vs):
@@ -116,9 +119,16 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False):
                 M.commit("i", f"ve{t % vs}"), M.commit("i", f"pv{t & 1}")
             yield None
 
-    def softmax():
+    parts = {}
+
+    def part_done(what):  # the groups' parts of P(t), or of the read of a piece's O
+        parts[what] = parts.get(what, 0) + 1
+        if parts[what] == groups:
+            done.add(what)
+
+    def softmax(g):
         run = True
-        r = random.Random(seed + 1)
+        r, r2 = random.Random(seed + 1 + g), random.Random(seed + 5)
         for t, (p, k, last) in enumerate(T):
             if run:
                 run = yield from M.wait(f"sf{t & 1}", (t >> 1) & 1)
@@ -130,25 +140,25 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False):
                 need(not run or ("PV", t - 1) in done, f"O rescaled at {t} before PV({t - 1})")
             if run:  # no wait: PV(t - 2) was issued before S(t)
                 need(t < 2 or ("PV", t - 2) in done, f"P({t}) over P({t - 2}) before PV read it")
-            if last and r.random() < 0.7:  # the unit's last tile: V's rows past the last key become 0
+            if last and r2.random() < 0.7:  # the unit's last tile: V's rows past the last key become 0
                 if run:
                     run = yield from M.wait(f"vf{t % vs}", (t // vs) & 1)
                 need(not run or (("v", t) in done and ("PV", t) not in done), f"V({t}) zeroed at the wrong time")
             yield None
             if run:
-                done.add(("P", t))
+                part_done(("P", t))
                 M.B["p0" if one_p else f"p{t & 1}"].arrive()
             if last:
                 if run and not skip_pv_wait:
                     run = yield from M.wait(f"pv{t & 1}", (t >> 1) & 1)
                 need(not run or ("PV", t) in done, f"O read before PV({t})")
                 if run:
-                    done.add(("O", p))
+                    part_done(("O", p))
                     M.B[f"of{p & 1}"].arrive()
 
     def issued():
         return last_phases("qf", count["q"], 2) + last_phases("kf", count["k"], ks) + last_phases("vf", count["v"], vs)
-    return finish(M, {"prod": producer(), "mma": issuer(), "soft": softmax()}, issued)
+    return finish(M, {"prod": producer(), "mma": issuer(), **{f"soft{g}": softmax(g) for g in range(groups)}}, issued)
 
 
 def pieces_for(seed):
@@ -161,13 +171,13 @@ RINGS = [(3, 3), (3, 2), (2, 2), (4, 4)]
 
 def test_decode_has_no_deadlock_or_hazard():
     for seed in range(2500):
-        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed)
+        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, groups=(1, 2, 4)[seed % 3])
         assert res == "ok" and not errs, (pieces_for(seed), RINGS[seed % 4], seed, res, errs[:3])
 
 
 def test_decode_ends_after_waits_that_run_out():
     for seed in range(1500):
-        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, abort_p=0.02)
+        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, abort_p=0.02, groups=(1, 2, 4)[seed % 3])
         assert res == "ok" and not errs, (pieces_for(seed), RINGS[seed % 4], seed, res, errs[:3])
 
 
