@@ -113,6 +113,11 @@ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32
   return sum;
 }
 
+// a / b of numbers >= 0: 64-bit divisions take a few hundred cycles, and those here mostly fit 32 bits.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A CTA's share of the work. Units (of key tiles, or of query tiles) stand in one line, ordered by
 // sequence, head and unit; each is kOpen positions, which stand for the time a unit takes besides its
 // tiles, and then a position per tile. CTA c of n takes [total c / n, total (c + 1) / n). A share that
@@ -153,7 +158,7 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
   }
   __syncthreads();  // scan is read
   const long long n = min(total, (long long)gridDim.x), c = blockIdx.x;  // no CTA before the last busy one is idle
-  const long long lo = c < n ? total * c / n : 0, hi = c < n ? total * (c + 1) / n : 0;
+  const long long lo = c < n ? div_pos(total * c, n) : 0, hi = c < n ? div_pos(total * (c + 1), n) : 0;
   if (lo < hi && lo >= base && lo < base + mine) {  // the sequence, the line's position where it begins, its size
     int b = first;
     long long size = mine;
@@ -170,9 +175,8 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
   __syncthreads();
   if (lo >= hi) return;
   const auto x = make(sh.b);
-  const long long from = scan[0], each = scan[1] / x.heads;
-  const long long in = lo - from;
-  const int head = in >> 31 == 0 && each >> 31 == 0 ? (int)((uint32_t)in / (uint32_t)each) : (int)(in / each);
+  const long long from = scan[0], each = div_pos(scan[1], x.heads);
+  const int head = (int)div_pos(lo - from, each);
   const long long at = from + head * each;
   for (int u = threadIdx.x; u < x.count; u += kThreads) {
     const long long start = at + x.before(u);
@@ -182,9 +186,9 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
     sh.tile = (int)(lo - start);
     sh.todo = hi - lo;
     const long long tile0 = start + x.open;
-    const long long c0 = ((tile0 + 1) * n - 1) / total;
+    const long long c0 = div_pos((tile0 + 1) * n - 1, total);
     sh.first_cta = (int)c0;
-    sh.first_slot = 2 * (int)c0 + (total * c0 / n >= start ? 0 : 1);
+    sh.first_slot = 2 * (int)c0 + (div_pos(total * c0, n) >= start ? 0 : 1);
   }
   __syncthreads();
 }

@@ -12,9 +12,10 @@
 // CTA per unit instead runs in whole waves: 2048 tokens x 32 heads are 256 units on 152 SMs, 1.7
 // waves that take the time of 2.
 //
-// Roles (320 threads): warp 0 reads the page table and copies, warp 1 issues the MMAs, warps 2-5 and
-// 6-9 are the softmax of tile 0 and tile 1. Copies run ahead across units. Stage t of the ring holds
-// V of key tile t and K of key tile t + 1.
+// Roles: warp 0 and at d = 128 the last warp read the page table and copy (64 columns each: a warp issues a copy
+// per ~100 cycles, and small pages need many: 2048 tokens over 16384 keys in pages of 16 take 377 us, with one
+// warp 561), warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of tile 0 and tile 1. Copies run ahead
+// across units. Stage t of the ring holds V of key tile t and K of key tile t + 1.
 // Tensor memory: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P over S.
 #include "fa_paged.cuh"
 #include "fa_softmax.cuh"
@@ -25,13 +26,13 @@ namespace {
 
 using namespace tc;
 
-constexpr int kChThreads = 320;
-
 template <int D>
 struct ChCfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kSmem = 2 * kTileBytes + 2 * kStages * kTileBytes + 1024;
+  static constexpr int kThreads = 320 + 32 * (D / 64 - 1);
+  static constexpr int kStaging = 8 * 4096;  // the epilogue's, 32 rows of 128 bytes per warp
+  static constexpr int kSmem = 2 * kTileBytes + 2 * kStages * kTileBytes + kStaging + 1024;
   static constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
   static constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
 };
@@ -43,9 +44,9 @@ struct ChCtl {
   uint64_t p_ready, tail, drain;  // p_ready: of tile 1
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[kChThreads / 32];
+  long long scan[11];
   Share share;
-  int issued_q, issued_k0, issued_t, issued_tail;  // copies issued (abort-path drain)
+  int issued_q[2], issued_k0[2], issued_t[2], issued_tail[2];  // copies issued, by producer (abort-path drain)
   int needs_p0[4];   // by stage buffer: tile 0's softmax arrives on its last stage
   int p0_last[128];  // by row of tile 0: the last stage its thread arrived on
 };
@@ -102,14 +103,21 @@ struct ChPieces {
   SeqInfo seq;
   __device__ ChPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh)
       : s(s_), c(c_), b(sh.b), hv(sh.head), u(sh.unit), kt(0), n(0), end(0), nu(0), todo(sh.todo), finished(false) {
-    if (todo > 0) open(sh.tile);
+    if (todo == 0) return;
+    sequence();
+    open(sh.tile);
   }
-  __device__ void open(int at) {  // at: position within the unit
+  __device__ void sequence() {  // looks at sequence b
     const Units x(s, c, b);
     seq = x.q;
     nu = x.count;
-    if (nu == 0) return;
-    n = x.tiles(u);
+  }
+  __device__ int tiles_to(int last) const {  // key tiles that token `last` sees
+    const int keys = s.causal ? min(seq.Lk, last + seq.off + 1) : seq.Lk;
+    return keys <= 0 ? 0 : (keys + 127) >> 7;
+  }
+  __device__ void open(int at) {  // at: position within the unit
+    n = max(1, tiles_to(min(seq.Lq, 2 * (u + 1) * c.tpt) - 1));
     kt = max(0, at - kChOpen);
     const long long stop = at + todo - kChOpen;
     end = stop < n ? (int)stop : n;
@@ -127,26 +135,24 @@ struct ChPieces {
       u = 0;
       if (++hv == c.Hv) {
         hv = 0;
-        ++b;
+        do {  // todo > 0: a later sequence has units
+          ++b;
+          sequence();
+        } while (nu == 0);
       }
     }
     open(0);
-    while (nu == 0) {  // todo > 0: a later sequence has units
-      ++b;
-      open(0);
-    }
   }
   // Key tiles query tile x sees, and whether it exists.
   __device__ int tiles(int x) const {
     const int first = (2 * u + x) * c.tpt, last = min(seq.Lq, first + c.tpt) - 1;
     if (first >= seq.Lq) return 0;
-    const int keys = s.causal ? min(seq.Lk, last + seq.off + 1) : seq.Lk;
-    return keys <= 0 ? 0 : (keys + 127) >> 7;
+    return tiles_to(last);
   }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kChThreads, 1)
+__global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const PagedRows rows,
                        const ChWork wk) {
@@ -155,6 +161,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   __shared__ ChCtl ctl;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;  // two tiles
   const uint32_t sKV = sQ + 2 * C::kTileBytes;                // stage i: V then K
+  const uint32_t sO = sKV + 2 * C::kStages * C::kTileBytes;
   volatile int* abort_flag = &ctl.abort_flag;
   const PagedShape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -164,13 +171,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
-    ctl.issued_q = ctl.issued_k0 = ctl.issued_t = ctl.issued_tail = 0;
-    mbar_init(bar(ctl.q_full), 1);
+    for (int i = 0; i < 2; ++i) ctl.issued_q[i] = ctl.issued_k0[i] = ctl.issued_t[i] = ctl.issued_tail[i] = 0;
+    mbar_init(bar(ctl.q_full), D / 64);
     mbar_init(bar(ctl.q_empty), 1);
-    mbar_init(bar(ctl.k0_full), 1);
+    mbar_init(bar(ctl.k0_full), D / 64);
     mbar_init(bar(ctl.k0_empty), 1);
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(ctl.full[i]), 1 + 128);  // the copies, and P of tile 0 (or its stand-in)
+      mbar_init(bar(ctl.full[i]), D / 64 + 128);  // the copies, and P of tile 0 (or its stand-in)
       mbar_init(bar(ctl.empty[i]), 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       mbar_init(bar(ctl.o_free[x]), 128);
     }
     mbar_init(bar(ctl.p_ready), 128);
-    mbar_init(bar(ctl.tail), 1);
+    mbar_init(bar(ctl.tail), D / 64);
     mbar_init(bar(ctl.drain), 1);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   }
   // Rows of the query tiles that no copy fills are zero.
   const int used = rows.gs * rows.tpt;
-  for (int i = threadIdx.x; i < 2 * (D / 64) * (128 - used) * 8; i += kChThreads) {
+  for (int i = threadIdx.x; i < 2 * (D / 64) * (128 - used) * 8; i += C::kThreads) {
     const int r = used + i / 8 % (128 - used), part = i / 8 / (128 - used);
     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sQ + (part * 128 + r) * 128 + (i & 7) * 16), "r"(0)
                  : "memory");
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   __syncthreads();
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
-  find_share<kChThreads>(s.B, [&](int b) { return Units(s, rows, b); }, ctl.share, ctl.scan);
+  find_share<C::kThreads>(s.B, [&](int b) { return Units(s, rows, b); }, ctl.share, ctl.scan);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -220,8 +227,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
     wk.desc[blockIdx.x] = d;
   }
 
-  if (warp == 0) {
+  if (warp == 0 || (D > 64 && warp == C::kThreads / 32 - 1)) {
     // ------------------------------------------------------------------ copies
+    const int half = warp != 0;  // the 64 columns that this warp copies, of Q, K and V
     const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     bool run = true;
     auto page_of = [&](const ChPieces& x, int kt) -> int {
@@ -234,21 +242,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
     };
     auto copy = [&](uint32_t dst, const CUtensorMap* tm, const ChPieces& x, int kt, int page, uint32_t on) {
       if (lane < pages_in(x, kt))
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(dst + c * 16384 + lane * prows * 128, tm, c * 64, (kt << 7) & (P - 1), x.hv / rows.per_kv, page,
-                      on);
+        tma_load_4d(dst + half * 16384 + lane * prows * 128, tm, half * 64, (kt << 7) & (P - 1), x.hv / rows.per_kv,
+                    page, on);
     };
     auto copy_q = [&](const ChPieces& x, int piece) {
       if (run && piece > 0) run = mbar_wait(bar(ctl.q_empty), (piece - 1) & 1, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
       if (!run || lane > 0) return;
       const int tiles = (2 * x.u + 1) * rows.tpt < x.seq.Lq ? 2 : 1;
-      mbar_expect_tx(bar(ctl.q_full), tiles * used * D * 2);
+      mbar_expect_tx(bar(ctl.q_full), tiles * used * 128);
       for (int y = 0; y < tiles; ++y)
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sQ + y * C::kTileBytes + c * 16384, &tmQ, c * 64, x.hv * rows.gs,
-                      x.seq.q0 + (2 * x.u + y) * rows.tpt, x.seq.bb, bar(ctl.q_full));
-      ctl.issued_q = piece + 1;
+        tma_load_4d(sQ + y * C::kTileBytes + half * 16384, &tmQ, half * 64, x.hv * rows.gs,
+                    x.seq.q0 + (2 * x.u + y) * rows.tpt, x.seq.bb, bar(ctl.q_full));
+      ctl.issued_q[half] = piece + 1;
     };
     if (!w.done()) {
       ChPieces v = w;  // the piece of the next K
@@ -256,8 +262,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
       int page = page_of(w, w.kt);
       copy_q(w, 0);
       if (lane == 0) {
-        mbar_expect_tx(bar(ctl.k0_full), pages_in(w, w.kt) * prows * D * 2);
-        ctl.issued_k0 = 1;
+        mbar_expect_tx(bar(ctl.k0_full), pages_in(w, w.kt) * prows * 128);
+        ctl.issued_k0[half] = 1;
       }
       __syncwarp();
       copy(sK(C::kStages - 1), &tmK, w, w.kt, page, bar(ctl.k0_full));
@@ -281,8 +287,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #endif
           if (!run) continue;
           const int valid = w.seq.Lk - (kt << 7);
-          const int vbytes = pages_in(w, kt) * prows * D * 2, kbytes = more ? pages_in(v, vkt) * prows * D * 2 : 0;
-          if (lane == 0) {
+          const int vbytes = pages_in(w, kt) * prows * 128, kbytes = more ? pages_in(v, vkt) * prows * 128 : 0;
+          if (lane == 0 && half == 0) {
             const bool p0 = kt < w.tiles(0);
             if (!p0) mbar_arrive_cnt(bar(ctl.full[st]), 128);  // tile 0 has no P for this key tile
             ctl.needs_p0[st] = p0;
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (valid >= 128) {
             if (lane == 0) {
               mbar_expect_tx(bar(ctl.full[st]), vbytes + kbytes);
-              ctl.issued_t = t + 1;
+              ctl.issued_t[half] = t + 1;
             }
             __syncwarp();
             copy(sV(st), &tmV, w, kt, page, bar(ctl.full[st]));
@@ -301,8 +307,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (lane == 0) {
               mbar_add_tx(bar(ctl.full[st]), kbytes);
               mbar_expect_tx(bar(ctl.tail), vbytes);
-              ctl.issued_t = t + 1;
-              ctl.issued_tail = tails + 1;
+              ctl.issued_t[half] = t + 1;
+              ctl.issued_tail[half] = tails + 1;
             }
             __syncwarp();
             copy(sV(st), &tmV, w, kt, page, bar(ctl.tail));
@@ -311,13 +317,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
             run = __all_sync(0xffffffffu, run);
             ++tails;
             if (run)
-              for (int i = max(valid, 0) * (D / 8) + lane; i < 128 * (D / 8); i += 32) {
-                const int r = i / (D / 8), c = i % (D / 8);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + (c >> 3) * 16384 + r * 128 +
-                                                                            (c & 7) * 16),
-                             "r"(0)
+              for (int i = max(valid, 0) * 8 + lane; i < 128 * 8; i += 32)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + half * 16384 + i * 16), "r"(0)
                              : "memory");
-              }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ctl.full[st]));  // after a failed wait too: K may be in flight
@@ -486,34 +488,66 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const bool whole = w.whole();
       const size_t slot = (size_t)(2 * blockIdx.x + (piece == 0 ? 0 : 1)) * 256 + x * 128 + r;
       const int h = w.hv * rows.gs + g;
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h);
-      float* part = wk.part_o + slot * D;
+      // A thread has a row of O; written as it lies, every store would touch 32 lines (5000 to 11000 cycles a
+      // piece). So 128 bytes of each of the warp's rows at a time cross through shared memory (chunks of 16
+      // bytes in an order that keeps the banks apart) and leave as whole lines.
+      const uint32_t stage = sO + (warp - 2) * 4096;
+      const long long at = live ? (long long)elem_offset(a.so, seq.bb, seq.q0 + i, h) : -1;
+      float* part = wk.part_o + (slot - lane) * D;  // (a row that does not exist leaves something there, which is not read)
+      auto write_lines = [&](const uint32_t (&y)[32], auto&& store) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+        for (int k = 0; k < 8; ++k)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stage + lane * 128 + ((k ^ (lane & 7)) << 4)),
+                       "r"(y[4 * k]), "r"(y[4 * k + 1]), "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = 4 * k + (lane >> 3);
+          uint4 z;
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
+                       : "r"(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4))
+                       : "memory");
+          store(row, z);
+        }
+        __syncwarp();
+      };
+      auto load_o = [&](int c, uint32_t(&o)[32]) {  // columns [32 c, 32 c + 32) of the row, normalised
         if (any) {
           tmem_ld32(tO + c * 32, o);
           tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
-        if (live && whole) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(out + c * 32 + k) =
-                make_uint4(pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
-                           pack_bf16x2(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
-                           pack_bf16x2(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
-                           pack_bf16x2(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
-        } else if (live) {
+        for (int k = 0; k < 32; ++k) o[k] = any ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+      };
+      if (whole) {
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(part + c * 32 + k) =
-                make_float4(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv,
-                            __uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t y[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            load_o(2 * c + half, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              y[half * 16 + k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+          }
+          write_lines(y, [&](int row, uint4 z) {
+            const long long to = __shfl_sync(0xffffffffu, at, row);
+            if (to >= 0) *reinterpret_cast<uint4*>(out + to + c * 64 + (lane & 7) * 8) = z;
+          });
         }
-        __syncwarp();  // the next load is the whole warp's
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          load_o(c, o);
+          write_lines(o, [&](int row, uint4 z) {
+            *reinterpret_cast<uint4*>(part + row * D + c * 32 + (lane & 7) * 4) = z;
+          });
+        }
       }
       if (any) {
         fence_before_sync();
@@ -535,21 +569,29 @@ __global__ void __launch_bounds__(kChThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort_flag) {
-    // Copies still in flight land before the CTA exits: the last ones issued on each barrier.
-    if (ctl.issued_q > 0) mbar_wait_drain(bar(ctl.q_full), (ctl.issued_q - 1) & 1);
-    if (ctl.issued_k0 > 0) mbar_wait_drain(bar(ctl.k0_full), 0);
-    if (ctl.issued_tail > 0) mbar_wait_drain(bar(ctl.tail), (ctl.issued_tail - 1) & 1);
-    for (int t = max(0, ctl.issued_t - C::kStages); t < ctl.issued_t; ++t) {
-      // The arrivals of tile 0's softmax that never came are made here: a thread that stopped earlier
-      // arrived on no later stage.
+    // Copies still in flight land before the CTA exits: the last ones issued on each barrier. A producer that
+    // stopped before the other did has its arrival made here.
+    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i) {
+      for (int p = 0; p < D / 64; ++p)
+        if (issued[p] <= i) mbar_arrive(bar(full));
+      mbar_wait_drain(bar(full), parity);
+    };
+    const int nq = max(ctl.issued_q[0], ctl.issued_q[1]), nt = max(ctl.issued_t[0], ctl.issued_t[1]);
+    const int ntail = max(ctl.issued_tail[0], ctl.issued_tail[1]);
+    if (nq > 0) drain(ctl.q_full, (nq - 1) & 1, ctl.issued_q, nq - 1);
+    if (ctl.issued_k0[0] + ctl.issued_k0[1] > 0) drain(ctl.k0_full, 0, ctl.issued_k0, 0);
+    if (ntail > 0) drain(ctl.tail, (ntail - 1) & 1, ctl.issued_tail, ntail - 1);
+    for (int t = max(0, nt - C::kStages); t < nt; ++t) {
+      // The arrivals of tile 0's softmax that never came, or of its stand-in, are made here: a thread that stopped
+      // earlier arrived on no later stage.
       const int st = t % C::kStages;
       if (mbar_test(bar(ctl.full[st]), (t / C::kStages) & 1)) continue;
-      if (ctl.needs_p0[st]) {
+      if (ctl.issued_t[0] <= t || ctl.needs_p0[st]) {
         int arrived = 0;
         for (int i = 0; i < 128; ++i) arrived += ctl.p0_last[i] >= t;
         if (arrived < 128) mbar_arrive_cnt(bar(ctl.full[st]), 128 - arrived);
       }
-      mbar_wait_drain(bar(ctl.full[st]), (t / C::kStages) & 1);
+      drain(ctl.full[st], (t / C::kStages) & 1, ctl.issued_t, t);
     }
   }
 }
@@ -634,7 +676,7 @@ cudaError_t launch_chunk(const FaPagedArgs& a, cudaStream_t st) {
   auto kern = paged_chunk_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(a.num_sms), dim3(kChThreads), C::kSmem, st, tq, tk, tv, a, rows, wk);
+  e = launch_dependent(kern, dim3(a.num_sms), dim3(C::kThreads), C::kSmem, st, tq, tk, tv, a, rows, wk);
   if (e != cudaSuccess) return e;
   return launch_dependent(paged_chunk_join_kernel<D>, dim3(a.num_sms, 8), dim3(256), 0, st, a, rows, wk);
 }

@@ -17,8 +17,10 @@
 // partials (two slots per CTA) that the merge kernel joins by their log-sum-exp; whole ones are
 // written directly.
 //
-// Roles: warp 0 reads the page table and copies (TMA, a lane per page), warp 1 issues the MMAs, groups of
-// four warps are the softmax and the epilogue, of 16 rows each. Copies run ahead across pieces, so memory never waits for an
+// Roles: warp 0 and at d = 128 the last warp read the page table and copy (TMA, a lane per page; 64 columns
+// each, since a warp issues a copy per ~100 cycles and small pages need many: 16 x 8192 keys in pages of 16 in
+// 93 us, with one warp 100, in pages of 8 107 and 155, of 32 and more 89 both ways),
+// warp 1 issues the MMAs, groups of four warps are the softmax and the epilogue, of 16 rows each. Copies run ahead across pieces, so memory never waits for an
 // epilogue.
 #include "fa_paged.cuh"
 #include "fa_tmap.h"
@@ -45,7 +47,7 @@ struct DecCfg {
   // Groups of four softmax warps, 16 rows (columns of S^T, which are independent) each: one group for all
   // leaves a scheduler one warp and its chain of dependent steps (64 sequences of 1000 keys, 8 K/V heads, d = 128:
   // 64 rows 112 us with one group, 87 with two, 76 with four; 32 rows 64 and 61; d = 64: 99, 69 and 59; 54 and 41).
-  static constexpr int kGroups = NP / 16, kThreads = 64 + 128 * kGroups;
+  static constexpr int kGroups = NP / 16, kThreads = 64 + 128 * kGroups + 32 * (D / 64 - 1);
   static constexpr int kKStages = NP == 64 ? 256 / D : 3, kVStages = NP == 64 ? 256 / D : D == 64 ? 2 : 3;
   static constexpr int kQBytes = NP * D * 2;
   static constexpr int kQBufs = 2;
@@ -74,7 +76,7 @@ struct DecCtl {
   int abort_flag;
   long long scan[18];
   Share share;
-  int issued_q, issued_t;                         // copies issued (abort-path drain)
+  int issued_q[2], issued_t[2];                   // copies issued, by producer (abort-path drain)
   alignas(16) float m[NP];
   alignas(16) float alpha[NP];
   float wmax[4][NP];
@@ -105,14 +107,16 @@ struct Pieces {
   SeqInfo seq;
   __device__ Pieces(const PagedShape& s_, const Share& sh)
       : s(s_), b(sh.b), hk(sh.head), kt(0), n(0), end(0), todo(sh.todo), finished(false) {
-    if (todo > 0) open(sh.tile);
+    if (todo == 0) return;
+    sequence();
+    open(sh.tile);
   }
-  __device__ void open(int at) {  // at: position within the unit
+  __device__ void sequence() {  // looks at sequence b
     const DecUnits x(s, b);
     seq = x.q;
-    n = 0;
-    if (x.count == 0) return;
-    n = x.tiles();
+    n = x.count ? x.tiles() : 0;
+  }
+  __device__ void open(int at) {  // at: position within the unit
     kt = max(0, at - kDecOpen);
     const long long stop = at + todo - kDecOpen;
     end = stop < n ? (int)stop : n;
@@ -128,13 +132,12 @@ struct Pieces {
     }
     if (++hk == s.Hkv) {
       hk = 0;
-      ++b;
+      do {  // todo > 0: a later sequence has new tokens
+        ++b;
+        sequence();
+      } while (n == 0);
     }
     open(0);
-    while (n == 0) {  // todo > 0: a later sequence has new tokens
-      ++b;
-      open(0);
-    }
   }
 };
 
@@ -191,9 +194,9 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
 
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
-    ctl.issued_q = ctl.issued_t = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(ctl.q_full[i]), 1);
+      ctl.issued_q[i] = ctl.issued_t[i] = 0;
+      mbar_init(bar(ctl.q_full[i]), D / 64);
       mbar_init(bar(ctl.q_empty[i]), 1);
       mbar_init(bar(ctl.s_full[i]), 1);
       mbar_init(bar(ctl.o_free[i]), 128 * C::kGroups);
@@ -201,9 +204,9 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
       mbar_init(bar(ctl.pv_done[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(ctl.k_full[i]), 1);
+      mbar_init(bar(ctl.k_full[i]), D / 64);
       mbar_init(bar(ctl.k_empty[i]), 1);
-      mbar_init(bar(ctl.v_full[i]), 1);
+      mbar_init(bar(ctl.v_full[i]), D / 64);
       mbar_init(bar(ctl.v_empty[i]), 1);
     }
     mbar_init(bar(ctl.drain), 1);
@@ -244,8 +247,9 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
     wk.desc[2 * blockIdx.x + 1] = make_int4(w.seq.Lq, w.seq.q0, w.seq.bb, 0);
   }
 
-  if (warp == 0) {
+  if (warp == 0 || (D > 64 && warp == C::kThreads / 32 - 1)) {
     // ------------------------------------------------------------------ copies
+    const int half = warp != 0;  // the 64 columns that this warp copies, of Q, K and V
     const int P = 1 << s.page_shift, rows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     bool run = true;
     int t = 0;
@@ -260,11 +264,10 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
       if (run && qu > 0) run = mbar_wait(bar(ctl.q_empty[qb]), (qu - 1) & 1, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
       if (run && lane == 0) {
-        mbar_expect_tx(bar(ctl.q_full[qb]), box * D * 2);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sQ + (qb * (D / 64) + c) * NP * 128, &tmQ, c * 64, w.hk * G, w.seq.q0, w.seq.bb,
-                      bar(ctl.q_full[qb]));
-        ctl.issued_q = piece + 1;
+        mbar_expect_tx(bar(ctl.q_full[qb]), box * 128);
+        tma_load_4d(sQ + (qb * (D / 64) + half) * NP * 128, &tmQ, half * 64, w.hk * G, w.seq.q0, w.seq.bb,
+                    bar(ctl.q_full[qb]));
+        ctl.issued_q[half] = piece + 1;
       }
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
         const int left = w.seq.Lk - (kt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
@@ -282,14 +285,13 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
 #endif
           if (!run) continue;
           if (lane == 0) {
-            mbar_expect_tx(full, pages * rows * D * 2);
-            ctl.issued_t = 2 * t + x + 1;
+            mbar_expect_tx(full, pages * rows * 128);
+            ctl.issued_t[half] = 2 * t + x + 1;
           }
           __syncwarp();
           if (lane < pages)
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d((x ? sV(st) : sK(st)) + c * 16384 + lane * rows * 128, x ? &tmV : &tmK, c * 64, slot, w.hk,
-                          page, full);
+            tma_load_4d((x ? sV(st) : sK(st)) + half * 16384 + lane * rows * 128, x ? &tmV : &tmK, half * 64, slot, w.hk,
+                        page, full);
         }
         page = next;
       }
@@ -543,13 +545,20 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
     tmem_dealloc(tmem, C::kTmemCols);
   }
   if (threadIdx.x == 0 && *abort_flag) {
-    // Copies still in flight land before the CTA exits: the last one issued into each buffer.
-    for (int i = max(0, ctl.issued_q - C::kQBufs); i < ctl.issued_q; ++i)
-      mbar_wait_drain(bar(ctl.q_full[i % C::kQBufs]), (i / C::kQBufs) & 1);
-    for (int i = max(0, ctl.issued_t - 8); i < ctl.issued_t; ++i) {
+    // Copies still in flight land before the CTA exits: the last one issued into each buffer. A producer that stopped
+    // before the other did has its arrival made here.
+    const int nq = max(ctl.issued_q[0], ctl.issued_q[1]), nt = max(ctl.issued_t[0], ctl.issued_t[1]);
+    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i) {
+      for (int p = 0; p < D / 64; ++p)
+        if (issued[p] <= i) mbar_arrive(bar(full));
+      mbar_wait_drain(bar(full), parity);
+    };
+    for (int i = max(0, nq - C::kQBufs); i < nq; ++i)
+      drain(ctl.q_full[i % C::kQBufs], (i / C::kQBufs) & 1, ctl.issued_q, i);
+    for (int i = max(0, nt - 8); i < nt; ++i) {
       const int t = i >> 1, stages = (i & 1) ? C::kVStages : C::kKStages;
-      if (t + stages <= (ctl.issued_t - 1 - (i & 1)) >> 1) continue;  // a later copy used the buffer
-      mbar_wait_drain((i & 1) ? bar(ctl.v_full[t % stages]) : bar(ctl.k_full[t % stages]), (t / stages) & 1);
+      if (t + stages <= (nt - 1 - (i & 1)) >> 1) continue;  // a later copy used the buffer
+      drain((i & 1) ? ctl.v_full[t % stages] : ctl.k_full[t % stages], (t / stages) & 1, ctl.issued_t, i);
     }
   }
 }

@@ -11,7 +11,8 @@
 // leaves 128 partial sums per piece (two slots per CTA), which the join kernel adds in the pieces'
 // order; with one query tile per unit nothing is cut.
 //
-// Roles: warp 0 reads the page table and copies; one warp issues the MMAs, or with many rows two, a
+// Roles: warp 0 and at d = 128 the last warp read the page table and copy (64 columns each: a warp issues a copy
+// per ~100 cycles, and small pages need many); one warp issues the MMAs, or with many rows two, a
 // query tile each in turn: an MMA takes its thread about 70 cycles whatever its width, so a tile's eight and
 // the waits around them fill 1200 cycles of one thread, twice what the tensor pipe needs. Groups of four
 // warps (three, with many rows four) take the query tiles in turn; with many rows a last group adds their
@@ -38,7 +39,8 @@ struct WCfg {
   // its own, which sees the buffer's every phase.
   static constexpr int kGroups = kFew ? 3 : 4;
   static constexpr int kIssuers = kFew ? 1 : 2;
-  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128 + 32);
+  static constexpr int kIssuer2 = 2 + 4 * kGroups + 4;  // the second issuer's warp, behind the sums' group
+  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128 + 32) + 32 * (D / 64 - 1);
   static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 2) * (128 / D);
   static constexpr int kQBufs = kFew ? 2 : 4 * (128 / D);  // (even: a buffer has one issuer, which sees its every phase)
   static constexpr int kOpen = kFew ? 0 : 3;
@@ -52,9 +54,9 @@ struct WCtl {
   uint64_t k_full[12], k_empty[12], q_full[8], q_empty[8], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[23];
+  long long scan[24];
   Share share;
-  int issued_k, issued_q;               // copies issued (abort-path drain)
+  int issued_k[2], issued_q[2];         // copies issued, by producer (abort-path drain)
   alignas(16) float nlse[4][2][NP];  // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
   alignas(16) int seen[4][2][NP];    // last key the row sees
   float sums[2][4][NP == 128 ? 128 : 1];  // many rows: the groups' sums of a piece, per parity
@@ -223,13 +225,13 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
-    ctl.issued_k = ctl.issued_q = 0;
+    for (int i = 0; i < 2; ++i) ctl.issued_k[i] = ctl.issued_q[i] = 0;
     for (int i = 0; i < C::kKBufs; ++i) {
-      mbar_init(bar(ctl.k_full[i]), 1);
+      mbar_init(bar(ctl.k_full[i]), D / 64);
       mbar_init(bar(ctl.k_empty[i]), C::kIssuers);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
-      mbar_init(bar(ctl.q_full[i]), 1);
+      mbar_init(bar(ctl.q_full[i]), D / 64);
       mbar_init(bar(ctl.q_empty[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -276,8 +278,9 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     wk.desc[blockIdx.x] = d;
   }
 
-  if (warp == 0) {
+  if (warp == 0 || (D > 64 && warp == C::kThreads / 32 - 1)) {
     // ------------------------------------------------------------------ copies
+    const int half = warp != 0;  // the 64 columns that this warp copies, of Q and K
     const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     bool run = true;
     int kn = 0, qn = 0;  // key tiles and query tiles copied
@@ -293,11 +296,10 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       const int st = qn % C::kQBufs, u = qn / C::kQBufs;
       if (run && u > 0) run = mbar_wait(bar(ctl.q_empty[st]), (u - 1) & 1, abort_flag, a.status);
       if (go() && lane == 0) {
-        mbar_expect_tx(bar(ctl.q_full[st]), used * D * 2);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sQ + st * C::kQBytes + c * NP * 128, &tmQ, c * 64, head0, w.x.q.q0 + token, w.x.q.bb,
-                      bar(ctl.q_full[st]));
-        ctl.issued_q = qn + 1;
+        mbar_expect_tx(bar(ctl.q_full[st]), used * 128);
+        tma_load_4d(sQ + st * C::kQBytes + half * NP * 128, &tmQ, half * 64, head0, w.x.q.q0 + token, w.x.q.bb,
+                    bar(ctl.q_full[st]));
+        ctl.issued_q[half] = qn + 1;
       }
       ++qn;
     };
@@ -312,14 +314,13 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       if (go()) {
         const int pages = min(per, (w.x.q.Lk - (w.kt << 7) + prows - 1) >> shift);
         if (lane == 0) {
-          mbar_expect_tx(bar(ctl.k_full[st]), pages * prows * D * 2);
-          ctl.issued_k = kn + 1;
+          mbar_expect_tx(bar(ctl.k_full[st]), pages * prows * 128);
+          ctl.issued_k[half] = kn + 1;
         }
         __syncwarp();
         if (lane < pages)
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sK + st * C::kKBytes + c * 16384 + lane * prows * 128, &tmK, c * 64, (w.kt << 7) & (P - 1), w.hk,
-                        page, bar(ctl.k_full[st]));
+          tma_load_4d(sK + st * C::kKBytes + half * 16384 + lane * prows * 128, &tmK, half * 64, (w.kt << 7) & (P - 1),
+                      w.hk, page, bar(ctl.k_full[st]));
       }
       ++kn;
       if (!C::kFew) {
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       w.next();
       page = w.done() ? 0 : page_of(w);
     }
-  } else if (warp == 1 || warp == C::kThreads / 32 - C::kIssuers + 1) {
+  } else if (warp == 1 || (C::kIssuers == 2 && warp == C::kIssuer2)) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0) {
       // Positions in the rings are counters and the group that sees the scores releases the query tile:
@@ -526,11 +527,18 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     tmem_dealloc(tmem, C::kTmemCols);
   }
   if (threadIdx.x == 0 && *abort_flag) {
-    // Copies still in flight land before the CTA exits: the last one issued into each buffer.
-    for (int i = max(0, ctl.issued_q - C::kQBufs); i < ctl.issued_q; ++i)
-      mbar_wait_drain(bar(ctl.q_full[i % C::kQBufs]), (i / C::kQBufs) & 1);
-    for (int i = max(0, ctl.issued_k - C::kKBufs); i < ctl.issued_k; ++i)
-      mbar_wait_drain(bar(ctl.k_full[i % C::kKBufs]), (i / C::kKBufs) & 1);
+    // Copies still in flight land before the CTA exits: the last one issued into each buffer. A producer that stopped
+    // before the other did has its arrival made here.
+    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i) {
+      for (int p = 0; p < D / 64; ++p)
+        if (issued[p] <= i) mbar_arrive(bar(full));
+      mbar_wait_drain(bar(full), parity);
+    };
+    const int nq = max(ctl.issued_q[0], ctl.issued_q[1]), nk = max(ctl.issued_k[0], ctl.issued_k[1]);
+    for (int i = max(0, nq - C::kQBufs); i < nq; ++i)
+      drain(ctl.q_full[i % C::kQBufs], (i / C::kQBufs) & 1, ctl.issued_q, i);
+    for (int i = max(0, nk - C::kKBufs); i < nk; ++i)
+      drain(ctl.k_full[i % C::kKBufs], (i / C::kKBufs) & 1, ctl.issued_k, i);
   }
 }
 

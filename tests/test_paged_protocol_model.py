@@ -5,7 +5,7 @@ A CTA walks pieces of units; here a piece is the number of its tiles. Each model
 commits, with copies, MMAs and commits completing at random times, and checks: no deadlock, no buffer reloaded before
 its readers have completed, no MMA before its operands are there, no operand or accumulator overwritten while it is
 read, and with waits that run out at random: every role ends and no copy is left in flight. A planted mistake must be
-found in each.
+found in each. Every copy is made by one or two producers, of 64 columns each, which arrive on the same barriers.
 
 decode   fa_paged_decode.cu: K and V rings of their own lengths, two Q buffers, S and P double buffered, O per piece
          double buffered; the softmax waits for V itself in a unit's last tile, whose rows past the last key it zeroes.
@@ -38,31 +38,47 @@ def finish(M, roles, issued):
     return M.run(roles, final=drain), M.errors
 
 
-def last_phases(name, n, bufs):
-    """Barrier and parity of the last copy into each of `bufs` buffers after n copies."""
-    return [(f"{name}{i % bufs}", (i // bufs) & 1) for i in range(max(0, n - bufs), n)]
+def last_phases(M, name, counts, bufs):
+    """Barrier and parity of the last copy into each of `bufs` buffers, after counts[p] copies by producer p; the arrivals
+    of a producer that stopped before the other are made here."""
+    n = max(counts)
+    out = []
+    for i in range(max(0, n - bufs), n):
+        bar = name if name in M.B else f"{name}{i % bufs}"
+        for c in counts:
+            if c <= i:
+                M.B[bar].arrive()
+        out.append((bar, (i // bufs) & 1))
+    return out
+
+
+def landed(M, prods, *what):
+    """Every producer's part of a copy has landed."""
+    return all((*what, h) in M.done for h in range(prods))
 
 
 # ----------------------------------------------------------------------------- decode
 
 
-def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, groups=1):
+def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, groups=1, prods=1):
     """groups: softmax groups, each with an equal part of every tile's rows."""
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
     T = tiles_of(pieces)
     for i in range(2):
-        for n in ("qf", "qe", "sf", "pv"):
+        for n in ("qe", "sf", "pv"):
             M.bar(f"{n}{i}", 1)
+        M.bar(f"qf{i}", prods)
         for n in ("of", "p"):
             M.bar(f"{n}{i}", groups)
     for i in range(ks):
-        M.bar(f"kf{i}", 1), M.bar(f"ke{i}", 1)
+        M.bar(f"kf{i}", prods), M.bar(f"ke{i}", 1)
     for i in range(vs):
-        M.bar(f"vf{i}", 1), M.bar(f"ve{i}", 1)
-    count = {"q": 0, "k": 0, "v": 0}
+        M.bar(f"vf{i}", prods), M.bar(f"ve{i}", 1)
+    count = {n: [0] * prods for n in "qkv"}
+    has = lambda *what: landed(M, prods, *what)
 
-    def producer():
+    def producer(h):
         run = True
         for t, (p, k, _) in enumerate(T):
             if k == 0:
@@ -72,16 +88,16 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, g
                 if run:
                     for u in range(len(T)):
                         need(T[u][0] != p - 2 or ("S", u) in done, f"Q of piece {p - 2} overwritten before S({u})")
-                    M.load(f"qf{p % 2}", 1, ("Q", p))
-                    count["q"] = p + 1
+                    M.load(f"qf{p % 2}", 1, ("Q", p, h))
+                    count["q"][h] = p + 1
             for x, n, reader in (("k", ks, "S"), ("v", vs, "PV")):
                 if run and t >= n:
                     run = yield from M.wait(f"{x}e{t % n}", (t // n - 1) & 1)
                 run = run and not M.aborted
                 if run:
                     need(t < n or (reader, t - n) in done, f"{x} of tile {t - n} overwritten before {reader}")
-                    M.load(f"{x}f{t % n}", 1, (x, t))
-                    count[x] = t + 1
+                    M.load(f"{x}f{t % n}", 1, (x, t, h))
+                    count[x][h] = t + 1
             yield None
 
     def issuer():
@@ -94,7 +110,7 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, g
             if run:
                 run = yield from M.wait(f"kf{t % ks}", (t // ks) & 1)
             if run:
-                need(("Q", p) in done and ("k", t) in done, f"S({t}) before its operands")
+                need(has("Q", p) and has("k", t), f"S({t}) before its operands")
                 need(t < 2 or ("P", t - 2) in done, f"S({t}) over S({t - 2}) before it was read")
                 M.mma("i", ("S", t))
                 M.commit("i", f"sf{t & 1}"), M.commit("i", f"ke{t % ks}")
@@ -113,7 +129,7 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, g
             if run and k == 0 and p >= 2:
                 run = yield from M.wait(f"of{p & 1}", ((p >> 1) - 1) & 1)
             if run:
-                need(("v", t) in done and ("P", t) in done, f"PV({t}) before its operands")
+                need(has("v", t) and ("P", t) in done, f"PV({t}) before its operands")
                 need(k > 0 or p < 2 or ("O", p - 2) in done, f"PV({t}) over O of piece {p - 2} before it was read")
                 M.mma("i", ("PV", t))
                 M.commit("i", f"ve{t % vs}"), M.commit("i", f"pv{t & 1}")
@@ -143,7 +159,7 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, g
             if last and r2.random() < 0.7:  # the unit's last tile: V's rows past the last key become 0
                 if run:
                     run = yield from M.wait(f"vf{t % vs}", (t // vs) & 1)
-                need(not run or (("v", t) in done and ("PV", t) not in done), f"V({t}) zeroed at the wrong time")
+                need(not run or (has("v", t) and ("PV", t) not in done), f"V({t}) zeroed at the wrong time")
             yield None
             if run:
                 part_done(("P", t))
@@ -157,8 +173,9 @@ def decode(pieces, ks, vs, seed, abort_p=0.0, skip_pv_wait=False, one_p=False, g
                     M.B[f"of{p & 1}"].arrive()
 
     def issued():
-        return last_phases("qf", count["q"], 2) + last_phases("kf", count["k"], ks) + last_phases("vf", count["v"], vs)
-    return finish(M, {"prod": producer(), "mma": issuer(), **{f"soft{g}": softmax(g) for g in range(groups)}}, issued)
+        return [x for n, c in (("q", 2), ("k", ks), ("v", vs)) for x in last_phases(M, f"{n}f", count[n], c)]
+    return finish(M, {**{f"prod{h}": producer(h) for h in range(prods)}, "mma": issuer(),
+                      **{f"soft{g}": softmax(g) for g in range(groups)}}, issued)
 
 
 def pieces_for(seed):
@@ -171,13 +188,13 @@ RINGS = [(3, 3), (3, 2), (2, 2), (4, 4)]
 
 def test_decode_has_no_deadlock_or_hazard():
     for seed in range(2500):
-        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, groups=(1, 2, 4)[seed % 3])
+        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, groups=(1, 2, 4)[seed % 3], prods=1 + seed // 3 % 2)
         assert res == "ok" and not errs, (pieces_for(seed), RINGS[seed % 4], seed, res, errs[:3])
 
 
 def test_decode_ends_after_waits_that_run_out():
     for seed in range(1500):
-        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, abort_p=0.02, groups=(1, 2, 4)[seed % 3])
+        res, errs = decode(pieces_for(seed), *RINGS[seed % 4], seed, abort_p=0.02, groups=(1, 2, 4)[seed % 3], prods=1 + seed // 3 % 2)
         assert res == "ok" and not errs, (pieces_for(seed), RINGS[seed % 4], seed, res, errs[:3])
 
 
@@ -190,24 +207,27 @@ def test_decode_model_finds_a_missing_wait():
 # ----------------------------------------------------------------------------- chunk
 
 
-def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
+def chunk(pieces, stages, seed, abort_p=0.0, early_q=False, prods=1):
     """pieces: (tiles, tiles query tile 0 sees, tiles query tile 1 sees, the last tile is the sequence's last)."""
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
     T = tiles_of([n for n, *_ in pieces])
     sees = lambda x, t: t < len(T) and T[t][1] < pieces[T[t][0]][1 + x]
-    for n in ("qf", "qe", "k0f", "k0e", "tail"):
+    for n in ("qf", "k0f", "tail"):
+        M.bar(n, prods)
+    for n in ("qe", "k0e"):
         M.bar(n, 1)
     for i in range(stages):
-        M.bar(f"f{i}", 2), M.bar(f"e{i}", 1)  # f: the copies, and P of tile 0 (128 threads, modelled as one arrival)
+        M.bar(f"f{i}", prods + 1), M.bar(f"e{i}", 1)  # f: the copies, and P of tile 0 (128 threads, modelled as one arrival)
     M.bar("p1", 1)
     for x in (0, 1):
         for n in ("sf", "od", "of"):
             M.bar(f"{n}{x}", 1)
-    count = {"q": 0, "k0": 0, "t": 0, "tail": 0}
+    count = {n: [0] * prods for n in ("q", "k0", "t", "tail")}
     needs_p0, p0_last = {}, [-1]
+    has = lambda *what: landed(M, prods, *what)
 
-    def producer():
+    def producer(h):
         run = True
         if not T:
             return
@@ -220,12 +240,12 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                 for u in range(len(T)):
                     for x in (0, 1):
                         need(T[u][0] != p - 1 or not sees(x, u) or (f"S{x}", u) in done, f"Q {p - 1} overwritten")
-                M.load("qf", 1, ("Q", p))
-                count["q"] = p + 1
+                M.load("qf", 1, ("Q", p, h))
+                count["q"][h] = p + 1
             return run
         run = yield from copy_q(0, run)
-        M.load("k0f", 1, ("K", 0))
-        count["k0"] = 1
+        M.load("k0f", 1, ("K", 0, h))
+        count["k0"][h] = 1
         tails = 0
         for t, (p, k, last) in enumerate(T):
             b = t % stages
@@ -240,26 +260,27 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                     need(t < stages or not sees(x, t - stages) or (f"PV{x}", t - stages) in done, f"V {t} too early")
                     need(t + 1 < stages or not sees(x, t - stages + 1) or (f"S{x}", t - stages + 1) in done,
                          f"K {t + 1} too early")
-                count["t"] = t + 1
-                needs_p0[b] = sees(0, t)
-                if not sees(0, t):
-                    M.B[f"f{b}"].arrive()  # stands in for tile 0's softmax
+                if h == 0:
+                    needs_p0[b] = sees(0, t)
+                    if not sees(0, t):
+                        M.B[f"f{b}"].arrive()  # stands in for tile 0's softmax
+                count["t"][h] = t + 1
                 if not (last and pieces[p][3]):
                     M.expect(f"f{b}", 2 if more else 1)
-                    M.copy(f"f{b}", 1, ("V", t))
+                    M.copy(f"f{b}", 1, ("V", t, h))
                     if more:
-                        M.copy(f"f{b}", 1, ("K", t + 1))
-                    done.add(("clean", t))
+                        M.copy(f"f{b}", 1, ("K", t + 1, h))
+                    done.add(("clean", t, h))
                 else:
                     M.B[f"f{b}"].tx += 1 if more else 0
-                    M.load("tail", 1, ("V", t))
-                    count["tail"] = tails + 1
+                    M.load("tail", 1, ("V", t, h))
+                    count["tail"][h] = tails + 1
                     if more:
-                        M.copy(f"f{b}", 1, ("K", t + 1))
+                        M.copy(f"f{b}", 1, ("K", t + 1, h))
                     run = yield from M.wait("tail", tails & 1)
                     tails += 1
                     if run:
-                        done.add(("clean", t))
+                        done.add(("clean", t, h))
                     M.B[f"f{b}"].arrive()
             if more and T[t + 1][1] == 0:
                 run = yield from copy_q(T[t + 1][0], run)
@@ -271,7 +292,7 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
         np1, seen = 0, [0, 0]
 
         def issue_s(x, t):
-            need(("Q", T[t][0]) in done and ("K", t) in done, f"S{x}({t}) before its operands")
+            need(has("Q", T[t][0]) and has("K", t), f"S{x}({t}) before its operands")
             M.mma("i", (f"S{x}", t))
             M.commit("i", f"sf{x}")
         run = yield from M.wait("qf", 0)
@@ -303,7 +324,7 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                     if not run:
                         break
                     # (after an abort the stage is completed as it is; the product then runs on stale data)
-                    need(M.aborted or (("V", t) in done and ("clean", t) in done), f"PV{x}({t}) before V")
+                    need(M.aborted or (has("V", t) and has("clean", t)), f"PV{x}({t}) before V")
                     need((f"P{x}", t) in done, f"PV{x}({t}) before P")
                     M.mma("i", (f"PV{x}", t))
                     if k + 1 == min(pieces[p][0], pieces[p][1 + x]):
@@ -350,14 +371,15 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False):
                     M.B[f"of{x}"].arrive()
 
     def issued():
-        out = [("qf", (count["q"] - 1) & 1)] if count["q"] else []
-        out += [("k0f", 0)] if count["k0"] else []
-        out += [("tail", (count["tail"] - 1) & 1)] if count["tail"] else []
-        for t in range(max(0, count["t"] - stages), count["t"]):
-            if not M.B[f"f{t % stages}"].passes((t // stages) & 1) and needs_p0[t % stages] and p0_last[0] < t:
-                M.B[f"f{t % stages}"].arrive()  # the softmax arrival that never came
-        return out + last_phases("f", count["t"], stages)
-    return finish(M, {"prod": producer(), "mma": issuer(), "s0": softmax(0), "s1": softmax(1)}, issued)
+        out = [x for n in ("q", "k0", "tail") for x in last_phases(M, "tail" if n == "tail" else f"{n}f", count[n], 1)]
+        n = max(count["t"])
+        for t in range(max(0, n - stages), n):
+            if not M.B[f"f{t % stages}"].passes((t // stages) & 1):
+                if (count["t"][0] <= t or needs_p0[t % stages]) and p0_last[0] < t:
+                    M.B[f"f{t % stages}"].arrive()  # the softmax arrival that never came, or its stand-in
+        return out + last_phases(M, "f", count["t"], stages)
+    return finish(M, {**{f"prod{h}": producer(h) for h in range(prods)}, "mma": issuer(), "s0": softmax(0),
+                      "s1": softmax(1)}, issued)
 
 
 def chunk_pieces(seed):
@@ -373,13 +395,13 @@ def chunk_pieces(seed):
 
 def test_chunk_has_no_deadlock_or_hazard():
     for seed in range(2500):
-        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed)
+        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, prods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (chunk_pieces(seed), seed, res, errs[:3])
 
 
 def test_chunk_ends_after_waits_that_run_out():
     for seed in range(1500):
-        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, abort_p=0.02)
+        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, abort_p=0.02, prods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (chunk_pieces(seed), seed, res, errs[:3])
 
 
@@ -390,7 +412,7 @@ def test_chunk_model_finds_a_missing_wait():
 # ----------------------------------------------------------------------------- weights
 
 
-def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, three=False):
+def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, three=False, prods=1):
     """pieces: the query tiles of each key tile (few rows: one each, and every third begins another head)."""
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
@@ -400,12 +422,13 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
     q_of = (lambda t: T[t][0] // 3) if few else (lambda t: t)
     for n, c in (("kf", kb), ("ke", kb), ("qf", qb), ("qe", qb), ("sf", sb), ("fr", sb)):
         for i in range(c):
-            M.bar(f"{n}{i}", issuers if n == "ke" else 1)
+            M.bar(f"{n}{i}", issuers if n == "ke" else prods if n in ("kf", "qf") else 1)
     for i in range(2):
         M.bar(f"sr{i}", G), M.bar(f"sx{i}", 1)
-    count = {"k": 0, "q": 0}
+    count = {n: [0] * prods for n in "kq"}
+    has = lambda *what: landed(M, prods, *what)
 
-    def producer():
+    def producer(h):
         run = True
 
         def copy_q(q, run):
@@ -414,8 +437,8 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
             run = run and not M.aborted
             if run:
                 need(all(("S", t) in done for t in range(len(T)) if q_of(t) == q - qb), f"Q {q - qb} overwritten")
-                M.load(f"qf{q % qb}", 1, ("Q", q))
-                count["q"] = q + 1
+                M.load(f"qf{q % qb}", 1, ("Q", q, h))
+                count["q"][h] = q + 1
             return run
         for p, n in enumerate(pieces):
             if few and head(p):
@@ -425,8 +448,8 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
             run = run and not M.aborted
             if run:
                 need(all(("S", t) in done for t in range(len(T)) if T[t][0] == p - kb), f"K {p - kb} overwritten")
-                M.load(f"kf{p % kb}", 1, ("K", p))
-                count["k"] = p + 1
+                M.load(f"kf{p % kb}", 1, ("K", p, h))
+                count["k"][h] = p + 1
             if not few:
                 for t in range(len(T)):
                     if T[t][0] == p:
@@ -447,7 +470,7 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
                     run = yield from M.wait(f"fr{t % sb}", (t // sb - 1) & 1)
                 if not run:
                     break
-                need(("K", p) in done and ("Q", q_of(t)) in done, f"S({t}) before its operands")
+                need(has("K", p) and has("Q", q_of(t)), f"S({t}) before its operands")
                 need(t < sb or ("read", t - sb) in done, f"S({t}) over S({t - sb})")
                 M.mma(f"i{me}", ("S", t))
                 M.commit(f"i{me}", f"sf{t % sb}")
@@ -492,12 +515,12 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
                 M.B[f"sx{p & 1}"].arrive()
             yield None
 
-    roles = {"prod": producer(), "mma0": issuer(0), **{f"g{g}": group(g) for g in range(G)}}
+    roles = {**{f"prod{h}": producer(h) for h in range(prods)}, "mma0": issuer(0), **{f"g{g}": group(g) for g in range(G)}}
     if not few:
         roles |= {"mma1": issuer(1), "add": adder()}
 
     def issued():
-        return last_phases("qf", count["q"], qb) + last_phases("kf", count["k"], kb)
+        return last_phases(M, "qf", count["q"], qb) + last_phases(M, "kf", count["k"], kb)
     return finish(M, roles, issued)
 
 
@@ -508,14 +531,14 @@ def weight_pieces(seed, few):
 def test_weights_has_no_deadlock_or_hazard():
     for seed in range(2500):
         few = bool(seed & 1)
-        res, errs = weights(weight_pieces(seed, few), few, seed)
+        res, errs = weights(weight_pieces(seed, few), few, seed, prods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (weight_pieces(seed, few), few, seed, res, errs[:3])
 
 
 def test_weights_ends_after_waits_that_run_out():
     for seed in range(1500):
         few = bool(seed & 1)
-        res, errs = weights(weight_pieces(seed, few), few, seed, abort_p=0.02)
+        res, errs = weights(weight_pieces(seed, few), few, seed, abort_p=0.02, prods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (weight_pieces(seed, few), few, seed, res, errs[:3])
 
 
