@@ -72,9 +72,22 @@ __device__ __forceinline__ size_t weight_offset(const PagedShape& s, int page, i
 
 // How query rows lie in tiles: gs heads side by side for each of tpt tokens; Hv such groups of heads,
 // per_kv of them per K/V head.
+struct FastDiv {  // division of 0 <= n < 2^31 by a constant of the launch: n ceil(2^(31 + k) / d) >> (31 + k), 2^k >= d
+  uint32_t mul, shift;
+  __device__ int div(int n) const { return (int)(((unsigned long long)(uint32_t)n * mul) >> shift); }
+};
+inline FastDiv fast_div(int d) {
+  uint32_t k = 0;
+  while ((1 << k) < d) ++k;
+  return {(uint32_t)(((1ull << (31 + k)) + d - 1) / d), 31 + k};
+}
 struct PagedRows {
   int gs, Hv, per_kv, tpt;
+  FastDiv by_per_kv, by_tpt;
 };
+inline PagedRows paged_rows(int gs, int Hv, int per_kv, int tpt) {
+  return {gs, Hv, per_kv, tpt, fast_div(per_kv), fast_div(tpt)};
+}
 
 // 128-row tiles: the divisor of the heads per K/V head that fills the rows best, the largest of equals
 // (a K/V tile then serves more heads).
@@ -83,7 +96,7 @@ inline PagedRows paged_rows_for(const PagedShape& s) {
   int best = 1;
   for (int g = 1; g <= G && g <= 128; ++g)
     if (G % g == 0 && 128 / g * g >= 128 / best * best) best = g;
-  return {best, s.H / best, G / best, 128 / best};
+  return paged_rows(best, s.H / best, G / best, 128 / best);
 }
 
 // Up to 64 rows (tokens x heads of one K/V head) fit the few-row kernels: one tile of 16, 32 or 64
@@ -94,9 +107,21 @@ inline bool paged_few_rows(const PagedShape& s) { return (long long)s.Nq * (s.H 
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// sum of floor((a i + b) / m) for 0 <= i < n, by Euclid's steps on (a, m). The arguments and a n + b
-// are positions of keys, tokens or tiles and fit 31 bits, so the divisions are 32-bit ones.
+// sum of floor((a i + b) / m) for 0 <= i < n, by Euclid's steps on (a, m), or without a division where both are powers
+// of two (head counts that divide 128). The arguments and a n + b are positions of keys, tokens or tiles and fit
+// 31 bits, so the divisions are 32-bit ones.
 __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  if ((a & (a - 1)) == 0 && (m & (m - 1)) == 0) {
+    const int x = 31 - __clz(m), y = 31 - __clz(a);
+    const long long pairs = (long long)n * (n - 1) / 2;
+    if (y >= x) return (pairs << (y - x)) + (long long)n * (b >> x);
+    const int r = x - y;  // floor((a i + b) / m) = (i + b / a) >> r
+    auto below = [r](long long e) {  // sum of j >> r for j < e
+      const long long k = e >> r;
+      return (k * (k - 1) / 2 << r) + k * (e - (k << r));
+    };
+    return below((long long)(b >> y) + n) - below(b >> y);
+  }
   long long sum = 0;
   while (n > 0) {
     sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
@@ -120,75 +145,96 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
 
 // A CTA's share of the work. Units (of key tiles, or of query tiles) stand in one line, ordered by
 // sequence, head and unit; each is kOpen positions, which stand for the time a unit takes besides its
-// tiles, and then a position per tile. CTA c of n takes [total c / n, total (c + 1) / n). A share that
-// begins inside a unit's first kOpen positions begins with its first tile; one that ends there
-// has none of them.
+// tiles, and then a position per tile. Of `total` positions CTA c of n takes total / n, the first total % n
+// CTAs one more. A share that begins inside a unit's first kOpen positions begins with its first tile; one
+// that ends there has none of them.
 struct Share {
   int b, head, unit, tile;   // where the CTA begins
   long long todo;            // its positions, from there
   int first_cta, first_slot; // of the unit in which it begins: the CTA with its first tile, the slot of that piece
 };
 
-// Finds the share of CTA blockIdx.x; all threads of the CTA take part, and `sh` and `scan` (one entry per
-// warp, at least two) are in shared memory. Units(b): heads, count, before(u) (positions before unit u, one
-// head's), tiles(u), and open, the positions of a unit before its first tile.
-template <int kThreads, typename Make>
-__device__ void find_share(int B, Make&& make, Share& sh, long long* scan) {
+struct Division {
+  long long each, more;  // positions of a CTA; CTAs with one more
+  __device__ Division(long long total, long long n) : each(div_pos(total, n)), more(total - each * n) {}
+  __device__ long long begin(long long c) const { return each * c + min(c, more); }
+  __device__ long long cta(long long at) const {
+    const long long wide = more * (each + 1);
+    return at < wide ? div_pos(at, each + 1) : more + div_pos(at - wide, each);
+  }
+};
+
+// Finds the share of CTA blockIdx.x; all threads of the CTA take part, and `sh`, `scan` (one entry per
+// warp, at least two) and `at` are in shared memory; `at` becomes the units of sequence sh.b where the share is not
+// empty. Units, made by make(b): heads, count, before(u) (positions before unit u, one head's), tiles(u), and open,
+// the positions of a unit before its first tile. Every kernel begins with this and can load nothing before it knows its
+// share, so it counts in full: each sequence is looked at once, and few divisions are left.
+template <int kThreads, typename Units, typename Make>
+__device__ void find_share(int B, Make&& make, Share& sh, long long* scan, Units& at) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (B + kThreads - 1) / kThreads, first = threadIdx.x * per, last = min(B, first + per);
-  auto size_of = [&](int b) {
-    const auto x = make(b);
-    return x.before(x.count) * x.heads;
-  };
-  long long mine = 0;
-  for (int b = first; b < last; ++b) mine += size_of(b);
+  const int per = B <= kThreads ? 1 : (B + kThreads - 1) / kThreads, first = threadIdx.x * per, last = min(B, first + per);
+  Units x;
+  long long size = 0, mine = 0;  // of the thread's first sequence (one head's), and of all of its
+  if (first < last) {
+    x = make(first);
+    size = x.before(x.count);
+    mine = size * x.heads;
+    for (int b = first + 1; b < last; ++b) {
+      const Units y = make(b);
+      mine += y.before(y.count) * y.heads;
+    }
+  }
+  const int warps = min(kThreads / 32, per == 1 ? (B + 31) >> 5 : kThreads / 32);  // that have sequences
   long long inc = mine;
+  if (warp < warps) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) scan[warp] = inc;
   }
   if (threadIdx.x == 0) sh.todo = 0;
-  if (lane == 31) scan[warp] = inc;
   __syncthreads();
   long long base = inc - mine, total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
+  for (int i = 0; i < warps; ++i) {
     if (i < warp) base += scan[i];
     total += scan[i];
   }
   __syncthreads();  // scan is read
+  if (total == 0) return;
   const long long n = min(total, (long long)gridDim.x), c = blockIdx.x;  // no CTA before the last busy one is idle
-  const long long lo = c < n ? div_pos(total * c, n) : 0, hi = c < n ? div_pos(total * (c + 1), n) : 0;
-  if (lo < hi && lo >= base && lo < base + mine) {  // the sequence, the line's position where it begins, its size
+  if (c >= n) return;
+  const Division cut(total, n);
+  const long long lo = cut.begin(c);
+  if (lo >= base && lo < base + mine) {  // the sequence, and the line's position where it begins
     int b = first;
-    long long size = mine;
-    if (per > 1)
-      for (;; ++b) {
-        size = size_of(b);
-        if (lo < base + size) break;
-        base += size;
-      }
+    while (lo >= base + size * x.heads) {
+      base += size * x.heads;
+      x = make(++b);
+      size = x.before(x.count);
+    }
     sh.b = b;
+    at = x;
     scan[0] = base;
     scan[1] = size;
   }
   __syncthreads();
-  if (lo >= hi) return;
-  const auto x = make(sh.b);
-  const long long from = scan[0], each = div_pos(scan[1], x.heads);
-  const int head = (int)div_pos(lo - from, each);
-  const long long at = from + head * each;
-  for (int u = threadIdx.x; u < x.count; u += kThreads) {
-    const long long start = at + x.before(u);
-    if (start > lo || lo >= start + x.tiles(u) + x.open) continue;
+  const long long from = scan[0];
+  size = scan[1];
+  const int head = (int)div_pos(lo - from, size);
+  const long long line = from + head * size;  // where the head's units begin
+  const int count = at.count, open = at.open;
+  for (int u = threadIdx.x; u < count; u += kThreads) {
+    const long long start = line + at.before(u);
+    if (start > lo || lo >= start + at.tiles(u) + open) continue;
     sh.head = head;
     sh.unit = u;
     sh.tile = (int)(lo - start);
-    sh.todo = hi - lo;
-    const long long tile0 = start + x.open;
-    const long long c0 = div_pos((tile0 + 1) * n - 1, total);
+    sh.todo = cut.begin(c + 1) - lo;
+    const long long c0 = cut.cta(start + open);
     sh.first_cta = (int)c0;
-    sh.first_slot = 2 * (int)c0 + (div_pos(total * c0, n) >= start ? 0 : 1);
+    sh.first_slot = 2 * (int)c0 + (cut.begin(c0) >= start ? 0 : 1);
   }
   __syncthreads();
 }

@@ -37,6 +37,39 @@ struct ChCfg {
   static constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
 };
 
+// A unit's copies of Q and its epilogue take the time of about four key tiles.
+constexpr int kChOpen = 4;
+
+// The units of one sequence, for one head group: unit u has tokens [u U, u U + U).
+struct Units {
+  int heads, count, open, U, causal, none;
+  SeqInfo q;
+  Units() = default;
+  __device__ Units(const PagedShape& s, const PagedRows& c, int b)
+      : heads(c.Hv), count(0), open(kChOpen), U(2 * c.tpt), causal(s.causal), none(0), q(paged_seq(s, b)) {
+    count = c.by_tpt.div(q.Lq + U - 1) >> 1;
+    // With more tokens than keys the first units see no key: one empty tile each.
+    if (q.off < 0) none = c.by_tpt.div(-q.off) >> 1;
+  }
+  // Key tiles that token `last` of the sequence, and so any row before it, may see.
+  __device__ int tiles_to(int last) const {
+    const int keys = causal ? min(q.Lk, last + q.off + 1) : q.Lk;
+    return keys <= 0 ? 0 : (keys + 127) >> 7;
+  }
+  __device__ int tiles(int u) const { return max(1, tiles_to(min(q.Lq, (u + 1) * U) - 1)); }
+  __device__ long long before(int u) const {
+    long long sum = (long long)u * open;
+    if (!causal) return sum + (long long)u * max(1, tiles_to(q.Lq - 1));
+    int n = u;
+    if (u == count && u > 0) {
+      --n;
+      sum += tiles(n);
+    }
+    const int empty = min(n, none);
+    return sum + empty + floor_sum(n - empty, 128, U, q.off + (empty + 1) * U + 127);
+  }
+};
+
 struct ChCtl {
   uint64_t q_full, q_empty, k0_full, k0_empty;
   uint64_t full[4], empty[4];
@@ -46,6 +79,7 @@ struct ChCtl {
   int abort_flag;
   long long scan[11];
   Share share;
+  Units units;  // of the sequence where the share begins
   int issued_q[2], issued_k0[2], issued_t[2], issued_tail[2];  // copies issued, by producer (abort-path drain)
   int needs_p0[4];   // by stage buffer: tile 0's softmax arrives on its last stage
   int p0_last[128];  // by row of tile 0: the last stage its thread arrived on
@@ -62,37 +96,6 @@ struct ChWork {
   JoinDesc* desc;   // [CTAs]; b = -1: no unit ends here in pieces
 };
 
-// A unit's copies of Q and its epilogue take the time of about four key tiles.
-constexpr int kChOpen = 4;
-
-// The units of one sequence, for one head group: unit u has tokens [u U, u U + U).
-struct Units {
-  int heads, count, open, U, causal;
-  SeqInfo q;
-  __device__ Units(const PagedShape& s, const PagedRows& c, int b)
-      : heads(c.Hv), count(0), open(kChOpen), U(2 * c.tpt), causal(s.causal), q(paged_seq(s, b)) {
-    count = (q.Lq + U - 1) / U;
-  }
-  // Key tiles that token `last` of the sequence, and so any row before it, may see.
-  __device__ int tiles_to(int last) const {
-    const int keys = causal ? min(q.Lk, last + q.off + 1) : q.Lk;
-    return keys <= 0 ? 0 : (keys + 127) >> 7;
-  }
-  __device__ int tiles(int u) const { return max(1, tiles_to(min(q.Lq, (u + 1) * U) - 1)); }
-  __device__ long long before(int u) const {
-    long long sum = (long long)u * open;
-    if (!causal) return sum + (long long)u * max(1, tiles_to(q.Lq - 1));
-    int n = u;
-    if (u == count && u > 0) {
-      --n;
-      sum += tiles(n);
-    }
-    // The first units may see no key (more tokens than keys): one empty tile each.
-    const int none = q.off < 0 ? min(n, -q.off / U) : 0;
-    return sum + none + floor_sum(n - none, 128, U, q.off + (none + 1) * U + 127);
-  }
-};
-
 // The pieces of a CTA's share: key tiles [kt, end) of the n that unit u sees.
 struct ChPieces {
   const PagedShape& s;
@@ -104,11 +107,10 @@ struct ChPieces {
   __device__ ChPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh)
       : s(s_), c(c_), b(sh.b), hv(sh.head), u(sh.unit), kt(0), n(0), end(0), nu(0), todo(sh.todo), finished(false) {
     if (todo == 0) return;
-    sequence();
+    sequence(Units(s, c, b));
     open(sh.tile);
   }
-  __device__ void sequence() {  // looks at sequence b
-    const Units x(s, c, b);
+  __device__ void sequence(const Units& x) {
     seq = x.q;
     nu = x.count;
   }
@@ -137,7 +139,7 @@ struct ChPieces {
         hv = 0;
         do {  // todo > 0: a later sequence has units
           ++b;
-          sequence();
+          sequence(Units(s, c, b));
         } while (nu == 0);
       }
     }
@@ -208,12 +210,12 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
   __syncthreads();
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
-  find_share<C::kThreads>(s.B, [&](int b) { return Units(s, rows, b); }, ctl.share, ctl.scan);
+  find_share<C::kThreads>(s.B, [&](int b) { return Units(s, rows, b); }, ctl.share, ctl.scan, ctl.units);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  ChPieces w(s, rows, ctl.share);
+  ChPieces w(s, rows, ctl.share);  // (looks again: carrying ctl.units here spilled registers, 384 us for 376)
   if (threadIdx.x == 0) {
     JoinDesc d{};
     d.b = !w.done() && w.kt > 0 && w.end == w.n ? w.b : -1;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
                        "r"(y[4 * k]), "r"(y[4 * k + 1]), "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
                        : "memory");
         __syncwarp();
-#pragma unroll
+#pragma unroll 2  // (all 8 spill registers: 376 us for 371)
         for (int k = 0; k < 8; ++k) {
           const int row = 4 * k + (lane >> 3);
           uint4 z;

@@ -64,6 +64,22 @@ struct DecCfg {
   static constexpr uint32_t kIdPV = idesc_bf16(128, NP, true, true);
 };
 
+// A unit (sequence, K/V head) without keys still has a tile, which writes its zeros. Its epilogue takes
+// the time of about one tile (weighed as 1, 2 or 3: 48 sequences of 1024 keys, 12 heads of d = 64, in 34.4, 34.9
+// and 35.1 us).
+constexpr int kDecOpen = 1;
+
+struct DecUnits {
+  int heads, count, open;
+  SeqInfo q;
+  DecUnits() = default;
+  __device__ DecUnits(const PagedShape& s, int b) : heads(s.Hkv), count(0), open(kDecOpen), q(paged_seq(s, b)) {
+    count = q.Lq > 0;
+  }
+  __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
+  __device__ long long before(int u) const { return u * (tiles() + open); }
+};
+
 template <int NP>
 struct DecCtl {
   uint64_t q_full[2], q_empty[2];
@@ -76,26 +92,12 @@ struct DecCtl {
   int abort_flag;
   long long scan[18];
   Share share;
+  DecUnits units;  // of the sequence where the share begins
   int issued_q[2], issued_t[2];                   // copies issued, by producer (abort-path drain)
   alignas(16) float m[NP];
   alignas(16) float alpha[NP];
   float wmax[4][NP];
   int lim[NP];
-};
-
-// A unit (sequence, K/V head) without keys still has a tile, which writes its zeros. Its epilogue takes
-// the time of about one tile (weighed as 1, 2 or 3: 48 sequences of 1024 keys, 12 heads of d = 64, in 34.4, 34.9
-// and 35.1 us).
-constexpr int kDecOpen = 1;
-
-struct DecUnits {
-  int heads, count, open;
-  SeqInfo q;
-  __device__ DecUnits(const PagedShape& s, int b) : heads(s.Hkv), count(0), open(kDecOpen), q(paged_seq(s, b)) {
-    count = q.Lq > 0;
-  }
-  __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
-  __device__ long long before(int u) const { return u * (tiles() + open); }
 };
 
 // The pieces of a CTA's share: key tiles [kt, end) of the n of (b, hk), walked in order by every role.
@@ -105,14 +107,13 @@ struct Pieces {
   long long todo;  // positions from the piece on
   bool finished;
   SeqInfo seq;
-  __device__ Pieces(const PagedShape& s_, const Share& sh)
+  __device__ Pieces(const PagedShape& s_, const Share& sh, const DecUnits& first)
       : s(s_), b(sh.b), hk(sh.head), kt(0), n(0), end(0), todo(sh.todo), finished(false) {
     if (todo == 0) return;
-    sequence();
+    sequence(first);
     open(sh.tile);
   }
-  __device__ void sequence() {  // looks at sequence b
-    const DecUnits x(s, b);
+  __device__ void sequence(const DecUnits& x) {
     seq = x.q;
     n = x.count ? x.tiles() : 0;
   }
@@ -134,7 +135,7 @@ struct Pieces {
       hk = 0;
       do {  // todo > 0: a later sequence has new tokens
         ++b;
-        sequence();
+        sequence(DecUnits(s, b));
       } while (n == 0);
     }
     open(0);
@@ -231,16 +232,17 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
   if (wk.desc != nullptr) {
-    find_share<C::kThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan);
+    find_share<C::kThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan, ctl.units);
   } else if (threadIdx.x == 0) {  // a unit per CTA
     const DecUnits x(s, blockIdx.x / s.Hkv);
     ctl.share = Share{(int)blockIdx.x / s.Hkv, (int)blockIdx.x % s.Hkv, 0, 0, x.count ? x.before(1) : 0, 0, 0};
+    ctl.units = x;
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  Pieces w(s, ctl.share);
+  Pieces w(s, ctl.share, ctl.units);
   if (wk.desc != nullptr && threadIdx.x == 0) {
     const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
     wk.desc[2 * blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);

@@ -49,6 +49,37 @@ struct WCfg {
   static constexpr uint32_t kId = idesc_bf16(128, NP, false, false);
 };
 
+// One sequence's units, per K/V head: key tile kt is seen by the token tiles from first(kt) on, each
+// of per_kv groups.
+struct WUnits {
+  SeqInfo q;
+  int heads, count, open, ntt, tpt, per_kv, causal;
+  FastDiv by_tpt;
+  WUnits() = default;
+  __device__ WUnits(const PagedShape& s, const PagedRows& c, int b, int open_)
+      : q(paged_seq(s, b)),
+        heads(s.Hkv),
+        count(0),
+        open(open_),
+        ntt(c.by_tpt.div(q.Lq + c.tpt - 1)),
+        tpt(c.tpt),
+        per_kv(c.per_kv),
+        causal(s.causal),
+        by_tpt(c.by_tpt) {
+    if (q.Lq > 0) count = (q.Lk + 127) >> 7;
+  }
+  __device__ int first(int kt) const { return causal ? by_tpt.div(max(0, (kt << 7) - q.off)) : 0; }
+  __device__ int tiles(int kt) const { return per_kv * (ntt - first(kt)); }
+  __device__ long long before(int kt) const {
+    long long sum = (long long)kt * ntt;
+    if (causal) {
+      const int none = min(kt, max(0, (q.off + 127) >> 7));  // key tiles that every token sees whole
+      sum -= floor_sum(kt - none, tpt, 128, (none << 7) - q.off);
+    }
+    return sum * per_kv + (long long)kt * open;
+  }
+};
+
 template <int NP>
 struct WCtl {
   uint64_t k_full[12], k_empty[12], q_full[8], q_empty[8], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
@@ -56,6 +87,7 @@ struct WCtl {
   int abort_flag;
   long long scan[24];
   Share share;
+  WUnits units;                         // of the sequence where the share begins
   int issued_k[2], issued_q[2];         // copies issued, by producer (abort-path drain)
   alignas(16) float nlse[4][2][NP];  // -LSE (log2 units) of the rows, per group and parity; -inf: no weight
   alignas(16) int seen[4][2][NP];    // last key the row sees
@@ -71,34 +103,6 @@ struct WWork {
   WJoin* desc;   // [CTAs]; b = -1: no unit ends here in pieces
 };
 
-// One sequence's units, per K/V head: key tile kt is seen by the token tiles from first(kt) on, each
-// of per_kv groups.
-struct WUnits {
-  SeqInfo q;
-  int heads, count, open, ntt, tpt, per_kv, causal;
-  __device__ WUnits(const PagedShape& s, const PagedRows& c, int b, int open_)
-      : q(paged_seq(s, b)),
-        heads(s.Hkv),
-        count(0),
-        open(open_),
-        ntt((q.Lq + c.tpt - 1) / c.tpt),
-        tpt(c.tpt),
-        per_kv(c.per_kv),
-        causal(s.causal) {
-    if (q.Lq > 0) count = (q.Lk + 127) >> 7;
-  }
-  __device__ int first(int kt) const { return causal ? max(0, (kt << 7) - q.off) / tpt : 0; }
-  __device__ int tiles(int kt) const { return per_kv * (ntt - first(kt)); }
-  __device__ long long before(int kt) const {
-    long long sum = (long long)kt * ntt;
-    if (causal) {
-      const int none = min(kt, max(0, (q.off + 127) >> 7));  // key tiles that every token sees whole
-      sum -= floor_sum(kt - none, tpt, 128, (none << 7) - q.off);
-    }
-    return sum * per_kv + (long long)kt * open;
-  }
-};
-
 // The pieces of a CTA's share: query tiles [it, end) of the n that see key tile kt.
 template <bool FEW>
 struct WPieces {
@@ -110,9 +114,9 @@ struct WPieces {
   bool finished;
   int n, tt0;
   WUnits x;
-  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh, int open)
+  __device__ WPieces(const PagedShape& s_, const PagedRows& c_, const Share& sh, const WUnits& first)
       : s(s_), c(c_), b(sh.b), hk(sh.head), kt(sh.unit), it(0), end(0), todo(sh.todo), head(true),
-        finished(sh.todo == 0), n(0), tt0(0), x(s_, c_, sh.todo > 0 ? sh.b : 0, open) {
+        finished(sh.todo == 0), n(0), tt0(0), x(first) {
     if (todo > 0) unit(sh.tile);
   }
   __device__ void unit(int at) {  // opens unit kt at position `at` of it
@@ -121,8 +125,8 @@ struct WPieces {
       --todo;
       return;
     }
-    n = x.tiles(kt);
     tt0 = x.first(kt);
+    n = x.per_kv * (x.ntt - tt0);
     it = max(0, at - x.open);
     const long long stop = at + todo - x.open;
     end = stop < n ? (int)stop : n;
@@ -163,7 +167,7 @@ struct WPieces {
   // A query tile of the unit: its first token, and the first head of its group.
   struct Cursor {
     int tt, g;  // token tile, group
-    __device__ Cursor(const WPieces& w, int i) : tt(w.tt0 + i / w.c.per_kv), g(i % w.c.per_kv) {}
+    __device__ Cursor(const WPieces& w, int i) : tt(w.c.by_per_kv.div(i)), g(i - tt * w.c.per_kv) { tt += w.tt0; }
     __device__ void advance(const WPieces& w, int by) {
       for (g += by; g >= w.c.per_kv; g -= w.c.per_kv) ++tt;
     }
@@ -262,12 +266,12 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
   __syncthreads();
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
-  find_share<C::kThreads>(s.B, [&](int b) { return WUnits(s, rows, b, C::kOpen); }, ctl.share, ctl.scan);
+  find_share<C::kThreads>(s.B, [&](int b) { return WUnits(s, rows, b, C::kOpen); }, ctl.share, ctl.scan, ctl.units);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  WPieces<C::kFew> w(s, rows, ctl.share, C::kOpen);
+  WPieces<C::kFew> w(s, rows, ctl.share, ctl.units);
   if (!C::kFew && threadIdx.x == 0) {
     WJoin d{};
     d.b = !w.done() && w.it > 0 && w.end == w.n ? w.b : -1;
@@ -471,21 +475,30 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
         __syncwarp();
       }
     } else {
-      for (int piece = 0; !w.done(); ++piece, w.next()) {
-        int i = w.it + (gr + C::kGroups - t % C::kGroups) % C::kGroups;  // this group's first tile of the piece
-        const int t0 = t;
+      // The LSE of a piece's first tile is on its way while the sums of the piece before are handed over.
+      typename WPieces<C::kFew>::Cursor at(w, 0);
+      float lse = 0.f;
+      int i = 0;
+      auto first_tile = [&]() {
+        i = w.it + (gr + C::kGroups - t % C::kGroups) % C::kGroups;  // this group's first tile of the piece
+        at = typename WPieces<C::kFew>::Cursor(w, i);
+        if (i < w.end) lse = load_lse(at.token(w), at.head0(w));
+      };
+      if (!w.done()) first_tile();
+      for (int piece = 0; !w.done(); ++piece) {
+        const int t0 = t - w.it;
         float sum = 0.f;
-        typename WPieces<C::kFew>::Cursor at(w, i);
-        float lse = i < w.end ? load_lse(at.token(w), at.head0(w)) : 0.f;
         for (; i < w.end; i += C::kGroups) {
-          t = t0 + (i - w.it);
+          t = t0 + i;
           const int token = at.token(w);
           stage_lse(token, lse);
           at.advance(w, C::kGroups);
           if (i + C::kGroups < w.end) lse = load_lse(at.token(w), at.head0(w));
           sum += tile(token);
         }
-        t = t0 + (w.end - w.it);
+        t = t0 + w.end;
+        w.next();
+        if (!w.done()) first_tile();
         const int pp = piece & 1;
         if (run && piece >= 2) run = mbar_wait(bar(ctl.sum_free[pp]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
         ctl.sums[pp][gr][r] = sum;
@@ -586,7 +599,7 @@ template <int D>
 cudaError_t launch_weights_d(const FaPagedArgs& a, cudaStream_t st) {
   const int G = a.s.H / a.s.Hkv;
   if (!paged_few_rows(a.s)) return launch_weights<D, 128>(a, paged_rows_for(a.s), st);
-  const PagedRows few{G, a.s.Hkv, 1, a.s.Nq};  // all rows of a K/V head in one tile
+  const PagedRows few = paged_rows(G, a.s.Hkv, 1, a.s.Nq);  // all rows of a K/V head in one tile
   const int n = a.s.Nq * G;
   return n <= 16 ? launch_weights<D, 16>(a, few, st)
          : n <= 32 ? launch_weights<D, 32>(a, few, st)
