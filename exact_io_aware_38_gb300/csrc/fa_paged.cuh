@@ -105,6 +105,41 @@ inline PagedRows paged_rows_for(const PagedShape& s) {
 // weights 50 and 87, 31 and 48. Four rows: 87 and 119, 51 and 99.
 inline bool paged_few_rows(const PagedShape& s) { return (long long)s.Nq * (s.H / s.Hkv) <= 64; }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A load from the shared memory of CTA `cta` of the cluster, at the address that `p` has there.
+__device__ __forceinline__ int load_peer(const int* p, uint32_t cta) {
+  uint32_t at;
+  int x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(cta));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ float load_peer(const float* p, uint32_t cta) {
+  return __int_as_float(load_peer(reinterpret_cast<const int*>(p), cta));
+}
+__device__ __forceinline__ float4 load_peer4(const float* p, uint32_t cta) {
+  uint32_t at;
+  float4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(cta));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
+}
+
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // sum of floor((a i + b) / m) for 0 <= i < n, by Euclid's steps on (a, m), or without a division where both are powers

@@ -84,28 +84,6 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const FaPagedArgs a) 
 
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32, kSelRow = 4 * kSelThreads;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// A load from the shared memory of CTA `cta` of the cluster, at the address that `p` has there.
-__device__ __forceinline__ int load_peer(const int* p, uint32_t cta) {
-  uint32_t at;
-  int x;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(cta));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-  return x;
-}
-
 // The order of weights as unsigned integers: larger weight, larger number; -0 equals 0, NaN is 0.
 __device__ __forceinline__ uint32_t weight_rank(float w) {
   if (w != w) return 0u;

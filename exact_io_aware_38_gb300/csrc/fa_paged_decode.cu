@@ -15,7 +15,8 @@
 // the CTAs (one or two per SM, persistent) divide evenly, whatever the lengths are. A CTA's share
 // begins and ends inside a (sequence, head) at most twice; those pieces leave normalised fp32
 // partials (two slots per CTA) that the merge kernel joins by their log-sum-exp; whole ones are
-// written directly.
+// written directly. Few (sequence, head) units of not too many tiles are shared by a cluster each instead, whose
+// CTAs join their parts through shared memory: one launch, no workspace and no search for the share.
 //
 // Roles: warp 0 and at d = 128 the last warp read the page table and copy (TMA, a lane per page; 64 columns
 // each, since a warp issues a copy per ~100 cycles and small pages need many: 16 x 8192 keys in pages of 16 in
@@ -31,6 +32,7 @@ namespace {
 
 using namespace tc;
 
+constexpr int kDecCluster = 8;       // CTAs of the largest cluster that shares a unit
 constexpr float kNoMax = -3.0e38f;   // reference max of a row that has seen no key
 constexpr float kRaise = 8.f;       // log2 units a score may exceed the reference by
 
@@ -56,7 +58,7 @@ struct DecCfg {
   static constexpr int kPBytes = (NP == 64 ? 2 : 1) * 128 * 128;
   static constexpr int kPStep = NP == 64 ? 128 * 128 : NP * 2;
   static constexpr int kSmem = kQBufs * kQBytes + (kKStages + kVStages) * kTileBytes + kPBytes + 1024;
-  static_assert(kCtas * (kSmem + 576 + 36 * NP + 1024) <= 228 * 1024, "with the control block");
+  static_assert(kCtas * (kSmem + 576 + 32 * NP + 1024) <= 228 * 1024, "with the control block");
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : 256;  // S x 2, O x 2
   static constexpr uint32_t kIdS = idesc_bf16(128, NP, false, false);
   // O^T = V^T P^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared
@@ -97,6 +99,7 @@ struct DecCtl {
   alignas(16) float m[NP];
   alignas(16) float alpha[NP];
   float wmax[4][NP];
+  float part_lse[NP];  // log2 units, of this CTA's part of a unit that a cluster shares
   int lim[NP];
 };
 
@@ -172,7 +175,7 @@ struct DecWork {
   float* part_o;    // [2 CTAs][NP][D]
   float* part_lse;  // [2 CTAs][NP], log2 units
   int4* desc;       // [CTAs][2]: {b, hk, first CTA, its slot}, {L_q, q0, bb, 0} of the sequence; b = -1: no (sequence,
-                    // head) ends here in pieces. Null: every (sequence, head) has a CTA of its own
+                    // head) ends here in pieces. Null: every (sequence, head) has a CTA or a cluster of its own
 };
 
 template <int D, int NP>
@@ -185,6 +188,7 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
   const uint32_t sK0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sV0 = sK0 + C::kKStages * C::kTileBytes, sP = sV0 + C::kVStages * C::kTileBytes;
   const uint32_t sQ = sP + C::kPBytes;
+  float* my_part = reinterpret_cast<float*>(smem_raw + (sK0 - smem_u32(smem_raw)));
   volatile int* abort_flag = &ctl.abort_flag;
   const PagedShape& s = a.s;
   const int G = s.H / s.Hkv;
@@ -216,6 +220,7 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  if (threadIdx.x < NP) ctl.part_lse[threadIdx.x] = -INFINITY;
   if (warp == 1) {
     tmem_alloc(smem_u32(&ctl.tmem_base), C::kTmemCols);
     tmem_relinquish();
@@ -231,11 +236,14 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
   __syncthreads();
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
+  const int ctas = wk.desc != nullptr ? 1 : (int)cluster_size();  // that share a unit
   if (wk.desc != nullptr) {
     find_share<C::kThreads>(s.B, [&](int b) { return DecUnits(s, b); }, ctl.share, ctl.scan, ctl.units);
-  } else if (threadIdx.x == 0) {  // a unit per CTA
-    const DecUnits x(s, blockIdx.x / s.Hkv);
-    ctl.share = Share{(int)blockIdx.x / s.Hkv, (int)blockIdx.x % s.Hkv, 0, 0, x.count ? x.before(1) : 0, 0, 0};
+  } else if (threadIdx.x == 0) {  // tiles [n rank / ctas, n (rank + 1) / ctas) of the cluster's unit
+    const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv;
+    const DecUnits x(s, b);
+    const int n = x.count ? x.tiles() : 0, lo = n * rank / ctas, hi = n * (rank + 1) / ctas;
+    ctl.share = Share{b, unit - b * s.Hkv, 0, kDecOpen + lo, hi - lo, 0, 0};
     ctl.units = x;
   }
   fence_before_sync();
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
       columns_reduce(l, lane, [](float p, float q) { return p + q; });
       ctl.wmax[quad][n0 + (lane >> 1)] = l[0];
       named_bar_sync(on, 128);
-      const bool whole = w.whole();
+      const bool whole = w.whole() && ctas == 1;
       const int slot = 2 * blockIdx.x + (piece == 0 ? 0 : 1);
       if (r < NC) {
         const int n = n0 + r;
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
         if (whole) {
           if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n % G, n / G)] = lse2 * kLn2;
         } else {
-          wk.part_lse[(size_t)slot * NP + n] = lse2;
+          (ctas > 1 ? ctl.part_lse : wk.part_lse + (size_t)slot * NP)[n] = lse2;
         }
       }
       __syncwarp();
@@ -512,7 +520,8 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
       if (run) run = wait_pv(t - 1);
       fence_after_sync();
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0, w.hk * G) + r;
-      float* part = wk.part_o + (size_t)slot * NP * D + r;
+      // (the cluster's parts lie over the ring: with the last P V done nothing reads it or is on its way there)
+      float* part = (ctas > 1 ? my_part : wk.part_o + (size_t)slot * NP * D) + r;
       int i = n0 / G, g = n0 % G;  // token and head of the group of column n
       uint32_t o[NC];
       tmem_ld16(tO, o);
@@ -546,6 +555,35 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
     fence_after_sync();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if (ctas > 1) {
+    // The cluster's CTAs join their parts, each some of the elements: M = max LSE, w = 2^(LSE - M), O = sum w O / sum w.
+    cluster_sync();
+    const SeqInfo& seq = ctl.units.q;
+    const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv, hk = unit - b * s.Hkv;
+    for (int x = rank * C::kThreads + threadIdx.x; x < seq.Lq * G * (D / 4); x += ctas * C::kThreads) {
+      const int n = x / (D / 4), e = x % (D / 4) * 4, i = n / G, h = hk * G + n - i * G;
+      float l[kDecCluster], M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kDecCluster; ++c) {
+        l[c] = c < ctas ? load_peer(ctl.part_lse + n, c) : -INFINITY;
+        M = fmaxf(M, l[c]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kDecCluster; ++c)
+        if (l[c] != -INFINITY) {
+          const float wt = exp2f(l[c] - M);
+          const float4 o = load_peer4(my_part + n * D + e, c);
+          sum += wt;
+          acc = make_float4(acc.x + wt * o.x, acc.y + wt * o.y, acc.z + wt * o.z, acc.w + wt * o.w);
+        }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (e == 0) a.lse[paged_row(s, seq, b, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    cluster_sync();  // no CTA leaves while its part is read
+  }
   if (threadIdx.x == 0 && *abort_flag) {
     // Copies still in flight land before the CTA exits: the last one issued into each buffer. A producer that stopped
     // before the other did has its arrival made here.
@@ -565,34 +603,43 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
   }
 }
 
-// Joins the pieces of each divided (sequence, head). Block c takes the one that ends in CTA c's first
-// piece, if it began before.
+// Joins the pieces of each divided (sequence, head). Block (c, y) takes 16 rows of the one that ends in CTA c's
+// first piece, if it began before; a thread has four elements of a row.
 template <int D, int NP>
-__global__ void __launch_bounds__(256) paged_join_kernel(const FaPagedArgs a, const DecWork wk) {
+__global__ void __launch_bounds__(4 * D) paged_join_kernel(const FaPagedArgs a, const DecWork wk) {
   let_dependent_start();
   grid_dependency_wait();
   const int4 d = wk.desc[2 * blockIdx.x], of = wk.desc[2 * blockIdx.x + 1];
-  if (d.x < 0) return;
   const PagedShape& s = a.s;
+  const int G = s.H / s.Hkv, n = blockIdx.y * 16 + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4;
+  if (d.x < 0 || n >= of.x * G) return;
   SeqInfo seq{};
   seq.Lq = of.x;
   seq.q0 = of.y;
   seq.bb = of.z;
-  const int G = s.H / s.Hkv, c1 = blockIdx.x;
-  for (int x = threadIdx.x; x < seq.Lq * G * (D / 4); x += 256) {
-    const int n = x / (D / 4), e = x % (D / 4) * 4;
-    join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, c1, d.w, n, e, seq, d.x, n / G, d.y * G + n % G);
-  }
+  join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, blockIdx.x, d.w, n, e, seq, d.x, n / G, d.y * G + n % G);
 }
 
 int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// Short keys and few (sequence, head) units: a CTA takes a whole one. A tile more costs about 1.2 us there,
-// the search for shares and the merge launch 4 us and a workspace (one sequence of 777 keys, 7 tiles: 16.0 us
-// undivided, 10.2 us divided).
-bool undivided(const PagedShape& s, int num_sms) {
-  const int np = padded_rows(s.Nq * (s.H / s.Hkv));
-  return s.max_k <= 3 * 128 && (long long)s.B * s.Hkv <= (long long)num_sms * dec_ctas(s.d, np);
+// CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0. Alone up to two tiles (one
+// sequence of 8 K/V heads, d = 128, 250 keys: 6.8 us with 1 CTA a unit, 7.1 with 2, 7.6 with 8, 8.4 divided), else the
+// largest cluster that does not outnumber the tiles twice and of which all run at once (16 clusters of 8 do not, 15.9
+// us for 8.5), and at most four tiles a CTA (777 keys: 8.5 us with 8, 8.9 with 4, 9.6 divided; 4096 keys: 11.1 with 8, 11.6
+// divided; 8192 keys: 15.4 and 13.6).
+int unit_ctas(const PagedShape& s, int num_sms) {
+  const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * dec_ctas(s.d, padded_rows(s.Nq * (s.H / s.Hkv)));
+  const int tiles = (s.max_k + 127) >> 7;
+  int ctas = 1;
+  if (tiles > 2) {
+    if (tiles > 4 && units * 8 * 3 <= room * 2)
+      ctas = 8;
+    else if (units * 4 * 8 <= room * 7)
+      ctas = 4;
+    else if (units * 2 <= room)
+      ctas = 2;
+  }
+  return units * ctas <= room && tiles <= 4 * ctas ? ctas : 0;
 }
 
 template <int D, int NP>
@@ -608,10 +655,9 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
       !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128) ||
       !fa_make_tmap_bf16(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, P < 128 ? P : 128))
     return cudaErrorInvalidValue;
-  const bool whole = undivided(s, a.num_sms);
-  const int ctas = whole ? s.B * s.Hkv : a.num_sms * C::kCtas;
+  const int shared = unit_ctas(s, a.num_sms), ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
   DecWork wk{};
-  if (!whole) {
+  if (shared == 0) {
     char* ws = static_cast<char*>(a.workspace);
     wk.desc = reinterpret_cast<int4*>(ws);
     ws += up256((size_t)ctas * 2 * sizeof(int4));
@@ -624,16 +670,18 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (C::kCtas > 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
+  if (shared > 0)
+    return launch_dependent_cluster(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, shared, st, tq, tk, tv, a, wk);
   e = launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tq, tk, tv, a, wk);
-  if (e != cudaSuccess || whole) return e;
-  return launch_dependent(paged_join_kernel<D, NP>, dim3(ctas), dim3(256), 0, st, a, wk);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_join_kernel<D, NP>, dim3(ctas, NP / 16), dim3(4 * D), 0, st, a, wk);
 }
 
 }  // namespace
 }  // namespace fa
 
 size_t fa_paged_decode_workspace(const fa::PagedShape& s, int num_sms) {
-  if (fa::undivided(s, num_sms)) return 0;
+  if (fa::unit_ctas(s, num_sms) > 0) return 0;
   const int np = fa::padded_rows(s.Nq * (s.H / s.Hkv));
   const size_t ctas = (size_t)num_sms * fa::dec_ctas(s.d, np), rows = ctas * 2 * np;
   return fa::up256(ctas * 2 * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);

@@ -34,20 +34,20 @@ lens = torch.tensor([L, 300, 1], dtype=torch.int32, device="cuda")
 for d in (64, 128):
     k, v = rand(pages, P, Hkv, d), rand(pages, P, Hkv, d)
     w = torch.zeros(pages, Hkv, P, device="cuda")
-    for n in (1, 100):
+    for n, sms in ((1, None), (1, 4), (100, None)):  # few rows by clusters and divided, many rows
         q = rand(B, n, Hkv * G, d)
-        want = fa.fwd_paged(q, k, v, table, lens, causal=True)
+        want = fa.fwd_paged(q, k, v, table, lens, causal=True, num_sms=sms)
         for call in ("attend", "weights"):
             status = torch.zeros(1, dtype=torch.int32, device="cuda")
             fa._lib = broken
             if call == "attend":
-                fa.fwd_paged(q, k, v, table, lens, causal=True, status=status)
+                fa.fwd_paged(q, k, v, table, lens, causal=True, status=status, num_sms=sms)
             else:
-                fa.paged_key_weights(q, k, table, lens, want[1], w, causal=True, status=status)
+                fa.paged_key_weights(q, k, table, lens, want[1], w, causal=True, status=status, num_sms=sms)
             torch.cuda.synchronize()
             fa._lib = real
             assert int(status.item()) == -5, (d, n, call, int(status.item()))
-            got = fa.fwd_paged(q, k, v, table, lens, causal=True)
+            got = fa.fwd_paged(q, k, v, table, lens, causal=True, num_sms=sms)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (d, n, call)
 print("CHILD_OK")
 '''

@@ -79,7 +79,7 @@ def test_buffer_refusals():
 
 
 @pytest.mark.parametrize("call,size,kw", [
-    (attend, "fa_fwd_paged_workspace_bytes", dict(max_pages=1000, seqlen_k=4000)),
+    (attend, "fa_fwd_paged_workspace_bytes", dict(max_pages=1000, seqlen_k=9000)),
     (attend, "fa_fwd_paged_workspace_bytes", dict(B=200)),
     (attend, "fa_fwd_paged_workspace_bytes", dict(seqlen_q=500)),
     (weights, "fa_paged_key_weights_workspace_bytes", dict(seqlen_q=500))])
