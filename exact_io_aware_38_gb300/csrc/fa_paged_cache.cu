@@ -119,7 +119,8 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_tot, int& total) {
 // weight is found 8 bits at a time from the top, in four passes of a histogram in shared memory (summed
 // over the cluster) of which each thread scans a bin. Then a key's place is the number of larger weights
 // before it plus that of equal ones, as far as those stay, by a scan over threads and rows in key order.
-// Bound by latency: counting against bounds instead, 16 steps of 2 bits, took 13 us for 1030 keys.
+// Bound by latency: 4.5 us for 8 heads of 1030 keys, 11 for 12 x 8 of up to 8192; counting against bounds instead, 16
+// steps of 2 bits, took 13 us for the former.
 template <int R>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPagedArgs a) {
   let_dependent_start();
@@ -286,7 +287,8 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPaged
 // One cluster per (sequence, K/V head, K or V). The kept rows move down in blocks of the cluster's
 // shared memory: every row of a block is read before any is written, and since kept[t] >= t a block's
 // destinations hold no row that a later block still has to read. A row that keeps its place is not
-// moved. Bound by memory, with the latency of index, page and row once per block.
+// moved. Bound by memory, with the latency of index, page and row once per block: 12 x 8 heads of up to 8192 keys
+// down to 2050, 211 MB in 35 us, 6.0 TB/s (blocks of 128 rows a CTA: 39, of 64: 44).
 constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveRows = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {  // per: rows a CTA takes of a block

@@ -16,6 +16,12 @@
 // per ~100 cycles, and small pages need many: 2048 tokens over 16384 keys in pages of 16 take 377 us, with one
 // warp 561), warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of tile 0 and tile 1. Copies run ahead
 // across units. Stage t of the ring holds V of key tile t and K of key tile t + 1.
+//
+// Measured: 2048 tokens over 16384 keys, 32 heads over 8 of d = 128: 370 us, 1390 TFLOP/s, the tensor pipe 61% busy: a
+// pair of query tiles takes 3214 cycles a key tile, of which its products are 2048; the softmax step is the
+// length, as in the forward over contiguous tensors. Six sequences of 1 to 509 tokens over up to 6001 keys: 125 us, 930
+// TFLOP/s (shares of 55 key tiles; 15000 cycles each until their first keys are no longer read from DRAM).
+//
 // Tensor memory: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P over S.
 #include "fa_paged.cuh"
 #include "fa_softmax.cuh"
@@ -37,7 +43,8 @@ struct ChCfg {
   static constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
 };
 
-// A unit's copies of Q and its epilogue take the time of about four key tiles.
+// A unit's copies of Q and its epilogue take the time of about four key tiles (weighed as 1, 2, 3, 4, 6: a mixed batch
+// 127, 125, 134, 125 and 125 us, 2048 tokens over 16384 keys 374, 370, 370, 369 and 370).
 constexpr int kChOpen = 4;
 
 // The units of one sequence, for one head group: unit u has tokens [u U, u U + U).

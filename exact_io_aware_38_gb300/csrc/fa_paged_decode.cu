@@ -6,6 +6,9 @@
 // products cost N = 16, 32 or 64 columns instead of a 128-row tile that would be nearly empty, and a
 // softmax thread handles 16 numbers per tile instead of 128. P^T goes back through shared memory
 // (bf16, keys x rows) and O^T += V^T P^T accumulates in tensor memory, a head dimension per lane.
+// Measured: 32 sequences of up to 8192 keys, 32 heads over 8 of d = 128, one token: 824 MB in 132 us, 6.2 TB/s (94% of the
+// copy rate); 48 of up to 1024 keys, 12 heads of d = 64: 116 MB in 33 us (a share has 13 tiles and 2.6 units' borders);
+// one sequence of 777 keys: 8.4 us, latency.
 // The exponentials are taken against a reference max per row, set by the row's first tile and raised
 // (O and the row sums rescaled) only when a score exceeds it by more than 2^8: exact, since fp32 and bf16
 // keep their relative precision over that range (a wider one would leave values near the top of bf16

@@ -18,6 +18,10 @@
 // warps (three, with many rows four) take the query tiles in turn; with many rows a last group adds their
 // sums of a finished unit to the weights, so that no exponential waits for that read and write.
 // Tensor memory: four score buffers of NP columns.
+//
+// Measured: 16 sequences of up to 8192 keys, one token, 32 heads over 8 of d = 128: 216 MB in 41 us, 5.3 TB/s (79% of
+// the copy rate; 4 us until the first keys arrive). 700 tokens over 8192 keys: 51 us, 870 TFLOP/s, the tensor and the
+// exponential pipe busy 39% each: 900 cycles a tile of 128 x 128, of which either needs 512.
 #include "fa_paged.cuh"
 #include "fa_tmap.h"
 #include "sm103_ptx.cuh"
@@ -26,7 +30,6 @@ namespace fa {
 namespace {
 
 using namespace tc;
-
 
 // NP: rows of a query tile (columns of S^T); FEW: one query tile holds all rows of a K/V head (NP <=
 // 64), stays in shared memory for all key tiles of the head and the ring holds K; else the ring
@@ -43,7 +46,8 @@ struct WCfg {
   static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128 + 32) + 32 * (D / 64 - 1);
   static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 2) * (128 / D);
   static constexpr int kQBufs = kFew ? 2 : 4 * (128 / D);  // (even: a buffer has one issuer, which sees its every phase)
-  static constexpr int kOpen = kFew ? 0 : 3;
+  // A unit's sums and hand-over, in query tiles (weighed as 1, 2, 3, 4: 51.3, 51.6, 52.1 and 53.4 us).
+  static constexpr int kOpen = kFew ? 0 : 1;
   static constexpr int kSmem = kKBufs * kKBytes + kQBufs * kQBytes + 1024;
   static constexpr uint32_t kTmemCols = NP == 16 ? 64 : NP == 32 ? 128 : NP == 64 ? 256 : 512;
   static constexpr uint32_t kId = idesc_bf16(128, NP, false, false);
