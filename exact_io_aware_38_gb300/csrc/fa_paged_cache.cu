@@ -113,7 +113,7 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_tot, int& total) {
   return before;
 }
 
-// One cluster per (sequence, K/V head). A row is 1024 consecutive keys, four to a thread (a page holds
+// A cluster (or one CTA) selects the keys of a (sequence, K/V head) into `kept`. A row is 1024 consecutive keys, four to a thread (a page holds
 // them together, so one table entry and one 16-byte load fetch them); a thread keeps R rows' weights as
 // ranks in registers and reads those of further rows again in each pass. The rank of the last kept
 // weight is found 8 bits at a time from the top, in four passes of a histogram in shared memory (summed
@@ -122,24 +122,15 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_tot, int& total) {
 // Bound by latency: 4.5 us for 8 heads of 1030 keys, 11 for 12 x 8 of up to 8192; counting against bounds instead, 16
 // steps of 2 bits, took 13 us for the former.
 template <int R>
-__global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPagedArgs a) {
-  let_dependent_start();
-  grid_dependency_wait();
+__device__ __forceinline__ void select_keys(const FaPagedArgs& a, int b, int hk, int L, uint32_t cta, uint32_t ctas,
+                                            int32_t* kept) {
   __shared__ int hist[2][256];
   __shared__ int warp_tot[kSelWarps];
   __shared__ int s_digit, s_need;
   __shared__ int cta_tot;  // this CTA's larger and equal weights, packed below
   __shared__ int cta_eq;
   const PagedShape& s = a.s;
-  const uint32_t cta = cluster_rank(), ctas = cluster_size();
-  const int head = blockIdx.x / ctas, hk = head % s.Hkv, b = head / s.Hkv, tid = threadIdx.x;
-  const int L = paged_seq(s, b).Lk;
-  int32_t* kept = a.kept + (size_t)head * a.keep;
-  if (hk == 0 && cta == 0 && tid == 0) a.seqlens_out[b] = min(L, a.keep);
-  if (L <= a.keep) {  // (the whole cluster)
-    for (int t = cta * kSelThreads + tid; t < a.keep; t += ctas * kSelThreads) kept[t] = t < L ? t : -1;
-    return;
-  }
+  const int tid = threadIdx.x;
   const int old = L - a.recent, take = a.keep - a.recent;  // candidates, and how many of them stay
   for (int t = cta * kSelThreads + tid; t < a.recent; t += ctas * kSelThreads) kept[take + t] = old + t;
   if (take == 0) return;
@@ -284,47 +275,66 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPaged
   for (int k = R; k < rows; ++k) place(ranks_at(k, page_at(k)), k);
 }
 
-// One cluster per (sequence, K/V head, K or V). The kept rows move down in blocks of the cluster's
-// shared memory: every row of a block is read before any is written, and since kept[t] >= t a block's
-// destinations hold no row that a later block still has to read. A row that keeps its place is not
-// moved. Bound by memory, with the latency of index, page and row once per block: 12 x 8 heads of up to 8192 keys
-// down to 2050, 211 MB in 35 us, 6.0 TB/s (blocks of 128 rows a CTA: 39, of 64: 44).
-constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveRows = 256;
+// The end of a selection that needs none: the lengths, and all keys of a sequence within the budget. True then.
+__device__ __forceinline__ bool keeps_all(const FaPagedArgs& a, int b, int hk, int L, uint32_t cta, uint32_t ctas,
+                                          int32_t* kept) {
+  if (hk == 0 && cta == 0 && threadIdx.x == 0) a.seqlens_out[b] = min(L, a.keep);
+  if (L > a.keep) return false;
+  for (int t = cta * kSelThreads + threadIdx.x; t < a.keep; t += ctas * kSelThreads) kept[t] = t < L ? t : -1;
+  return true;
+}
 
-__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {  // per: rows a CTA takes of a block
+template <int R>
+__global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const FaPagedArgs a) {
   let_dependent_start();
   grid_dependency_wait();
-  extern __shared__ __align__(16) uint8_t rows_smem[];
-  __shared__ const __nv_bfloat16* from[256];  // of a row of the block; null: it keeps its place
-  __shared__ __nv_bfloat16* to[256];
   const PagedShape& s = a.s;
-  const int cta = (int)cluster_rank(), unit = blockIdx.x / kMoveCtas;
-  const bool is_v = unit & 1;
-  const int head = unit >> 1, hk = head % s.Hkv, b = head / s.Hkv;
-  if (paged_seq(s, b).Lk <= a.keep) return;  // (the whole cluster)
-  const int32_t* kept = a.kept + (size_t)head * a.keep;
-  const FaStrides& ts = is_v ? a.sv : a.sk;
-  __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v : a.k);
+  const uint32_t cta = cluster_rank(), ctas = cluster_size();
+  const int head = blockIdx.x / ctas, hk = head % s.Hkv, b = head / s.Hkv, L = paged_seq(s, b).Lk;
+  int32_t* kept = a.kept + (size_t)head * a.keep;
+  if (!keeps_all(a, b, hk, L, cta, ctas, kept)) select_keys<R>(a, b, hk, L, cta, ctas, kept);  // (the whole cluster)
+}
+
+// The kept rows of T tensors (K, V, or both; the weights go with K) move down in blocks of a cluster's shared
+// memory: every row of a block is read before any is written, and since kept[t] >= t a block's destinations hold no
+// row that a later block still has to read. A row that keeps its place is not moved. Bound by memory, with the
+// latency of index, page and row once per block: 12 x 8 heads of up to 8192 keys down to 2050, 211 MB in 35 us, 6.0
+// TB/s (blocks of 128 rows a CTA: 39, of 64: 44).
+constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveRows = 256;
+
+template <int T>
+__device__ __forceinline__ void move_rows(const FaPagedArgs& a, int b, int hk, int tensor, int cta, int per,
+                                          const int32_t* kept, uint8_t* rows_smem) {  // per: rows a CTA takes of a block
+  __shared__ const __nv_bfloat16* from[kMoveRows];  // of a row of the block (T = 2: K's, then V's); null: it stays
+  __shared__ __nv_bfloat16* to[kMoveRows];
+  const PagedShape& s = a.s;
   const int shift = s.d == 128 ? 4 : 3, mask = (1 << s.page_shift) - 1;  // 16-byte chunks of a row
   for (int t0 = cta * per; t0 - cta * per < a.keep; t0 += kMoveCtas * per) {
     const int n = max(0, min(per, a.keep - t0));  // this CTA's rows of the block (none or fewer at the end)
     float w = 0.f, *wt = nullptr;
     __syncthreads();  // the last block's rows are written
-    if ((int)threadIdx.x < n) {
-      const int t = t0 + threadIdx.x, j = kept[t];
-      const int pt = paged_page(s, b, t >> s.page_shift, a.status);
-      const int pj = paged_page(s, b, j >> s.page_shift, a.status);
-      const bool moves = j != t && pt >= 0 && pj >= 0;
-      from[threadIdx.x] = moves ? base + paged_offset(ts, pj, j & mask, hk) : nullptr;
-      to[threadIdx.x] = base + paged_offset(ts, max(pt, 0), t & mask, hk);
-      if (!is_v && moves) {
-        w = a.weights[weight_offset(s, pj, hk, j & mask)];
-        wt = a.weights + weight_offset(s, pt, hk, t & mask);
+    if ((int)threadIdx.x < T * per) {
+      const int is_v = T == 1 ? tensor : (int)threadIdx.x >= per, i = threadIdx.x - (T == 1 ? 0 : is_v * per);
+      from[threadIdx.x] = nullptr;
+      if (i < n) {
+        const FaStrides& ts = is_v ? a.sv : a.sk;
+        __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v : a.k);
+        const int t = t0 + i, j = kept[t];
+        const int pt = paged_page(s, b, t >> s.page_shift, a.status);
+        const int pj = paged_page(s, b, j >> s.page_shift, a.status);
+        const bool moves = j != t && pt >= 0 && pj >= 0;
+        if (moves) from[threadIdx.x] = base + paged_offset(ts, pj, j & mask, hk);
+        to[threadIdx.x] = base + paged_offset(ts, max(pt, 0), t & mask, hk);
+        if (!is_v && moves) {
+          w = a.weights[weight_offset(s, pj, hk, j & mask)];
+          wt = a.weights + weight_offset(s, pt, hk, t & mask);
+        }
       }
     }
     __syncthreads();
+    const int chunks = (T == 1 ? n : T * per) << shift;
 #pragma unroll 4
-    for (int c = threadIdx.x; c < n << shift; c += kMoveThreads) {
+    for (int c = threadIdx.x; c < chunks; c += kMoveThreads) {
       const __nv_bfloat16* p = from[c >> shift];
       if (p != nullptr)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(rows_smem + c * 16)),
@@ -335,12 +345,51 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedA
     __syncthreads();
     cluster_sync();
 #pragma unroll 4
-    for (int c = threadIdx.x; c < n << shift; c += kMoveThreads)
+    for (int c = threadIdx.x; c < chunks; c += kMoveThreads)
       if (from[c >> shift] != nullptr)
         *reinterpret_cast<uint4*>(to[c >> shift] + (c & ((1 << shift) - 1)) * 8) =
             *reinterpret_cast<const uint4*>(rows_smem + c * 16);
     if (wt != nullptr) *wt = w;
   }
+}
+
+// One cluster per (sequence, K/V head, K or V).
+__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {
+  let_dependent_start();
+  grid_dependency_wait();
+  extern __shared__ __align__(16) uint8_t rows_smem[];
+  const PagedShape& s = a.s;
+  const int unit = blockIdx.x / kMoveCtas, head = unit >> 1, hk = head % s.Hkv, b = head / s.Hkv;
+  if (paged_seq(s, b).Lk <= a.keep) return;  // (the whole cluster)
+  move_rows<1>(a, b, hk, unit & 1, (int)cluster_rank(), per, a.kept + (size_t)head * a.keep, rows_smem);
+}
+
+// Both in one launch, for short sequences: one cluster per (sequence, K/V head), of which each CTA selects all keys by
+// itself (into its shared memory, without a cluster barrier) and moves its rows of K and V. The weights that the
+// others still read are written after the move's barrier only.
+constexpr int kEvictRows = 2;  // rows of 1024 candidates at most
+
+__global__ void __launch_bounds__(kMoveThreads) paged_evict_kernel(const FaPagedArgs a, int per) {
+  let_dependent_start();
+  grid_dependency_wait();
+  extern __shared__ __align__(16) uint8_t rows_smem[];
+  const PagedShape& s = a.s;
+  const int cta = (int)cluster_rank(), head = blockIdx.x / kMoveCtas, hk = head % s.Hkv, b = head / s.Hkv;
+  const int L = paged_seq(s, b).Lk;
+  int32_t* kept = a.kept + (size_t)head * a.keep;
+  if (keeps_all(a, b, hk, L, cta, kMoveCtas, kept)) return;  // (the whole cluster)
+  int32_t* mine = reinterpret_cast<int32_t*>(rows_smem + (size_t)2 * per * s.d * 2);
+  select_keys<kEvictRows>(a, b, hk, L, 0, 1, mine);
+  __syncthreads();
+  for (int t = cta * kMoveThreads + threadIdx.x; t < a.keep; t += kMoveCtas * kMoveThreads) kept[t] = mine[t];
+  move_rows<2>(a, b, hk, 0, cta, per, mine, rows_smem);
+}
+
+// One launch for a few heads of short sequences, where every CTA has an SM to itself and repeats the selection for
+// nothing: 8 heads of 1030 keys 7.1 us for 7.8 (and a launch less on the host, 22 us for 25), of 2000 keys 9.5 for 9.6; 32
+// heads of 2000 keys 13.6 for 13.1, 128 heads 36 for 27.
+bool evict_at_once(const PagedShape& s) {
+  return s.max_k <= kEvictRows * kSelRow && (long long)s.B * s.Hkv <= 16;
 }
 
 template <int R>
@@ -360,20 +409,33 @@ cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st) {
 
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st) {
   const long long heads = (long long)a.s.B * a.s.Hkv;
+  const int share = (a.keep + fa::kMoveCtas - 1) / fa::kMoveCtas;  // rows of a CTA
+  auto even = [share](int most) {  // in blocks of equal size, of at most `most` rows
+    const int blocks = (share + most - 1) / most, n = (share + blocks - 1) / blocks;
+    return n < 16 ? 16 : n;
+  };
+  cudaError_t e;
+  if (fa::evict_at_once(a.s)) {
+    // (with a.keep >= max_k nothing is selected, and no more than max_k kept keys are ever in shared memory)
+    const int per = even(fa::kMoveRows / 2);
+    const size_t smem = (size_t)2 * per * a.s.d * 2 + (size_t)(a.keep < a.s.max_k ? a.keep : a.s.max_k) * sizeof(int32_t);
+    e = cudaFuncSetAttribute(fa::paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             256 * 128 * 2 + fa::kEvictRows * fa::kSelRow * 4);
+    if (e != cudaSuccess) return e;
+    return launch_dependent_cluster(fa::paged_evict_kernel, dim3((unsigned)(heads * fa::kMoveCtas)),
+                                    dim3(fa::kMoveThreads), smem, fa::kMoveCtas, st, a, per);
+  }
   // Registers for the candidates of the longest sequence: up to 8 rows a thread, then CTAs, then 16 rows. CTAs
   // that need not be there cost cluster barriers (1030 keys: 4.5 us with one, 7.7 with two; 12 x 8 heads of 8192
   // keys: 11, 15, 17 and 29 with 1, 2, 4 and 8), rows past the registers are read five times (8 heads of 16384
   // keys: 24, 14, 12 and 12; of 65536: 123, 90, 41 and 16).
   const long long rows = ((long long)a.s.max_k + fa::kSelRow - 1) / fa::kSelRow;
   const unsigned ctas = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
-  cudaError_t e = rows <= 2    ? fa::launch_select<2>(a, ctas, st)
+  e = rows <= 2    ? fa::launch_select<2>(a, ctas, st)
                   : rows <= 64 ? fa::launch_select<8>(a, ctas, st)
                                : fa::launch_select<16>(a, ctas, st);
   if (e != cudaSuccess) return e;
-  // Blocks of equal size, of at most kMoveRows rows a CTA.
-  const int share = (a.keep + fa::kMoveCtas - 1) / fa::kMoveCtas;
-  const int blocks = (share + fa::kMoveRows - 1) / fa::kMoveRows, even = (share + blocks - 1) / blocks;
-  const int per = even < 16 ? 16 : even;
+  const int per = even(fa::kMoveRows);
   const size_t smem = (size_t)per * a.s.d * 2;
   e = cudaFuncSetAttribute(fa::paged_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 256 * 128 * 2);
   if (e != cudaSuccess) return e;

@@ -441,7 +441,8 @@ def test_append_places_outside_the_table_are_reported():
 
 
 EVICT = [([100, 20, 0, 64], 64, 10), ([300], 1, 0), ([300], 1, 1), ([1000, 129], 128, 128), ([1500, 700], 600, 0),
-         ([5000], 4000, 77), ([260, 2600], 255, 3), ([2500], 2499, 2000)]
+         ([5000], 4000, 77), ([260, 2600], 255, 3), ([2500], 2499, 2000),
+         ([2048, 1500, 40], 1499, 9), ([30, 2047], 1900, 1900), ([40] * 30 + [900], 300, 1)]
 
 
 @pytest.mark.parametrize("weights", ["heavy", "ties", "odd"])
