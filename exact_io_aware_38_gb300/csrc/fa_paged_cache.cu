@@ -113,12 +113,13 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_tot, int& total) {
   return before;
 }
 
-// A cluster (or one CTA) selects the keys of a (sequence, K/V head) into `kept`. A row is 1024 consecutive keys, four to a thread (a page holds
-// them together, so one table entry and one 16-byte load fetch them); a thread keeps R rows' weights as
-// ranks in registers and reads those of further rows again in each pass. The rank of the last kept
-// weight is found 8 bits at a time from the top, in four passes of a histogram in shared memory (summed
-// over the cluster) of which each thread scans a bin. Then a key's place is the number of larger weights
-// before it plus that of equal ones, as far as those stay, by a scan over threads and rows in key order.
+// A cluster (or one CTA) selects the keys of a (sequence, K/V head) into `kept`. A row is 1024 consecutive
+// keys, four to a thread (a page holds them together, so one table entry and one 16-byte load fetch them); a
+// thread keeps R rows' weights as ranks in registers and reads those of further rows again in each pass. The rank of
+// the last kept weight is found 8 bits at a time from the top, in four passes of a histogram in shared memory
+// (summed over the cluster) of which each thread scans a bin (three passes of 11 bits: the same time in one CTA,
+// twice as long in a cluster of 8). Then a key's place is the number of larger weights before it plus that of equal
+// ones, as far as those stay, by a scan over threads and rows in key order.
 // Bound by latency: 4.5 us for 8 heads of 1030 keys, 11 for 12 x 8 of up to 8192; counting against bounds instead, 16
 // steps of 2 bits, took 13 us for the former.
 template <int R>

@@ -169,6 +169,22 @@ def test_attend_many_sequences():
         p.check_attend(*p.attend(True, num_sms=sms), True)
 
 
+@pytest.mark.parametrize("rows", ["few", "many"])
+def test_more_sequences_than_threads(rows):
+    """Shares are found by threads that look at several sequences each, most of them without tokens or keys."""
+    r = np.random.default_rng(14)
+    lk = r.integers(0, 150, 1500) * (r.random(1500) < 0.2)
+    lq = r.integers(0, 5 if rows == "few" else 70, 1500) * (r.random(1500) < 0.1)
+    p = Problem(lk.tolist(), lq.tolist(), 4, 1, 64, page=16, packed=True, seed=18)
+    for sms in (2, 152):
+        o, lse = p.attend(True, num_sms=sms)
+        p.check_attend(o, lse, True)
+    w = torch.zeros_like(p.cw)
+    fa.paged_key_weights(p.cq, p.ck, p.ctable, p.clen, lse, w, causal=True, scale=p.scale, **p.tokens)
+    seen = int((~torch.isneginf(lse[:, :int(p.cu[-1])])).sum())  # every row that sees a key pays 1 in all
+    assert abs(float(w.sum()) - seen) < 1e-3 * seen
+
+
 @pytest.mark.parametrize("n", [1, 4, 70])
 @pytest.mark.parametrize("layout", ["hpd", "gap"])
 @pytest.mark.parametrize("d", [64, 128])
