@@ -70,6 +70,19 @@ __device__ __forceinline__ size_t weight_offset(const PagedShape& s, int page, i
   return (((size_t)page * s.Hkv + hk) << s.page_shift) + slot;
 }
 
+// The two copying warps of the chunk and key-weight kernels: at d = 128 each copies 64 columns of every page, at d = 64
+// every other page (a lane per page either way), and the first warp Q.
+template <int D>
+struct CopyShare {
+  int who;  // 0 or 1
+  __device__ int column() const { return D == 128 ? who : 0; }  // in units of 64
+  __device__ bool lane(int l, int pages) const { return l < pages && (D == 128 || (l & 1) == who); }
+  __device__ int bytes(int pages, int rows) const {
+    return (D == 128 ? pages : (pages + 1 - who) >> 1) * rows * 128;
+  }
+  __device__ bool copies_q() const { return who < D / 64; }
+};
+
 // How query rows lie in tiles: gs heads side by side for each of tpt tokens; Hv such groups of heads,
 // per_kv of them per K/V head.
 struct FastDiv {  // division of 0 <= n < 2^31 by a constant of the launch: n ceil(2^(31 + k) / d) >> (31 + k), 2^k >= d

@@ -12,9 +12,8 @@
 // CTA per unit instead runs in whole waves: 2048 tokens x 32 heads are 256 units on 152 SMs, 1.7
 // waves that take the time of 2.
 //
-// Roles: warp 0 and at d = 128 the last warp read the page table and copy (64 columns each: a warp issues a copy
-// per ~100 cycles, and small pages need many: 2048 tokens over 16384 keys in pages of 16 take 377 us, with one
-// warp 561), warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of tile 0 and tile 1. Copies run ahead
+// Roles: warp 0 and the last warp read the page table and copy (a warp issues a copy per ~100 cycles, and small
+// pages need many: 2048 tokens over 16384 keys in pages of 16 take 372 us, with one warp 561; d = 64 322 and 411), warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of tile 0 and tile 1. Copies run ahead
 // across units. Stage t of the ring holds V of key tile t and K of key tile t + 1.
 //
 // Measured: 2048 tokens over 16384 keys, 32 heads over 8 of d = 128: 370 us, 1390 TFLOP/s, the tensor pipe 61% busy: a
@@ -36,7 +35,7 @@ template <int D>
 struct ChCfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kThreads = 320 + 32 * (D / 64 - 1);
+  static constexpr int kThreads = 352;
   static constexpr int kStaging = 8 * 4096;  // the epilogue's, 32 rows of 128 bytes per warp
   static constexpr int kSmem = 2 * kTileBytes + 2 * kStages * kTileBytes + kStaging + 1024;
   static constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
@@ -183,10 +182,10 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
     for (int i = 0; i < 2; ++i) ctl.issued_q[i] = ctl.issued_k0[i] = ctl.issued_t[i] = ctl.issued_tail[i] = 0;
     mbar_init(bar(ctl.q_full), D / 64);
     mbar_init(bar(ctl.q_empty), 1);
-    mbar_init(bar(ctl.k0_full), D / 64);
+    mbar_init(bar(ctl.k0_full), 2);
     mbar_init(bar(ctl.k0_empty), 1);
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(ctl.full[i]), D / 64 + 128);  // the copies, and P of tile 0 (or its stand-in)
+      mbar_init(bar(ctl.full[i]), 2 + 128);  // the copies, and P of tile 0 (or its stand-in)
       mbar_init(bar(ctl.empty[i]), 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
       mbar_init(bar(ctl.o_free[x]), 128);
     }
     mbar_init(bar(ctl.p_ready), 128);
-    mbar_init(bar(ctl.tail), D / 64);
+    mbar_init(bar(ctl.tail), 2);
     mbar_init(bar(ctl.drain), 1);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
@@ -236,9 +235,10 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
     wk.desc[blockIdx.x] = d;
   }
 
-  if (warp == 0 || (D > 64 && warp == C::kThreads / 32 - 1)) {
+  if (warp == 0 || warp == C::kThreads / 32 - 1) {
     // ------------------------------------------------------------------ copies
-    const int half = warp != 0;  // the 64 columns that this warp copies, of Q, K and V
+    const int who = warp != 0;
+    const CopyShare<D> my{who};
     const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     bool run = true;
     auto page_of = [&](const ChPieces& x, int kt) -> int {
@@ -250,20 +250,21 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
       return left <= 0 ? 0 : min(per, (left + prows - 1) >> shift);
     };
     auto copy = [&](uint32_t dst, const CUtensorMap* tm, const ChPieces& x, int kt, int page, uint32_t on) {
-      if (lane < pages_in(x, kt))
-        tma_load_4d(dst + half * 16384 + lane * prows * 128, tm, half * 64, (kt << 7) & (P - 1), x.hv / rows.per_kv,
+      if (my.lane(lane, pages_in(x, kt)))
+        tma_load_4d(dst + my.column() * 16384 + lane * prows * 128, tm, my.column() * 64, (kt << 7) & (P - 1), x.hv / rows.per_kv,
                     page, on);
     };
     auto copy_q = [&](const ChPieces& x, int piece) {
+      if (!my.copies_q()) return;
       if (run && piece > 0) run = mbar_wait(bar(ctl.q_empty), (piece - 1) & 1, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
       if (!run || lane > 0) return;
       const int tiles = (2 * x.u + 1) * rows.tpt < x.seq.Lq ? 2 : 1;
       mbar_expect_tx(bar(ctl.q_full), tiles * used * 128);
       for (int y = 0; y < tiles; ++y)
-        tma_load_4d(sQ + y * C::kTileBytes + half * 16384, &tmQ, half * 64, x.hv * rows.gs,
+        tma_load_4d(sQ + y * C::kTileBytes + who * 16384, &tmQ, who * 64, x.hv * rows.gs,
                     x.seq.q0 + (2 * x.u + y) * rows.tpt, x.seq.bb, bar(ctl.q_full));
-      ctl.issued_q[half] = piece + 1;
+      ctl.issued_q[who] = piece + 1;
     };
     if (!w.done()) {
       ChPieces v = w;  // the piece of the next K
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
       int page = page_of(w, w.kt);
       copy_q(w, 0);
       if (lane == 0) {
-        mbar_expect_tx(bar(ctl.k0_full), pages_in(w, w.kt) * prows * 128);
-        ctl.issued_k0[half] = 1;
+        mbar_expect_tx(bar(ctl.k0_full), my.bytes(pages_in(w, w.kt), prows));
+        ctl.issued_k0[who] = 1;
       }
       __syncwarp();
       copy(sK(C::kStages - 1), &tmK, w, w.kt, page, bar(ctl.k0_full));
@@ -296,8 +297,8 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
 #endif
           if (!run) continue;
           const int valid = w.seq.Lk - (kt << 7);
-          const int vbytes = pages_in(w, kt) * prows * 128, kbytes = more ? pages_in(v, vkt) * prows * 128 : 0;
-          if (lane == 0 && half == 0) {
+          const int vbytes = my.bytes(pages_in(w, kt), prows), kbytes = more ? my.bytes(pages_in(v, vkt), prows) : 0;
+          if (lane == 0 && who == 0) {
             const bool p0 = kt < w.tiles(0);
             if (!p0) mbar_arrive_cnt(bar(ctl.full[st]), 128);  // tile 0 has no P for this key tile
             ctl.needs_p0[st] = p0;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
           if (valid >= 128) {
             if (lane == 0) {
               mbar_expect_tx(bar(ctl.full[st]), vbytes + kbytes);
-              ctl.issued_t[half] = t + 1;
+              ctl.issued_t[who] = t + 1;
             }
             __syncwarp();
             copy(sV(st), &tmV, w, kt, page, bar(ctl.full[st]));
@@ -316,8 +317,8 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
             if (lane == 0) {
               mbar_add_tx(bar(ctl.full[st]), kbytes);
               mbar_expect_tx(bar(ctl.tail), vbytes);
-              ctl.issued_t[half] = t + 1;
-              ctl.issued_tail[half] = tails + 1;
+              ctl.issued_t[who] = t + 1;
+              ctl.issued_tail[who] = tails + 1;
             }
             __syncwarp();
             copy(sV(st), &tmV, w, kt, page, bar(ctl.tail));
@@ -326,8 +327,8 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
             run = __all_sync(0xffffffffu, run);
             ++tails;
             if (run)
-              for (int i = max(valid, 0) * 8 + lane; i < 128 * 8; i += 32)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + half * 16384 + i * 16), "r"(0)
+              for (int i = max(valid, 0) * 8 + lane + (D == 128 ? 0 : 32 * who); i < 128 * 8; i += D == 128 ? 32 : 64)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sV(st) + my.column() * 16384 + i * 16), "r"(0)
                              : "memory");
             fence_proxy_async_smem();
             __syncwarp();
@@ -580,14 +581,14 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) {
     // Copies still in flight land before the CTA exits: the last ones issued on each barrier. A producer that
     // stopped before the other did has its arrival made here.
-    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i) {
-      for (int p = 0; p < D / 64; ++p)
+    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i, int producers = 2) {
+      for (int p = 0; p < producers; ++p)
         if (issued[p] <= i) mbar_arrive(bar(full));
       mbar_wait_drain(bar(full), parity);
     };
     const int nq = max(ctl.issued_q[0], ctl.issued_q[1]), nt = max(ctl.issued_t[0], ctl.issued_t[1]);
     const int ntail = max(ctl.issued_tail[0], ctl.issued_tail[1]);
-    if (nq > 0) drain(ctl.q_full, (nq - 1) & 1, ctl.issued_q, nq - 1);
+    if (nq > 0) drain(ctl.q_full, (nq - 1) & 1, ctl.issued_q, nq - 1, D / 64);
     if (ctl.issued_k0[0] + ctl.issued_k0[1] > 0) drain(ctl.k0_full, 0, ctl.issued_k0, 0);
     if (ntail > 0) drain(ctl.tail, (ntail - 1) & 1, ctl.issued_tail, ntail - 1);
     for (int t = max(0, nt - C::kStages); t < nt; ++t) {

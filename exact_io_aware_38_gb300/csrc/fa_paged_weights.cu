@@ -11,8 +11,8 @@
 // leaves 128 partial sums per piece (two slots per CTA), which the join kernel adds in the pieces'
 // order; with one query tile per unit nothing is cut.
 //
-// Roles: warp 0 and at d = 128 the last warp read the page table and copy (64 columns each: a warp issues a copy
-// per ~100 cycles, and small pages need many); one warp issues the MMAs, or with many rows two, a
+// Roles: warp 0 and the last warp read the page table and copy (a warp issues a copy per ~100 cycles, and small
+// pages need many: 16 x 8192 keys in pages of 16 take 50 us, with one warp 56; d = 64 37 and 41); one warp issues the MMAs, or with many rows two, a
 // query tile each in turn: an MMA takes its thread about 70 cycles whatever its width, so a tile's eight and
 // the waits around them fill 1200 cycles of one thread, twice what the tensor pipe needs. Groups of four
 // warps (three, with many rows four) take the query tiles in turn; with many rows a last group adds their
@@ -43,7 +43,7 @@ struct WCfg {
   static constexpr int kGroups = kFew ? 3 : 4;
   static constexpr int kIssuers = kFew ? 1 : 2;
   static constexpr int kIssuer2 = 2 + 4 * kGroups + 4;  // the second issuer's warp, behind the sums' group
-  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128 + 32) + 32 * (D / 64 - 1);
+  static constexpr int kThreads = 64 + 128 * kGroups + (kFew ? 0 : 128 + 32) + 32;
   static constexpr int kKBufs = (kFew ? (NP == 64 ? 5 : 6) : 2) * (128 / D);
   static constexpr int kQBufs = kFew ? 2 : 4 * (128 / D);  // (even: a buffer has one issuer, which sees its every phase)
   // A unit's sums and hand-over, in query tiles (weighed as 1, 2, 3, 4: 51.3, 51.6, 52.1 and 53.4 us).
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     ctl.abort_flag = 0;
     for (int i = 0; i < 2; ++i) ctl.issued_k[i] = ctl.issued_q[i] = 0;
     for (int i = 0; i < C::kKBufs; ++i) {
-      mbar_init(bar(ctl.k_full[i]), D / 64);
+      mbar_init(bar(ctl.k_full[i]), 2);
       mbar_init(bar(ctl.k_empty[i]), C::kIssuers);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
@@ -286,9 +286,10 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
     wk.desc[blockIdx.x] = d;
   }
 
-  if (warp == 0 || (D > 64 && warp == C::kThreads / 32 - 1)) {
+  if (warp == 0 || warp == C::kThreads / 32 - 1) {
     // ------------------------------------------------------------------ copies
-    const int half = warp != 0;  // the 64 columns that this warp copies, of Q and K
+    const int who = warp != 0;
+    const CopyShare<D> my{who};
     const int P = 1 << s.page_shift, prows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     bool run = true;
     int kn = 0, qn = 0;  // key tiles and query tiles copied
@@ -301,13 +302,14 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       return run;
     };
     auto copy_q = [&](int token, int head0) {
+      if (!my.copies_q()) return;
       const int st = qn % C::kQBufs, u = qn / C::kQBufs;
       if (run && u > 0) run = mbar_wait(bar(ctl.q_empty[st]), (u - 1) & 1, abort_flag, a.status);
       if (go() && lane == 0) {
         mbar_expect_tx(bar(ctl.q_full[st]), used * 128);
-        tma_load_4d(sQ + st * C::kQBytes + half * NP * 128, &tmQ, half * 64, head0, w.x.q.q0 + token, w.x.q.bb,
+        tma_load_4d(sQ + st * C::kQBytes + who * NP * 128, &tmQ, who * 64, head0, w.x.q.q0 + token, w.x.q.bb,
                     bar(ctl.q_full[st]));
-        ctl.issued_q[half] = qn + 1;
+        ctl.issued_q[who] = qn + 1;
       }
       ++qn;
     };
@@ -322,13 +324,13 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       if (go()) {
         const int pages = min(per, (w.x.q.Lk - (w.kt << 7) + prows - 1) >> shift);
         if (lane == 0) {
-          mbar_expect_tx(bar(ctl.k_full[st]), pages * prows * 128);
-          ctl.issued_k[half] = kn + 1;
+          mbar_expect_tx(bar(ctl.k_full[st]), my.bytes(pages, prows));
+          ctl.issued_k[who] = kn + 1;
         }
         __syncwarp();
-        if (lane < pages)
-          tma_load_4d(sK + st * C::kKBytes + half * 16384 + lane * prows * 128, &tmK, half * 64, (w.kt << 7) & (P - 1),
-                      w.hk, page, bar(ctl.k_full[st]));
+        if (my.lane(lane, pages))
+          tma_load_4d(sK + st * C::kKBytes + my.column() * 16384 + lane * prows * 128, &tmK, my.column() * 64,
+                      (w.kt << 7) & (P - 1), w.hk, page, bar(ctl.k_full[st]));
       }
       ++kn;
       if (!C::kFew) {
@@ -546,14 +548,14 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) {
     // Copies still in flight land before the CTA exits: the last one issued into each buffer. A producer that stopped
     // before the other did has its arrival made here.
-    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i) {
-      for (int p = 0; p < D / 64; ++p)
+    auto drain = [&](uint64_t& full, int parity, const int (&issued)[2], int i, int producers = 2) {
+      for (int p = 0; p < producers; ++p)
         if (issued[p] <= i) mbar_arrive(bar(full));
       mbar_wait_drain(bar(full), parity);
     };
     const int nq = max(ctl.issued_q[0], ctl.issued_q[1]), nk = max(ctl.issued_k[0], ctl.issued_k[1]);
     for (int i = max(0, nq - C::kQBufs); i < nq; ++i)
-      drain(ctl.q_full[i % C::kQBufs], (i / C::kQBufs) & 1, ctl.issued_q, i);
+      drain(ctl.q_full[i % C::kQBufs], (i / C::kQBufs) & 1, ctl.issued_q, i, D / 64);
     for (int i = max(0, nk - C::kKBufs); i < nk; ++i)
       drain(ctl.k_full[i % C::kKBufs], (i / C::kKBufs) & 1, ctl.issued_k, i);
   }

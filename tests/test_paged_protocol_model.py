@@ -5,7 +5,7 @@ A CTA walks pieces of units; here a piece is the number of its tiles. Each model
 commits, with copies, MMAs and commits completing at random times, and checks: no deadlock, no buffer reloaded before
 its readers have completed, no MMA before its operands are there, no operand or accumulator overwritten while it is
 read, and with waits that run out at random: every role ends and no copy is left in flight. A planted mistake must be
-found in each. Every copy is made by one or two producers, of 64 columns each, which arrive on the same barriers.
+found in each. Keys and values are copied by one or two producers, which arrive on the same barriers; so is Q, or by the first alone.
 
 decode   fa_paged_decode.cu: K and V rings of their own lengths, two Q buffers, S and P double buffered, O per piece
          double buffered; the softmax waits for V itself in a unit's last tile, whose rows past the last key it zeroes.
@@ -207,13 +207,14 @@ def test_decode_model_finds_a_missing_wait():
 # ----------------------------------------------------------------------------- chunk
 
 
-def chunk(pieces, stages, seed, abort_p=0.0, early_q=False, prods=1):
+def chunk(pieces, stages, seed, abort_p=0.0, early_q=False, prods=1, qprods=1):
     """pieces: (tiles, tiles query tile 0 sees, tiles query tile 1 sees, the last tile is the sequence's last)."""
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
     T = tiles_of([n for n, *_ in pieces])
     sees = lambda x, t: t < len(T) and T[t][1] < pieces[T[t][0]][1 + x]
-    for n in ("qf", "k0f", "tail"):
+    M.bar("qf", qprods)
+    for n in ("k0f", "tail"):
         M.bar(n, prods)
     for n in ("qe", "k0e"):
         M.bar(n, 1)
@@ -223,7 +224,7 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False, prods=1):
     for x in (0, 1):
         for n in ("sf", "od", "of"):
             M.bar(f"{n}{x}", 1)
-    count = {n: [0] * prods for n in ("q", "k0", "t", "tail")}
+    count = {n: [0] * (qprods if n == "q" else prods) for n in ("q", "k0", "t", "tail")}
     needs_p0, p0_last = {}, [-1]
     has = lambda *what: landed(M, prods, *what)
 
@@ -233,6 +234,8 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False, prods=1):
             return
 
         def copy_q(p, run):
+            if h >= qprods:
+                return run
             if run and p > 0 and not early_q:
                 run = yield from M.wait("qe", (p - 1) & 1)
             run = run and not M.aborted
@@ -292,7 +295,7 @@ def chunk(pieces, stages, seed, abort_p=0.0, early_q=False, prods=1):
         np1, seen = 0, [0, 0]
 
         def issue_s(x, t):
-            need(has("Q", T[t][0]) and has("K", t), f"S{x}({t}) before its operands")
+            need(landed(M, qprods, "Q", T[t][0]) and has("K", t), f"S{x}({t}) before its operands")
             M.mma("i", (f"S{x}", t))
             M.commit("i", f"sf{x}")
         run = yield from M.wait("qf", 0)
@@ -395,13 +398,13 @@ def chunk_pieces(seed):
 
 def test_chunk_has_no_deadlock_or_hazard():
     for seed in range(2500):
-        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, prods=1 + seed // 2 % 2)
+        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, prods=2, qprods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (chunk_pieces(seed), seed, res, errs[:3])
 
 
 def test_chunk_ends_after_waits_that_run_out():
     for seed in range(1500):
-        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, abort_p=0.02, prods=1 + seed // 2 % 2)
+        res, errs = chunk(chunk_pieces(seed), (2, 4)[seed & 1], seed, abort_p=0.02, prods=2, qprods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (chunk_pieces(seed), seed, res, errs[:3])
 
 
@@ -412,7 +415,7 @@ def test_chunk_model_finds_a_missing_wait():
 # ----------------------------------------------------------------------------- weights
 
 
-def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, three=False, prods=1):
+def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, three=False, prods=1, qprods=1):
     """pieces: the query tiles of each key tile (few rows: one each, and every third begins another head)."""
     M = Machine(seed, abort_p)
     done, need = M.done, M.need
@@ -422,16 +425,18 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
     q_of = (lambda t: T[t][0] // 3) if few else (lambda t: t)
     for n, c in (("kf", kb), ("ke", kb), ("qf", qb), ("qe", qb), ("sf", sb), ("fr", sb)):
         for i in range(c):
-            M.bar(f"{n}{i}", issuers if n == "ke" else prods if n in ("kf", "qf") else 1)
+            M.bar(f"{n}{i}", issuers if n == "ke" else prods if n == "kf" else qprods if n == "qf" else 1)
     for i in range(2):
         M.bar(f"sr{i}", G), M.bar(f"sx{i}", 1)
-    count = {n: [0] * prods for n in "kq"}
+    count = {"k": [0] * prods, "q": [0] * qprods}
     has = lambda *what: landed(M, prods, *what)
 
     def producer(h):
         run = True
 
         def copy_q(q, run):
+            if h >= qprods:
+                return run
             if run and q >= qb:
                 run = yield from M.wait(f"qe{q % qb}", (q // qb - 1) & 1)
             run = run and not M.aborted
@@ -470,7 +475,7 @@ def weights(pieces, few, seed, abort_p=0.0, no_sum_free=False, odd_ring=False, t
                     run = yield from M.wait(f"fr{t % sb}", (t // sb - 1) & 1)
                 if not run:
                     break
-                need(has("K", p) and has("Q", q_of(t)), f"S({t}) before its operands")
+                need(has("K", p) and landed(M, qprods, "Q", q_of(t)), f"S({t}) before its operands")
                 need(t < sb or ("read", t - sb) in done, f"S({t}) over S({t - sb})")
                 M.mma(f"i{me}", ("S", t))
                 M.commit(f"i{me}", f"sf{t % sb}")
@@ -531,14 +536,14 @@ def weight_pieces(seed, few):
 def test_weights_has_no_deadlock_or_hazard():
     for seed in range(2500):
         few = bool(seed & 1)
-        res, errs = weights(weight_pieces(seed, few), few, seed, prods=1 + seed // 2 % 2)
+        res, errs = weights(weight_pieces(seed, few), few, seed, prods=2, qprods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (weight_pieces(seed, few), few, seed, res, errs[:3])
 
 
 def test_weights_ends_after_waits_that_run_out():
     for seed in range(1500):
         few = bool(seed & 1)
-        res, errs = weights(weight_pieces(seed, few), few, seed, abort_p=0.02, prods=1 + seed // 2 % 2)
+        res, errs = weights(weight_pieces(seed, few), few, seed, abort_p=0.02, prods=2, qprods=1 + seed // 2 % 2)
         assert res == "ok" and not errs, (weight_pieces(seed, few), few, seed, res, errs[:3])
 
 
