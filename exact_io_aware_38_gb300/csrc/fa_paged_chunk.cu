@@ -16,10 +16,10 @@
 // pages need many: 2048 tokens over 16384 keys in pages of 16 take 372 us, with one warp 561; d = 64 322 and 411), warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of tile 0 and tile 1. Copies run ahead
 // across units. Stage t of the ring holds V of key tile t and K of key tile t + 1.
 //
-// Measured: 2048 tokens over 16384 keys, 32 heads over 8 of d = 128: 370 us, 1390 TFLOP/s, the tensor pipe 61% busy: a
+// Measured: 2048 tokens over 16384 keys, 32 heads over 8 of d = 128: 368 us, 1400 TFLOP/s, the tensor pipe 61% busy: a
 // pair of query tiles takes 3214 cycles a key tile, of which its products are 2048; the softmax step is the
-// length, as in the forward over contiguous tensors. Six sequences of 1 to 509 tokens over up to 6001 keys: 125 us, 930
-// TFLOP/s (shares of 55 key tiles; 15000 cycles each until their first keys are no longer read from DRAM).
+// length, as in the forward over contiguous tensors. Six sequences of 1 to 509 tokens over up to 6001 keys: 123 us, 945
+// TFLOP/s (shares of 55 key tiles; 13000 cycles each until the first scores, and 13 us of joining).
 //
 // Tensor memory: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P over S.
 #include "fa_paged.cuh"
@@ -607,22 +607,20 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
 }
 
 // Joins the pieces of each divided unit by their log-sum-exp: M = max LSE, w = 2^(LSE - M),
-// O = sum w O / sum w, LSE = M + log2 sum w. Block (c, y) takes 32 rows of the unit that ends in CTA c's first
-// piece, if it began before; a thread takes four elements of several rows, whose loads are in flight
-// together. (Letting its own dependent start early cost 4% of a mixed batch: this grid is several waves.)
+// O = sum w O / sum w, LSE = M + log2 sum w. Block (c, y) takes kJoinRows rows of the unit that ends in CTA c's first
+// piece, if it began before; a thread takes four elements of two rows, whose loads from two pieces are in flight
+// together (four rows and a piece at a time: a mixed batch 125 us for 123, 2048 tokens over 16384 keys 370 for 368;
+// letting its own dependent start early: 125). It and the kernel border before it are 13 us of those.
+constexpr int kJoinRows = 16;
 template <int D>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs a, const PagedRows rows,
-                                                               const ChWork wk) {
+__global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const FaPagedArgs a, const PagedRows rows,
+                                                                  const ChWork wk) {
   grid_dependency_wait();
   const JoinDesc d = wk.desc[blockIdx.x];
   if (d.b < 0) return;
-  constexpr int kPer = 32 * (D / 4) / 256, kStep = 256 / (D / 4);  // rows of a thread, and between them
+  constexpr int kPer = kJoinRows * (D / 4) / 256, kStep = 256 / (D / 4);  // rows of a thread, and between them
   const PagedShape& s = a.s;
-  SeqInfo seq{};
-  seq.Lq = d.Lq;
-  seq.q0 = d.q0;
-  seq.bb = d.bb;
-  const int r0 = blockIdx.y * 32 + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4, c1 = blockIdx.x;
+  const int r0 = blockIdx.y * kJoinRows + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4, c1 = blockIdx.x;
   float4 acc[kPer];
   float M[kPer], sum[kPer];
 #pragma unroll
@@ -631,29 +629,38 @@ __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const FaPagedArgs
     M[k] = -INFINITY;
     sum[k] = 0.f;
   }
-  for (int c = d.first_cta; c <= c1; ++c) {
-    const size_t slot = (size_t)(c == d.first_cta ? d.first_slot : 2 * c) * 256 + r0;
-    float l[kPer];
-    float4 o[kPer];
+  for (int c = d.first_cta; c <= c1; c += 2) {
+    float l[2][kPer];
+    float4 o[2][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {  // (rows that do not exist hold anything; they are not written)
-      l[k] = wk.part_lse[slot + k * kStep];
-      o[k] = *reinterpret_cast<const float4*>(wk.part_o + (slot + k * kStep) * D + e);
+    for (int p = 0; p < 2; ++p) {
+      const size_t slot = (size_t)(c + p == d.first_cta ? d.first_slot : 2 * min(c + p, c1)) * 256 + r0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {  // (rows that do not exist hold anything; they are not written)
+        l[p][k] = wk.part_lse[slot + k * kStep];
+        o[p][k] = *reinterpret_cast<const float4*>(wk.part_o + (slot + k * kStep) * D + e);
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (l[k] == -INFINITY) continue;
-      const float top = fmaxf(M[k], l[k]), old = exp2f(M[k] - top), w = exp2f(l[k] - top);
-      M[k] = top;
-      sum[k] = sum[k] * old + w;
-      acc[k] = make_float4(acc[k].x * old + w * o[k].x, acc[k].y * old + w * o[k].y, acc[k].z * old + w * o[k].z,
-                           acc[k].w * old + w * o[k].w);
-    }
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (c + p > c1 || l[p][k] == -INFINITY) continue;
+        const float top = fmaxf(M[k], l[p][k]), old = exp2f(M[k] - top), w = exp2f(l[p][k] - top);
+        M[k] = top;
+        sum[k] = sum[k] * old + w;
+        acc[k] = make_float4(acc[k].x * old + w * o[p][k].x, acc[k].y * old + w * o[p][k].y,
+                             acc[k].z * old + w * o[p][k].z, acc[k].w * old + w * o[p][k].w);
+      }
   }
+  SeqInfo seq{};
+  seq.Lq = d.Lq;
+  seq.q0 = d.q0;
+  seq.bb = d.bb;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = r0 + k * kStep, rr = r & 127;
-    const int i = (2 * d.u + (r >> 7)) * rows.tpt + rr / rows.gs, h = d.hv * rows.gs + rr % rows.gs;
+    const int ti = rr / rows.gs, i = (2 * d.u + (r >> 7)) * rows.tpt + ti, h = d.hv * rows.gs + rr - ti * rows.gs;
     if (rr >= rows.gs * rows.tpt || i >= seq.Lq) continue;
     const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
@@ -688,7 +695,7 @@ cudaError_t launch_chunk(const FaPagedArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(a.num_sms), dim3(C::kThreads), C::kSmem, st, tq, tk, tv, a, rows, wk);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_chunk_join_kernel<D>, dim3(a.num_sms, 8), dim3(256), 0, st, a, rows, wk);
+  return launch_dependent(paged_chunk_join_kernel<D>, dim3(a.num_sms, 256 / kJoinRows), dim3(256), 0, st, a, rows, wk);
 }
 
 }  // namespace
