@@ -550,20 +550,21 @@ def test_a_run_of_all_operators(heads):
         assert new.tolist() == have
 
 
-def test_captured_and_replayed_step_follows_the_lengths():
+@pytest.mark.parametrize("sms", [152, 3])
+def test_captured_and_replayed_step_follows_the_lengths(sms):
     """One decode step captured once, replayed with other lengths, rows and page tables in the same buffers, equals the
-    eager calls; two graphs share the workspace."""
+    eager calls; two graphs share the workspace (152 SMs: clusters, without one; 3: the work is divided)."""
     p = Problem([700, 1200], [1, 1], 8, 2, 128, page=16, seed=92)
     q, k, v = p.cq.clone(), p.k_new.cuda(), p.v_new.cuda()
     bound = p.width * p.P
     prob = fa._paged(q, p.ck, p.cv, p.ctable, p.clen, None, None, bound, True, p.scale)[0]
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
     ws = torch.empty(fa.fa_fwd_paged_workspace_bytes(prob, sms), dtype=torch.uint8, device="cuda")
+    assert (ws.numel() > 0) == (sms == 3)
     state0 = [t.clone() for t in (p.ck, p.cv, p.cw)]
 
     def step():
         fa.paged_append(k, v, p.ck, p.cv, p.ctable, p.clen, key_weights=p.cw)
-        o, lse = fa.fwd_paged(q, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale, workspace=ws)
+        o, lse = fa.fwd_paged(q, p.ck, p.cv, p.ctable, p.clen, causal=True, scale=p.scale, num_sms=sms, workspace=ws)
         fa.paged_key_weights(q, p.ck, p.ctable, p.clen, lse, p.cw, causal=True, scale=p.scale)
         kept, n = fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, p.clen, 500, recent=50)
         return o, lse, kept, n
