@@ -675,13 +675,11 @@ cudaError_t launch_chunk(const FaPagedArgs& a, cudaStream_t st) {
   using C = ChCfg<D>;
   const PagedShape& s = a.s;
   const bool packed = s.cu_q != nullptr;
-  const int P = 1 << s.page_shift;
   const PagedRows rows = paged_rows_for(s);
   CUtensorMap tq, tk, tv;
   if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
                          rows.gs, rows.tpt) ||
-      !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128) ||
-      !fa_make_tmap_bf16(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, P < 128 ? P : 128))
+      !paged_tmap(&tk, a.k, s, a.sk) || !paged_tmap(&tv, a.v, s, a.sv))
     return cudaErrorInvalidValue;
   ChWork wk;
   char* ws = static_cast<char*>(a.workspace);

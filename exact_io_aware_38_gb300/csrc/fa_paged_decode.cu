@@ -7,7 +7,7 @@
 // softmax thread handles 16 numbers per tile instead of 128. P^T goes back through shared memory
 // (bf16, keys x rows) and O^T += V^T P^T accumulates in tensor memory, a head dimension per lane.
 // Measured: 32 sequences of up to 8192 keys, 32 heads over 8 of d = 128, one token: 824 MB in 132 us, 6.2 TB/s (94% of the
-// copy rate); 48 of up to 1024 keys, 12 heads of d = 64: 116 MB in 33 us (a share has 13 tiles and 2.6 units' borders);
+// copy rate); 48 of up to 1024 keys, 12 heads of d = 64: 116 MB in 31 us (a share has 13 tiles and 2.6 units' borders);
 // one sequence of 777 keys: 8.4 us, latency.
 // The exponentials are taken against a reference max per row, set by the row's first tile and raised
 // (O and the row sums rescaled) only when a score exceeds it by more than 2^8: exact, since fp32 and bf16
@@ -651,13 +651,12 @@ cudaError_t launch_decode(const FaPagedArgs& a, cudaStream_t st) {
   using C = DecCfg<D, NP>;
   const PagedShape& s = a.s;
   const bool packed = s.cu_q != nullptr;
-  const int P = 1 << s.page_shift, G = s.H / s.Hkv;
+  const int G = s.H / s.Hkv;
   CUtensorMap tq, tk, tv;
   // Q by tokens and heads: a box holds the G heads of a K/V head for Nq tokens, in row order token G + head.
   if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
                          G, s.Nq) ||
-      !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128) ||
-      !fa_make_tmap_bf16(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, P < 128 ? P : 128))
+      !paged_tmap(&tk, a.k, s, a.sk) || !paged_tmap(&tv, a.v, s, a.sv))
     return cudaErrorInvalidValue;
   const int shared = unit_ctas(s, a.num_sms), ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
   DecWork wk{};

@@ -582,11 +582,10 @@ cudaError_t launch_weights(const FaPagedArgs& a, const PagedRows& rows, cudaStre
   static_assert(C::kSmem + sizeof(WCtl<NP>) <= 227 * 1024, "with the control block");
   const PagedShape& s = a.s;
   const bool packed = s.cu_q != nullptr;
-  const int P = 1 << s.page_shift;
   CUtensorMap tq, tk;
   if (!fa_make_tmap_bf16(&tq, a.q, D, s.H, packed ? s.rows_q : s.Nq, packed ? 1 : s.B, a.sq.head, a.sq.row, a.sq.batch,
                          rows.gs, rows.tpt) ||
-      !fa_make_tmap_bf16(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, P < 128 ? P : 128))
+      !paged_tmap(&tk, a.k, s, a.sk))
     return cudaErrorInvalidValue;
   WWork wk{};
   if (!C::kFew) {

@@ -298,7 +298,7 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
  *   cache      k_cache and v_cache are bf16, addressed as [page][slot][head][d] with d contiguous and the
  *              element strides of fa_strides (row = slot, head, batch = page: multiples of 8, > 0); num_pages
  *              pages of page_size slots (a power of two, 8 .. 65536). Element offsets are 64-bit: a cache may
- *              hold more than 2^31 elements.
+ *              hold more than 2^31 elements. Any order of slots and heads works.
  *   page table device int32 [B][max_pages]: key j of sequence b lies in page page_table[b][j / page_size], slot
  *              j % page_size. Only entries that a sequence's length reaches are read. One outside
  *              [0, num_pages) writes FA_ERR_BOUNDS into *dev_status; nothing outside the cache is read or
