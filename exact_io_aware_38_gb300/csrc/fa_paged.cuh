@@ -73,8 +73,8 @@ __device__ __forceinline__ size_t weight_offset(const PagedShape& s, int page, i
 
 // A cache's tensor map, boxes of a page's slots (128 at most). At d = 64 a head's row is 128 bytes and the next 128 are
 // often another head's, which misses of 256 bytes would fetch for nothing and lose before its turn: 128 sequences of
-// 2048 keys, 12 heads, took 182 us that way and 128 this way (4.4 and 6.3 TB/s; 48 of 1024 keys 33 and 31); with a
-// head's slots next to one another in the page 128 either way.
+// 2048 keys, 12 heads, took 182 us that way and 128 to 138 on two cards this way (4.4 and 5.8 to 6.3 TB/s; 48 of 1024 keys
+// 33 and 31); with a head's slots next to one another in the page 128 either way.
 inline bool paged_tmap(CUtensorMap* m, const void* cache, const PagedShape& s, const FaStrides& t) {
   const int P = 1 << s.page_shift;
   return fa_make_tmap_bf16(m, cache, s.d, P, s.Hkv, s.num_pages, t.row, t.head, t.batch, P < 128 ? P : 128, 1, s.d > 64);
