@@ -76,6 +76,7 @@ struct Units {
   }
 };
 
+template <int D>
 struct ChCtl {
   uint64_t q_full, q_empty, k0_full, k0_empty;
   uint64_t full[4], empty[4];
@@ -83,7 +84,7 @@ struct ChCtl {
   uint64_t p_ready, tail, drain;  // p_ready: of tile 1
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[11];
+  long long scan[ChCfg<D>::kThreads / 32];  // an entry per warp
   Share share;
   Units units;  // of the sequence where the share begins
   int issued_q[2], issued_k0[2], issued_t[2], issued_tail[2];  // copies issued, by producer (abort-path drain)
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
                        const ChWork wk) {
   using C = ChCfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ ChCtl ctl;
+  __shared__ ChCtl<D> ctl;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;  // two tiles
   const uint32_t sKV = sQ + 2 * C::kTileBytes;                // stage i: V then K
   const uint32_t sO = sKV + 2 * C::kStages * C::kTileBytes;

@@ -85,7 +85,7 @@ struct DecUnits {
   __device__ long long before(int u) const { return u * (tiles() + open); }
 };
 
-template <int NP>
+template <int D, int NP>
 struct DecCtl {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -95,7 +95,7 @@ struct DecCtl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[18];
+  long long scan[DecCfg<D, NP>::kThreads / 32];  // an entry per warp
   Share share;
   DecUnits units;  // of the sequence where the share begins
   int issued_q[2], issued_t[2];                   // copies issued, by producer (abort-path drain)
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
                         const __grid_constant__ CUtensorMap tmV, const FaPagedArgs a, const DecWork wk) {
   using C = DecCfg<D, NP>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) DecCtl<NP> ctl;
+  __shared__ __align__(16) DecCtl<D, NP> ctl;
   const uint32_t sK0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sV0 = sK0 + C::kKStages * C::kTileBytes, sP = sV0 + C::kVStages * C::kTileBytes;
   const uint32_t sQ = sP + C::kPBytes;

@@ -84,12 +84,12 @@ struct WUnits {
   }
 };
 
-template <int NP>
+template <int D, int NP>
 struct WCtl {
   uint64_t k_full[12], k_empty[12], q_full[8], q_empty[8], s_full[4], s_free[4], sum_ready[2], sum_free[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[24];
+  long long scan[WCfg<D, NP>::kThreads / 32];  // an entry per warp
   Share share;
   WUnits units;                         // of the sequence where the share begins
   int issued_k[2], issued_q[2];         // copies issued, by producer (abort-path drain)
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
                          const FaPagedArgs a, const PagedRows rows, const WWork wk) {
   using C = WCfg<D, NP>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ WCtl<NP> ctl;
+  __shared__ WCtl<D, NP> ctl;
   const uint32_t sK = (smem_u32(smem_raw) + 1023u) & ~1023u, sQ = sK + C::kKBufs * C::kKBytes;
   volatile int* abort_flag = &ctl.abort_flag;
   const PagedShape& s = a.s;
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(128) paged_weights_join_kernel(const FaPagedAr
 template <int D, int NP>
 cudaError_t launch_weights(const FaPagedArgs& a, const PagedRows& rows, cudaStream_t st) {
   using C = WCfg<D, NP>;
-  static_assert(C::kSmem + sizeof(WCtl<NP>) <= 227 * 1024, "with the control block");
+  static_assert(C::kSmem + sizeof(WCtl<D, NP>) <= 227 * 1024, "with the control block");
   const PagedShape& s = a.s;
   const bool packed = s.cu_q != nullptr;
   CUtensorMap tq, tk;

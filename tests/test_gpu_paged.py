@@ -185,6 +185,18 @@ def test_more_sequences_than_threads(rows):
     assert abs(float(w.sum()) - seen) < 1e-3 * seen
 
 
+@pytest.mark.parametrize("B", [577, 600, 1300])
+def test_more_sequences_than_threads_of_the_largest_block(B):
+    """40 rows per K/V head at d = 128: the block of the most warps, all of which have sequences to look at."""
+    r = np.random.default_rng(B)
+    lk = r.integers(0, 200, B) * (r.random(B) < 0.2)
+    lq = r.integers(0, 6, B) * (r.random(B) < 0.2)
+    lk[-1], lq[0], lq[-1] = 150, 5, 5
+    p = Problem(lk.tolist(), lq.tolist(), 16, 2, 128, page=16, packed=True, seed=19)
+    for sms in (1, 152):
+        p.check_attend(*p.attend(True, num_sms=sms), True)
+
+
 @pytest.mark.parametrize("n", [1, 4, 70])
 @pytest.mark.parametrize("layout", ["hpd", "gap"])
 @pytest.mark.parametrize("d", [64, 128])
