@@ -24,7 +24,9 @@ struct PagedShape {
 // scheduled as soon as all its CTAs run, sets up what is not in global memory, and then waits for the kernel
 // before it; the dependent does the same, so one kernel's set-up lies under the other's end. The order of
 // memory stays that of the stream: nothing is read or written before the wait, and a kernel that the
-// predecessor waited for is complete when the predecessor is.
+// predecessor waited for is complete when the predecessor is. Lengths, offsets and page tables are read by ordinary
+// loads for this reason: a kernel may be resident while one before it still writes them (an eviction its lengths), and
+// the read-only path (__ldg) holds only for data that nothing writes while the kernel lives.
 __device__ __forceinline__ void let_dependent_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // One sequence of the batch: its new rows, its keys and the causal offset (key j visible to row i iff
@@ -33,15 +35,15 @@ __device__ __forceinline__ void let_dependent_start() { asm volatile("griddepcon
 __device__ __forceinline__ SeqInfo paged_seq(const PagedShape& s, int b) {
   SeqInfo r;
   if (s.cu_q != nullptr) {
-    r.q0 = clampi(__ldg(s.cu_q + b), 0, s.rows_q);
-    r.Lq = clampi(__ldg(s.cu_q + b + 1) - r.q0, 0, min(s.Nq, s.rows_q - r.q0));
+    r.q0 = clampi(s.cu_q[b], 0, s.rows_q);
+    r.Lq = clampi(s.cu_q[b + 1] - r.q0, 0, min(s.Nq, s.rows_q - r.q0));
     r.bb = 0;
   } else {
     r.q0 = 0;
     r.Lq = s.Nq;
     r.bb = b;
   }
-  r.Lk = clampi(__ldg(s.seqlens + b), 0, s.max_k);
+  r.Lk = clampi(s.seqlens[b], 0, s.max_k);
   r.k0 = 0;
   r.off = r.Lk - r.Lq;
   r.krows = r.Lk;
@@ -55,7 +57,7 @@ __device__ __forceinline__ size_t paged_row(const PagedShape& s, const SeqInfo& 
 
 // The page of the table entry `e` of sequence b, or -1 (reported) when it is none of the cache's.
 __device__ __forceinline__ int paged_page(const PagedShape& s, int b, int e, int* status) {
-  const int page = __ldg(s.table + (size_t)b * s.max_pages + e);
+  const int page = s.table[(size_t)b * s.max_pages + e];
   if ((unsigned)page < (unsigned)s.num_pages) return page;
   report_status(status, FA_ERR_BOUNDS);
   return -1;

@@ -12,7 +12,7 @@ __device__ __forceinline__ int sequence_of(const PagedShape& s, int row) {
   int lo = 0, n = s.B;  // the answer is in [lo, lo + n]
   while (n > 0) {
     const int step = (n + 31) >> 5, at = (lane + 1) * step;  // the lane's probe: sequence lo + at - 1
-    const int cnt = __popc(__ballot_sync(0xffffffffu, at <= n && __ldg(s.cu_q + lo + min(at, n)) <= row));
+    const int cnt = __popc(__ballot_sync(0xffffffffu, at <= n && s.cu_q[lo + min(at, n)] <= row));
     lo += cnt * step;
     n = min(n - cnt * step, step - 1);
   }
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const FaPagedArgs a) 
   const SeqInfo seq = paged_seq(s, b);
   if (s.cu_q != nullptr) i = (int)row - seq.q0;
   if (i < 0 || i >= seq.Lq) return;
-  const long long j = (long long)__ldg(s.seqlens + b) - seq.Lq + i;  // the unclamped length places the token
+  const long long j = (long long)s.seqlens[b] - seq.Lq + i;  // the unclamped length places the token
   if (j < 0 || (j >> s.page_shift) >= s.max_pages) {
     if (lane == 0) report_status(a.status, FA_ERR_BOUNDS);
     return;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void select_keys(const FaPagedArgs& a, int b, int hk,
   // No branch: such a place reads page 0, and the loads of all rows are in flight together.
   bool bad = false;
   auto page_at = [&](int k) {
-    return __ldg(s.table + (size_t)b * s.max_pages + (min(j0 + k * kSelRow, old - 1) >> s.page_shift));
+    return s.table[(size_t)b * s.max_pages + (min(j0 + k * kSelRow, old - 1) >> s.page_shift)];
   };
   auto ranks_at = [&](int k, int page) -> uint4 {
     const int j = j0 + k * kSelRow, left = k < rows ? old - j : 0;  // keys of the four that are candidates
@@ -354,10 +354,13 @@ __device__ __forceinline__ void move_rows(const FaPagedArgs& a, int b, int hk, i
   }
 }
 
+// An eviction's dependents start after its new lengths are written, since the forwards over contiguous tensors read their
+// lengths as data that nothing writes while they live.
+
 // One cluster per (sequence, K/V head, K or V).
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedArgs a, int per) {
+  grid_dependency_wait();  // the selection, which writes the lengths, is complete
   let_dependent_start();
-  grid_dependency_wait();
   extern __shared__ __align__(16) uint8_t rows_smem[];
   const PagedShape& s = a.s;
   const int unit = blockIdx.x / kMoveCtas, head = unit >> 1, hk = head % s.Hkv, b = head / s.Hkv;
@@ -371,7 +374,6 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const FaPagedA
 constexpr int kEvictRows = 2;  // rows of 1024 candidates at most
 
 __global__ void __launch_bounds__(kMoveThreads) paged_evict_kernel(const FaPagedArgs a, int per) {
-  let_dependent_start();
   grid_dependency_wait();
   extern __shared__ __align__(16) uint8_t rows_smem[];
   const PagedShape& s = a.s;
@@ -382,6 +384,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_evict_kernel(const FaPaged
   int32_t* mine = reinterpret_cast<int32_t*>(rows_smem + (size_t)2 * per * s.d * 2);
   select_keys<kEvictRows>(a, b, hk, L, 0, 1, mine);
   __syncthreads();
+  let_dependent_start();
   for (int t = cta * kMoveThreads + threadIdx.x; t < a.keep; t += kMoveCtas * kMoveThreads) kept[t] = mine[t];
   move_rows<2>(a, b, hk, 0, cta, per, mine, rows_smem);
 }

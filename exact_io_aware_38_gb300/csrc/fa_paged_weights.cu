@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(WCfg<D, NP>::kThreads, 1)
       // tile earlier than the weight it leads to).
       auto page_of = [&](const WPieces<C::kFew>& y) -> int {
         const int key = (y.kt << 7) + r;
-        return key < y.x.q.Lk ? __ldg(s.table + (size_t)y.b * s.max_pages + (key >> s.page_shift)) : 0;
+        return key < y.x.q.Lk ? s.table[(size_t)y.b * s.max_pages + (key >> s.page_shift)] : 0;
       };
       auto weight_at = [&](const WPieces<C::kFew>& y, int page) -> float* {
         const int key = (y.kt << 7) + r;

@@ -655,3 +655,43 @@ def test_other_streams_and_back_to_back_calls():
     torch.cuda.synchronize()
     for o, lse in outs:
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("L,heads", [(1900, (4, 2, 128)), (6000, (24, 12, 64))])  # an eviction of one launch, and of two
+def test_lengths_of_an_eviction_go_straight_into_the_next_call(L, heads):
+    """Lengths written by an eviction and read by the next calls with no other kernel between, the old ones beside the new
+    in one buffer: the same as with a wait after every call."""
+    p = Problem([L, 700, 40], [1, 1, 1], *heads, page=16, seed=101)
+    k, v = p.k_new.cuda(), p.v_new.cuda()
+    first = [p.ck.clone(), p.cv.clone(), p.cw.clone()]
+    lens = torch.zeros(3, 3, dtype=torch.int32, device="cuda")
+    cont = [torch.randn(3, p.H, 256, p.d, device="cuda").to(torch.bfloat16) for _ in range(3)]
+
+    def chain(n, wait):
+        for t, t0 in zip((p.ck, p.cv, p.cw), first):
+            t.copy_(t0)
+        lens.zero_()
+        lens[0] = torch.tensor(n, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        outs = []
+
+        def done(*x):
+            outs.extend(x)
+            if wait:
+                torch.cuda.synchronize()
+
+        done(*fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, lens[0], 600, recent=30, seqlens_out=lens[1]))
+        done(*fa.fwd(*cont, seqlens_k=lens[1]))
+        done(*fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, lens[1], 200, recent=10, seqlens_out=lens[2]))
+        done(*fa.fwd_paged(p.cq, p.ck, p.cv, p.ctable, lens[2], causal=True, scale=p.scale))
+        done(*fa.paged_evict(p.ck, p.cv, p.cw, p.ctable, lens[2], 100, recent=10, seqlens_out=lens[1]))
+        fa.paged_append(k, v, p.ck, p.cv, p.ctable, lens[1], key_weights=p.cw)
+        done(*fa.fwd_paged(p.cq, p.ck, p.cv, p.ctable, lens[1], causal=True, scale=p.scale))
+        torch.cuda.synchronize()
+        return [t.clone() for t in (*outs, p.ck, p.cv, p.cw)]
+
+    for n in ([L, 700, 40], [650, 20, 1], [L // 2, 300, 7]):
+        want = chain(n, True)
+        for _ in range(30):
+            for x, y in zip(chain(n, False), want):
+                assert torch.equal(torch.nan_to_num(x.float(), 9.0), torch.nan_to_num(y.float(), 9.0))
