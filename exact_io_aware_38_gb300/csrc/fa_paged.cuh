@@ -347,9 +347,13 @@ __device__ __forceinline__ void join_pieces(const FaPagedArgs& a, const float* p
       o[k] = there ? *reinterpret_cast<const float4*>(part_o + at * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float top = M;
+    bool any = false;  // a piece with a visible key, or with NaN (which no maximum shows)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, l[k]);
-    if (top == -INFINITY) continue;
+    for (int k = 0; k < 8; ++k) {
+      top = fmaxf(top, l[k]);
+      any |= l[k] != -INFINITY;
+    }
+    if (!any) continue;
     const float alpha = exp2f(M - top);
     acc = make_float4(acc.x * alpha, acc.y * alpha, acc.z * alpha, acc.w * alpha);
     sum *= alpha;
@@ -364,10 +368,10 @@ __device__ __forceinline__ void join_pieces(const FaPagedArgs& a, const float* p
       acc.w += w * o[k].w;
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (e == 0) a.lse[paged_row(a.s, seq, b, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  if (e == 0) a.lse[paged_row(a.s, seq, b, h, i)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
 }  // namespace fa

@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
         ++pieces;
         fence_after_sync();
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f, lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+      const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? -INFINITY : m + log2f(l);  // (a NaN stays one)
       const bool whole = w.whole();
       const size_t slot = (size_t)(2 * blockIdx.x + (piece == 0 ? 0 : 1)) * 256 + x * 128 + r;
       const int h = w.hv * rows.gs + g;
@@ -663,11 +663,11 @@ __global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const FaPagedA
     const int r = r0 + k * kStep, rr = r & 127;
     const int ti = rr / rows.gs, i = (2 * d.u + (r >> 7)) * rows.tpt + ti, h = d.hv * rows.gs + rr - ti * rows.gs;
     if (rr >= rows.gs * rows.tpt || i >= seq.Lq) continue;
-    const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
         make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
     if (e == 0)
-      a.lse[paged_row(s, seq, d.b, h, i)] = sum[k] > 0.f ? (M[k] + log2f(sum[k])) * kLn2 : -INFINITY;
+      a.lse[paged_row(s, seq, d.b, h, i)] = sum[k] == 0.f ? -INFINITY : (M[k] + log2f(sum[k])) * kLn2;
   }
 }
 

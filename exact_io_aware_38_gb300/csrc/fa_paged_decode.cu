@@ -510,8 +510,8 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
       if (r < NC) {
         const int n = n0 + r;
         const float sum = (ctl.wmax[0][n] + ctl.wmax[1][n]) + (ctl.wmax[2][n] + ctl.wmax[3][n]);
-        ctl.alpha[n] = sum > 0.f ? 1.f / sum : 0.f;
-        const float lse2 = sum > 0.f ? ctl.m[n] + log2f(sum) : -INFINITY;
+        ctl.alpha[n] = sum == 0.f ? 0.f : 1.f / sum;  // (0: no visible key; a NaN stays one)
+        const float lse2 = sum == 0.f ? -INFINITY : ctl.m[n] + log2f(sum);
         if (whole) {
           if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n % G, n / G)] = lse2 * kLn2;
         } else {
@@ -580,10 +580,10 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
           sum += wt;
           acc = make_float4(acc.x + wt * o.x, acc.y + wt * o.y, acc.z + wt * o.z, acc.w + wt * o.w);
         }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (e == 0) a.lse[paged_row(s, seq, b, h, i)] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+      if (e == 0) a.lse[paged_row(s, seq, b, h, i)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
     }
     cluster_sync();  // no CTA leaves while its part is read
   }

@@ -311,7 +311,8 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
  *              keys: token i of L_q is key i + L_k - L_q.
  *   weights    key_weights fp32 [num_pages][Hkv][page_size], contiguous, 16-byte aligned: one number per cached key
  *              and K/V head.
- *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result. A value (not a
+ *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result. A row with a
+ *              NaN, or that sees a key with one, has O = LSE = NaN, and so are the weights that it pays. A value (not a
  *              key) that is infinite or NaN reaches every row of its 128-key tile, also those that causally do not
  *              see it, since a probability of 0 times it is NaN.
  *   sharing    pages may be shared by sequences for reading; a page that a call writes (fa_paged_append,

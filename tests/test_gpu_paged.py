@@ -279,6 +279,29 @@ def test_attend_large_values_behind_growing_scores(n):
     p.check_attend(*p.attend(False), False)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,sms", [(1, 152), (1, 3), (1, 1), (10, 152), (10, 3), (600, 152), (600, 5)])
+def test_nan_key_or_query_is_seen_however_the_work_is_divided(n, sms, d):
+    """A NaN in a key makes O and LSE of the rows that see it NaN, one in a query row those of the row; the rest is as
+    without. Shares of clusters, of divided units and whole ones alike."""
+    L, j, bad_row = 1100, 700, n // 3
+    p = Problem([L, 300], [n, min(n, 300)], 8, 2, d, page=16, seed=31, packed=True)
+    tol = p.score_error() + 2.0**-18
+    ref = p.check_attend(*p.attend(True, num_sms=sms), True)
+    p.ck[p.ctable[0, j // 16].long(), j % 16, 1, 5] = NAN
+    p.cq[bad_row, 2, 7] = NAN
+    o, lse = p.attend(True, num_sms=sms)
+    end = int(p.cu[-1])
+    bad = torch.zeros(end, 8, dtype=torch.bool, device="cuda")
+    bad[:n, 4:] = (torch.arange(n, device="cuda") + L - n >= j)[:, None]
+    bad[bad_row, 2] = True
+    assert torch.isnan(o[:end][bad]).all() and torch.isnan(lse[:, :end].t()[bad]).all()
+    ro, rl, a = np.concatenate([x[0] for x in ref]), np.concatenate([x[1].T for x in ref]), np.concatenate([x[2] for x in ref])
+    good = ~bad.cpu().numpy()
+    assert (np.abs(p.np(o)[:end] - ro) <= 1.05 * 2.0**-8 * (a + np.abs(ro)))[good].all()
+    assert (np.abs(p.np(lse)[:, :end].T - rl) <= tol)[good].all()
+
+
 def test_attend_shared_pages_and_bound():
     """Two sequences share their first pages; a bound above the longest length changes nothing, one below cuts."""
     p = Problem([200, 200], [2, 2], 4, 2, 128, page=16, seed=6)
