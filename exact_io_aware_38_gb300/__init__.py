@@ -739,7 +739,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q=Non
     """Write new keys and values k, v ([B, N, Hkv, d], or packed [rows, Hkv, d] with cu_seqlens_q and max_seqlen_q)
     into the cache (fa_paged_append): as the last keys of each sequence, whose lengths seqlens_k already count them.
     key_weights (float32 [num_pages, Hkv, page_size]), where given, is set to 0 at the written slots."""
-    p, dims = _paged(k, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, None, False, 1.0)
+    # (no bound on the lengths: the table's width alone decides which places exist, and a wide one is no larger work)
+    p, dims = _paged(k, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, 1, False, 1.0)
     if v.shape != k.shape or v.device != k.device or p.H != p.Hkv:
         raise ValueError("k and v must have one shape, with the cache's heads, on the cache's device")
     _check_aux("status", status, torch.int32, 1, k.device)

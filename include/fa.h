@@ -359,7 +359,9 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strid
  * max_pages * page_size is not written and writes FA_ERR_BOUNDS into *dev_status.
  *   k_new, v_new  bf16 [batch][row][head][d], Hkv heads, strides sk_new, sv_new
  *   key_weights   nullable: the weights of the written slots are set to 0
- * p->H, seqlen_k, causal and scale are not used.
+ * seqlen_k bounds nothing here: the table's width decides which places exist. It is checked as for the other calls (at least
+ * 1, and the limit on sizes), so that one problem serves them all; 1 admits a table of any width. p->H, causal and scale
+ * are not used.
  */
 int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_new, const void* v_new,
                     fa_strides sv_new, void* k_cache, fa_strides sk, void* v_cache, fa_strides sv, float* key_weights,

@@ -477,6 +477,25 @@ def test_append_of_many_packed_sequences(B):
     assert np.array_equal(p.np(p.cw), w, equal_nan=True)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_append_with_a_table_far_wider_than_the_lengths(packed):
+    """512 sequences of 32 K/V heads with room for 131072 keys each: the places are what counts, not the table's width."""
+    B, P, wide = 512, 16, 131072 // 16
+    lq = [(b % 3 if packed else 1) for b in range(B)]
+    p = Problem([n + b % 17 for b, n in enumerate(lq)], lq, 32, 32, 64, page=P, packed=packed, seed=73)
+    k, v = p.np(p.k), p.np(p.v)
+    paged.append(p.np(p.k_new), p.np(p.v_new), k, v, p.table.numpy(), p.lk, p.cu)
+    table = torch.full((B, wide), -7, dtype=torch.int32)
+    table[:, :p.width] = p.table
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fa.paged_append(p.k_new.cuda(), p.v_new.cuda(), p.ck, p.cv, table.cuda(), p.clen, status=status, **p.tokens)
+    assert int(status.item()) == 0
+    assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cv), v, equal_nan=True)
+    o, lse = fa.fwd_paged(p.cq, p.ck, p.cv, table.cuda(), p.clen, max_seqlen_k=18, causal=True, scale=p.scale, **p.tokens)
+    p.k, p.v = torch.tensor(k), torch.tensor(v)
+    p.check_attend(o, lse, True)
+
+
 def test_append_places_outside_the_table_are_reported():
     """A length below the token count and one past the table's capacity: the tokens with a place are written."""
     p = Problem([16, 32], [4, 4], 2, 2, 128, page=16, seed=71)

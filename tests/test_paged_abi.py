@@ -119,6 +119,14 @@ def test_sizes_whose_indices_would_not_fit():
     assert evict(problem(B=1, Hkv=1, H=1), keep=(1 << 31) - 1) == evict(problem(), keep=1 << 29) == -2
 
 
+def test_append_takes_a_table_of_any_width():
+    """The bound on the lengths limits the sizes, and an append has no use for a large one (the refusals are the next
+    ones, a missing pointer)."""
+    wide = dict(B=512, H=32, Hkv=32, page_size=16, num_pages=2000, max_pages=131072 // 16)
+    sc = fa.Strides(32 * 128, 128, 16 * 32 * 128)
+    assert append(problem(**wide, seqlen_k=1), sk=sc, sv=sc, kn=None) == -1
+
+
 def test_host_arrays_are_refused():
     """Arrays the kernels read must be device-accessible; this address is not (and there may be no GPU at all)."""
     import ctypes
