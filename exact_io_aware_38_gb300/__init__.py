@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 import os
 
@@ -651,12 +652,18 @@ def _num_sms(dev):
 
 def _on_stream(f):
     """Runs a helper on its `stream` argument (a torch stream or a handle) as the current stream, so that what it
-    allocates belongs to that stream too: a workspace goes back to the pool when the helper returns."""
+    allocates belongs to that stream too: a workspace goes back to the pool when the helper returns. The device is that of
+    the helper's first parameter, by position or by name."""
+    first = next(iter(inspect.signature(f).parameters))
+
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        dev = (args[0] if args else next(iter(kw.values()))).device
+        tensor = args[0] if args else kw.get(first)
+        if not isinstance(tensor, torch.Tensor):
+            return f(*args, **kw)  # (which refuses it)
+        dev = tensor.device
         if dev.type != "cuda":
             raise ValueError(f"the tensors must be on a CUDA device, not {dev}")
         if not hasattr(stream, "cuda_stream"):

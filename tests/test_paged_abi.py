@@ -155,3 +155,22 @@ def test_binding_refuses():
                  lambda s: fa.paged_evict(k, k, z(4, 2, 16, dtype=torch.float32), table, lens, 3, stream=s)):
         with pytest.raises(ValueError, match="CUDA"):  # a stream beside CPU tensors
             call(0)
+
+
+def test_stream_beside_keyword_arguments_in_any_order():
+    """The device is that of the call's first tensor by name; CPU tensors get the refusal that names it."""
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)
+    k, w = z(4, 16, 2, 64), z(4, 2, 16, dtype=torch.float32)
+    table, lens = z(2, 3, dtype=torch.int32), z(2, dtype=torch.int32)
+    at = dict(page_table=table, seqlens_k=lens)
+    for call in (lambda: fa.fwd_paged(causal=True, scale=0.5, **at, k_cache=k, v_cache=k, q=z(2, 1, 4, 64), stream=0),
+                 lambda: fa.fwd_paged(cu_seqlens_q=None, stream=0, v_cache=k, k_cache=k, q=z(2, 1, 4, 64), **at),
+                 lambda: fa.paged_append(**at, key_weights=None, k_cache=k, v_cache=k, v=k[:2], k=k[:2], stream=0),
+                 lambda: fa.paged_key_weights(num_sms=3, **at, lse=w, key_weights=w, k_cache=k, q=z(2, 1, 4, 64), stream=0),
+                 lambda: fa.paged_evict(keep=3, recent=1, **at, key_weights=w, v_cache=k, k_cache=k, stream=0)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError, match="q"):  # without the tensor: the call's own error
+        fa.fwd_paged(causal=True, k_cache=k, v_cache=k, **at, stream=0)
+    with pytest.raises(TypeError):
+        fa.fwd_paged(stream=0)
