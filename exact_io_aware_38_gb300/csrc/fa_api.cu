@@ -293,8 +293,12 @@ int launch_partial(const fa::AttnShape& s, const fa_varlen_problem* p, int split
 // Keys of all (sequence, K/V head) pairs: an index of a key, rounded up to whatever a CTA takes at a time, fits an int.
 constexpr double kMaxKeys = kMaxElems - (1 << 17);
 
-// Paged problem -> shape; FA_OK or an error code. `attend`: the call reads q (heads, scale and causal count).
-int paged_shape(const fa_paged_problem* p, bool attend, fa::PagedShape* out) {
+enum class PagedRowsOf { kQueries, kNewKeys, kNone };
+
+// Paged problem -> shape; FA_OK or an error code. Of: the rows that the call reads. Queries: heads, scale and causal
+// count. None: the shape has no rows, whatever the problem says of them (it is checked like any other).
+int paged_shape(const fa_paged_problem* p, PagedRowsOf of, fa::PagedShape* out) {
+  const bool attend = of == PagedRowsOf::kQueries;
   if (p == nullptr || p->page_table == nullptr || p->seqlens_k == nullptr) return FA_ERR_INVALID_ARG;
   const int rc = attend ? check_common(p->B, p->H, p->Hkv, p->d, p->causal, p->scale)
                         : check_common(p->B, p->Hkv, p->Hkv, p->d, 0, 1.f);
@@ -310,11 +314,11 @@ int paged_shape(const fa_paged_problem* p, bool attend, fa::PagedShape* out) {
   s.H = attend ? p->H : p->Hkv;
   s.Hkv = p->Hkv;
   s.d = p->d;
-  s.Nq = p->seqlen_q;
+  s.Nq = of == PagedRowsOf::kNone ? 1 : p->seqlen_q;
   const long long capacity = (long long)p->max_pages * p->page_size;
   s.max_k = capacity < p->seqlen_k ? (int)capacity : p->seqlen_k;
-  s.cu_q = p->cu_seqlens_q;
-  s.rows_q = p->cu_seqlens_q != nullptr ? p->rows_q : 0;
+  s.cu_q = of == PagedRowsOf::kNone ? nullptr : p->cu_seqlens_q;
+  s.rows_q = s.cu_q != nullptr ? p->rows_q : 0;
   s.causal = attend ? p->causal : 0;
   while ((1 << s.page_shift) < p->page_size) ++s.page_shift;
   s.num_pages = p->num_pages;
@@ -322,9 +326,9 @@ int paged_shape(const fa_paged_problem* p, bool attend, fa::PagedShape* out) {
   s.table = p->page_table;
   s.seqlens = p->seqlens_k;
   const double rows = s.cu_q != nullptr ? (double)s.rows_q : (double)s.B * s.Nq;
-  if (rows * s.H * s.d >= kMaxElems || (double)s.B * s.H * s.Nq >= kMaxElems ||
-      (double)s.B * s.Hkv * s.max_k >= kMaxKeys)
+  if (of != PagedRowsOf::kNone && (rows * s.H * s.d >= kMaxElems || (double)s.B * s.H * s.Nq >= kMaxElems))
     return FA_ERR_UNSUPPORTED;
+  if ((double)s.B * s.Hkv * s.max_k >= kMaxKeys) return FA_ERR_UNSUPPORTED;
   *out = s;
   return FA_OK;
 }
@@ -646,7 +650,7 @@ static int bwd_varlen_impl(const fa_varlen_problem* p, const void* q, fa_strides
 
 size_t fa_fwd_paged_workspace_bytes(const fa_paged_problem* p, int num_sms) {
   fa::PagedShape s;
-  if (paged_shape(p, true, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
+  if (paged_shape(p, PagedRowsOf::kQueries, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
   return paged_workspace(s, num_sms);
 }
 
@@ -654,7 +658,7 @@ int fa_fwd_paged(const fa_paged_problem* p, int num_sms, const void* q, fa_strid
                  fa_strides sk, const void* v_cache, fa_strides sv, void* o, fa_strides so, float* lse, void* workspace,
                  size_t workspace_bytes, int* dev_status, void* stream) {
   FaPagedArgs a{};
-  int rc = paged_shape(p, true, &a.s);
+  int rc = paged_shape(p, PagedRowsOf::kQueries, &a.s);
   if (rc != FA_OK) return rc;
   if (num_sms < 1 || num_sms > kMaxSms) return FA_ERR_INVALID_ARG;
   const size_t need = paged_workspace(a.s, num_sms);
@@ -688,7 +692,7 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
                     fa_strides sv_new, void* k_cache, fa_strides sk, void* v_cache, fa_strides sv, float* key_weights,
                     int* dev_status, void* stream) {
   FaPagedArgs a{};
-  int rc = paged_shape(p, false, &a.s);
+  int rc = paged_shape(p, PagedRowsOf::kNewKeys, &a.s);
   if (rc != FA_OK) return rc;
   const bool packed = a.s.cu_q != nullptr;
   const int rows = packed ? a.s.rows_q : a.s.Nq;
@@ -712,7 +716,7 @@ int fa_paged_append(const fa_paged_problem* p, const void* k_new, fa_strides sk_
 
 size_t fa_paged_key_weights_workspace_bytes(const fa_paged_problem* p, int num_sms) {
   fa::PagedShape s;
-  if (paged_shape(p, true, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
+  if (paged_shape(p, PagedRowsOf::kQueries, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
   return round_up(fa_paged_weights_workspace(s, num_sms));
 }
 
@@ -720,7 +724,7 @@ int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, 
                          fa_strides sk, const float* lse, float* key_weights, void* workspace, size_t workspace_bytes,
                          int* dev_status, void* stream) {
   FaPagedArgs a{};
-  int rc = paged_shape(p, true, &a.s);
+  int rc = paged_shape(p, PagedRowsOf::kQueries, &a.s);
   if (rc != FA_OK) return rc;
   if (num_sms < 1 || num_sms > kMaxSms) return FA_ERR_INVALID_ARG;
   const size_t need = round_up(fa_paged_weights_workspace(a.s, num_sms));
@@ -749,7 +753,7 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
                    fa_strides sv, float* key_weights, int32_t* kept, int32_t* seqlens_out, int* dev_status,
                    void* stream) {
   FaPagedArgs a{};
-  int rc = paged_shape(p, false, &a.s);
+  int rc = paged_shape(p, PagedRowsOf::kNone, &a.s);
   if (rc != FA_OK) return rc;
   if (keep < 1 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
   if ((double)a.s.B * a.s.Hkv * keep >= kMaxKeys) return FA_ERR_UNSUPPORTED;

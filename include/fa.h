@@ -391,7 +391,8 @@ int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, 
  *   seqlens_out   out: int32 [B]: min(L, keep); not the array seqlens_k itself
  * Slots past the new length keep what they held; their pages are the caller's to release. Each K/V head keeps keys
  * of its own, so after an eviction a key index means another token in each head (kept tells which).
- * p->H, seqlen_q, cu_seqlens_q, rows_q, causal and scale are not used.
+ * p->H, causal and scale are not used. Nor are seqlen_q, cu_seqlens_q and rows_q, beyond the checks that every call makes
+ * of them (at least 1, the pointer's alignment): the eviction of a packed step takes the step's problem.
  */
 int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cache, fa_strides sk, void* v_cache,
                    fa_strides sv, float* key_weights, int32_t* kept, int32_t* seqlens_out, int* dev_status,

@@ -554,6 +554,24 @@ def test_evict_long(L):
     assert np.array_equal(p.np(p.cw), w, equal_nan=True)
 
 
+def test_evict_does_not_look_at_the_rows_of_its_problem():
+    """A packed step's problem serves its eviction after cu_seqlens_q is gone (here: an address that no GPU may read)."""
+    import ctypes
+    p = Problem([100, 30], [1, 1], 2, 2, 128, page=16, seed=99)
+    k, v, w = p.np(p.k), p.np(p.v), p.w.double().numpy().copy()
+    kept, n = paged.evict(k, v, w, p.table.numpy(), p.lk, 64, 10)
+    host = (ctypes.c_int32 * 3)(5, 1, 0)
+    prob = fa._paged(None, p.ck, p.cv, p.ctable, p.clen, None, None, None, False, 1.0)[0]
+    prob.cu_seqlens_q, prob.rows_q, prob.seqlen_q = ctypes.addressof(host), 7, 1 << 30
+    got = torch.empty((2, 2, 64), dtype=torch.int32, device="cuda")
+    lens = torch.empty(2, dtype=torch.int32, device="cuda")
+    st = fa._paged_view("k", p.ck, 4)
+    assert fa.fa_paged_evict(prob, 64, 10, p.ck.data_ptr(), st, p.cv.data_ptr(), st, p.cw.data_ptr(), got.data_ptr(),
+                             lens.data_ptr(), None, torch.cuda.current_stream().cuda_stream) == 0
+    assert np.array_equal(got.cpu().numpy(), kept) and np.array_equal(lens.cpu().numpy(), n)
+    assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cw), w, equal_nan=True)
+
+
 # ----------------------------------------------------------------------------- together
 
 

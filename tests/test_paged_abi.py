@@ -104,6 +104,13 @@ def test_no_workspace():
     assert attend(ws=None, nbytes=0, o=A + 2) == weights(ws=None, nbytes=0, w=A + 2) == -3
 
 
+def test_evict_has_no_rows():
+    """An eviction's problem may be that of the step before it: whatever rows it tells of limit nothing (the refusal is
+    the next one, a missing pointer)."""
+    for kw in (dict(seqlen_q=1 << 30), dict(cu_seqlens_q=A, rows_q=1 << 30, seqlen_q=1 << 30)):
+        assert evict(problem(**kw), k=None) == -1
+
+
 def test_evict_budget_and_alias():
     for keep, recent in ((0, 0), (-1, 0), (5, 6), (5, -1)):
         assert evict(keep=keep, recent=recent) == -1
