@@ -758,7 +758,10 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
   if (keep < 1 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
   if ((double)a.s.B * a.s.Hkv * keep >= kMaxKeys) return FA_ERR_UNSUPPORTED;
   if ((rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK) return rc;
-  if (!k_cache || !v_cache || !key_weights || !kept || !seqlens_out || seqlens_out == p->seqlens_k)
+  if (!k_cache || !v_cache || !key_weights || !kept || !seqlens_out) return FA_ERR_INVALID_ARG;
+  // A cluster writes its sequence's new length while others may still have to read their old ones.
+  const uintptr_t old = reinterpret_cast<uintptr_t>(p->seqlens_k), now = reinterpret_cast<uintptr_t>(seqlens_out);
+  if (aligned(seqlens_out, 4) && (now > old ? now - old : old - now) < (size_t)p->B * sizeof(int32_t))
     return FA_ERR_INVALID_ARG;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key_weights, 16) || !aligned(kept, 4) ||
       !aligned(seqlens_out, 4) || !aligned(dev_status, 4))

@@ -388,7 +388,7 @@ int fa_paged_key_weights(const fa_paged_problem* p, int num_sms, const void* q, 
  *   keep, recent  keep >= 1, 0 <= recent <= keep
  *   kept          out: int32 [B][Hkv][keep]: the former index of each kept key, ascending; a sequence of
  *                 L <= keep keys gets 0 .. L - 1 and then -1
- *   seqlens_out   out: int32 [B]: min(L, keep); not the array seqlens_k itself
+ *   seqlens_out   out: int32 [B]: min(L, keep); apart from seqlens_k in memory
  * Slots past the new length keep what they held; their pages are the caller's to release. Each K/V head keeps keys
  * of its own, so after an eviction a key index means another token in each head (kept tells which).
  * p->H, causal and scale are not used. Nor are seqlen_q, cu_seqlens_q and rows_q, beyond the checks that every call makes

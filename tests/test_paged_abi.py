@@ -104,6 +104,15 @@ def test_no_workspace():
     assert attend(ws=None, nbytes=0, o=A + 2) == weights(ws=None, nbytes=0, w=A + 2) == -3
 
 
+def test_evict_lengths_may_not_overlap():
+    """The new lengths of a sequence may not lie over the old ones of any; side by side in one buffer they may."""
+    p = problem(B=5, seqlens_k=2 * A)
+    for off in (-16, -4, 0, 4, 16):
+        assert evict(p, out=2 * A + off, k=None) == -1 and evict(p, out=2 * A + off, kept=A + 2) == -1
+    for off in (-20, 20):
+        assert evict(p, out=2 * A + off, kept=A + 2) == -3
+
+
 def test_evict_has_no_rows():
     """An eviction's problem may be that of the step before it: whatever rows it tells of limit nothing (the refusal is
     the next one, a missing pointer)."""
