@@ -326,8 +326,7 @@ int paged_shape(const fa_paged_problem* p, PagedRowsOf of, fa::PagedShape* out) 
   s.table = p->page_table;
   s.seqlens = p->seqlens_k;
   const double rows = s.cu_q != nullptr ? (double)s.rows_q : (double)s.B * s.Nq;
-  if (of != PagedRowsOf::kNone && (rows * s.H * s.d >= kMaxElems || (double)s.B * s.H * s.Nq >= kMaxElems))
-    return FA_ERR_UNSUPPORTED;
+  if (of != PagedRowsOf::kNone && rows * s.H * s.d >= kMaxElems) return FA_ERR_UNSUPPORTED;
   if ((double)s.B * s.Hkv * s.max_k >= kMaxKeys) return FA_ERR_UNSUPPORTED;
   *out = s;
   return FA_OK;

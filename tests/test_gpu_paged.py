@@ -197,6 +197,23 @@ def test_more_sequences_than_threads_of_the_largest_block(B):
         p.check_attend(*p.attend(True, num_sms=sms), True)
 
 
+def test_packed_batch_with_a_wide_bound_on_its_lengths():
+    """512 sequences whose new tokens are bounded by 2^20: append, attention and key weights."""
+    r = np.random.default_rng(15)
+    lq = r.integers(0, 3, 512)
+    lk = lq + r.integers(0, 40, 512)
+    lq[7], lk[7] = 200, 300
+    p = Problem(lk.tolist(), lq.tolist(), 4, 2, 64, page=16, packed=True, seed=20)
+    p.tokens["max_seqlen_q"] = 1 << 20
+    k, v, w = p.np(p.k), p.np(p.v), p.np(p.w)
+    paged.append(p.np(p.k_new), p.np(p.v_new), k, v, p.table.numpy(), p.lk, p.cu, w)
+    fa.paged_append(p.k_new.cuda(), p.v_new.cuda(), p.ck, p.cv, p.ctable, p.clen, key_weights=p.cw, **p.tokens)
+    assert np.array_equal(p.np(p.ck), k, equal_nan=True) and np.array_equal(p.np(p.cw), w, equal_nan=True)
+    p.k, p.v, p.w = torch.tensor(k), torch.tensor(v), torch.tensor(w).float()
+    p.check_attend(*p.attend(True), True)
+    check_weights(p, True)
+
+
 @pytest.mark.parametrize("n", [1, 4, 70])
 @pytest.mark.parametrize("layout", ["hpd", "gap"])
 @pytest.mark.parametrize("d", [64, 128])

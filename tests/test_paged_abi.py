@@ -143,6 +143,15 @@ def test_append_takes_a_table_of_any_width():
     assert append(problem(**wide, seqlen_k=1), sk=sc, sv=sc, kn=None) == -1
 
 
+def test_packed_rows_are_limited_by_their_number_alone():
+    """The bound on a packed batch's lengths sizes nothing: many sequences may stand beside one long prompt's bound."""
+    p = problem(B=512, H=32, Hkv=8, cu_seqlens_q=A, rows_q=5000, seqlen_q=131072, seqlen_k=131072, max_pages=8192)
+    assert fa.fa_fwd_paged_workspace_bytes(p, 152) > 0 and fa.fa_paged_key_weights_workspace_bytes(p, 152) > 0
+    assert attend(p, q=None) == weights(p, q=None) == append(p, kn=None) == -1
+    p = problem(B=512, H=32, Hkv=8, cu_seqlens_q=A, rows_q=1 << 20, seqlen_q=8, seqlen_k=1024)
+    assert attend(p) == weights(p) == -2
+
+
 def test_host_arrays_are_refused():
     """Arrays the kernels read must be device-accessible; this address is not (and there may be no GPU at all)."""
     import ctypes
