@@ -755,7 +755,8 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
   int rc = paged_shape(p, PagedRowsOf::kNone, &a.s);
   if (rc != FA_OK) return rc;
   if (keep < 1 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
-  if ((double)a.s.B * a.s.Hkv * keep >= kMaxKeys) return FA_ERR_UNSUPPORTED;
+  // (a grid has up to 16 CTAs per sequence and head)
+  if ((double)a.s.B * a.s.Hkv * keep >= kMaxKeys || (double)a.s.B * a.s.Hkv * 16 >= kMaxElems) return FA_ERR_UNSUPPORTED;
   if ((rc = take_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_cache_strides(sv, p, &a.sv)) != FA_OK) return rc;
   if (!k_cache || !v_cache || !key_weights || !kept || !seqlens_out) return FA_ERR_INVALID_ARG;
   // A cluster writes its sequence's new length while others may still have to read their old ones.

@@ -319,7 +319,8 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
  *              fa_paged_key_weights, fa_paged_evict) stands at one place of that call's table, else the writes race.
  *   sizes      all at least 1; (sequences) x (K/V heads) x min(seqlen_k, capacity), and x keep for an eviction, stay
  *              below 2^31 - 2^17 (a table much wider than the lengths in use needs seqlen_k); each tensor of new tokens
- *              has fewer than 2^31 elements (rows x heads x d; packed: rows_q rows, whatever seqlen_q is).
+ *              has fewer than 2^31 elements (rows x heads x d; packed: rows_q rows, whatever seqlen_q is); an eviction
+ *              has fewer than 2^27 sequences x K/V heads.
  *   at once    calls that may overlap (two streams, two captured graphs) each need a workspace of their own.
  * d, H and Hkv as for fa_fwd_gqa. Errors, ownership, dev_status and streams as for fa_fwd.
  */

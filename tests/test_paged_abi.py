@@ -113,6 +113,12 @@ def test_evict_lengths_may_not_overlap():
         assert evict(p, out=2 * A + off, kept=A + 2) == -3
 
 
+def test_evict_heads_that_do_not_fit_a_grid():
+    """16 blocks per sequence and K/V head stay below 2^31."""
+    for B, rc in ((1 << 27, -2), ((1 << 27) - 1, -1)):
+        assert evict(problem(B=B, H=1, Hkv=1, seqlen_k=1), keep=1, recent=0, k=None) == rc
+
+
 def test_evict_has_no_rows():
     """An eviction's problem may be that of the step before it: whatever rows it tells of limit nothing (the refusal is
     the next one, a missing pointer)."""
