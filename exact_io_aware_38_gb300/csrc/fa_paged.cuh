@@ -115,7 +115,8 @@ inline PagedRows paged_rows(int gs, int Hv, int per_kv, int tpt) {
 }
 
 // 128-row tiles: the divisor of the heads per K/V head that fills the rows best, the largest of equals
-// (a K/V tile then serves more heads).
+// (a K/V tile then serves more heads). It does not look at how many tokens there are: a few of a group that does not
+// divide 128 take more tiles than they could (10 tokens of 7 heads: seven of one head each, where one would hold all).
 inline PagedRows paged_rows_for(const PagedShape& s) {
   const int G = s.H / s.Hkv;
   int best = 1;

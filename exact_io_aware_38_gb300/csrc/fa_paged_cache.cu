@@ -390,8 +390,9 @@ __global__ void __launch_bounds__(kMoveThreads) paged_evict_kernel(const FaPaged
 }
 
 // One launch for a few heads of short sequences, where every CTA has an SM to itself and repeats the selection for
-// nothing: 8 heads of 1030 keys 7.1 us for 7.8 (and a launch less on the host, 22 us for 25), of 2000 keys 9.5 for 9.6; 32
-// heads of 2000 keys 13.6 for 13.1, 128 heads 36 for 27.
+// nothing (16 heads have 128 CTAs): 8 heads of 1030 keys 6.8 us for 7.4 (and a launch less on the host, 22 us for 25), of
+// 2000 keys 8.0 for 8.4. From 16 to 32 heads neither form is far ahead: of 1030 keys 7.8 for 8.0 and 8.1 for 8.8, of 2000
+// keys 9.6 for 8.9 and 10.0 for 10.3 (13.6 for 13.1 in another set-up); 128 heads 36 for 27.
 bool evict_at_once(const PagedShape& s) {
   return s.max_k <= kEvictRows * kSelRow && (long long)s.B * s.Hkv <= 16;
 }

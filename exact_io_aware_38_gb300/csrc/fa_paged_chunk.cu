@@ -2,7 +2,8 @@
 // kernel takes, so the pass is bound by the tensor cores (and by the exponentials beside them).
 //
 // What it computes: two 128-row query tiles share every 128-key tile; S = Q K^T, the online softmax
-// and O += P V as in the forward kernel over contiguous tensors, with P in tensor memory. A row of a
+// and O += P V as in the forward kernel over contiguous tensors, with P in tensor memory (rounded to bf16, the type of V
+// beside it in the product: off by 2^-8 of each probability at most; the row sums take it unrounded). A row of a
 // tile is a (token, head) pair: the gs query heads of a group lie side by side for each of tpt = 128 /
 // gs tokens, so a K/V tile serves all of them and a chunk of 32 tokens with 4 heads fills a tile.
 //

@@ -461,6 +461,8 @@ __global__ void __launch_bounds__(DecCfg<D, NP>::kThreads, DecCfg<D, NP>::kCtas)
             tmem_st_wait();
           }
         }
+        // P is rounded to bf16, the type of V beside it in the product (off by 2^-8 of each probability at most); the sum
+        // that O is divided by takes it unrounded.
         uint32_t pk[NC / 2];
 #pragma unroll
         for (int n = 0; n < NC; n += 4) {
@@ -628,9 +630,11 @@ int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0. Alone up to two tiles (one
 // sequence of 8 K/V heads, d = 128, 250 keys: 6.8 us with 1 CTA a unit, 7.1 with 2, 7.6 with 8, 8.4 divided), else the
 // largest cluster that does not outnumber the tiles twice and of which all run at once (16 clusters of 8 do not, 15.9
-// us for 8.5), and at most four tiles a CTA of a cluster (777 keys: 8.5 us with 8, 8.9 with 4, 9.6 divided; 4096 keys: 11.1 with 8, 11.6
-// divided; 8192 keys: 15.4 and 13.6) or eight of one alone (16 sequences of 8 heads, 1024 keys: 13.9 and 17.2; of
-// 12 heads of d = 64: 13.8 and 15.8, of 2048 keys 26 and 24).
+// us for 8.5): a cluster lies within a part of the chip, and 152 SMs hold 15 clusters of 8, 36 of 4 and 76 of 2 at a CTA
+// per SM (by cudaOccupancyMaxActiveClusters). The rule takes 8 up to 2/3 of the CTAs and 4 up to 7/8 (12 and 33 clusters),
+// which leaves some where other work has SMs of such a part. At most four tiles a CTA of a cluster (777 keys: 8.5 us with
+// 8, 8.9 with 4, 9.6 divided; 4096 keys: 11.1 with 8, 11.6 divided; 8192 keys: 15.4 and 13.6) or eight of one alone (16
+// sequences of 8 heads, 1024 keys: 13.9 and 17.2; of 12 heads of d = 64: 13.8 and 15.8, of 2048 keys 26 and 24).
 int unit_ctas(const PagedShape& s, int num_sms) {
   const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * dec_ctas(s.d, padded_rows(s.Nq * (s.H / s.Hkv)));
   const int tiles = (s.max_k + 127) >> 7;

@@ -312,9 +312,10 @@ int fa_finalize_partials(const fa_varlen_problem* p, const float* acc_o, const f
  *   weights    key_weights fp32 [num_pages][Hkv][page_size], contiguous, 16-byte aligned: one number per cached key
  *              and K/V head.
  *   contents   a slot that no length reaches may hold anything, NaN included: it enters no result. A row with a
- *              NaN, or that sees a key with one, has O = LSE = NaN, and so are the weights that it pays. A value (not a
- *              key) that is infinite or NaN reaches every row of its 128-key tile, also those that causally do not
- *              see it, since a probability of 0 times it is NaN.
+ *              NaN, or that sees a key with one, has O = LSE = NaN, and so are the weights that it pays. A key with an
+ *              infinity may get a weight of NaN, also where every row's score for it is -inf. A value (not a key) that
+ *              is infinite or NaN reaches every row of its 128-key tile, also those that causally do not see it, since
+ *              a probability of 0 times it is NaN.
  *   sharing    pages may be shared by sequences for reading; a page that a call writes (fa_paged_append,
  *              fa_paged_key_weights, fa_paged_evict) stands at one place of that call's table, else the writes race.
  *   sizes      all at least 1; (sequences) x (K/V heads) x min(seqlen_k, capacity), and x keep for an eviction, stay
@@ -339,8 +340,8 @@ typedef struct {
 /*
  * Forward attention of the new tokens over the cache: O and LSE. Key j is visible to query i iff j < L_k and
  * (!causal || j <= i + L_k - L_q); a row with no visible key gets O = 0 and LSE = -inf. One token per sequence
- * (decode), a few drafted ones and whole prompt chunks are the same call; rows of q outside every sequence are
- * neither read nor written.
+ * (decode), a few drafted ones and whole prompt chunks are the same call; rows of q outside every sequence
+ * enter no result (a tile may read them) and get none: their O and LSE are not written.
  *   q, o         bf16, strides sq, so; lse fp32 as in fa_fwd_varlen ([B, H, seqlen_q], packed [H, rows_q])
  *   num_sms      1 .. 1024: the CTAs that the work is divided among, one per SM (normally the device's SM count;
  *                fewer leave SMs to other work). The division follows the lengths on the device: each CTA takes an
