@@ -26,3 +26,29 @@ def test_step_percentiles_nearest_rank():
     assert bench.percentiles(list(reversed(xs))) == [2.0, 10.0, 18.0]
     assert bench.percentiles([5.0]) == [5.0, 5.0, 5.0]
     assert bench.percentiles([3.0, 1.0, 2.0], qs=(0, 100)) == [1.0, 3.0]
+
+
+def test_traffic_record_is_of_these_sources():
+    """The counters of every recorded kernel were taken with the committed sources, and the record names all of them:
+    the translation unit, the headers that it includes, directly or not, and what makes its tensor maps."""
+    import json
+    import os
+    import re
+
+    import bench
+
+    csrc = "exact_io_aware_38_gb300/csrc"
+
+    def with_headers(path, seen):
+        if path not in seen:
+            seen.add(path)
+            for name in re.findall(r'^#include "([^"]+)"', open(os.path.join(bench.ROOT, path)).read(), re.M):
+                with_headers(os.path.normpath(os.path.join(csrc, name)), seen)
+        return seen
+
+    for name, rec in json.load(open(os.path.join(bench.ROOT, "profiles", "traffic.json"))).items():
+        unit = [p for p in rec["sources"] if p.endswith("_sm103.cu")]
+        assert len(unit) == 1, name
+        assert with_headers(unit[0], {f"{csrc}/fa_tmap.cu"}) <= set(rec["sources"]), name
+        assert bench.kernel_traffic(name, "c4", None) == rec["dram_bytes_per_launch"], name
+        assert bench.kernel_traffic(name, "c4", 16) is None and bench.kernel_traffic(name, "c5", None) is None
