@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_evict_kernel(const FaPaged
   int32_t* kept = a.kept + (size_t)head * a.keep;
   if (keeps_all(a, b, hk, L, cta, kMoveCtas, kept)) return;  // (the whole cluster)
   int32_t* mine = reinterpret_cast<int32_t*>(rows_smem + (size_t)2 * per * s.d * 2);
+  if (hk == 0 && cta == 0 && threadIdx.x == 0) __threadfence();  // the length that this thread wrote
   select_keys<kEvictRows>(a, b, hk, L, 0, 1, mine);
   __syncthreads();
   let_dependent_start();
