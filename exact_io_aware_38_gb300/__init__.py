@@ -9,7 +9,8 @@ Raw C-ABI names (same signatures as ``include/fa.h``, pointers as ints):
     fa_status_string, fa_bwd_noalloc,
     fa_fwd_varlen, fa_bwd_varlen, fa_bwd_varlen_accumulate, fa_bwd_varlen_workspace_bytes (with the Strides /
     VarlenProblem structs), fa_fwd_paged_workspace_bytes, fa_fwd_paged, fa_paged_append,
-    fa_paged_key_weights, fa_paged_key_weights_workspace_bytes, fa_paged_evict (with the PagedProblem struct)
+    fa_paged_key_weights, fa_paged_key_weights_workspace_bytes, fa_paged_evict, fa_fwd_paged_fp8_workspace_bytes,
+    fa_fwd_paged_fp8, fa_paged_append_fp8, fa_paged_read_fp8 (with the PagedProblem struct)
 Tensor helpers (grouped-query attention when k, v have fewer heads than q):
     fwd(q, k, v, ...) -> (o, lse);  bwd(q, k, v, o, lse, do, ...) -> (dq, dk, dv)
     fwd_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, ...) -> (o, lse): e4m3 inputs (fa_fwd_fp8)
@@ -20,6 +21,8 @@ Tensor helpers (grouped-query attention when k, v have fewer heads than q):
     chunk per sequence) over a K/V cache held in pages; paged_append(...) writes their keys and values,
     paged_key_weights(...) adds the attention weight each cached key received and paged_evict(...) cuts long
     sequences down to the keys of the largest weight.
+    fwd_paged_fp8, paged_append_fp8: the same over a cache held in 8 bits (e4m3 rows with an exponent each);
+    paged_read_fp8(...) reads rows back in bf16.
     fwd_partial / merge_partials / finalize_partials: per-key-block partials and their
     log-sum-exp merge (ring.py builds sequence-sharded ring attention on them).
 """
@@ -105,6 +108,11 @@ _SIGS = {
     "fa_paged_key_weights_workspace_bytes": (ctypes.c_size_t, [_PP, _I]),
     "fa_paged_key_weights": (_I, [_PP, _I, _P, Strides, _P, Strides, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "fa_paged_evict": (_I, [_PP, _I, _I, _P, Strides, _P, Strides, _P, _P, _P, _P, _P]),
+    "fa_fwd_paged_fp8_workspace_bytes": (ctypes.c_size_t, [_PP, _I]),
+    "fa_fwd_paged_fp8": (_I, [_PP, _I, _P, Strides, _P, Strides, _P, Strides, _P, _P, Strides, _P, _P, ctypes.c_size_t,
+                              _P, _P]),
+    "fa_paged_append_fp8": (_I, [_PP, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, _P]),
+    "fa_paged_read_fp8": (_I, [_PP, _P, Strides, _P, Strides, _P, Strides, _P, Strides, _P, _P, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P]),
 }
@@ -239,6 +247,26 @@ def fa_paged_evict(p, keep, recent, k_cache, sk, v_cache, sv, key_weights, kept,
                    stream) -> int:
     return int(lib().fa_paged_evict(ctypes.byref(p), keep, recent, k_cache, sk, v_cache, sv, key_weights, kept,
                                     seqlens_out, dev_status, stream))
+
+
+def fa_fwd_paged_fp8_workspace_bytes(p, num_sms) -> int:
+    return lib().fa_fwd_paged_fp8_workspace_bytes(ctypes.byref(p), num_sms)
+
+
+def fa_fwd_paged_fp8(p, num_sms, q, sq, k_cache, sk, v_cache, sv, codes, o, so, lse, workspace, workspace_bytes,
+                     dev_status, stream) -> int:
+    return lib().fa_fwd_paged_fp8(ctypes.byref(p), num_sms, q, sq, k_cache, sk, v_cache, sv, codes, o, so, lse, workspace,
+                                  workspace_bytes, dev_status, stream)
+
+
+def fa_paged_append_fp8(p, k_new, sk_new, v_new, sv_new, k_cache, sk, v_cache, sv, codes, dev_status, stream) -> int:
+    return lib().fa_paged_append_fp8(ctypes.byref(p), k_new, sk_new, v_new, sv_new, k_cache, sk, v_cache, sv, codes,
+                                     dev_status, stream)
+
+
+def fa_paged_read_fp8(p, k_rows, sk_rows, v_rows, sv_rows, k_cache, sk, v_cache, sv, codes, dev_status, stream) -> int:
+    return lib().fa_paged_read_fp8(ctypes.byref(p), k_rows, sk_rows, v_rows, sv_rows, k_cache, sk, v_cache, sv, codes,
+                                   dev_status, stream)
 
 
 def fa_bwd_noalloc(q, k, v, o, dout, lse, dq, dk, dv, B, H, N, d, causal, block_mask, seqlens_k, scale, dev_status,
@@ -578,23 +606,24 @@ def fwd_splitkv(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=None
 # tensor once, and equal strides share one structure.
 
 
-def _paged_view(name, t, dims):
+def _paged_view(name, t, dims, dtype=torch.bfloat16):
     """fa_strides of a [batch or page, row, head, d] view, or of packed [rows, heads, d] rows. The stride of an
     axis of one element is never used; it is replaced by a legal one."""
     n, st = t.shape, t.stride()
-    if t.dtype is not torch.bfloat16 or len(n) != dims or st[-1] != 1 or not t.is_cuda:
+    if t.dtype is not dtype or len(n) != dims or st[-1] != 1 or not t.is_cuda:
         shape = "[rows, heads, d]" if dims == 3 else "4-D, [batch or page, row, head, d]"
-        raise ValueError(f"{name} must be a bf16 CUDA tensor, {shape}, with a contiguous last dimension")
+        kind = "bf16" if dtype is torch.bfloat16 else "float8_e4m3fn"
+        raise ValueError(f"{name} must be a {kind} CUDA tensor, {shape}, with a contiguous last dimension")
     if 1 in n:
         st = [n[-1] if size == 1 else x for size, x in zip(n, st)]
     return Strides(st[0], st[1], 0) if dims == 3 else Strides(st[1], st[2], st[0])
 
 
-def _paged_views(name_a, a, name_b, b, dims):
+def _paged_views(name_a, a, name_b, b, dims, dtype=torch.bfloat16):
     """_paged_view of two tensors of one shape."""
-    va = _paged_view(name_a, a, dims)
+    va = _paged_view(name_a, a, dims, dtype)
     same = b.stride() == a.stride() and b.dtype is a.dtype and b.device == a.device
-    return va, va if same else _paged_view(name_b, b, dims)
+    return va, va if same else _paged_view(name_b, b, dims, dtype)
 
 
 def _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal, scale):
@@ -810,6 +839,85 @@ def paged_evict(k_cache, v_cache, key_weights, page_table, seqlens_k, keep, *, r
         _launch(dev, lib().fa_paged_evict, ctypes.byref(p), keep, recent, k_cache.data_ptr(), sk,
                 v_cache.data_ptr(), sv, key_weights.data_ptr(), kept.data_ptr(), seqlens_out.data_ptr(), _ptr(status))
     return kept, seqlens_out
+
+
+def _check_codes(scales, p, dev):
+    shape = (p.num_pages, p.Hkv, p.page_size, 2)
+    if not (scales.dtype is torch.uint8 and scales.shape == shape and scales.is_contiguous() and scales.device == dev):
+        raise ValueError(f"scales must be a contiguous uint8 {list(shape)} tensor on {dev}")
+
+
+@_on_stream
+def fwd_paged_fp8(q, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None,
+                  max_seqlen_k=None, *, num_sms=None, causal=False, scale=None, out=None, lse=None, workspace=None,
+                  status=None, stream=None):
+    """fwd_paged over a cache held in 8 bits (fa_fwd_paged_fp8): k_cache and v_cache are float8_e4m3fn [num_pages,
+    page_size, Hkv, d], any strides that are multiples of 16, and scales is uint8 [num_pages, Hkv, page_size, 2], the
+    exponents of each slot's key and value: a row stands for its numbers times 2^(scale - 127). paged_append_fp8 writes
+    them. q, O and LSE are as in fwd_paged. max_seqlen_k sizes the workspace: give the longest length in use."""
+    p, dims = _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal,
+                     scale)
+    dev = q.device
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.device != dev:
+        raise ValueError("out must have q's shape and device")
+    if lse is None:
+        n = q.shape
+        lse = torch.empty((n[1], n[0]) if dims == 3 else (n[0], n[2], n[1]), dtype=torch.float32, device=dev)
+    else:
+        _check_aux("lse", lse, torch.float32, q.numel() // p.d, dev)
+    if status is not None:
+        _check_aux("status", status, torch.int32, 1, dev)
+    _check_codes(scales, p, dev)
+    sq, so = _paged_views("q", q, "out", out, dims)
+    sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4, torch.float8_e4m3fn)
+    if p.B == 0 or q.numel() == 0:  # no new token anywhere
+        return out, lse
+    if num_sms is None:
+        num_sms = _num_sms(dev)
+    L, at = lib(), ctypes.byref(p)
+    ws, nbytes, _keep = _scratch(workspace, L.fa_fwd_paged_fp8_workspace_bytes(at, num_sms), dev)
+    _launch(dev, L.fa_fwd_paged_fp8, at, num_sms, q.data_ptr(), sq, k_cache.data_ptr(), sk, v_cache.data_ptr(), sv,
+            scales.data_ptr(), out.data_ptr(), so, lse.data_ptr(), ws, nbytes, _ptr(status))
+    return out, lse
+
+
+def _rows_fp8(call, k, v, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, status):
+    """paged_append_fp8 or paged_read_fp8: rows k, v on one side, the cache on the other."""
+    # (no bound on the lengths: the table's width alone decides which places exist, and a wide one is no larger work)
+    p, dims = _paged(k, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, 1, False, 1.0)
+    dev = k.device
+    if v.shape != k.shape or v.device != dev or p.H != p.Hkv:
+        raise ValueError("k and v must have one shape, with the cache's heads, on the cache's device")
+    if status is not None:
+        _check_aux("status", status, torch.int32, 1, dev)
+    _check_codes(scales, p, dev)
+    skn, svn = _paged_views("k", k, "v", v, dims)
+    sk, sv = _paged_views("k_cache", k_cache, "v_cache", v_cache, 4, torch.float8_e4m3fn)
+    if p.B > 0 and k.numel() > 0:
+        _launch(dev, call, ctypes.byref(p), k.data_ptr(), skn, v.data_ptr(), svn, k_cache.data_ptr(), sk,
+                v_cache.data_ptr(), sv, scales.data_ptr(), _ptr(status))
+
+
+@_on_stream
+def paged_append_fp8(k, v, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, *,
+                     status=None, stream=None):
+    """Quantise new bf16 keys and values k, v ([B, N, Hkv, d], or packed [rows, Hkv, d] with cu_seqlens_q and
+    max_seqlen_q) and write them into a cache held in 8 bits (fa_paged_append_fp8), in place: as the last keys of each
+    sequence, whose lengths seqlens_k already count them. The cache and its scales are those of fwd_paged_fp8."""
+    _rows_fp8(lib().fa_paged_append_fp8, k, v, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q,
+              status)
+
+
+@_on_stream
+def paged_read_fp8(k, v, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q=None, max_seqlen_q=None, *,
+                   status=None, stream=None):
+    """The way back (fa_paged_read_fp8): fill bf16 rows k, v, laid out as for paged_append_fp8, with the last keys and
+    values of each sequence. Returns (k, v)."""
+    _rows_fp8(lib().fa_paged_read_fp8, k, v, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q,
+              status)
+    return k, v
 
 
 # ----------------------------------------------------------------------------- partials

@@ -339,6 +339,14 @@ int take_cache_strides(const fa_strides& in, const fa_paged_problem* p, FaStride
   return out->row >= most || out->head >= most || out->batch >= most ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
+// The same for a cache of bytes, whose rows start on 16-byte boundaries for every stride.
+int take_byte_cache_strides(const fa_strides& in, const fa_paged_problem* p, FaStrides* out) {
+  if (in.row % 16 || in.head % 16 || (p->num_pages > 1 && in.batch % 16)) return FA_ERR_INVALID_ARG;
+  const int rc = take_cache_strides(in, p, out);
+  out->batch = (out->batch + 15) / 16 * 16;  // (of a single page it is never used)
+  return rc;
+}
+
 bool paged_on_device(const fa::PagedShape& s) {
   return device_accessible(s.table) && device_accessible(s.seqlens) && device_accessible(s.cu_q);
 }
@@ -776,6 +784,99 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
   a.seqlens_out = seqlens_out;
   a.status = dev_status;
   return fa_launch_paged_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_fwd_paged_fp8_workspace_bytes(const fa_paged_problem* p, int num_sms) {
+  fa::PagedShape s;
+  if (paged_shape(p, PagedRowsOf::kQueries, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
+  return round_up(fa_paged_fp8_workspace(s, num_sms));
+}
+
+int fa_fwd_paged_fp8(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
+                     fa_strides sk, const void* v_cache, fa_strides sv, const uint8_t* codes, void* o, fa_strides so,
+                     float* lse, void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
+  FaPagedArgs a{};
+  int rc = paged_shape(p, PagedRowsOf::kQueries, &a.s);
+  if (rc != FA_OK) return rc;
+  if (num_sms < 1 || num_sms > kMaxSms) return FA_ERR_INVALID_ARG;
+  const size_t need = round_up(fa_paged_fp8_workspace(a.s, num_sms));
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  const bool packed = a.s.cu_q != nullptr;
+  const int rows = packed ? a.s.rows_q : a.s.Nq;
+  if ((rc = take_strides(sq, packed, a.s.B, rows, a.s.H, &a.sq)) != FA_OK ||
+      (rc = take_byte_cache_strides(sk, p, &a.sk)) != FA_OK || (rc = take_byte_cache_strides(sv, p, &a.sv)) != FA_OK ||
+      (rc = take_strides(so, packed, a.s.B, rows, a.s.H, &a.so)) != FA_OK)
+    return rc;
+  if (!q || !k_cache || !v_cache || !codes || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(codes, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4) || !aligned(dev_status, 4) || (need > 0 && !aligned(workspace, kAlign)))
+    return FA_ERR_MISALIGNED;
+  if (!paged_on_device(a.s)) return FA_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = const_cast<void*>(k_cache);
+  a.v = const_cast<void*>(v_cache);
+  a.codes = const_cast<uint8_t*>(codes);
+  a.o = o;
+  a.lse = lse;
+  a.scale = p->scale;
+  a.status = dev_status;
+  a.num_sms = num_sms;
+  a.workspace = workspace;
+  return fa_launch_paged_fp8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The arguments that append and read share: rows of new tokens on one side, the cache on the other.
+int take_byte_rows(const fa_paged_problem* p, const void* k, fa_strides sk_rows, const void* v, fa_strides sv_rows,
+                   const void* k_cache, fa_strides sk, const void* v_cache, fa_strides sv, const uint8_t* codes,
+                   int* dev_status, FaPagedArgs* a) {
+  int rc = paged_shape(p, PagedRowsOf::kNewKeys, &a->s);
+  if (rc != FA_OK) return rc;
+  const bool packed = a->s.cu_q != nullptr;
+  const int rows = packed ? a->s.rows_q : a->s.Nq;
+  if ((rc = take_strides(sk_rows, packed, a->s.B, rows, a->s.Hkv, &a->sk_new)) != FA_OK ||
+      (rc = take_strides(sv_rows, packed, a->s.B, rows, a->s.Hkv, &a->sv_new)) != FA_OK ||
+      (rc = take_byte_cache_strides(sk, p, &a->sk)) != FA_OK || (rc = take_byte_cache_strides(sv, p, &a->sv)) != FA_OK)
+    return rc;
+  if (!k || !v || !k_cache || !v_cache || !codes) return FA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(codes, 16) ||
+      !aligned(dev_status, 4))
+    return FA_ERR_MISALIGNED;
+  if (!paged_on_device(a->s)) return FA_ERR_INVALID_ARG;
+  a->k = const_cast<void*>(k_cache);
+  a->v = const_cast<void*>(v_cache);
+  a->codes = const_cast<uint8_t*>(codes);
+  a->status = dev_status;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_paged_append_fp8(const fa_paged_problem* p, const void* k_new, fa_strides sk_new, const void* v_new,
+                        fa_strides sv_new, void* k_cache, fa_strides sk, void* v_cache, fa_strides sv, uint8_t* codes,
+                        int* dev_status, void* stream) {
+  FaPagedArgs a{};
+  const int rc = take_byte_rows(p, k_new, sk_new, v_new, sv_new, k_cache, sk, v_cache, sv, codes, dev_status, &a);
+  if (rc != FA_OK) return rc;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  return fa_launch_paged_append_fp8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_read_fp8(const fa_paged_problem* p, void* k_rows, fa_strides sk_rows, void* v_rows, fa_strides sv_rows,
+                      const void* k_cache, fa_strides sk, const void* v_cache, fa_strides sv, const uint8_t* codes,
+                      int* dev_status, void* stream) {
+  FaPagedArgs a{};
+  const int rc = take_byte_rows(p, k_rows, sk_rows, v_rows, sv_rows, k_cache, sk, v_cache, sv, codes, dev_status, &a);
+  if (rc != FA_OK) return rc;
+  a.k_out = k_rows;
+  a.v_out = v_rows;
+  return fa_launch_paged_read_fp8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -63,6 +63,20 @@ __device__ __forceinline__ int paged_page(const PagedShape& s, int b, int e, int
   return -1;
 }
 
+// The sequence of packed row `row`: the number of sequences that end at or before it. A whole warp looks, 32
+// ends at a time, so 32 sequences take one load and 1000 take two.
+__device__ __forceinline__ int sequence_of(const PagedShape& s, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = s.B;  // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) >> 5, at = (lane + 1) * step;  // the lane's probe: sequence lo + at - 1
+    const int cnt = __popc(__ballot_sync(0xffffffffu, at <= n && s.cu_q[lo + min(at, n)] <= row));
+    lo += cnt * step;
+    n = min(n - cnt * step, step - 1);
+  }
+  return lo;
+}
+
 // Element offset of (page, slot, head) in a cache.
 __device__ __forceinline__ size_t paged_offset(const FaStrides& t, int page, int slot, int h) {
   return (size_t)page * t.batch + (size_t)slot * t.row + (size_t)h * t.head;
@@ -311,7 +325,9 @@ struct FaPagedArgs {
   float* lse;
   FaStrides sq, sk, sv, so;
   const void *k_new, *v_new;  // append
-  FaStrides sk_new, sv_new;
+  void *k_out, *v_out;        // reading back
+  FaStrides sk_new, sv_new;   // of either
+  uint8_t* codes;             // of an 8-bit cache, [num_pages][Hkv][page_size][2]
   float* weights;
   float scale;
   int* status;
@@ -381,3 +397,8 @@ cudaError_t fa_launch_paged_append(const FaPagedArgs& a, cudaStream_t st);
 size_t fa_paged_weights_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_key_weights(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);
+// The cache held in 8 bits: append, reading rows back, and the attention with its workspace.
+cudaError_t fa_launch_paged_append_fp8(const FaPagedArgs& a, cudaStream_t st);
+cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st);
+size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms);
+cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st);

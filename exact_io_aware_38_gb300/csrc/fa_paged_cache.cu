@@ -5,20 +5,6 @@
 namespace fa {
 namespace {
 
-// The sequence of packed row `row`: the number of sequences that end at or before it. A whole warp looks, 32
-// ends at a time, so 32 sequences take one load and 1000 take two.
-__device__ __forceinline__ int sequence_of(const PagedShape& s, int row) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = s.B;  // the answer is in [lo, lo + n]
-  while (n > 0) {
-    const int step = (n + 31) >> 5, at = (lane + 1) * step;  // the lane's probe: sequence lo + at - 1
-    const int cnt = __popc(__ballot_sync(0xffffffffu, at <= n && s.cu_q[lo + min(at, n)] <= row));
-    lo += cnt * step;
-    n = min(n - cnt * step, step - 1);
-  }
-  return lo;
-}
-
 // Append: one warp per new token and tensor (K, V), 16 bytes a lane and up to four of them in flight.
 // Bound by memory: the rows are read and written once (134 MB of 16384 tokens in 23 us, 5.8 TB/s; a thread
 // per 16 bytes took 32 us). 64 tokens take 2.3 us, the latency of a launch and three loads in a row. Packed

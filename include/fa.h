@@ -402,6 +402,55 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
                    void* stream);
 
 /*
+ * The paged cache held in 8 bits: half the memory, and half the bytes that a decode step reads.
+ *   cache      k_cache and v_cache are bytes (e4m3), [page][slot][head][d] as above, d contiguous, with element strides
+ *              (here bytes) that are multiples of 16. Everything said above of pages, the table, lengths, new tokens,
+ *              sharing, sizes and calls at once holds here too.
+ *   codes      uint8 [num_pages][Hkv][page_size][2], contiguous, 16-byte aligned: the exponent of each slot's key (0) and value
+ *              (1). A row stands for its e4m3 numbers y times 2^(code - 127); code 0: a row of zeros; 255: of NaN.
+ *   rounding   fa_paged_append_fp8 writes code = floor(log2 max|x|) - 7 + 127, at least 47, and y = x 2^(127 - code) rounded to
+ *              e4m3 (nearest, ties to even): off by at most 2^-4 of x, or 2^-17 of the row's largest number where that is
+ *              more. A row with NaN or an infinity gets code 255 and bytes of 0. Rows whose largest number is below 2^-73
+ *              lose precision, and numbers below 2^-90 become 0; a number within 2^-5 of bf16's largest may round up to
+ *              2^128, which reads as an infinity. (So a cached row is a row of bf16 numbers, each of them exact.)
+ *   contents   a slot that no length reaches may hold any bytes and codes: it enters no result. A row that sees a key or
+ *              value of code 255, or that holds NaN or an infinity itself, has O = LSE = NaN; rows that do not see it have none of it.
+ *              Bytes of NaN (127 and 255), which an append never writes, reach the rows of their 128-key tile as a NaN
+ *              in a bf16 cache does.
+ * Key weights and eviction take bf16 caches only.
+ */
+
+/*
+ * fa_paged_append into such a cache; no key weights. Arguments, placement and errors as there.
+ */
+int fa_paged_append_fp8(const fa_paged_problem* p, const void* k_new, fa_strides sk_new, const void* v_new,
+                        fa_strides sv_new, void* k_cache, fa_strides sk, void* v_cache, fa_strides sv, uint8_t* codes,
+                        int* dev_status, void* stream);
+
+/*
+ * The way back: row i of sequence b receives key i + seqlens_k[b] - L_q and its value, in bf16 (the places that fa_paged_append_fp8
+ * gives new tokens; L_q = the length reads a whole sequence). A row whose place is negative or past the table, or
+ * whose page is none of the cache's, is left as it was and writes FA_ERR_BOUNDS into *dev_status; so are rows outside every
+ * sequence, without an error.
+ *   k_rows, v_rows  out: bf16 [batch][row][head][d], Hkv heads, strides sk_rows, sv_rows
+ */
+int fa_paged_read_fp8(const fa_paged_problem* p, void* k_rows, fa_strides sk_rows, void* v_rows, fa_strides sv_rows,
+                      const void* k_cache, fa_strides sk, const void* v_cache, fa_strides sv, const uint8_t* codes,
+                      int* dev_status, void* stream);
+
+/*
+ * fa_fwd_paged over such a cache: O and LSE of the new tokens against the rows that it stands for. Arguments, masks, layouts and
+ * errors as there, with the codes beside the caches.
+ *   workspace    device, >= fa_fwd_paged_fp8_workspace_bytes(p, num_sms) bytes, 256-byte aligned; scratch only. It holds
+ *                keys and values read back to bf16, of as many sequences as fit 1 GiB by the bound seqlen_k (one at least), so it
+ *                grows with that bound: give the longest length in use.
+ */
+size_t fa_fwd_paged_fp8_workspace_bytes(const fa_paged_problem* p, int num_sms);
+int fa_fwd_paged_fp8(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
+                     fa_strides sk, const void* v_cache, fa_strides sv, const uint8_t* codes, void* o, fa_strides so,
+                     float* lse, void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
  * Backward pass that allocates nothing, for callers that cannot allocate device memory (a plugin
  * or custom operator inside another framework receives only its input and output buffers; the
  * host framework owns the memory pool, and a cudaMalloc of its own would bypass that pool's
