@@ -400,5 +400,8 @@ cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);
 // The cache held in 8 bits: append, reading rows back, and the attention with its workspace.
 cudaError_t fa_launch_paged_append_fp8(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st);
+bool fa_paged_few8(const fa::PagedShape& s);  // few enough rows for the kernel that reads the bytes as they lie
+size_t fa_paged_few8_workspace(const fa::PagedShape& s, int num_sms);
+cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, cudaStream_t st);
 size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st);

@@ -26,7 +26,7 @@
 // 93 us, with one warp 100, in pages of 8 107 and 155, of 32 and more 89 both ways),
 // warp 1 issues the MMAs, groups of four warps are the softmax and the epilogue, of 16 rows each. Copies run ahead across pieces, so memory never waits for an
 // epilogue.
-#include "fa_paged.cuh"
+#include "fa_paged_few.cuh"
 #include "fa_tmap.h"
 #include "sm103_ptx.cuh"
 
@@ -35,8 +35,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kDecCluster = 8;       // CTAs of the largest cluster that shares a unit
-constexpr float kNoMax = -3.0e38f;   // reference max of a row that has seen no key
 constexpr float kRaise = 8.f;       // log2 units a score may exceed the reference by
 
 // CTAs per SM.
@@ -147,32 +145,6 @@ struct Pieces {
     open(0);
   }
 };
-
-// Reduce v[0 .. 16) over the 32 lanes; afterwards lane l holds column l / 2 in v[0]. A halving exchange: 16
-// shuffles instead of 80.
-template <typename F>
-__device__ __forceinline__ void columns_reduce(float (&v)[16], int lane, F f) {
-#pragma unroll
-  for (int half = 8; half > 0; half >>= 1) {
-    const bool up = lane & (2 * half);
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
-      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, 2 * half));
-    }
-  }
-  v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
-}
-
-__device__ __forceinline__ bool vote_any(bool x, int id) {
-  uint32_t r;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
-      : "=r"(r)
-      : "r"((uint32_t)x), "r"(id)
-      : "memory");
-  return r != 0;
-}
 
 struct DecWork {
   float* part_o;    // [2 CTAs][NP][D]
@@ -624,8 +596,6 @@ __global__ void __launch_bounds__(4 * D) paged_join_kernel(const FaPagedArgs a, 
   seq.bb = of.z;
   join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, blockIdx.x, d.w, n, e, seq, d.x, n / G, d.y * G + n % G);
 }
-
-int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0. Alone up to two tiles (one
 // sequence of 8 K/V heads, d = 128, 250 keys: 6.8 us with 1 CTA a unit, 7.1 with 2, 7.6 with 8, 8.4 divided), else the

@@ -286,10 +286,13 @@ cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st) {
                      : launch_dependent(fa::paged_read_fp8_kernel<128>, grid, block, 0, st, a);
 }
 
-size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms) { return fa::stage_plan(s, num_sms).bytes(); }
+size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms) {
+  return fa_paged_few8(s) ? fa_paged_few8_workspace(s, num_sms) : fa::stage_plan(s, num_sms).bytes();
+}
 
 cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st) {
   const fa::PagedShape& s = a.s;
+  if (fa_paged_few8(s)) return fa_launch_paged_few8(a, st);
   const fa::StagePlan plan = fa::stage_plan(s, a.num_sms);
   char* ws = static_cast<char*>(a.workspace);
   fa::Staged to;

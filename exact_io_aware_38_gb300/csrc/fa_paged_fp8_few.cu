@@ -1,0 +1,773 @@
+// Attention of a few new tokens per sequence over a paged cache held in 8 bits (decode, drafted tokens, short chunks): bound by
+// reading K and V once, half the bytes of the bf16 cache.
+//
+// What it computes: as fa_paged_decode.cu, S^T = K Q^T with a key on each tensor-memory lane and a row on each column, and
+// O^T += V^T P^T, but the products take the e4m3 bytes as they lie in the cache (kind::f8f6f4), so nothing is converted on
+// its way and a 128-key tile is half as many bytes and products. The other operands are split so that nothing of their
+// precision is lost:
+//   Q  a row is scaled by a power of two to a largest element in [128, 256) and split into hi + lo / 32, both e4m3: a bf16
+//      number has 8 bits, hi takes 4 and the signed rest 4, so the sum is exact down to 2^-15 of the row's largest element.
+//   P  = hi + mid + lo, three e5m2 numbers cut from its fp16 rounding: 9 bits and more, off by 2^-9 of a probability at most
+//      (bf16 2^-8), and by 2^-17 below, where the row's largest is 2^7 at least.
+// The parts lie side by side as columns of one product (N = 2 rows for S, 3 rows for O), and are added up in fp32 when they
+// are read: at few rows the columns cost nothing beside the 128 lanes.
+//
+// The exponents of a key and its value are a lane's: the key's scales the scores of its lane, and the value's goes into the
+// exponent of P, y = c s 2^k log2 e + v, P = 2^(y - ref). So P V needs no further factor, and the reference follows the
+// products P |V|: a key with much weight but a tiny value (or none) does not push the others out of e5m2's range. The row sum
+// takes P 2^-v, by an FMA with a lane's constant.
+//
+// The exponentials are taken against a reference per row that starts 2^7 below the first tile's largest and is raised
+// (O and the row sums rescaled) only when a score exceeds it by more than 2^15.
+//
+// Rows: up to 64 (tokens x heads of a K/V head) are one unit of 16, 32 or 64 columns; more are units of 64 that each
+// read the keys, mostly from L2. Division of the work, pieces, clusters and joins as in fa_paged_decode.cu.
+//
+// Roles: warp 0 copies keys, the warp before the last values and codes (TMA, a lane per page; the codes by 8-byte asynchronous
+// copies, four keys a lane), warp 1 issues the MMAs, groups of four warps are the softmax and the epilogue, of 16 rows each,
+// and the last warp splits Q, a piece ahead.
+#include <cuda_fp16.h>
+
+#include "fa_paged_few.cuh"
+#include "fa_tmap.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace tc;
+
+constexpr float kFirst = 7.f;    // log2 units that the reference starts below the first tile's largest
+constexpr float kRaise8 = 15.f;  // and that a score may exceed it by: 2^15 is near the top of e5m2 and fp16
+constexpr float kLoScale = 32.f;
+constexpr int kZeroRow = -80;    // exponent that stands for a value row of zeros: only its place in the row sum counts
+
+constexpr int few8_ctas(int np) { return np == 16 ? 2 : 1; }  // per SM
+
+template <int D, int NP>
+struct F8Cfg {
+  static constexpr int kTileBytes = 128 * D;
+  static constexpr int kCtas = few8_ctas(NP);
+  static constexpr int kGroups = NP / 16, kThreads = 128 + 128 * kGroups;
+  static constexpr int kKStages = NP == 16 ? (D == 128 ? 3 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;
+  static constexpr int kVStages = NP == 16 ? (D == 128 ? 2 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 3 : 6;
+  static constexpr int kQBytes = 2 * NP * D, kQBufs = 2;
+  // P: 128 keys, a row of 3 NP bytes each, cut into blocks of 128. Two buffers: at 16 rows side by side in a row, else
+  // one behind the other.
+  static constexpr int kPBlocks = (3 * NP + 127) / 128;
+  static constexpr int kPStep = NP == 16 ? 64 : kPBlocks * 16384;
+  static constexpr int kPBytes = NP == 16 ? 16384 : 2 * kPStep;
+  static constexpr int kSmem = kQBufs * kQBytes + (kKStages + kVStages) * kTileBytes + kPBytes + 1024;
+  static constexpr int kOBufs = NP == 64 ? 1 : 2;
+  static constexpr uint32_t kO = 4 * NP;  // tensor memory: S x 2, then O
+  static constexpr uint32_t kTmemCols = NP == 16 ? 256 : 512;
+  static_assert(kO + kOBufs * 3 * NP <= kTmemCols);
+  static constexpr uint32_t kIdS = idesc_e4m3(128, 2 * NP);
+  // O^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared memory and are never read.
+  static constexpr uint32_t kIdPV = idesc_e4m3_e5m2_mn(128, 3 * NP);
+};
+
+constexpr int kF8Open = 1;  // positions of a unit before its first tile, for its epilogue
+
+struct F8Units {
+  int heads, count, open;
+  SeqInfo q;
+  F8Units() = default;
+  __device__ F8Units(const PagedShape& s, int tpu, int b) : heads(s.Hkv), open(kF8Open), q(paged_seq(s, b)) {
+    count = q.Lq <= tpu ? q.Lq > 0 : (q.Lq + tpu - 1) / tpu;
+  }
+  __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
+  __device__ long long before(int u) const { return (long long)u * (tiles() + open); }
+};
+
+template <int D, int NP>
+struct F8Ctl {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], c_full[8];
+  uint64_t s_full[2];
+  uint64_t p_ready[2], pv_done[2];  // per buffer of P
+  uint64_t o_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  long long scan[F8Cfg<D, NP>::kThreads / 32];  // an entry per warp
+  Share share;
+  F8Units units;             // of the sequence where the share begins
+  int issued_k, issued_v;    // copies issued (abort-path drain)
+  alignas(16) uint8_t codes[8][256];  // by stage of V: key and value of each slot
+  alignas(16) float qmul[2][NP];      // by buffer of Q: c log2 e times the row's power of two
+  alignas(16) float ref[NP];
+  alignas(16) float alpha[NP];
+  float wmax[4][NP];
+  float part_lse[NP];  // log2 units, of this CTA's part of a unit that a cluster shares
+  int lim[NP];
+};
+
+// The pieces of a CTA's share: key tiles [kt, end) of the n of (b, hk, u), walked in order by every role.
+struct F8Pieces {
+  const PagedShape& s;
+  int tpu, b, hk, u, kt, n, end, count;
+  long long todo;  // positions from the piece on
+  bool finished;
+  SeqInfo seq;
+  __device__ F8Pieces(const PagedShape& s_, int tpu_, const Share& sh, const F8Units& first)
+      : s(s_), tpu(tpu_), b(sh.b), hk(sh.head), u(sh.unit), kt(0), n(0), end(0), count(0), todo(sh.todo), finished(false) {
+    if (todo == 0) return;
+    sequence(first);
+    open(sh.tile);
+  }
+  __device__ void sequence(const F8Units& x) {
+    seq = x.q;
+    count = x.count;
+    n = count ? x.tiles() : 0;
+  }
+  __device__ void open(int at) {  // at: position within the unit
+    kt = max(0, at - kF8Open);
+    const long long stop = at + todo - kF8Open;
+    end = stop < n ? (int)stop : n;
+    todo -= min((long long)(n + kF8Open - at), todo);
+    if (end <= kt) finished = true;  // the share ends before the unit's first tile
+  }
+  __device__ bool done() const { return finished || n == 0; }
+  __device__ bool whole() const { return kt == 0 && end == n; }
+  __device__ int token() const { return u * tpu; }  // the unit's first
+  __device__ int tokens() const { return min(tpu, seq.Lq - u * tpu); }
+  __device__ void next() {
+    if (todo == 0) {
+      finished = true;
+      return;
+    }
+    if (++u == count) {
+      u = 0;
+      if (++hk == s.Hkv) {
+        hk = 0;
+        do {  // todo > 0: a later sequence has new tokens
+          ++b;
+          sequence(F8Units(s, tpu, b));
+        } while (n == 0);
+      }
+    }
+    open(0);
+  }
+};
+
+struct F8Work {
+  float* part_o;    // [2 CTAs][NP][D]
+  float* part_lse;  // [2 CTAs][NP], log2 units
+  int4* desc;       // [CTAs][2]: {b, hk, first CTA, its slot}, {rows, q0, bb, first token} of the unit; b = -1: none ends
+                    // here in pieces. Null: every unit has a CTA or a cluster of its own
+  int tpu;          // tokens of a unit
+};
+
+// Two probabilities' parts: hi and mid by cutting their fp16 after two fraction bits (a byte), lo by rounding the rest.
+__device__ __forceinline__ void split_p(float p0, float p1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  __half2 h = __floats2half2_rn(p0, p1);
+  hi = *reinterpret_cast<uint32_t*>(&h) & 0xff00ff00u;
+  __half2 r = __hsub2(h, *reinterpret_cast<__half2*>(&hi));
+  mid = *reinterpret_cast<uint32_t*>(&r) & 0xff00ff00u;
+  r = __hsub2(r, *reinterpret_cast<__half2*>(&mid));
+  uint16_t y;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(y) : "r"(*reinterpret_cast<uint32_t*>(&r)));
+  lo = y;
+}
+
+__device__ __forceinline__ void store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
+    paged_few8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const FaPagedArgs a, const F8Work wk) {
+  using C = F8Cfg<D, NP>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) F8Ctl<D, NP> ctl;
+  const uint32_t sK0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sV0 = sK0 + C::kKStages * C::kTileBytes, sP = sV0 + C::kVStages * C::kTileBytes;
+  const uint32_t sQ = sP + C::kPBytes;
+  float* my_part = reinterpret_cast<float*>(smem_raw + (sK0 - smem_u32(smem_raw)));
+  volatile int* abort_flag = &ctl.abort_flag;
+  const PagedShape& s = a.s;
+  const int G = s.H / s.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto sV = [&](int i) { return sV0 + i * C::kTileBytes; };
+  auto bar = [&](uint64_t& x) { return smem_u32(&x); };
+
+  if (threadIdx.x == 0) {
+    ctl.abort_flag = 0;
+    ctl.issued_k = ctl.issued_v = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(ctl.q_full[i]), 32);
+      mbar_init(bar(ctl.q_empty[i]), 1 + 4 * C::kGroups);
+      mbar_init(bar(ctl.s_full[i]), 1);
+      mbar_init(bar(ctl.o_free[i]), 128 * C::kGroups);
+      mbar_init(bar(ctl.p_ready[i]), 128 * C::kGroups);
+      mbar_init(bar(ctl.pv_done[i]), 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(bar(ctl.k_full[i]), 1);
+      mbar_init(bar(ctl.k_empty[i]), 1);
+      mbar_init(bar(ctl.v_full[i]), 1);
+      mbar_init(bar(ctl.v_empty[i]), 1);
+      mbar_init(bar(ctl.c_full[i]), 32);
+    }
+    mbar_init(bar(ctl.drain), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (threadIdx.x < NP) ctl.part_lse[threadIdx.x] = -INFINITY;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
+  grid_dependency_wait();
+  const int ctas = wk.desc != nullptr ? 1 : (int)cluster_size();  // that share a unit
+  if (wk.desc != nullptr) {
+    find_share<C::kThreads>(s.B, [&](int b) { return F8Units(s, wk.tpu, b); }, ctl.share, ctl.scan, ctl.units);
+  } else if (threadIdx.x == 0) {  // tiles [n rank / ctas, n (rank + 1) / ctas) of the cluster's unit
+    const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv;
+    const F8Units x(s, wk.tpu, b);
+    const int n = x.count ? x.tiles() : 0, lo = n * rank / ctas, hi = n * (rank + 1) / ctas;
+    ctl.share = Share{b, unit - b * s.Hkv, 0, kF8Open + lo, hi - lo, 0, 0};
+    ctl.units = x;
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  F8Pieces w(s, wk.tpu, ctl.share, ctl.units);
+  if (wk.desc != nullptr && threadIdx.x == 0) {
+    const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
+    wk.desc[2 * blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);
+    wk.desc[2 * blockIdx.x + 1] = make_int4(joins ? w.tokens() * G : 0, w.seq.q0, w.seq.bb, w.token());
+  }
+
+  if (warp == 0 || warp == C::kThreads / 32 - 2) {
+    // ------------------------------------------------------------------ copies of K; of V and the codes
+    const bool values = warp != 0;
+    const int P = 1 << s.page_shift, rows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
+    const int stages = values ? C::kVStages : C::kKStages;
+    const uint32_t full0 = values ? bar(ctl.v_full[0]) : bar(ctl.k_full[0]);
+    const uint32_t empty0 = values ? bar(ctl.v_empty[0]) : bar(ctl.k_empty[0]);
+    const uint32_t tile0 = values ? sV0 : sK0;
+    const CUtensorMap* tm = values ? &tmV : &tmK;
+    bool run = true;
+    int t = 0, st = 0;
+    uint32_t phase = 1;
+    // Page of tile kt that this lane copies (-1, reported: none of the cache's, reads as zero).
+    auto page_of = [&](const F8Pieces& x, int kt) -> int {
+      const int key = (kt << 7) + (lane << shift);
+      return lane < per && key < x.seq.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
+    };
+    while (!w.done()) {
+      int page = page_of(w, w.kt);
+      for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+        const int left = w.seq.Lk - (kt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
+        const int next = kt + 1 < w.end ? page_of(w, kt + 1) : 0;
+        const uint32_t full = full0 + st * 8;
+        if (run && t >= stages) run = mbar_wait(empty0 + st * 8, phase, abort_flag, a.status);
+        run = __all_sync(0xffffffffu, run) && !*abort_flag;
+#ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for keys and values must run out cleanly
+        run = false;
+#endif
+        if (run) {
+          if (lane == 0) {
+            mbar_expect_tx(full, pages * rows * D);
+            (values ? ctl.issued_v : ctl.issued_k) = t + 1;
+          }
+          __syncwarp();
+          if (lane < pages)
+            tma_load_4d(tile0 + st * C::kTileBytes + lane * rows * D, tm, 0, (kt << 7) & (P - 1), w.hk, page, full);
+          if (values) {
+            const int at = __shfl_sync(0xffffffffu, page, (4 * lane) >> shift), key = (kt << 7) + 4 * lane;
+            if (key < w.seq.Lk && at >= 0)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(ctl.codes[st] + 8 * lane)),
+                           "l"(a.codes + 2 * weight_offset(s, at, w.hk, key & (P - 1)))
+                           : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.c_full[st])) : "memory");
+          }
+        }
+        if (++st == stages) {
+          st = 0;
+          phase ^= 1;
+        }
+        page = next;
+      }
+      w.next();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == C::kThreads / 32 - 1) {
+    // ------------------------------------------------------------------ Q, split
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
+    constexpr int kBatch = NP / kPer < 8 ? NP / kPer : 8;
+    const int r0 = lane / kLanes, part = lane % kLanes;
+    const float sl2 = a.scale * kLog2e;
+    bool run = true;
+    for (int piece = 0; !w.done(); ++piece, w.next()) {
+      const int qb = piece & 1, live = w.tokens() * G;
+      if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+      run = __all_sync(0xffffffffu, run) && !*abort_flag;
+      if (!run) continue;
+      const uint32_t to = sQ + qb * C::kQBytes;
+      for (int n0 = 0; n0 < NP; n0 += kBatch * kPer) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int n = n0 + k * kPer + r0, i = n / G;
+          x[k] = n < live ? *reinterpret_cast<const uint4*>(
+                                reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                elem_offset(a.sq, w.seq.bb, w.seq.q0 + w.token() + i, w.hk * G + n - i * G) + part * 8)
+                          : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int n = n0 + k * kPer + r0;
+          const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t top = max(m & 0xffffu, m >> 16);
+          const bool bad = top >= 0x7f80u;
+          const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
+          const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
+            hi[i] = pack_e4m3x2(f0, f1);
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
+            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+            lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
+            if (bad) hi[i] = lo[i] = 0;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int row = half * NP + n;
+            const uint32_t* y = half ? lo : hi;
+            const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + row * D + (chunk << 4) + (part & 1) * 8),
+                         "r"(y[0] | y[1] << 16), "r"(y[2] | y[3] << 16)
+                         : "memory");
+          }
+          if (part == 0) ctl.qmul[qb][n] = bad ? NAN : n < live ? sl2 * __uint_as_float(code << 23) : 0.f;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(ctl.q_full[qb]));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      bool run = true;
+      F8Pieces v = w;  // the piece of the next S
+      int left = v.end - v.kt, ks = 0, vpiece = 0;  // its key tiles without S; ring position
+      uint32_t kphase = 0, sb = 0;
+      bool opens = true;
+      const uint64_t dk0 = D == 128 ? desc_kmajor_sw128(sK0) : desc_kmajor_sw64(sK0);
+      const uint64_t dq0 = D == 128 ? desc_kmajor_sw128(sQ) : desc_kmajor_sw64(sQ);
+      const uint64_t dv0 = D == 128 ? desc_mnmajor_sw128(sV0, 16384) : desc_mnmajor_sw64(sV0, C::kTileBytes);
+      const uint64_t dp0 = desc_mnmajor_sw128(sP, 16384);
+      auto issue_s = [&]() {
+        const int qb = vpiece & 1;
+        if (run && opens) run = mbar_wait_spin(bar(ctl.q_full[qb]), (vpiece >> 1) & 1, abort_flag, a.status);
+        if (run) run = mbar_wait_spin(bar(ctl.k_full[ks]), kphase, abort_flag, a.status);
+        fence_after_sync();
+        if (run) {
+          const uint64_t dk = desc_add(dk0, ks * C::kTileBytes), dq = desc_add(dq0, qb * C::kQBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_ss_f8(tmem + sb * 2 * NP, desc_add(dk, kk * 32), desc_add(dq, kk * 32), C::kIdS, kk > 0);
+          mma_commit(bar(ctl.s_full[sb]));
+          mma_commit(bar(ctl.k_empty[ks]));
+          if (left == 1) mma_commit(bar(ctl.q_empty[qb]));
+        }
+        sb ^= 1;
+        if (++ks == C::kKStages) {
+          ks = 0;
+          kphase ^= 1;
+        }
+        opens = --left == 0;
+        if (opens) {
+          v.next();
+          left = v.end - v.kt;
+          ++vpiece;
+        }
+      };
+      if (!w.done()) issue_s();
+      int vs = 0;
+      uint32_t vphase = 0, pb = 0, pphase = 0;
+      for (int piece = 0; !w.done(); ++piece) {
+        const int ob = C::kOBufs == 2 ? piece & 1 : 0, uses = C::kOBufs == 2 ? piece >> 1 : piece;
+        const uint32_t tO = tmem + C::kO + ob * 3 * NP;
+        for (int kt = w.kt; kt < w.end; ++kt) {
+          if (!v.done()) issue_s();
+          if (run) run = mbar_wait_spin(bar(ctl.p_ready[pb]), pphase, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.v_full[vs]), vphase, abort_flag, a.status);
+          if (run && kt == w.kt && uses > 0)
+            run = mbar_wait_spin(bar(ctl.o_free[ob]), (uses - 1) & 1, abort_flag, a.status);
+          fence_after_sync();
+          if (run) {
+            const uint64_t dv = desc_add(dv0, vs * C::kTileBytes), dp = desc_add(dp0, pb * C::kPStep);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss_f8(tO, desc_add(dv, kk * 32 * D), desc_add(dp, kk * 4096), C::kIdPV, kk > 0 || kt > w.kt);
+            mma_commit(bar(ctl.v_empty[vs]));
+            mma_commit(bar(ctl.pv_done[pb]));
+          }
+          pphase ^= pb;
+          pb ^= 1;
+          if (++vs == C::kVStages) {
+            vs = 0;
+            vphase ^= 1;
+          }
+        }
+        w.next();
+      }
+      mma_commit(bar(ctl.drain));
+      mbar_wait_drain(bar(ctl.drain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, epilogue
+    const int quad = warp & 3, r = quad * 32 + lane;  // key within the tile; head dimension of O^T
+    constexpr int NC = 16;
+    const int gr = C::kGroups == 1 ? 0 : (warp - 2) >> 2, n0 = gr * NC, on = 1 + gr;  // group, first column, barrier
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    bool run = true;
+    int t = 0, vs = 0;
+    uint32_t vphase = 0;
+    auto wait_pv = [&](int j) -> bool {  // P V of tile j has completed
+      return mbar_wait(bar(ctl.pv_done[j & 1]), (j >> 1) & 1, abort_flag, a.status);
+    };
+    for (int piece = 0; !w.done(); ++piece) {
+      const SeqInfo& seq = w.seq;
+      const int live = w.tokens() * G, tok = w.token(), qb = piece & 1;
+      const uint32_t tO = tmem + lane_off + C::kO + (C::kOBufs == 2 ? piece & 1 : 0) * 3 * NP + n0;
+      if (run) run = mbar_wait(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
+      if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, tok + (n0 + r) / G + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
+      const int least = s.causal ? min(seq.Lk, tok + seq.off + 1) : seq.Lk;
+      float l[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) l[n] = 0.f;
+      for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+        if (run) run = mbar_wait(bar(ctl.c_full[vs]), vphase, abort_flag, a.status);
+        const uint32_t code = *reinterpret_cast<const uint16_t*>(ctl.codes[vs] + 2 * r), kc = code & 255u, vc = code >> 8;
+        const float kmul = kc == 255u ? NAN : __uint_as_float(kc << 23);
+        const float vexp = vc == 255u ? NAN : vc == 0u ? (float)kZeroRow : (float)((int)vc - 127);
+        const float back = __uint_as_float((vc == 0u ? (uint32_t)(127 - kZeroRow) : 254u - min(vc, 253u)) << 23);  // 2^-vexp
+        if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
+        fence_after_sync();
+        float y[NC];
+        {
+          uint32_t hi[NC], lo[NC];
+          tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + n0, hi);
+          tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + NP + n0, lo);
+          tmem_ld_wait();
+          const float2 part = make_float2(1.f / kLoScale, 1.f / kLoScale), km = make_float2(kmul, kmul);
+          const float2 ve = make_float2(vexp, vexp);
+#pragma unroll
+          for (int n = 0; n < NC; n += 2) {
+            const float2 q = *reinterpret_cast<const float2*>(ctl.qmul[qb] + n0 + n);
+            const float2 x = fma2(make_float2(__uint_as_float(lo[n]), __uint_as_float(lo[n + 1])), part,
+                                  make_float2(__uint_as_float(hi[n]), __uint_as_float(hi[n + 1])));
+            const float2 z = fma2(x, mul2(km, q), ve);
+            y[n] = z.x;
+            y[n + 1] = z.y;
+          }
+        }
+        const int key = (kt << 7) + r;
+        const bool opens = kt == w.kt;
+        if (opens) named_bar_sync(on, 128);  // ctl.lim is written; the last piece's ctl.ref is no longer read
+        if ((kt << 7) + 128 > least) {
+#pragma unroll
+          for (int n = 0; n < NC; ++n) y[n] = key < ctl.lim[n0 + n] ? y[n] : -INFINITY;
+        }
+        bool raise = opens;
+        if (!opens) {
+          bool big = false;
+#pragma unroll
+          for (int n = 0; n < NC; n += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ctl.ref + n0 + n);
+            big |= fmaxf(fmax3(y[n] - m.x, y[n + 1] - m.y, y[n + 2] - m.z), y[n + 3] - m.w) > kRaise8;
+          }
+          raise = vote_any(big, on);
+        }
+        if (raise) {
+          float z[NC];
+#pragma unroll
+          for (int n = 0; n < NC; ++n) z[n] = y[n];
+          columns_reduce(z, lane, [](float p, float q) { return fmaxf(p, q); });
+          ctl.wmax[quad][n0 + (lane >> 1)] = z[0];
+          named_bar_sync(on, 128);
+          if (r < NC) {
+            const int n = n0 + r;
+            const float old = opens ? kNoMax : ctl.ref[n];
+            const float now = fmaxf(
+                fmaxf(fmaxf(ctl.wmax[0][n], ctl.wmax[1][n]), fmaxf(ctl.wmax[2][n], ctl.wmax[3][n])) - kFirst, old);
+            ctl.alpha[n] = ex2_approx(old - now);
+            ctl.ref[n] = now;
+          }
+          __syncwarp();
+          named_bar_sync(on, 128);
+          if (!opens) {
+            if (run) run = wait_pv(t - 1);
+            fence_after_sync();
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              uint32_t o[NC];
+              tmem_ld16(tO + part * NP, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < NC; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ctl.alpha[n0 + i]);
+              tmem_st16(tO + part * NP, o);
+            }
+            tmem_st_wait();
+#pragma unroll
+            for (int i = 0; i < NC; ++i) l[i] *= ctl.alpha[n0 + i];
+          }
+        }
+        uint32_t hi[NC / 4], mid[NC / 4], lo[NC / 4];
+#pragma unroll
+        for (int n = 0; n < NC; n += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(ctl.ref + n0 + n);
+          const float p0 = ex2_approx(y[n] - m.x), p1 = ex2_approx(y[n + 1] - m.y);
+          const float p2 = ex2_approx(y[n + 2] - m.z), p3 = ex2_approx(y[n + 3] - m.w);
+          l[n] = fmaf(p0, back, l[n]);
+          l[n + 1] = fmaf(p1, back, l[n + 1]);
+          l[n + 2] = fmaf(p2, back, l[n + 2]);
+          l[n + 3] = fmaf(p3, back, l[n + 3]);
+          uint32_t ha, hb, ma, mb, la, lb;
+          split_p(p0, p1, ha, ma, la);
+          split_p(p2, p3, hb, mb, lb);
+          hi[n / 4] = __byte_perm(ha, hb, 0x7531);
+          mid[n / 4] = __byte_perm(ma, mb, 0x7531);
+          lo[n / 4] = la | lb << 16;
+        }
+        // P's buffer is free: the P V that read it, of tile t - 2, was issued before S of tile t, which has
+        // completed.
+        const uint32_t sPt = sP + (NP == 16 ? 0 : (t & 1) * C::kPStep) + r * 128;
+        auto put = [&](int c, const uint32_t (&x)[NC / 4]) {  // c: 16-byte chunk of the row's 3 NP bytes
+          store16(sPt + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+        };
+        const int c0 = gr + (NP == 16 ? (t & 1) * 4 : 0);
+        put(c0, hi);
+        put(c0 + NP / 16, mid);
+        put(c0 + 2 * (NP / 16), lo);
+        // Value rows past the last key may hold anything, and 0 times NaN is NaN: they become 0.
+        const int valid = seq.Lk - (kt << 7);
+        if (valid < 128) {
+          if (run) run = mbar_wait(bar(ctl.v_full[vs]), vphase, abort_flag, a.status);
+          if (run && r >= valid)
+#pragma unroll
+            for (int c = gr * (D / 16 / C::kGroups); c < (gr + 1) * (D / 16 / C::kGroups); ++c)
+              store16(sV(vs) + r * D + c * 16, 0, 0, 0, 0);
+          __syncwarp();
+        }
+        fence_proxy_async_smem();
+        fence_before_sync();
+        if (run) mbar_arrive(bar(ctl.p_ready[t & 1]));
+        if (++vs == C::kVStages) {
+          vs = 0;
+          vphase ^= 1;
+        }
+      }
+      // ---------------------------------------------------------------- end of the piece
+      __syncwarp();
+      if (run && lane == 0) mbar_arrive(bar(ctl.q_empty[qb]));  // (its scales are read)
+      columns_reduce(l, lane, [](float p, float q) { return p + q; });
+      ctl.wmax[quad][n0 + (lane >> 1)] = l[0];
+      named_bar_sync(on, 128);
+      const bool whole = w.whole() && ctas == 1;
+      const int slot = 2 * blockIdx.x + (piece == 0 ? 0 : 1);
+      if (r < NC) {
+        const int n = n0 + r;
+        const float sum = (ctl.wmax[0][n] + ctl.wmax[1][n]) + (ctl.wmax[2][n] + ctl.wmax[3][n]);
+        ctl.alpha[n] = sum == 0.f ? 0.f : 1.f / sum;  // (0: no visible key; a NaN stays one)
+        const float lse2 = sum == 0.f ? -INFINITY : ctl.ref[n] + log2f(sum);
+        if (whole) {
+          if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n % G, tok + n / G)] = lse2 * kLn2;
+        } else {
+          (ctas > 1 ? ctl.part_lse : wk.part_lse + (size_t)slot * NP)[n] = lse2;
+        }
+      }
+      __syncwarp();
+      named_bar_sync(on, 128);
+      if (run) run = wait_pv(t - 1);
+      fence_after_sync();
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + tok, w.hk * G) + r;
+      // (the cluster's parts lie over the ring: with the last P V done nothing reads it or is on its way there)
+      float* part = (ctas > 1 ? my_part : wk.part_o + (size_t)slot * NP * D) + r;
+      int i = n0 / G, g = n0 % G;  // token and head of the group of column n
+      float o[NC];
+      {
+        uint32_t x[NC], z[NC];
+        tmem_ld16(tO, reinterpret_cast<uint32_t(&)[NC]>(o));
+        tmem_ld16(tO + NP, x);
+        tmem_ld16(tO + 2 * NP, z);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < NC; ++k) o[k] += __uint_as_float(x[k]) + __uint_as_float(z[k]);
+      }
+      if (r < D) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          const int n = n0 + k;
+          if (n < live) {
+            const float val = o[k] * ctl.alpha[n];
+            if (whole)
+              out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
+            else
+              part[n * D] = val;
+          }
+          if (++g == G) {
+            g = 0;
+            ++i;
+          }
+        }
+      }
+      fence_before_sync();
+      if (run) mbar_arrive(bar(ctl.o_free[C::kOBufs == 2 ? piece & 1 : 0]));
+      w.next();
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (ctas > 1) {
+    // The cluster's CTAs join their parts, each some of the elements: M = max LSE, w = 2^(LSE - M), O = sum w O / sum w.
+    cluster_sync();
+    const SeqInfo& seq = ctl.units.q;
+    const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv, hk = unit - b * s.Hkv;
+    for (int x = rank * C::kThreads + threadIdx.x; x < seq.Lq * G * (D / 4); x += ctas * C::kThreads) {
+      const int n = x / (D / 4), e = x % (D / 4) * 4, i = n / G, h = hk * G + n - i * G;
+      float l[kDecCluster], M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kDecCluster; ++c) {
+        l[c] = c < ctas ? load_peer(ctl.part_lse + n, c) : -INFINITY;
+        M = fmaxf(M, l[c]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kDecCluster; ++c)
+        if (l[c] != -INFINITY) {
+          const float wt = exp2f(l[c] - M);
+          const float4 o = load_peer4(my_part + n * D + e, c);
+          sum += wt;
+          acc = make_float4(acc.x + wt * o.x, acc.y + wt * o.y, acc.z + wt * o.z, acc.w + wt * o.w);
+        }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + i, h) + e) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (e == 0) a.lse[paged_row(s, seq, b, h, i)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // no CTA leaves while its part is read
+  }
+  if (threadIdx.x == 0 && *abort_flag) {  // copies still in flight land before the CTA exits: the last one into each buffer
+    for (int i = max(0, ctl.issued_k - C::kKStages); i < ctl.issued_k; ++i)
+      mbar_wait_drain(bar(ctl.k_full[i % C::kKStages]), (i / C::kKStages) & 1);
+    for (int i = max(0, ctl.issued_v - C::kVStages); i < ctl.issued_v; ++i)
+      mbar_wait_drain(bar(ctl.v_full[i % C::kVStages]), (i / C::kVStages) & 1);
+  }
+}
+
+// Joins the pieces of each divided unit. Block (c, y) takes 16 rows of the one that ends in CTA c's first piece, if it
+// began before; a thread has four elements of a row.
+template <int D, int NP>
+__global__ void __launch_bounds__(4 * D) paged_few8_join_kernel(const FaPagedArgs a, const F8Work wk) {
+  let_dependent_start();
+  grid_dependency_wait();
+  const int4 d = wk.desc[2 * blockIdx.x], of = wk.desc[2 * blockIdx.x + 1];
+  const PagedShape& s = a.s;
+  const int G = s.H / s.Hkv, n = blockIdx.y * 16 + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4;
+  if (d.x < 0 || n >= of.x) return;
+  SeqInfo seq{};
+  seq.q0 = of.y;
+  seq.bb = of.z;
+  join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, blockIdx.x, d.w, n, e, seq, d.x, of.w + n / G, d.y * G + n % G);
+}
+
+int unit_tokens(const PagedShape& s) {
+  const int G = s.H / s.Hkv;
+  return (long long)s.Nq * G <= 64 ? s.Nq : 64 / G;
+}
+int unit_rows(const PagedShape& s) { return padded_rows(unit_tokens(s) * (s.H / s.Hkv)); }
+
+// CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0; the rule of fa_paged_decode.cu.
+int unit_ctas(const PagedShape& s, int num_sms) {
+  if (unit_tokens(s) < s.Nq) return 0;
+  const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s));
+  const int tiles = (s.max_k + 127) >> 7;
+  int ctas = 1;
+  if (tiles > 2) {
+    if (tiles > 4 && units * 8 * 3 <= room * 2)
+      ctas = 8;
+    else if (units * 4 * 8 <= room * 7)
+      ctas = 4;
+    else if (units * 2 <= room)
+      ctas = 2;
+  }
+  return units * ctas <= room && tiles <= (ctas == 1 ? 8 : 4 * ctas) ? ctas : 0;
+}
+
+template <int D, int NP>
+cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
+  using C = F8Cfg<D, NP>;
+  const PagedShape& s = a.s;
+  const int P = 1 << s.page_shift, box = P < 128 ? P : 128;
+  CUtensorMap tk, tv;
+  if (!fa_make_tmap_u8(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, D, box, D) ||
+      !fa_make_tmap_u8(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, D, box, D))
+    return cudaErrorInvalidValue;
+  const int shared = unit_ctas(s, a.num_sms), ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
+  F8Work wk{};
+  wk.tpu = unit_tokens(s);
+  if (shared == 0) {
+    char* ws = static_cast<char*>(a.workspace);
+    wk.desc = reinterpret_cast<int4*>(ws);
+    ws += up256((size_t)ctas * 2 * sizeof(int4));
+    wk.part_lse = reinterpret_cast<float*>(ws);
+    ws += up256((size_t)ctas * 2 * NP * sizeof(float));
+    wk.part_o = reinterpret_cast<float*>(ws);
+  }
+  auto kern = paged_few8_kernel<D, NP>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  if (C::kCtas > 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e != cudaSuccess) return e;
+  if (shared > 0) return launch_dependent_cluster(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, shared, st, tk, tv, a, wk);
+  e = launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tk, tv, a, wk);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_few8_join_kernel<D, NP>, dim3(ctas, NP / 16), dim3(4 * D), 0, st, a, wk);
+}
+
+}  // namespace
+}  // namespace fa
+
+// Up to four units of 64 rows; more rows, or a group of heads that no unit holds, go by way of the chunk kernel.
+bool fa_paged_few8(const fa::PagedShape& s) {
+  const int G = s.H / s.Hkv;
+  return G <= 64 && (long long)s.Nq <= 4ll * (64 / G);
+}
+
+size_t fa_paged_few8_workspace(const fa::PagedShape& s, int num_sms) {
+  if (fa::unit_ctas(s, num_sms) > 0) return 0;
+  const int np = fa::unit_rows(s);
+  const size_t ctas = (size_t)num_sms * fa::few8_ctas(np), rows = ctas * 2 * np;
+  return fa::up256(ctas * 2 * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
+}
+
+cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, cudaStream_t st) {
+  const int np = fa::unit_rows(a.s);
+  if (a.s.d == 64)
+    return np == 16 ? fa::launch_few8<64, 16>(a, st) : np == 32 ? fa::launch_few8<64, 32>(a, st) : fa::launch_few8<64, 64>(a, st);
+  return np == 16 ? fa::launch_few8<128, 16>(a, st) : np == 32 ? fa::launch_few8<128, 32>(a, st) : fa::launch_few8<128, 64>(a, st);
+}

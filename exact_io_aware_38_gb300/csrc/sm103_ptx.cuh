@@ -196,6 +196,16 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t 
   return d;
 }
 
+// The same two for rows of 64 bytes (64 e4m3 elements) under the 64-byte swizzle: 8 rows are 512 bytes.
+__device__ __forceinline__ uint64_t desc_kmajor_sw64(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(512u >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)4 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mnmajor_sw64(uint32_t saddr, uint32_t mn_block_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((mn_block_bytes >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)(512u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
+}
+
 // The descriptor of (base + byte_off), given the descriptor of base: the start-address field holds
 // address >> 4 in 14 bits and shared-memory addresses stay below 2^18, so adding byte_off >> 4
 // never carries out of the field. Saves the issuing thread rebuilding descriptors per MMA.
@@ -210,6 +220,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
 // kind::f8f6f4 instruction descriptor: e4m3 A and B (format code 0), fp32 D, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with both operands MN-major and B in e5m2 (format code 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_mn(int M, int N) {
+  return idesc_e4m3(M, N) | (1u << 10) | (1u << 15) | (1u << 16);
 }
 
 // ----------------------------------------------------------------------------- tcgen05
