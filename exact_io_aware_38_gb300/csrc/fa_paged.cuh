@@ -239,13 +239,14 @@ struct Division {
   }
 };
 
-// Finds the share of CTA blockIdx.x; all threads of the CTA take part, and `sh`, `scan` (an entry per
+// Finds the share of CTA `cta` of `ctas`; all threads of the CTA take part, and `sh`, `scan` (an entry per
 // warp) and `at` are in shared memory; `at` becomes the units of sequence sh.b where the share is not
 // empty. Units, made by make(b): heads, count, before(u) (positions before unit u, one head's), tiles(u), and open,
 // the positions of a unit before its first tile. Every kernel begins with this and can load nothing before it knows its
 // share, so it counts in full: each sequence is looked at once, and few divisions are left.
 template <int kThreads, int kScan, typename Units, typename Make>
-__device__ void find_share(int B, Make&& make, Share& sh, long long (&scan)[kScan], Units& at) {
+__device__ void find_share(int B, Make&& make, Share& sh, long long (&scan)[kScan], Units& at, int cta = blockIdx.x,
+                           int ctas = gridDim.x) {
   static_assert(kScan >= kThreads / 32 && kScan >= 2, "scan has an entry per warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = B <= kThreads ? 1 : (B + kThreads - 1) / kThreads, first = threadIdx.x * per, last = min(B, first + per);
@@ -279,7 +280,7 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long (&scan)[kSca
   }
   __syncthreads();  // scan is read
   if (total == 0) return;
-  const long long n = min(total, (long long)gridDim.x), c = blockIdx.x;  // no CTA before the last busy one is idle
+  const long long n = min(total, (long long)ctas), c = cta;  // no CTA before the last busy one is idle
   if (c >= n) return;
   const Division cut(total, n);
   const long long lo = cut.begin(c);

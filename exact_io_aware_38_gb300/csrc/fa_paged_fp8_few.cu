@@ -23,9 +23,10 @@
 // Rows: up to 64 (tokens x heads of a K/V head) are one unit of 16, 32 or 64 columns; more are units of 64 that each
 // read the keys, mostly from L2. Division of the work, pieces, clusters and joins as in fa_paged_decode.cu.
 //
-// Roles: warp 0 copies keys, the warp before the last values and codes (TMA, a lane per page; the codes by 8-byte asynchronous
-// copies, four keys a lane), warp 1 issues the MMAs, groups of four warps are the softmax and the epilogue, of 16 rows each,
-// and the last warp splits Q, a piece ahead.
+// Roles: warp 0 copies keys and codes (TMA, a lane per page; the codes by 8-byte asynchronous copies, four keys a lane), warp 1
+// issues S, groups of four warps are the softmax and the epilogue, of 16 rows each, the warp before the last issues P V, and
+// the last copies values and splits Q, a piece ahead. Each of these takes 600 to 1300 cycles a tile: one thread that issued both
+// products took 2000, and issuers that also copied more, since whatever follows an MMA waits for its dispatch.
 #include <cuda_fp16.h>
 
 #include "fa_paged_few.cuh"
@@ -67,14 +68,27 @@ struct F8Cfg {
   static constexpr uint32_t kIdPV = idesc_e4m3_e5m2_mn(128, 3 * NP);
 };
 
+// Codes wait in a ring of their own, longer than the keys' (whose copies they go with): a copy of keys t follows S of t - kKStages,
+// which follows P V of two tiles before that, so the codes of t - 16 are read.
+constexpr int kCodeStages = 16;
+
 constexpr int kF8Open = 1;  // positions of a unit before its first tile, for its epilogue
+
+// How the work is cut. The K/V heads of a sequence are `turns` turns of `side` neighbours each: CTA c takes head c % side of every
+// turn, and the line of units that the CTAs of one residue divide has a turn where it would have a head. So `side` CTAs walk
+// over the same keys of neighbouring heads at about the same time, and what lies next to one another in memory is
+// fetched at about the same time.
+struct F8Cut {
+  int tokens;  // of a unit
+  int side, turns;
+};
 
 struct F8Units {
   int heads, count, open;
   SeqInfo q;
   F8Units() = default;
-  __device__ F8Units(const PagedShape& s, int tpu, int b) : heads(s.Hkv), open(kF8Open), q(paged_seq(s, b)) {
-    count = q.Lq <= tpu ? q.Lq > 0 : (q.Lq + tpu - 1) / tpu;
+  __device__ F8Units(const PagedShape& s, const F8Cut& c, int b) : heads(c.turns), open(kF8Open), q(paged_seq(s, b)) {
+    count = q.Lq <= c.tokens ? q.Lq > 0 : (q.Lq + c.tokens - 1) / c.tokens;
   }
   __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
   __device__ long long before(int u) const { return (long long)u * (tiles() + open); }
@@ -83,18 +97,19 @@ struct F8Units {
 template <int D, int NP>
 struct F8Ctl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], c_full[8];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // (v_empty: also that P V has completed)
+  uint64_t c_full[kCodeStages];
   uint64_t s_full[2];
-  uint64_t p_ready[2], pv_done[2];  // per buffer of P
+  uint64_t p_ready[2];  // per buffer of P
   uint64_t o_free[2];
-  uint64_t drain;
+  uint64_t drain[2];    // per issuer
   uint32_t tmem_base;
   int abort_flag;
   long long scan[F8Cfg<D, NP>::kThreads / 32];  // an entry per warp
   Share share;
   F8Units units;             // of the sequence where the share begins
   int issued_k, issued_v;    // copies issued (abort-path drain)
-  alignas(16) uint8_t codes[8][256];  // by stage of V: key and value of each slot
+  alignas(16) uint8_t codes[kCodeStages][256];  // key and value of each slot
   alignas(16) float qmul[2][NP];      // by buffer of Q: c log2 e times the row's power of two
   alignas(16) float ref[NP];
   alignas(16) float alpha[NP];
@@ -106,12 +121,14 @@ struct F8Ctl {
 // The pieces of a CTA's share: key tiles [kt, end) of the n of (b, hk, u), walked in order by every role.
 struct F8Pieces {
   const PagedShape& s;
-  int tpu, b, hk, u, kt, n, end, count;
+  const F8Cut& cut;
+  int b, hk, u, kt, n, end, count;
   long long todo;  // positions from the piece on
   bool finished;
   SeqInfo seq;
-  __device__ F8Pieces(const PagedShape& s_, int tpu_, const Share& sh, const F8Units& first)
-      : s(s_), tpu(tpu_), b(sh.b), hk(sh.head), u(sh.unit), kt(0), n(0), end(0), count(0), todo(sh.todo), finished(false) {
+  __device__ F8Pieces(const PagedShape& s_, const F8Cut& cut_, const Share& sh, const F8Units& first, int beside)
+      : s(s_), cut(cut_), b(sh.b), hk(sh.head * cut.side + beside), u(sh.unit), kt(0), n(0), end(0), count(0), todo(sh.todo),
+        finished(false) {
     if (todo == 0) return;
     sequence(first);
     open(sh.tile);
@@ -130,8 +147,8 @@ struct F8Pieces {
   }
   __device__ bool done() const { return finished || n == 0; }
   __device__ bool whole() const { return kt == 0 && end == n; }
-  __device__ int token() const { return u * tpu; }  // the unit's first
-  __device__ int tokens() const { return min(tpu, seq.Lq - u * tpu); }
+  __device__ int token() const { return u * cut.tokens; }  // the unit's first
+  __device__ int tokens() const { return min(cut.tokens, seq.Lq - u * cut.tokens); }
   __device__ void next() {
     if (todo == 0) {
       finished = true;
@@ -139,11 +156,12 @@ struct F8Pieces {
     }
     if (++u == count) {
       u = 0;
-      if (++hk == s.Hkv) {
-        hk = 0;
+      hk += cut.side;
+      if (hk >= s.Hkv) {
+        hk -= s.Hkv;
         do {  // todo > 0: a later sequence has new tokens
           ++b;
-          sequence(F8Units(s, tpu, b));
+          sequence(F8Units(s, cut, b));
         } while (n == 0);
       }
     }
@@ -156,7 +174,7 @@ struct F8Work {
   float* part_lse;  // [2 CTAs][NP], log2 units
   int4* desc;       // [CTAs][2]: {b, hk, first CTA, its slot}, {rows, q0, bb, first token} of the unit; b = -1: none ends
                     // here in pieces. Null: every unit has a CTA or a cluster of its own
-  int tpu;          // tokens of a unit
+  F8Cut cut;
 };
 
 // Two probabilities' parts: hi and mid by cutting their fp16 after two fraction bits (a byte), lo by rounding the rest.
@@ -202,16 +220,15 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       mbar_init(bar(ctl.s_full[i]), 1);
       mbar_init(bar(ctl.o_free[i]), 128 * C::kGroups);
       mbar_init(bar(ctl.p_ready[i]), 128 * C::kGroups);
-      mbar_init(bar(ctl.pv_done[i]), 1);
+      mbar_init(bar(ctl.drain[i]), 1);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(bar(ctl.k_full[i]), 1);
       mbar_init(bar(ctl.k_empty[i]), 1);
       mbar_init(bar(ctl.v_full[i]), 1);
       mbar_init(bar(ctl.v_empty[i]), 1);
-      mbar_init(bar(ctl.c_full[i]), 32);
     }
-    mbar_init(bar(ctl.drain), 1);
+    for (int i = 0; i < kCodeStages; ++i) mbar_init(bar(ctl.c_full[i]), 32);
     fence_mbar_init();
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -225,11 +242,15 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
   let_dependent_start();  // (this CTA has its tensor memory: a dependent that takes some cannot be in its way)
   grid_dependency_wait();
   const int ctas = wk.desc != nullptr ? 1 : (int)cluster_size();  // that share a unit
+  // The CTA among those that divide the work, and its number: those of one residue follow one another.
+  const int beside = blockIdx.x % wk.cut.side, group = blockIdx.x / wk.cut.side, groups = gridDim.x / wk.cut.side;
+  const int me = beside * groups + group;
   if (wk.desc != nullptr) {
-    find_share<C::kThreads>(s.B, [&](int b) { return F8Units(s, wk.tpu, b); }, ctl.share, ctl.scan, ctl.units);
+    find_share<C::kThreads>(s.B, [&](int b) { return F8Units(s, wk.cut, b); }, ctl.share, ctl.scan, ctl.units, group,
+                            groups);
   } else if (threadIdx.x == 0) {  // tiles [n rank / ctas, n (rank + 1) / ctas) of the cluster's unit
     const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv;
-    const F8Units x(s, wk.tpu, b);
+    const F8Units x(s, wk.cut, b);
     const int n = x.count ? x.tiles() : 0, lo = n * rank / ctas, hi = n * (rank + 1) / ctas;
     ctl.share = Share{b, unit - b * s.Hkv, 0, kF8Open + lo, hi - lo, 0, 0};
     ctl.units = x;
@@ -238,15 +259,17 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  F8Pieces w(s, wk.tpu, ctl.share, ctl.units);
+  F8Pieces w(s, wk.cut, ctl.share, ctl.units, beside);
   if (wk.desc != nullptr && threadIdx.x == 0) {
     const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
-    wk.desc[2 * blockIdx.x] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta, ctl.share.first_slot);
-    wk.desc[2 * blockIdx.x + 1] = make_int4(joins ? w.tokens() * G : 0, w.seq.q0, w.seq.bb, w.token());
+    wk.desc[2 * me] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta + me - group,
+                                ctl.share.first_slot + 2 * (me - group));
+    wk.desc[2 * me + 1] = make_int4(joins ? w.tokens() * G : 0, w.seq.q0, w.seq.bb, w.token());
   }
 
-  if (warp == 0 || warp == C::kThreads / 32 - 2) {
-    // ------------------------------------------------------------------ copies of K; of V and the codes
+  constexpr int kLast = C::kThreads / 32 - 1;
+  if (warp == 0 || warp == kLast) {
+    // ------------------------------------------------------------------ copies of K and codes; of V, and Q split
     const bool values = warp != 0;
     const int P = 1 << s.page_shift, rows = min(P, 128), shift = min(s.page_shift, 7), per = 128 >> shift;
     const int stages = values ? C::kVStages : C::kKStages;
@@ -255,182 +278,211 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     const uint32_t tile0 = values ? sV0 : sK0;
     const CUtensorMap* tm = values ? &tmV : &tmK;
     bool run = true;
-    int t = 0, st = 0;
-    uint32_t phase = 1;
-    // Page of tile kt that this lane copies (-1, reported: none of the cache's, reads as zero).
-    auto page_of = [&](const F8Pieces& x, int kt) -> int {
-      const int key = (kt << 7) + (lane << shift);
-      return lane < per && key < x.seq.Lk ? paged_page(s, x.b, key >> s.page_shift, a.status) : 0;
+    F8Pieces x = w;  // of the next copy
+    int xkt = x.kt, xt = 0, xst = 0;
+    uint32_t xphase = 1;
+    // The page of the next copy that is this lane's, as the table has it: it is looked at when the copy is made, so that
+    // nothing waits for the load.
+    auto look_up = [&]() -> int {
+      const int key = (xkt << 7) + (lane << shift);
+      return lane < per && key < x.seq.Lk ? s.table[(size_t)x.b * s.max_pages + (key >> s.page_shift)] : 0;
     };
-    while (!w.done()) {
-      int page = page_of(w, w.kt);
-      for (int kt = w.kt; kt < w.end; ++kt, ++t) {
-        const int left = w.seq.Lk - (kt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
-        const int next = kt + 1 < w.end ? page_of(w, kt + 1) : 0;
-        const uint32_t full = full0 + st * 8;
-        if (run && t >= stages) run = mbar_wait(empty0 + st * 8, phase, abort_flag, a.status);
-        run = __all_sync(0xffffffffu, run) && !*abort_flag;
-#ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for keys and values must run out cleanly
-        run = false;
-#endif
-        if (run) {
-          if (lane == 0) {
-            mbar_expect_tx(full, pages * rows * D);
-            (values ? ctl.issued_v : ctl.issued_k) = t + 1;
-          }
-          __syncwarp();
-          if (lane < pages)
-            tma_load_4d(tile0 + st * C::kTileBytes + lane * rows * D, tm, 0, (kt << 7) & (P - 1), w.hk, page, full);
-          if (values) {
-            const int at = __shfl_sync(0xffffffffu, page, (4 * lane) >> shift), key = (kt << 7) + 4 * lane;
-            if (key < w.seq.Lk && at >= 0)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(ctl.codes[st] + 8 * lane)),
-                           "l"(a.codes + 2 * weight_offset(s, at, w.hk, key & (P - 1)))
-                           : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.c_full[st])) : "memory");
-          }
-        }
-        if (++st == stages) {
-          st = 0;
-          phase ^= 1;
-        }
-        page = next;
-      }
-      w.next();
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == C::kThreads / 32 - 1) {
-    // ------------------------------------------------------------------ Q, split
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-    constexpr int kBatch = NP / kPer < 8 ? NP / kPer : 8;
-    const int r0 = lane / kLanes, part = lane % kLanes;
-    const float sl2 = a.scale * kLog2e;
-    bool run = true;
-    for (int piece = 0; !w.done(); ++piece, w.next()) {
-      const int qb = piece & 1, live = w.tokens() * G;
-      if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+    int listed = x.done() ? 0 : look_up();
+    const uint64_t once = l2_evict_first();
+    auto copy = [&]() {  // the next tile
+      const int left = x.seq.Lk - (xkt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
+      const uint32_t full = full0 + xst * 8;
+      if (run && xt >= stages) run = mbar_wait(empty0 + xst * 8, xphase, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
-      if (!run) continue;
-      const uint32_t to = sQ + qb * C::kQBytes;
-      for (int n0 = 0; n0 < NP; n0 += kBatch * kPer) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int n = n0 + k * kPer + r0, i = n / G;
-          x[k] = n < live ? *reinterpret_cast<const uint4*>(
-                                reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                elem_offset(a.sq, w.seq.bb, w.seq.q0 + w.token() + i, w.hk * G + n - i * G) + part * 8)
-                          : make_uint4(0, 0, 0, 0);
+#ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for keys and values must run out cleanly
+      run = false;
+#endif
+      if (run) {
+        const bool ours = (unsigned)listed < (unsigned)s.num_pages;
+        if (!ours) report_status(a.status, FA_ERR_BOUNDS);
+        const int page = ours ? listed : -1;  // (-1 reads as zero)
+        if (lane == 0) {
+          mbar_expect_tx(full, pages * rows * D);
+          (values ? ctl.issued_v : ctl.issued_k) = xt + 1;
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int n = n0 + k * kPer + r0;
-          const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t top = max(m & 0xffffu, m >> 16);
-          const bool bad = top >= 0x7f80u;
-          const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
-          const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
-            hi[i] = pack_e4m3x2(f0, f1);
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
-            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
-            lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
-            if (bad) hi[i] = lo[i] = 0;
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = half * NP + n;
-            const uint32_t* y = half ? lo : hi;
-            const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
-            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + row * D + (chunk << 4) + (part & 1) * 8),
-                         "r"(y[0] | y[1] << 16), "r"(y[2] | y[3] << 16)
+        __syncwarp();
+        if (lane < pages)
+          tma_load_4d_policy(tile0 + xst * C::kTileBytes + lane * rows * D, tm, 0, (xkt << 7) & (P - 1), x.hk, page, full,
+                             once);
+        if (!values) {
+          const int at = __shfl_sync(0xffffffffu, page, (4 * lane) >> shift), key = (xkt << 7) + 4 * lane;
+          const int to = xt % kCodeStages;
+          if (key < x.seq.Lk && at >= 0)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(ctl.codes[to] + 8 * lane)),
+                         "l"(a.codes + 2 * weight_offset(s, at, x.hk, key & (P - 1)))
                          : "memory");
-          }
-          if (part == 0) ctl.qmul[qb][n] = bad ? NAN : n < live ? sl2 * __uint_as_float(code << 23) : 0.f;
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.c_full[to])) : "memory");
         }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(ctl.q_full[qb]));
+      ++xt;
+      if (++xst == stages) {
+        xst = 0;
+        xphase ^= 1;
+      }
+      if (++xkt == x.end) {
+        x.next();
+        xkt = x.kt;
+      }
+      if (!x.done()) listed = look_up();
+    };
+    if (!values) {
+      while (!x.done()) copy();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // Q of a piece is split while the one before it runs, once the buffer's last piece is sure to be over (or, in a short
+      // piece, behind its last copy).
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
+      constexpr int kBatch = NP / kPer < 8 ? NP / kPer : 8;
+      const int r0 = lane / kLanes, part = lane % kLanes;
+      const float sl2 = a.scale * kLog2e;
+      F8Pieces y = w;
+      int piece = 0;
+      auto split_q = [&]() {  // of piece y
+        const int qb = piece & 1, live = y.tokens() * G;
+        if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+        run = __all_sync(0xffffffffu, run) && !*abort_flag;
+        if (!run) return;
+        const uint32_t to = sQ + qb * C::kQBytes;
+        for (int n0 = 0; n0 < NP; n0 += kBatch * kPer) {
+          uint4 e[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int n = n0 + k * kPer + r0, i = n / G;
+            e[k] = n < live ? *reinterpret_cast<const uint4*>(
+                                  reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                  elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token() + i, y.hk * G + n - i * G) + part * 8)
+                            : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int n = n0 + k * kPer + r0;
+            const uint32_t v[4] = {e[k].x, e[k].y, e[k].z, e[k].w};
+            uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const uint32_t top = max(m & 0xffffu, m >> 16);
+            const bool bad = top >= 0x7f80u;
+            const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
+            const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
+              hi[i] = pack_e4m3x2(f0, f1);
+              uint32_t h;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
+              const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+              lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
+              if (bad) hi[i] = lo[i] = 0;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int row = half * NP + n;
+              const uint32_t* z = half ? lo : hi;
+              const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
+              asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + row * D + (chunk << 4) + (part & 1) * 8),
+                           "r"(z[0] | z[1] << 16), "r"(z[2] | z[3] << 16)
+                           : "memory");
+            }
+            if (part == 0) ctl.qmul[qb][n] = bad ? NAN : n < live ? sl2 * __uint_as_float(code << 23) : 0.f;
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(ctl.q_full[qb]));
+        ++piece;
+        y.next();
+      };
+      int copied = 0;  // tiles of the piece
+      bool pending = true;
+      while (!x.done()) {
+        copy();
+        ++copied;
+        if (xt == 1) split_q();
+        const bool ended = x.done() || xkt == x.kt;
+        if (pending && !y.done() && (ended || copied == C::kVStages + 2)) {
+          split_q();
+          pending = false;
+        }
+        if (ended) {
+          copied = 0;
+          pending = true;
+        }
+      }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      bool run = true;
-      F8Pieces v = w;  // the piece of the next S
-      int left = v.end - v.kt, ks = 0, vpiece = 0;  // its key tiles without S; ring position
-      uint32_t kphase = 0, sb = 0;
-      bool opens = true;
+  } else if (warp == 1 || warp == kLast - 1) {
+    // ------------------------------------------------------------------ MMAs: S; P V
+    const bool scores = warp == 1;
+    bool run = true;
+    int t = 0, st = 0;
+    uint32_t phase = 0;
+    if (scores) {
       const uint64_t dk0 = D == 128 ? desc_kmajor_sw128(sK0) : desc_kmajor_sw64(sK0);
       const uint64_t dq0 = D == 128 ? desc_kmajor_sw128(sQ) : desc_kmajor_sw64(sQ);
+      for (int piece = 0; !w.done(); ++piece, w.next()) {
+        const int qb = piece & 1;
+        if (run) run = mbar_wait_spin(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
+        for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+          // With P V of tile t - 2 done, its scores are read and its P's buffer is free for tile t.
+          if (run && t >= 2)
+            run = mbar_wait_spin(bar(ctl.v_empty[(t - 2) % C::kVStages]), ((t - 2) / C::kVStages) & 1, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.k_full[st]), phase, abort_flag, a.status);
+          run = __all_sync(0xffffffffu, run);
+          fence_after_sync();
+          if (run && lane == 0) {
+            const uint64_t dk = desc_add(dk0, st * C::kTileBytes), dq = desc_add(dq0, qb * C::kQBytes);
+            const uint32_t to = tmem + (t & 1) * 2 * NP;
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_ss_f8(to, desc_add(dk, kk * 32), desc_add(dq, kk * 32), C::kIdS, kk > 0);
+            mma_commit(bar(ctl.s_full[t & 1]));
+            mma_commit(bar(ctl.k_empty[st]));
+            if (kt + 1 == w.end) mma_commit(bar(ctl.q_empty[qb]));
+          }
+          __syncwarp();
+          if (++st == C::kKStages) {
+            st = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    } else {
       const uint64_t dv0 = D == 128 ? desc_mnmajor_sw128(sV0, 16384) : desc_mnmajor_sw64(sV0, C::kTileBytes);
       const uint64_t dp0 = desc_mnmajor_sw128(sP, 16384);
-      auto issue_s = [&]() {
-        const int qb = vpiece & 1;
-        if (run && opens) run = mbar_wait_spin(bar(ctl.q_full[qb]), (vpiece >> 1) & 1, abort_flag, a.status);
-        if (run) run = mbar_wait_spin(bar(ctl.k_full[ks]), kphase, abort_flag, a.status);
-        fence_after_sync();
-        if (run) {
-          const uint64_t dk = desc_add(dk0, ks * C::kTileBytes), dq = desc_add(dq0, qb * C::kQBytes);
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_ss_f8(tmem + sb * 2 * NP, desc_add(dk, kk * 32), desc_add(dq, kk * 32), C::kIdS, kk > 0);
-          mma_commit(bar(ctl.s_full[sb]));
-          mma_commit(bar(ctl.k_empty[ks]));
-          if (left == 1) mma_commit(bar(ctl.q_empty[qb]));
-        }
-        sb ^= 1;
-        if (++ks == C::kKStages) {
-          ks = 0;
-          kphase ^= 1;
-        }
-        opens = --left == 0;
-        if (opens) {
-          v.next();
-          left = v.end - v.kt;
-          ++vpiece;
-        }
-      };
-      if (!w.done()) issue_s();
-      int vs = 0;
-      uint32_t vphase = 0, pb = 0, pphase = 0;
-      for (int piece = 0; !w.done(); ++piece) {
+      for (int piece = 0; !w.done(); ++piece, w.next()) {
         const int ob = C::kOBufs == 2 ? piece & 1 : 0, uses = C::kOBufs == 2 ? piece >> 1 : piece;
         const uint32_t tO = tmem + C::kO + ob * 3 * NP;
-        for (int kt = w.kt; kt < w.end; ++kt) {
-          if (!v.done()) issue_s();
-          if (run) run = mbar_wait_spin(bar(ctl.p_ready[pb]), pphase, abort_flag, a.status);
-          if (run) run = mbar_wait_spin(bar(ctl.v_full[vs]), vphase, abort_flag, a.status);
+        for (int kt = w.kt; kt < w.end; ++kt, ++t) {
           if (run && kt == w.kt && uses > 0)
             run = mbar_wait_spin(bar(ctl.o_free[ob]), (uses - 1) & 1, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.v_full[st]), phase, abort_flag, a.status);
+          if (run) run = mbar_wait_spin(bar(ctl.p_ready[t & 1]), (t >> 1) & 1, abort_flag, a.status);
+          run = __all_sync(0xffffffffu, run);
           fence_after_sync();
-          if (run) {
-            const uint64_t dv = desc_add(dv0, vs * C::kTileBytes), dp = desc_add(dp0, pb * C::kPStep);
+          if (run && lane == 0) {
+            const uint64_t dv = desc_add(dv0, st * C::kTileBytes), dp = desc_add(dp0, (t & 1) * C::kPStep);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ss_f8(tO, desc_add(dv, kk * 32 * D), desc_add(dp, kk * 4096), C::kIdPV, kk > 0 || kt > w.kt);
-            mma_commit(bar(ctl.v_empty[vs]));
-            mma_commit(bar(ctl.pv_done[pb]));
+            mma_commit(bar(ctl.v_empty[st]));
           }
-          pphase ^= pb;
-          pb ^= 1;
-          if (++vs == C::kVStages) {
-            vs = 0;
-            vphase ^= 1;
+          __syncwarp();
+          if (++st == C::kVStages) {
+            st = 0;
+            phase ^= 1;
           }
         }
-        w.next();
       }
-      mma_commit(bar(ctl.drain));
-      mbar_wait_drain(bar(ctl.drain), 0);
+    }
+    if (lane == 0) {
+      mma_commit(bar(ctl.drain[scores ? 0 : 1]));
+      mbar_wait_drain(bar(ctl.drain[scores ? 0 : 1]), 0);
     }
   } else {
     // ------------------------------------------------------------------ softmax, epilogue
@@ -442,7 +494,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     int t = 0, vs = 0;
     uint32_t vphase = 0;
     auto wait_pv = [&](int j) -> bool {  // P V of tile j has completed
-      return mbar_wait(bar(ctl.pv_done[j & 1]), (j >> 1) & 1, abort_flag, a.status);
+      return mbar_wait(bar(ctl.v_empty[j % C::kVStages]), (j / C::kVStages) & 1, abort_flag, a.status);
     };
     for (int piece = 0; !w.done(); ++piece) {
       const SeqInfo& seq = w.seq;
@@ -455,8 +507,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll
       for (int n = 0; n < NC; ++n) l[n] = 0.f;
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
-        if (run) run = mbar_wait(bar(ctl.c_full[vs]), vphase, abort_flag, a.status);
-        const uint32_t code = *reinterpret_cast<const uint16_t*>(ctl.codes[vs] + 2 * r), kc = code & 255u, vc = code >> 8;
+        const int cs = t % kCodeStages;
+        if (run) run = mbar_wait(bar(ctl.c_full[cs]), (t / kCodeStages) & 1, abort_flag, a.status);
+        const uint32_t code = *reinterpret_cast<const uint16_t*>(ctl.codes[cs] + 2 * r), kc = code & 255u, vc = code >> 8;
         const float kmul = kc == 255u ? NAN : __uint_as_float(kc << 23);
         const float vexp = vc == 255u ? NAN : vc == 0u ? (float)kZeroRow : (float)((int)vc - 127);
         const float back = __uint_as_float((vc == 0u ? (uint32_t)(127 - kZeroRow) : 254u - min(vc, 253u)) << 23);  // 2^-vexp
@@ -548,8 +601,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           mid[n / 4] = __byte_perm(ma, mb, 0x7531);
           lo[n / 4] = la | lb << 16;
         }
-        // P's buffer is free: the P V that read it, of tile t - 2, was issued before S of tile t, which has
-        // completed.
+        // P's buffer is free: S of tile t, which has completed, was issued when the P V that read it had.
         const uint32_t sPt = sP + (NP == 16 ? 0 : (t & 1) * C::kPStep) + r * 128;
         auto put = [&](int c, const uint32_t (&x)[NC / 4]) {  // c: 16-byte chunk of the row's 3 NP bytes
           store16(sPt + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
@@ -583,7 +635,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       ctl.wmax[quad][n0 + (lane >> 1)] = l[0];
       named_bar_sync(on, 128);
       const bool whole = w.whole() && ctas == 1;
-      const int slot = 2 * blockIdx.x + (piece == 0 ? 0 : 1);
+      const int slot = 2 * me + (piece == 0 ? 0 : 1);
       if (r < NC) {
         const int n = n0 + r;
         const float sum = (ctl.wmax[0][n] + ctl.wmax[1][n]) + (ctl.wmax[2][n] + ctl.wmax[3][n]);
@@ -701,6 +753,13 @@ int unit_tokens(const PagedShape& s) {
 }
 int unit_rows(const PagedShape& s) { return padded_rows(unit_tokens(s) * (s.H / s.Hkv)); }
 
+// Heads side by side: the most that leave no more than 3% of the CTAs without work.
+F8Cut cut_of(const PagedShape& s, int ctas) {
+  int side = s.Hkv;
+  while (side > 1 && (s.Hkv % side != 0 || ctas / side * side * 100ll < 97ll * ctas)) --side;
+  return {unit_tokens(s), side, s.Hkv / side};
+}
+
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0; the rule of fa_paged_decode.cu.
 int unit_ctas(const PagedShape& s, int num_sms) {
   if (unit_tokens(s) < s.Nq) return 0;
@@ -723,14 +782,20 @@ cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
   using C = F8Cfg<D, NP>;
   const PagedShape& s = a.s;
   const int P = 1 << s.page_shift, box = P < 128 ? P : 128;
+  // A miss fetches 128 bytes, at d = 64 two heads' rows (64, 128 and 256: within 1% while neighbours walk together; 147, - and 190 us
+  // of 64 x 8192 keys before they did).
+  constexpr int kL2 = 128;
   CUtensorMap tk, tv;
-  if (!fa_make_tmap_u8(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, D, box, D) ||
-      !fa_make_tmap_u8(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, D, box, D))
+  if (!fa_make_tmap_u8(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, D, box, kL2) ||
+      !fa_make_tmap_u8(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, D, box, kL2))
     return cudaErrorInvalidValue;
-  const int shared = unit_ctas(s, a.num_sms), ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
+  const int shared = unit_ctas(s, a.num_sms);
+  int ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
   F8Work wk{};
-  wk.tpu = unit_tokens(s);
+  wk.cut = {unit_tokens(s), 1, s.Hkv};
   if (shared == 0) {
+    wk.cut = cut_of(s, ctas);
+    ctas = ctas / wk.cut.side * wk.cut.side;
     char* ws = static_cast<char*>(a.workspace);
     wk.desc = reinterpret_cast<int4*>(ws);
     ws += up256((size_t)ctas * 2 * sizeof(int4));
