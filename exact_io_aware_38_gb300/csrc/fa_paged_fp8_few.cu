@@ -72,7 +72,9 @@ struct F8Cfg {
 // which follows P V of two tiles before that, so the codes of t - 16 are read.
 constexpr int kCodeStages = 16;
 
-constexpr int kF8Open = 1;  // positions of a unit before its first tile, for its epilogue
+// Positions of a unit before its first tile, for its epilogue and the first tile of the next (weighed as 1 and 3: 64 x 8192 keys 128.4 and 126.5 us,
+// 16 x 2048 keys of 32 heads 48.1 and 46.8, 48 x 1024 of 12 heads at d = 64 37.2 and 36.8).
+constexpr int kF8Open = 3;
 
 // How the work is cut. The K/V heads of a sequence are `turns` turns of `side` neighbours each: CTA c takes head c % side of every
 // turn, and the line of units that the CTAs of one residue divide has a turn where it would have a head. So `side` CTAs walk
@@ -97,8 +99,7 @@ struct F8Units {
 template <int D, int NP>
 struct F8Ctl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // (v_empty: also that P V has completed)
-  uint64_t c_full[kCodeStages];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // (k_full: codes too; v_empty: also that P V has completed)
   uint64_t s_full[2];
   uint64_t p_ready[2];  // per buffer of P
   uint64_t o_free[2];
@@ -175,6 +176,7 @@ struct F8Work {
   int4* desc;       // [CTAs][2]: {b, hk, first CTA, its slot}, {rows, q0, bb, first token} of the unit; b = -1: none ends
                     // here in pieces. Null: every unit has a CTA or a cluster of its own
   F8Cut cut;
+  FastDiv by_group;  // rows to tokens
 };
 
 // Two probabilities' parts: hi and mid by cutting their fp16 after two fraction bits (a byte), lo by rounding the rest.
@@ -217,18 +219,17 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(ctl.q_full[i]), 32);
       mbar_init(bar(ctl.q_empty[i]), 1 + 4 * C::kGroups);
-      mbar_init(bar(ctl.s_full[i]), 1);
-      mbar_init(bar(ctl.o_free[i]), 128 * C::kGroups);
-      mbar_init(bar(ctl.p_ready[i]), 128 * C::kGroups);
+      mbar_init(bar(ctl.s_full[i]), 2);
+      mbar_init(bar(ctl.o_free[i]), 4 * C::kGroups);
+      mbar_init(bar(ctl.p_ready[i]), 4 * C::kGroups);
       mbar_init(bar(ctl.drain[i]), 1);
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(bar(ctl.k_full[i]), 1);
+      mbar_init(bar(ctl.k_full[i]), 1 + 32);
       mbar_init(bar(ctl.k_empty[i]), 1);
       mbar_init(bar(ctl.v_full[i]), 1);
       mbar_init(bar(ctl.v_empty[i]), 1);
     }
-    for (int i = 0; i < kCodeStages; ++i) mbar_init(bar(ctl.c_full[i]), 32);
     fence_mbar_init();
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(ctl.codes[to] + 8 * lane)),
                          "l"(a.codes + 2 * weight_offset(s, at, x.hk, key & (P - 1)))
                          : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.c_full[to])) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
         }
       }
       ++xt;
@@ -335,84 +336,88 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       // Q of a piece is split while the one before it runs, once the buffer's last piece is sure to be over (or, in a short
-      // piece, behind its last copy).
+      // piece, behind its last copy): a few rows behind each copy, loaded one step before they are split.
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-      constexpr int kBatch = NP / kPer < 8 ? NP / kPer : 8;
+      constexpr int kBatch = 2;  // (loads of a lane: more, unrolled, is code that runs once and waits for its instructions)
       const int r0 = lane / kLanes, part = lane % kLanes;
       const float sl2 = a.scale * kLog2e;
       F8Pieces y = w;
-      int piece = 0;
-      auto split_q = [&]() {  // of piece y
-        const int qb = piece & 1, live = y.tokens() * G;
-        if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
-        run = __all_sync(0xffffffffu, run) && !*abort_flag;
-        if (!run) return;
-        const uint32_t to = sQ + qb * C::kQBytes;
-        for (int n0 = 0; n0 < NP; n0 += kBatch * kPer) {
-          uint4 e[kBatch];
+      int piece = 0, at = 0;  // of y; the first row of the batch
+      uint4 e[kBatch];
+      auto load_q = [&]() {
+        const int live = y.tokens() * G;
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                 elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.hk * G) + part * 8;
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int n = n0 + k * kPer + r0, i = n / G;
-            e[k] = n < live ? *reinterpret_cast<const uint4*>(
-                                  reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                  elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token() + i, y.hk * G + n - i * G) + part * 8)
-                            : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int n = n0 + k * kPer + r0;
-            const uint32_t v[4] = {e[k].x, e[k].y, e[k].z, e[k].w};
-            uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const uint32_t top = max(m & 0xffffu, m >> 16);
-            const bool bad = top >= 0x7f80u;
-            const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
-            const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
-              hi[i] = pack_e4m3x2(f0, f1);
-              uint32_t h;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
-              const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
-              lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
-              if (bad) hi[i] = lo[i] = 0;
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int row = half * NP + n;
-              const uint32_t* z = half ? lo : hi;
-              const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
-              asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + row * D + (chunk << 4) + (part & 1) * 8),
-                           "r"(z[0] | z[1] << 16), "r"(z[2] | z[3] << 16)
-                           : "memory");
-            }
-            if (part == 0) ctl.qmul[qb][n] = bad ? NAN : n < live ? sl2 * __uint_as_float(code << 23) : 0.f;
-          }
+        for (int k = 0; k < kBatch; ++k) {
+          const int n = at + k * kPer + r0, i = wk.by_group.div(n);
+          e[k] = n < live ? *reinterpret_cast<const uint4*>(q + (size_t)i * a.sq.row + (size_t)(n - i * G) * a.sq.head)
+                          : make_uint4(0, 0, 0, 0);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(ctl.q_full[qb]));
-        ++piece;
-        y.next();
       };
-      int copied = 0;  // tiles of the piece
-      bool pending = true;
-      while (!x.done()) {
+      auto split_q = [&]() {  // the batch, and the next one's loads
+        const int qb = piece & 1, live = y.tokens() * G;
+        if (run && at == 0 && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+        run = __all_sync(0xffffffffu, run) && !*abort_flag;
+        const uint32_t to = sQ + qb * C::kQBytes;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int n = at + k * kPer + r0;
+          const uint32_t v[4] = {e[k].x, e[k].y, e[k].z, e[k].w};
+          uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t top = max(m & 0xffffu, m >> 16);
+          const bool bad = top >= 0x7f80u;
+          const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
+          const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
+            hi[i] = pack_e4m3x2(f0, f1);
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
+            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+            lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
+            if (bad) hi[i] = lo[i] = 0;
+          }
+          if (!run) continue;  // (the buffer may still be in use)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int row = half * NP + n;
+            const uint32_t* z = half ? lo : hi;
+            const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + row * D + (chunk << 4) + (part & 1) * 8),
+                         "r"(z[0] | z[1] << 16), "r"(z[2] | z[3] << 16)
+                         : "memory");
+          }
+          if (part == 0) ctl.qmul[qb][n] = bad ? NAN : n < live ? sl2 * __uint_as_float(code << 23) : 0.f;
+        }
+        at += kBatch * kPer;
+        if (at >= NP) {
+          fence_proxy_async_smem();
+          if (run) mbar_arrive(bar(ctl.q_full[qb]));
+          at = 0;
+          ++piece;
+          y.next();
+        }
+        if (!y.done()) load_q();
+      };
+      if (!y.done()) load_q();
+      for (int of = 0, copied = 0; !x.done();) {  // the piece of the copies, its tiles so far
         copy();
         ++copied;
-        if (xt == 1) split_q();
         const bool ended = x.done() || xkt == x.kt;
-        if (pending && !y.done() && (ended || copied == C::kVStages + 2)) {
-          split_q();
-          pending = false;
-        }
+        const int due = ended ? of + 1 : of;  // pieces whose Q has to be there now
+        int more = copied > C::kVStages ? NP / 16 : 0;
+#pragma unroll 1
+        while (!y.done() && (piece <= due || (piece == of + 1 && more-- > 0))) split_q();
         if (ended) {
+          ++of;
           copied = 0;
-          pending = true;
         }
       }
     }
@@ -436,6 +441,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           run = __all_sync(0xffffffffu, run);
           fence_after_sync();
           if (run && lane == 0) {
+            mbar_arrive(bar(ctl.s_full[t & 1]));  // (the codes are there: what this thread has seen, the softmax will)
             const uint64_t dk = desc_add(dk0, st * C::kTileBytes), dq = desc_add(dq0, qb * C::kQBytes);
             const uint32_t to = tmem + (t & 1) * 2 * NP;
 #pragma unroll
@@ -501,36 +507,40 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       const int live = w.tokens() * G, tok = w.token(), qb = piece & 1;
       const uint32_t tO = tmem + lane_off + C::kO + (C::kOBufs == 2 ? piece & 1 : 0) * 3 * NP + n0;
       if (run) run = mbar_wait(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
-      if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, tok + (n0 + r) / G + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
+      if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, tok + wk.by_group.div(n0 + r) + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
       const int least = s.causal ? min(seq.Lk, tok + seq.off + 1) : seq.Lk;
       float l[NC];
 #pragma unroll
       for (int n = 0; n < NC; ++n) l[n] = 0.f;
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
-        const int cs = t % kCodeStages;
-        if (run) run = mbar_wait(bar(ctl.c_full[cs]), (t / kCodeStages) & 1, abort_flag, a.status);
-        const uint32_t code = *reinterpret_cast<const uint16_t*>(ctl.codes[cs] + 2 * r), kc = code & 255u, vc = code >> 8;
+        if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
+        fence_after_sync();
+        uint32_t shi[NC], slo[NC];
+        tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + n0, shi);
+        tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + NP + n0, slo);
+        const uint32_t code = *reinterpret_cast<const uint16_t*>(ctl.codes[t % kCodeStages] + 2 * r);
+        const uint32_t kc = code & 255u, vc = code >> 8;
         const float kmul = kc == 255u ? NAN : __uint_as_float(kc << 23);
         const float vexp = vc == 255u ? NAN : vc == 0u ? (float)kZeroRow : (float)((int)vc - 127);
         const float back = __uint_as_float((vc == 0u ? (uint32_t)(127 - kZeroRow) : 254u - min(vc, 253u)) << 23);  // 2^-vexp
-        if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
-        fence_after_sync();
-        float y[NC];
+        tmem_ld_wait();
+        float y[NC];  // the exponents of P, and (below) their distance from the reference
         {
-          uint32_t hi[NC], lo[NC];
-          tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + n0, hi);
-          tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + NP + n0, lo);
-          tmem_ld_wait();
           const float2 part = make_float2(1.f / kLoScale, 1.f / kLoScale), km = make_float2(kmul, kmul);
           const float2 ve = make_float2(vexp, vexp);
 #pragma unroll
-          for (int n = 0; n < NC; n += 2) {
-            const float2 q = *reinterpret_cast<const float2*>(ctl.qmul[qb] + n0 + n);
-            const float2 x = fma2(make_float2(__uint_as_float(lo[n]), __uint_as_float(lo[n + 1])), part,
-                                  make_float2(__uint_as_float(hi[n]), __uint_as_float(hi[n + 1])));
-            const float2 z = fma2(x, mul2(km, q), ve);
-            y[n] = z.x;
-            y[n + 1] = z.y;
+          for (int n = 0; n < NC; n += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(ctl.qmul[qb] + n0 + n);
+            const float2 x0 = fma2(make_float2(__uint_as_float(slo[n]), __uint_as_float(slo[n + 1])), part,
+                                   make_float2(__uint_as_float(shi[n]), __uint_as_float(shi[n + 1])));
+            const float2 x1 = fma2(make_float2(__uint_as_float(slo[n + 2]), __uint_as_float(slo[n + 3])), part,
+                                   make_float2(__uint_as_float(shi[n + 2]), __uint_as_float(shi[n + 3])));
+            const float2 z0 = fma2(x0, mul2(km, make_float2(q.x, q.y)), ve);
+            const float2 z1 = fma2(x1, mul2(km, make_float2(q.z, q.w)), ve);
+            y[n] = z0.x;
+            y[n + 1] = z0.y;
+            y[n + 2] = z1.x;
+            y[n + 3] = z1.y;
           }
         }
         const int key = (kt << 7) + r;
@@ -540,15 +550,24 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll
           for (int n = 0; n < NC; ++n) y[n] = key < ctl.lim[n0 + n] ? y[n] : -INFINITY;
         }
-        bool raise = opens;
-        if (!opens) {
-          bool big = false;
+        auto from_ref = [&](const float (&x)[NC], float (&d)[NC]) {
 #pragma unroll
           for (int n = 0; n < NC; n += 4) {
             const float4 m = *reinterpret_cast<const float4*>(ctl.ref + n0 + n);
-            big |= fmaxf(fmax3(y[n] - m.x, y[n + 1] - m.y, y[n + 2] - m.z), y[n + 3] - m.w) > kRaise8;
+            d[n] = x[n] - m.x;
+            d[n + 1] = x[n + 1] - m.y;
+            d[n + 2] = x[n + 2] - m.z;
+            d[n + 3] = x[n + 3] - m.w;
           }
-          raise = vote_any(big, on);
+        };
+        bool raise = opens;
+        float d[NC];
+        if (!opens) {
+          from_ref(y, d);
+          float big = d[0];
+#pragma unroll
+          for (int n = 1; n < NC - 1; n += 2) big = fmax3(big, d[n], d[n + 1]);
+          raise = vote_any(fmaxf(big, d[NC - 1]) > kRaise8, on);
         }
         if (raise) {
           float z[NC];
@@ -583,17 +602,18 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll
             for (int i = 0; i < NC; ++i) l[i] *= ctl.alpha[n0 + i];
           }
+          from_ref(y, d);
         }
         uint32_t hi[NC / 4], mid[NC / 4], lo[NC / 4];
 #pragma unroll
         for (int n = 0; n < NC; n += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(ctl.ref + n0 + n);
-          const float p0 = ex2_approx(y[n] - m.x), p1 = ex2_approx(y[n + 1] - m.y);
-          const float p2 = ex2_approx(y[n + 2] - m.z), p3 = ex2_approx(y[n + 3] - m.w);
-          l[n] = fmaf(p0, back, l[n]);
-          l[n + 1] = fmaf(p1, back, l[n + 1]);
-          l[n + 2] = fmaf(p2, back, l[n + 2]);
-          l[n + 3] = fmaf(p3, back, l[n + 3]);
+          const float p0 = ex2_approx(d[n]), p1 = ex2_approx(d[n + 1]), p2 = ex2_approx(d[n + 2]), p3 = ex2_approx(d[n + 3]);
+          const float2 l0 = fma2(make_float2(p0, p1), make_float2(back, back), make_float2(l[n], l[n + 1]));
+          const float2 l1 = fma2(make_float2(p2, p3), make_float2(back, back), make_float2(l[n + 2], l[n + 3]));
+          l[n] = l0.x;
+          l[n + 1] = l0.y;
+          l[n + 2] = l1.x;
+          l[n + 3] = l1.y;
           uint32_t ha, hb, ma, mb, la, lb;
           split_p(p0, p1, ha, ma, la);
           split_p(p2, p3, hb, mb, lb);
@@ -622,7 +642,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         }
         fence_proxy_async_smem();
         fence_before_sync();
-        if (run) mbar_arrive(bar(ctl.p_ready[t & 1]));
+        __syncwarp();
+        if (run && lane == 0) mbar_arrive(bar(ctl.p_ready[t & 1]));
         if (++vs == C::kVStages) {
           vs = 0;
           vphase ^= 1;
@@ -642,7 +663,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         ctl.alpha[n] = sum == 0.f ? 0.f : 1.f / sum;  // (0: no visible key; a NaN stays one)
         const float lse2 = sum == 0.f ? -INFINITY : ctl.ref[n] + log2f(sum);
         if (whole) {
-          if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n % G, tok + n / G)] = lse2 * kLn2;
+          const int i = wk.by_group.div(n);
+          if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n - i * G, tok + i)] = lse2 * kLn2;
         } else {
           (ctas > 1 ? ctl.part_lse : wk.part_lse + (size_t)slot * NP)[n] = lse2;
         }
@@ -654,7 +676,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + tok, w.hk * G) + r;
       // (the cluster's parts lie over the ring: with the last P V done nothing reads it or is on its way there)
       float* part = (ctas > 1 ? my_part : wk.part_o + (size_t)slot * NP * D) + r;
-      int i = n0 / G, g = n0 % G;  // token and head of the group of column n
+      int i = wk.by_group.div(n0), g = n0 - i * G;  // token and head of the group of column n
       float o[NC];
       {
         uint32_t x[NC], z[NC];
@@ -683,7 +705,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         }
       }
       fence_before_sync();
-      if (run) mbar_arrive(bar(ctl.o_free[C::kOBufs == 2 ? piece & 1 : 0]));
+      __syncwarp();
+      if (run && lane == 0) mbar_arrive(bar(ctl.o_free[C::kOBufs == 2 ? piece & 1 : 0]));
       w.next();
     }
   }
@@ -793,6 +816,7 @@ cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
   int ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
   F8Work wk{};
   wk.cut = {unit_tokens(s), 1, s.Hkv};
+  wk.by_group = fast_div(s.H / s.Hkv);
   if (shared == 0) {
     wk.cut = cut_of(s, ctas);
     ctas = ctas / wk.cut.side * wk.cut.side;
