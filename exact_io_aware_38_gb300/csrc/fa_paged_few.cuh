@@ -10,20 +10,22 @@ constexpr float kNoMax = -3.0e38f;  // reference max of a row that has seen no k
 
 inline int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// Reduce v[0 .. 16) over the 32 lanes; afterwards lane l holds column l / 2 in v[0]. A halving exchange: 16
-// shuffles instead of 80.
-template <typename F>
-__device__ __forceinline__ void columns_reduce(float (&v)[16], int lane, F f) {
+// Reduce the N columns v over the 32 lanes; afterwards lane l holds column l N / 32 in v[0]. A halving exchange: 16
+// shuffles for 16 columns instead of 80.
+template <int N, typename F>
+__device__ __forceinline__ void columns_reduce(float (&v)[N], int lane, F f) {
+  constexpr int kLanes = 32 / N;  // of a column in the end
 #pragma unroll
-  for (int half = 8; half > 0; half >>= 1) {
-    const bool up = lane & (2 * half);
+  for (int half = N / 2; half > 0; half >>= 1) {
+    const bool up = lane & (kLanes * half);
 #pragma unroll
     for (int i = 0; i < half; ++i) {
       const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
-      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, 2 * half));
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, kLanes * half));
     }
   }
-  v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
 }
 
 __device__ __forceinline__ bool vote_any(bool x, int id) {

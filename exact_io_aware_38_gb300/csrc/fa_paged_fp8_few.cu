@@ -43,29 +43,33 @@ constexpr float kRaise8 = 15.f;  // and that a score may exceed it by: 2^15 is n
 constexpr float kLoScale = 32.f;
 constexpr int kZeroRow = -80;    // exponent that stands for a value row of zeros: only its place in the row sum counts
 
-constexpr int few8_ctas(int np) { return np == 16 ? 2 : 1; }  // per SM
+constexpr int few8_ctas(int np) { return np <= 16 ? 2 : 1; }  // per SM
 
 template <int D, int NP>
 struct F8Cfg {
   static constexpr int kTileBytes = 128 * D;
   static constexpr int kCtas = few8_ctas(NP);
-  static constexpr int kGroups = NP / 16, kThreads = 128 + 128 * kGroups;
-  static constexpr int kKStages = NP == 16 ? (D == 128 ? 3 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;
-  static constexpr int kVStages = NP == 16 ? (D == 128 ? 2 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 3 : 6;
+  static constexpr int kCols = NP < 16 ? NP : 16, kGroups = NP / kCols;  // rows of a group of four softmax warps; groups
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kKStages = NP <= 16 ? (D == 128 ? 3 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;
+  static constexpr int kVStages = NP <= 16 ? (D == 128 ? 2 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 3 : 6;
   static constexpr int kQBytes = 2 * NP * D, kQBufs = 2;
-  // P: 128 keys, a row of 3 NP bytes each, cut into blocks of 128. Two buffers: at 16 rows side by side in a row, else
+  // Columns of P V: three parts of every row (at 8 rows a fourth, unused, since N is a multiple of 16).
+  static constexpr int kParts = NP == 8 ? 32 : 3 * NP;
+  // P: 128 keys, a row of kParts bytes each, cut into blocks of 128. Two buffers: up to 16 rows side by side in a row, else
   // one behind the other.
-  static constexpr int kPBlocks = (3 * NP + 127) / 128;
-  static constexpr int kPStep = NP == 16 ? 64 : kPBlocks * 16384;
-  static constexpr int kPBytes = NP == 16 ? 16384 : 2 * kPStep;
+  static constexpr int kPBlocks = (kParts + 127) / 128;
+  static constexpr int kPStep = NP <= 16 ? 64 : kPBlocks * 16384;
+  static constexpr int kPBytes = NP <= 16 ? 16384 : 2 * kPStep;
   static constexpr int kSmem = kQBufs * kQBytes + (kKStages + kVStages) * kTileBytes + kPBytes + 1024;
+  static constexpr bool kSoftSplit = NP > 16;  // the softmax warps split Q
   static constexpr int kOBufs = NP == 64 ? 1 : 2;
   static constexpr uint32_t kO = 4 * NP;  // tensor memory: S x 2, then O
-  static constexpr uint32_t kTmemCols = NP == 16 ? 256 : 512;
-  static_assert(kO + kOBufs * 3 * NP <= kTmemCols);
+  static constexpr uint32_t kTmemCols = NP == 8 ? 128 : NP == 16 ? 256 : 512;
+  static_assert(kO + kOBufs * kParts <= kTmemCols);
   static constexpr uint32_t kIdS = idesc_e4m3(128, 2 * NP);
   // O^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared memory and are never read.
-  static constexpr uint32_t kIdPV = idesc_e4m3_e5m2_mn(128, 3 * NP);
+  static constexpr uint32_t kIdPV = idesc_e4m3_e5m2_mn(128, kParts);
 };
 
 // Codes wait in a ring of their own, longer than the keys' (whose copies they go with): a copy of keys t follows S of t - kKStages,
@@ -98,7 +102,7 @@ struct F8Units {
 
 template <int D, int NP>
 struct F8Ctl {
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_raw[2], q_full[2], q_empty[2];
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // (k_full: codes too; v_empty: also that P V has completed)
   uint64_t s_full[2];
   uint64_t p_ready[2];  // per buffer of P
@@ -148,6 +152,7 @@ struct F8Pieces {
   }
   __device__ bool done() const { return finished || n == 0; }
   __device__ bool whole() const { return kt == 0 && end == n; }
+  __device__ bool more() const { return todo > kF8Open; }  // another piece follows
   __device__ int token() const { return u * cut.tokens; }  // the unit's first
   __device__ int tokens() const { return min(cut.tokens, seq.Lq - u * cut.tokens); }
   __device__ void next() {
@@ -191,8 +196,67 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t& hi, uint32
   lo = y;
 }
 
+__device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&r)[16]) { tmem_ld16(at, r); }
+__device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld8(at, r); }
+__device__ __forceinline__ void store_cols(uint32_t at, const uint32_t (&r)[16]) { tmem_st16(at, r); }
+__device__ __forceinline__ void store_cols(uint32_t at, const uint32_t (&r)[8]) { tmem_st8(at, r); }
+
 __device__ __forceinline__ void store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Where 16 bytes of row n of Q lie as they arrive: the row's first half in hi's place, its second in lo's.
+template <int D, int NP>
+__device__ __forceinline__ uint32_t raw_q(uint32_t q, int n, int part) {
+  return q + (part / (D / 16) * NP + n) * D + part % (D / 16) * 16;
+}
+
+// Splits kTimes x 512 / D rows from `first` on in place, by a warp: D / 8 lanes a row. store: false where the buffer may still be
+// in use (after a wait that ran out).
+template <int D, int NP, int kTimes>
+__device__ __forceinline__ void split_rows(uint32_t q, float* qmul, int first, float sl2, bool store) {
+  constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+  const int lane = threadIdx.x & 31, r0 = lane / kLanes, part = lane % kLanes;
+#pragma unroll
+  for (int k = 0; k < kTimes; ++k) {
+    const int n = first + k * kPer + r0;
+    uint32_t v[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(raw_q<D, NP>(q, n, part))
+                 : "memory");
+    uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    const bool bad = top >= 0x7f80u;
+    const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
+    const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
+      hi[i] = pack_e4m3x2(f0, f1);
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
+      const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+      lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
+      if (bad) hi[i] = lo[i] = 0;
+    }
+    if (!store) continue;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // (the row's lanes have all read: they have exchanged their maxima)
+      const int row = half * NP + n;
+      const uint32_t* z = half ? lo : hi;
+      const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
+      asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(q + row * D + (chunk << 4) + (part & 1) * 8),
+                   "r"(z[0] | z[1] << 16), "r"(z[2] | z[3] << 16)
+                   : "memory");
+    }
+    if (part == 0) qmul[n] = bad ? NAN : sl2 * __uint_as_float(code << 23);
+  }
 }
 
 template <int D, int NP>
@@ -217,7 +281,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     ctl.abort_flag = 0;
     ctl.issued_k = ctl.issued_v = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(ctl.q_full[i]), 32);
+      mbar_init(bar(ctl.q_raw[i]), 32);
+      mbar_init(bar(ctl.q_full[i]), C::kSoftSplit ? 4 * C::kGroups : 1);
       mbar_init(bar(ctl.q_empty[i]), 1 + 4 * C::kGroups);
       mbar_init(bar(ctl.s_full[i]), 2);
       mbar_init(bar(ctl.o_free[i]), 4 * C::kGroups);
@@ -335,91 +400,65 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       while (!x.done()) copy();
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-      // Q of a piece is split while the one before it runs, once the buffer's last piece is sure to be over (or, in a short
-      // piece, behind its last copy): a few rows behind each copy, loaded one step before they are split.
+      // Q of a piece is asked for while the one before it runs, once the buffer's last piece is sure to be over (or, in a short
+      // piece, behind its last copy). Its rows arrive where their parts will lie, all at once, and up to 16 are split here, a few
+      // behind each copy, more by the softmax warps: 32 rows in this loop take 8000 cycles.
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-      constexpr int kBatch = 2;  // (loads of a lane: more, unrolled, is code that runs once and waits for its instructions)
       const int r0 = lane / kLanes, part = lane % kLanes;
-      const float sl2 = a.scale * kLog2e;
       F8Pieces y = w;
-      int piece = 0, at = 0;  // of y; the first row of the batch
-      uint4 e[kBatch];
-      auto load_q = [&]() {
-        const int live = y.tokens() * G;
-        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                 elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.hk * G) + part * 8;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int n = at + k * kPer + r0, i = wk.by_group.div(n);
-          e[k] = n < live ? *reinterpret_cast<const uint4*>(q + (size_t)i * a.sq.row + (size_t)(n - i * G) * a.sq.head)
-                          : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto split_q = [&]() {  // the batch, and the next one's loads
-        const int qb = piece & 1, live = y.tokens() * G;
-        if (run && at == 0 && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
-        run = __all_sync(0xffffffffu, run) && !*abort_flag;
+      int piece = 0, at = -1;  // of y; the next row, -1: none has been asked for
+      auto step_q = [&]() {
+        const int qb = piece & 1;
         const uint32_t to = sQ + qb * C::kQBytes;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int n = at + k * kPer + r0;
-          const uint32_t v[4] = {e[k].x, e[k].y, e[k].z, e[k].w};
-          uint32_t m = 0;  // magnitudes of two elements in each word: bf16 bits without the sign are ordered as integers
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t top = max(m & 0xffffu, m >> 16);
-          const bool bad = top >= 0x7f80u;
-          const uint32_t code = (top >> 7) > 8 ? (top >> 7) - 7 : 1;
-          const float by = bad ? 0.f : __uint_as_float((254 - code) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float f0 = __uint_as_float(v[i] << 16) * by, f1 = __uint_as_float(v[i] & 0xffff0000u) * by;
-            hi[i] = pack_e4m3x2(f0, f1);
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[i]));
-            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
-            lo[i] = pack_e4m3x2((f0 - g.x) * kLoScale, (f1 - g.y) * kLoScale);
-            if (bad) hi[i] = lo[i] = 0;
-          }
-          if (!run) continue;  // (the buffer may still be in use)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = half * NP + n;
-            const uint32_t* z = half ? lo : hi;
-            const uint32_t chunk = D == 128 ? ((part >> 1) ^ (row & 7)) : ((part >> 1) ^ ((row >> 1) & 3));
-            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + row * D + (chunk << 4) + (part & 1) * 8),
-                         "r"(z[0] | z[1] << 16), "r"(z[2] | z[3] << 16)
-                         : "memory");
-          }
-          if (part == 0) ctl.qmul[qb][n] = bad ? NAN : n < live ? sl2 * __uint_as_float(code << 23) : 0.f;
-        }
-        at += kBatch * kPer;
-        if (at >= NP) {
-          fence_proxy_async_smem();
-          if (run) mbar_arrive(bar(ctl.q_full[qb]));
+        if (at < 0) {
+          if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+          run = __all_sync(0xffffffffu, run) && !*abort_flag;
+          const int live = y.tokens() * G;
+          const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                   elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.hk * G) + part * 8;
+          if (run)
+#pragma unroll 2
+            for (int n = r0; n < NP; n += kPer) {  // (rows that do not exist become zeros)
+              const int i = n < live ? wk.by_group.div(n) : 0, g = n < live ? n - i * G : 0;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_q<D, NP>(to, n, part)),
+                           "l"(q + (size_t)i * a.sq.row + (size_t)g * a.sq.head), "r"(n < live ? 16 : 0)
+                           : "memory");
+            }
           at = 0;
-          ++piece;
-          y.next();
+          if constexpr (!C::kSoftSplit) return;
+          if (run)
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.q_raw[qb])) : "memory");
+        } else {
+          if (at == 0) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+          }
+          split_rows<D, NP, 2>(to, ctl.qmul[qb], at, a.scale * kLog2e, run);
+          at += 2 * kPer;
+          if (at < NP) return;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (run && lane == 0) mbar_arrive(bar(ctl.q_full[qb]));
         }
-        if (!y.done()) load_q();
+        at = -1;
+        ++piece;
+        y.next();
       };
-      if (!y.done()) load_q();
+      if (!y.done()) step_q();
       for (int of = 0, copied = 0; !x.done();) {  // the piece of the copies, its tiles so far
         copy();
         ++copied;
         const bool ended = x.done() || xkt == x.kt;
-        const int due = ended ? of + 1 : of;  // pieces whose Q has to be there now
-        int more = copied > C::kVStages ? NP / 16 : 0;
+        const int due = ended ? of + 1 : of;  // pieces whose Q has to be there (or asked for) now
+        int more = copied > C::kVStages;
 #pragma unroll 1
-        while (!y.done() && (piece <= due || (piece == of + 1 && more-- > 0))) split_q();
+        while (!y.done() && (piece <= due || (piece == of + 1 && more-- > 0))) step_q();
         if (ended) {
           ++of;
           copied = 0;
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp == 1 || warp == kLast - 1) {
     // ------------------------------------------------------------------ MMAs: S; P V
@@ -463,7 +502,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       const uint64_t dp0 = desc_mnmajor_sw128(sP, 16384);
       for (int piece = 0; !w.done(); ++piece, w.next()) {
         const int ob = C::kOBufs == 2 ? piece & 1 : 0, uses = C::kOBufs == 2 ? piece >> 1 : piece;
-        const uint32_t tO = tmem + C::kO + ob * 3 * NP;
+        const uint32_t tO = tmem + C::kO + ob * C::kParts;
         for (int kt = w.kt; kt < w.end; ++kt, ++t) {
           if (run && kt == w.kt && uses > 0)
             run = mbar_wait_spin(bar(ctl.o_free[ob]), (uses - 1) & 1, abort_flag, a.status);
@@ -493,7 +532,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
   } else {
     // ------------------------------------------------------------------ softmax, epilogue
     const int quad = warp & 3, r = quad * 32 + lane;  // key within the tile; head dimension of O^T
-    constexpr int NC = 16;
+    constexpr int NC = C::kCols;
     const int gr = C::kGroups == 1 ? 0 : (warp - 2) >> 2, n0 = gr * NC, on = 1 + gr;  // group, first column, barrier
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     bool run = true;
@@ -502,22 +541,37 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     auto wait_pv = [&](int j) -> bool {  // P V of tile j has completed
       return mbar_wait(bar(ctl.v_empty[j % C::kVStages]), (j / C::kVStages) & 1, abort_flag, a.status);
     };
+    auto split_q = [&](int piece) {  // the warp's four rows of the piece's Q
+      const int qb = piece & 1;
+      if (run) run = mbar_wait(bar(ctl.q_raw[qb]), (piece >> 1) & 1, abort_flag, a.status);
+      run = __all_sync(0xffffffffu, run);
+      split_rows<D, NP, D / 64>(sQ + qb * C::kQBytes, ctl.qmul[qb], n0 + 4 * quad, a.scale * kLog2e, run);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (run && lane == 0) mbar_arrive(bar(ctl.q_full[qb]));
+    };
+    int split = 0;  // pieces whose Q is
     for (int piece = 0; !w.done(); ++piece) {
       const SeqInfo& seq = w.seq;
       const int live = w.tokens() * G, tok = w.token(), qb = piece & 1;
-      const uint32_t tO = tmem + lane_off + C::kO + (C::kOBufs == 2 ? piece & 1 : 0) * 3 * NP + n0;
-      if (run) run = mbar_wait(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
+      const uint32_t tO = tmem + lane_off + C::kO + (C::kOBufs == 2 ? piece & 1 : 0) * C::kParts + n0;
       if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, tok + wk.by_group.div(n0 + r) + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
       const int least = s.causal ? min(seq.Lk, tok + seq.off + 1) : seq.Lk;
       float l[NC];
 #pragma unroll
       for (int n = 0; n < NC; ++n) l[n] = 0.f;
       for (int kt = w.kt; kt < w.end; ++kt, ++t) {
+        if constexpr (C::kSoftSplit) {  // Q of this piece, if it is the first, and before the last tile that of the next
+          const int due = kt + 1 == w.end && w.more() ? piece + 1 : piece;
+#pragma unroll 1
+          for (; split <= due; ++split) split_q(split);
+        }
+        if (run && kt == w.kt) run = mbar_wait(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
         if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
         fence_after_sync();
         uint32_t shi[NC], slo[NC];
-        tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + n0, shi);
-        tmem_ld16(tmem + lane_off + (t & 1) * 2 * NP + NP + n0, slo);
+        load_cols(tmem + lane_off + (t & 1) * 2 * NP + n0, shi);
+        load_cols(tmem + lane_off + (t & 1) * 2 * NP + NP + n0, slo);
         const uint32_t code = *reinterpret_cast<const uint16_t*>(ctl.codes[t % kCodeStages] + 2 * r);
         const uint32_t kc = code & 255u, vc = code >> 8;
         const float kmul = kc == 255u ? NAN : __uint_as_float(kc << 23);
@@ -574,7 +628,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll
           for (int n = 0; n < NC; ++n) z[n] = y[n];
           columns_reduce(z, lane, [](float p, float q) { return fmaxf(p, q); });
-          ctl.wmax[quad][n0 + (lane >> 1)] = z[0];
+          ctl.wmax[quad][n0 + lane * NC / 32] = z[0];
           named_bar_sync(on, 128);
           if (r < NC) {
             const int n = n0 + r;
@@ -592,11 +646,11 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll
             for (int part = 0; part < 3; ++part) {
               uint32_t o[NC];
-              tmem_ld16(tO + part * NP, o);
+              load_cols(tO + part * NP, o);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < NC; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ctl.alpha[n0 + i]);
-              tmem_st16(tO + part * NP, o);
+              store_cols(tO + part * NP, o);
             }
             tmem_st_wait();
 #pragma unroll
@@ -622,14 +676,19 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           lo[n / 4] = la | lb << 16;
         }
         // P's buffer is free: S of tile t, which has completed, was issued when the P V that read it had.
-        const uint32_t sPt = sP + (NP == 16 ? 0 : (t & 1) * C::kPStep) + r * 128;
-        auto put = [&](int c, const uint32_t (&x)[NC / 4]) {  // c: 16-byte chunk of the row's 3 NP bytes
-          store16(sPt + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+        const uint32_t sPt = sP + (NP <= 16 ? 0 : (t & 1) * C::kPStep) + r * 128;
+        auto put = [&](int c, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {  // c: 16-byte chunk of the row
+          store16(sPt + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), x0, x1, x2, x3);
         };
-        const int c0 = gr + (NP == 16 ? (t & 1) * 4 : 0);
-        put(c0, hi);
-        put(c0 + NP / 16, mid);
-        put(c0 + 2 * (NP / 16), lo);
+        const int c0 = gr + (NP <= 16 ? (t & 1) * 4 : 0);
+        if constexpr (NP == 8) {
+          put(c0, hi[0], hi[1], mid[0], mid[1]);
+          put(c0 + 1, lo[0], lo[1], 0, 0);
+        } else {
+          put(c0, hi[0], hi[1], hi[2], hi[3]);
+          put(c0 + NP / 16, mid[0], mid[1], mid[2], mid[3]);
+          put(c0 + 2 * (NP / 16), lo[0], lo[1], lo[2], lo[3]);
+        }
         // Value rows past the last key may hold anything, and 0 times NaN is NaN: they become 0.
         const int valid = seq.Lk - (kt << 7);
         if (valid < 128) {
@@ -653,7 +712,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       __syncwarp();
       if (run && lane == 0) mbar_arrive(bar(ctl.q_empty[qb]));  // (its scales are read)
       columns_reduce(l, lane, [](float p, float q) { return p + q; });
-      ctl.wmax[quad][n0 + (lane >> 1)] = l[0];
+      ctl.wmax[quad][n0 + lane * NC / 32] = l[0];
       named_bar_sync(on, 128);
       const bool whole = w.whole() && ctas == 1;
       const int slot = 2 * me + (piece == 0 ? 0 : 1);
@@ -680,9 +739,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       float o[NC];
       {
         uint32_t x[NC], z[NC];
-        tmem_ld16(tO, reinterpret_cast<uint32_t(&)[NC]>(o));
-        tmem_ld16(tO + NP, x);
-        tmem_ld16(tO + 2 * NP, z);
+        load_cols(tO, reinterpret_cast<uint32_t(&)[NC]>(o));
+        load_cols(tO + NP, x);
+        load_cols(tO + 2 * NP, z);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < NC; ++k) o[k] += __uint_as_float(x[k]) + __uint_as_float(z[k]);
@@ -691,13 +750,12 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
           const int n = n0 + k;
-          if (n < live) {
-            const float val = o[k] * ctl.alpha[n];
-            if (whole)
-              out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
-            else
-              part[n * D] = val;
-          }
+          if (n >= live) break;
+          const float val = o[k] * ctl.alpha[n];
+          if (whole)
+            out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
+          else
+            part[n * D] = val;
           if (++g == G) {
             g = 0;
             ++i;
@@ -774,7 +832,10 @@ int unit_tokens(const PagedShape& s) {
   const int G = s.H / s.Hkv;
   return (long long)s.Nq * G <= 64 ? s.Nq : 64 / G;
 }
-int unit_rows(const PagedShape& s) { return padded_rows(unit_tokens(s) * (s.H / s.Hkv)); }
+int unit_rows(const PagedShape& s) {
+  const int rows = unit_tokens(s) * (s.H / s.Hkv);
+  return rows <= 8 ? 8 : padded_rows(rows);
+}
 
 // Heads side by side: the most that leave no more than 3% of the CTAs without work.
 F8Cut cut_of(const PagedShape& s, int ctas) {
@@ -835,7 +896,7 @@ cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
   if (shared > 0) return launch_dependent_cluster(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, shared, st, tk, tv, a, wk);
   e = launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, st, tk, tv, a, wk);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_few8_join_kernel<D, NP>, dim3(ctas, NP / 16), dim3(4 * D), 0, st, a, wk);
+  return launch_dependent(paged_few8_join_kernel<D, NP>, dim3(ctas, (NP + 15) / 16), dim3(4 * D), 0, st, a, wk);
 }
 
 }  // namespace
@@ -854,9 +915,20 @@ size_t fa_paged_few8_workspace(const fa::PagedShape& s, int num_sms) {
   return fa::up256(ctas * 2 * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
 }
 
+namespace fa {
+namespace {
+template <int D>
+cudaError_t launch_rows(const FaPagedArgs& a, cudaStream_t st) {
+  switch (unit_rows(a.s)) {
+    case 8: return launch_few8<D, 8>(a, st);
+    case 16: return launch_few8<D, 16>(a, st);
+    case 32: return launch_few8<D, 32>(a, st);
+    default: return launch_few8<D, 64>(a, st);
+  }
+}
+}  // namespace
+}  // namespace fa
+
 cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, cudaStream_t st) {
-  const int np = fa::unit_rows(a.s);
-  if (a.s.d == 64)
-    return np == 16 ? fa::launch_few8<64, 16>(a, st) : np == 32 ? fa::launch_few8<64, 32>(a, st) : fa::launch_few8<64, 64>(a, st);
-  return np == 16 ? fa::launch_few8<128, 16>(a, st) : np == 32 ? fa::launch_few8<128, 32>(a, st) : fa::launch_few8<128, 64>(a, st);
+  return a.s.d == 64 ? fa::launch_rows<64>(a, st) : fa::launch_rows<128>(a, st);
 }
