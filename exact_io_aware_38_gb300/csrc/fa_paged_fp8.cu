@@ -12,8 +12,6 @@
 namespace fa {
 namespace {
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
 // The code of a row whose largest magnitude has these bf16 bits.
 __device__ __forceinline__ uint32_t row_code(uint32_t top) {
   return top == 0 ? 0u : top >= 0x7f80u ? 255u : (top >> 7) < 54 ? 47u : (top >> 7) - 7u;
@@ -34,141 +32,144 @@ __device__ __forceinline__ uint2 quantised8(uint4 x, float by) {
   return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
 }
 
-// Append: one warp per new token, its keys and values both; 16 values a lane and two such chunks of each in flight.
-template <int D>
-__global__ void __launch_bounds__(128) paged_append_fp8_kernel(const FaPagedArgs a) {
-  let_dependent_start();
-  grid_dependency_wait();
-  constexpr int kLanes = D / 16;  // that share a head's row
-  const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31;
-  const uint32_t row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+// Eight e4m3 bytes times 2^(code - 127) as eight bf16 values, each exact: f16 holds every e4m3 number.
+__device__ __forceinline__ uint4 read8(uint2 y, uint32_t code) {
+  const float by = code == 255 ? NAN : __uint_as_float(code << 23);
+  const uint32_t w[2] = {y.x, y.y};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> ((i & 1) * 16))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    r[i] = pack_bf16x2(f.x * by, f.y * by);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+constexpr int kRowThreads = 64;  // (of a block, appending 64 tokens: 2.3 us; 128: 2.4, 256: 2.7)
+
+// Which key of which sequence packed or fixed row `row` is, by the whole warp: false where it has no place (reported where it
+// should). Both ways move a row per warp, its keys and values, all of 8 heads at d = 128 in flight at once.
+struct Place {
+  int b, key;
+  int row, batch;  // in the tensors of new tokens
+};
+__device__ __forceinline__ bool find_place(const PagedShape& s, uint32_t row, int* status, Place& at) {
   int b, i = 0;
   if (s.cu_q != nullptr) {
-    if (row >= (uint32_t)s.rows_q) return;
+    if (row >= (uint32_t)s.rows_q) return false;
     b = sequence_of(s, (int)row);
   } else {
     b = (int)(row / (uint32_t)s.Nq);
     i = (int)(row % (uint32_t)s.Nq);
   }
-  if (b >= s.B) return;
+  if (b >= s.B) return false;
   const SeqInfo seq = paged_seq(s, b);
   if (s.cu_q != nullptr) i = (int)row - seq.q0;
-  if (i < 0 || i >= seq.Lq) return;
+  if (i < 0 || i >= seq.Lq) return false;
   const long long j = (long long)s.seqlens[b] - seq.Lq + i;  // the unclamped length places the token
   if (j < 0 || (j >> s.page_shift) >= s.max_pages) {
-    if (lane == 0) report_status(a.status, FA_ERR_BOUNDS);
-    return;
+    report_status(status, FA_ERR_BOUNDS);
+    return false;
   }
-  const uint8_t* src[2] = {
-      reinterpret_cast<const uint8_t*>(a.k_new) + 2 * elem_offset(a.sk_new, seq.bb, seq.q0 + i, 0),
-      reinterpret_cast<const uint8_t*>(a.v_new) + 2 * elem_offset(a.sv_new, seq.bb, seq.q0 + i, 0)};
-  const long long head[2] = {2 * a.sk_new.head, 2 * a.sv_new.head};
-  const int chunks = s.Hkv * kLanes;
-  uint4 x[2][2][2];  // [tensor][chunk][half]
+  at = Place{b, (int)j, seq.q0 + i, seq.bb};
+  return true;
+}
+
+// Append: bound by memory, 6 bytes a value (a row of 8 heads is read and written by one warp). 16 values a lane here: a row's
+// largest takes one exchange less (64 tokens of 8 heads, d = 128, 2.4 us, with 8 values 3.0; 16388 tokens 18.7 and 20.8).
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) paged_append_fp8_kernel(const FaPagedArgs a) {
+  let_dependent_start();
+  grid_dependency_wait();
+  constexpr int kLanes = D / 16;  // that share a head's row
+  const PagedShape& s = a.s;
+  const int lane = threadIdx.x & 31, chunks = s.Hkv * kLanes;
+  Place at;
+  if (!find_place(s, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, a.status, at)) return;
+  const __nv_bfloat16* src[2] = {
+      static_cast<const __nv_bfloat16*>(a.k_new) + elem_offset(a.sk_new, at.batch, at.row, 0) + lane % kLanes * 16,
+      static_cast<const __nv_bfloat16*>(a.v_new) + elem_offset(a.sv_new, at.batch, at.row, 0) + lane % kLanes * 16};
+  const long long from[2] = {a.sk_new.head, a.sv_new.head}, to[2] = {a.sk.head, a.sv.head};
+  uint4 x[2][2][2];  // [tensor][step][half]
   auto load = [&](int c0) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = c0 + k * 32 + lane;
-        if (c < chunks) {
-          const uint4* at = reinterpret_cast<const uint4*>(src[t] + (c / kLanes) * head[t]) + (c % kLanes) * 2;
-          x[t][k][0] = at[0];
-          x[t][k][1] = at[1];
-        } else {
-          x[t][k][0] = x[t][k][1] = make_uint4(0, 0, 0, 0);
+      for (int t = 0; t < 2; ++t) {
+        const uint4* p = reinterpret_cast<const uint4*>(src[t] + (c0 + 32 * k) / kLanes * from[t]);
+        x[t][k][0] = x[t][k][1] = make_uint4(0, 0, 0, 0);
+        if (c0 + 32 * k < chunks) {
+          x[t][k][0] = p[0];
+          x[t][k][1] = p[1];
         }
       }
   };
-  load(0);  // on its way while the page is looked up
-  const int page = paged_page(s, b, (int)(j >> s.page_shift), a.status);
+  load(lane);  // on its way while the page is looked up
+  const int page = paged_page(s, at.b, at.key >> s.page_shift, a.status), slot = at.key & ((1 << s.page_shift) - 1);
   if (page < 0) return;
-  const int slot = (int)(j & ((1 << s.page_shift) - 1));
-  uint8_t* dst[2] = {static_cast<uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0),
-                     static_cast<uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0)};
-  const long long to[2] = {a.sk.head, a.sv.head};
-  for (int c0 = 0; c0 < chunks; c0 += 64) {
-    if (c0 > 0) load(c0);
+  uint8_t* dst[2] = {static_cast<uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0) + lane % kLanes * 16,
+                     static_cast<uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0) + lane % kLanes * 16};
+  for (int c0 = lane; c0 < chunks + lane; c0 += 64) {
+    if (c0 > lane) load(c0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = c0 + k * 32 + lane;
+      const int c = c0 + 32 * k, h = c / kLanes;
+      if (c - lane >= chunks) break;  // (by whole warps)
       uint32_t code[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const uint4 p = x[t][k][0], q = x[t][k][1];
         uint32_t m = 0;  // magnitudes of two values in each word: bf16 bits without the sign are ordered as integers
-        for (uint32_t w : {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}) m = max_u16x2(m, w & 0x7fff7fffu);
+        for (uint32_t w : {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}) m = __vmaxu2(m, w & 0x7fff7fffu);
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
         code[t] = row_code(max(m & 0xffffu, m >> 16));
         const float by = code[t] == 0 || code[t] == 255 ? 0.f : __uint_as_float((254 - code[t]) << 23);
         const uint2 lo = quantised8(p, by), hi = quantised8(q, by);
-        if (c < chunks)
-          *reinterpret_cast<uint4*>(dst[t] + (c / kLanes) * to[t] + (c % kLanes) * 16) =
-              make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (c < chunks) *reinterpret_cast<uint4*>(dst[t] + h * to[t]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
       if (c < chunks && c % kLanes == 0)
-        *reinterpret_cast<uint16_t*>(a.codes + 2 * weight_offset(s, page, c / kLanes, slot)) =
-            (uint16_t)(code[0] | code[1] << 8);
+        *reinterpret_cast<uint16_t*>(a.codes + 2 * weight_offset(s, page, h, slot)) = (uint16_t)(code[0] | code[1] << 8);
     }
   }
 }
 
-// 16 e4m3 bytes times 2^(code - 127) as 16 bf16 values, each exact: f16 holds every e4m3 number.
-__device__ __forceinline__ void read16(uint4 y, uint32_t code, uint4 (&out)[2]) {
-  const float by = code == 255 ? NAN : __uint_as_float(code << 23);
-  const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-  uint32_t r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint16_t two = (uint16_t)(w[i >> 1] >> ((i & 1) * 16));
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    r[i] = pack_bf16x2(f.x * by, f.y * by);
-  }
-  out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  out[1] = make_uint4(r[4], r[5], r[6], r[7]);
-}
-
-// One key and value of the cache as rows of bf16, by a warp: 16 values a lane. kJoint: for the attention, where a value of
-// NaN would reach rows that do not see it (0 times NaN): its key becomes NaN, which only rows that see it look at, and the value 0.
+// One key and value of the cache as rows of bf16, by a warp, 8 values a lane: every store of the warp is then whole lines
+// (57345 rows of 8 heads 36.5 us, 6.2 TB/s; with 16 values 44.4). kJoint: for the attention, where a value of NaN would reach rows
+// that do not see it (0 times NaN): its key becomes NaN, which only rows that see it look at, and the value 0.
 template <int D, bool kJoint>
 __device__ __forceinline__ void read_row(const FaPagedArgs& a, int page, int slot, __nv_bfloat16* k, long long k_head,
                                          __nv_bfloat16* v, long long v_head) {
-  constexpr int kLanes = D / 16;
+  constexpr int kLanes = D / 8, kSteps = 4;  // steps in flight
   const PagedShape& s = a.s;
   const int lane = threadIdx.x & 31, chunks = s.Hkv * kLanes;
-  const uint8_t* src[2] = {static_cast<const uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0),
-                           static_cast<const uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0)};
+  const uint8_t* src[2] = {static_cast<const uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0) + lane % kLanes * 8,
+                           static_cast<const uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0) + lane % kLanes * 8};
+  const uint8_t* codes = a.codes + 2 * weight_offset(s, page, 0, slot);
   const long long from[2] = {a.sk.head, a.sv.head}, to[2] = {k_head, v_head};
-  __nv_bfloat16* dst[2] = {k, v};
-  for (int c0 = 0; c0 < chunks; c0 += 64) {
-    uint4 y[2][2];
-    uint32_t codes[2];
+  __nv_bfloat16* dst[2] = {k + lane % kLanes * 8, v + lane % kLanes * 8};
+  for (int c0 = lane; c0 < chunks; c0 += 32 * kSteps) {
+    uint2 y[2][kSteps];
+    uint32_t both[kSteps];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int c = c0 + n * 32 + lane;
-      if (c >= chunks) continue;
+    for (int n = 0; n < kSteps; ++n) {
+      const int h = (c0 + 32 * n) / kLanes;
+      if (c0 + 32 * n >= chunks) break;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        y[t][n] = *reinterpret_cast<const uint4*>(src[t] + (c / kLanes) * from[t] + (c % kLanes) * 16);
-      codes[n] = *reinterpret_cast<const uint16_t*>(a.codes + 2 * weight_offset(s, page, c / kLanes, slot));
+      for (int t = 0; t < 2; ++t) y[t][n] = *reinterpret_cast<const uint2*>(src[t] + h * from[t]);
+      both[n] = *reinterpret_cast<const uint16_t*>(codes + ((size_t)h << s.page_shift) * 2);
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int c = c0 + n * 32 + lane;
-      if (c >= chunks) continue;
+    for (int n = 0; n < kSteps; ++n) {
+      const int h = (c0 + 32 * n) / kLanes;
+      if (c0 + 32 * n >= chunks) break;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        uint4 out[2];
-        uint32_t code = (codes[n] >> (8 * t)) & 255u;
-        if (kJoint) code = t == 0 && (codes[n] >> 8) == 255u ? 255u : t == 1 && code == 255u ? 0u : code;
-        read16(y[t][n], code, out);
-        uint4* at = reinterpret_cast<uint4*>(dst[t] + (c / kLanes) * to[t] + (c % kLanes) * 16);
-        at[0] = out[0];
-        at[1] = out[1];
+        uint32_t code = (both[n] >> (8 * t)) & 255u;
+        if (kJoint) code = t == 0 && (both[n] >> 8) == 255u ? 255u : t == 1 && code == 255u ? 0u : code;
+        *reinterpret_cast<uint4*>(dst[t] + h * to[t]) = read8(y[t][n], code);
       }
     }
   }
@@ -176,38 +177,20 @@ __device__ __forceinline__ void read_row(const FaPagedArgs& a, int page, int slo
 
 // Reading the last L_q keys of each sequence: one warp per row.
 template <int D>
-__global__ void __launch_bounds__(128) paged_read_fp8_kernel(const FaPagedArgs a) {
+__global__ void __launch_bounds__(kRowThreads) paged_read_fp8_kernel(const FaPagedArgs a) {
   let_dependent_start();
   grid_dependency_wait();
-  const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31;
-  const uint32_t row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  int b, i = 0;
-  if (s.cu_q != nullptr) {
-    if (row >= (uint32_t)s.rows_q) return;
-    b = sequence_of(s, (int)row);
-  } else {
-    b = (int)(row / (uint32_t)s.Nq);
-    i = (int)(row % (uint32_t)s.Nq);
-  }
-  if (b >= s.B) return;
-  const SeqInfo seq = paged_seq(s, b);
-  if (s.cu_q != nullptr) i = (int)row - seq.q0;
-  if (i < 0 || i >= seq.Lq) return;
-  const long long j = (long long)s.seqlens[b] - seq.Lq + i;
-  if (j < 0 || (j >> s.page_shift) >= s.max_pages) {
-    if (lane == 0) report_status(a.status, FA_ERR_BOUNDS);
-    return;
-  }
-  const int page = paged_page(s, b, (int)(j >> s.page_shift), a.status);
+  Place at;
+  if (!find_place(a.s, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, a.status, at)) return;
+  const int page = paged_page(a.s, at.b, at.key >> a.s.page_shift, a.status);
   if (page < 0) return;
-  read_row<D, false>(a, page, (int)(j & ((1 << s.page_shift) - 1)),
-              static_cast<__nv_bfloat16*>(a.k_out) + elem_offset(a.sk_new, seq.bb, seq.q0 + i, 0), a.sk_new.head,
-              static_cast<__nv_bfloat16*>(a.v_out) + elem_offset(a.sv_new, seq.bb, seq.q0 + i, 0), a.sv_new.head);
+  read_row<D, false>(a, page, at.key & ((1 << a.s.page_shift) - 1),
+                     static_cast<__nv_bfloat16*>(a.k_out) + elem_offset(a.sk_new, at.batch, at.row, 0), a.sk_new.head,
+                     static_cast<__nv_bfloat16*>(a.v_out) + elem_offset(a.sv_new, at.batch, at.row, 0), a.sv_new.head);
 }
 
 // Reading all keys of every sequence into a cache of its own, in pages of 128 keys [page][head][slot][d], `tiles` of them
-// a sequence, and that cache's page table.
+// a sequence, and that cache's page table. A warp per key, counted on over the sequences (4 keys of a page a warp: 1 us more).
 struct Staged {
   __nv_bfloat16 *k, *v;
   int32_t* table;
@@ -221,16 +204,17 @@ __global__ void __launch_bounds__(256) paged_stage_fp8_kernel(const FaPagedArgs 
   const PagedShape& s = a.s;
   const int at = blockIdx.x * blockDim.x + threadIdx.x, threads = gridDim.x * blockDim.x;
   for (int i = at; i < s.B * to.tiles; i += threads) to.table[i] = i;
-  const int warps = threads >> 5;
+  int j = at >> 5;
   for (int b = 0; b < s.B; ++b) {
     const SeqInfo seq = paged_seq(s, b);
-    if (seq.Lq == 0) continue;
-    for (int j = at >> 5; j < seq.Lk; j += warps) {
+    const int keys = seq.Lq > 0 ? seq.Lk : 0;
+    for (; j < keys; j += threads >> 5) {
       const int page = paged_page(s, b, j >> s.page_shift, a.status);
       if (page < 0) continue;
       const size_t row = ((size_t)(b * to.tiles + (j >> 7)) * s.Hkv * 128 + (j & 127)) * D;
       read_row<D, true>(a, page, j & ((1 << s.page_shift) - 1), to.k + row, 128 * D, to.v + row, 128 * D);
     }
+    j -= keys;
   }
 }
 
@@ -266,22 +250,22 @@ StagePlan stage_plan(const PagedShape& s, int num_sms) {
   return p;
 }
 
-unsigned row_blocks(const PagedShape& s) {  // a warp per row, four to a block
+unsigned row_blocks(const PagedShape& s) {  // a warp per row
   const long long rows = s.cu_q != nullptr ? s.rows_q : (long long)s.B * s.Nq;
-  return (unsigned)((rows + 3) / 4);
+  return (unsigned)((rows * 32 + kRowThreads - 1) / kRowThreads);
 }
 
 }  // namespace
 }  // namespace fa
 
 cudaError_t fa_launch_paged_append_fp8(const FaPagedArgs& a, cudaStream_t st) {
-  const dim3 grid(fa::row_blocks(a.s)), block(128);
+  const dim3 grid(fa::row_blocks(a.s)), block(fa::kRowThreads);
   return a.s.d == 64 ? launch_dependent(fa::paged_append_fp8_kernel<64>, grid, block, 0, st, a)
                      : launch_dependent(fa::paged_append_fp8_kernel<128>, grid, block, 0, st, a);
 }
 
 cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st) {
-  const dim3 grid(fa::row_blocks(a.s)), block(128);
+  const dim3 grid(fa::row_blocks(a.s)), block(fa::kRowThreads);
   return a.s.d == 64 ? launch_dependent(fa::paged_read_fp8_kernel<64>, grid, block, 0, st, a)
                      : launch_dependent(fa::paged_read_fp8_kernel<128>, grid, block, 0, st, a);
 }

@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     }
   } else if (warp == 1 || warp == kLast - 1) {
     // ------------------------------------------------------------------ MMAs: S; P V
+    // (Their waits suspend: polling takes issue slots from the softmax, 39.4 us for 37.4 with 16 x 4099 keys and 20 rows.)
     const bool scores = warp == 1;
     bool run = true;
     int t = 0, st = 0;
@@ -471,12 +472,12 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       const uint64_t dq0 = D == 128 ? desc_kmajor_sw128(sQ) : desc_kmajor_sw64(sQ);
       for (int piece = 0; !w.done(); ++piece, w.next()) {
         const int qb = piece & 1;
-        if (run) run = mbar_wait_spin(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
+        if (run) run = mbar_wait(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
         for (int kt = w.kt; kt < w.end; ++kt, ++t) {
           // With P V of tile t - 2 done, its scores are read and its P's buffer is free for tile t.
           if (run && t >= 2)
-            run = mbar_wait_spin(bar(ctl.v_empty[(t - 2) % C::kVStages]), ((t - 2) / C::kVStages) & 1, abort_flag, a.status);
-          if (run) run = mbar_wait_spin(bar(ctl.k_full[st]), phase, abort_flag, a.status);
+            run = mbar_wait(bar(ctl.v_empty[(t - 2) % C::kVStages]), ((t - 2) / C::kVStages) & 1, abort_flag, a.status);
+          if (run) run = mbar_wait(bar(ctl.k_full[st]), phase, abort_flag, a.status);
           run = __all_sync(0xffffffffu, run);
           fence_after_sync();
           if (run && lane == 0) {
@@ -505,9 +506,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         const uint32_t tO = tmem + C::kO + ob * C::kParts;
         for (int kt = w.kt; kt < w.end; ++kt, ++t) {
           if (run && kt == w.kt && uses > 0)
-            run = mbar_wait_spin(bar(ctl.o_free[ob]), (uses - 1) & 1, abort_flag, a.status);
-          if (run) run = mbar_wait_spin(bar(ctl.v_full[st]), phase, abort_flag, a.status);
-          if (run) run = mbar_wait_spin(bar(ctl.p_ready[t & 1]), (t >> 1) & 1, abort_flag, a.status);
+            run = mbar_wait(bar(ctl.o_free[ob]), (uses - 1) & 1, abort_flag, a.status);
+          if (run) run = mbar_wait(bar(ctl.v_full[st]), phase, abort_flag, a.status);
+          if (run) run = mbar_wait(bar(ctl.p_ready[t & 1]), (t >> 1) & 1, abort_flag, a.status);
           run = __all_sync(0xffffffffu, run);
           fence_after_sync();
           if (run && lane == 0) {
