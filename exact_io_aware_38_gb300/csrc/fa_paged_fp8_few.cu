@@ -49,7 +49,9 @@ template <int D, int NP>
 struct F8Cfg {
   static constexpr int kTileBytes = 128 * D;
   static constexpr int kCtas = few8_ctas(NP);
-  static constexpr int kCols = NP < 16 ? NP : 16, kGroups = NP / kCols;  // rows of a group of four softmax warps; groups
+  // Rows of a group of four softmax warps, and groups. Eight rows are a shorter chain of steps (16 x 4099 keys, 20 rows: 35.8 us,
+  // with 16 a group 37.2), but twice the warps, for which 16 rows twice on an SM have no registers (28.1 us, with 8 a group 32).
+  static constexpr int kCols = NP == 8 || NP == 32 ? 8 : 16, kGroups = NP / kCols;
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kKStages = NP <= 16 ? (D == 128 ? 3 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;
   static constexpr int kVStages = NP <= 16 ? (D == 128 ? 2 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 3 : 6;
@@ -542,11 +544,11 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     auto wait_pv = [&](int j) -> bool {  // P V of tile j has completed
       return mbar_wait(bar(ctl.v_empty[j % C::kVStages]), (j / C::kVStages) & 1, abort_flag, a.status);
     };
-    auto split_q = [&](int piece) {  // the warp's four rows of the piece's Q
+    auto split_q = [&](int piece) {  // four rows a warp of the piece's Q
       const int qb = piece & 1;
       if (run) run = mbar_wait(bar(ctl.q_raw[qb]), (piece >> 1) & 1, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run);
-      split_rows<D, NP, D / 64>(sQ + qb * C::kQBytes, ctl.qmul[qb], n0 + 4 * quad, a.scale * kLog2e, run);
+      if (4 * quad < NC) split_rows<D, NP, D / 64>(sQ + qb * C::kQBytes, ctl.qmul[qb], n0 + 4 * quad, a.scale * kLog2e, run);
       fence_proxy_async_smem();
       __syncwarp();
       if (run && lane == 0) mbar_arrive(bar(ctl.q_full[qb]));
@@ -681,10 +683,19 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         auto put = [&](int c, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {  // c: 16-byte chunk of the row
           store16(sPt + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), x0, x1, x2, x3);
         };
-        const int c0 = gr + (NP <= 16 ? (t & 1) * 4 : 0);
+        const int c0 = n0 / 16 + (NP <= 16 ? (t & 1) * 4 : 0);
         if constexpr (NP == 8) {
           put(c0, hi[0], hi[1], mid[0], mid[1]);
           put(c0 + 1, lo[0], lo[1], 0, 0);
+        } else if constexpr (NC == 8) {
+          auto put8 = [&](int c, const uint32_t (&x)[2]) {
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(sPt + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4) + (n0 & 8)),
+                         "r"(x[0]), "r"(x[1])
+                         : "memory");
+          };
+          put8(c0, hi);
+          put8(c0 + NP / 16, mid);
+          put8(c0 + 2 * (NP / 16), lo);
         } else {
           put(c0, hi[0], hi[1], hi[2], hi[3]);
           put(c0 + NP / 16, mid[0], mid[1], mid[2], mid[3]);
