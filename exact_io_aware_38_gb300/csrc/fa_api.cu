@@ -1,5 +1,6 @@
 // C ABI of the attention library: argument validation, workspace layout and kernel launches.
 // Every check runs on the host before any CUDA call, so invalid arguments never reach a GPU.
+#include <limits.h>
 #include <math.h>
 
 #include "fa_common.cuh"
@@ -325,6 +326,7 @@ int paged_shape(const fa_paged_problem* p, PagedRowsOf of, fa::PagedShape* out) 
   s.max_pages = p->max_pages;
   s.table = p->page_table;
   s.seqlens = p->seqlens_k;
+  s.max_q = INT_MAX;
   const double rows = s.cu_q != nullptr ? (double)s.rows_q : (double)s.B * s.Nq;
   if (of != PagedRowsOf::kNone && rows * s.H * s.d >= kMaxElems) return FA_ERR_UNSUPPORTED;
   if ((double)s.B * s.Hkv * s.max_k >= kMaxKeys) return FA_ERR_UNSUPPORTED;

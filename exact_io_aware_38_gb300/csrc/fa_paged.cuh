@@ -18,6 +18,7 @@ struct PagedShape {
   int num_pages, max_pages;
   const int32_t* table;    // [B][max_pages]
   const int32_t* seqlens;  // [B]
+  int min_q, max_q;        // sequences with fewer or more new tokens count as without any: another kernel has them
 };
 
 // The kernels of this family are programmatic dependents of one another. Each lets its own dependent be
@@ -43,6 +44,7 @@ __device__ __forceinline__ SeqInfo paged_seq(const PagedShape& s, int b) {
     r.Lq = s.Nq;
     r.bb = b;
   }
+  if (r.Lq < s.min_q || r.Lq > s.max_q) r.Lq = 0;
   r.Lk = clampi(s.seqlens[b], 0, s.max_k);
   r.k0 = 0;
   r.off = r.Lk - r.Lq;
@@ -401,8 +403,10 @@ cudaError_t fa_launch_paged_evict(const FaPagedArgs& a, cudaStream_t st);
 // The cache held in 8 bits: append, reading rows back, and the attention with its workspace.
 cudaError_t fa_launch_paged_append_fp8(const FaPagedArgs& a, cudaStream_t st);
 cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st);
-bool fa_paged_few8(const fa::PagedShape& s);  // few enough rows for the kernel that reads the bytes as they lie
-size_t fa_paged_few8_workspace(const fa::PagedShape& s, int num_sms);
-cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, cudaStream_t st);
+// Attention by the kernel that reads the bytes as they lie, in units of `tokens` new tokens (tokens x grouped heads up to
+// 64): the tokens of a unit for which it takes the whole batch, or 0 where there are too many rows.
+int fa_paged_few8_tokens(const fa::PagedShape& s);
+size_t fa_paged_few8_workspace(const fa::PagedShape& s, int tokens, int num_sms);
+cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, int tokens, cudaStream_t st);
 size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms);
 cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st);

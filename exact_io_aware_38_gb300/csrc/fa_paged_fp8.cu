@@ -250,6 +250,18 @@ StagePlan stage_plan(const PagedShape& s, int num_sms) {
   return p;
 }
 
+// A packed batch whose sequences are of different lengths may hold prompts beside single tokens, and a token's keys are not
+// read back for it alone: sequences of up to four units of 16 rows go to the few-row kernel. The tokens of such a unit, 0 where
+// all sequences go one way. What the host knows is the sum of the new tokens' lengths, and bounds. The further launches take
+// 15 to 20 us, which few or short sequences do not give back: 6 sequences up to 6001 keys, two of them of one token,
+// 163 us apart and 156 together, 12 up to 4000 of 12 heads, d = 64, 131 and 132; 33 up to 8000 606 and 679.
+int apart_tokens(const PagedShape& s) {
+  const int G = s.H / s.Hkv;
+  if (s.cu_q == nullptr || G > 64 || s.rows_q * 4ll > 3ll * s.B * s.Nq) return 0;
+  if ((double)s.B * s.max_k * s.Hkv * s.d < (double)(1 << 26)) return 0;
+  return G <= 16 ? 16 / G : 1;
+}
+
 unsigned row_blocks(const PagedShape& s) {  // a warp per row
   const long long rows = s.cu_q != nullptr ? s.rows_q : (long long)s.B * s.Nq;
   return (unsigned)((rows * 32 + kRowThreads - 1) / kRowThreads);
@@ -271,12 +283,22 @@ cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st) {
 }
 
 size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms) {
-  return fa_paged_few8(s) ? fa_paged_few8_workspace(s, num_sms) : fa::stage_plan(s, num_sms).bytes();
+  if (const int tokens = fa_paged_few8_tokens(s)) return fa_paged_few8_workspace(s, tokens, num_sms);
+  const int apart = fa::apart_tokens(s);
+  const size_t few = apart > 0 ? fa_paged_few8_workspace(s, apart, num_sms) : 0, staged = fa::stage_plan(s, num_sms).bytes();
+  return few > staged ? few : staged;
 }
 
 cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st) {
-  const fa::PagedShape& s = a.s;
-  if (fa_paged_few8(s)) return fa_launch_paged_few8(a, st);
+  if (const int tokens = fa_paged_few8_tokens(a.s)) return fa_launch_paged_few8(a, tokens, st);
+  fa::PagedShape s = a.s;
+  if (const int tokens = fa::apart_tokens(s)) {
+    FaPagedArgs x = a;
+    x.s.max_q = 4 * tokens;
+    const cudaError_t e = fa_launch_paged_few8(x, tokens, st);
+    if (e != cudaSuccess) return e;
+    s.min_q = 4 * tokens + 1;
+  }
   const fa::StagePlan plan = fa::stage_plan(s, a.num_sms);
   char* ws = static_cast<char*>(a.workspace);
   fa::Staged to;
@@ -287,6 +309,7 @@ cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st) {
   for (int b = 0; b < s.B; b += plan.group) {
     const int group = s.B - b < plan.group ? s.B - b : plan.group;
     FaPagedArgs x = a;  // the sequences [b, b + group)
+    x.s = s;
     x.s.B = group;
     x.s.table += (size_t)b * s.max_pages;
     x.s.seqlens += b;

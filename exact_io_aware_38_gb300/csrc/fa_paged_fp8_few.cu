@@ -840,26 +840,22 @@ __global__ void __launch_bounds__(4 * D) paged_few8_join_kernel(const FaPagedArg
   join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, blockIdx.x, d.w, n, e, seq, d.x, of.w + n / G, d.y * G + n % G);
 }
 
-int unit_tokens(const PagedShape& s) {
-  const int G = s.H / s.Hkv;
-  return (long long)s.Nq * G <= 64 ? s.Nq : 64 / G;
-}
-int unit_rows(const PagedShape& s) {
-  const int rows = unit_tokens(s) * (s.H / s.Hkv);
+int unit_rows(const PagedShape& s, int tokens) {
+  const int rows = tokens * (s.H / s.Hkv);
   return rows <= 8 ? 8 : padded_rows(rows);
 }
 
 // Heads side by side: the most that leave no more than 3% of the CTAs without work.
-F8Cut cut_of(const PagedShape& s, int ctas) {
+F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
   int side = s.Hkv;
   while (side > 1 && (s.Hkv % side != 0 || ctas / side * side * 100ll < 97ll * ctas)) --side;
-  return {unit_tokens(s), side, s.Hkv / side};
+  return {tokens, side, s.Hkv / side};
 }
 
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0; the rule of fa_paged_decode.cu.
-int unit_ctas(const PagedShape& s, int num_sms) {
-  if (unit_tokens(s) < s.Nq) return 0;
-  const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s));
+int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
+  if (tokens < s.Nq) return 0;
+  const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s, tokens));
   const int tiles = (s.max_k + 127) >> 7;
   int ctas = 1;
   if (tiles > 2) {
@@ -874,7 +870,7 @@ int unit_ctas(const PagedShape& s, int num_sms) {
 }
 
 template <int D, int NP>
-cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
+cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
   using C = F8Cfg<D, NP>;
   const PagedShape& s = a.s;
   const int P = 1 << s.page_shift, box = P < 128 ? P : 128;
@@ -885,13 +881,13 @@ cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
   if (!fa_make_tmap_u8(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, D, box, kL2) ||
       !fa_make_tmap_u8(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, D, box, kL2))
     return cudaErrorInvalidValue;
-  const int shared = unit_ctas(s, a.num_sms);
+  const int shared = unit_ctas(s, tokens, a.num_sms);
   int ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
   F8Work wk{};
-  wk.cut = {unit_tokens(s), 1, s.Hkv};
+  wk.cut = {tokens, 1, s.Hkv};
   wk.by_group = fast_div(s.H / s.Hkv);
   if (shared == 0) {
-    wk.cut = cut_of(s, ctas);
+    wk.cut = cut_of(s, tokens, ctas);
     ctas = ctas / wk.cut.side * wk.cut.side;
     char* ws = static_cast<char*>(a.workspace);
     wk.desc = reinterpret_cast<int4*>(ws);
@@ -915,14 +911,15 @@ cudaError_t launch_few8(const FaPagedArgs& a, cudaStream_t st) {
 }  // namespace fa
 
 // Up to four units of 64 rows; more rows, or a group of heads that no unit holds, go by way of the chunk kernel.
-bool fa_paged_few8(const fa::PagedShape& s) {
+int fa_paged_few8_tokens(const fa::PagedShape& s) {
   const int G = s.H / s.Hkv;
-  return G <= 64 && (long long)s.Nq <= 4ll * (64 / G);
+  if (G > 64 || (long long)s.Nq > 4ll * (64 / G)) return 0;
+  return (long long)s.Nq * G <= 64 ? s.Nq : 64 / G;
 }
 
-size_t fa_paged_few8_workspace(const fa::PagedShape& s, int num_sms) {
-  if (fa::unit_ctas(s, num_sms) > 0) return 0;
-  const int np = fa::unit_rows(s);
+size_t fa_paged_few8_workspace(const fa::PagedShape& s, int tokens, int num_sms) {
+  if (fa::unit_ctas(s, tokens, num_sms) > 0) return 0;
+  const int np = fa::unit_rows(s, tokens);
   const size_t ctas = (size_t)num_sms * fa::few8_ctas(np), rows = ctas * 2 * np;
   return fa::up256(ctas * 2 * sizeof(int4)) + fa::up256(rows * sizeof(float)) + rows * s.d * sizeof(float);
 }
@@ -930,17 +927,17 @@ size_t fa_paged_few8_workspace(const fa::PagedShape& s, int num_sms) {
 namespace fa {
 namespace {
 template <int D>
-cudaError_t launch_rows(const FaPagedArgs& a, cudaStream_t st) {
-  switch (unit_rows(a.s)) {
-    case 8: return launch_few8<D, 8>(a, st);
-    case 16: return launch_few8<D, 16>(a, st);
-    case 32: return launch_few8<D, 32>(a, st);
-    default: return launch_few8<D, 64>(a, st);
+cudaError_t launch_rows(const FaPagedArgs& a, int tokens, cudaStream_t st) {
+  switch (unit_rows(a.s, tokens)) {
+    case 8: return launch_few8<D, 8>(a, tokens, st);
+    case 16: return launch_few8<D, 16>(a, tokens, st);
+    case 32: return launch_few8<D, 32>(a, tokens, st);
+    default: return launch_few8<D, 64>(a, tokens, st);
   }
 }
 }  // namespace
 }  // namespace fa
 
-cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, cudaStream_t st) {
-  return a.s.d == 64 ? fa::launch_rows<64>(a, st) : fa::launch_rows<128>(a, st);
+cudaError_t fa_launch_paged_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
+  return a.s.d == 64 ? fa::launch_rows<64>(a, tokens, st) : fa::launch_rows<128>(a, tokens, st);
 }

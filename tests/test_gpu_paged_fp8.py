@@ -482,6 +482,26 @@ def test_chunks_in_rounds_through_one_workspace():
         p.check_attend(*p.attend(True), True)
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (20, 1, 128), (5, 5, 64)])
+def test_prompts_beside_single_tokens(heads):
+    """A packed batch in which two kernels share the sequences by their new tokens: none, one, at the limit between them,
+    one past it, and prompts; a bound on the keys that makes the batch look large."""
+    G = heads[0] // heads[1]
+    limit = 4 * (16 // G if G <= 16 else 1)
+    lq = [1, 300, 0, limit, limit + 1, 1, limit - 1, 90, 2, 0, 1]
+    lk = [700, 300, 50, 129, 260, 0, 40, 500, 128, 0, 1]
+    p = Problem8(lk, lq, *heads, page=16, seed=34, packed=True)
+    wide = torch.full((len(lk), (1 << 26) // (len(lk) * heads[1] * heads[2] * 16) + 1), -7, dtype=torch.int32)
+    wide[:, :p.table.shape[1]] = p.table
+    p.ctable = wide.cuda()
+    out = torch.full_like(p.cq, 3.0)
+    for sms in (152, 7):
+        o, lse = p.attend(True, num_sms=sms, out=out)
+        p.check_attend(o, lse, True)
+        assert (o[int(p.cu[-1]):] == 3.0).all()
+    p.check_attend(*p.attend(False), False)
+
+
 # ------------------------------------------------------------------------------------------- as they are used
 
 
