@@ -65,10 +65,10 @@ struct F8Cfg {
   static constexpr int kPBytes = NP <= 16 ? 16384 : 2 * kPStep;
   static constexpr int kSmem = kQBufs * kQBytes + (kKStages + kVStages) * kTileBytes + kPBytes + 1024;
   static constexpr bool kSoftSplit = NP > 16;  // the softmax warps split Q
-  static constexpr int kOBufs = NP == 64 ? 1 : 2;
-  static constexpr uint32_t kO = 4 * NP;  // tensor memory: S x 2, then O
-  static constexpr uint32_t kTmemCols = NP == 8 ? 128 : NP == 16 ? 256 : 512;
-  static_assert(kO + kOBufs * kParts <= kTmemCols);
+  // Tensor memory: S x 2, then O. One O is enough: the first P of a piece follows the last one's epilogue.
+  static constexpr uint32_t kO = 4 * NP;
+  static constexpr uint32_t kTmemCols = NP == 8 ? 64 : NP == 16 ? 128 : NP == 32 ? 256 : 512;
+  static_assert(kO + kParts <= kTmemCols);
   static constexpr uint32_t kIdS = idesc_e4m3(128, 2 * NP);
   // O^T has D rows; at D = 64 the upper 64 lanes multiply whatever follows V in shared memory and are never read.
   static constexpr uint32_t kIdPV = idesc_e4m3_e5m2_mn(128, kParts);
@@ -108,7 +108,6 @@ struct F8Ctl {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // (k_full: codes too; v_empty: also that P V has completed)
   uint64_t s_full[2];
   uint64_t p_ready[2];  // per buffer of P
-  uint64_t o_free[2];
   uint64_t drain[2];    // per issuer
   uint32_t tmem_base;
   int abort_flag;
@@ -287,7 +286,6 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       mbar_init(bar(ctl.q_full[i]), C::kSoftSplit ? 4 * C::kGroups : 1);
       mbar_init(bar(ctl.q_empty[i]), 1 + 4 * C::kGroups);
       mbar_init(bar(ctl.s_full[i]), 2);
-      mbar_init(bar(ctl.o_free[i]), 4 * C::kGroups);
       mbar_init(bar(ctl.p_ready[i]), 4 * C::kGroups);
       mbar_init(bar(ctl.drain[i]), 1);
     }
@@ -503,12 +501,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     } else {
       const uint64_t dv0 = D == 128 ? desc_mnmajor_sw128(sV0, 16384) : desc_mnmajor_sw64(sV0, C::kTileBytes);
       const uint64_t dp0 = desc_mnmajor_sw128(sP, 16384);
-      for (int piece = 0; !w.done(); ++piece, w.next()) {
-        const int ob = C::kOBufs == 2 ? piece & 1 : 0, uses = C::kOBufs == 2 ? piece >> 1 : piece;
-        const uint32_t tO = tmem + C::kO + ob * C::kParts;
+      const uint32_t tO = tmem + C::kO;
+      for (; !w.done(); w.next()) {
         for (int kt = w.kt; kt < w.end; ++kt, ++t) {
-          if (run && kt == w.kt && uses > 0)
-            run = mbar_wait(bar(ctl.o_free[ob]), (uses - 1) & 1, abort_flag, a.status);
           if (run) run = mbar_wait(bar(ctl.v_full[st]), phase, abort_flag, a.status);
           if (run) run = mbar_wait(bar(ctl.p_ready[t & 1]), (t >> 1) & 1, abort_flag, a.status);
           run = __all_sync(0xffffffffu, run);
@@ -538,6 +533,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     constexpr int NC = C::kCols;
     const int gr = C::kGroups == 1 ? 0 : (warp - 2) >> 2, n0 = gr * NC, on = 1 + gr;  // group, first column, barrier
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tO = tmem + lane_off + C::kO + n0;
     bool run = true;
     int t = 0, vs = 0;
     uint32_t vphase = 0;
@@ -557,7 +553,6 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     for (int piece = 0; !w.done(); ++piece) {
       const SeqInfo& seq = w.seq;
       const int live = w.tokens() * G, tok = w.token(), qb = piece & 1;
-      const uint32_t tO = tmem + lane_off + C::kO + (C::kOBufs == 2 ? piece & 1 : 0) * C::kParts + n0;
       if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, tok + wk.by_group.div(n0 + r) + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
       const int least = s.causal ? min(seq.Lk, tok + seq.off + 1) : seq.Lk;
       float l[NC];
@@ -774,10 +769,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           }
         }
       }
-      fence_before_sync();
-      __syncwarp();
-      if (run && lane == 0) mbar_arrive(bar(ctl.o_free[C::kOBufs == 2 ? piece & 1 : 0]));
-      w.next();
+      w.next();  // (the arrival on the next tile's P orders the reads of O before the product that overwrites it)
     }
   }
 
