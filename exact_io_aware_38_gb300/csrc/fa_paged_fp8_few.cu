@@ -735,11 +735,16 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       named_bar_sync(on, 128);
       const bool whole = w.whole() && ctas == 1;
       const int slot = 2 * me + (piece == 0 ? 0 : 1);
+      auto total = [&](int n) { return (ctl.wmax[0][n] + ctl.wmax[1][n]) + (ctl.wmax[2][n] + ctl.wmax[3][n]); };
       if (r < NC) {
-        const int n = n0 + r;
-        const float sum = (ctl.wmax[0][n] + ctl.wmax[1][n]) + (ctl.wmax[2][n] + ctl.wmax[3][n]);
-        ctl.alpha[n] = sum == 0.f ? 0.f : 1.f / sum;  // (0: no visible key; a NaN stays one)
-        const float lse2 = sum == 0.f ? -INFINITY : ctl.ref[n] + log2f(sum);
+        const float sum = total(n0 + r);
+        ctl.alpha[n0 + r] = sum == 0.f ? 0.f : 1.f / sum;  // (0: no visible key; a NaN stays one)
+      }
+      __syncwarp();
+      named_bar_sync(on, 128);
+      if (quad == 3 && lane < NC) {  // (a warp that at d = 64 has nothing to store)
+        const int n = n0 + lane;
+        const float sum = total(n), lse2 = sum == 0.f ? -INFINITY : ctl.ref[n] + log2f(sum);
         if (whole) {
           const int i = wk.by_group.div(n);
           if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n - i * G, tok + i)] = lse2 * kLn2;
@@ -747,8 +752,6 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           (ctas > 1 ? ctl.part_lse : wk.part_lse + (size_t)slot * NP)[n] = lse2;
         }
       }
-      __syncwarp();
-      named_bar_sync(on, 128);
       if (run) run = wait_pv(t - 1);
       fence_after_sync();
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + tok, w.hk * G) + r;
