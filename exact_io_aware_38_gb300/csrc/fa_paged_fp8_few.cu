@@ -770,7 +770,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       }
       if (r < D) {
         // The strides are looked at once where many rows are stored: their lines of the arguments miss (48 x 1024 keys of 12 heads,
-        // d = 64, 64 rows: 75 us and 66). Up to 16 rows that costs the loop above registers it needs (1 row: 26.4 and 27.1).
+        // d = 64, 64 rows: 75 us and 66, 16 rows 40.7 and 38.6). With few it costs the loop above registers it needs (1 row: 26.4 us
+        // and 27.1; 16 rows at d = 128 26.7 and 30.5).
+        constexpr bool kStep = NP > 16 || (NP == 16 && D == 64);
         const long long step = a.so.head, wrap = a.so.row - (long long)G * a.so.head;
         __nv_bfloat16* to = out + (size_t)i * a.so.row + (size_t)g * a.so.head;
 #pragma unroll
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           const float val = o[k] * ctl.alpha[n];
           if (!whole)
             part[n * D] = val;
-          else if constexpr (C::kGroups > 1)
+          else if constexpr (kStep)
             *to = __float2bfloat16(val);
           else
             out[(size_t)i * a.so.row + (size_t)g * a.so.head] = __float2bfloat16(val);
@@ -867,7 +869,10 @@ F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
   return {tokens, side, s.Hkv / side};
 }
 
-// CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0; the rule of fa_paged_decode.cu.
+// CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0: the rule of fa_paged_decode.cu with
+// limits of its own, since a tile is half as many bytes. Eight tiles a CTA of a cluster (8 sequences of 8 heads, 4000 keys:
+// 13.9 us, divided 14.7; one of 8000 12.5 and 13.3; 4 of 4000 12.7 and 12.4; with 16 tiles 8 of 8000 21.3 and 19.6) or 16 of one
+// alone (24 of 12 heads, d = 64, 2000 keys: 16.1 and 20.0).
 int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
   if (tokens < s.Nq) return 0;
   const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s, tokens));
@@ -881,7 +886,7 @@ int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
     else if (units * 2 <= room)
       ctas = 2;
   }
-  return units * ctas <= room && tiles <= (ctas == 1 ? 8 : 4 * ctas) ? ctas : 0;
+  return units * ctas <= room && tiles <= (ctas == 1 ? 16 : 8 * ctas) ? ctas : 0;
 }
 
 template <int D, int NP>
