@@ -416,7 +416,10 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
  *   contents   a slot that no length reaches may hold any bytes and codes: it enters no result. A row that sees a key or
  *              value of code 255, or that holds NaN or an infinity itself, has O = LSE = NaN; rows that do not see it have none of it.
  *              Bytes of NaN (127 and 255), which an append never writes, reach the rows of their 128-key tile as a NaN
- *              in a bf16 cache does.
+ *              in a bf16 cache does; codes 1 to 46 and 248 to 254, which it never writes either, may overflow the row sums.
+ *   range      up to 256 rows (tokens x heads) of a K/V head, row sums are taken by way of the weighted values: a key whose value is
+ *              2^100 times smaller than another that the row sees may be missing from them, and so may keys with values of
+ *              zeros beside values of more than 2^30. More rows have no such limit.
  * Key weights and eviction take bf16 caches only.
  */
 
@@ -441,9 +444,10 @@ int fa_paged_read_fp8(const fa_paged_problem* p, void* k_rows, fa_strides sk_row
 /*
  * fa_fwd_paged over such a cache: O and LSE of the new tokens against the rows that it stands for. Arguments, masks, layouts and
  * errors as there, with the codes beside the caches.
- *   workspace    device, >= fa_fwd_paged_fp8_workspace_bytes(p, num_sms) bytes, 256-byte aligned; scratch only. It holds
- *                keys and values read back to bf16, of as many sequences as fit 1 GiB by the bound seqlen_k (one at least), so it
- *                grows with that bound: give the longest length in use.
+ *   workspace    device, >= fa_fwd_paged_fp8_workspace_bytes(p, num_sms) bytes, 256-byte aligned; scratch only. Up to 256 rows of a
+ *                K/V head (and 64 heads) as for fa_fwd_paged. For more it also holds keys and values read back to bf16, of as many
+ *                sequences as fit 1 GiB by the bound seqlen_k (one at least): it grows with that bound, so give the longest
+ *                length in use.
  */
 size_t fa_fwd_paged_fp8_workspace_bytes(const fa_paged_problem* p, int num_sms);
 int fa_fwd_paged_fp8(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,
