@@ -255,6 +255,18 @@ def test_attend_many_sequences(B):
         p.check_attend(*p.attend(True, num_sms=sms), True)
 
 
+@pytest.mark.parametrize("B", [31, 64, 65, 96, 256, 321, 600])
+def test_read_back_of_many_sequences(B):
+    """More sequences than a warp that reads keys back looks at in a step, many of them empty or without new tokens."""
+    r = np.random.default_rng(B)
+    for packed in (False, True):
+        lk = r.integers(0, 140, B) * (r.random(B) < 0.4)
+        lq = r.integers(1, 3, B) * (r.random(B) < 0.5) if packed else np.ones(B, dtype=int)
+        p = Problem8(lk.tolist(), lq.tolist(), 65, 1, 64, page=32, packed=packed, seed=14)
+        for sms in (1, 152):
+            p.check_attend(*p.attend(True, num_sms=sms), True)
+
+
 @pytest.mark.parametrize("n", [1, 4, 70])
 @pytest.mark.parametrize("layout", ["hpd", "gap"])
 @pytest.mark.parametrize("d", [64, 128])
