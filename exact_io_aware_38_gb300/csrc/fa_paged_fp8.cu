@@ -49,17 +49,35 @@ __device__ __forceinline__ uint4 read8(uint2 y, uint32_t code) {
 
 constexpr int kRowThreads = 64;  // (of a block, appending 64 tokens: 2.3 us; 128: 2.4, 256: 2.7)
 
-// Which key of which sequence packed or fixed row `row` is, by the whole warp: false where it has no place (reported where it
-// should). Both ways move a row per warp, its keys and values, all of 8 heads at d = 128 in flight at once.
+// Both ways move kRows rows per warp, keys and values: one, all of 8 heads at d = 128 in flight at once, or as many of fewer
+// heads (400000 rows of one head, d = 64, written and read: 29 and 29 us, one per warp 203 and 202). Where the rows are a warp
+// each, or a few, one is less to look up: 4096 packed ones of one head, each a sequence, take 5 us, 4 or 8 a warp 6.
+int rows_per_warp(const PagedShape& s, long long rows) {
+  const int most = 1024 / (s.Hkv * s.d);
+  return rows < (s.cu_q != nullptr ? 8192 : 2048) || most < 2 ? 1 : most < 4 ? 2 : most < 8 ? 4 : 8;
+}
+
+// Which key of which sequence this lane's row is, of the warp's rows from `first` on (packed or fixed), by the whole warp:
+// false where it has no place (reported where it should).
 struct Place {
   int b, key;
   int row, batch;  // in the tensors of new tokens
 };
-__device__ __forceinline__ bool find_place(const PagedShape& s, uint32_t row, int* status, Place& at) {
+template <int kRows>
+__device__ __forceinline__ bool find_place(const PagedShape& s, uint32_t first, int* status, Place& at) {
+  const uint32_t own = (threadIdx.x & 31) / (32 / kRows), row = first + own;
   int b, i = 0;
   if (s.cu_q != nullptr) {
+    if (first >= (uint32_t)s.rows_q) return false;
+    b = sequence_of(s, (int)first);
+    if (kRows > 1 && (b >= s.B || s.cu_q[b + 1] < (int)first + kRows)) {
+#pragma unroll 1
+      for (int n = 1; n < kRows; ++n) {
+        const int of = sequence_of(s, (int)first + n);
+        if (n == own) b = of;
+      }
+    }
     if (row >= (uint32_t)s.rows_q) return false;
-    b = sequence_of(s, (int)row);
   } else {
     b = (int)(row / (uint32_t)s.Nq);
     i = (int)(row % (uint32_t)s.Nq);
@@ -79,15 +97,16 @@ __device__ __forceinline__ bool find_place(const PagedShape& s, uint32_t row, in
 
 // Append: bound by memory, 6 bytes a value (a row of 8 heads is read and written by one warp). 16 values a lane here: a row's
 // largest takes one exchange less (64 tokens of 8 heads, d = 128, 2.4 us, with 8 values 3.0; 16388 tokens 18.7 and 20.8).
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kRowThreads) paged_append_fp8_kernel(const FaPagedArgs a) {
   let_dependent_start();
   grid_dependency_wait();
-  constexpr int kLanes = D / 16;  // that share a head's row
+  constexpr int kLanes = D / 16, kWide = 32 / kRows;  // lanes of a head's row, of a row
   const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31, chunks = s.Hkv * kLanes;
-  Place at;
-  if (!find_place(s, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, a.status, at)) return;
+  const int lane = threadIdx.x % kWide, chunks = s.Hkv * kLanes;
+  Place at{};
+  const bool placed = find_place<kRows>(s, ((blockIdx.x * blockDim.x + threadIdx.x) >> 5) * kRows, a.status, at);
+  if (kRows == 1 && !placed) return;
   const __nv_bfloat16* src[2] = {
       static_cast<const __nv_bfloat16*>(a.k_new) + elem_offset(a.sk_new, at.batch, at.row, 0) + lane % kLanes * 16,
       static_cast<const __nv_bfloat16*>(a.v_new) + elem_offset(a.sv_new, at.batch, at.row, 0) + lane % kLanes * 16};
@@ -98,24 +117,26 @@ __global__ void __launch_bounds__(kRowThreads) paged_append_fp8_kernel(const FaP
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint4* p = reinterpret_cast<const uint4*>(src[t] + (c0 + 32 * k) / kLanes * from[t]);
+        const uint4* p = reinterpret_cast<const uint4*>(src[t] + (c0 + kWide * k) / kLanes * from[t]);
         x[t][k][0] = x[t][k][1] = make_uint4(0, 0, 0, 0);
-        if (c0 + 32 * k < chunks) {
+        if ((kRows == 1 || placed) && c0 + kWide * k < chunks) {
           x[t][k][0] = p[0];
           x[t][k][1] = p[1];
         }
       }
   };
   load(lane);  // on its way while the page is looked up
-  const int page = paged_page(s, at.b, at.key >> s.page_shift, a.status), slot = at.key & ((1 << s.page_shift) - 1);
-  if (page < 0) return;
+  const int page = kRows == 1 || placed ? paged_page(s, at.b, at.key >> s.page_shift, a.status) : -1;
+  const int slot = at.key & ((1 << s.page_shift) - 1);
+  if (kRows == 1 && page < 0) return;
   uint8_t* dst[2] = {static_cast<uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0) + lane % kLanes * 16,
                      static_cast<uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0) + lane % kLanes * 16};
-  for (int c0 = lane; c0 < chunks + lane; c0 += 64) {
+  for (int c0 = lane; c0 < chunks + lane; c0 += 2 * kWide) {
     if (c0 > lane) load(c0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = c0 + 32 * k, h = c / kLanes;
+      const int c = c0 + kWide * k, h = c / kLanes;
+      const bool mine = c < chunks && page >= 0;
       if (c - lane >= chunks) break;  // (by whole warps)
       uint32_t code[2];
 #pragma unroll
@@ -128,77 +149,78 @@ __global__ void __launch_bounds__(kRowThreads) paged_append_fp8_kernel(const FaP
         code[t] = row_code(max(m & 0xffffu, m >> 16));
         const float by = code[t] == 0 || code[t] == 255 ? 0.f : __uint_as_float((254 - code[t]) << 23);
         const uint2 lo = quantised8(p, by), hi = quantised8(q, by);
-        if (c < chunks) *reinterpret_cast<uint4*>(dst[t] + h * to[t]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (mine) *reinterpret_cast<uint4*>(dst[t] + h * to[t]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
-      if (c < chunks && c % kLanes == 0)
+      if (mine && c % kLanes == 0)
         *reinterpret_cast<uint16_t*>(a.codes + 2 * weight_offset(s, page, h, slot)) = (uint16_t)(code[0] | code[1] << 8);
     }
   }
 }
 
-// One key and value of the cache as rows of bf16, by a warp, 8 values a lane: every store of the warp is then whole lines
+// One key and value of the cache as rows of bf16, by a warp or kWide lanes of it, 8 values a lane: every store of the warp is then whole lines
 // (57345 rows of 8 heads 36.5 us, 6.2 TB/s; with 16 values 44.4). kJoint: for the attention, where a value of NaN would reach rows
 // that do not see it (0 times NaN): its key becomes NaN, which only rows that see it look at, and the value 0.
-template <int D, bool kJoint>
+template <int D, int kWide, bool kJoint>
 __device__ __forceinline__ void read_row(const FaPagedArgs& a, int page, int slot, __nv_bfloat16* k, long long k_head,
                                          __nv_bfloat16* v, long long v_head) {
   constexpr int kLanes = D / 8, kSteps = 4;  // steps in flight
   const PagedShape& s = a.s;
-  const int lane = threadIdx.x & 31, chunks = s.Hkv * kLanes;
-  const uint8_t* src[2] = {static_cast<const uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0) + lane % kLanes * 8,
-                           static_cast<const uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0) + lane % kLanes * 8};
+  const int lane = threadIdx.x % kWide, chunks = s.Hkv * kLanes;
+  const uint8_t* src[2] = {static_cast<const uint8_t*>(a.k) + paged_offset(a.sk, page, slot, 0),
+                           static_cast<const uint8_t*>(a.v) + paged_offset(a.sv, page, slot, 0)};
   const uint8_t* codes = a.codes + 2 * weight_offset(s, page, 0, slot);
   const long long from[2] = {a.sk.head, a.sv.head}, to[2] = {k_head, v_head};
-  __nv_bfloat16* dst[2] = {k + lane % kLanes * 8, v + lane % kLanes * 8};
-  for (int c0 = lane; c0 < chunks; c0 += 32 * kSteps) {
+  __nv_bfloat16* dst[2] = {k, v};
+  for (int c0 = lane; c0 < chunks; c0 += kWide * kSteps) {
     uint2 y[2][kSteps];
     uint32_t both[kSteps];
 #pragma unroll
     for (int n = 0; n < kSteps; ++n) {
-      const int h = (c0 + 32 * n) / kLanes;
-      if (c0 + 32 * n >= chunks) break;
+      const int h = (c0 + kWide * n) / kLanes, at = (kWide % kLanes ? c0 + kWide * n : lane) % kLanes * 8;
+      if (c0 + kWide * n >= chunks) break;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) y[t][n] = *reinterpret_cast<const uint2*>(src[t] + h * from[t]);
+      for (int t = 0; t < 2; ++t) y[t][n] = *reinterpret_cast<const uint2*>(src[t] + h * from[t] + at);
       both[n] = *reinterpret_cast<const uint16_t*>(codes + ((size_t)h << s.page_shift) * 2);
     }
 #pragma unroll
     for (int n = 0; n < kSteps; ++n) {
-      const int h = (c0 + 32 * n) / kLanes;
-      if (c0 + 32 * n >= chunks) break;
+      const int h = (c0 + kWide * n) / kLanes, at = (kWide % kLanes ? c0 + kWide * n : lane) % kLanes * 8;
+      if (c0 + kWide * n >= chunks) break;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         uint32_t code = (both[n] >> (8 * t)) & 255u;
         if (kJoint) code = t == 0 && (both[n] >> 8) == 255u ? 255u : t == 1 && code == 255u ? 0u : code;
-        *reinterpret_cast<uint4*>(dst[t] + h * to[t]) = read8(y[t][n], code);
+        *reinterpret_cast<uint4*>(dst[t] + h * to[t] + at) = read8(y[t][n], code);
       }
     }
   }
 }
 
-// Reading the last L_q keys of each sequence: one warp per row.
-template <int D>
+// Reading the last L_q keys of each sequence.
+template <int D, int kRows>
 __global__ void __launch_bounds__(kRowThreads) paged_read_fp8_kernel(const FaPagedArgs a) {
   let_dependent_start();
   grid_dependency_wait();
   Place at;
-  if (!find_place(a.s, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, a.status, at)) return;
+  if (!find_place<kRows>(a.s, ((blockIdx.x * blockDim.x + threadIdx.x) >> 5) * kRows, a.status, at)) return;
   const int page = paged_page(a.s, at.b, at.key >> a.s.page_shift, a.status);
   if (page < 0) return;
-  read_row<D, false>(a, page, at.key & ((1 << a.s.page_shift) - 1),
+  read_row<D, 32 / kRows, false>(a, page, at.key & ((1 << a.s.page_shift) - 1),
                      static_cast<__nv_bfloat16*>(a.k_out) + elem_offset(a.sk_new, at.batch, at.row, 0), a.sk_new.head,
                      static_cast<__nv_bfloat16*>(a.v_out) + elem_offset(a.sv_new, at.batch, at.row, 0), a.sv_new.head);
 }
 
 // Reading all keys of every sequence into a cache of its own, in pages of 128 keys [page][head][slot][d], `tiles` of them
-// a sequence, and that cache's page table. A warp per key, counted on over the sequences (4 keys of a page a warp: 1 us more);
-// looking at the sequences one by one, 2048 of 256 keys took 1190 us with the attention, which now takes 278.
+// a sequence, and that cache's page table. A warp per key, or per kRows keys of few heads, counted on over the sequences;
+// looking at the sequences one by one, 2048 of 256 keys of one head, d = 64, took 1190 us with the attention, 32 at a time 278,
+// with eight keys a warp 166.
 struct Staged {
   __nv_bfloat16 *k, *v;
   int32_t* table;
   int tiles;
 };
 
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(256) paged_stage_fp8_kernel(const FaPagedArgs a, const Staged to) {
   let_dependent_start();
   grid_dependency_wait();
@@ -211,15 +233,16 @@ __global__ void __launch_bounds__(256) paged_stage_fp8_kernel(const FaPagedArgs 
     const SeqInfo seq = paged_seq(s, b);
     return seq.Lq > 0 ? seq.Lk : 0;
   };
-  // The warp's keys, counted from the first sequence of the 32 (or 256) that it looks at: a lane has one each (or eight, whose
-  // loads are in flight together, where none of the 256 may concern the warp).
-  for (int b0 = 0, j = at >> 5; b0 < s.B; b0 += 32) {
+  // A lane's keys (all the warp's, or one of its kRows), counted from the first sequence of the 32 (or 256) that the warp looks
+  // at: a lane has one each (or eight, whose loads are in flight together, where none of the 256 may concern the warp).
+  const int step = (threads >> 5) * kRows;
+  for (int b0 = 0, j = at / (32 / kRows); b0 < s.B; b0 += 32) {
     if (s.B - b0 > 64 && b0 % 256 == 0) {
       int sum = 0;
 #pragma unroll
       for (int n = 0; n < 8; ++n) sum += keys_of(b0 + 32 * n + lane);
       sum = __reduce_add_sync(0xffffffffu, sum);
-      if (j >= sum) {
+      if (__all_sync(0xffffffffu, j >= sum)) {
         j -= sum;
         b0 += 256 - 32;
         continue;
@@ -232,13 +255,23 @@ __global__ void __launch_bounds__(256) paged_stage_fp8_kernel(const FaPagedArgs 
       if (lane >= o) end += up;
     }
     const int total = __shfl_sync(0xffffffffu, end, 31);
-    for (; j < total; j += threads >> 5) {
-      const int of = __popc(__ballot_sync(0xffffffffu, end <= j)), before = __shfl_sync(0xffffffffu, end, max(of - 1, 0));
+    while (__any_sync(0xffffffffu, j < total)) {
+      int of = 0;  // sequences that end at or before j
+      if (kRows == 1) {
+        of = __popc(__ballot_sync(0xffffffffu, end <= j));
+      } else {
+#pragma unroll
+        for (int n = 16; n > 0; n >>= 1)
+          if (__shfl_sync(0xffffffffu, end, of + n - 1) <= j) of += n;
+      }
+      const int before = __shfl_sync(0xffffffffu, end, max(of - 1, 0));
+      if (j >= total) continue;
       const int b = b0 + of, key = of == 0 ? j : j - before;
+      j += step;
       const int page = paged_page(s, b, key >> s.page_shift, a.status);
       if (page < 0) continue;
       const size_t row = ((size_t)(b * to.tiles + (key >> 7)) * s.Hkv * 128 + (key & 127)) * D;
-      read_row<D, true>(a, page, key & ((1 << s.page_shift) - 1), to.k + row, 128 * D, to.v + row, 128 * D);
+      read_row<D, 32 / kRows, true>(a, page, key & ((1 << s.page_shift) - 1), to.k + row, 128 * D, to.v + row, 128 * D);
     }
     j -= total;
   }
@@ -288,24 +321,47 @@ int apart_tokens(const PagedShape& s) {
   return G <= 16 ? 16 / G : 1;
 }
 
-unsigned row_blocks(const PagedShape& s) {  // a warp per row
-  const long long rows = s.cu_q != nullptr ? s.rows_q : (long long)s.B * s.Nq;
-  return (unsigned)((rows * 32 + kRowThreads - 1) / kRowThreads);
+// Appending (16 values a lane) or reading, a warp per kRows rows.
+template <int D, int kRows, bool kAppend>
+cudaError_t launch_rows(const FaPagedArgs& a, cudaStream_t st) {
+  const long long rows = a.s.cu_q != nullptr ? a.s.rows_q : (long long)a.s.B * a.s.Nq, warps = (rows + kRows - 1) / kRows;
+  const dim3 grid((unsigned)((warps * 32 + kRowThreads - 1) / kRowThreads)), block(kRowThreads);
+  if constexpr (kAppend) return launch_dependent(paged_append_fp8_kernel<D, kRows>, grid, block, 0, st, a);
+  else return launch_dependent(paged_read_fp8_kernel<D, kRows>, grid, block, 0, st, a);
+}
+
+template <int D, bool kAppend>
+cudaError_t launch_rows(const FaPagedArgs& a, cudaStream_t st) {
+  const long long rows = a.s.cu_q != nullptr ? a.s.rows_q : (long long)a.s.B * a.s.Nq;
+  switch (rows_per_warp(a.s, rows)) {
+    case 8:
+      if constexpr (!kAppend || D == 64) return launch_rows<D, 8, kAppend>(a, st);  // (two lanes have no row of 128 to append)
+    case 4: return launch_rows<D, 4, kAppend>(a, st);
+    case 2: return launch_rows<D, 2, kAppend>(a, st);
+    default: return launch_rows<D, 1, kAppend>(a, st);
+  }
+}
+
+template <int D>
+cudaError_t launch_stage(const FaPagedArgs& a, const Staged& to, cudaStream_t st) {
+  const dim3 grid(a.num_sms * 8), block(256);
+  switch (rows_per_warp(a.s, (long long)a.s.B * a.s.max_k)) {
+    case 8: return launch_dependent(paged_stage_fp8_kernel<D, 8>, grid, block, 0, st, a, to);
+    case 4: return launch_dependent(paged_stage_fp8_kernel<D, 4>, grid, block, 0, st, a, to);
+    case 2: return launch_dependent(paged_stage_fp8_kernel<D, 2>, grid, block, 0, st, a, to);
+    default: return launch_dependent(paged_stage_fp8_kernel<D, 1>, grid, block, 0, st, a, to);
+  }
 }
 
 }  // namespace
 }  // namespace fa
 
 cudaError_t fa_launch_paged_append_fp8(const FaPagedArgs& a, cudaStream_t st) {
-  const dim3 grid(fa::row_blocks(a.s)), block(fa::kRowThreads);
-  return a.s.d == 64 ? launch_dependent(fa::paged_append_fp8_kernel<64>, grid, block, 0, st, a)
-                     : launch_dependent(fa::paged_append_fp8_kernel<128>, grid, block, 0, st, a);
+  return a.s.d == 64 ? fa::launch_rows<64, true>(a, st) : fa::launch_rows<128, true>(a, st);
 }
 
 cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st) {
-  const dim3 grid(fa::row_blocks(a.s)), block(fa::kRowThreads);
-  return a.s.d == 64 ? launch_dependent(fa::paged_read_fp8_kernel<64>, grid, block, 0, st, a)
-                     : launch_dependent(fa::paged_read_fp8_kernel<128>, grid, block, 0, st, a);
+  return a.s.d == 64 ? fa::launch_rows<64, false>(a, st) : fa::launch_rows<128, false>(a, st);
 }
 
 size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms) {
@@ -346,9 +402,7 @@ cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st) {
       x.o = static_cast<__nv_bfloat16*>(a.o) + (size_t)b * a.so.batch;
       x.lse += (size_t)b * s.H * s.Nq;
     }
-    const dim3 grid(a.num_sms * 8), block(256);
-    cudaError_t e = s.d == 64 ? launch_dependent(fa::paged_stage_fp8_kernel<64>, grid, block, 0, st, x, to)
-                              : launch_dependent(fa::paged_stage_fp8_kernel<128>, grid, block, 0, st, x, to);
+    cudaError_t e = s.d == 64 ? fa::launch_stage<64>(x, to, st) : fa::launch_stage<128>(x, to, st);
     if (e != cudaSuccess) return e;
     x.s = fa::staged_shape(x.s, group, plan.tiles);
     x.s.table = to.table;

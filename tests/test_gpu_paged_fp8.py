@@ -177,6 +177,46 @@ def test_read(packed, heads):
     assert np.array_equal(p.np(k), bf(wk), equal_nan=True) and np.array_equal(p.np(v), bf(wv), equal_nan=True)
 
 
+@pytest.mark.parametrize("heads", [(1, 1, 64), (1, 1, 128), (2, 2, 64), (2, 2, 128), (3, 3, 64), (4, 4, 128), (6, 6, 64)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_many_rows_of_few_heads(packed, heads):
+    """Rows enough that a warp moves several: sequences of none to a few tokens, some with fewer keys than new tokens, one
+    whose new tokens lie on no page of the cache."""
+    r = np.random.default_rng(heads[2] + heads[0] + packed)
+    B = 3001 if packed else 701
+    lq = np.minimum(r.integers(0, 8, B) * (r.random(B) < 0.9), 6) if packed else np.full(B, 3)
+    lq[-3:] = (9, 0, 2) if packed else 3
+    assert lq.sum() > (8192 if packed else 2048)
+    lk = lq + r.integers(0, 12, B) - (r.random(B) < 0.05)
+    p = Problem8(np.maximum(lk, 0).tolist(), lq.tolist(), *heads, page=8, packed=packed, seed=12)
+    lost = int(np.flatnonzero((lk > 8) & (lq > 0) & (lk - lq >= 8))[0])  # (its new tokens are all on its second page)
+    p.ctable[lost, 1] = 1 << 20
+    ky, vy, codes = p.ky.copy(), p.vy.copy(), p.codes.copy()
+    new = p.np(p.k_new), p.np(p.v_new)
+    cu = p.cu
+    gone = {(lost, i) if cu is None else (int(cu[lost]) + i,) for i in range(int(lq[lost]))}
+    keep = [x for x in p8.places(p.table.numpy(), p.lk, int(lq[0]), 8, cu) if x[0] not in gone]
+    at = tuple(np.array([x[0] for x in keep]).T)
+    page, slot = np.array([x[1] for x in keep]), np.array([x[2] for x in keep])
+    for x, cache, which in ((new[0], ky, 0), (new[1], vy, 1)):
+        cache[page, slot], c = p8.quantise(x[at])
+        codes[page, :, slot, which] = c
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fa.paged_append_fp8(p.k_new.cuda(), p.v_new.cuda(), *p.cache, status=status, **p.tokens)
+    assert int(status.item()) == -6
+    for got, want in ((raw(p.ck), ky), (raw(p.cv), vy)):
+        assert np.array_equal(p8.TABLE[got], p8.TABLE[want], equal_nan=True)
+    assert np.array_equal(p.ccodes.cpu().numpy(), codes)
+    k, v = torch.full_like(p.k_new, 7.0).cuda(), torch.full_like(p.v_new, 7.0).cuda()
+    wk, wv = p.np(k), p.np(v)
+    for w, y, which in ((wk, ky, 0), (wv, vy, 1)):
+        w[at] = p8.cache_values(y, codes, which)[page, slot]
+    status.zero_()
+    fa.paged_read_fp8(k, v, *p.cache, status=status, **p.tokens)
+    assert int(status.item()) == -6
+    assert np.array_equal(p.np(k), wk) and np.array_equal(p.np(v), wv)
+
+
 def test_rows_without_a_place_are_reported():
     """More new tokens than keys, and keys past the table: those rows are left on both ways, the others move."""
     p = Problem8([3, 60], [5, 5], 2, 2, 64, page=16, seed=10)
@@ -255,14 +295,15 @@ def test_attend_many_sequences(B):
         p.check_attend(*p.attend(True, num_sms=sms), True)
 
 
-@pytest.mark.parametrize("B", [31, 64, 65, 96, 256, 321, 600])
-def test_read_back_of_many_sequences(B):
+@pytest.mark.parametrize("B,heads", [(B, (65, 1, 64)) for B in (31, 64, 65, 96, 256, 321, 600)]
+                         + [(97, (65, 1, 128)), (97, (130, 2, 128)), (70, (330, 5, 64))])
+def test_read_back_of_many_sequences(B, heads):
     """More sequences than a warp that reads keys back looks at in a step, many of them empty or without new tokens."""
     r = np.random.default_rng(B)
     for packed in (False, True):
         lk = r.integers(0, 140, B) * (r.random(B) < 0.4)
         lq = r.integers(1, 3, B) * (r.random(B) < 0.5) if packed else np.ones(B, dtype=int)
-        p = Problem8(lk.tolist(), lq.tolist(), 65, 1, 64, page=32, packed=packed, seed=14)
+        p = Problem8(lk.tolist(), lq.tolist(), *heads, page=32, packed=packed, seed=14)
         for sms in (1, 152):
             p.check_attend(*p.attend(True, num_sms=sms), True)
 
