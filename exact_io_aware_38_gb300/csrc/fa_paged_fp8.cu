@@ -310,15 +310,21 @@ StagePlan stage_plan(const PagedShape& s, int num_sms) {
 }
 
 // A packed batch whose sequences are of different lengths may hold prompts beside single tokens, and a token's keys are not
-// read back for it alone: sequences of up to four units of 16 rows go to the few-row kernel. The tokens of such a unit, 0 where
-// all sequences go one way. What the host knows is the sum of the new tokens' lengths, and bounds. The further launches take
-// 15 to 20 us, which few or short sequences do not give back: 6 sequences up to 6001 keys, two of them of one token,
+// read back for it alone: sequences of up to four units of 16 rows (of more than 64 heads of a K/V head: as many as go this
+// way alone) go to the few-row kernel. What the host knows is the sum of the new tokens' lengths, and bounds. The further launches
+// take 15 to 20 us, which few or short sequences do not give back: 6 sequences up to 6001 keys, two of them of one token,
 // 163 us apart and 156 together, 12 up to 4000 of 12 heads, d = 64, 131 and 132; 33 up to 8000 606 and 679.
-int apart_tokens(const PagedShape& s) {
+struct Apart {
+  int unit, most;  // tokens of a unit, and of a sequence that goes this way: 0 where all sequences go one way
+};
+
+Apart apart_tokens(const PagedShape& s) {
   const int G = s.H / s.Hkv;
-  if (s.cu_q == nullptr || G > 64 || s.rows_q * 4ll > 3ll * s.B * s.Nq) return 0;
-  if ((double)s.B * s.max_k * s.Hkv * s.d < (double)(1 << 26)) return 0;
-  return G <= 16 ? 16 / G : 1;
+  if (s.cu_q == nullptr || G > 256 || s.rows_q * 4ll > 3ll * s.B * s.Nq) return {};
+  if ((double)s.B * s.max_k * s.Hkv * s.d < (double)(1 << 26)) return {};
+  if (G > 64) return {1, 4 / ((G + 63) / 64)};
+  const int unit = G <= 16 ? 16 / G : 1;
+  return {unit, 4 * unit};
 }
 
 // Appending (16 values a lane) or reading, a warp per kRows rows.
@@ -366,20 +372,20 @@ cudaError_t fa_launch_paged_read_fp8(const FaPagedArgs& a, cudaStream_t st) {
 
 size_t fa_paged_fp8_workspace(const fa::PagedShape& s, int num_sms) {
   if (const int tokens = fa_paged_few8_tokens(s)) return fa_paged_few8_workspace(s, tokens, num_sms);
-  const int apart = fa::apart_tokens(s);
-  const size_t few = apart > 0 ? fa_paged_few8_workspace(s, apart, num_sms) : 0, staged = fa::stage_plan(s, num_sms).bytes();
+  const fa::Apart apart = fa::apart_tokens(s);
+  const size_t few = apart.most > 0 ? fa_paged_few8_workspace(s, apart.unit, num_sms) : 0, staged = fa::stage_plan(s, num_sms).bytes();
   return few > staged ? few : staged;
 }
 
 cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st) {
   if (const int tokens = fa_paged_few8_tokens(a.s)) return fa_launch_paged_few8(a, tokens, st);
   fa::PagedShape s = a.s;
-  if (const int tokens = fa::apart_tokens(s)) {
+  if (const fa::Apart apart = fa::apart_tokens(s); apart.most > 0) {
     FaPagedArgs x = a;
-    x.s.max_q = 4 * tokens;
-    const cudaError_t e = fa_launch_paged_few8(x, tokens, st);
+    x.s.max_q = apart.most;
+    const cudaError_t e = fa_launch_paged_few8(x, apart.unit, st);
     if (e != cudaSuccess) return e;
-    s.min_q = 4 * tokens + 1;
+    s.min_q = apart.most + 1;
   }
   const fa::StagePlan plan = fa::stage_plan(s, a.num_sms);
   char* ws = static_cast<char*>(a.workspace);

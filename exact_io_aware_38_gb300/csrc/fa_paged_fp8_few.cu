@@ -20,8 +20,10 @@
 // The exponentials are taken against a reference per row that starts 2^7 below the first tile's largest and is raised
 // (O and the row sums rescaled) only when a score exceeds it by more than 2^15.
 //
-// Rows: up to 64 (tokens x heads of a K/V head) are one unit of 16, 32 or 64 columns; more are units of 64 that each
-// read the keys, mostly from L2. Division of the work, pieces, clusters and joins as in fa_paged_decode.cu.
+// Rows: up to 64 (tokens x heads of a K/V head) are one unit of 8, 16, 32 or 64 columns; more are up to four units that each
+// read the keys, mostly from L2: of more tokens, or of a token's heads where there are more than 64 (64 x 4096 keys of one head,
+// d = 128, with 128 heads on it: 54 us, 84 read back to bf16; 65 heads 51 and 1539). Division of the work, pieces,
+// clusters and joins as in fa_paged_decode.cu.
 //
 // Roles: warp 0 copies keys and codes (TMA, a lane per page; the codes by 8-byte asynchronous copies, four keys a lane), warp 1
 // issues S, groups of four warps are the softmax and the epilogue, of 16 rows each, the warp before the last issues P V, and
@@ -86,23 +88,28 @@ constexpr int kF8Open = 3;
 // turn, and the line of units that the CTAs of one residue divide has a turn where it would have a head. So `side` CTAs walk
 // over the same keys of neighbouring heads at about the same time, and what lies next to one another in memory is
 // fetched at about the same time.
+// A unit has `tokens` tokens of all heads of a K/V head, or, of more than 64 heads, one token of one of `parts` parts of them
+// (a kernel of its own: these divisions alone cost the others 1 to 10%).
 struct F8Cut {
-  int tokens;  // of a unit
+  int tokens;               // of a unit
+  int heads, group, parts;  // of a K/V head, of a unit; units of a token
   int side, turns;
 };
 
+template <bool kParts>  // more than one unit of a token
 struct F8Units {
   int heads, count, open;
   SeqInfo q;
   F8Units() = default;
   __device__ F8Units(const PagedShape& s, const F8Cut& c, int b) : heads(c.turns), open(kF8Open), q(paged_seq(s, b)) {
     count = q.Lq <= c.tokens ? q.Lq > 0 : (q.Lq + c.tokens - 1) / c.tokens;
+    if (kParts) count *= c.parts;
   }
   __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
   __device__ long long before(int u) const { return (long long)u * (tiles() + open); }
 };
 
-template <int D, int NP>
+template <int D, int NP, bool kParts>
 struct F8Ctl {
   uint64_t q_raw[2], q_full[2], q_empty[2];
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // (k_full: codes too; v_empty: also that P V has completed)
@@ -113,7 +120,7 @@ struct F8Ctl {
   int abort_flag;
   long long scan[F8Cfg<D, NP>::kThreads / 32];  // an entry per warp
   Share share;
-  F8Units units;             // of the sequence where the share begins
+  F8Units<kParts> units;     // of the sequence where the share begins
   int issued_k, issued_v;    // copies issued (abort-path drain)
   alignas(16) uint8_t codes[kCodeStages][256];  // key and value of each slot
   alignas(16) float qmul[2][NP];      // by buffer of Q: c log2 e times the row's power of two
@@ -125,6 +132,7 @@ struct F8Ctl {
 };
 
 // The pieces of a CTA's share: key tiles [kt, end) of the n of (b, hk, u), walked in order by every role.
+template <bool kParts>
 struct F8Pieces {
   const PagedShape& s;
   const F8Cut& cut;
@@ -132,14 +140,14 @@ struct F8Pieces {
   long long todo;  // positions from the piece on
   bool finished;
   SeqInfo seq;
-  __device__ F8Pieces(const PagedShape& s_, const F8Cut& cut_, const Share& sh, const F8Units& first, int beside)
+  __device__ F8Pieces(const PagedShape& s_, const F8Cut& cut_, const Share& sh, const F8Units<kParts>& first, int beside)
       : s(s_), cut(cut_), b(sh.b), hk(sh.head * cut.side + beside), u(sh.unit), kt(0), n(0), end(0), count(0), todo(sh.todo),
         finished(false) {
     if (todo == 0) return;
     sequence(first);
     open(sh.tile);
   }
-  __device__ void sequence(const F8Units& x) {
+  __device__ void sequence(const F8Units<kParts>& x) {
     seq = x.q;
     count = x.count;
     n = count ? x.tiles() : 0;
@@ -154,8 +162,12 @@ struct F8Pieces {
   __device__ bool done() const { return finished || n == 0; }
   __device__ bool whole() const { return kt == 0 && end == n; }
   __device__ bool more() const { return todo > kF8Open; }  // another piece follows
-  __device__ int token() const { return u * cut.tokens; }  // the unit's first
-  __device__ int tokens() const { return min(cut.tokens, seq.Lq - u * cut.tokens); }
+  // The unit's first token and head, and its rows.
+  __device__ int token() const { return kParts ? u / cut.parts : u * cut.tokens; }
+  __device__ int head() const { return kParts ? hk * cut.heads + u % cut.parts * cut.group : hk * cut.group; }
+  __device__ int rows() const {
+    return kParts ? min(cut.group, (hk + 1) * cut.heads - head()) : min(cut.tokens, seq.Lq - token()) * cut.group;
+  }
   __device__ void next() {
     if (todo == 0) {
       finished = true;
@@ -168,7 +180,7 @@ struct F8Pieces {
         hk -= s.Hkv;
         do {  // todo > 0: a later sequence has new tokens
           ++b;
-          sequence(F8Units(s, cut, b));
+          sequence(F8Units<kParts>(s, cut, b));
         } while (n == 0);
       }
     }
@@ -179,8 +191,8 @@ struct F8Pieces {
 struct F8Work {
   float* part_o;    // [2 CTAs][NP][D]
   float* part_lse;  // [2 CTAs][NP], log2 units
-  int4* desc;       // [CTAs][2]: {b, hk, first CTA, its slot}, {rows, q0, bb, first token} of the unit; b = -1: none ends
-                    // here in pieces. Null: every unit has a CTA or a cluster of its own
+  int4* desc;       // [CTAs][2]: {b, first head, first CTA, its slot}, {rows, q0, bb, first token} of the unit; b = -1: none
+                    // ends here in pieces. Null: every unit has a CTA or a cluster of its own
   F8Cut cut;
   FastDiv by_group;  // rows to tokens
 };
@@ -272,20 +284,20 @@ __device__ __forceinline__ void split_rows(uint32_t q, float* qmul, int first, f
   }
 }
 
-template <int D, int NP>
+template <int D, int NP, bool kParts>
 __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     paged_few8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const F8Args a, const F8Work wk) {
   using C = F8Cfg<D, NP>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) F8Ctl<D, NP> ctl;
+  __shared__ __align__(16) F8Ctl<D, NP, kParts> ctl;
   const uint32_t sK0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sV0 = sK0 + C::kKStages * C::kTileBytes, sP = sV0 + C::kVStages * C::kTileBytes;
   const uint32_t sQ = sP + C::kPBytes;
   float* my_part = reinterpret_cast<float*>(smem_raw + (sK0 - smem_u32(smem_raw)));
   volatile int* abort_flag = &ctl.abort_flag;
   const PagedShape& s = a.s;
-  const int G = s.H / s.Hkv;
+  const int G = wk.cut.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto sV = [&](int i) { return sV0 + i * C::kTileBytes; };
   auto bar = [&](uint64_t& x) { return smem_u32(&x); };
@@ -324,11 +336,11 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
   const int beside = blockIdx.x % wk.cut.side, group = blockIdx.x / wk.cut.side, groups = gridDim.x / wk.cut.side;
   const int me = beside * groups + group;
   if (wk.desc != nullptr) {
-    find_share<C::kThreads>(s.B, [&](int b) { return F8Units(s, wk.cut, b); }, ctl.share, ctl.scan, ctl.units, group,
+    find_share<C::kThreads>(s.B, [&](int b) { return F8Units<kParts>(s, wk.cut, b); }, ctl.share, ctl.scan, ctl.units, group,
                             groups);
   } else if (threadIdx.x == 0) {  // tiles [n rank / ctas, n (rank + 1) / ctas) of the cluster's unit
     const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv;
-    const F8Units x(s, wk.cut, b);
+    const F8Units<kParts> x(s, wk.cut, b);
     const int n = x.count ? x.tiles() : 0, lo = n * rank / ctas, hi = n * (rank + 1) / ctas;
     ctl.share = Share{b, unit - b * s.Hkv, 0, kF8Open + lo, hi - lo, 0, 0};
     ctl.units = x;
@@ -337,12 +349,12 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
-  F8Pieces w(s, wk.cut, ctl.share, ctl.units, beside);
+  F8Pieces<kParts> w(s, wk.cut, ctl.share, ctl.units, beside);
   if (wk.desc != nullptr && threadIdx.x == 0) {
     const bool joins = !w.done() && w.kt > 0 && w.end == w.n;
-    wk.desc[2 * me] = make_int4(joins ? w.b : -1, w.hk, ctl.share.first_cta + me - group,
+    wk.desc[2 * me] = make_int4(joins ? w.b : -1, w.head(), ctl.share.first_cta + me - group,
                                 ctl.share.first_slot + 2 * (me - group));
-    wk.desc[2 * me + 1] = make_int4(joins ? w.tokens() * G : 0, w.seq.q0, w.seq.bb, w.token());
+    wk.desc[2 * me + 1] = make_int4(joins ? w.rows() : 0, w.seq.q0, w.seq.bb, w.token());
   }
 
   constexpr int kLast = C::kThreads / 32 - 1;
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     const uint32_t tile0 = values ? sV0 : sK0;
     const CUtensorMap* tm = values ? &tmV : &tmK;
     bool run = true;
-    F8Pieces x = w;  // of the next copy
+    F8Pieces<kParts> x = w;  // of the next copy
     int xkt = x.kt, xt = 0, xst = 0;
     uint32_t xphase = 1;
     // The page of the next copy that is this lane's, as the table has it: it is looked at when the copy is made, so that
@@ -417,7 +429,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       // behind each copy, more by the softmax warps: 32 rows in this loop take 8000 cycles.
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
       const int r0 = lane / kLanes, part = lane % kLanes;
-      F8Pieces y = w;
+      F8Pieces<kParts> y = w;
       int piece = 0, at = -1;  // of y; the next row, -1: none has been asked for
       auto step_q = [&]() {
         const int qb = piece & 1;
@@ -425,9 +437,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         if (at < 0) {
           if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
           run = __all_sync(0xffffffffu, run) && !*abort_flag;
-          const int live = y.tokens() * G;
+          const int live = y.rows();
           const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                   elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.hk * G) + part * 8;
+                                   elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.head()) + part * 8;
           if (run)
 #pragma unroll 2
             for (int n = r0; n < NP; n += kPer) {  // (rows that do not exist become zeros)
@@ -564,7 +576,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     int split = 0;  // pieces whose Q is
     for (int piece = 0; !w.done(); ++piece) {
       const SeqInfo& seq = w.seq;
-      const int live = w.tokens() * G, tok = w.token(), qb = piece & 1;
+      const int live = w.rows(), tok = w.token(), head = w.head(), qb = piece & 1;
       if (r < NC) ctl.lim[n0 + r] = s.causal ? min(seq.Lk, tok + wk.by_group.div(n0 + r) + seq.off + 1) : seq.Lk;  // keys [0, lim) visible
       const int least = s.causal ? min(seq.Lk, tok + seq.off + 1) : seq.Lk;
       float l[NC];
@@ -747,14 +759,14 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         const float sum = total(n), lse2 = sum == 0.f ? -INFINITY : ctl.ref[n] + log2f(sum);
         if (whole) {
           const int i = wk.by_group.div(n);
-          if (n < live) a.lse[paged_row(s, seq, w.b, w.hk * G + n - i * G, tok + i)] = lse2 * kLn2;
+          if (n < live) a.lse[paged_row(s, seq, w.b, head + n - i * G, tok + i)] = lse2 * kLn2;
         } else {
           (ctas > 1 ? ctl.part_lse : wk.part_lse + (size_t)slot * NP)[n] = lse2;
         }
       }
       if (run) run = wait_pv(t - 1);
       fence_after_sync();
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + tok, w.hk * G) + r;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + elem_offset(a.so, seq.bb, seq.q0 + tok, head) + r;
       // (the cluster's parts lie over the ring: with the last P V done nothing reads it or is on its way there)
       float* part = (ctas > 1 ? my_part : wk.part_o + (size_t)slot * NP * D) + r;
       int i = wk.by_group.div(n0), g = n0 - i * G;  // token and head of the group of column n
@@ -849,16 +861,20 @@ __global__ void __launch_bounds__(4 * D) paged_few8_join_kernel(const FaPagedArg
   grid_dependency_wait();
   const int4 d = wk.desc[2 * blockIdx.x], of = wk.desc[2 * blockIdx.x + 1];
   const PagedShape& s = a.s;
-  const int G = s.H / s.Hkv, n = blockIdx.y * 16 + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4;
+  const int G = wk.cut.group, n = blockIdx.y * 16 + threadIdx.x / (D / 4), e = threadIdx.x % (D / 4) * 4;
   if (d.x < 0 || n >= of.x) return;
   SeqInfo seq{};
   seq.q0 = of.y;
   seq.bb = of.z;
-  join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, blockIdx.x, d.w, n, e, seq, d.x, of.w + n / G, d.y * G + n % G);
+  join_pieces<D, NP>(a, wk.part_o, wk.part_lse, d.z, blockIdx.x, d.w, n, e, seq, d.x, of.w + n / G, d.y + n % G);
 }
 
+// Units of a token, 1 unless a K/V head has more than 64 heads: then parts of them as equal as may be, of 33 heads or more.
+int token_units(const PagedShape& s) { return (s.H / s.Hkv + 63) / 64; }
+int unit_heads(const PagedShape& s) { return (s.H / s.Hkv + token_units(s) - 1) / token_units(s); }
+
 int unit_rows(const PagedShape& s, int tokens) {
-  const int rows = tokens * (s.H / s.Hkv);
+  const int rows = tokens * unit_heads(s);
   return rows <= 8 ? 8 : padded_rows(rows);
 }
 
@@ -866,7 +882,7 @@ int unit_rows(const PagedShape& s, int tokens) {
 F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
   int side = s.Hkv;
   while (side > 1 && (s.Hkv % side != 0 || ctas / side * side * 100ll < 97ll * ctas)) --side;
-  return {tokens, side, s.Hkv / side};
+  return {tokens, s.H / s.Hkv, unit_heads(s), token_units(s), side, s.Hkv / side};
 }
 
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0: the rule of fa_paged_decode.cu with
@@ -874,7 +890,7 @@ F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
 // 13.9 us, divided 14.7; one of 8000 12.5 and 13.3; 4 of 4000 12.7 and 12.4; with 16 tiles 8 of 8000 21.3 and 19.6) or 16 of one
 // alone (24 of 12 heads, d = 64, 2000 keys: 16.1 and 20.0).
 int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
-  if (tokens < s.Nq) return 0;
+  if (tokens < s.Nq || token_units(s) > 1) return 0;
   const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s, tokens));
   const int tiles = (s.max_k + 127) >> 7;
   int ctas = 1;
@@ -889,7 +905,7 @@ int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
   return units * ctas <= room && tiles <= (ctas == 1 ? 16 : 8 * ctas) ? ctas : 0;
 }
 
-template <int D, int NP>
+template <int D, int NP, bool kParts = false>
 cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
   using C = F8Cfg<D, NP>;
   const PagedShape& s = a.s;
@@ -904,8 +920,8 @@ cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
   const int shared = unit_ctas(s, tokens, a.num_sms);
   int ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;
   F8Work wk{};
-  wk.cut = {tokens, 1, s.Hkv};
-  wk.by_group = fast_div(s.H / s.Hkv);
+  wk.cut = {tokens, s.H / s.Hkv, unit_heads(s), token_units(s), 1, s.Hkv};
+  wk.by_group = fast_div(unit_heads(s));
   if (shared == 0) {
     wk.cut = cut_of(s, tokens, ctas);
     ctas = ctas / wk.cut.side * wk.cut.side;
@@ -917,7 +933,7 @@ cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
     wk.part_o = reinterpret_cast<float*>(ws);
   }
   const F8Args x{s, a.q, a.codes, a.o, a.lse, a.sq, a.so, a.scale, a.status};
-  auto kern = paged_few8_kernel<D, NP>;
+  auto kern = paged_few8_kernel<D, NP, kParts>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   if (C::kCtas > 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -931,10 +947,11 @@ cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
 }  // namespace
 }  // namespace fa
 
-// Up to four units of 64 rows; more rows, or a group of heads that no unit holds, go by way of the chunk kernel.
+// Up to four units of 64 rows; more go by way of the chunk kernel.
 int fa_paged_few8_tokens(const fa::PagedShape& s) {
   const int G = s.H / s.Hkv;
-  if (G > 64 || (long long)s.Nq > 4ll * (64 / G)) return 0;
+  if (G > 64) return (long long)s.Nq * fa::token_units(s) <= 4 ? 1 : 0;
+  if (s.Nq > 4 * (64 / G)) return 0;
   return (long long)s.Nq * G <= 64 ? s.Nq : 64 / G;
 }
 
@@ -953,7 +970,7 @@ cudaError_t launch_rows(const FaPagedArgs& a, int tokens, cudaStream_t st) {
     case 8: return launch_few8<D, 8>(a, tokens, st);
     case 16: return launch_few8<D, 16>(a, tokens, st);
     case 32: return launch_few8<D, 32>(a, tokens, st);
-    default: return launch_few8<D, 64>(a, tokens, st);
+    default: return token_units(a.s) > 1 ? launch_few8<D, 64, true>(a, tokens, st) : launch_few8<D, 64>(a, tokens, st);
   }
 }
 }  // namespace

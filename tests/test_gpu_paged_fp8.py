@@ -302,7 +302,8 @@ def test_read_back_of_many_sequences(B, heads):
     r = np.random.default_rng(B)
     for packed in (False, True):
         lk = r.integers(0, 140, B) * (r.random(B) < 0.4)
-        lq = r.integers(1, 3, B) * (r.random(B) < 0.5) if packed else np.ones(B, dtype=int)
+        lq = r.integers(1, 4, B) * (r.random(B) < 0.5) if packed else np.full(B, 3)
+        lq[B // 2] = 3
         p = Problem8(lk.tolist(), lq.tolist(), *heads, page=32, packed=packed, seed=14)
         for sms in (1, 152):
             p.check_attend(*p.attend(True, num_sms=sms), True)
@@ -328,6 +329,19 @@ def test_attend_strided_cache_and_rows(d, layout, n):
 def test_many_heads_per_kv_head(heads, n):
     p = Problem8([300, 77], [n, n], *heads, page=32, seed=14)
     p.check_attend(*p.attend(True), True)
+
+
+@pytest.mark.parametrize("n,heads", [(1, (142, 2, 128)), (2, (142, 2, 64)), (2, (128, 1, 128)), (1, (256, 1, 64)), (1, (257, 1, 64)),
+                                     (1, (390, 3, 64)), (2, (65, 1, 128))])
+@pytest.mark.parametrize("sms", [1, 5, 152])
+def test_parts_of_a_group_of_heads(n, heads, sms):
+    """More than 64 heads on a K/V head: units of some of them, whole and divided, rows of other units left alone."""
+    for packed in (False, True):
+        p = Problem8([1111, 250, 0, 129], [n, 1, 0, n] if packed else [n] * 4, *heads, page=32, packed=packed, seed=n)
+        out = torch.full_like(p.cq, 3.0)
+        p.check_attend(*p.attend(True, num_sms=sms, out=out), True)
+        if packed:
+            assert (out[int(p.cu[-1]):] == 3.0).all()
 
 
 def test_page_sizes_at_both_ends():
@@ -535,12 +549,12 @@ def test_chunks_in_rounds_through_one_workspace():
         p.check_attend(*p.attend(True), True)
 
 
-@pytest.mark.parametrize("heads", [(8, 2, 128), (20, 1, 128), (5, 5, 64)])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (20, 1, 128), (5, 5, 64), (96, 1, 64), (130, 1, 64), (142, 2, 128)])
 def test_prompts_beside_single_tokens(heads):
     """A packed batch in which two kernels share the sequences by their new tokens: none, one, at the limit between them,
     one past it, and prompts; a bound on the keys that makes the batch look large."""
     G = heads[0] // heads[1]
-    limit = 4 * (16 // G if G <= 16 else 1)
+    limit = 4 * (16 // G if G <= 16 else 1) if G <= 64 else 4 // -(-G // 64)
     lq = [1, 300, 0, limit, limit + 1, 1, limit - 1, 90, 2, 0, 1]
     lk = [700, 300, 50, 129, 260, 0, 40, 500, 128, 0, 1]
     p = Problem8(lk, lq, *heads, page=16, seed=34, packed=True)
