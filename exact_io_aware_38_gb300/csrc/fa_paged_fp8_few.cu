@@ -420,70 +420,69 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       }
       if (!x.done()) listed = look_up();
     };
-    if (!values) {
-      while (!x.done()) copy();
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-      // Q of a piece is asked for while the one before it runs, once the buffer's last piece is sure to be over (or, in a short
-      // piece, behind its last copy). Its rows arrive where their parts will lie, all at once, and up to 16 are split here, a few
-      // behind each copy, more by the softmax warps: 32 rows in this loop take 8000 cycles.
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-      const int r0 = lane / kLanes, part = lane % kLanes;
-      F8Pieces<kParts> y = w;
-      int piece = 0, at = -1;  // of y; the next row, -1: none has been asked for
-      auto step_q = [&]() {
-        const int qb = piece & 1;
-        const uint32_t to = sQ + qb * C::kQBytes;
-        if (at < 0) {
-          if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
-          run = __all_sync(0xffffffffu, run) && !*abort_flag;
-          const int live = y.rows();
-          const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                   elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.head()) + part * 8;
-          if (run)
+    // Q of a piece is asked for while the one before it runs, once the buffer's last piece is sure to be over (or, in a short
+    // piece, behind its last copy). Its rows arrive where their parts will lie, all at once, and up to 16 are split here, a few
+    // behind each copy, more by the softmax warps: 32 rows in this loop take 8000 cycles.
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
+    const int r0 = lane / kLanes, part = lane % kLanes;
+    F8Pieces<kParts> y = w;
+    int piece = 0, at = -1;  // of y; the next row, -1: none has been asked for
+    auto step_q = [&]() {
+      const int qb = piece & 1;
+      const uint32_t to = sQ + qb * C::kQBytes;
+      if (at < 0) {
+        if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+        run = __all_sync(0xffffffffu, run) && !*abort_flag;
+        const int live = y.rows();
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                 elem_offset(a.sq, y.seq.bb, y.seq.q0 + y.token(), y.head()) + part * 8;
+        if (run)
 #pragma unroll 2
-            for (int n = r0; n < NP; n += kPer) {  // (rows that do not exist become zeros)
-              const int i = n < live ? wk.by_group.div(n) : 0, g = n < live ? n - i * G : 0;
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_q<D, NP>(to, n, part)),
-                           "l"(q + (size_t)i * a.sq.row + (size_t)g * a.sq.head), "r"(n < live ? 16 : 0)
-                           : "memory");
-            }
-          at = 0;
-          if constexpr (!C::kSoftSplit) return;
-          if (run)
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.q_raw[qb])) : "memory");
-        } else {
-          if (at == 0) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
+          for (int n = r0; n < NP; n += kPer) {  // (rows that do not exist become zeros)
+            const int i = n < live ? wk.by_group.div(n) : 0, g = n < live ? n - i * G : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_q<D, NP>(to, n, part)),
+                         "l"(q + (size_t)i * a.sq.row + (size_t)g * a.sq.head), "r"(n < live ? 16 : 0)
+                         : "memory");
           }
-          split_rows<D, NP, 2>(to, ctl.qmul[qb], at, a.scale * kLog2e, run);
-          at += 2 * kPer;
-          if (at < NP) return;
-          fence_proxy_async_smem();
+        at = 0;
+        if constexpr (!C::kSoftSplit) return;
+        if (run)
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.q_raw[qb])) : "memory");
+      } else {
+        if (at == 0) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
-          if (run && lane == 0) mbar_arrive(bar(ctl.q_full[qb]));
         }
-        at = -1;
-        ++piece;
-        y.next();
-      };
-      if (!y.done()) step_q();
-      for (int of = 0, copied = 0; !x.done();) {  // the piece of the copies, its tiles so far
-        copy();
-        ++copied;
-        const bool ended = x.done() || xkt == x.kt;
-        const int due = ended ? of + 1 : of;  // pieces whose Q has to be there (or asked for) now
-        int more = copied > C::kVStages;
+        split_rows<D, NP, 2>(to, ctl.qmul[qb], at, a.scale * kLog2e, run);
+        at += 2 * kPer;
+        if (at < NP) return;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (run && lane == 0) mbar_arrive(bar(ctl.q_full[qb]));
+      }
+      at = -1;
+      ++piece;
+      y.next();
+    };
+    // (One loop for both warps, and one place for a step: what they share is fetched once.)
+    bool ended = true;
+    int of = -1, copied = 0, due = -1, more = 1;  // the piece of the copies, its tiles so far; the last whose Q has to be there
+    for (;;) {
+      if (values)
 #pragma unroll 1
         while (!y.done() && (piece <= due || (piece == of + 1 && more-- > 0))) step_q();
-        if (ended) {
-          ++of;
-          copied = 0;
-        }
+      if (x.done()) break;
+      if (ended) {
+        ++of;
+        copied = 0;
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      copy();
+      ++copied;
+      ended = x.done() || xkt == x.kt;
+      due = ended ? of + 1 : of;
+      more = copied > C::kVStages;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1 || warp == kLast - 1) {
     // ------------------------------------------------------------------ MMAs: S; P V
     // (Their waits suspend: polling takes issue slots from the softmax, 39.4 us for 37.4 with 16 x 4099 keys and 20 rows.)
