@@ -219,24 +219,28 @@ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32
 __device__ __forceinline__ long long div_pos(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
+__device__ __forceinline__ int div_pos(int a, int b) { return (int)((uint32_t)a / (uint32_t)b); }
 
 // A CTA's share of the work. Units (of key tiles, or of query tiles) stand in one line, ordered by
 // sequence, head and unit; each is kOpen positions, which stand for the time a unit takes besides its
 // tiles, and then a position per tile. Of `total` positions CTA c of n takes total / n, the first total % n
 // CTAs one more. A share that begins inside a unit's first kOpen positions begins with its first tile; one
-// that ends there has none of them.
-struct Share {
+// that ends there has none of them. Pos counts positions: int where a caller has shown that they fit.
+template <typename Pos>
+struct ShareOf {
   int b, head, unit, tile;   // where the CTA begins
-  long long todo;            // its positions, from there
+  Pos todo;                  // its positions, from there
   int first_cta, first_slot; // of the unit in which it begins: the CTA with its first tile, the slot of that piece
 };
+using Share = ShareOf<long long>;
 
+template <typename Pos>
 struct Division {
-  long long each, more;  // positions of a CTA; CTAs with one more
-  __device__ Division(long long total, long long n) : each(div_pos(total, n)), more(total - each * n) {}
-  __device__ long long begin(long long c) const { return each * c + min(c, more); }
-  __device__ long long cta(long long at) const {
-    const long long wide = more * (each + 1);
+  Pos each, more;  // positions of a CTA; CTAs with one more
+  __device__ Division(Pos total, Pos n) : each(div_pos(total, n)), more(total - each * n) {}
+  __device__ Pos begin(Pos c) const { return each * c + min(c, more); }
+  __device__ Pos cta(Pos at) const {
+    const Pos wide = more * (each + 1);
     return at < wide ? div_pos(at, each + 1) : more + div_pos(at - wide, each);
   }
 };
@@ -246,14 +250,14 @@ struct Division {
 // empty. Units, made by make(b): heads, count, before(u) (positions before unit u, one head's), tiles(u), and open,
 // the positions of a unit before its first tile. Every kernel begins with this and can load nothing before it knows its
 // share, so it counts in full: each sequence is looked at once, and few divisions are left.
-template <int kThreads, int kScan, typename Units, typename Make>
-__device__ void find_share(int B, Make&& make, Share& sh, long long (&scan)[kScan], Units& at, int cta = blockIdx.x,
+template <int kThreads, int kScan, typename Units, typename Make, typename Pos>
+__device__ void find_share(int B, Make&& make, ShareOf<Pos>& sh, Pos (&scan)[kScan], Units& at, int cta = blockIdx.x,
                            int ctas = gridDim.x) {
   static_assert(kScan >= kThreads / 32 && kScan >= 2, "scan has an entry per warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = B <= kThreads ? 1 : (B + kThreads - 1) / kThreads, first = threadIdx.x * per, last = min(B, first + per);
   Units x;
-  long long size = 0, mine = 0;  // of the thread's first sequence (one head's), and of all of its
+  Pos size = 0, mine = 0;  // of the thread's first sequence (one head's), and of all of its
   if (first < last) {
     x = make(first);
     size = x.before(x.count);
@@ -264,28 +268,29 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long (&scan)[kSca
     }
   }
   const int warps = min(kThreads / 32, per == 1 ? (B + 31) >> 5 : kThreads / 32);  // that have sequences
-  long long inc = mine;
+  Pos inc = mine;
   if (warp < warps) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const Pos y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     if (lane == 31) scan[warp] = inc;
   }
   if (threadIdx.x == 0) sh.todo = 0;
   __syncthreads();
-  long long base = inc - mine, total = 0;
+  Pos base = inc - mine, total = 0;
+#pragma unroll (sizeof(Pos) == 4 ? 1 : 4)
   for (int i = 0; i < warps; ++i) {
     if (i < warp) base += scan[i];
     total += scan[i];
   }
   __syncthreads();  // scan is read
   if (total == 0) return;
-  const long long n = min(total, (long long)ctas), c = cta;  // no CTA before the last busy one is idle
+  const Pos n = min(total, (Pos)ctas), c = cta;  // no CTA before the last busy one is idle
   if (c >= n) return;
-  const Division cut(total, n);
-  const long long lo = cut.begin(c);
+  const Division<Pos> cut(total, n);
+  const Pos lo = cut.begin(c);
   if (lo >= base && lo < base + mine) {  // the sequence, and the line's position where it begins
     int b = first;
     while (lo >= base + size * x.heads) {
@@ -299,19 +304,20 @@ __device__ void find_share(int B, Make&& make, Share& sh, long long (&scan)[kSca
     scan[1] = size;
   }
   __syncthreads();
-  const long long from = scan[0];
+  const Pos from = scan[0];
   size = scan[1];
   const int head = (int)div_pos(lo - from, size);
-  const long long line = from + head * size;  // where the head's units begin
+  const Pos line = from + head * size;  // where the head's units begin
   const int count = at.count, open = at.open;
+#pragma unroll (sizeof(Pos) == 4 ? 1 : 4)
   for (int u = threadIdx.x; u < count; u += kThreads) {
-    const long long start = line + at.before(u);
+    const Pos start = line + at.before(u);
     if (start > lo || lo >= start + at.tiles(u) + open) continue;
     sh.head = head;
     sh.unit = u;
     sh.tile = (int)(lo - start);
     sh.todo = cut.begin(c + 1) - lo;
-    const long long c0 = cut.cta(start + open);
+    const Pos c0 = cut.cta(start + open);
     sh.first_cta = (int)c0;
     sh.first_slot = 2 * (int)c0 + (cut.begin(c0) >= start ? 0 : 1);
   }

@@ -83,6 +83,9 @@ constexpr int kCodeStages = 16;
 // Positions of a unit before its first tile, for its epilogue and the first tile of the next (weighed as 1 and 3: 64 x 8192 keys 128.4 and 126.5 us,
 // 16 x 2048 keys of 32 heads 48.1 and 46.8, 48 x 1024 of 12 heads at d = 64 37.2 and 36.8).
 constexpr int kF8Open = 3;
+// Positions fit an int: a sequence with new tokens has at most 4 units a head of max_k / 128 + 4 positions each, and fewer than 2^31
+// keys and 2^26 sequences, times heads, are checked by the caller. (In 64 bits the search for a CTA's share is 24 KB of
+// code, each line of which is waited for at the start: WHAT.)
 
 // How the work is cut. The K/V heads of a sequence are `turns` turns of `side` neighbours each: CTA c takes head c % side of every
 // turn, and the line of units that the CTAs of one residue divide has a turn where it would have a head. So `side` CTAs walk
@@ -106,7 +109,7 @@ struct F8Units {
     if (kParts) count *= c.parts;
   }
   __device__ int tiles(int = 0) const { return max(1, (q.Lk + 127) >> 7); }
-  __device__ long long before(int u) const { return (long long)u * (tiles() + open); }
+  __device__ int before(int u) const { return u * (tiles() + open); }
 };
 
 template <int D, int NP, bool kParts>
@@ -118,8 +121,8 @@ struct F8Ctl {
   uint64_t drain[2];    // per issuer
   uint32_t tmem_base;
   int abort_flag;
-  long long scan[F8Cfg<D, NP>::kThreads / 32];  // an entry per warp
-  Share share;
+  int scan[F8Cfg<D, NP>::kThreads / 32];  // an entry per warp
+  ShareOf<int> share;
   F8Units<kParts> units;     // of the sequence where the share begins
   int issued_k, issued_v;    // copies issued (abort-path drain)
   alignas(16) uint8_t codes[kCodeStages][256];  // key and value of each slot
@@ -137,10 +140,10 @@ struct F8Pieces {
   const PagedShape& s;
   const F8Cut& cut;
   int b, hk, u, kt, n, end, count;
-  long long todo;  // positions from the piece on
+  int todo;  // positions from the piece on
   bool finished;
   SeqInfo seq;
-  __device__ F8Pieces(const PagedShape& s_, const F8Cut& cut_, const Share& sh, const F8Units<kParts>& first, int beside)
+  __device__ F8Pieces(const PagedShape& s_, const F8Cut& cut_, const ShareOf<int>& sh, const F8Units<kParts>& first, int beside)
       : s(s_), cut(cut_), b(sh.b), hk(sh.head * cut.side + beside), u(sh.unit), kt(0), n(0), end(0), count(0), todo(sh.todo),
         finished(false) {
     if (todo == 0) return;
@@ -154,9 +157,8 @@ struct F8Pieces {
   }
   __device__ void open(int at) {  // at: position within the unit
     kt = max(0, at - kF8Open);
-    const long long stop = at + todo - kF8Open;
-    end = stop < n ? (int)stop : n;
-    todo -= min((long long)(n + kF8Open - at), todo);
+    end = min(at + todo - kF8Open, n);
+    todo -= min(n + kF8Open - at, todo);
     if (end <= kt) finished = true;  // the share ends before the unit's first tile
   }
   __device__ bool done() const { return finished || n == 0; }
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas, b = unit / s.Hkv;
     const F8Units<kParts> x(s, wk.cut, b);
     const int n = x.count ? x.tiles() : 0, lo = n * rank / ctas, hi = n * (rank + 1) / ctas;
-    ctl.share = Share{b, unit - b * s.Hkv, 0, kF8Open + lo, hi - lo, 0, 0};
+    ctl.share = ShareOf<int>{b, unit - b * s.Hkv, 0, kF8Open + lo, hi - lo, 0, 0};
     ctl.units = x;
   }
   fence_before_sync();
