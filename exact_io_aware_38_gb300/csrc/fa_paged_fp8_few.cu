@@ -83,9 +83,9 @@ constexpr int kCodeStages = 16;
 // Positions of a unit before its first tile, for its epilogue and the first tile of the next (weighed as 1 and 3: 64 x 8192 keys 128.4 and 126.5 us,
 // 16 x 2048 keys of 32 heads 48.1 and 46.8, 48 x 1024 of 12 heads at d = 64 37.2 and 36.8).
 constexpr int kF8Open = 3;
-// Positions fit an int: a sequence with new tokens has at most 4 units a head of max_k / 128 + 4 positions each, and fewer than 2^31
-// keys and 2^26 sequences, times heads, are checked by the caller. (In 64 bits the search for a CTA's share is 24 KB of
-// code, each line of which is waited for at the start: WHAT.)
+// Positions fit an int: a sequence with new tokens has at most 4 units a head of max_k / 128 + 4 positions each, sequences times
+// heads are fewer than 2^26 and times keys fewer than 2^31 (checked by the caller). In 64 bits the search for a CTA's share
+// is longer code, each line of which is waited for at the start (48 x 1024 keys of 12 heads, d = 64: 23.4 us, so 22.6).
 
 // How the work is cut. The K/V heads of a sequence are `turns` turns of `side` neighbours each: CTA c takes head c % side of every
 // turn, and the line of units that the CTAs of one residue divide has a turn where it would have a head. So `side` CTAs walk
@@ -210,6 +210,17 @@ struct F8Args {
   float scale;
   int* status;
 };
+
+// A wait that is mostly over when it is asked for: what else it takes is a call, out of the way of the code around it, since the
+// kernel waits for its instructions (512 x 500 keys of 12 heads, d = 64, 16 rows: 218 us inline and 140). Not for the issuers of MMAs
+// (16 x 4099 keys, 16 rows: 26 and 29.5).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return mbar_wait(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ bool wait_near(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (__builtin_expect(mbar_try(bar, parity), 1)) return true;
+  return wait_on(bar, parity, abort_flag, status);
+}
 
 // Two probabilities' parts: hi and mid by cutting their fp16 after two fraction bits (a byte), lo by rounding the rest.
 __device__ __forceinline__ void split_p(float p0, float p1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     auto copy = [&]() {  // the next tile
       const int left = x.seq.Lk - (xkt << 7), pages = left <= 0 ? 0 : min(per, (left + rows - 1) >> shift);
       const uint32_t full = full0 + xst * 8;
-      if (run && xt >= stages) run = mbar_wait(empty0 + xst * 8, xphase, abort_flag, a.status);
+      if (run && xt >= stages) run = wait_near(empty0 + xst * 8, xphase, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run) && !*abort_flag;
 #ifdef FA_TEST_WITHHOLD_KV  // a test-only build: every wait for keys and values must run out cleanly
       run = false;
@@ -433,7 +444,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
       const int qb = piece & 1;
       const uint32_t to = sQ + qb * C::kQBytes;
       if (at < 0) {
-        if (run && piece >= 2) run = mbar_wait(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
+        if (run && piece >= 2) run = wait_near(bar(ctl.q_empty[qb]), ((piece >> 1) - 1) & 1, abort_flag, a.status);
         run = __all_sync(0xffffffffu, run) && !*abort_flag;
         const int live = y.rows();
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) +
@@ -455,8 +466,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
         }
-        split_rows<D, NP, 2>(to, ctl.qmul[qb], at, a.scale * kLog2e, run);
-        at += 2 * kPer;
+        split_rows<D, NP, D / 64>(to, ctl.qmul[qb], at, a.scale * kLog2e, run);
+        at += D / 64 * kPer;  // (4 rows; 8 at d = 64: 512 x 500 keys of 12 heads, 16 rows 140 us and 135, at d = 128 2: 5% more)
         if (at < NP) return;
         fence_proxy_async_smem();
         __syncwarp();
@@ -563,11 +574,11 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
     int t = 0, vs = 0;
     uint32_t vphase = 0;
     auto wait_pv = [&](int j) -> bool {  // P V of tile j has completed
-      return mbar_wait(bar(ctl.v_empty[j % C::kVStages]), (j / C::kVStages) & 1, abort_flag, a.status);
+      return wait_near(bar(ctl.v_empty[j % C::kVStages]), (j / C::kVStages) & 1, abort_flag, a.status);
     };
     auto split_q = [&](int piece) {  // four rows a warp of the piece's Q
       const int qb = piece & 1;
-      if (run) run = mbar_wait(bar(ctl.q_raw[qb]), (piece >> 1) & 1, abort_flag, a.status);
+      if (run) run = wait_near(bar(ctl.q_raw[qb]), (piece >> 1) & 1, abort_flag, a.status);
       run = __all_sync(0xffffffffu, run);
       if (4 * quad < NC) split_rows<D, NP, D / 64>(sQ + qb * C::kQBytes, ctl.qmul[qb], n0 + 4 * quad, a.scale * kLog2e, run);
       fence_proxy_async_smem();
@@ -589,8 +600,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
 #pragma unroll 1
           for (; split <= due; ++split) split_q(split);
         }
-        if (run && kt == w.kt) run = mbar_wait(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
-        if (run) run = mbar_wait(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
+        if (run && kt == w.kt) run = wait_near(bar(ctl.q_full[qb]), (piece >> 1) & 1, abort_flag, a.status);
+        if (run) run = wait_near(bar(ctl.s_full[t & 1]), (t >> 1) & 1, abort_flag, a.status);
         fence_after_sync();
         uint32_t shi[NC], slo[NC];
         load_cols(tmem + lane_off + (t & 1) * 2 * NP + n0, shi);
@@ -724,7 +735,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         // Value rows past the last key may hold anything, and 0 times NaN is NaN: they become 0.
         const int valid = seq.Lk - (kt << 7);
         if (valid < 128) {
-          if (run) run = mbar_wait(bar(ctl.v_full[vs]), vphase, abort_flag, a.status);
+          if (run) run = wait_near(bar(ctl.v_full[vs]), vphase, abort_flag, a.status);
           if (run && r >= valid)
 #pragma unroll
             for (int c = gr * (D / 16 / C::kGroups); c < (gr + 1) * (D / 16 / C::kGroups); ++c)
@@ -782,10 +793,9 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         for (int k = 0; k < NC; ++k) o[k] += __uint_as_float(x[k]) + __uint_as_float(z[k]);
       }
       if (r < D) {
-        // The strides are looked at once where many rows are stored: their lines of the arguments miss (48 x 1024 keys of 12 heads,
-        // d = 64, 64 rows: 75 us and 66, 16 rows 40.7 and 38.6). With few it costs the loop above registers it needs (1 row: 26.4 us
-        // and 27.1; 16 rows at d = 128 26.7 and 30.5).
-        constexpr bool kStep = NP > 16 || (NP == 16 && D == 64);
+        // The strides are looked at once: their lines of the arguments miss (48 x 1024 keys of 12 heads, d = 64, 64 rows: 75 us and
+        // 66, 16 rows 34.8 and 29.4). Not with 16 rows at d = 128, whose loop needs the registers (16 x 4099 keys: 27.4 and 26.4).
+        constexpr bool kStep = NP != 16 || D == 64;
         const long long step = a.so.head, wrap = a.so.row - (long long)G * a.so.head;
         __nv_bfloat16* to = out + (size_t)i * a.so.row + (size_t)g * a.so.head;
 #pragma unroll
