@@ -788,9 +788,23 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
   return fa_launch_paged_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+// The few-row kernel counts its work in 32 bits.
+int paged_fp8_shape(const fa_paged_problem* p, fa::PagedShape* out) {
+  const int rc = paged_shape(p, PagedRowsOf::kQueries, out);
+  return rc == FA_OK && (long long)out->B * out->Hkv >= 1ll << 26 ? FA_ERR_UNSUPPORTED : rc;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t fa_fwd_paged_fp8_workspace_bytes(const fa_paged_problem* p, int num_sms) {
   fa::PagedShape s;
-  if (paged_shape(p, PagedRowsOf::kQueries, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
+  if (paged_fp8_shape(p, &s) != FA_OK || num_sms < 1 || num_sms > kMaxSms) return 0;
   return round_up(fa_paged_fp8_workspace(s, num_sms));
 }
 
@@ -798,7 +812,7 @@ int fa_fwd_paged_fp8(const fa_paged_problem* p, int num_sms, const void* q, fa_s
                      fa_strides sk, const void* v_cache, fa_strides sv, const uint8_t* codes, void* o, fa_strides so,
                      float* lse, void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
   FaPagedArgs a{};
-  int rc = paged_shape(p, PagedRowsOf::kQueries, &a.s);
+  int rc = paged_fp8_shape(p, &a.s);
   if (rc != FA_OK) return rc;
   if (num_sms < 1 || num_sms > kMaxSms) return FA_ERR_INVALID_ARG;
   const size_t need = round_up(fa_paged_fp8_workspace(a.s, num_sms));

@@ -414,12 +414,18 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
  *              lose precision, and numbers below 2^-90 become 0; a number within 2^-5 of bf16's largest may round up to
  *              2^128, which reads as an infinity. (So a cached row is a row of bf16 numbers, each of them exact.)
  *   contents   a slot that no length reaches may hold any bytes and codes: it enters no result. A row that sees a key or
- *              value of code 255, or that holds NaN or an infinity itself, has O = LSE = NaN; rows that do not see it have none of it.
+ *              value of code 255, or sees a key and holds NaN or an infinity itself, has O = LSE = NaN (an infinity by which all of the
+ *              row's scores are -inf may instead make it a row without keys); rows that do not see it have none of it.
  *              Bytes of NaN (127 and 255), which an append never writes, reach the rows of their 128-key tile as a NaN
  *              in a bf16 cache does; codes 1 to 46 and 248 to 254, which it never writes either, may overflow the row sums.
- *   range      up to 256 rows (tokens x heads) of a K/V head, row sums are taken by way of the weighted values: a key whose value is
- *              2^100 times smaller than another that the row sees may be missing from them, and so may keys with values of
- *              zeros beside values of more than 2^30. More rows have no such limit.
+ *   few rows   of a K/V head are those of fewer than five units of 64 rows (tokens x heads; whole tokens, or, of more than 64 heads,
+ *              parts of one token). Their products are of the bytes as they lie. A term P v of O is off by 2^-9 of itself or by 2^-24
+ *              of what it would be with the largest P 2^code of the row, whichever is more. Row sums are taken by way of the
+ *              weighted values: a key whose value is 2^100 times smaller than another that the row sees may be missing from
+ *              them, and so may keys with values of zeros beside values of more than 2^30. A row and a key whose largest elements
+ *              multiply to 2^127 or more have no defined score, not even 0. More rows go by way of keys and values read back to
+ *              bf16, and have no such limits.
+ *   sizes      besides those above, an attention has fewer than 2^26 sequences x K/V heads.
  * Key weights and eviction take bf16 caches only.
  */
 
@@ -444,10 +450,9 @@ int fa_paged_read_fp8(const fa_paged_problem* p, void* k_rows, fa_strides sk_row
 /*
  * fa_fwd_paged over such a cache: O and LSE of the new tokens against the rows that it stands for. Arguments, masks, layouts and
  * errors as there, with the codes beside the caches.
- *   workspace    device, >= fa_fwd_paged_fp8_workspace_bytes(p, num_sms) bytes, 256-byte aligned; scratch only. Up to 256 rows of a
- *                K/V head (and 64 heads) as for fa_fwd_paged. For more it also holds keys and values read back to bf16, of as many
- *                sequences as fit 1 GiB by the bound seqlen_k (one at least): it grows with that bound, so give the longest
- *                length in use.
+ *   workspace    device, >= fa_fwd_paged_fp8_workspace_bytes(p, num_sms) bytes, 256-byte aligned; scratch only. For few rows as
+ *                for fa_fwd_paged. For more it also holds keys and values read back to bf16, of as many sequences as fit 1 GiB by
+ *                the bound seqlen_k (one at least): it grows with that bound, so give the longest length in use.
  */
 size_t fa_fwd_paged_fp8_workspace_bytes(const fa_paged_problem* p, int num_sms);
 int fa_fwd_paged_fp8(const fa_paged_problem* p, int num_sms, const void* q, fa_strides sq, const void* k_cache,

@@ -481,6 +481,23 @@ def test_infinities_in_a_query_row():
         assert (np.abs(p.np(o)[0] - ro) <= 1.05 * 2.0**-8 * (a + np.abs(ro)))[keep].all()
 
 
+@pytest.mark.parametrize("n", [1, 70, 200])
+def test_infinity_that_makes_all_scores_minus_infinity(n):
+    """NaN, or a row without keys; the other rows are as without it."""
+    p = Problem8([200], [n], 4, 2, 64, page=16, seed=33)
+    p.k[..., 3] = -1.0 - p.k[..., 3].abs()
+    p.quantise()
+    ref = p.check_attend(*p.attend(False), False)
+    p.cq[0, 0, 1, 3] = math.inf
+    o, lse = p.attend(False)
+    got, at = o[0, 0, 1].float(), float(lse[0, 1, 0])
+    assert (bool(torch.isnan(got).all()) and math.isnan(at)) or (bool((got == 0).all()) and at == -math.inf)
+    keep = np.ones((n, 4), dtype=bool)
+    keep[0, 1] = False
+    ro, rl, a = ref[0]
+    assert (np.abs(p.np(o)[0] - ro) <= 1.05 * 2.0**-8 * (a + np.abs(ro)))[keep].all()
+
+
 def test_attend_shared_pages_and_bound():
     """Two sequences share their first pages; a bound above the longest length changes nothing, one below cuts."""
     for n in (2, 70):

@@ -47,6 +47,16 @@ def test_problem_refusals_of_the_attention(kw, rc):
     assert attend(problem(**kw)) == rc and append(problem(**kw), c=None) == -1
 
 
+def test_sequences_past_the_counters_of_the_attention():
+    """2^26 sequences, times heads, of packed rows: few of them can have tokens. Append and reading take them (their next
+    refusal is a misaligned pointer)."""
+    kw = dict(Hkv=2, H=2, max_pages=1, page_size=8, seqlen_k=8, seqlen_q=1, cu_seqlens_q=A, rows_q=1 << 20)
+    big, fits = problem(B=1 << 25, **kw), problem(B=(1 << 25) - 1, **kw)
+    assert attend(big) == -2 and fa.fa_fwd_paged_fp8_workspace_bytes(big, 152) == 0
+    assert attend(fits, lse=A + 2) == append(big, c=A + 2) == read(big, c=A + 2) == -3
+    assert fa.fa_fwd_paged_fp8_workspace_bytes(fits, 152) > 0
+
+
 def test_buffer_refusals():
     for call, names in ((attend, "q k v c o lse"), (append, "kn vn k v c"), (read, "kn vn k v c")):
         for n in names.split():
