@@ -958,11 +958,14 @@ cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
 }  // namespace
 }  // namespace fa
 
-// Up to four units of 64 rows; more go by way of the chunk kernel.
+// Up to four units of 64 rows; more go by way of the chunk kernel. Where a number of heads that divides 128 fills its tiles,
+// it is ahead from three units on at d = 64 (128 sequences of 1000 keys, 12 heads: 100 rows 256 us and 290, 130 rows 375 and 346), and
+// from four at d = 128 (16 x 4000 keys, 32 / 8 heads: 132 rows 121 and 155, 240 rows 157 and 157; 300 x 500 674 and 430).
 int fa_paged_few8_tokens(const fa::PagedShape& s) {
   const int G = s.H / s.Hkv;
   if (G > 64) return (long long)s.Nq * fa::token_units(s) <= 4 ? 1 : 0;
-  if (s.Nq > 4 * (64 / G)) return 0;
+  const int most = 128 % G != 0 ? 4 : s.d == 128 ? 3 : 2;
+  if (s.Nq > most * (64 / G)) return 0;
   return (long long)s.Nq * G <= 64 ? s.Nq : 64 / G;
 }
 

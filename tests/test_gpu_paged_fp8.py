@@ -331,6 +331,14 @@ def test_many_heads_per_kv_head(heads, n):
     p.check_attend(*p.attend(True), True)
 
 
+@pytest.mark.parametrize("n,heads", [(48, (8, 2, 128)), (49, (8, 2, 128)), (32, (8, 2, 64)), (33, (8, 2, 64)), (84, (3, 1, 64)),
+                                     (85, (3, 1, 64)), (36, (7, 1, 128)), (37, (7, 1, 128)), (4, (37, 1, 64)), (5, (37, 1, 64))])
+def test_most_rows_of_one_way_and_least_of_the_other(n, heads):
+    p = Problem8([700, 130, 0, n], [n] * 4, *heads, page=32, seed=n)
+    for sms in (3, 152):
+        p.check_attend(*p.attend(True, num_sms=sms), True)
+
+
 @pytest.mark.parametrize("n,heads", [(1, (142, 2, 128)), (2, (142, 2, 64)), (2, (128, 1, 128)), (1, (256, 1, 64)), (1, (257, 1, 64)),
                                      (1, (390, 3, 64)), (2, (65, 1, 128))])
 @pytest.mark.parametrize("sms", [1, 5, 152])
