@@ -899,7 +899,10 @@ F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0: the rule of fa_paged_decode.cu with
 // limits of its own, since a tile is half as many bytes. Eight tiles a CTA of a cluster (8 sequences of 8 heads, 4000 keys:
 // 13.9 us, divided 14.7; one of 8000 12.5 and 13.3; 4 of 4000 12.7 and 12.4; with 16 tiles 8 of 8000 21.3 and 19.6) or 16 of one
-// alone (24 of 12 heads, d = 64, 2000 keys: 16.1 and 20.0).
+// alone (24 of 12 heads, d = 64, 2000 keys: 16.1 and 20.0). Nearly two units a place, of up to 8 tiles, are as fast undivided (48 of 12
+// heads, d = 64, 1024 keys: 19.4 and 20.0, with 16 rows 24.3 and 28.1; 64 of 8 heads, d = 128, 500 keys 17.9 and 19.2; 128 keys 13.4
+// and 13.1), and are one launch without a workspace, which saves a caller 10 us. Not a few more than the places (40 of 8 heads, 1000
+// keys: 22.4 and 19.5), nor 16 tiles (64 of 8 heads, 2000 keys: 40.9 and 39.3).
 int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
   if (tokens < s.Nq || token_units(s) > 1) return 0;
   const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s, tokens));
@@ -913,6 +916,7 @@ int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
     else if (units * 2 <= room)
       ctas = 2;
   }
+  if (2 * units >= 3 * room && units <= 2 * room && tiles <= 8) return 1;
   return units * ctas <= room && tiles <= (ctas == 1 ? 16 : 8 * ctas) ? ctas : 0;
 }
 

@@ -284,6 +284,15 @@ def test_attend_any_division(n, heads, sms):
     p.check_attend(*p.attend(True, num_sms=sms), True)
 
 
+@pytest.mark.parametrize("n,heads", [(1, (8, 2, 128)), (3, (8, 2, 64)), (7, (8, 2, 128)), (12, (8, 2, 64))])
+@pytest.mark.parametrize("sms", [2, 3, 4, 5])
+def test_attend_more_short_units_than_places(n, heads, sms):
+    """8 units, of up to 8 tiles, on 2 to 10 places: undivided where they are nearly two a place; packed rows stay in place."""
+    for packed in (False, True):
+        p = Problem8([900, 130, 0, 128], [n, 1, n, 0] if packed else [n] * 4, *heads, page=32, packed=packed, seed=n)
+        p.check_attend(*p.attend(True, num_sms=sms), True)
+
+
 @pytest.mark.parametrize("B", [500, 600, 1300])
 def test_attend_many_sequences(B):
     """More sequences than threads look for a CTA's share, many of them empty, in a packed batch with gaps."""
