@@ -7,8 +7,9 @@
 // precision is lost:
 //   Q  a row is scaled by a power of two to a largest element in [128, 256) and split into hi + lo / 32, both e4m3: a bf16
 //      number has 8 bits, hi takes 4 and the signed rest 4, so the sum is exact down to 2^-15 of the row's largest element.
-//   P  = hi + mid + lo, three e5m2 numbers cut from its fp16 rounding: 9 bits and more, off by 2^-9 of a probability at most
-//      (bf16 2^-8), and by 2^-17 below, where the row's largest is 2^7 at least.
+//   P  = hi + mid / 8 + lo / 64, three e5m2 numbers cut from its fp16 rounding: 9 bits and more, off by 2^-9 of a probability at most
+//      (bf16 2^-8), and by 1.25 x 2^-23 where that is more, where the row's largest is 2^7 at least. The factors lift mid and lo out of
+//      e5m2's last bits (2^-16): without them a row of 2^18 equal keys beside one of half its weight was off by 1.1%, with 2^20 by 4%.
 // The parts lie side by side as columns of one product (N = 2 rows for S, 3 rows for O), and are added up in fp32 when they
 // are read: at few rows the columns cost nothing beside the 128 lanes.
 //
@@ -43,6 +44,7 @@ using namespace tc;
 constexpr float kFirst = 7.f;    // log2 units that the reference starts below the first tile's largest
 constexpr float kRaise8 = 15.f;  // and that a score may exceed it by: 2^15 is near the top of e5m2 and fp16
 constexpr float kLoScale = 32.f;
+constexpr float kMidScale = 8.f;  // of P's second part; the third's is its square
 constexpr int kZeroRow = -80;    // exponent that stands for a value row of zeros: only its place in the row sum counts
 
 constexpr int few8_ctas(int np) { return np <= 16 ? 2 : 1; }  // per SM
@@ -222,13 +224,16 @@ __device__ __forceinline__ bool wait_near(uint32_t bar, uint32_t parity, volatil
   return wait_on(bar, parity, abort_flag, status);
 }
 
-// Two probabilities' parts: hi and mid by cutting their fp16 after two fraction bits (a byte), lo by rounding the rest.
+// Two probabilities' parts: hi and mid by cutting their fp16 after two fraction bits (a byte), lo by rounding the rest; mid is held 8 and
+// lo 64 times larger. All of it but the fp16 and lo's rounding is exact, also among fp16's subnormals: P is at most 2^15, what is left
+// of it after hi less than 2^12, after mid less than 2^9.
 __device__ __forceinline__ void split_p(float p0, float p1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   __half2 h = __floats2half2_rn(p0, p1);
   hi = *reinterpret_cast<uint32_t*>(&h) & 0xff00ff00u;
-  __half2 r = __hsub2(h, *reinterpret_cast<__half2*>(&hi));
+  const __half2 eight = __float2half2_rn(kMidScale);
+  __half2 r = __hmul2(__hsub2(h, *reinterpret_cast<__half2*>(&hi)), eight);
   mid = *reinterpret_cast<uint32_t*>(&r) & 0xff00ff00u;
-  r = __hsub2(r, *reinterpret_cast<__half2*>(&mid));
+  r = __hmul2(__hsub2(r, *reinterpret_cast<__half2*>(&mid)), eight);
   uint16_t y;
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(y) : "r"(*reinterpret_cast<uint32_t*>(&r)));
   lo = y;
@@ -790,7 +795,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
         load_cols(tO + 2 * NP, z);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < NC; ++k) o[k] += __uint_as_float(x[k]) + __uint_as_float(z[k]);
+        for (int k = 0; k < NC; ++k)
+          o[k] += (__uint_as_float(x[k]) + __uint_as_float(z[k]) * (1.f / kMidScale)) * (1.f / kMidScale);
       }
       if (r < D) {
         // The strides are looked at once: their lines of the arguments miss (48 x 1024 keys of 12 heads, d = 64, 64 rows: 75 us and

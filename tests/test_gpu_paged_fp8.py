@@ -422,6 +422,40 @@ def test_many_small_weights_beside_a_large_one(n):
     p.check_attend(*p.attend(False), False)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", [(8, 1), (4, 4), (8, 4), (8, 8)])
+@pytest.mark.parametrize("L", [1 << 18, (1 << 20) + 77])
+def test_precision_of_one_long_piece(L, G, n, d):
+    """One CTA goes through all keys of a head: the first weighs about as much as all the others, which are equal, each row's by another
+    factor. Half of O is the first key's share, half the others'. Off by: 1.25 x 2^-9 of a probability, or 1.25 x 2^-23 where the largest
+    is 2^7; 2^-8 for O in bf16; L / 32 sums in fp32, each off by up to 2^-23 of a sum that is half the last one in the mean; and
+    L / 128 of a lane's row sum, each off by up to 2^-24 of one that may be near the last from the beginning."""
+    P, rows = 4096, G * n
+    pages = -(-L // P)
+    one = int(np.flatnonzero(p8.TABLE == 1.0)[0])
+    k, v = (torch.zeros(pages, P, 2, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    k[..., 1] = one
+    v[..., d // 2:] = one
+    k[0, 0, :, 1], k[0, 0, :, 0] = 0, one
+    v[0, 0, :, d // 2:], v[0, 0, :, :d // 2] = 0, one
+    codes = torch.full((pages, 2, P, 2), 127, dtype=torch.uint8, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    q = torch.zeros(1, n, 2, G, d, dtype=torch.float64)
+    q[..., 0] = torch.tensor([math.log(L) + math.log(2) * (2 * i / rows - 1) for i in range(rows)]).view(1, n, 1, G)
+    q = q.view(1, n, 2 * G, d).to(torch.bfloat16)
+    e4 = torch.float8_e4m3fn
+    o, lse = fa.fwd_paged_fp8(q.cuda(), k.view(e4), v.view(e4), codes, table, torch.tensor([L], dtype=torch.int32, device="cuda"),
+                              scale=1.0, num_sms=1)
+    x = q[0, :, :, 0].double()
+    first, total = torch.exp(x), torch.exp(x) + (L - 1)
+    small = torch.clamp(1.25 * 2.0**-23 * first / 2**7, min=1.25 * 2.0**-9)
+    tol = (small + 2.0**-8 + L / 64 * 2.0**-23 + L / 128 * 2.0**-24)[..., None]
+    o = o[0].double().cpu()
+    for got, want in ((o[..., :d // 2], first / total), (o[..., d // 2:], (L - 1) / total)):
+        assert ((got - want[..., None]).abs() <= tol * want[..., None]).all()
+    assert ((lse[0].t().double().cpu() - torch.log(total)).abs() <= 2.0**-18 + 16 * 2.0**-22 + L / 128 * 2.0**-24).all()
+
+
 def test_rows_and_keys_of_extreme_sizes():
     """q of 2^40 against keys of 2^-40 and the reverse, beside rows of zeros: the scores are ordinary numbers."""
     for n in (1, 5, 100):

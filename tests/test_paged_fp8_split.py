@@ -1,0 +1,49 @@
+"""The few-row kernel's split of the probabilities over an 8-bit cache, restated in fp64 with the formats' own roundings, against the errors
+that fa.h states for it.
+
+P is rounded to fp16 and split into hi + mid / 8 + lo / 64 of e5m2 numbers: hi and mid are cut after two fraction bits (toward zero; an
+e5m2 number is the upper byte of an fp16 one), lo is rounded to the nearest."""
+
+import numpy as np
+
+
+def cut(x):
+    """Toward zero to e5m2: fp16's upper byte."""
+    return (x.astype(np.float16).view(np.uint16) & 0xFF00).view(np.float16).astype(np.float64)
+
+
+def nearest_e5m2(x):
+    """Two fraction bits, steps of 2^-16 at least; ties to even."""
+    e = np.maximum(np.frexp(x)[1] - 1, -14)
+    step = 2.0 ** (e - 2)
+    return np.rint(x / step) * step
+
+
+def split_p(p):
+    h = p.astype(np.float16).astype(np.float64)
+    hi = cut(h)
+    r = (h - hi) * 8
+    assert np.array_equal(r.astype(np.float16).astype(np.float64), r)  # (what the kernel computes in fp16 is exact)
+    mid = cut(r)
+    r = (r - mid) * 8
+    assert np.array_equal(r.astype(np.float16).astype(np.float64), r)
+    lo = nearest_e5m2(r)
+    assert max(hi.max(), mid.max(), lo.max()) <= 57344  # e5m2's largest number
+    return hi + mid / 8 + lo / 64
+
+
+def every_p():
+    """Every fp16 number from 0 to 2^15, the middles between two, and a step of fp32 beside each middle."""
+    h = np.arange(0x7801, dtype=np.uint16).view(np.float16).astype(np.float64)
+    mid = ((h[:-1] + h[1:]) / 2).astype(np.float32)
+    beside = [np.nextafter(mid, np.float32(s)).astype(np.float64) for s in (0, 1e9)]
+    return np.concatenate([h, mid.astype(np.float64), *beside])
+
+
+def test_probabilities_keep_their_precision_far_below_the_largest():
+    """Where the row's largest is 2^7 at least: 1.25 x 2^-23 of what is too small for the relative bound is 1.25 x 2^-30 of the largest."""
+    p = every_p()
+    binade = 2.0 ** (np.frexp(np.where(p == 0, 2.0**-60, p))[1] - 1)
+    assert (np.abs(split_p(p) - p) <= np.maximum(1.25 * 2.0**-9 * binade, 1.25 * 2.0**-23)).all()
+    one = np.abs(split_p(p) - p) / np.where(p == 0, 1, p)
+    assert one[p >= 2.0**-13].max() <= 1.25 * 2.0**-9  # a key of 2^-20 of the largest
