@@ -18,7 +18,7 @@ struct PagedShape {
   int num_pages, max_pages;
   const int32_t* table;    // [B][max_pages]
   const int32_t* seqlens;  // [B]
-  int min_q, max_q;        // sequences with fewer or more new tokens count as without any: another kernel has them
+  int min_q, max_q;        // to paged_part, sequences with fewer or more new tokens are without any: another kernel has them
 };
 
 // The kernels of this family are programmatic dependents of one another. Each lets its own dependent be
@@ -44,11 +44,20 @@ __device__ __forceinline__ SeqInfo paged_seq(const PagedShape& s, int b) {
     r.Lq = s.Nq;
     r.bb = b;
   }
-  if (r.Lq < s.min_q || r.Lq > s.max_q) r.Lq = 0;
   r.Lk = clampi(s.seqlens[b], 0, s.max_k);
   r.k0 = 0;
   r.off = r.Lk - r.Lq;
   r.krows = r.Lk;
+  return r;
+}
+// The same for the kernels that may share the sequences of a batch by their new tokens. (Not for all: an append of 64 tokens takes
+// 2.1 us without the look at the limits and 2.2 with it.)
+__device__ __forceinline__ SeqInfo paged_part(const PagedShape& s, int b) {
+  SeqInfo r = paged_seq(s, b);
+  if (r.Lq < s.min_q || r.Lq > s.max_q) {
+    r.Lq = 0;
+    r.off = r.Lk;
+  }
   return r;
 }
 

@@ -53,7 +53,7 @@ struct Units {
   SeqInfo q;
   Units() = default;
   __device__ Units(const PagedShape& s, const PagedRows& c, int b)
-      : heads(c.Hv), count(0), open(kChOpen), U(2 * c.tpt), causal(s.causal), none(0), q(paged_seq(s, b)) {
+      : heads(c.Hv), count(0), open(kChOpen), U(2 * c.tpt), causal(s.causal), none(0), q(paged_part(s, b)) {
     count = c.by_tpt.div(q.Lq + U - 1) >> 1;
     // With more tokens than keys the first units see no key: one empty tile each.
     if (q.off < 0) none = c.by_tpt.div(-q.off) >> 1;

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(256) paged_stage_fp8_kernel(const FaPagedArgs 
   const int lane = threadIdx.x & 31;
   auto keys_of = [&](int b) {
     if (b >= s.B) return 0;
-    const SeqInfo seq = paged_seq(s, b);
+    const SeqInfo seq = paged_part(s, b);
     return seq.Lq > 0 ? seq.Lk : 0;
   };
   // A lane's keys (all the warp's, or one of its kRows), counted from the first sequence of the 32 (or 256) that the warp looks

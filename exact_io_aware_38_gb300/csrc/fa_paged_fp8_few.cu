@@ -106,7 +106,7 @@ struct F8Units {
   int heads, count, open;
   SeqInfo q;
   F8Units() = default;
-  __device__ F8Units(const PagedShape& s, const F8Cut& c, int b) : heads(c.turns), open(kF8Open), q(paged_seq(s, b)) {
+  __device__ F8Units(const PagedShape& s, const F8Cut& c, int b) : heads(c.turns), open(kF8Open), q(paged_part(s, b)) {
     count = q.Lq <= c.tokens ? q.Lq > 0 : (q.Lq + c.tokens - 1) / c.tokens;
     if (kParts) count *= c.parts;
   }
