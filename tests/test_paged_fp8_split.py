@@ -47,3 +47,11 @@ def test_probabilities_keep_their_precision_far_below_the_largest():
     assert (np.abs(split_p(p) - p) <= np.maximum(1.25 * 2.0**-9 * binade, 1.25 * 2.0**-23)).all()
     one = np.abs(split_p(p) - p) / np.where(p == 0, 1, p)
     assert one[p >= 2.0**-13].max() <= 1.25 * 2.0**-9  # a key of 2^-20 of the largest
+
+
+def test_the_largest_error_of_a_probability():
+    """1.1 x 2^-9 of itself, which is more than lo's rounding alone (2^-9): down to 2^-13, which is 2^-20 of a row's largest."""
+    p = every_p()
+    p = p[p >= 2.0**-13]
+    worst = (np.abs(split_p(p) - p) / p).max()
+    assert 2.0**-9 < worst <= 1.1 * 2.0**-9
