@@ -3,13 +3,14 @@
 //
 // What it computes: as fa_paged_decode.cu, S^T = K Q^T with a key on each tensor-memory lane and a row on each column, and
 // O^T += V^T P^T, but the products take the e4m3 bytes as they lie in the cache (kind::f8f6f4), so nothing is converted on
-// its way and a 128-key tile is half as many bytes and products. The other operands are split so that nothing of their
-// precision is lost:
+// its way and a 128-key tile is half as many bytes and products. The other operands are split into parts of 8 bits:
 //   Q  a row is scaled by a power of two to a largest element in [128, 256) and split into hi + lo / 32, both e4m3: a bf16
-//      number has 8 bits, hi takes 4 and the signed rest 4, so the sum is exact down to 2^-15 of the row's largest element.
+//      number has 8 bits, hi takes 4 and the signed rest 4, so the sum is exact for elements from the largest's binade to 2^-14 of it;
+//      smaller ones are off by at most 2^-22 of the largest.
 //   P  = hi + mid / 8 + lo / 64, three e5m2 numbers cut from its fp16 rounding: off by 2^-11 (fp16) and 2^-9 (lo) of its binade,
-//      together by 1.1 x 2^-9 of a probability at most (bf16 2^-8), or by 1.25 x 2^-23 where that is more; the row's largest is 2^7 at least. The factors lift mid and lo out of
-//      e5m2's last bits (2^-16): without them a row of 2^18 equal keys beside one of half its weight was off by 1.1%, with 2^20 by 4%.
+//      together by 1.1 x 2^-9 of a probability at most (bf16 2^-8), or by 1.25 x 2^-23 where that is more; the row's largest is
+//      2^7 at least. The factors lift mid and lo out of e5m2's last bits (2^-16): without them 2^18 equal keys of one piece beside a key
+//      of about their weight were off by up to 2.3%, 2^20 by 11%; with them by no more than O's rounding (2^-8).
 // The parts lie side by side as columns of one product (N = 2 rows for S, 3 rows for O), and are added up in fp32 when they
 // are read: at few rows the columns cost nothing beside the 128 lanes.
 //

@@ -8,7 +8,7 @@ Bounds, derived from the roundings on the way:
   O    the probabilities are rounded (to bf16, or to three e5m2 numbers whose sum is as near; 2^-8 sum_j P |v|) and so is O
        (2^-8 |O|); 5% more for the fp32 sums, which also holds what is below 2^-24 of a row's largest P |v|;
   LSE  a score is an fp32 sum of d exact products: off by at most d 2^-23 c sum |q k|; q may be held as two e4m3 numbers, exact
-       but for elements below 2^-15 of the row's largest, which are off by at most 2^-22 of that: sqrt(d) 2^-22 c |q| |k| in all;
+       but for elements below 2^-14 of the row's largest, which are off by at most 2^-22 of that: sqrt(d) 2^-22 c |q| |k| in all;
        the sum of the exponentials adds 2^-18.
 """
 

@@ -1,10 +1,14 @@
-"""The few-row kernel's split of the probabilities over an 8-bit cache, restated in fp64 with the formats' own roundings, against the errors
-that fa.h states for it.
+"""The few-row kernel's splits of the probabilities and of Q over an 8-bit cache, restated in fp64 with the formats' own roundings, against
+the errors that fa.h and the kernel state for them.
 
 P is rounded to fp16 and split into hi + mid / 8 + lo / 64 of e5m2 numbers: hi and mid are cut after two fraction bits (toward zero; an
-e5m2 number is the upper byte of an fp16 one), lo is rounded to the nearest."""
+e5m2 number is the upper byte of an fp16 one), lo is rounded to the nearest. A row of Q, scaled to a largest element in [128, 256), is hi + lo / 32 of e4m3 numbers, both rounded to the
+nearest."""
 
 import numpy as np
+import pytest
+
+from oracle.paged_fp8 import TABLE, round_e4m3
 
 
 def cut(x):
@@ -55,3 +59,16 @@ def test_the_largest_error_of_a_probability():
     p = p[p >= 2.0**-13]
     worst = (np.abs(split_p(p) - p) / p).max()
     assert 2.0**-9 < worst <= 1.1 * 2.0**-9
+
+
+@pytest.mark.parametrize("top", [128.0, 191.0, 255.0])
+def test_elements_of_q_are_exact_to_the_14th_binade_below_the_largest(top):
+    """Every bf16 number up to the row's largest, binade by binade; the first that are off are off by 2^-22 of the largest at most."""
+    nearest = lambda x: TABLE[round_e4m3(x)]  # noqa: E731
+    for k in range(40):
+        x = 2.0 ** (7 - k) * (1 + np.arange(128) / 128)
+        x = x[x <= top]
+        hi = nearest(x)
+        off = np.abs(hi + nearest((x - hi) * 32) / 32 - x)
+        assert (off.max() > 0) == (k > 14)
+        assert off.max() <= 2.0**-22 * top
