@@ -863,7 +863,8 @@ def fwd_paged_fp8(q, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens
     """fwd_paged over a cache held in 8 bits (fa_fwd_paged_fp8): k_cache and v_cache are float8_e4m3fn [num_pages,
     page_size, Hkv, d], any strides that are multiples of 16, and scales is uint8 [num_pages, Hkv, page_size, 2], the
     exponents of each slot's key and value: a row stands for its numbers times 2^(scale - 127). paged_append_fp8 writes
-    them. q, O and LSE are as in fwd_paged. max_seqlen_k sizes the workspace: give the longest length in use."""
+    them. q, O and LSE are as in fwd_paged. max_seqlen_k sizes the workspace: give the longest length in use. num_sms sets how
+    the work is divided (all SMs by default); it does not keep the call off the others."""
     if stream is not None:
         return _on_its_stream[fwd_paged_fp8](q, k_cache, v_cache, scales, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q,
                                              max_seqlen_k, num_sms=num_sms, causal=causal, scale=scale, out=out, lse=lse,

@@ -450,6 +450,9 @@ int fa_paged_read_fp8(const fa_paged_problem* p, void* k_rows, fa_strides sk_row
 /*
  * fa_fwd_paged over such a cache: O and LSE of the new tokens against the rows that it stands for. Arguments, masks, layouts and
  * errors as there, with the codes beside the caches.
+ *   num_sms      sets the division of the work and the workspace, as there, but the call is not confined to so many SMs: for each of
+ *                num_sms it may launch two CTAs (up to 16 rows; four where short units are not divided), and eight blocks that read
+ *                keys and values back. A caller who keeps SMs for other work has to keep them by other means.
  *   workspace    device, >= fa_fwd_paged_fp8_workspace_bytes(p, num_sms) bytes, 256-byte aligned; scratch only. For few rows as
  *                for fa_fwd_paged. For more it also holds keys and values read back to bf16, of as many sequences as fit 1 GiB by
  *                the bound seqlen_k (one at least): it grows with that bound, so give the longest length in use.
