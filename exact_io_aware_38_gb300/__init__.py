@@ -619,11 +619,11 @@ def _paged_view(name, t, dims, dtype=torch.bfloat16):
     return Strides(st[0], st[1], 0) if dims == 3 else Strides(st[1], st[2], st[0])
 
 
-def _paged_views(name_a, a, name_b, b, dims, dtype=torch.bfloat16):
+def _paged_views(name_a, a, name_b, b, dims):
     """_paged_view of two tensors of one shape."""
-    va = _paged_view(name_a, a, dims, dtype)
+    va = _paged_view(name_a, a, dims)
     same = b.stride() == a.stride() and b.dtype is a.dtype and b.device == a.device
-    return va, va if same else _paged_view(name_b, b, dims, dtype)
+    return va, va if same else _paged_view(name_b, b, dims)
 
 
 def _paged(q, k_cache, v_cache, page_table, seqlens_k, cu_seqlens_q, max_seqlen_q, max_seqlen_k, causal, scale):

@@ -305,7 +305,7 @@ StagePlan stage_plan(const PagedShape& s, int num_sms) {
   p.table = up256((size_t)p.group * p.tiles * sizeof(int32_t));
   p.tensor = up256(p.group * one);
   const PagedShape t = staged_shape(s, p.group, p.tiles);
-  p.attend = up256(paged_few_rows(t) ? fa_paged_decode_workspace(t, num_sms) : fa_paged_chunk_workspace(t, num_sms));
+  p.attend = up256(fa_paged_chunk_workspace(t, num_sms));
   return p;
 }
 
@@ -418,7 +418,7 @@ cudaError_t fa_launch_paged_fp8(const FaPagedArgs& a, cudaStream_t st) {
     x.sk.head = 128ll * s.d;
     x.sk.batch = 128ll * s.d * s.Hkv;
     x.sv = x.sk;
-    e = fa::paged_few_rows(x.s) ? fa_launch_paged_decode(x, st) : fa_launch_paged_chunk(x, st);
+    e = fa_launch_paged_chunk(x, st);  // (what comes this way has more than 64 rows)
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

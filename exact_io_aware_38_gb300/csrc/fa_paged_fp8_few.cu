@@ -934,10 +934,10 @@ cudaError_t launch_few8(const FaPagedArgs& a, int tokens, cudaStream_t st) {
   const int P = 1 << s.page_shift, box = P < 128 ? P : 128;
   // A miss fetches 128 bytes, at d = 64 two heads' rows (64, 128 and 256: within 1% while neighbours walk together; 147, - and 190 us
   // of 64 x 8192 keys before they did).
-  constexpr int kL2 = 128;
+  constexpr bool kWideL2 = false;
   CUtensorMap tk, tv;
-  if (!fa_make_tmap_u8(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, D, box, kL2) ||
-      !fa_make_tmap_u8(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, D, box, kL2))
+  if (!fa_make_tmap_u8(&tk, a.k, D, P, s.Hkv, s.num_pages, a.sk.row, a.sk.head, a.sk.batch, D, box, kWideL2) ||
+      !fa_make_tmap_u8(&tv, a.v, D, P, s.Hkv, s.num_pages, a.sv.row, a.sv.head, a.sv.batch, D, box, kWideL2))
     return cudaErrorInvalidValue;
   const int shared = unit_ctas(s, tokens, a.num_sms);
   int ctas = shared > 0 ? s.B * s.Hkv * shared : a.num_sms * C::kCtas;

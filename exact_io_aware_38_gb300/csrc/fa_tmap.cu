@@ -35,7 +35,7 @@ bool fa_make_tmap_bf16(CUtensorMap* m, const void* ptr, int D, int rows, int hea
 }
 
 bool fa_make_tmap_u8(CUtensorMap* m, const void* ptr, int inner, int rows, int heads, int batches, long long row_stride,
-                     long long head_stride, long long batch_stride, int box_inner, int box_rows, int l2_bytes) {
+                     long long head_stride, long long batch_stride, int box_inner, int box_rows, bool wide_l2) {
   auto enc = get_encode();
   if (enc == nullptr) return false;
   cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)batches};
@@ -44,8 +44,6 @@ bool fa_make_tmap_u8(CUtensorMap* m, const void* ptr, int inner, int rows, int h
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, box_inner <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             l2_bytes == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-             : l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-                               : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+             wide_l2 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

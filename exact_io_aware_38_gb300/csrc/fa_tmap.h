@@ -10,7 +10,6 @@ bool fa_make_tmap_bf16(CUtensorMap* m, const void* ptr, int D, int rows, int hea
                        long long head_stride, long long batch_stride, int box_rows = 128, int box_heads = 1,
                        bool wide_l2 = true);
 // The same for 8-bit elements (e4m3 operands) with a box of box_inner elements (bytes) x box_rows;
-// strides in bytes. The swizzle is of 128 bytes, or of 64 where box_inner is at most that; l2_bytes (64, 128 or 256): what a miss
-// fetches into L2.
+// strides in bytes. The swizzle is of 128 bytes, or of 64 where box_inner is at most that.
 bool fa_make_tmap_u8(CUtensorMap* m, const void* ptr, int inner, int rows, int heads, int batches, long long row_stride,
-                     long long head_stride, long long batch_stride, int box_inner, int box_rows, int l2_bytes = 256);
+                     long long head_stride, long long batch_stride, int box_inner, int box_rows, bool wide_l2 = true);
