@@ -255,7 +255,7 @@ __device__ __forceinline__ uint32_t raw_q(uint32_t q, int n, int part) {
   return q + (part / (D / 16) * NP + n) * D + part % (D / 16) * 16;
 }
 
-// Splits kTimes x 512 / D rows from `first` on in place, by a warp: D / 8 lanes a row. store: false where the buffer may still be
+// Splits kTimes x 256 / D rows from `first` on in place, by a warp: D / 8 lanes a row. store: false where the buffer may still be
 // in use (after a wait that ran out).
 template <int D, int NP, int kTimes>
 __device__ __forceinline__ void split_rows(uint32_t q, float* qmul, int first, float sl2, bool store) {
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           __syncwarp();
         }
         split_rows<D, NP, D / 64>(to, ctl.qmul[qb], at, a.scale * kLog2e, run);
-        at += D / 64 * kPer;  // (4 rows; 8 at d = 64: 512 x 500 keys of 12 heads, 16 rows 140 us and 135, at d = 128 2: 5% more)
+        at += D / 64 * kPer;  // (4 rows for either d; others tried: 8 at d = 64, 512 x 500 keys of 12 heads, 16 rows 140 us and with 4 135; 2 at d = 128: 5% more)
         if (at < NP) return;
         fence_proxy_async_smem();
         __syncwarp();
