@@ -54,8 +54,9 @@ template <int D, int NP>
 struct F8Cfg {
   static constexpr int kTileBytes = 128 * D;
   static constexpr int kCtas = few8_ctas(NP);
-  // Rows of a group of four softmax warps, and groups. Eight rows are a shorter chain of steps (16 x 4099 keys, 20 rows: 35.8 us,
-  // with 16 a group 37.2), but twice the warps, for which 16 rows twice on an SM have no registers (28.1 us, with 8 a group 32).
+  // Rows of a group of four softmax warps, and groups. Eight rows are a shorter chain of steps (16 x 4099 keys, 20 rows: 31.3 us,
+  // with 16 a group 32.3; 32 rows 32.5 and 34.3), but twice the warps, which 16 rows, twice on an SM, do not gain by (16 rows 26.5 us
+  // and, with 8 a group, 26.4; 48 x 1024 keys of 12 heads, d = 64, 24.9 and 25.7).
   static constexpr int kCols = NP == 8 || NP == 32 ? 8 : 16, kGroups = NP / kCols;
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kKStages = NP <= 16 ? (D == 128 ? 3 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;
@@ -83,8 +84,8 @@ struct F8Cfg {
 // which follows P V of two tiles before that, so the codes of t - 16 are read.
 constexpr int kCodeStages = 16;
 
-// Positions of a unit before its first tile, for its epilogue and the first tile of the next (weighed as 1 and 3: 64 x 8192 keys 128.4 and 126.5 us,
-// 16 x 2048 keys of 32 heads 48.1 and 46.8, 48 x 1024 of 12 heads at d = 64 37.2 and 36.8).
+// Positions of a unit before its first tile, for its epilogue and the first tile of the next (weighed as 1 and 3: 16 x 2048 keys of 32
+// heads 38.9 and 38.2 us; 64 x 8192 keys 120.8 and 120.9, 64 x 4096 of 12 heads at d = 64 56.2 and 56.3).
 constexpr int kF8Open = 3;
 // Positions fit an int: a sequence with new tokens has at most 4 units a head of max_k / 128 + 4 positions each, sequences times
 // heads are fewer than 2^26 and times keys fewer than 2^31 (checked by the caller). In 64 bits the search for a CTA's share
@@ -905,11 +906,11 @@ F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
 
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0: the rule of fa_paged_decode.cu with
 // limits of its own, since a tile is half as many bytes. Eight tiles a CTA of a cluster (8 sequences of 8 heads, 4000 keys:
-// 13.9 us, divided 14.7; one of 8000 12.5 and 13.3; 4 of 4000 12.7 and 12.4; with 16 tiles 8 of 8000 21.3 and 19.6) or 16 of one
-// alone (24 of 12 heads, d = 64, 2000 keys: 16.1 and 20.0). Nearly two units a place, of up to 8 tiles, are as fast undivided (48 of 12
-// heads, d = 64, 1024 keys: 19.4 and 20.0, with 16 rows 24.3 and 28.1; 64 of 8 heads, d = 128, 500 keys 17.9 and 19.2; 128 keys 13.4
-// and 13.1), and are one launch without a workspace, which saves a caller 10 us. Not a few more than the places (40 of 8 heads, 1000
-// keys: 22.4 and 19.5), nor 16 tiles (64 of 8 heads, 2000 keys: 40.9 and 39.3).
+// 13.9 us, divided 14.1; one of 777 8.3 and 9.5, of 8000 12.4 and 12.8; 4 of 4000 12.8 and 12.0, which clusters of 8 would do in 10.9; with
+// 16 tiles 8 of 8000 21.3 and 19.3) or 16 of one alone (24 of 12 heads, d = 64, 2000 keys: 16.0 and 18.0). Nearly two units a place, of up
+// to 8 tiles, mostly gain undivided (48 of 12 heads, d = 64, 1024 keys in pages of 64: 19.6 and 20.1, with 16 rows 24.9 and 29.0; 64 of 8
+// heads, d = 128, 500 keys 17.8 and 19.2; 128 keys 13.4 and 13.1), and are one launch without a workspace. Not a few more than the
+// places (40 of 8 heads, 1000 keys: 20.8 and 18.9), nor 16 tiles (64 of 8 heads, 2000 keys: 39.7 and 37.4).
 int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
   if (tokens < s.Nq || token_units(s) > 1) return 0;
   const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s, tokens));

@@ -617,6 +617,19 @@ def test_chunks_in_rounds_through_one_workspace():
         p.check_attend(*p.attend(True), True)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_many_sequences_in_rounds_of_two(packed):
+    """Nine sequences, two of which the workspace holds by the table's width: five rounds, the last of one sequence; packed, those of few
+    tokens go another way, and one round has no tokens left."""
+    lq = [70, 200, 1, 0, 65, 3, 129, 66, 90] if packed else [70] * 9
+    p = Problem8([300, 200, 1000, 50, 65, 128, 131, 700, 90], lq, 16, 8, 128, page=1024, seed=35, packed=packed)
+    wide = torch.full((9, 1 << 7), -7, dtype=torch.int32)
+    wide[:, :p.table.shape[1]] = p.table
+    p.ctable = wide.cuda()
+    assert 2 * ((1 << 17) * 8 * 128 * 4) == 1 << 30
+    p.check_attend(*p.attend(True), True)
+
+
 @pytest.mark.parametrize("heads", [(8, 2, 128), (20, 1, 128), (5, 5, 64), (96, 1, 64), (130, 1, 64), (142, 2, 128)])
 def test_prompts_beside_single_tokens(heads):
     """A packed batch in which two kernels share the sequences by their new tokens: none, one, at the limit between them,
