@@ -419,12 +419,11 @@ int fa_paged_evict(const fa_paged_problem* p, int keep, int recent, void* k_cach
  *              Bytes of NaN (127 and 255), which an append never writes, reach the rows of their 128-key tile as a NaN
  *              in a bf16 cache does; codes 1 to 46 and 248 to 254, which it never writes either, may overflow the row sums.
  *   few rows   of a K/V head are at most four units of 64 rows (tokens x heads; whole tokens, or, of more than 64 heads, parts of
- *              one token), by the size of d and the heads as few as two. Their products are of the bytes as they lie. A term P v of O is off by 1.1 x 2^-9 of itself or by
- *              2^-29 of what it would be with the largest P 2^code of the row, whichever is more. Row sums are taken by way of the
- *              weighted values: a key whose value is 2^100 times smaller than another that the row sees may be missing from
- *              them, and so may keys with values of zeros beside values of more than 2^30. A row and a key whose largest elements
- *              multiply to 2^127 or more have no defined score, not even 0. More rows go by way of keys and values read back to
- *              bf16, and have no such limits.
+ *              one token), by the size of d and the heads as few as two. Their products are of the bytes as they lie. A term P v of O
+ *              is off by 1.1 x 2^-9 of itself or by 2^-29 of what it would be with the largest P 2^code of the row, whichever is
+ *              more. Beside values of more than 2^116 that a row sees, keys of less than 2^-12 of the largest's weight may be missing
+ *              from its sum (2^-24 at 2^116). A row and a key whose largest elements multiply to 2^127 or more have no defined score,
+ *              not even 0. More rows go by way of keys and values read back to bf16, and have no such limits.
  *   sizes      besides those above, an attention has fewer than 2^26 sequences x K/V heads.
  * Key weights and eviction take bf16 caches only.
  */

@@ -385,6 +385,25 @@ def test_attend_extreme_scores(d):
             p.check_attend(*p.attend(True), True)
 
 
+@pytest.mark.parametrize("small,large", [(None, 60), (None, 115), (-60, 60), (-70, 100), (0, 113)])
+@pytest.mark.parametrize("n,sms", [(1, None), (6, 1), (20, 3), (32, 1), (130, None)])
+@pytest.mark.parametrize("where", ["first", "last", "all over"])
+def test_row_sums_do_not_depend_on_the_values(where, n, sms, small, large):
+    """Keys whose values are 2^large, others whose values are 2^small (or zeros), and ordinary ones between them: all of them count in the
+    row sums by their scores alone. The large ones come before all others, behind them, or among them."""
+    for d in (64, 128):
+        p = Problem8([700, 390], [n, n], 4, 2, d, page=16, seed=36, spread=0.0)
+        for b in range(2):
+            L = p.lk[b]
+            j = torch.arange(L)
+            row = (p.table[b][j // 16].long(), j % 16)
+            big = {"first": j < 9, "last": j >= L - n - 9, "all over": j % 41 == 3}[where]
+            for at, by in (((j % 2 == 0) & ~big, 0.0 if small is None else 2.0**small), (big, 2.0**large)):
+                p.v[row[0][at], row[1][at]] *= by
+        p.quantise()
+        p.check_attend(*p.attend(True, num_sms=sms), True)
+
+
 @pytest.mark.parametrize("n", [1, 6, 130])
 @pytest.mark.parametrize("d", [64, 128])
 def test_values_of_very_different_sizes(d, n):
