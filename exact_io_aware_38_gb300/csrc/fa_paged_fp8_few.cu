@@ -56,10 +56,11 @@ template <int D, int NP>
 struct F8Cfg {
   static constexpr int kTileBytes = 128 * D;
   static constexpr int kCtas = few8_ctas(NP);
-  // Rows of a group of four softmax warps, and groups. Eight rows are a shorter chain of steps (16 x 4099 keys, 20 rows: 31.3 us,
-  // with 16 a group 32.3; 32 rows 32.5 and 34.3), but twice the warps, which 16 rows, twice on an SM, do not gain by (16 rows 26.5 us
-  // and, with 8 a group, 26.4; 48 x 1024 keys of 12 heads, d = 64, 24.9 and 25.7).
-  static constexpr int kCols = NP == 8 || NP == 32 ? 8 : 16, kGroups = NP / kCols;
+  // Rows of a group of four softmax warps, and groups: eight of 8 rows, a shorter chain of steps with twice the warps, else 16. Of 17 to 32
+  // rows at d = 128 groups of 16 are ahead (16 x 4099 keys, 20 rows: 30.5 us, of 8 31.7; 64 x 8192 keys, 24 rows 151 and 159), at d = 64
+  // mostly groups of 8 (512 x 500 keys of 12 heads, 24 rows 266 and 218, 48 x 1024 39.8 and 38.9, 64 x 4096 116 and 126). Of 16 rows, twice
+  // on an SM, groups of 16 (16 x 4099 keys 26.7 and, of 8, 26.8; 48 x 1024 keys of 12 heads, d = 64, 24.4 and 25.4).
+  static constexpr int kCols = NP == 8 || (NP == 32 && D == 64) ? 8 : 16, kGroups = NP / kCols;
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kKStages = NP <= 16 ? (D == 128 ? 3 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;
   static constexpr int kVStages = NP <= 16 ? (D == 128 ? 2 : 5) : NP == 32 ? (D == 128 ? 5 : 8) : D == 128 ? 3 : 6;
