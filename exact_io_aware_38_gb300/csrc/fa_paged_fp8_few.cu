@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(F8Cfg<D, NP>::kThreads, F8Cfg<D, NP>::kCtas)
           if (!opens) {
             if (run) run = wait_pv(t - 1);
             fence_after_sync();
-#pragma unroll 1  // (512 x 500 keys of 12 heads, d = 64, 16 rows: 182 us unrolled and 148)
+// (512 x 500 keys of 12 heads, d = 64, 16 rows: 182 us unrolled and 148; of 8 rows, 4096 x 128 keys, 365 and 376)
+#pragma unroll (NP == 8 ? 3 : 1)
             for (int part = 0; part < 3; ++part) {
               uint32_t o[NC];
               load_cols(tO + part * NP, o);
