@@ -18,8 +18,8 @@
 // exponent of P, y = c s 2^k log2 e + v, P = 2^(y - ref). So P V needs no further factor, and the reference follows the
 // products P |V|: a key with much weight but a tiny value (or none) does not push the others out of e5m2's range. The row sum
 // takes P 2^-v, which must not be lost where P is too small for fp32: the exponential is taken without v where v < 0 and P is a lane's
-// constant times it; where v > 0 the sum's FMA has the constant (before, values of zeros beside 2^60 were missing from the sums; the
-// multiplication: 16 x 4099 keys, 20 rows, 31.3 -> 31.7 us, 4096 x 128 keys of 12 heads, d = 64, 408 -> 415, others within 1%).
+// constant times it; where v > 0 the sum's FMA has the constant (else keys of values of zeros beside 2^60 are missing from the sums; the
+// multiplication costs 1%: 4096 x 128 keys of 12 heads, d = 64, 362 -> 365 us, 48 x 1024, 20 rows, 38.3 -> 38.9).
 //
 // The exponentials are taken against a reference per row that starts 2^7 below the first tile's largest and is raised
 // (O and the row sums rescaled) only when a score exceeds it by more than 2^15.
@@ -88,7 +88,7 @@ struct F8Cfg {
 constexpr int kCodeStages = 16;
 
 // Positions of a unit before its first tile, for its epilogue and the first tile of the next (weighed as 1 and 3: 16 x 2048 keys of 32
-// heads 38.9 and 38.2 us; 64 x 8192 keys 120.8 and 120.9, 64 x 4096 of 12 heads at d = 64 56.2 and 56.3).
+// heads 39.3 and 38.7 us; 64 x 8192 keys 123.0 and 123.1, 64 x 4096 of 12 heads at d = 64 56.9 and 57.0).
 constexpr int kF8Open = 3;
 // Positions fit an int: a sequence with new tokens has at most 4 units a head of max_k / 128 + 4 positions each, sequences times
 // heads are fewer than 2^26 and times keys fewer than 2^31 (checked by the caller). In 64 bits the search for a CTA's share
@@ -915,11 +915,11 @@ F8Cut cut_of(const PagedShape& s, int tokens, int ctas) {
 
 // CTAs that share a (sequence, head) unit where nothing is divided by the lengths, or 0: the rule of fa_paged_decode.cu with
 // limits of its own, since a tile is half as many bytes. Eight tiles a CTA of a cluster (8 sequences of 8 heads, 4000 keys:
-// 13.9 us, divided 14.1; one of 777 8.3 and 9.5, of 8000 12.4 and 12.8; 4 of 4000 12.8 and 12.0, which clusters of 8 would do in 10.9; with
-// 16 tiles 8 of 8000 21.3 and 19.3) or 16 of one alone (24 of 12 heads, d = 64, 2000 keys: 16.0 and 18.0). Nearly two units a place, of up
-// to 8 tiles, mostly gain undivided (48 of 12 heads, d = 64, 1024 keys in pages of 64: 19.6 and 20.1, with 16 rows 24.9 and 29.0; 64 of 8
-// heads, d = 128, 500 keys 17.8 and 19.2; 128 keys 13.4 and 13.1), and are one launch without a workspace. Not a few more than the
-// places (40 of 8 heads, 1000 keys: 20.8 and 18.9), nor 16 tiles (64 of 8 heads, 2000 keys: 39.7 and 37.4).
+// 13.9 us, divided 14.3; one of 777 8.4 and 9.5, of 8000 12.5 and 12.7; 4 of 4000 12.8 and 11.9, which clusters of 8 would do in 10.9; with
+// 16 tiles 8 of 8000 21.5 and 19.5) or 16 of one alone (24 of 12 heads, d = 64, 2000 keys: 16.1 and 18.1). Nearly two units a place, of up
+// to 8 tiles, mostly gain undivided (48 of 12 heads, d = 64, 1024 keys in pages of 64: 19.5 and 20.3, with 16 rows 24.4 and 28.2; 64 of 8
+// heads, d = 128, 500 keys 17.9 and 19.3; 128 keys 13.5 and 13.2), and are one launch without a workspace. Not a few more than the
+// places (40 of 8 heads, 1000 keys: 20.9 and 19.0), nor 16 tiles (64 of 8 heads, 2000 keys: 40.2 and 37.8).
 int unit_ctas(const PagedShape& s, int tokens, int num_sms) {
   if (tokens < s.Nq || token_units(s) > 1) return 0;
   const long long units = (long long)s.B * s.Hkv, room = (long long)num_sms * few8_ctas(unit_rows(s, tokens));
